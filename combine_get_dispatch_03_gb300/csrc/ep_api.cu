@@ -13,56 +13,22 @@
 #include <string>
 
 #include "ep_common.cuh"
+#include "ep_handle.h"
 #include "ep_kernels.h"
 #include "ep_trace.h"
 
 namespace ep {
 cudaError_t plan_dispatch_combine(LaunchPlan* plan, int hidden);
 cudaError_t plan_ll(LaunchPlan* plan, int num_experts);
+cudaError_t plan_gemm();
+cudaError_t plan_rows();
 }  // namespace ep
 
-struct ep_handle {
-    ep_config cfg;
-    int device = -1;
-    ep::LaunchPlan plan;
-    void* dmem = nullptr;
-    size_t dmem_bytes = 0;
-    int32_t* status = nullptr;
-    int32_t* rank_prefix = nullptr;          // [R][R]
-    int32_t* channel_prefix = nullptr;       // [R][R][C]
-    int32_t* recv_channel_prefix = nullptr;  // [R][R][C]
-    int32_t* num_recv = nullptr;             // [R]
-    int32_t* recv_src_idx = nullptr;         // [R][cap]
-    int32_t* send_head = nullptr;            // [R][maxT][R]
-    int32_t* ll_slot = nullptr;              // [R][maxT][K]
-    int32_t* ll_cnt = nullptr;               // [R][E]
-    int32_t* rank_mask = nullptr;            // [R], nonzero = masked
-    int32_t* rdma_channel_prefix = nullptr;    // [R][NN][C], NN = R / 8 whole nodes (see has_nodes)
-    int32_t* recv_rdma_rank_prefix = nullptr;  // [R][NN]
-    int32_t* claims = nullptr;                 // [2]: the combine's next token and finished warps
-    int32_t* layout_scratch = nullptr;         // tile states of the one-pass layout + record scan
-    int normal_tokens = -1;                  // T of the current dispatch record, -1 = none
-    bool prepared = false;                   // record built by ep_notify_dispatch, not yet used
-    int ll_tokens = -1;                      // T of the last LL dispatch, -1 = none
-};
+using namespace ep;
 
 namespace {
 
 thread_local std::string g_last_error;
-
-ep_status fail(ep_status code, const char* fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    g_last_error = buf;
-    return code;
-}
-
-ep_status cuda_fail(cudaError_t err, const char* what) {
-    return fail(EP_ERR_CUDA, "%s: %s", what, cudaGetErrorString(err));
-}
 
 // Two or more whole nodes of 8 ranks: the handle keeps the node-level record.
 bool has_nodes(const ep_config& c) { return c.num_ranks > 8 && c.num_ranks % 8 == 0; }
@@ -72,32 +38,6 @@ int32_t* node_record(const ep_handle* h, int which) {
     if (!has_nodes(h->cfg)) return nullptr;
     return which == 0 ? h->rdma_channel_prefix : h->recv_rdma_rank_prefix;
 }
-
-#define EP_CHECK_ARG(cond, ...)                                  \
-    do {                                                         \
-        if (!(cond)) return fail(EP_ERR_INVALID_ARG, __VA_ARGS__); \
-    } while (0)
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
-
-// Makes the handle's device current for the duration of a call.
-class DeviceGuard {
-public:
-    explicit DeviceGuard(int device) {
-        cudaGetDevice(&prev_);
-        if (prev_ != device) cudaSetDevice(device);
-        restore_ = prev_ != device;
-    }
-    ~DeviceGuard() {
-        if (restore_) cudaSetDevice(prev_);
-    }
-
-private:
-    int prev_ = 0;
-    bool restore_ = false;
-};
 
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
@@ -139,8 +79,36 @@ ep_status check_tokens(const ep_handle* h, int32_t num_tokens) {
 }  // namespace
 
 namespace ep {
+
+ep_status fail(ep_status code, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    g_last_error = buf;
+    return code;
+}
+
+ep_status cuda_fail(cudaError_t err, const char* what) {
+    return fail(EP_ERR_CUDA, "%s: %s", what, cudaGetErrorString(err));
+}
+
+ep_status check_group_args(const ep_handle* h, int64_t num_rows, const int32_t* group_count,
+                           const int32_t* group_begin) {
+    EP_CHECK_ARG(num_rows >= 0 && num_rows <= INT32_MAX, "num_rows %lld outside [0, 2^31)",
+                 static_cast<long long>(num_rows));
+    EP_CHECK_ARG(group_count != nullptr && aligned4(group_count) && aligned4(group_begin),
+                 "group_count is NULL, or a group array is misaligned");
+    EP_CHECK_ARG(group_begin != nullptr || num_rows % h->cfg.num_experts == 0,
+                 "without group_begin, num_rows %lld must be a multiple of num_experts %d",
+                 static_cast<long long>(num_rows), h->cfg.num_experts);
+    return EP_OK;
+}
+
 // Lets other translation units of the library set the thread's ep_last_error() text.
 void record_error(const char* message) { g_last_error = message ? message : ""; }
+
 }  // namespace ep
 
 extern "C" {
@@ -189,6 +157,8 @@ ep_status ep_handle_create(const ep_config* cfg, ep_handle** out) {
     }
     if (err == cudaSuccess) err = ep::plan_dispatch_combine(&h->plan, cfg->hidden);
     if (err == cudaSuccess) err = ep::plan_ll(&h->plan, cfg->num_experts);
+    if (err == cudaSuccess) err = ep::plan_gemm();
+    if (err == cudaSuccess) err = ep::plan_rows();
     if (err != cudaSuccess) {
         delete h;
         return cuda_fail(err, "planning launches");
@@ -199,11 +169,12 @@ ep_status ep_handle_create(const ep_config* cfg, ep_handle** out) {
     const size_t NN = (R + 7) / 8;
     const size_t scan_words = ep::layout_scan_scratch_words(cfg->num_ranks, cfg->num_experts, cfg->num_max_tokens);
     const size_t sizes[] = {1, R * R, R * R * C, R * R * C, R, R * cap, R * T * R, R * T * K, R * E, R,
-                            R * NN * C, R * NN, 2, scan_words};
+                            R * NN * C, R * NN, 2, scan_words,
+                            cap ? static_cast<size_t>(ep::layout_chunks(*cfg)) * E : 0};
     int32_t** slots[] = {&h->status,   &h->rank_prefix,  &h->channel_prefix, &h->recv_channel_prefix,
                          &h->num_recv, &h->recv_src_idx, &h->send_head,      &h->ll_slot,
                          &h->ll_cnt,   &h->rank_mask,    &h->rdma_channel_prefix, &h->recv_rdma_rank_prefix,
-                         &h->claims,   &h->layout_scratch};
+                         &h->claims,   &h->layout_scratch, &h->expert_counts};
     size_t total = 0;
     for (size_t s : sizes) total += align_up(s * sizeof(int32_t), 256);
     err = cudaMalloc(&h->dmem, total);

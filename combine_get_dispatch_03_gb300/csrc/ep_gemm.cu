@@ -1,0 +1,698 @@
+// ep_gemm.cu -- matrix products grouped by expert, with ragged groups (sm_103a tensor cores).
+//
+// Rows of all experts lie in one array; expert e has rows [begin[e], begin[e] + count[e]) and its own
+// weights.  Four forms share one persistent kernel:
+//   forward       out[r][j] = sum_c x[r][c] * w[e][j][c]          bf16, both operands contraction-major
+//   transposed    out[r][j] = sum_c x[r][c] * w[e][c][j]          bf16, the weights read across (gradient of the rows)
+//   weight grad   dw[e][j][c] = sum_r dy[r][j] * x[r][c]          bf16, both operands read across, contraction over a group's rows
+//   fp8           out[r][j] = sum_b sx[r][b] * sw[e][j/128][b] * sum_{c in block b} x[r][c] * w[e][j][c]    e4m3, blocks of 128
+//
+// Work is cut into output tiles of 128 rows (256 for a pair of CTAs) by 64, 128 or 256 columns, taken
+// in turn by the CTAs of one resident wave.  In a CTA one warp loads operand tiles with tensor maps into a
+// ring of shared-memory stages (128 bytes of the contraction a stage), one warp issues tcgen05.mma from
+// them into tensor memory, and the remaining warps read the fp32 accumulators back, round and store.  Two
+// accumulators of 256 columns let the next tile's products run under this tile's stores.
+//
+// The group table (tiles before each expert, counts, begins) is built in shared memory by each CTA from the
+// device arrays, so that no count has to reach the host.
+#include <cudaTypedefs.h>
+
+#include "ep_groups.cuh"
+#include "ep_handle.h"
+#include "ep_tc.cuh"
+#include "ep_trace.h"
+
+namespace ep {
+namespace {
+
+enum GemmForm { kForward = 0, kTransposed = 1, kWeightGrad = 2, kFp8 = 3 };
+
+constexpr int kTileRows = 128;      // output rows per CTA
+constexpr int kMaxTileCols = 256;
+constexpr int kRowBytes = 128;      // bytes of one operand row in a stage (the swizzle's span)
+constexpr int kRowBox = 32;         // rows per tensor-map load of a row operand: a short group loads few
+constexpr int kColBox = 64;         // rows (or bf16 columns) per load of a weight operand
+constexpr int kMaxStages = 12;
+constexpr int kEpilogueWarps = 8;
+constexpr int kGemmThreads = (4 + kEpilogueWarps) * kWarpSize;  // warps 2 and 3 are idle: register splits go by four warps
+constexpr int kMaxSmem = 232448;
+constexpr int kControlBytes = 512;
+
+struct GemmParams {
+    Groups groups;          // of the row operand (weight grad: operands) and the output's rows
+    int32_t rows_dim;       // weight grad: output rows per group (n)
+    int32_t cols_dim;       // output columns
+    int32_t contraction;    // contraction length (weight grad: a group's count instead)
+    void* out;
+    int64_t out_row_bytes;
+    const uint8_t* x_scales;
+    int64_t x_scale_row_bytes;
+    const float* w_scales;
+    int32_t scales_ue8m0;
+    int32_t out_fp32;       // weight grad
+    int32_t accumulate;     // weight grad
+    int32_t wide_stores;    // output rows are 32-byte aligned
+    int32_t* status;
+};
+
+struct Control {
+    uint64_t full[kMaxStages];
+    uint64_t empty[kMaxStages];
+    uint64_t acc_full[2];
+    uint64_t acc_empty[2];
+    uint64_t tail_full[kMaxStages];  // weight grad: instead of full, for a group's last, partial block of rows
+    uint64_t drained;
+    uint32_t tmem;
+    int32_t abort_flag;
+    int32_t warp_sums[kGemmThreads / kWarpSize];
+};
+static_assert(sizeof(Control) <= kControlBytes, "control block");
+
+struct Tile {
+    int group, row0, rows, m0, n0, steps;  // rows: valid rows of the group; m0: tile's first row in the group
+};
+
+// The group table in shared memory, and how tiles are numbered.
+struct Table {
+    int32_t* before;  // [groups + 1] row tiles before each group
+    int32_t* count;   // [groups]
+    int32_t* begin;   // [groups]
+    int32_t groups, col_tiles, tile_cols, tile_rows;
+    int total;
+};
+
+template <int FORM>
+__device__ __forceinline__ Tile decode(const Table& t, const GemmParams& p, int tile) {
+    Tile r;
+    const int lo = find_group(t.before, t.groups, tile / t.col_tiles);
+    const int in = tile - t.before[lo] * t.col_tiles;
+    const int row_tiles = t.before[lo + 1] - t.before[lo];
+    r.group = lo;
+    r.row0 = t.begin[lo];
+    r.rows = t.count[lo];
+    // row tiles turn fastest: CTAs side by side share a weight tile
+    r.n0 = in / row_tiles * t.tile_cols;
+    r.m0 = in % row_tiles * t.tile_rows;
+    if constexpr (FORM == kWeightGrad) r.steps = (r.rows + 63) >> 6;
+    else if constexpr (FORM == kFp8) r.steps = (p.contraction + 127) >> 7;
+    else r.steps = (p.contraction + 63) >> 6;
+    return r;
+}
+
+// Fills the table: clamps every group to the rows that exist (the first group that does not fit sets
+// EP_ERR_CAPACITY), and sums the row tiles.  All threads of the CTA.
+template <int FORM, int CG>
+__device__ __forceinline__ void build_table(Table& t, const GemmParams& p, Control* ctl) {
+    const int per = (t.groups + kGemmThreads - 1) / kGemmThreads;
+    const int first = threadIdx.x * per;
+    const int last = min(first + per, t.groups);
+    int sum = 0, total = 0;
+    for (int g = first; g < last; ++g) {
+        const Group q = load_group(p.groups, g, p.status);
+        t.count[g] = q.count;
+        t.begin[g] = q.begin;
+        t.before[g] = sum;
+        sum += ((FORM == kWeightGrad ? p.rows_dim : q.count) + t.tile_rows - 1) / t.tile_rows;
+    }
+    const int base = block_prefix<kGemmThreads>(sum, ctl->warp_sums, &total);
+    for (int g = first; g < last; ++g) t.before[g] += base;
+    if (threadIdx.x == 0) t.before[t.groups] = total;
+    __syncthreads();
+    // Tile width: the one whose waves over the CTAs take the least time, a wave costing its columns plus
+    // what a tile costs at any width.
+    const int workers = gridDim.x / CG;
+    int best = kMaxTileCols;
+    int64_t best_cost = INT64_MAX;
+    for (int cols = kMaxTileCols; cols >= kColBox; cols >>= 1) {
+        const int64_t tiles = static_cast<int64_t>(total) * ((p.cols_dim + cols - 1) / cols);
+        const int64_t cost = (tiles + workers - 1) / workers * (cols + 32);
+        if (cost < best_cost) best_cost = cost, best = cols;
+    }
+    t.tile_cols = best;
+    t.col_tiles = (p.cols_dim + best - 1) / best;
+    t.total = total * t.col_tiles;
+}
+
+__device__ __forceinline__ float scale_of(const uint8_t* row, int block, int ue8m0) {
+    if (ue8m0) {
+        const uint32_t e = row[block];
+        return __uint_as_float(e == 255 ? 0x7fc00000u : e == 0 ? 0x00400000u : e << 23);
+    }
+    return *reinterpret_cast<const float*>(row + 4 * static_cast<int64_t>(block));
+}
+
+// 32 columns of one output row, rounded to bf16; columns at or past `cols` (a multiple of 8) are left out.
+__device__ __forceinline__ void store_bf16(uint8_t* row, int col, int cols, const float (&v)[32], bool wide) {
+    uint8_t* p = row + 2 * static_cast<int64_t>(col);
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (wide && col + 16 * i + 16 <= cols) {
+            const uint32_t q[8] = {w[8 * i], w[8 * i + 1], w[8 * i + 2], w[8 * i + 3],
+                                   w[8 * i + 4], w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]};
+            st_global_v8(p + 32 * i, q);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (col + 16 * i + 8 * j + 8 <= cols)
+                    *reinterpret_cast<uint4*>(p + 32 * i + 16 * j) =
+                        make_uint4(w[8 * i + 4 * j], w[8 * i + 4 * j + 1], w[8 * i + 4 * j + 2], w[8 * i + 4 * j + 3]);
+        }
+    }
+}
+
+// The same in fp32, optionally added to what is there.
+__device__ __forceinline__ void store_fp32(uint8_t* row, int col, int cols, const float (&v)[32], bool accumulate) {
+    float* p = reinterpret_cast<float*>(row) + col;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (col + 4 * i + 4 > cols) break;
+        float4 q = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        if (accumulate) {
+            const float4 o = *reinterpret_cast<const float4*>(p + 4 * i);
+            q = make_float4(q.x + o.x, q.y + o.y, q.z + o.z, q.w + o.w);
+        }
+        *reinterpret_cast<float4*>(p + 4 * i) = q;
+    }
+}
+
+template <int FORM, int CG>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                        const GemmParams p) {
+    extern __shared__ uint8_t raw[];
+    uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    Control* ctl = reinterpret_cast<Control*>(smem);
+    Table t;
+    t.groups = p.groups.groups;
+    t.tile_rows = kTileRows * CG;
+    t.before = reinterpret_cast<int32_t*>(smem + kControlBytes);
+    t.count = t.before + t.groups + 1;
+    t.begin = t.count + t.groups;
+    uint32_t dyn;
+    asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(dyn));
+    const uint32_t table_end = (kControlBytes + 4u * (3u * t.groups + 1u) + 1023u) & ~1023u;
+    uint8_t* const stages = smem + table_end;
+
+    const int warp = threadIdx.x / kWarpSize;
+    const uint32_t rank = CG == 1 ? 0 : cluster_rank();
+    volatile int32_t* abort_flag = &ctl->abort_flag;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kMaxStages; ++i) {
+            mbar_init(&ctl->full[i], CG);
+            mbar_init(&ctl->empty[i], 1);
+            mbar_init(&ctl->tail_full[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl->acc_full[i], 1);
+            mbar_init(&ctl->acc_empty[i], kEpilogueWarps * CG);
+        }
+        mbar_init(&ctl->drained, 1);
+        ctl->abort_flag = 0;
+        fence_barrier_init();
+        prefetch_map(&map_a);
+        prefetch_map(&map_b);
+    }
+    if (warp == 1) tmem_alloc<CG>(&ctl->tmem, 512);
+    pdl_enter();
+    build_table<FORM, CG>(t, p, ctl);
+    tc_fence_before();
+    if constexpr (CG == 2) cluster_barrier();
+    else __syncthreads();
+    tc_fence_after();
+
+    const uint32_t tmem = ctl->tmem;
+    const int cols_here = t.tile_cols / CG;  // columns of the weight operand that this CTA loads
+    const uint32_t a_bytes = kTileRows * kRowBytes;
+    const uint32_t stage_bytes = a_bytes + cols_here * kRowBytes;
+    const int num_stages = min(kMaxStages, static_cast<int>((dyn - 1024u - table_end) / stage_bytes));
+    const int worker = blockIdx.x / CG, workers = gridDim.x / CG;
+
+    // The FP8 form holds 128 sums a thread in its eight epilogue warps: registers move there from the
+    // others (72 + 2 * 216 = 3 * 168, what the block was launched with).
+    if (warp < 4) {
+    if constexpr (FORM == kFp8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 0 && lane_id() == 0) {
+        // ------------------------------------------------------------- loads
+        uint32_t stage = 0, phase = 0;
+        uint32_t tail_phase = 0, tail_last = 0;  // per stage: uses of tail_full, mod 2; whether its last use was one
+        bool ok = true;
+        const uint32_t full0 = CG == 1 ? smem_u32(ctl->full) : cluster_addr(ctl->full, 0);
+        uint32_t used = 0;
+        for (int tile = worker; ok && tile < t.total; tile += workers) {
+            const Tile q = decode<FORM>(t, p, tile);
+            const int my_m0 = q.m0 + static_cast<int>(rank) * kTileRows;
+            const int boxes = max(0, min(kTileRows, q.rows - my_m0) + kRowBox - 1) / kRowBox;
+            for (int s = 0; s < q.steps; ++s) {
+                ok = wait_phase(&ctl->empty[stage], phase ^ 1, abort_flag, p.status);
+                if (!ok) break;
+                uint8_t* a = stages + stage * stage_bytes;
+                uint8_t* b = a + a_bytes;
+                uint32_t bar = full0 + 8 * stage;
+                const int cb = static_cast<int>(rank) * cols_here;
+                if constexpr (FORM == kWeightGrad) {
+                    const bool tail = (s + 1) * 64 > q.rows;
+                    if (tail) {
+                        bar = smem_u32(&ctl->tail_full[stage]);
+                        mbar_arrive_expect_tx(&ctl->tail_full[stage], stage_bytes);
+                        tail_phase ^= 1u << stage;
+                        tail_last |= 1u << stage;
+                    } else {
+                        cluster_arrive_expect_tx(bar, stage_bytes);
+                        tail_last &= ~(1u << stage);
+                    }
+                    const int r = q.row0 + s * 64;
+                    for (int c = 0; c < kTileRows / 64; ++c) tma_load_2d<CG>(a + c * 8192, &map_a, my_m0 + c * 64, r, bar);
+                    for (int c = 0; c < cols_here / 64; ++c) tma_load_2d<CG>(b + c * 8192, &map_b, q.n0 + cb + c * 64, r, bar);
+                } else {
+                    cluster_arrive_expect_tx(bar, boxes * (kRowBox * kRowBytes) + cols_here * kRowBytes);
+                    const int x = s * (FORM == kFp8 ? 128 : 64);
+                    for (int c = 0; c < boxes; ++c)
+                        tma_load_2d<CG>(a + c * (kRowBox * kRowBytes), &map_a, x, q.row0 + my_m0 + c * kRowBox, bar);
+                    for (int c = 0; c < cols_here / kColBox; ++c) {
+                        if constexpr (FORM == kTransposed)
+                            tma_load_3d<CG>(b + c * 8192, &map_b, q.n0 + cb + c * kColBox, x, q.group, bar);
+                        else
+                            tma_load_3d<CG>(b + c * 8192, &map_b, x, q.n0 + cb + c * kColBox, q.group, bar);
+                    }
+                }
+                ++used;
+                if (++stage == static_cast<uint32_t>(num_stages)) stage = 0, phase ^= 1;
+            }
+        }
+        if (!ok) {
+            // Given up: wait (again with a limit) for the copies in flight before the memory goes away.
+            // (With a pair, both CTAs' copies arrive at the leader, and neither leaves before the other.)
+            for (int i = 0; i < num_stages && used > 0; ++i, --used) {
+                if (stage == 0) phase ^= 1;
+                stage = (stage == 0 ? num_stages : stage) - 1;
+                const bool tail = (tail_last >> stage) & 1;
+                uint64_t* bar = tail ? &ctl->tail_full[stage] : &ctl->full[stage];
+                const uint32_t parity = tail ? ((tail_phase >> stage) & 1) ^ 1 : phase;
+                for (int k = 0; k < (1 << 12) && !mbar_try_wait(bar, parity); ++k) {
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------------- products
+        uint32_t stage = 0, phase = 0, acc_phase = 0;
+        uint32_t tail_phase = 0;  // per stage: uses of tail_full, mod 2
+        int buf = 0;
+        bool ok = true;
+        constexpr bool a_mn = FORM == kWeightGrad;
+        constexpr bool b_mn = FORM == kWeightGrad || FORM == kTransposed;
+        const uint32_t idesc = mma_desc(FORM == kFp8 ? 0 : 1, a_mn, b_mn, kTileRows * CG, t.tile_cols);
+        const bool leader = rank == 0;
+        for (int tile = worker; ok && tile < t.total; tile += workers) {
+            const Tile q = decode<FORM>(t, p, tile);
+            if (FORM != kFp8 && leader) {
+                ok = warp_wait(&ctl->acc_empty[buf], acc_phase ^ 1, abort_flag, p.status);
+                tc_fence_after();
+            }
+            for (int s = 0; s < q.steps && ok; ++s) {
+                uint8_t* a = stages + stage * stage_bytes;
+                if constexpr (FORM == kWeightGrad) {
+                    const int valid = q.rows - s * 64;
+                    if (valid < 64) {
+                        // The block's rows past the group belong to others: zero them in both operands.
+                        ok = warp_wait(&ctl->tail_full[stage], (tail_phase >> stage) & 1, abort_flag, p.status);
+                        tail_phase ^= 1u << stage;
+                        const int chunks = (kTileRows + cols_here) / 64;
+                        const int pieces = (64 - valid) * 8;
+                        for (int c = 0; c < chunks; ++c) {
+                            uint4* z = reinterpret_cast<uint4*>(a + c * 8192 + valid * 128);
+                            for (int i = lane_id(); i < pieces; i += kWarpSize) z[i] = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane_id() == 0)
+                            cluster_arrive(CG == 1 ? smem_u32(&ctl->full[stage]) : cluster_addr(&ctl->full[stage], 0));
+                    }
+                }
+                if (leader && ok) {
+                    if (FORM == kFp8) {
+                        ok = warp_wait(&ctl->acc_empty[buf], acc_phase ^ 1, abort_flag, p.status);
+                        if (!ok) break;
+                    }
+                    ok = warp_wait(&ctl->full[stage], phase, abort_flag, p.status);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (lane_id() == 0) {
+                        const uint64_t da = smem_desc(smem_u32(a), a_mn ? 8192 : 16);
+                        const uint64_t db = smem_desc(smem_u32(a) + a_bytes, b_mn ? 8192 : 16);
+                        const uint32_t d = tmem + buf * kMaxTileCols;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            tc_mma<CG, FORM == kFp8>(d, da + i * (a_mn ? 128 : 2), db + i * (b_mn ? 128 : 2), idesc,
+                                                     (FORM == kFp8 ? 0 : s) | i);
+                        tc_commit<CG>(&ctl->empty[stage]);
+                        if (FORM == kFp8) tc_commit<CG>(&ctl->acc_full[buf]);
+                    }
+                    __syncwarp();
+                }
+                if (FORM == kFp8) {
+                    buf ^= 1;
+                    acc_phase ^= buf == 0;
+                }
+                if (++stage == static_cast<uint32_t>(num_stages)) stage = 0, phase ^= 1;
+            }
+            if (FORM != kFp8) {
+                if (leader && ok && lane_id() == 0) tc_commit<CG>(&ctl->acc_full[buf]);
+                __syncwarp();
+                buf ^= 1;
+                acc_phase ^= buf == 0;
+            }
+        }
+        if (!ok && leader) {
+            // Given up: the products already issued still write tensor memory.
+            if (lane_id() == 0) tc_commit<CG>(&ctl->drained);
+            for (int k = 0; k < (1 << 12) && !mbar_try_wait(&ctl->drained, 0); ++k) {
+            }
+            __syncwarp();
+        }
+    }
+    } else {
+        // ------------------------------------------------- accumulators out
+        if constexpr (FORM == kFp8) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        const int w = warp - 4;
+        const int quarter = warp & 3;               // the 32 lanes of tensor memory that this warp may read
+        const int half = w >> 2;                    // which half of the tile's columns
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        const int cols_half = t.tile_cols / 2;
+        const uint32_t acc_empty0 = CG == 1 ? smem_u32(ctl->acc_empty) : cluster_addr(ctl->acc_empty, 0);
+        int buf = 0;
+        uint32_t acc_phase = 0;
+        bool ok = true;
+        for (int tile = worker; ok && tile < t.total; tile += workers) {
+            const Tile q = decode<FORM>(t, p, tile);
+            const int row = q.m0 + static_cast<int>(rank) * kTileRows + quarter * 32 + lane_id();  // in the group
+            const int col0 = q.n0 + half * cols_half;
+            uint8_t* out_row;
+            bool row_ok;
+            if constexpr (FORM == kWeightGrad) {
+                row_ok = row < p.rows_dim;
+                out_row = static_cast<uint8_t*>(p.out) + (static_cast<int64_t>(q.group) * p.rows_dim + row) * p.out_row_bytes;
+            } else {
+                row_ok = row < q.rows;
+                out_row = static_cast<uint8_t*>(p.out) + (static_cast<int64_t>(q.row0) + row) * p.out_row_bytes;
+            }
+            if constexpr (FORM != kFp8) {
+                ok = warp_wait(&ctl->acc_full[buf], acc_phase, abort_flag, p.status);
+                if (!ok) break;
+                tc_fence_after();
+                for (int c = 0; c < cols_half; c += 32) {
+                    uint32_t u[32];
+                    __syncwarp();
+                    tc_ld32(lane_base + buf * kMaxTileCols + half * cols_half + c, u);
+                    tc_wait_ld(u);
+                    if (c + 32 >= cols_half) {  // read out: the accumulator is free before the last stores
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane_id() == 0) cluster_arrive(acc_empty0 + 8 * buf);
+                    }
+                    float v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = FORM == kWeightGrad && q.steps == 0 ? 0.0f : __uint_as_float(u[i]);
+                    if (row_ok && col0 + c < p.cols_dim) {
+                        if (FORM == kWeightGrad && p.out_fp32)
+                            store_fp32(out_row, col0 + c, p.cols_dim, v, p.accumulate != 0);
+                        else
+                            store_bf16(out_row, col0 + c, p.cols_dim, v, p.wide_stores != 0);
+                    }
+                }
+                buf ^= 1;
+                acc_phase ^= buf == 0;
+            } else {
+                // Each block of 128 has its own scales: its products arrive in an accumulator of their own and
+                // are scaled and added here, in fp32 registers, 128 columns a thread at most.
+                float acc[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) acc[c][i] = 0.0f;
+                const int64_t src = static_cast<int64_t>(q.row0) + min(row, q.rows - 1);
+                const uint8_t* xs = p.x_scales + src * p.x_scale_row_bytes;
+                const int nb = min(col0, p.cols_dim - 1) >> 7;
+                const float* ws = p.w_scales + (static_cast<int64_t>(q.group) * ((p.cols_dim + 127) >> 7) + nb) * q.steps;
+                float cur[4], next[4];
+                auto fetch = [&](float (&f)[4], int s0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        f[i] = s0 + i < q.steps ? scale_of(xs, s0 + i, p.scales_ue8m0) * ws[s0 + i] : 0.0f;
+                };
+                fetch(cur, 0);
+                for (int s0 = 0; s0 < q.steps && ok; s0 += 4) {
+                    fetch(next, s0 + 4);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (s0 + j >= q.steps) break;
+                        ok = warp_wait(&ctl->acc_full[buf], acc_phase, abort_flag, p.status);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t at = lane_base + buf * kMaxTileCols + half * cols_half;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            if (c * 32 < cols_half) {
+                                uint32_t u[32];
+                                tc_ld32(at + c * 32, u);
+                                tc_wait_ld(u);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) acc[c][i] = fmaf(__uint_as_float(u[i]), cur[j], acc[c][i]);
+                            }
+                        }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane_id() == 0) cluster_arrive(acc_empty0 + 8 * buf);
+                        buf ^= 1;
+                        acc_phase ^= buf == 0;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) cur[i] = next[i];
+                }
+                if (ok && row_ok) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (c * 32 < cols_half && col0 + c * 32 < p.cols_dim)
+                            store_bf16(out_row, col0 + c * 32, p.cols_dim, acc[c], p.wide_stores != 0);
+                }
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    if constexpr (CG == 2) cluster_barrier();
+    else __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc<CG>(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+// The driver's tensor-map encoder, looked up once (the library does not link against libcuda).
+PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }();
+    return fn;
+}
+
+struct Operand {
+    const void* base;
+    bool fp8;
+    int dims;
+    uint64_t size[3];
+    uint64_t stride[2];  // bytes
+    uint32_t box[3];
+};
+
+ep_status encode(CUtensorMap* map, const Operand& o) {
+    const PFN_cuTensorMapEncodeTiled_v12000 fn = map_encoder();
+    if (fn == nullptr) return fail(EP_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
+    cuuint64_t size[3], stride[2];
+    cuuint32_t box[3], step[3] = {1, 1, 1};
+    for (int i = 0; i < 3; ++i) size[i] = o.size[i], box[i] = o.box[i];
+    for (int i = 0; i < 2; ++i) stride[i] = o.stride[i];
+    const CUresult rc = fn(map, o.fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, o.dims,
+                           const_cast<void*>(o.base), size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (rc != CUDA_SUCCESS) return fail(EP_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(rc));
+    return EP_OK;
+}
+
+// Rows [rows][inner] with a row stride.
+Operand row_operand(const void* base, bool fp8, int64_t inner, int64_t rows, int64_t row_bytes, uint32_t box_rows) {
+    return {base, fp8, 2, {static_cast<uint64_t>(inner), static_cast<uint64_t>(rows), 1},
+            {static_cast<uint64_t>(row_bytes), 0}, {fp8 ? 128u : 64u, box_rows, 1}};
+}
+
+// Weights [groups][rows][inner], contiguous.
+Operand weight_operand(const void* base, bool fp8, int64_t inner, int64_t rows, int64_t groups) {
+    const uint64_t row = static_cast<uint64_t>(inner) * (fp8 ? 1 : 2);
+    return {base, fp8, 3, {static_cast<uint64_t>(inner), static_cast<uint64_t>(rows), static_cast<uint64_t>(groups)},
+            {row, row * static_cast<uint64_t>(rows)}, {fp8 ? 128u : 64u, static_cast<uint32_t>(kColBox), 1}};
+}
+
+template <int FORM>
+ep_status launch(const ep_handle* h, const Operand& a, const Operand& b, const GemmParams& p, cudaStream_t stream) {
+    CUtensorMap ma, mb;
+    ep_status st = encode(&ma, a);
+    if (st == EP_OK) st = encode(&mb, b);
+    if (st != EP_OK) return st;
+    DeviceGuard guard(h->device);
+    const cudaError_t err = launch_kernel(grouped_gemm_kernel<FORM, 1>, dim3(h->plan.num_sms), dim3(kGemmThreads),
+                                          kMaxSmem, stream, 1, ma, mb, p);
+    if (err != cudaSuccess) return cuda_fail(err, "grouped product launch");
+    return EP_OK;
+}
+
+// Checks that every form shares; fills the groups' part of the parameters.
+ep_status check_groups(const ep_handle* h, int64_t num_rows, int32_t n, int32_t k, const int32_t* group_count,
+                       const int32_t* group_begin, GemmParams* p) {
+    if (h == nullptr) return fail(EP_ERR_INVALID_ARG, "handle is NULL");
+    const ep_status st = check_group_args(h, num_rows, group_count, group_begin);
+    if (st != EP_OK) return st;
+    const int32_t groups = h->cfg.num_experts;
+    EP_CHECK_ARG(n >= 8 && n % 8 == 0 && k >= 8 && k % 8 == 0, "n %d and k %d must be positive multiples of 8", n, k);
+    // tiles are numbered in 32 bits
+    const int64_t wide = n > k ? n : k;
+    const int64_t row_tiles = (num_rows > wide * groups ? num_rows : wide * groups) / kTileRows + groups;
+    if (row_tiles * (wide / kColBox + 1) >= (INT64_C(1) << 30))
+        return fail(EP_ERR_UNSUPPORTED, "%lld rows by %lld columns need too many tiles", static_cast<long long>(num_rows),
+                    static_cast<long long>(wide));
+    p->groups = {group_count, group_begin, num_rows, static_cast<int32_t>(num_rows / groups), groups};
+    p->status = h->status;
+    return EP_OK;
+}
+
+bool row_stride_ok(int64_t bytes, int64_t least) { return bytes >= least && bytes % 16 == 0 && bytes < (INT64_C(1) << 40); }
+
+bool rows_aligned32(const void* p, int64_t row_bytes) {
+    return (reinterpret_cast<uintptr_t>(p) & 31u) == 0 && row_bytes % 32 == 0;
+}
+
+}  // namespace
+
+template <int FORM>
+cudaError_t plan_form() {
+    return cudaFuncSetAttribute(grouped_gemm_kernel<FORM, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+}
+
+cudaError_t plan_gemm() {
+    cudaError_t err = plan_form<kForward>();
+    if (err == cudaSuccess) err = plan_form<kTransposed>();
+    if (err == cudaSuccess) err = plan_form<kWeightGrad>();
+    if (err == cudaSuccess) err = plan_form<kFp8>();
+    return err;
+}
+
+}  // namespace ep
+
+using namespace ep;
+
+extern "C" {
+
+ep_status ep_grouped_gemm(ep_handle* h, int64_t num_rows, int32_t n, int32_t k, const int32_t* group_count,
+                          const int32_t* group_begin, const void* x, int64_t x_row_bytes, const void* w,
+                          int32_t w_transposed, void* out, int64_t out_row_bytes, int64_t expected_rows,
+                          ep_stream_t stream) {
+    EP_TRACE();
+    GemmParams p = {};
+    const ep_status st = check_groups(h, num_rows, n, k, group_count, group_begin, &p);
+    if (st != EP_OK) return st;
+    EP_CHECK_ARG(expected_rows >= 0, "expected_rows %lld < 0", static_cast<long long>(expected_rows));
+    if (num_rows == 0) return EP_OK;
+    EP_CHECK_ARG(x && w && out && aligned16(x) && aligned16(w) && aligned16(out),
+                 "x, w and out must be 16-byte aligned device pointers");
+    EP_CHECK_ARG(row_stride_ok(x_row_bytes, 2 * static_cast<int64_t>(k)) &&
+                     row_stride_ok(out_row_bytes, 2 * static_cast<int64_t>(n)),
+                 "row strides must be multiples of 16 that hold a row (x %lld, out %lld bytes)",
+                 static_cast<long long>(x_row_bytes), static_cast<long long>(out_row_bytes));
+    p.cols_dim = n;
+    p.contraction = k;
+    p.out = out;
+    p.out_row_bytes = out_row_bytes;
+    p.wide_stores = rows_aligned32(out, out_row_bytes);
+    const Operand a = row_operand(x, false, k, num_rows, x_row_bytes, kRowBox);
+    return w_transposed ? launch<kTransposed>(h, a, weight_operand(w, false, n, k, p.groups.groups), p, stream)
+                        : launch<kForward>(h, a, weight_operand(w, false, k, n, p.groups.groups), p, stream);
+}
+
+ep_status ep_grouped_gemm_wgrad(ep_handle* h, int64_t num_rows, int32_t n, int32_t k, const int32_t* group_count,
+                                const int32_t* group_begin, const void* dy, int64_t dy_row_bytes, const void* x,
+                                int64_t x_row_bytes, void* dw, ep_dtype dw_dtype, int32_t accumulate,
+                                ep_stream_t stream) {
+    EP_TRACE();
+    GemmParams p = {};
+    const ep_status st = check_groups(h, num_rows, n, k, group_count, group_begin, &p);
+    if (st != EP_OK) return st;
+    EP_CHECK_ARG(dw_dtype == EP_FP32 || dw_dtype == EP_BF16, "dw_dtype must be EP_FP32 or EP_BF16");
+    EP_CHECK_ARG(!accumulate || dw_dtype == EP_FP32, "accumulate needs an fp32 dw");
+    EP_CHECK_ARG(dw && aligned16(dw), "dw must be a 16-byte aligned device pointer");
+    if (num_rows == 0) {
+        if (accumulate) return EP_OK;
+        DeviceGuard guard(h->device);
+        const size_t bytes = static_cast<size_t>(p.groups.groups) * n * k * (dw_dtype == EP_FP32 ? 4 : 2);
+        const cudaError_t err = cudaMemsetAsync(dw, 0, bytes, stream);
+        return err == cudaSuccess ? EP_OK : cuda_fail(err, "clearing dw");
+    }
+    EP_CHECK_ARG(dy && x && aligned16(dy) && aligned16(x), "dy and x must be 16-byte aligned device pointers");
+    EP_CHECK_ARG(row_stride_ok(x_row_bytes, 2 * static_cast<int64_t>(k)) &&
+                     row_stride_ok(dy_row_bytes, 2 * static_cast<int64_t>(n)),
+                 "row strides must be multiples of 16 that hold a row (x %lld, dy %lld bytes)",
+                 static_cast<long long>(x_row_bytes), static_cast<long long>(dy_row_bytes));
+    p.rows_dim = n;
+    p.cols_dim = k;
+    p.out = dw;
+    p.out_fp32 = dw_dtype == EP_FP32;
+    p.accumulate = accumulate != 0;
+    p.out_row_bytes = static_cast<int64_t>(k) * (p.out_fp32 ? 4 : 2);
+    p.wide_stores = rows_aligned32(dw, p.out_row_bytes);
+    return launch<kWeightGrad>(h, row_operand(dy, false, n, num_rows, dy_row_bytes, 64),
+                               row_operand(x, false, k, num_rows, x_row_bytes, 64), p, stream);
+}
+
+ep_status ep_grouped_gemm_fp8(ep_handle* h, int64_t num_rows, int32_t n, int32_t k, const int32_t* group_count,
+                              const int32_t* group_begin, const void* x, int64_t x_row_bytes, const void* x_scales,
+                              int64_t x_scale_row_bytes, int32_t scales_ue8m0, const void* w, const float* w_scales,
+                              void* out, int64_t out_row_bytes, int64_t expected_rows, ep_stream_t stream) {
+    EP_TRACE();
+    GemmParams p = {};
+    const ep_status st = check_groups(h, num_rows, n, k, group_count, group_begin, &p);
+    if (st != EP_OK) return st;
+    if (k % kFp8Group != 0) return fail(EP_ERR_UNSUPPORTED, "FP8 products need k %% 128 == 0 (k %d)", k);
+    EP_CHECK_ARG(expected_rows >= 0, "expected_rows %lld < 0", static_cast<long long>(expected_rows));
+    if (num_rows == 0) return EP_OK;
+    EP_CHECK_ARG(x && w && out && aligned16(x) && aligned16(w) && aligned16(out),
+                 "x, w and out must be 16-byte aligned device pointers");
+    EP_CHECK_ARG(row_stride_ok(x_row_bytes, k) && row_stride_ok(out_row_bytes, 2 * static_cast<int64_t>(n)),
+                 "row strides must be multiples of 16 that hold a row (x %lld, out %lld bytes)",
+                 static_cast<long long>(x_row_bytes), static_cast<long long>(out_row_bytes));
+    const int64_t scale_row = static_cast<int64_t>(k / kFp8Group) * (scales_ue8m0 ? 1 : 4);
+    EP_CHECK_ARG(x_scales && w_scales && aligned4(w_scales) && x_scale_row_bytes >= scale_row &&
+                     (scales_ue8m0 || (aligned4(x_scales) && x_scale_row_bytes % 4 == 0)),
+                 "x_scales or w_scales missing or misaligned, or x_scale_row_bytes %lld too small",
+                 static_cast<long long>(x_scale_row_bytes));
+    p.cols_dim = n;
+    p.contraction = k;
+    p.out = out;
+    p.out_row_bytes = out_row_bytes;
+    p.wide_stores = rows_aligned32(out, out_row_bytes);
+    p.x_scales = static_cast<const uint8_t*>(x_scales);
+    p.x_scale_row_bytes = x_scale_row_bytes;
+    p.scales_ue8m0 = scales_ue8m0 != 0;
+    p.w_scales = w_scales;
+    return launch<kFp8>(h, row_operand(x, true, k, num_rows, x_row_bytes, kRowBox),
+                        weight_operand(w, true, k, n, p.groups.groups), p, stream);
+}
+
+}  // extern "C"

@@ -30,6 +30,13 @@ constexpr int kLLCountThreads = 512;
 constexpr int kLLDispatchThreads = 512;
 constexpr int kLLCombineThreads = 256;
 
+// Top-k slots of one rank that a CTA of the expert layout's counting sort takes, and how many such chunks a rank has.
+constexpr int kLayoutChunk = 2048;
+inline int64_t layout_chunks(const ep_config& c) {
+    const int64_t n = (c.recv_capacity * c.num_topk + kLayoutChunk - 1) / kLayoutChunk;
+    return n > 0 ? n : 1;
+}
+
 enum DispatchMode { kModeBf16 = 0, kModeCastFp8 = 1, kModeFp8In = 2 };
 
 cudaError_t plan_launches(LaunchPlan* plan, int device, int num_experts);

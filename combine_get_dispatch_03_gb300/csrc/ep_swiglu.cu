@@ -1,0 +1,240 @@
+// ep_swiglu.cu -- the gated activation between an expert's two products, and its gradient (sm_103a).
+//
+// A row of the first product holds gate and up values, [gate: width][up: width] bf16.  With
+// sig = 1 / (1 + exp(-gate)) and the row's weight p (1 without weights):
+//   forward    v = gate * sig * up * p, to bf16, or to e4m3 codes and one scale per 128 columns
+//   gradient   dgate = dv * p * up * sig * (1 + gate * (1 - sig));  dup = dv * p * gate * sig;
+//              dp = sum over the row of dv * gate * sig * up
+// All in fp32, rounded once.  exp and the reciprocal are the hardware's approximations (2 ulp each for the
+// |gate| that leaves a value bf16 can tell from 0): with the correctly rounded ones the forward pass was bound by
+// its instructions and not by memory.
+//
+// A warp owns a row: 32 lanes of 8 columns, so that a scale's 128 columns are 16 lanes and their maximum four
+// shuffles.  Only rows of a group are touched; warps stride over them through the group table.
+#include "ep_groups.cuh"
+#include "ep_handle.h"
+#include "ep_trace.h"
+
+namespace ep {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kLaneCols = 8;
+constexpr int kWarpCols = kWarpSize * kLaneCols;
+
+struct SwigluParams {
+    Groups groups;
+    int32_t width;
+    int32_t round_scale;
+    const uint8_t* x;
+    int64_t x_row_bytes;
+    const uint8_t* dy;
+    int64_t dy_row_bytes;
+    const float* row_weights;
+    uint8_t* out;
+    int64_t out_row_bytes;
+    float* out_scales;      // [num_rows][width / 128]
+    float* d_row_weights;   // [num_rows]
+    int32_t* status;
+};
+
+enum SwigluForm { kToBf16 = 0, kToFp8 = 1, kGradient = 2 };
+
+// rcp.approx keeps the subnormal results that __fdividef turns into 0: gates down to -88.7 leave a sigmoid.
+__device__ __forceinline__ float sigmoid(float g) {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-g)));
+    return r;
+}
+
+template <int FORM>
+__device__ __forceinline__ void swiglu_row(const SwigluParams& p, int64_t row) {
+    const uint8_t* gate = p.x + row * p.x_row_bytes;
+    const uint8_t* up = gate + 2 * static_cast<int64_t>(p.width);
+    const uint8_t* dy = FORM == kGradient ? p.dy + row * p.dy_row_bytes : nullptr;
+    uint8_t* out = p.out + row * p.out_row_bytes;
+    const float weight = p.row_weights ? p.row_weights[row] : 1.0f;
+    float dp = 0.0f;
+    // two passes of 256 columns at a time: up to six 16-byte loads of a lane in flight
+    for (int c0 = 0; c0 < p.width; c0 += 2 * kWarpCols) {
+        int4 g4[2], u4[2], d4[2];
+        int col[2];
+        bool in[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            col[i] = c0 + i * kWarpCols + lane_id() * kLaneCols;
+            in[i] = col[i] < p.width;
+            if (in[i]) {
+                g4[i] = ld_stream_v4(reinterpret_cast<const int4*>(gate + 2 * col[i]));
+                u4[i] = ld_stream_v4(reinterpret_cast<const int4*>(up + 2 * col[i]));
+                if (FORM == kGradient) d4[i] = ld_stream_v4(reinterpret_cast<const int4*>(dy + 2 * col[i]));
+            } else {
+                g4[i] = u4[i] = d4[i] = make_int4(0, 0, 0, 0);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (c0 + i * kWarpCols >= p.width) break;
+            float g[8], u[8];
+            unpack8(g4[i], g);
+            unpack8(u4[i], u);
+            if constexpr (FORM == kGradient) {
+                float d[8], dg[8], du[8];
+                unpack8(d4[i], d);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float sig = sigmoid(g[j]);
+                    const float act = g[j] * sig;
+                    const float dv = d[j] * weight;
+                    dg[j] = dv * u[j] * (sig * (1.0f + g[j] * (1.0f - sig)));
+                    du[j] = dv * act;
+                    dp += d[j] * act * u[j];
+                }
+                if (in[i]) {
+                    st_stream_v4(reinterpret_cast<int4*>(out + 2 * col[i]), pack8_bf16(dg));
+                    st_stream_v4(reinterpret_cast<int4*>(out + 2 * (static_cast<int64_t>(p.width) + col[i])), pack8_bf16(du));
+                }
+            } else {
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = g[j] * sigmoid(g[j]) * u[j] * weight;
+                if constexpr (FORM == kToBf16) {
+                    if (in[i]) st_stream_v4(reinterpret_cast<int4*>(out + 2 * col[i]), pack8_bf16(v));
+                } else {
+                    float amax = absmax8(v);
+#pragma unroll
+                    for (int o = 1; o < kFp8Group / kLaneCols; o <<= 1)
+                        amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, o));
+                    const Fp8Scale s = fp8_scale(amax, p.round_scale != 0);
+                    if (in[i]) {
+                        st_stream_v2(reinterpret_cast<int2*>(out + col[i]), cast8_e4m3(v, s.mult));
+                        if (lane_id() % (kFp8Group / kLaneCols) == 0)
+                            p.out_scales[row * (p.width / kFp8Group) + col[i] / kFp8Group] = s.scale;
+                    }
+                }
+            }
+        }
+    }
+    if (FORM == kGradient && p.d_row_weights) {
+#pragma unroll
+        for (int o = kWarpSize / 2; o > 0; o >>= 1) dp += __shfl_xor_sync(kFullMask, dp, o);
+        if (lane_id() == 0) p.d_row_weights[row] = dp;
+    }
+}
+
+template <int FORM>
+__global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluParams p) {
+    extern __shared__ int32_t table[];
+    __shared__ int32_t sums[kThreads / kWarpSize];
+    const int groups = p.groups.groups;
+    int32_t* before = table;              // [groups] rows before each group
+    int32_t* begin = table + groups;      // [groups]
+    pdl_enter();
+    const int per = (groups + kThreads - 1) / kThreads;
+    const int first = threadIdx.x * per, last = min(first + per, groups);
+    int sum = 0, total = 0;
+    for (int g = first; g < last; ++g) {
+        const Group q = load_group(p.groups, g, p.status);
+        before[g] = sum;
+        begin[g] = q.begin;
+        sum += q.count;
+    }
+    const int base = block_prefix<kThreads>(sum, sums, &total);
+    for (int g = first; g < last; ++g) before[g] += base;
+    __syncthreads();
+    const int warps = gridDim.x * (kThreads / kWarpSize);
+    for (int i = blockIdx.x * (kThreads / kWarpSize) + threadIdx.x / kWarpSize; i < total; i += warps) {
+        const int g = find_group(before, groups, i);
+        swiglu_row<FORM>(p, static_cast<int64_t>(begin[g]) + (i - before[g]));
+    }
+}
+
+template <int FORM>
+ep_status launch(const ep_handle* h, const SwigluParams& p, cudaStream_t stream) {
+    DeviceGuard guard(h->device);
+    // no more warps than rows, and no more CTAs than fill the SMs' threads once
+    const int64_t wanted = (p.groups.num_rows + kThreads / kWarpSize - 1) / (kThreads / kWarpSize);
+    const int64_t most = static_cast<int64_t>(h->plan.num_sms) * (2048 / kThreads);
+    const cudaError_t err = launch_kernel(swiglu_kernel<FORM>, dim3(static_cast<unsigned>(wanted < most ? wanted : most)),
+                                          dim3(kThreads), 2 * sizeof(int32_t) * p.groups.groups, stream, 1, p);
+    if (err != cudaSuccess) return cuda_fail(err, "swiglu launch");
+    return EP_OK;
+}
+
+ep_status check(const ep_handle* h, int64_t num_rows, int32_t width, const int32_t* group_count,
+                const int32_t* group_begin, const void* x, int64_t x_row_bytes, const float* row_weights,
+                SwigluParams* p) {
+    if (h == nullptr) return fail(EP_ERR_INVALID_ARG, "handle is NULL");
+    const ep_status st = check_group_args(h, num_rows, group_count, group_begin);
+    if (st != EP_OK) return st;
+    EP_CHECK_ARG(width >= 8 && width % 8 == 0 && width <= (1 << 28), "width %d must be a positive multiple of 8", width);
+    EP_CHECK_ARG(num_rows == 0 || (x && aligned16(x)), "x must be a 16-byte aligned device pointer");
+    EP_CHECK_ARG(x_row_bytes >= 4 * static_cast<int64_t>(width) && x_row_bytes % 16 == 0,
+                 "x_row_bytes %lld must be a multiple of 16 and hold 2 * width = %d values",
+                 static_cast<long long>(x_row_bytes), 2 * width);
+    EP_CHECK_ARG(aligned4(row_weights), "misaligned row_weights");
+    p->groups = {group_count, group_begin, num_rows, static_cast<int32_t>(num_rows / h->cfg.num_experts),
+                 h->cfg.num_experts};
+    p->width = width;
+    p->x = static_cast<const uint8_t*>(x);
+    p->x_row_bytes = x_row_bytes;
+    p->row_weights = row_weights;
+    p->status = h->status;
+    return EP_OK;
+}
+
+}  // namespace
+}  // namespace ep
+
+using namespace ep;
+
+extern "C" {
+
+ep_status ep_swiglu(ep_handle* h, int64_t num_rows, int32_t width, const int32_t* group_count,
+                    const int32_t* group_begin, const void* x, int64_t x_row_bytes, const float* row_weights,
+                    int32_t cast_to_fp8, int32_t round_scale, void* out, int64_t out_row_bytes, float* out_scales,
+                    ep_stream_t stream) {
+    EP_TRACE();
+    SwigluParams p = {};
+    const ep_status st = check(h, num_rows, width, group_count, group_begin, x, x_row_bytes, row_weights, &p);
+    if (st != EP_OK) return st;
+    if (cast_to_fp8 && width % kFp8Group != 0)
+        return fail(EP_ERR_UNSUPPORTED, "the FP8 cast needs width %% 128 == 0 (width %d)", width);
+    EP_CHECK_ARG(cast_to_fp8 || (!round_scale && out_scales == nullptr), "scales go with cast_to_fp8");
+    EP_CHECK_ARG(!cast_to_fp8 || num_rows == 0 || (out_scales && aligned4(out_scales)), "cast_to_fp8 needs out_scales");
+    EP_CHECK_ARG(num_rows == 0 || (out && aligned16(out)), "out must be a 16-byte aligned device pointer");
+    EP_CHECK_ARG(out_row_bytes >= static_cast<int64_t>(width) * (cast_to_fp8 ? 1 : 2) && out_row_bytes % 16 == 0,
+                 "out_row_bytes %lld must be a multiple of 16 that holds a row", static_cast<long long>(out_row_bytes));
+    if (num_rows == 0) return EP_OK;
+    p.round_scale = round_scale != 0;
+    p.out = static_cast<uint8_t*>(out);
+    p.out_row_bytes = out_row_bytes;
+    p.out_scales = out_scales;
+    return cast_to_fp8 ? launch<kToFp8>(h, p, stream) : launch<kToBf16>(h, p, stream);
+}
+
+ep_status ep_swiglu_grad(ep_handle* h, int64_t num_rows, int32_t width, const int32_t* group_count,
+                         const int32_t* group_begin, const void* dy, int64_t dy_row_bytes, const void* x,
+                         int64_t x_row_bytes, const float* row_weights, void* dx, int64_t dx_row_bytes,
+                         float* d_row_weights, ep_stream_t stream) {
+    EP_TRACE();
+    SwigluParams p = {};
+    const ep_status st = check(h, num_rows, width, group_count, group_begin, x, x_row_bytes, row_weights, &p);
+    if (st != EP_OK) return st;
+    EP_CHECK_ARG(num_rows == 0 || (dy && dx && aligned16(dy) && aligned16(dx)),
+                 "dy and dx must be 16-byte aligned device pointers");
+    EP_CHECK_ARG(dy_row_bytes >= 2 * static_cast<int64_t>(width) && dy_row_bytes % 16 == 0 &&
+                     dx_row_bytes >= 4 * static_cast<int64_t>(width) && dx_row_bytes % 16 == 0,
+                 "row strides must be multiples of 16 that hold a row (dy %lld, dx %lld bytes)",
+                 static_cast<long long>(dy_row_bytes), static_cast<long long>(dx_row_bytes));
+    EP_CHECK_ARG(aligned4(d_row_weights), "misaligned d_row_weights");
+    if (num_rows == 0) return EP_OK;
+    p.dy = static_cast<const uint8_t*>(dy);
+    p.dy_row_bytes = dy_row_bytes;
+    p.out = static_cast<uint8_t*>(dx);
+    p.out_row_bytes = dx_row_bytes;
+    p.d_row_weights = d_row_weights;
+    return launch<kGradient>(h, p, stream);
+}
+
+}  // extern "C"

@@ -52,7 +52,9 @@ EXPORTS = ("ep_handle_create", "ep_handle_destroy", "ep_handle_status", "ep_hand
            "ep_get_dispatch_layout", "ep_dispatch", "ep_combine", "ep_ll_msg_bytes", "ep_ll_dispatch",
            "ep_ll_combine", "ep_ll_dispatch_noalloc", "ep_notify_dispatch", "ep_update_mask_buffer",
            "ep_query_mask_buffer", "ep_clean_mask_buffer", "ep_selftest_bounded_wait", "ep_ll_combine_strided",
-           "ep_expected_topk", "ep_theoretical_num_sms", "ep_layout_notify")
+           "ep_expected_topk", "ep_theoretical_num_sms", "ep_layout_notify", "ep_grouped_gemm",
+           "ep_grouped_gemm_wgrad", "ep_grouped_gemm_fp8", "ep_swiglu", "ep_swiglu_grad",
+           "ep_expert_layout", "ep_expert_gather", "ep_expert_reduce")
 
 
 def library_path() -> str:
@@ -100,11 +102,21 @@ def lib():
         L.ep_selftest_bounded_wait.argtypes = [P, ctypes.c_uint32, I32, P]
         L.ep_ll_dispatch_noalloc.argtypes = [I32, I32, I32, I32, I32, I32, P, P, I32, I32, I32, P, P, P, P, P, P,
                                              P]
+        L.ep_grouped_gemm.argtypes = [P, I64, I32, I32, P, P, P, I64, P, I32, P, I64, I64, P]
+        L.ep_grouped_gemm_wgrad.argtypes = [P, I64, I32, I32, P, P, P, I64, P, I64, P, S, I32, P]
+        L.ep_grouped_gemm_fp8.argtypes = [P, I64, I32, I32, P, P, P, I64, P, I64, I32, P, P, P, I64, I64, P]
+        L.ep_swiglu.argtypes = [P, I64, I32, P, P, P, I64, P, I32, I32, P, I64, P, P]
+        L.ep_swiglu_grad.argtypes = [P, I64, I32, P, P, P, I64, P, I64, P, P, I64, P, P]
+        L.ep_expert_layout.argtypes = [P, P, P, I64, P, P, P, P]
+        L.ep_expert_gather.argtypes = [P, P, S, P, P, P, P, I64, P, P, P, P]
+        L.ep_expert_reduce.argtypes = [P, P, I64, P, P, P, I64, P, P, P]
         for name in ("ep_handle_create", "ep_handle_status", "ep_handle_num_recv", "ep_handle_export",
                      "ep_get_dispatch_layout", "ep_dispatch", "ep_combine", "ep_ll_dispatch", "ep_ll_combine",
                      "ep_ll_dispatch_noalloc", "ep_notify_dispatch", "ep_update_mask_buffer",
                      "ep_query_mask_buffer", "ep_clean_mask_buffer", "ep_selftest_bounded_wait",
-                     "ep_ll_combine_strided", "ep_layout_notify"):
+                     "ep_ll_combine_strided", "ep_layout_notify", "ep_grouped_gemm", "ep_grouped_gemm_wgrad",
+                     "ep_grouped_gemm_fp8", "ep_swiglu", "ep_swiglu_grad", "ep_expert_layout", "ep_expert_gather",
+                     "ep_expert_reduce"):
             getattr(L, name).restype = S
         _lib = L
     return _lib
@@ -533,6 +545,225 @@ def ep_ll_combine(h: Handle, x: torch.Tensor, topk_idx: torch.Tensor, topk_weigh
         _ptr(topk_weights, "topk_weights", torch.float32, (R, T, K), d),
         _ptr(combined_x, "combined_x", torch.bfloat16, (R, T, H), d), _stream(stream, h.device)))
     return combined_x
+
+
+def _rows(t, name, dtype, device, rows=None, width=None):
+    """(address, rows, width, row stride in bytes) of a row operand of the expert products: [rows][width], or a view
+    such as [R][EL][R*maxT][width], whose rows are evenly spaced and contiguous inside."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the handle lives on {device}")
+    if t.dim() < 2:
+        raise ValueError(f"{name} must be [rows][width], got {tuple(t.shape)}")
+    n, inner = t.numel() // t.shape[-1] if t.shape[-1] else 0, t.shape[-1]
+    if (rows is not None and n != rows) or (width is not None and inner != width):
+        raise ValueError(f"{name}: {n} rows of {inner}, expected {n if rows is None else rows} of "
+                         f"{inner if width is None else width}")
+    step = None  # elements between rows; an axis of one entry has no say in it
+    span = 1
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if step is None:
+            step = stride
+        elif stride != step * span:
+            raise ValueError(f"{name}: its rows are not evenly spaced")
+        span *= size
+    if n and inner > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    row_bytes = (inner if step is None else step) * t.element_size()
+    if step is None:  # one row: any stride will do
+        row_bytes = (row_bytes + 15) // 16 * 16
+    return (t.data_ptr() if t.numel() else _dummy(device).data_ptr()), n, inner, row_bytes
+
+
+def _group_arrays(h, group_count, group_begin):
+    E = (h.cfg.num_experts,)
+    if group_count is not None and group_count.dim() == 2:  # packed_recv_count [R][EL]
+        group_count = group_count.reshape(-1)
+    return (_ptr(group_count, "group_count", torch.int32, E, h.device),
+            _ptr(group_begin, "group_begin", torch.int32, E, h.device))
+
+
+def ep_grouped_gemm(h: Handle, x: torch.Tensor, w: torch.Tensor, group_count, group_begin=None,
+                    w_transposed: bool = False, out=None, expected_rows: int = 0, stream=None):
+    """Grouped product: each expert's rows times its bf16 weights w [E][n][k] (or, transposed, [E][k][n]).
+
+    x is [rows][k] or a view with evenly spaced rows, such as the packed_recv_x of a bf16 message buffer; out has
+    x's leading axes.  Rows outside every group are left as they are."""
+    d = h.device
+    if w.dim() != 3:
+        raise ValueError(f"w must be [E][n][k], got {tuple(w.shape)}")
+    n, k = (w.shape[2], w.shape[1]) if w_transposed else (w.shape[1], w.shape[2])
+    xp, rows, _, xs = _rows(x, "x", torch.bfloat16, d, None, k)
+    if out is None:
+        out = _empty(x.shape[:-1] + (n,), torch.bfloat16, d)
+    op, _, _, os_ = _rows(out, "out", torch.bfloat16, d, rows, n)
+    cnt, beg = _group_arrays(h, group_count, group_begin)
+    _raise(lib().ep_grouped_gemm(h.ptr, rows, n, k, cnt, beg, xp, xs,
+                                 _ptr(w, "w", torch.bfloat16, (h.cfg.num_experts,) + tuple(w.shape[1:]), d),
+                                 int(bool(w_transposed)), op, os_, expected_rows, _stream(stream, d)))
+    return out
+
+
+def ep_grouped_gemm_wgrad(h: Handle, dy: torch.Tensor, x: torch.Tensor, group_count, group_begin=None, out=None,
+                          out_dtype=torch.float32, accumulate: bool = False, stream=None):
+    """Weight gradient of a grouped product: dw[e] = dy_e^T x_e, [E][n][k], fp32 (or bf16)."""
+    d = h.device
+    xp, rows, k, xs = _rows(x, "x", torch.bfloat16, d)
+    yp, _, n, ys = _rows(dy, "dy", torch.bfloat16, d, rows)
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = _empty((h.cfg.num_experts, n, k), out_dtype, d)
+    if out.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("the weight gradient is float32 or bfloat16")
+    cnt, beg = _group_arrays(h, group_count, group_begin)
+    _raise(lib().ep_grouped_gemm_wgrad(h.ptr, rows, n, k, cnt, beg, yp, ys, xp, xs,
+                                       _ptr(out, "out", out.dtype, (h.cfg.num_experts, n, k), d),
+                                       EP_FP32 if out.dtype == torch.float32 else EP_BF16, int(bool(accumulate)),
+                                       _stream(stream, d)))
+    return out
+
+
+def ep_grouped_gemm_fp8(h: Handle, x: torch.Tensor, x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                        group_count, group_begin=None, out=None, expected_rows: int = 0, stream=None):
+    """Grouped product in FP8 e4m3: x rows with one scale per 128 channels, w [E][n][k] with one per 128 x 128.
+
+    x_scales is float32 [rows][k/128], or uint8 with the UE8M0 exponent bytes in its first k/128 columns; the views
+    that ll_views() gives of a message buffer are read in place (for fp32 scales: scales.view(torch.float32))."""
+    d = h.device
+    if w.dim() != 3:
+        raise ValueError(f"w must be [E][n][k], got {tuple(w.shape)}")
+    E, n, k = w.shape
+    G = k // 128
+    xp, rows, _, xs = _rows(x, "x", torch.float8_e4m3fn, d, None, k)
+    if x_scales.dtype not in (torch.float32, torch.uint8):
+        raise TypeError(f"x_scales: dtype {x_scales.dtype}, expected float32 or uint8")
+    ue8m0 = x_scales.dtype == torch.uint8
+    if ue8m0:
+        if x_scales.dim() < 2 or x_scales.shape[-1] < G:
+            raise ValueError(f"x_scales must hold {G} exponent bytes per row, got {tuple(x_scales.shape)}")
+        x_scales = x_scales[..., :G]
+    sp, _, _, ss = _rows(x_scales, "x_scales", x_scales.dtype, d, rows, G)
+    if out is None:
+        out = _empty(x.shape[:-1] + (n,), torch.bfloat16, d)
+    op, _, _, os_ = _rows(out, "out", torch.bfloat16, d, rows, n)
+    cnt, beg = _group_arrays(h, group_count, group_begin)
+    _raise(lib().ep_grouped_gemm_fp8(h.ptr, rows, n, k, cnt, beg, xp, xs, sp, ss, int(ue8m0),
+                                     _ptr(w, "w", torch.float8_e4m3fn, (h.cfg.num_experts, n, k), d),
+                                     _ptr(w_scales, "w_scales", torch.float32, (h.cfg.num_experts, -(-n // 128), G), d),
+                                     op, os_, expected_rows, _stream(stream, d)))
+    return out
+
+
+def ep_swiglu(h: Handle, x: torch.Tensor, group_count, group_begin=None, row_weights=None, cast_to_fp8: bool = False,
+              round_scale: bool = False, out=None, out_scales=None, stream=None):
+    """Gated activation of the experts' rows, [gate | up] bf16 -> silu(gate) * up (* row weight), bf16 or e4m3."""
+    d = h.device
+    xp, rows, wide, xs = _rows(x, "x", torch.bfloat16, d)
+    width = wide // 2
+    if wide != 2 * width:
+        raise ValueError(f"x must hold gate and up of one width, got rows of {wide}")
+    dtype = torch.float8_e4m3fn if cast_to_fp8 else torch.bfloat16
+    if out is None:
+        out = _empty(x.shape[:-1] + (width,), dtype, d)
+    if cast_to_fp8 and out_scales is None:
+        out_scales = _empty(x.shape[:-1] + (width // 128,), torch.float32, d)
+    op, _, _, os_ = _rows(out, "out", dtype, d, rows, width)
+    cnt, beg = _group_arrays(h, group_count, group_begin)
+    _raise(lib().ep_swiglu(h.ptr, rows, width, cnt, beg, xp, xs, _ptr(row_weights, "row_weights", torch.float32, (rows,), d),
+                           int(bool(cast_to_fp8)), int(bool(round_scale)), op, os_,
+                           _ptr(out_scales, "out_scales", torch.float32, tuple(x.shape[:-1]) + (width // 128,), d),
+                           _stream(stream, d)))
+    return dict(out=out, out_scales=out_scales)
+
+
+def ep_swiglu_grad(h: Handle, dy: torch.Tensor, x: torch.Tensor, group_count, group_begin=None, row_weights=None,
+                   dx=None, d_row_weights=None, stream=None):
+    """Gradient of ep_swiglu's bf16 form: dx, and with row_weights their gradient."""
+    d = h.device
+    xp, rows, wide, xs = _rows(x, "x", torch.bfloat16, d)
+    width = wide // 2
+    if wide != 2 * width:
+        raise ValueError(f"x must hold gate and up of one width, got rows of {wide}")
+    yp, _, _, ys = _rows(dy, "dy", torch.bfloat16, d, rows, width)
+    if dx is None:
+        dx = _empty(x.shape, torch.bfloat16, d)
+    if row_weights is not None and d_row_weights is None:
+        d_row_weights = _empty((rows,), torch.float32, d)
+    gp, _, _, gs = _rows(dx, "dx", torch.bfloat16, d, rows, wide)
+    cnt, beg = _group_arrays(h, group_count, group_begin)
+    _raise(lib().ep_swiglu_grad(h.ptr, rows, width, cnt, beg, yp, ys, xp, xs,
+                                _ptr(row_weights, "row_weights", torch.float32, (rows,), d), gp, gs,
+                                _ptr(d_row_weights, "d_row_weights", torch.float32, (rows,), d), _stream(stream, d)))
+    return dict(dx=dx, d_row_weights=d_row_weights)
+
+
+def ep_expert_layout(h: Handle, recv_topk_idx: torch.Tensor, num_rows: int, num_recv=None, group_count=None,
+                     group_begin=None, slot_row=None, stream=None):
+    """Expert order of a normal dispatch's rows: counts and begins of the experts, and the row of every top-k slot.
+
+    num_recv (int32 [R], device) defaults to that of the handle's last normal dispatch."""
+    c, d = h.cfg, h.device
+    R, K, cap, E = c.num_ranks, c.num_topk, c.recv_capacity, c.num_experts
+    if group_count is None:
+        group_count = _empty((E,), torch.int32, d)
+    if group_begin is None:
+        group_begin = _empty((E,), torch.int32, d)
+    if slot_row is None:
+        slot_row = _empty((R, cap, K), torch.int32, d)
+    _raise(lib().ep_expert_layout(
+        h.ptr, _ptr(recv_topk_idx, "recv_topk_idx", torch.int64, (R, cap, K), d),
+        _ptr(num_recv, "num_recv", torch.int32, (R,), d), num_rows,
+        _ptr(group_count, "group_count", torch.int32, (E,), d), _ptr(group_begin, "group_begin", torch.int32, (E,), d),
+        _ptr(slot_row, "slot_row", torch.int32, (R, cap, K), d), _stream(stream, d)))
+    return dict(group_count=group_count, group_begin=group_begin, slot_row=slot_row)
+
+
+def ep_expert_gather(h: Handle, x: torch.Tensor, slot_row: torch.Tensor, num_rows: int, num_recv=None, x_scales=None,
+                     topk_weights=None, out=None, out_scales=None, row_weights=None, stream=None):
+    """Received rows [R][cap][H] (bf16, or e4m3 with scales) into expert order, with their routing weights."""
+    c, d = h.cfg, h.device
+    R, K, cap, H = c.num_ranks, c.num_topk, c.recv_capacity, c.hidden
+    fp8 = x.dtype == torch.float8_e4m3fn
+    dtype = torch.float8_e4m3fn if fp8 else torch.bfloat16
+    if out is None:
+        out = _empty((num_rows, H), dtype, d)
+    if fp8 and out_scales is None:
+        out_scales = _empty((num_rows, H // 128), torch.float32, d)
+    if topk_weights is not None and row_weights is None:
+        row_weights = _empty((num_rows,), torch.float32, d)
+    _raise(lib().ep_expert_gather(
+        h.ptr, _ptr(x, "x", dtype, (R, cap, H), d), EP_FP8_E4M3 if fp8 else EP_BF16,
+        _ptr(x_scales, "x_scales", torch.float32, (R, cap, H // 128), d),
+        _ptr(topk_weights, "topk_weights", torch.float32, (R, cap, K), d),
+        _ptr(slot_row, "slot_row", torch.int32, (R, cap, K), d), _ptr(num_recv, "num_recv", torch.int32, (R,), d),
+        num_rows, _ptr(out, "out", dtype, (num_rows, H), d),
+        _ptr(out_scales, "out_scales", torch.float32, (num_rows, H // 128), d),
+        _ptr(row_weights, "row_weights", torch.float32, (num_rows,), d), _stream(stream, d)))
+    return dict(out=out, out_scales=out_scales, row_weights=row_weights)
+
+
+def ep_expert_reduce(h: Handle, y: torch.Tensor, slot_row: torch.Tensor, num_recv=None, row_weights=None, out=None,
+                     out_topk_weights=None, stream=None):
+    """Expert outputs [rows][H] bf16 summed back into receive rows [R][cap][H] (fp32 sums, slot order)."""
+    c, d = h.cfg, h.device
+    R, K, cap, H = c.num_ranks, c.num_topk, c.recv_capacity, c.hidden
+    yp, rows, _, ys = _rows(y, "y", torch.bfloat16, d, None, H)
+    if out is None:
+        out = _empty((R, cap, H), torch.bfloat16, d)
+    if row_weights is not None and out_topk_weights is None:
+        out_topk_weights = _empty((R, cap, K), torch.float32, d)
+    _raise(lib().ep_expert_reduce(
+        h.ptr, yp, ys, _ptr(slot_row, "slot_row", torch.int32, (R, cap, K), d),
+        _ptr(row_weights, "row_weights", torch.float32, (rows,), d), _ptr(num_recv, "num_recv", torch.int32, (R,), d),
+        rows, _ptr(out, "out", torch.bfloat16, (R, cap, H), d),
+        _ptr(out_topk_weights, "out_topk_weights", torch.float32, (R, cap, K), d), _stream(stream, d)))
+    return dict(out=out, out_topk_weights=out_topk_weights)
 
 
 def recv_hook(stream=None):

@@ -402,6 +402,110 @@ ep_status ep_ll_dispatch_noalloc(int32_t num_ranks, int32_t num_tokens, int32_t 
                                  int32_t* cumulative_local_expert_recv_stats, int32_t* slot_row,
                                  int32_t* status, ep_stream_t stream);
 
+/* ------------------------------------------------------------ expert products
+ * What the experts compute between a dispatch and a combine.  Rows of all
+ * experts lie in one array of num_rows rows; expert e (0 <= e < E, the
+ * handle's num_experts; e = d * EL + j for local expert j of rank d) has the
+ * rows [begin, begin + group_count[e]) with begin = group_begin[e], or
+ * e * (num_rows / E) when group_begin is NULL -- the [R][EL][R*maxT] rows of
+ * low-latency mode with group_count = packed_recv_count.  Both arrays are
+ * int32 [E] in device memory; groups may be empty, and rows outside every
+ * group are neither used nor written.  A group that passes num_rows (or
+ * num_rows / E without group_begin), or with a negative begin or count, sets
+ * EP_ERR_CAPACITY; the rows that do not fit are left out.
+ * Row operands and outputs have row strides in bytes: multiples of 16, base
+ * 16-byte aligned.  n and k are multiples of 8.  Sums are fp32, rounded once.
+ * NaN and infinities in a row reach that row's outputs only (a weight
+ * gradient: its expert's). */
+
+/* Grouped product, bf16: for every row r of expert e
+ *   w_transposed == 0:  out[r][j] = sum_c x[r][c] * w[e][j][c]   w [E][n][k]
+ *   w_transposed != 0:  out[r][j] = sum_c x[r][c] * w[e][c][j]   w [E][k][n]
+ * j < n, c < k; x rows of k, out rows of n bf16.  With the weights [E][n'][k']
+ * of a forward product, the transposed form with n = k', k = n' is the
+ * gradient of its rows.  expected_rows: rows that a group in use is expected to hold
+ * (0: num_rows / E); it only guides the choice of tiles. */
+ep_status ep_grouped_gemm(ep_handle* h, int64_t num_rows, int32_t n, int32_t k, const int32_t* group_count,
+                          const int32_t* group_begin, const void* x, int64_t x_row_bytes, const void* w,
+                          int32_t w_transposed, void* out, int64_t out_row_bytes, int64_t expected_rows,
+                          ep_stream_t stream);
+
+/* Gradient of the weights of a grouped product, for every expert e:
+ *   dw[e][j][c] = sum over e's rows r of dy[r][j] * x[r][c]      dw [E][n][k], contiguous
+ * dy rows of n, x rows of k bf16; dw fp32 or bf16 (dw_dtype).  An expert
+ * without rows gets zeros.  accumulate != 0 (fp32 only): adds to what dw holds. */
+ep_status ep_grouped_gemm_wgrad(ep_handle* h, int64_t num_rows, int32_t n, int32_t k, const int32_t* group_count,
+                                const int32_t* group_begin, const void* dy, int64_t dy_row_bytes, const void* x,
+                                int64_t x_row_bytes, void* dw, ep_dtype dw_dtype, int32_t accumulate,
+                                ep_stream_t stream);
+
+/* Grouped product in FP8: for every row r of expert e, with blocks b of 128
+ * channels,
+ *   out[r][j] = sum_b x_scales[r][b] * w_scales[e][j / 128][b] * sum_{c in b} x[r][c] * w[e][j][c]
+ * x rows of k e4m3 codes (k a multiple of 128); x_scales: k/128 fp32 per row,
+ * or with scales_ue8m0 k/128 exponent bytes (scale 2^(byte - 127), 255 = NaN),
+ * rows x_scale_row_bytes apart; w [E][n][k] e4m3, w_scales fp32
+ * [E][ceil(n/128)][k/128]; out bf16 rows of n.  Low-latency messages are read
+ * in place: x = recv_msgs + 16 and x_scales = recv_msgs + 16 + H, both with
+ * row strides ep_ll_msg_bytes(H, 1).  A handle with one expert makes this a
+ * dense product.  expected_rows as in ep_grouped_gemm(). */
+ep_status ep_grouped_gemm_fp8(ep_handle* h, int64_t num_rows, int32_t n, int32_t k, const int32_t* group_count,
+                              const int32_t* group_begin, const void* x, int64_t x_row_bytes, const void* x_scales,
+                              int64_t x_scale_row_bytes, int32_t scales_ue8m0, const void* w, const float* w_scales,
+                              void* out, int64_t out_row_bytes, int64_t expected_rows, ep_stream_t stream);
+
+/* Gated activation between an expert's two products.  A row of x holds
+ * [gate: width][up: width] bf16; for every row r of every expert
+ *   v[r][j] = gate * sigmoid(gate) * up * row_weights[r]      (row_weights fp32 [num_rows], NULL = 1)
+ * in fp32, then cast_to_fp8 == 0: out = bf16 rows of width; cast_to_fp8 != 0
+ * (width a multiple of 128): out = rows of width e4m3 codes and out_scales
+ * (fp32 [num_rows][width/128]) by the dispatch's rule (amax = max(max|v|,
+ * 1e-4), scale = amax/448; round_scale != 0: the next power of two). */
+ep_status ep_swiglu(ep_handle* h, int64_t num_rows, int32_t width, const int32_t* group_count,
+                    const int32_t* group_begin, const void* x, int64_t x_row_bytes, const float* row_weights,
+                    int32_t cast_to_fp8, int32_t round_scale, void* out, int64_t out_row_bytes, float* out_scales,
+                    ep_stream_t stream);
+
+/* Its gradient, from dy (the gradient of the bf16 output, rows of width):
+ * dx (rows of 2 * width bf16) and, if not NULL, d_row_weights (fp32 [num_rows]):
+ *   d gate = dy * w * up * s * (1 + gate * (1 - s)),  s = sigmoid(gate)
+ *   d up   = dy * w * gate * s,   d w = sum_j dy * gate * s * up */
+ep_status ep_swiglu_grad(ep_handle* h, int64_t num_rows, int32_t width, const int32_t* group_count,
+                         const int32_t* group_begin, const void* dy, int64_t dy_row_bytes, const void* x,
+                         int64_t x_row_bytes, const float* row_weights, void* dx, int64_t dx_row_bytes,
+                         float* d_row_weights, ep_stream_t stream);
+
+/* A normal dispatch delivers a token once per rank; a grouped product wants
+ * one row per (row, top-k slot), an expert's rows together.  Expert order:
+ * rank, local expert, receive row, slot.  From recv_topk_idx (int64
+ * [R][cap][K], as ep_dispatch() wrote it) and num_recv (int32 [R] on the device;
+ * NULL: that of the handle's last normal dispatch):
+ *   group_count[e], group_begin[e]   int32 [E]; each expert begins at a multiple of expert_alignment
+ *   slot_row[r][row][k]              int32 [R][cap][K]: the slot's row in expert order, -1 for none
+ * num_rows: rows that the expert-order arrays hold; slots past it get -1 and
+ * set EP_ERR_CAPACITY.  A local expert outside [-1, EL) sets
+ * EP_ERR_BAD_EXPERT and gets -1.  Every output element is written.
+ * Needs recv_capacity * num_topk < 2^31 - 2048. */
+ep_status ep_expert_layout(ep_handle* h, const int64_t* recv_topk_idx, const int32_t* num_recv, int64_t num_rows,
+                           int32_t* group_count, int32_t* group_begin, int32_t* slot_row, ep_stream_t stream);
+
+/* Received rows into expert order: out[slot_row[r][row][k]] = x[r][row] for every
+ * slot that has a row (x and out rows of H, bf16, or e4m3 with H/128 fp32 scales), and,
+ * if given, row_weights[slot_row[r][row][k]] = topk_weights[r][row][k].
+ * The gradient of ep_expert_reduce(); rows of padding are not written. */
+ep_status ep_expert_gather(ep_handle* h, const void* x, ep_dtype x_dtype, const float* x_scales,
+                           const float* topk_weights, const int32_t* slot_row, const int32_t* num_recv, int64_t num_rows,
+                           void* out, float* out_scales, float* row_weights, ep_stream_t stream);
+
+/* Expert outputs back into receive rows, the input of ep_combine(): for r and row < num_recv[r],
+ *   out[r][row] = bf16(sum over k with a row of y[slot_row[r][row][k]])     fp32, k ascending
+ * y bf16 rows of H; out bf16 [R][cap][H], later rows are not written.  If
+ * given, out_topk_weights[r][row][k] (fp32) = row_weights[slot_row[r][row][k]], 0
+ * without a row.  The gradient of ep_expert_gather(). */
+ep_status ep_expert_reduce(ep_handle* h, const void* y, int64_t y_row_bytes, const int32_t* slot_row,
+                           const float* row_weights, const int32_t* num_recv, int64_t num_rows, void* out,
+                           float* out_topk_weights, ep_stream_t stream);
+
 /* ------------------------------------------------------------ launch model
  * The SM-count model of [P1] (get_theoretical_num_sms, elastic.py), with the
  * one link of a single GPU -- HBM -- as the bottleneck.  All host-side; no
