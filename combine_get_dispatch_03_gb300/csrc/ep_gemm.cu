@@ -260,14 +260,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         tail_phase ^= 1u << stage;
                         tail_last |= 1u << stage;
                     } else {
-                        cluster_arrive_expect_tx(bar, stage_bytes);
+                        bar_arrive_expect_tx<CG>(bar, stage_bytes);
                         tail_last &= ~(1u << stage);
                     }
                     const int r = q.row0 + s * 64;
                     for (int c = 0; c < kTileRows / 64; ++c) tma_load_2d<CG>(a + c * 8192, &map_a, my_m0 + c * 64, r, bar);
                     for (int c = 0; c < cols_here / 64; ++c) tma_load_2d<CG>(b + c * 8192, &map_b, q.n0 + cb + c * 64, r, bar);
                 } else {
-                    cluster_arrive_expect_tx(bar, boxes * (kRowBox * kRowBytes) + cols_here * kRowBytes);
+                    bar_arrive_expect_tx<CG>(bar, boxes * (kRowBox * kRowBytes) + cols_here * kRowBytes);
                     const int x = s * (FORM == kFp8 ? 128 : 64);
                     for (int c = 0; c < boxes; ++c)
                         tma_load_2d<CG>(a + c * (kRowBox * kRowBytes), &map_a, x, q.row0 + my_m0 + c * kRowBox, bar);
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         fence_async_smem();
                         __syncwarp();
                         if (lane_id() == 0)
-                            cluster_arrive(CG == 1 ? smem_u32(&ctl->full[stage]) : cluster_addr(&ctl->full[stage], 0));
+                            bar_arrive<CG>(CG == 1 ? smem_u32(&ctl->full[stage]) : cluster_addr(&ctl->full[stage], 0));
                     }
                 }
                 if (leader && ok) {
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     if (c + 32 >= cols_half) {  // read out: the accumulator is free before the last stores
                         tc_fence_before();
                         __syncwarp();
-                        if (lane_id() == 0) cluster_arrive(acc_empty0 + 8 * buf);
+                        if (lane_id() == 0) bar_arrive<CG>(acc_empty0 + 8 * buf);
                     }
                     float v[32];
 #pragma unroll
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         }
                         tc_fence_before();
                         __syncwarp();
-                        if (lane_id() == 0) cluster_arrive(acc_empty0 + 8 * buf);
+                        if (lane_id() == 0) bar_arrive<CG>(acc_empty0 + 8 * buf);
                         buf ^= 1;
                         acc_phase ^= buf == 0;
                     }

@@ -69,13 +69,24 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
     return a;
 }
 
-__device__ __forceinline__ void cluster_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// Arrivals at a barrier of this CTA (CG == 1) or, by its address in the cluster's shared window, of any CTA
+// of the pair.  The pair's arrivals are relaxed: what they order is tensor-memory and bulk-copy traffic,
+// which has fences and completion of its own (a release at cluster scope took over 1000 cycles a time).
+template <int CG>
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+    if constexpr (CG == 1)
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+    else
+        asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-__device__ __forceinline__ void cluster_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-                 : "memory");
+template <int CG>
+__device__ __forceinline__ void bar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
+    if constexpr (CG == 1)
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+    else
+        asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                     : "memory");
 }
 
 // ---------------------------------------------------------------------------
