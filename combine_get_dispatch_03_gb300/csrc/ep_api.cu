@@ -20,7 +20,7 @@
 namespace ep {
 cudaError_t plan_dispatch_combine(LaunchPlan* plan, int hidden);
 cudaError_t plan_ll(LaunchPlan* plan, int num_experts);
-cudaError_t plan_gemm();
+cudaError_t plan_gemm(LaunchPlan* plan);
 cudaError_t plan_rows();
 }  // namespace ep
 
@@ -157,7 +157,7 @@ ep_status ep_handle_create(const ep_config* cfg, ep_handle** out) {
     }
     if (err == cudaSuccess) err = ep::plan_dispatch_combine(&h->plan, cfg->hidden);
     if (err == cudaSuccess) err = ep::plan_ll(&h->plan, cfg->num_experts);
-    if (err == cudaSuccess) err = ep::plan_gemm();
+    if (err == cudaSuccess) err = ep::plan_gemm(&h->plan);
     if (err == cudaSuccess) err = ep::plan_rows();
     if (err != cudaSuccess) {
         delete h;

@@ -123,7 +123,7 @@ __device__ __forceinline__ void build_table(Table& t, const GemmParams& p, Contr
     const int workers = gridDim.x / CG;
     int best = kMaxTileCols;
     int64_t best_cost = INT64_MAX;
-    for (int cols = kMaxTileCols; cols >= kColBox; cols >>= 1) {
+    for (int cols = kMaxTileCols; cols >= kColBox * CG; cols >>= 1) {
         const int64_t tiles = static_cast<int64_t>(total) * ((p.cols_dim + cols - 1) / cols);
         const int64_t cost = (tiles + workers - 1) / workers * (cols + 32);
         if (cost < best_cost) best_cost = cost, best = cols;
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         fence_async_smem();
                         __syncwarp();
                         if (lane_id() == 0)
-                            bar_arrive<CG>(CG == 1 ? smem_u32(&ctl->full[stage]) : cluster_addr(&ctl->full[stage], 0));
+                            bar_arrive_written<CG>(CG == 1 ? smem_u32(&ctl->full[stage]) : cluster_addr(&ctl->full[stage], 0));
                     }
                 }
                 if (leader && ok) {
@@ -338,6 +338,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     }
                     ok = warp_wait(&ctl->full[stage], phase, abort_flag, p.status);
                     if (!ok) break;
+                    if (FORM == kWeightGrad && q.rows - s * 64 < 64) fence_written<CG>();
                     tc_fence_after();
                     if (lane_id() == 0) {
                         const uint64_t da = smem_desc(smem_u32(a), a_mn ? 8192 : 16);
@@ -543,14 +544,21 @@ Operand weight_operand(const void* base, bool fp8, int64_t inner, int64_t rows, 
 }
 
 template <int FORM>
-ep_status launch(const ep_handle* h, const Operand& a, const Operand& b, const GemmParams& p, cudaStream_t stream) {
+ep_status launch(const ep_handle* h, const Operand& a, const Operand& b, const GemmParams& p, int64_t tile_rows,
+                 cudaStream_t stream) {
     CUtensorMap ma, mb;
     ep_status st = encode(&ma, a);
     if (st == EP_OK) st = encode(&mb, b);
     if (st != EP_OK) return st;
     DeviceGuard guard(h->device);
-    const cudaError_t err = launch_kernel(grouped_gemm_kernel<FORM, 1>, dim3(h->plan.num_sms), dim3(kGemmThreads),
-                                          kMaxSmem, stream, 1, ma, mb, p);
+    // A pair of CTAs computes 256 rows: each loads half of the weight tile, so that a row of products takes a
+    // third less shared-memory fill.  Where the rows of a group would leave one of the two idle, single CTAs.
+    const cudaError_t err =
+        tile_rows > kTileRows && h->plan.gemm_pairs > 0
+            ? launch_kernel(grouped_gemm_kernel<FORM, 2>, dim3(2 * h->plan.gemm_pairs), dim3(kGemmThreads), kMaxSmem, stream,
+                            2, ma, mb, p)
+            : launch_kernel(grouped_gemm_kernel<FORM, 1>, dim3(h->plan.num_sms), dim3(kGemmThreads), kMaxSmem, stream, 1,
+                            ma, mb, p);
     if (err != cudaSuccess) return cuda_fail(err, "grouped product launch");
     return EP_OK;
 }
@@ -583,15 +591,35 @@ bool rows_aligned32(const void* p, int64_t row_bytes) {
 }  // namespace
 
 template <int FORM>
-cudaError_t plan_form() {
-    return cudaFuncSetAttribute(grouped_gemm_kernel<FORM, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+cudaError_t plan_form(LaunchPlan* plan) {
+    cudaError_t err = cudaFuncSetAttribute(grouped_gemm_kernel<FORM, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (err == cudaSuccess)
+        err = cudaFuncSetAttribute(grouped_gemm_kernel<FORM, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(plan->num_sms / 2 * 2);
+    cfg.blockDim = dim3(kGemmThreads);
+    cfg.dynamicSmemBytes = kMaxSmem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int pairs = 0;
+    if (plan->num_sms >= 2) err = cudaOccupancyMaxActiveClusters(&pairs, grouped_gemm_kernel<FORM, 2>, &cfg);
+    if (err != cudaSuccess) return err;
+    if (pairs < plan->gemm_pairs) plan->gemm_pairs = pairs;
+    return cudaSuccess;
 }
 
-cudaError_t plan_gemm() {
-    cudaError_t err = plan_form<kForward>();
-    if (err == cudaSuccess) err = plan_form<kTransposed>();
-    if (err == cudaSuccess) err = plan_form<kWeightGrad>();
-    if (err == cudaSuccess) err = plan_form<kFp8>();
+// The pairs of CTAs that are resident at once.
+cudaError_t plan_gemm(LaunchPlan* plan) {
+    plan->gemm_pairs = plan->num_sms / 2;
+    cudaError_t err = plan_form<kForward>(plan);
+    if (err == cudaSuccess) err = plan_form<kTransposed>(plan);
+    if (err == cudaSuccess) err = plan_form<kWeightGrad>(plan);
+    if (err == cudaSuccess) err = plan_form<kFp8>(plan);
     return err;
 }
 
@@ -622,9 +650,10 @@ ep_status ep_grouped_gemm(ep_handle* h, int64_t num_rows, int32_t n, int32_t k, 
     p.out = out;
     p.out_row_bytes = out_row_bytes;
     p.wide_stores = rows_aligned32(out, out_row_bytes);
+    const int64_t rows_each = expected_rows ? expected_rows : num_rows / p.groups.groups;
     const Operand a = row_operand(x, false, k, num_rows, x_row_bytes, kRowBox);
-    return w_transposed ? launch<kTransposed>(h, a, weight_operand(w, false, n, k, p.groups.groups), p, stream)
-                        : launch<kForward>(h, a, weight_operand(w, false, k, n, p.groups.groups), p, stream);
+    return w_transposed ? launch<kTransposed>(h, a, weight_operand(w, false, n, k, p.groups.groups), p, rows_each, stream)
+                        : launch<kForward>(h, a, weight_operand(w, false, k, n, p.groups.groups), p, rows_each, stream);
 }
 
 ep_status ep_grouped_gemm_wgrad(ep_handle* h, int64_t num_rows, int32_t n, int32_t k, const int32_t* group_count,
@@ -658,7 +687,7 @@ ep_status ep_grouped_gemm_wgrad(ep_handle* h, int64_t num_rows, int32_t n, int32
     p.out_row_bytes = static_cast<int64_t>(k) * (p.out_fp32 ? 4 : 2);
     p.wide_stores = rows_aligned32(dw, p.out_row_bytes);
     return launch<kWeightGrad>(h, row_operand(dy, false, n, num_rows, dy_row_bytes, 64),
-                               row_operand(x, false, k, num_rows, x_row_bytes, 64), p, stream);
+                               row_operand(x, false, k, num_rows, x_row_bytes, 64), p, n, stream);
 }
 
 ep_status ep_grouped_gemm_fp8(ep_handle* h, int64_t num_rows, int32_t n, int32_t k, const int32_t* group_count,
@@ -691,8 +720,9 @@ ep_status ep_grouped_gemm_fp8(ep_handle* h, int64_t num_rows, int32_t n, int32_t
     p.x_scale_row_bytes = x_scale_row_bytes;
     p.scales_ue8m0 = scales_ue8m0 != 0;
     p.w_scales = w_scales;
+    const int64_t rows_each = expected_rows ? expected_rows : num_rows / p.groups.groups;
     return launch<kFp8>(h, row_operand(x, true, k, num_rows, x_row_bytes, kRowBox),
-                        weight_operand(w, true, k, n, p.groups.groups), p, stream);
+                        weight_operand(w, true, k, n, p.groups.groups), p, rows_each, stream);
 }
 
 }  // extern "C"

@@ -70,14 +70,29 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
 }
 
 // Arrivals at a barrier of this CTA (CG == 1) or, by its address in the cluster's shared window, of any CTA
-// of the pair.  The pair's arrivals are relaxed: what they order is tensor-memory and bulk-copy traffic,
-// which has fences and completion of its own (a release at cluster scope took over 1000 cycles a time).
+// of the pair.  They order tensor-memory and bulk-copy traffic, which has fences and completion of its own; an
+// explicit release at cluster scope, which took over 1000 cycles a time, is only for ordinary shared-memory writes.
 template <int CG>
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
     if constexpr (CG == 1)
         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
     else
-        asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+        asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// After this thread's fence_async_smem(): publishes the warp's shared-memory writes to the products of either CTA.
+template <int CG>
+__device__ __forceinline__ void bar_arrive_written(uint32_t bar) {
+    if constexpr (CG == 1)
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+    else
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// The other side of bar_arrive_written(), after the wait.
+template <int CG>
+__device__ __forceinline__ void fence_written() {
+    if constexpr (CG == 2) asm volatile("fence.acq_rel.cluster;\n\tfence.proxy.async;" ::: "memory");
 }
 
 template <int CG>
@@ -85,7 +100,7 @@ __device__ __forceinline__ void bar_arrive_expect_tx(uint32_t bar, uint32_t byte
     if constexpr (CG == 1)
         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
     else
-        asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+        asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                      : "memory");
 }
 

@@ -62,7 +62,8 @@ COUNTS = [
 @pytest.mark.parametrize("n,k", [(8, 8), (64, 64), (72, 136), (1000, 72), (264, 1032), (520, 2048)])
 @pytest.mark.parametrize("counts", COUNTS, ids=lambda c: f"{len(c)}g{sum(c)}")
 @pytest.mark.parametrize("transposed", [False, True])
-def test_grouped_gemm(counts, n, k, transposed):
+@pytest.mark.parametrize("expected", [1, 1000], ids=["single", "pair"])  # both tile heights on every shape
+def test_grouped_gemm(counts, n, k, transposed, expected):
     E = len(counts)
     begin, rows = packed(counts, gap=3)
     g = gen(n * 31 + k)
@@ -72,7 +73,7 @@ def test_grouped_gemm(counts, n, k, transposed):
     w = randn(g, (E, k, n) if transposed else (E, n, k), 0.1)
     out = Guarded((rows, n), torch.bfloat16)
     h = handle(E)
-    ep.ep_grouped_gemm(h, x, w, i32(counts), i32(begin), w_transposed=transposed, out=out.t)
+    ep.ep_grouped_gemm(h, x, w, i32(counts), i32(begin), w_transposed=transposed, out=out.t, expected_rows=expected)
     h.check()
     out.check()
     raw = out.t.view(torch.uint8)
@@ -162,7 +163,8 @@ def fp8_reference(x, xs, w, ws):
 
 @pytest.mark.parametrize("n,k", [(8, 128), (64, 256), (72, 384), (1000, 512), (264, 1152), (520, 2048)])
 @pytest.mark.parametrize("counts", COUNTS, ids=lambda c: f"{len(c)}g{sum(c)}")
-def test_grouped_gemm_fp8(counts, n, k):
+@pytest.mark.parametrize("expected", [1, 1000], ids=["single", "pair"])
+def test_grouped_gemm_fp8(counts, n, k, expected):
     E = len(counts)
     begin, rows = packed(counts, gap=1, order=list(reversed(range(E))))
     g = gen(n * 13 + k)
@@ -175,7 +177,7 @@ def test_grouped_gemm_fp8(counts, n, k):
     ws = torch.rand((E, -(-n // 128), k // 128), generator=g, device=DEV) * 0.01
     out = Guarded((rows, n), torch.bfloat16)
     h = handle(E)
-    ep.ep_grouped_gemm_fp8(h, x, xs, w, ws, i32(counts), i32(begin), out=out.t)
+    ep.ep_grouped_gemm_fp8(h, x, xs, w, ws, i32(counts), i32(begin), out=out.t, expected_rows=expected)
     h.check()
     out.check()
     used = torch.zeros(rows, dtype=torch.bool, device=DEV)
