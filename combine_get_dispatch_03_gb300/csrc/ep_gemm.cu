@@ -30,8 +30,9 @@ enum GemmForm { kForward = 0, kTransposed = 1, kWeightGrad = 2, kFp8 = 3 };
 constexpr int kTileRows = 128;      // output rows per CTA
 constexpr int kMaxTileCols = 256;
 constexpr int kRowBytes = 128;      // bytes of one operand row in a stage (the swizzle's span)
-constexpr int kRowBox = 32;         // rows per tensor-map load of a row operand: a short group loads few
-constexpr int kColBox = 64;         // rows (or bf16 columns) per load of a weight operand
+constexpr int kBox = 128;           // output elements (rows or columns) of a tensor-map load: 16 KB
+constexpr int kRowBox = 32;         // the same for a group's last rows: a short group loads few
+constexpr int kColBox = 64;         // the same for narrow tiles
 constexpr int kMaxStages = 12;
 constexpr int kEpilogueWarps = 8;
 constexpr int kGemmThreads = (4 + kEpilogueWarps) * kWarpSize;  // warps 2 and 3 are idle: register splits go by four warps
@@ -52,7 +53,13 @@ struct GemmParams {
     int32_t out_fp32;       // weight grad
     int32_t accumulate;     // weight grad
     int32_t wide_stores;    // output rows are 32-byte aligned
+    int32_t a_chunked, b_chunked;  // operands read across: kBox columns in one load (else kColBox)
     int32_t* status;
+};
+
+// Tensor maps of the two operands: loads of kBox output elements, and smaller ones.
+struct Maps {
+    CUtensorMap a, a_small, b, b_small;
 };
 
 struct Control {
@@ -180,8 +187,7 @@ __device__ __forceinline__ void store_fp32(uint8_t* row, int col, int cols, cons
 
 template <int FORM, int CG>
 __global__ void __launch_bounds__(kGemmThreads, 1)
-    grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                        const GemmParams p) {
+    grouped_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
     extern __shared__ uint8_t raw[];
     uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     Control* ctl = reinterpret_cast<Control*>(smem);
@@ -212,8 +218,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         mbar_init(&ctl->drained, 1);
         ctl->abort_flag = 0;
         fence_barrier_init();
-        prefetch_map(&map_a);
-        prefetch_map(&map_b);
+        prefetch_map(&maps.a);
+        prefetch_map(&maps.b);
     }
     if (warp == 1) tmem_alloc<CG>(&ctl->tmem, 512);
     pdl_enter();
@@ -231,9 +237,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const int worker = blockIdx.x / CG, workers = gridDim.x / CG;
 
     // The FP8 form holds 128 sums a thread in its eight epilogue warps: registers move there from the
-    // others (72 + 2 * 216 = 3 * 168, what the block was launched with).
+    // others (56 + 2 * 224 = 3 * 168, what the block was launched with).
     if (warp < 4) {
-    if constexpr (FORM == kFp8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if constexpr (FORM == kFp8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0 && lane_id() == 0) {
         // ------------------------------------------------------------- loads
         uint32_t stage = 0, phase = 0;
@@ -244,7 +250,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         for (int tile = worker; ok && tile < t.total; tile += workers) {
             const Tile q = decode<FORM>(t, p, tile);
             const int my_m0 = q.m0 + static_cast<int>(rank) * kTileRows;
-            const int boxes = max(0, min(kTileRows, q.rows - my_m0) + kRowBox - 1) / kRowBox;
+            const int rows_here = min(kTileRows, q.rows - my_m0);
+            const int small_boxes = rows_here > kTileRows / 2 ? 0 : (max(0, rows_here) + kRowBox - 1) / kRowBox;
+            const uint32_t bytes = FORM == kWeightGrad ? stage_bytes
+                                                       : cols_here * kRowBytes + (rows_here > kTileRows / 2 ? a_bytes : small_boxes * (kRowBox * kRowBytes));
             for (int s = 0; s < q.steps; ++s) {
                 ok = wait_phase(&ctl->empty[stage], phase ^ 1, abort_flag, p.status);
                 if (!ok) break;
@@ -264,18 +273,41 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         tail_last &= ~(1u << stage);
                     }
                     const int r = q.row0 + s * 64;
-                    for (int c = 0; c < kTileRows / 64; ++c) tma_load_2d<CG>(a + c * 8192, &map_a, my_m0 + c * 64, r, bar);
-                    for (int c = 0; c < cols_here / 64; ++c) tma_load_2d<CG>(b + c * 8192, &map_b, q.n0 + cb + c * 64, r, bar);
+                    if (p.a_chunked) {
+                        tma_load_3d<CG>(a, &maps.a, 0, r, my_m0 / 64, bar);
+                    } else {
+                        tma_load_2d<CG>(a, &maps.a_small, my_m0, r, bar);
+                        tma_load_2d<CG>(a + 8192, &maps.a_small, my_m0 + 64, r, bar);
+                    }
+                    if (p.b_chunked && cols_here >= kBox) {
+                        for (int c = 0; c < cols_here; c += kBox)
+                            tma_load_3d<CG>(b + c * kRowBytes, &maps.b, 0, r, (q.n0 + cb + c) / 64, bar);
+                    } else {
+                        for (int c = 0; c < cols_here; c += kColBox)
+                            tma_load_2d<CG>(b + c * kRowBytes, &maps.b_small, q.n0 + cb + c, r, bar);
+                    }
                 } else {
-                    bar_arrive_expect_tx<CG>(bar, boxes * (kRowBox * kRowBytes) + cols_here * kRowBytes);
+                    bar_arrive_expect_tx<CG>(bar, bytes);
                     const int x = s * (FORM == kFp8 ? 128 : 64);
-                    for (int c = 0; c < boxes; ++c)
-                        tma_load_2d<CG>(a + c * (kRowBox * kRowBytes), &map_a, x, q.row0 + my_m0 + c * kRowBox, bar);
-                    for (int c = 0; c < cols_here / kColBox; ++c) {
-                        if constexpr (FORM == kTransposed)
-                            tma_load_3d<CG>(b + c * 8192, &map_b, q.n0 + cb + c * kColBox, x, q.group, bar);
-                        else
-                            tma_load_3d<CG>(b + c * 8192, &map_b, x, q.n0 + cb + c * kColBox, q.group, bar);
+                    if (small_boxes == 0) {
+                        if (rows_here > 0) tma_load_2d<CG>(a, &maps.a, x, q.row0 + my_m0, bar);
+                    } else {
+                        for (int c = 0; c < small_boxes; ++c)
+                            tma_load_2d<CG>(a + c * (kRowBox * kRowBytes), &maps.a_small, x, q.row0 + my_m0 + c * kRowBox, bar);
+                    }
+                    if (FORM == kTransposed) {
+                        if (p.b_chunked && cols_here >= kBox) {
+                            for (int c = 0; c < cols_here; c += kBox)
+                                tma_load_4d<CG>(b + c * kRowBytes, &maps.b, 0, x, (q.n0 + cb + c) / 64, q.group, bar);
+                        } else {
+                            for (int c = 0; c < cols_here; c += kColBox)
+                                tma_load_3d<CG>(b + c * kRowBytes, &maps.b_small, q.n0 + cb + c, x, q.group, bar);
+                        }
+                    } else if (cols_here >= kBox) {
+                        for (int c = 0; c < cols_here; c += kBox)
+                            tma_load_3d<CG>(b + c * kRowBytes, &maps.b, x, q.n0 + cb + c, q.group, bar);
+                    } else {
+                        tma_load_3d<CG>(b, &maps.b_small, x, q.n0 + cb, q.group, bar);
                     }
                 }
                 ++used;
@@ -376,7 +408,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     } else {
         // ------------------------------------------------- accumulators out
-        if constexpr (FORM == kFp8) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        if constexpr (FORM == kFp8) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         const int w = warp - 4;
         const int quarter = warp & 3;               // the 32 lanes of tensor memory that this warp may read
         const int half = w >> 2;                    // which half of the tile's columns
@@ -428,11 +460,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             } else {
                 // Each block of 128 has its own scales: its products arrive in an accumulator of their own and
                 // are scaled and added here, in fp32 registers, 128 columns a thread at most.
-                float acc[4][32];
+                uint64_t acc[4][16];  // pairs of fp32
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) acc[c][i] = 0.0f;
+                    for (int i = 0; i < 16; ++i) acc[c][i] = 0;
                 const int64_t src = static_cast<int64_t>(q.row0) + min(row, q.rows - 1);
                 const uint8_t* xs = p.x_scales + src * p.x_scale_row_bytes;
                 const int nb = min(col0, p.cols_dim - 1) >> 7;
@@ -453,19 +485,26 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t at = lane_base + buf * kMaxTileCols + half * cols_half;
+                        const uint64_t scale = pack_f32x2(__float_as_uint(cur[j]), __float_as_uint(cur[j]));
+                        // the next 32 columns are on their way while these are added
+                        uint32_t u[2][32];
+                        __syncwarp();
+                        tc_ld32(at, u[0]);
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             if (c * 32 < cols_half) {
-                                uint32_t u[32];
-                                tc_ld32(at + c * 32, u);
-                                tc_wait_ld(u);
+                                tc_wait_ld(u[c & 1]);
+                                if (c < 3 && (c + 1) * 32 < cols_half) tc_ld32(at + (c + 1) * 32, u[(c + 1) & 1]);
+                                else {
+                                    tc_fence_before();
+                                    __syncwarp();
+                                    if (lane_id() == 0) bar_arrive<CG>(acc_empty0 + 8 * buf);
+                                }
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) acc[c][i] = fmaf(__uint_as_float(u[i]), cur[j], acc[c][i]);
+                                for (int i = 0; i < 16; ++i)
+                                    fma_f32x2(acc[c][i], pack_f32x2(u[c & 1][2 * i], u[c & 1][2 * i + 1]), scale);
                             }
                         }
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane_id() == 0) bar_arrive<CG>(acc_empty0 + 8 * buf);
                         buf ^= 1;
                         acc_phase ^= buf == 0;
                     }
@@ -475,8 +514,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 if (ok && row_ok) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        if (c * 32 < cols_half && col0 + c * 32 < p.cols_dim)
-                            store_bf16(out_row, col0 + c * 32, p.cols_dim, acc[c], p.wide_stores != 0);
+                        if (c * 32 < cols_half && col0 + c * 32 < p.cols_dim) {
+                            float v[32];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                v[2 * i] = __uint_as_float(static_cast<uint32_t>(acc[c][i]));
+                                v[2 * i + 1] = __uint_as_float(static_cast<uint32_t>(acc[c][i] >> 32));
+                            }
+                            store_bf16(out_row, col0 + c * 32, p.cols_dim, v, p.wide_stores != 0);
+                        }
                 }
             }
         }
@@ -510,18 +556,18 @@ struct Operand {
     const void* base;
     bool fp8;
     int dims;
-    uint64_t size[3];
-    uint64_t stride[2];  // bytes
-    uint32_t box[3];
+    uint64_t size[4];
+    uint64_t stride[3];  // bytes
+    uint32_t box[4];
 };
 
 ep_status encode(CUtensorMap* map, const Operand& o) {
     const PFN_cuTensorMapEncodeTiled_v12000 fn = map_encoder();
     if (fn == nullptr) return fail(EP_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
-    cuuint64_t size[3], stride[2];
-    cuuint32_t box[3], step[3] = {1, 1, 1};
-    for (int i = 0; i < 3; ++i) size[i] = o.size[i], box[i] = o.box[i];
-    for (int i = 0; i < 2; ++i) stride[i] = o.stride[i];
+    cuuint64_t size[4], stride[3];
+    cuuint32_t box[4], step[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 4; ++i) size[i] = o.size[i], box[i] = o.box[i];
+    for (int i = 0; i < 3; ++i) stride[i] = o.stride[i];
     const CUresult rc = fn(map, o.fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, o.dims,
                            const_cast<void*>(o.base), size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -531,24 +577,37 @@ ep_status encode(CUtensorMap* map, const Operand& o) {
 }
 
 // Rows [rows][inner] with a row stride.
-Operand row_operand(const void* base, bool fp8, int64_t inner, int64_t rows, int64_t row_bytes, uint32_t box_rows) {
-    return {base, fp8, 2, {static_cast<uint64_t>(inner), static_cast<uint64_t>(rows), 1},
-            {static_cast<uint64_t>(row_bytes), 0}, {fp8 ? 128u : 64u, box_rows, 1}};
+Operand row_operand(const void* base, bool fp8, uint64_t inner, uint64_t rows, uint64_t row_bytes, uint32_t box_rows) {
+    return {base, fp8, 2, {inner, rows, 1, 1}, {row_bytes, 0, 0}, {fp8 ? 128u : 64u, box_rows, 1, 1}};
+}
+
+// The same rows read across, 64 columns by 64 rows; `chunks` of 64 columns in one load. More than one needs inner % 64
+// == 0: a chunk is an index of its own there, and a last, partial one would reach into the next row.
+Operand across_operand(const void* base, uint64_t inner, uint64_t rows, uint64_t row_bytes, uint32_t chunks) {
+    if (chunks == 1) return row_operand(base, false, inner, rows, row_bytes, 64);
+    return {base, false, 3, {64, rows, inner / 64, 1}, {row_bytes, 128, 0}, {64, 64, chunks, 1}};
 }
 
 // Weights [groups][rows][inner], contiguous.
-Operand weight_operand(const void* base, bool fp8, int64_t inner, int64_t rows, int64_t groups) {
-    const uint64_t row = static_cast<uint64_t>(inner) * (fp8 ? 1 : 2);
-    return {base, fp8, 3, {static_cast<uint64_t>(inner), static_cast<uint64_t>(rows), static_cast<uint64_t>(groups)},
-            {row, row * static_cast<uint64_t>(rows)}, {fp8 ? 128u : 64u, static_cast<uint32_t>(kColBox), 1}};
+Operand weight_operand(const void* base, bool fp8, uint64_t inner, uint64_t rows, uint64_t groups, uint32_t box_rows) {
+    const uint64_t row = inner * (fp8 ? 1 : 2);
+    return {base, fp8, 3, {inner, rows, groups, 1}, {row, row * rows, 0}, {fp8 ? 128u : 64u, box_rows, 1, 1}};
+}
+
+Operand weight_across_operand(const void* base, uint64_t inner, uint64_t rows, uint64_t groups, uint32_t chunks) {
+    if (chunks == 1) return weight_operand(base, false, inner, rows, groups, 64);
+    const uint64_t row = inner * 2;
+    return {base, false, 4, {64, rows, inner / 64, groups}, {row, 128, row * rows}, {64, 64, chunks, 1}};
 }
 
 template <int FORM>
-ep_status launch(const ep_handle* h, const Operand& a, const Operand& b, const GemmParams& p, int64_t tile_rows,
-                 cudaStream_t stream) {
-    CUtensorMap ma, mb;
-    ep_status st = encode(&ma, a);
-    if (st == EP_OK) st = encode(&mb, b);
+ep_status launch(const ep_handle* h, const Operand& a, const Operand& a_small, const Operand& b, const Operand& b_small,
+                 const GemmParams& p, int64_t tile_rows, cudaStream_t stream) {
+    Maps m;
+    ep_status st = encode(&m.a, a);
+    if (st == EP_OK) st = encode(&m.a_small, a_small);
+    if (st == EP_OK) st = encode(&m.b, b);
+    if (st == EP_OK) st = encode(&m.b_small, b_small);
     if (st != EP_OK) return st;
     DeviceGuard guard(h->device);
     // A pair of CTAs computes 256 rows: each loads half of the weight tile, so that a row of products takes a
@@ -556,9 +615,9 @@ ep_status launch(const ep_handle* h, const Operand& a, const Operand& b, const G
     const cudaError_t err =
         tile_rows > kTileRows && h->plan.gemm_pairs > 0
             ? launch_kernel(grouped_gemm_kernel<FORM, 2>, dim3(2 * h->plan.gemm_pairs), dim3(kGemmThreads), kMaxSmem, stream,
-                            2, ma, mb, p)
+                            2, m, p)
             : launch_kernel(grouped_gemm_kernel<FORM, 1>, dim3(h->plan.num_sms), dim3(kGemmThreads), kMaxSmem, stream, 1,
-                            ma, mb, p);
+                            m, p);
     if (err != cudaSuccess) return cuda_fail(err, "grouped product launch");
     return EP_OK;
 }
@@ -651,9 +710,15 @@ ep_status ep_grouped_gemm(ep_handle* h, int64_t num_rows, int32_t n, int32_t k, 
     p.out_row_bytes = out_row_bytes;
     p.wide_stores = rows_aligned32(out, out_row_bytes);
     const int64_t rows_each = expected_rows ? expected_rows : num_rows / p.groups.groups;
-    const Operand a = row_operand(x, false, k, num_rows, x_row_bytes, kRowBox);
-    return w_transposed ? launch<kTransposed>(h, a, weight_operand(w, false, n, k, p.groups.groups), p, rows_each, stream)
-                        : launch<kForward>(h, a, weight_operand(w, false, k, n, p.groups.groups), p, rows_each, stream);
+    const int groups = p.groups.groups;
+    const Operand a = row_operand(x, false, k, num_rows, x_row_bytes, kBox);
+    const Operand a_small = row_operand(x, false, k, num_rows, x_row_bytes, kRowBox);
+    if (!w_transposed)
+        return launch<kForward>(h, a, a_small, weight_operand(w, false, k, n, groups, kBox),
+                                weight_operand(w, false, k, n, groups, kColBox), p, rows_each, stream);
+    p.b_chunked = n % 64 == 0;
+    return launch<kTransposed>(h, a, a_small, weight_across_operand(w, n, k, groups, p.b_chunked ? kBox / 64 : 1),
+                               weight_across_operand(w, n, k, groups, 1), p, rows_each, stream);
 }
 
 ep_status ep_grouped_gemm_wgrad(ep_handle* h, int64_t num_rows, int32_t n, int32_t k, const int32_t* group_count,
@@ -686,8 +751,12 @@ ep_status ep_grouped_gemm_wgrad(ep_handle* h, int64_t num_rows, int32_t n, int32
     p.accumulate = accumulate != 0;
     p.out_row_bytes = static_cast<int64_t>(k) * (p.out_fp32 ? 4 : 2);
     p.wide_stores = rows_aligned32(dw, p.out_row_bytes);
-    return launch<kWeightGrad>(h, row_operand(dy, false, n, num_rows, dy_row_bytes, 64),
-                               row_operand(x, false, k, num_rows, x_row_bytes, 64), p, n, stream);
+    p.a_chunked = n % 64 == 0;
+    p.b_chunked = k % 64 == 0;
+    return launch<kWeightGrad>(h, across_operand(dy, n, num_rows, dy_row_bytes, p.a_chunked ? kBox / 64 : 1),
+                               across_operand(dy, n, num_rows, dy_row_bytes, 1),
+                               across_operand(x, k, num_rows, x_row_bytes, p.b_chunked ? kBox / 64 : 1),
+                               across_operand(x, k, num_rows, x_row_bytes, 1), p, n, stream);
 }
 
 ep_status ep_grouped_gemm_fp8(ep_handle* h, int64_t num_rows, int32_t n, int32_t k, const int32_t* group_count,
@@ -721,8 +790,10 @@ ep_status ep_grouped_gemm_fp8(ep_handle* h, int64_t num_rows, int32_t n, int32_t
     p.scales_ue8m0 = scales_ue8m0 != 0;
     p.w_scales = w_scales;
     const int64_t rows_each = expected_rows ? expected_rows : num_rows / p.groups.groups;
-    return launch<kFp8>(h, row_operand(x, true, k, num_rows, x_row_bytes, kRowBox),
-                        weight_operand(w, true, k, n, p.groups.groups), p, rows_each, stream);
+    return launch<kFp8>(h, row_operand(x, true, k, num_rows, x_row_bytes, kBox),
+                        row_operand(x, true, k, num_rows, x_row_bytes, kRowBox),
+                        weight_operand(w, true, k, n, p.groups.groups, kBox),
+                        weight_operand(w, true, k, n, p.groups.groups, kColBox), p, rows_each, stream);
 }
 
 }  // extern "C"
