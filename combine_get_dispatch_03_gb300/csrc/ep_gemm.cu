@@ -140,12 +140,14 @@ __device__ __forceinline__ void build_table(Table& t, const GemmParams& p, Contr
     t.total = total * t.col_tiles;
 }
 
-__device__ __forceinline__ float scale_of(const uint8_t* row, int block, int ue8m0) {
-    if (ue8m0) {
-        const uint32_t e = row[block];
-        return __uint_as_float(e == 255 ? 0x7fc00000u : e == 0 ? 0x00400000u : e << 23);
-    }
-    return *reinterpret_cast<const float*>(row + 4 * static_cast<int64_t>(block));
+// A row's scale of one block as it lies in memory, and as the fp32 it stands for.
+__device__ __forceinline__ uint32_t raw_scale(const uint8_t* row, int block, int ue8m0) {
+    return ue8m0 ? row[block] : *reinterpret_cast<const uint32_t*>(row + 4 * static_cast<int64_t>(block));
+}
+
+__device__ __forceinline__ float scale_value(uint32_t raw, int ue8m0) {
+    if (!ue8m0) return __uint_as_float(raw);
+    return __uint_as_float(raw == 255 ? 0x7fc00000u : raw == 0 ? 0x00400000u : raw << 23);
 }
 
 // 32 columns of one output row, rounded to bf16; columns at or past `cols` (a multiple of 8) are left out.
@@ -183,6 +185,10 @@ __device__ __forceinline__ void store_fp32(uint8_t* row, int col, int cols, cons
         }
         *reinterpret_cast<float4*>(p + 4 * i) = q;
     }
+}
+
+__device__ __forceinline__ uint8_t* out_row(const GemmParams& p, int64_t row) {
+    return static_cast<uint8_t*>(p.out) + row * p.out_row_bytes;
 }
 
 template <int FORM, int CG>
@@ -237,9 +243,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const int worker = blockIdx.x / CG, workers = gridDim.x / CG;
 
     // The FP8 form holds 128 sums a thread in its eight epilogue warps: registers move there from the
-    // others (56 + 2 * 224 = 3 * 168, what the block was launched with).
+    // others (72 + 2 * 216 = 3 * 168, what the block was launched with).
     if (warp < 4) {
-    if constexpr (FORM == kFp8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if constexpr (FORM == kFp8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0 && lane_id() == 0) {
         // ------------------------------------------------------------- loads
         uint32_t stage = 0, phase = 0;
@@ -408,7 +414,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     } else {
         // ------------------------------------------------- accumulators out
-        if constexpr (FORM == kFp8) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        if constexpr (FORM == kFp8) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int w = warp - 4;
         const int quarter = warp & 3;               // the 32 lanes of tensor memory that this warp may read
         const int half = w >> 2;                    // which half of the tile's columns
@@ -422,15 +428,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const Tile q = decode<FORM>(t, p, tile);
             const int row = q.m0 + static_cast<int>(rank) * kTileRows + quarter * 32 + lane_id();  // in the group
             const int col0 = q.n0 + half * cols_half;
-            uint8_t* out_row;
-            bool row_ok;
-            if constexpr (FORM == kWeightGrad) {
-                row_ok = row < p.rows_dim;
-                out_row = static_cast<uint8_t*>(p.out) + (static_cast<int64_t>(q.group) * p.rows_dim + row) * p.out_row_bytes;
-            } else {
-                row_ok = row < q.rows;
-                out_row = static_cast<uint8_t*>(p.out) + (static_cast<int64_t>(q.row0) + row) * p.out_row_bytes;
-            }
+            const bool row_ok = row < (FORM == kWeightGrad ? p.rows_dim : q.rows);
+            const int64_t out_at = FORM == kWeightGrad ? static_cast<int64_t>(q.group) * p.rows_dim + row : static_cast<int64_t>(q.row0) + row;
             if constexpr (FORM != kFp8) {
                 ok = warp_wait(&ctl->acc_full[buf], acc_phase, abort_flag, p.status);
                 if (!ok) break;
@@ -450,9 +449,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     for (int i = 0; i < 32; ++i) v[i] = FORM == kWeightGrad && q.steps == 0 ? 0.0f : __uint_as_float(u[i]);
                     if (row_ok && col0 + c < p.cols_dim) {
                         if (FORM == kWeightGrad && p.out_fp32)
-                            store_fp32(out_row, col0 + c, p.cols_dim, v, p.accumulate != 0);
+                            store_fp32(out_row(p, out_at), col0 + c, p.cols_dim, v, p.accumulate != 0);
                         else
-                            store_bf16(out_row, col0 + c, p.cols_dim, v, p.wide_stores != 0);
+                            store_bf16(out_row(p, out_at), col0 + c, p.cols_dim, v, p.wide_stores != 0);
                     }
                 }
                 buf ^= 1;
@@ -469,47 +468,52 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 const uint8_t* xs = p.x_scales + src * p.x_scale_row_bytes;
                 const int nb = min(col0, p.cols_dim - 1) >> 7;
                 const float* ws = p.w_scales + (static_cast<int64_t>(q.group) * ((p.cols_dim + 127) >> 7) + nb) * q.steps;
-                float cur[4], next[4];
-                auto fetch = [&](float (&f)[4], int s0) {
+                // Scales of two blocks are loaded two blocks before they are used, and only then looked at: a
+                // multiplication next to the loads would wait for them.
+                uint32_t raw_x[2];
+                float raw_w[2];
+                auto fetch = [&](int s0) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        f[i] = s0 + i < q.steps ? scale_of(xs, s0 + i, p.scales_ue8m0) * ws[s0 + i] : 0.0f;
+                    for (int i = 0; i < 2; ++i) {
+                        const int b = min(s0 + i, q.steps - 1);
+                        raw_x[i] = raw_scale(xs, b, p.scales_ue8m0);
+                        raw_w[i] = ws[b];
+                    }
                 };
-                fetch(cur, 0);
-                for (int s0 = 0; s0 < q.steps && ok; s0 += 4) {
-                    fetch(next, s0 + 4);
+                fetch(0);
+                for (int s0 = 0; s0 < q.steps && ok; s0 += 2) {
+                    float cur[2];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int i = 0; i < 2; ++i) cur[i] = scale_value(raw_x[i], p.scales_ue8m0) * raw_w[i];
+                    fetch(s0 + 2);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
                         if (s0 + j >= q.steps) break;
                         ok = warp_wait(&ctl->acc_full[buf], acc_phase, abort_flag, p.status);
                         if (!ok) break;
                         tc_fence_after();
                         const uint32_t at = lane_base + buf * kMaxTileCols + half * cols_half;
                         const uint64_t scale = pack_f32x2(__float_as_uint(cur[j]), __float_as_uint(cur[j]));
-                        // the next 32 columns are on their way while these are added
-                        uint32_t u[2][32];
-                        __syncwarp();
-                        tc_ld32(at, u[0]);
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             if (c * 32 < cols_half) {
-                                tc_wait_ld(u[c & 1]);
-                                if (c < 3 && (c + 1) * 32 < cols_half) tc_ld32(at + (c + 1) * 32, u[(c + 1) & 1]);
-                                else {
+                                uint32_t u[32];
+                                __syncwarp();
+                                tc_ld32(at + c * 32, u);
+                                tc_wait_ld(u);
+                                if (c == 3 || (c + 1) * 32 >= cols_half) {  // all read: the accumulator is free
                                     tc_fence_before();
                                     __syncwarp();
                                     if (lane_id() == 0) bar_arrive<CG>(acc_empty0 + 8 * buf);
                                 }
 #pragma unroll
                                 for (int i = 0; i < 16; ++i)
-                                    fma_f32x2(acc[c][i], pack_f32x2(u[c & 1][2 * i], u[c & 1][2 * i + 1]), scale);
+                                    fma_f32x2(acc[c][i], pack_f32x2(u[2 * i], u[2 * i + 1]), scale);
                             }
                         }
                         buf ^= 1;
                         acc_phase ^= buf == 0;
                     }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) cur[i] = next[i];
                 }
                 if (ok && row_ok) {
 #pragma unroll
@@ -521,7 +525,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                                 v[2 * i] = __uint_as_float(static_cast<uint32_t>(acc[c][i]));
                                 v[2 * i + 1] = __uint_as_float(static_cast<uint32_t>(acc[c][i] >> 32));
                             }
-                            store_bf16(out_row, col0 + c * 32, p.cols_dim, v, p.wide_stores != 0);
+                            store_bf16(out_row(p, out_at), col0 + c * 32, p.cols_dim, v, p.wide_stores != 0);
                         }
                 }
             }
