@@ -246,7 +246,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     // others (72 + 2 * 216 = 3 * 168, what the block was launched with).
     if (warp < 4) {
     if constexpr (FORM == kFp8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 0 && lane_id() == 0) {
+    if (warp == 0) {
+        if (elect_one()) {
         // ------------------------------------------------------------- loads
         uint32_t stage = 0, phase = 0;
         uint32_t tail_phase = 0, tail_last = 0;  // per stage: uses of tail_full, mod 2; whether its last use was one
@@ -333,83 +334,81 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 }
             }
         }
+        }
     } else if (warp == 1) {
         // ---------------------------------------------------------- products
-        uint32_t stage = 0, phase = 0, acc_phase = 0;
-        uint32_t tail_phase = 0;  // per stage: uses of tail_full, mod 2
-        int buf = 0;
-        bool ok = true;
-        constexpr bool a_mn = FORM == kWeightGrad;
-        constexpr bool b_mn = FORM == kWeightGrad || FORM == kTransposed;
-        const uint32_t idesc = mma_desc(FORM == kFp8 ? 0 : 1, a_mn, b_mn, kTileRows * CG, t.tile_cols);
-        const bool leader = rank == 0;
-        for (int tile = worker; ok && tile < t.total; tile += workers) {
-            const Tile q = decode<FORM>(t, p, tile);
-            if (FORM != kFp8 && leader) {
-                ok = warp_wait(&ctl->acc_empty[buf], acc_phase ^ 1, abort_flag, p.status);
-                tc_fence_after();
-            }
-            for (int s = 0; s < q.steps && ok; ++s) {
-                uint8_t* a = stages + stage * stage_bytes;
-                if constexpr (FORM == kWeightGrad) {
-                    const int valid = q.rows - s * 64;
-                    if (valid < 64) {
-                        // The block's rows past the group belong to others: zero them in both operands.
-                        ok = warp_wait(&ctl->tail_full[stage], (tail_phase >> stage) & 1, abort_flag, p.status);
-                        tail_phase ^= 1u << stage;
-                        const int chunks = (kTileRows + cols_here) / 64;
-                        const int pieces = (64 - valid) * 8;
-                        for (int c = 0; c < chunks; ++c) {
-                            uint4* z = reinterpret_cast<uint4*>(a + c * 8192 + valid * 128);
-                            for (int i = lane_id(); i < pieces; i += kWarpSize) z[i] = make_uint4(0, 0, 0, 0);
-                        }
-                        fence_async_smem();
-                        __syncwarp();
-                        if (lane_id() == 0)
-                            bar_arrive_written<CG>(CG == 1 ? smem_u32(&ctl->full[stage]) : cluster_addr(&ctl->full[stage], 0));
-                    }
-                }
-                if (leader && ok) {
+        if (rank == 0 && elect_one()) {
+            uint32_t stage = 0, phase = 0, acc_phase = 0;
+            int buf = 0;
+            bool ok = true;
+            constexpr bool a_mn = FORM == kWeightGrad;
+            constexpr bool b_mn = FORM == kWeightGrad || FORM == kTransposed;
+            const uint32_t idesc = mma_desc(FORM == kFp8 ? 0 : 1, a_mn, b_mn, kTileRows * CG, t.tile_cols);
+            for (int tile = worker; ok && tile < t.total; tile += workers) {
+                const Tile q = decode<FORM>(t, p, tile);
+                if (FORM != kFp8) ok = wait_phase(&ctl->acc_empty[buf], acc_phase ^ 1, abort_flag, p.status);
+                for (int s = 0; s < q.steps && ok; ++s) {
                     if (FORM == kFp8) {
-                        ok = warp_wait(&ctl->acc_empty[buf], acc_phase ^ 1, abort_flag, p.status);
+                        ok = wait_phase(&ctl->acc_empty[buf], acc_phase ^ 1, abort_flag, p.status);
                         if (!ok) break;
                     }
-                    ok = warp_wait(&ctl->full[stage], phase, abort_flag, p.status);
+                    ok = wait_phase(&ctl->full[stage], phase, abort_flag, p.status);
                     if (!ok) break;
                     if (FORM == kWeightGrad && q.rows - s * 64 < 64) fence_written<CG>();
                     tc_fence_after();
-                    if (lane_id() == 0) {
-                        const uint64_t da = smem_desc(smem_u32(a), a_mn ? 8192 : 16);
-                        const uint64_t db = smem_desc(smem_u32(a) + a_bytes, b_mn ? 8192 : 16);
-                        const uint32_t d = tmem + buf * kMaxTileCols;
+                    const uint32_t a = smem_u32(stages) + stage * stage_bytes;
+                    const uint64_t da = smem_desc(a, a_mn ? 8192 : 16);
+                    const uint64_t db = smem_desc(a + a_bytes, b_mn ? 8192 : 16);
+                    const uint32_t d = tmem + buf * kMaxTileCols;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            tc_mma<CG, FORM == kFp8>(d, da + i * (a_mn ? 128 : 2), db + i * (b_mn ? 128 : 2), idesc,
-                                                     (FORM == kFp8 ? 0 : s) | i);
-                        tc_commit<CG>(&ctl->empty[stage]);
-                        if (FORM == kFp8) tc_commit<CG>(&ctl->acc_full[buf]);
+                    for (int i = 0; i < 4; ++i)
+                        tc_mma<CG, FORM == kFp8>(d, da + i * (a_mn ? 128 : 2), db + i * (b_mn ? 128 : 2), idesc,
+                                                 (FORM == kFp8 ? 0 : s) | i);
+                    tc_commit<CG>(&ctl->empty[stage]);
+                    if (FORM == kFp8) {
+                        tc_commit<CG>(&ctl->acc_full[buf]);
+                        buf ^= 1;
+                        acc_phase ^= buf == 0;
                     }
-                    __syncwarp();
+                    if (++stage == static_cast<uint32_t>(num_stages)) stage = 0, phase ^= 1;
                 }
-                if (FORM == kFp8) {
+                if (FORM != kFp8 && ok) {
+                    tc_commit<CG>(&ctl->acc_full[buf]);
                     buf ^= 1;
                     acc_phase ^= buf == 0;
                 }
-                if (++stage == static_cast<uint32_t>(num_stages)) stage = 0, phase ^= 1;
             }
-            if (FORM != kFp8) {
-                if (leader && ok && lane_id() == 0) tc_commit<CG>(&ctl->acc_full[buf]);
-                __syncwarp();
-                buf ^= 1;
-                acc_phase ^= buf == 0;
+            if (!ok) {
+                // Given up: the products already issued still write tensor memory.
+                tc_commit<CG>(&ctl->drained);
+                for (int k = 0; k < (1 << 12) && !mbar_try_wait(&ctl->drained, 0); ++k) {
+                }
             }
         }
-        if (!ok && leader) {
-            // Given up: the products already issued still write tensor memory.
-            if (lane_id() == 0) tc_commit<CG>(&ctl->drained);
-            for (int k = 0; k < (1 << 12) && !mbar_try_wait(&ctl->drained, 0); ++k) {
+    } else if (FORM == kWeightGrad && warp == 2) {
+        // ------------------------------------------------- ends of groups
+        // The rows of a group's last, partial block past its end belong to others: zero them in both operands.
+        uint32_t stage = 0, tail_phase = 0;  // tail_phase, per stage: uses of tail_full, mod 2
+        bool ok = true;
+        for (int tile = worker; ok && tile < t.total; tile += workers) {
+            const Tile q = decode<FORM>(t, p, tile);
+            const int whole = q.rows / 64, valid = q.rows % 64;
+            stage = (stage + whole) % num_stages;
+            if (valid == 0) continue;
+            ok = warp_wait(&ctl->tail_full[stage], (tail_phase >> stage) & 1, abort_flag, p.status);
+            tail_phase ^= 1u << stage;
+            uint8_t* a = stages + stage * stage_bytes;
+            const int chunks = (kTileRows + cols_here) / 64;
+            const int pieces = (64 - valid) * 8;
+            for (int c = 0; c < chunks; ++c) {
+                uint4* z = reinterpret_cast<uint4*>(a + c * 8192 + valid * 128);
+                for (int i = lane_id(); i < pieces; i += kWarpSize) z[i] = make_uint4(0, 0, 0, 0);
             }
+            fence_async_smem();
             __syncwarp();
+            if (lane_id() == 0)
+                bar_arrive_written<CG>(CG == 1 ? smem_u32(&ctl->full[stage]) : cluster_addr(&ctl->full[stage], 0));
+            stage = (stage + 1) % num_stages;
         }
     }
     } else {
@@ -468,52 +467,40 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 const uint8_t* xs = p.x_scales + src * p.x_scale_row_bytes;
                 const int nb = min(col0, p.cols_dim - 1) >> 7;
                 const float* ws = p.w_scales + (static_cast<int64_t>(q.group) * ((p.cols_dim + 127) >> 7) + nb) * q.steps;
-                // Scales of two blocks are loaded two blocks before they are used, and only then looked at: a
+                // A block's scales are loaded two blocks before they are used, and only then looked at: a
                 // multiplication next to the loads would wait for them.
-                uint32_t raw_x[2];
-                float raw_w[2];
-                auto fetch = [&](int s0) {
+                uint32_t x0 = raw_scale(xs, 0, p.scales_ue8m0), x1 = raw_scale(xs, min(1, q.steps - 1), p.scales_ue8m0);
+                float w0 = ws[0], w1 = ws[min(1, q.steps - 1)];
+#pragma unroll 1
+                for (int s = 0; s < q.steps; ++s) {
+                    const float f = scale_value(x0, p.scales_ue8m0) * w0;
+                    const uint64_t scale = pack_f32x2(__float_as_uint(f), __float_as_uint(f));
+                    x0 = x1, w0 = w1;
+                    const int ahead = min(s + 2, q.steps - 1);
+                    x1 = raw_scale(xs, ahead, p.scales_ue8m0);
+                    w1 = ws[ahead];
+                    ok = warp_wait(&ctl->acc_full[buf], acc_phase, abort_flag, p.status);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t at = lane_base + buf * kMaxTileCols + half * cols_half;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int b = min(s0 + i, q.steps - 1);
-                        raw_x[i] = raw_scale(xs, b, p.scales_ue8m0);
-                        raw_w[i] = ws[b];
-                    }
-                };
-                fetch(0);
-                for (int s0 = 0; s0 < q.steps && ok; s0 += 2) {
-                    float cur[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) cur[i] = scale_value(raw_x[i], p.scales_ue8m0) * raw_w[i];
-                    fetch(s0 + 2);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        if (s0 + j >= q.steps) break;
-                        ok = warp_wait(&ctl->acc_full[buf], acc_phase, abort_flag, p.status);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint32_t at = lane_base + buf * kMaxTileCols + half * cols_half;
-                        const uint64_t scale = pack_f32x2(__float_as_uint(cur[j]), __float_as_uint(cur[j]));
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            if (c * 32 < cols_half) {
-                                uint32_t u[32];
+                    for (int c = 0; c < 4; ++c) {
+                        if (c * 32 < cols_half) {
+                            uint32_t u[32];
+                            tc_ld32(at + c * 32, u);
+                            tc_wait_ld(u);
+                            if (c == 3 || (c + 1) * 32 >= cols_half) {  // all read: the accumulator is free
+                                tc_fence_before();
                                 __syncwarp();
-                                tc_ld32(at + c * 32, u);
-                                tc_wait_ld(u);
-                                if (c == 3 || (c + 1) * 32 >= cols_half) {  // all read: the accumulator is free
-                                    tc_fence_before();
-                                    __syncwarp();
-                                    if (lane_id() == 0) bar_arrive<CG>(acc_empty0 + 8 * buf);
-                                }
-#pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    fma_f32x2(acc[c][i], pack_f32x2(u[2 * i], u[2 * i + 1]), scale);
+                                if (lane_id() == 0) bar_arrive<CG>(acc_empty0 + 8 * buf);
                             }
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                fma_f32x2(acc[c][i], pack_f32x2(u[2 * i], u[2 * i + 1]), scale);
                         }
-                        buf ^= 1;
-                        acc_phase ^= buf == 0;
                     }
+                    buf ^= 1;
+                    acc_phase ^= buf == 0;
                 }
                 if (ok && row_ok) {
 #pragma unroll

@@ -37,10 +37,16 @@ __device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, volati
 
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int32_t* abort_flag,
                                            int32_t* status) {
-#pragma unroll 1
-    for (int i = 0; i < 16; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     return wait_long(bar, parity, abort_flag, status);
+}
+
+// One lane of a converged warp.  Code that it guards is known to run in a single thread: products and loads
+// issued under a test of the lane number took half as long again.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t is;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
+    return is != 0;
 }
 
 // The same for a whole warp: every lane gets the same answer.
