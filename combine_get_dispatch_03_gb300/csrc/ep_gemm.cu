@@ -173,17 +173,29 @@ __device__ __forceinline__ void store_bf16(uint8_t* row, int col, int cols, cons
 }
 
 // The same in fp32, optionally added to what is there.
-__device__ __forceinline__ void store_fp32(uint8_t* row, int col, int cols, const float (&v)[32], bool accumulate) {
+__device__ __forceinline__ void store_fp32(uint8_t* row, int col, int cols, const float (&v)[32], bool accumulate, bool wide) {
     float* p = reinterpret_cast<float*>(row) + col;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (col + 4 * i + 4 > cols) break;
-        float4 q = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        if (accumulate) {
-            const float4 o = *reinterpret_cast<const float4*>(p + 4 * i);
-            q = make_float4(q.x + o.x, q.y + o.y, q.z + o.z, q.w + o.w);
+    for (int i = 0; i < 4; ++i) {
+        if (col + 8 * i + 8 > cols) break;
+        float4 q[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            q[j] = make_float4(v[8 * i + 4 * j], v[8 * i + 4 * j + 1], v[8 * i + 4 * j + 2], v[8 * i + 4 * j + 3]);
+            if (accumulate) {
+                const float4 o = *reinterpret_cast<const float4*>(p + 8 * i + 4 * j);
+                q[j] = make_float4(q[j].x + o.x, q[j].y + o.y, q[j].z + o.z, q[j].w + o.w);
+            }
         }
-        *reinterpret_cast<float4*>(p + 4 * i) = q;
+        if (wide) {
+            const uint32_t w[8] = {__float_as_uint(q[0].x), __float_as_uint(q[0].y), __float_as_uint(q[0].z),
+                                   __float_as_uint(q[0].w), __float_as_uint(q[1].x), __float_as_uint(q[1].y),
+                                   __float_as_uint(q[1].z), __float_as_uint(q[1].w)};
+            st_global_v8(p + 8 * i, w);
+        } else {
+            *reinterpret_cast<float4*>(p + 8 * i) = q[0];
+            *reinterpret_cast<float4*>(p + 8 * i + 4) = q[1];
+        }
     }
 }
 
@@ -448,7 +460,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     for (int i = 0; i < 32; ++i) v[i] = FORM == kWeightGrad && q.steps == 0 ? 0.0f : __uint_as_float(u[i]);
                     if (row_ok && col0 + c < p.cols_dim) {
                         if (FORM == kWeightGrad && p.out_fp32)
-                            store_fp32(out_row(p, out_at), col0 + c, p.cols_dim, v, p.accumulate != 0);
+                            store_fp32(out_row(p, out_at), col0 + c, p.cols_dim, v, p.accumulate != 0, p.wide_stores != 0);
                         else
                             store_bf16(out_row(p, out_at), col0 + c, p.cols_dim, v, p.wide_stores != 0);
                     }
