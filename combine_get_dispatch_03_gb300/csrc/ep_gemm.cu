@@ -36,8 +36,8 @@ constexpr int kColBox = 64;         // the same for narrow tiles
 constexpr int kMaxStages = 12;
 constexpr int kEpilogueWarps = 8;
 constexpr int kGemmThreads = (4 + kEpilogueWarps) * kWarpSize;  // warps 2 and 3 are idle: register splits go by four warps
-constexpr int kMaxSmem = 232448;
-constexpr int kControlBytes = 512;
+constexpr int kControlBytes = 512;  // static shared memory
+constexpr int kMaxSmem = 232448 - kControlBytes;
 
 struct GemmParams {
     Groups groups;          // of the row operand (weight grad: operands) and the output's rows
@@ -72,6 +72,7 @@ struct Control {
     uint32_t tmem;
     int32_t abort_flag;
     int32_t warp_sums[kGemmThreads / kWarpSize];
+    int32_t tiles, col_tiles, tile_cols;  // output tiles in all, tiles across, columns of one
 };
 static_assert(sizeof(Control) <= kControlBytes, "control block");
 
@@ -79,27 +80,25 @@ struct Tile {
     int group, row0, rows, m0, n0, steps;  // rows: valid rows of the group; m0: tile's first row in the group
 };
 
-// The group table in shared memory, and how tiles are numbered.
+// The group table in shared memory.
 struct Table {
     int32_t* before;  // [groups + 1] row tiles before each group
     int32_t* count;   // [groups]
     int32_t* begin;   // [groups]
-    int32_t groups, col_tiles, tile_cols, tile_rows;
-    int total;
 };
 
-template <int FORM>
-__device__ __forceinline__ Tile decode(const Table& t, const GemmParams& p, int tile) {
+template <int FORM, int CG>
+__device__ __forceinline__ Tile decode(const Table& t, const GemmParams& p, const Control& ctl, int tile) {
     Tile r;
-    const int lo = find_group(t.before, t.groups, tile / t.col_tiles);
-    const int in = tile - t.before[lo] * t.col_tiles;
+    const int lo = find_group(t.before, p.groups.groups, tile / ctl.col_tiles);
+    const int in = tile - t.before[lo] * ctl.col_tiles;
     const int row_tiles = t.before[lo + 1] - t.before[lo];
     r.group = lo;
     r.row0 = t.begin[lo];
     r.rows = t.count[lo];
     // row tiles turn fastest: CTAs side by side share a weight tile
-    r.n0 = in / row_tiles * t.tile_cols;
-    r.m0 = in % row_tiles * t.tile_rows;
+    r.n0 = in / row_tiles * ctl.tile_cols;
+    r.m0 = in % row_tiles * (kTileRows * CG);
     if constexpr (FORM == kWeightGrad) r.steps = (r.rows + 63) >> 6;
     else if constexpr (FORM == kFp8) r.steps = (p.contraction + 127) >> 7;
     else r.steps = (p.contraction + 63) >> 6;
@@ -109,35 +108,38 @@ __device__ __forceinline__ Tile decode(const Table& t, const GemmParams& p, int 
 // Fills the table: clamps every group to the rows that exist (the first group that does not fit sets
 // EP_ERR_CAPACITY), and sums the row tiles.  All threads of the CTA.
 template <int FORM, int CG>
-__device__ __forceinline__ void build_table(Table& t, const GemmParams& p, Control* ctl) {
-    const int per = (t.groups + kGemmThreads - 1) / kGemmThreads;
+__device__ __forceinline__ void build_table(const Table& t, const GemmParams& p, Control& ctl) {
+    constexpr int kRows = kTileRows * CG;
+    const int groups = p.groups.groups;
+    const int per = (groups + kGemmThreads - 1) / kGemmThreads;
     const int first = threadIdx.x * per;
-    const int last = min(first + per, t.groups);
+    const int last = min(first + per, groups);
     int sum = 0, total = 0;
     for (int g = first; g < last; ++g) {
         const Group q = load_group(p.groups, g, p.status);
         t.count[g] = q.count;
         t.begin[g] = q.begin;
         t.before[g] = sum;
-        sum += ((FORM == kWeightGrad ? p.rows_dim : q.count) + t.tile_rows - 1) / t.tile_rows;
+        sum += ((FORM == kWeightGrad ? p.rows_dim : q.count) + kRows - 1) / kRows;
     }
-    const int base = block_prefix<kGemmThreads>(sum, ctl->warp_sums, &total);
+    const int base = block_prefix<kGemmThreads>(sum, ctl.warp_sums, &total);
     for (int g = first; g < last; ++g) t.before[g] += base;
-    if (threadIdx.x == 0) t.before[t.groups] = total;
-    __syncthreads();
-    // Tile width: the one whose waves over the CTAs take the least time, a wave costing its columns plus
-    // what a tile costs at any width.
-    const int workers = gridDim.x / CG;
-    int best = kMaxTileCols;
-    int64_t best_cost = INT64_MAX;
-    for (int cols = kMaxTileCols; cols >= kColBox * CG; cols >>= 1) {
-        const int64_t tiles = static_cast<int64_t>(total) * ((p.cols_dim + cols - 1) / cols);
-        const int64_t cost = (tiles + workers - 1) / workers * (cols + 32);
-        if (cost < best_cost) best_cost = cost, best = cols;
+    if (threadIdx.x == 0) {
+        t.before[groups] = total;
+        // Tile width: the one whose waves over the CTAs take the least time, a wave costing its columns plus
+        // what a tile costs at any width.
+        const int workers = gridDim.x / CG;
+        int best = kMaxTileCols;
+        int64_t best_cost = INT64_MAX;
+        for (int cols = kMaxTileCols; cols >= kColBox * CG; cols >>= 1) {
+            const int64_t tiles = static_cast<int64_t>(total) * ((p.cols_dim + cols - 1) / cols);
+            const int64_t cost = (tiles + workers - 1) / workers * (cols + 32);
+            if (cost < best_cost) best_cost = cost, best = cols;
+        }
+        ctl.tile_cols = best;
+        ctl.col_tiles = (p.cols_dim + best - 1) / best;
+        ctl.tiles = total * ctl.col_tiles;
     }
-    t.tile_cols = best;
-    t.col_tiles = (p.cols_dim + best - 1) / best;
-    t.total = total * t.col_tiles;
 }
 
 // A row's scale of one block as it lies in memory, and as the fp32 it stands for.
@@ -207,39 +209,34 @@ template <int FORM, int CG>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     grouped_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
     extern __shared__ uint8_t raw[];
+    __shared__ Control ctl;
     uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-    Control* ctl = reinterpret_cast<Control*>(smem);
     Table t;
-    t.groups = p.groups.groups;
-    t.tile_rows = kTileRows * CG;
-    t.before = reinterpret_cast<int32_t*>(smem + kControlBytes);
-    t.count = t.before + t.groups + 1;
-    t.begin = t.count + t.groups;
-    uint32_t dyn;
-    asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(dyn));
-    const uint32_t table_end = (kControlBytes + 4u * (3u * t.groups + 1u) + 1023u) & ~1023u;
+    t.before = reinterpret_cast<int32_t*>(smem);
+    t.count = t.before + p.groups.groups + 1;
+    t.begin = t.count + p.groups.groups;
+    const uint32_t table_end = (4u * (3u * p.groups.groups + 1u) + 1023u) & ~1023u;
     uint8_t* const stages = smem + table_end;
 
     const int warp = threadIdx.x / kWarpSize;
     const uint32_t rank = CG == 1 ? 0 : cluster_rank();
-    volatile int32_t* abort_flag = &ctl->abort_flag;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
-            mbar_init(&ctl->full[i], CG);
-            mbar_init(&ctl->empty[i], 1);
-            mbar_init(&ctl->tail_full[i], 1);
+            mbar_init(&ctl.full[i], CG);
+            mbar_init(&ctl.empty[i], 1);
+            mbar_init(&ctl.tail_full[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&ctl->acc_full[i], 1);
-            mbar_init(&ctl->acc_empty[i], kEpilogueWarps * CG);
+            mbar_init(&ctl.acc_full[i], 1);
+            mbar_init(&ctl.acc_empty[i], kEpilogueWarps * CG);
         }
-        mbar_init(&ctl->drained, 1);
-        ctl->abort_flag = 0;
+        mbar_init(&ctl.drained, 1);
+        ctl.abort_flag = 0;
         fence_barrier_init();
         prefetch_map(&maps.a);
         prefetch_map(&maps.b);
     }
-    if (warp == 1) tmem_alloc<CG>(&ctl->tmem, 512);
+    if (warp == 1) tmem_alloc<CG>(&ctl.tmem, 512);
     pdl_enter();
     build_table<FORM, CG>(t, p, ctl);
     tc_fence_before();
@@ -247,11 +244,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     else __syncthreads();
     tc_fence_after();
 
-    const uint32_t tmem = ctl->tmem;
-    const int cols_here = t.tile_cols / CG;  // columns of the weight operand that this CTA loads
+    const uint32_t tmem = ctl.tmem;
+    const int cols_here = ctl.tile_cols / CG;  // columns of the weight operand that this CTA loads
     const uint32_t a_bytes = kTileRows * kRowBytes;
     const uint32_t stage_bytes = a_bytes + cols_here * kRowBytes;
-    const int num_stages = min(kMaxStages, static_cast<int>((dyn - 1024u - table_end) / stage_bytes));
+    const int num_stages = min(kMaxStages, static_cast<int>((kMaxSmem - 1024u - table_end) / stage_bytes));
     const int worker = blockIdx.x / CG, workers = gridDim.x / CG;
 
     // The FP8 form holds 128 sums a thread in its eight epilogue warps: registers move there from the
@@ -264,17 +261,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         uint32_t stage = 0, phase = 0;
         uint32_t tail_phase = 0, tail_last = 0;  // per stage: uses of tail_full, mod 2; whether its last use was one
         bool ok = true;
-        const uint32_t full0 = CG == 1 ? smem_u32(ctl->full) : cluster_addr(ctl->full, 0);
+        const uint32_t full0 = CG == 1 ? smem_u32(ctl.full) : cluster_addr(ctl.full, 0);
         uint32_t used = 0;
-        for (int tile = worker; ok && tile < t.total; tile += workers) {
-            const Tile q = decode<FORM>(t, p, tile);
+        for (int tile = worker; ok && tile < ctl.tiles; tile += workers) {
+            const Tile q = decode<FORM, CG>(t, p, ctl, tile);
             const int my_m0 = q.m0 + static_cast<int>(rank) * kTileRows;
             const int rows_here = min(kTileRows, q.rows - my_m0);
             const int small_boxes = rows_here > kTileRows / 2 ? 0 : (max(0, rows_here) + kRowBox - 1) / kRowBox;
             const uint32_t bytes = FORM == kWeightGrad ? stage_bytes
                                                        : cols_here * kRowBytes + (rows_here > kTileRows / 2 ? a_bytes : small_boxes * (kRowBox * kRowBytes));
             for (int s = 0; s < q.steps; ++s) {
-                ok = wait_phase(&ctl->empty[stage], phase ^ 1, abort_flag, p.status);
+                ok = wait_phase(&ctl.empty[stage], phase ^ 1, &ctl.abort_flag, p.status);
                 if (!ok) break;
                 uint8_t* a = stages + stage * stage_bytes;
                 uint8_t* b = a + a_bytes;
@@ -283,8 +280,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 if constexpr (FORM == kWeightGrad) {
                     const bool tail = (s + 1) * 64 > q.rows;
                     if (tail) {
-                        bar = smem_u32(&ctl->tail_full[stage]);
-                        mbar_arrive_expect_tx(&ctl->tail_full[stage], stage_bytes);
+                        bar = smem_u32(&ctl.tail_full[stage]);
+                        mbar_arrive_expect_tx(&ctl.tail_full[stage], stage_bytes);
                         tail_phase ^= 1u << stage;
                         tail_last |= 1u << stage;
                     } else {
@@ -340,7 +337,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 if (stage == 0) phase ^= 1;
                 stage = (stage == 0 ? num_stages : stage) - 1;
                 const bool tail = (tail_last >> stage) & 1;
-                uint64_t* bar = tail ? &ctl->tail_full[stage] : &ctl->full[stage];
+                uint64_t* bar = tail ? &ctl.tail_full[stage] : &ctl.full[stage];
                 const uint32_t parity = tail ? ((tail_phase >> stage) & 1) ^ 1 : phase;
                 for (int k = 0; k < (1 << 12) && !mbar_try_wait(bar, parity); ++k) {
                 }
@@ -355,16 +352,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             bool ok = true;
             constexpr bool a_mn = FORM == kWeightGrad;
             constexpr bool b_mn = FORM == kWeightGrad || FORM == kTransposed;
-            const uint32_t idesc = mma_desc(FORM == kFp8 ? 0 : 1, a_mn, b_mn, kTileRows * CG, t.tile_cols);
-            for (int tile = worker; ok && tile < t.total; tile += workers) {
-                const Tile q = decode<FORM>(t, p, tile);
-                if (FORM != kFp8) ok = wait_phase(&ctl->acc_empty[buf], acc_phase ^ 1, abort_flag, p.status);
+            const uint32_t idesc = mma_desc(FORM == kFp8 ? 0 : 1, a_mn, b_mn, kTileRows * CG, ctl.tile_cols);
+            for (int tile = worker; ok && tile < ctl.tiles; tile += workers) {
+                const Tile q = decode<FORM, CG>(t, p, ctl, tile);
+                if (FORM != kFp8) ok = wait_phase(&ctl.acc_empty[buf], acc_phase ^ 1, &ctl.abort_flag, p.status);
                 for (int s = 0; s < q.steps && ok; ++s) {
                     if (FORM == kFp8) {
-                        ok = wait_phase(&ctl->acc_empty[buf], acc_phase ^ 1, abort_flag, p.status);
+                        ok = wait_phase(&ctl.acc_empty[buf], acc_phase ^ 1, &ctl.abort_flag, p.status);
                         if (!ok) break;
                     }
-                    ok = wait_phase(&ctl->full[stage], phase, abort_flag, p.status);
+                    ok = wait_phase(&ctl.full[stage], phase, &ctl.abort_flag, p.status);
                     if (!ok) break;
                     if (FORM == kWeightGrad && q.rows - s * 64 < 64) fence_written<CG>();
                     tc_fence_after();
@@ -376,24 +373,24 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     for (int i = 0; i < 4; ++i)
                         tc_mma<CG, FORM == kFp8>(d, da + i * (a_mn ? 128 : 2), db + i * (b_mn ? 128 : 2), idesc,
                                                  (FORM == kFp8 ? 0 : s) | i);
-                    tc_commit<CG>(&ctl->empty[stage]);
+                    tc_commit<CG>(&ctl.empty[stage]);
                     if (FORM == kFp8) {
-                        tc_commit<CG>(&ctl->acc_full[buf]);
+                        tc_commit<CG>(&ctl.acc_full[buf]);
                         buf ^= 1;
                         acc_phase ^= buf == 0;
                     }
                     if (++stage == static_cast<uint32_t>(num_stages)) stage = 0, phase ^= 1;
                 }
                 if (FORM != kFp8 && ok) {
-                    tc_commit<CG>(&ctl->acc_full[buf]);
+                    tc_commit<CG>(&ctl.acc_full[buf]);
                     buf ^= 1;
                     acc_phase ^= buf == 0;
                 }
             }
             if (!ok) {
                 // Given up: the products already issued still write tensor memory.
-                tc_commit<CG>(&ctl->drained);
-                for (int k = 0; k < (1 << 12) && !mbar_try_wait(&ctl->drained, 0); ++k) {
+                tc_commit<CG>(&ctl.drained);
+                for (int k = 0; k < (1 << 12) && !mbar_try_wait(&ctl.drained, 0); ++k) {
                 }
             }
         }
@@ -402,12 +399,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         // The rows of a group's last, partial block past its end belong to others: zero them in both operands.
         uint32_t stage = 0, tail_phase = 0;  // tail_phase, per stage: uses of tail_full, mod 2
         bool ok = true;
-        for (int tile = worker; ok && tile < t.total; tile += workers) {
-            const Tile q = decode<FORM>(t, p, tile);
+        for (int tile = worker; ok && tile < ctl.tiles; tile += workers) {
+            const Tile q = decode<FORM, CG>(t, p, ctl, tile);
             const int whole = q.rows / 64, valid = q.rows % 64;
             stage = (stage + whole) % num_stages;
             if (valid == 0) continue;
-            ok = warp_wait(&ctl->tail_full[stage], (tail_phase >> stage) & 1, abort_flag, p.status);
+            ok = warp_wait(&ctl.tail_full[stage], (tail_phase >> stage) & 1, &ctl.abort_flag, p.status);
             tail_phase ^= 1u << stage;
             uint8_t* a = stages + stage * stage_bytes;
             const int chunks = (kTileRows + cols_here) / 64;
@@ -419,7 +416,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             fence_async_smem();
             __syncwarp();
             if (lane_id() == 0)
-                bar_arrive_written<CG>(CG == 1 ? smem_u32(&ctl->full[stage]) : cluster_addr(&ctl->full[stage], 0));
+                bar_arrive_written<CG>(CG == 1 ? smem_u32(&ctl.full[stage]) : cluster_addr(&ctl.full[stage], 0));
             stage = (stage + 1) % num_stages;
         }
     }
@@ -430,19 +427,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int quarter = warp & 3;               // the 32 lanes of tensor memory that this warp may read
         const int half = w >> 2;                    // which half of the tile's columns
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-        const int cols_half = t.tile_cols / 2;
-        const uint32_t acc_empty0 = CG == 1 ? smem_u32(ctl->acc_empty) : cluster_addr(ctl->acc_empty, 0);
+        const int cols_half = ctl.tile_cols / 2;
+        const uint32_t acc_empty0 = CG == 1 ? smem_u32(ctl.acc_empty) : cluster_addr(ctl.acc_empty, 0);
         int buf = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
-        for (int tile = worker; ok && tile < t.total; tile += workers) {
-            const Tile q = decode<FORM>(t, p, tile);
+        for (int tile = worker; ok && tile < ctl.tiles; tile += workers) {
+            const Tile q = decode<FORM, CG>(t, p, ctl, tile);
             const int row = q.m0 + static_cast<int>(rank) * kTileRows + quarter * 32 + lane_id();  // in the group
             const int col0 = q.n0 + half * cols_half;
             const bool row_ok = row < (FORM == kWeightGrad ? p.rows_dim : q.rows);
             const int64_t out_at = FORM == kWeightGrad ? static_cast<int64_t>(q.group) * p.rows_dim + row : static_cast<int64_t>(q.row0) + row;
             if constexpr (FORM != kFp8) {
-                ok = warp_wait(&ctl->acc_full[buf], acc_phase, abort_flag, p.status);
+                ok = warp_wait(&ctl.acc_full[buf], acc_phase, &ctl.abort_flag, p.status);
                 if (!ok) break;
                 tc_fence_after();
                 for (int c = 0; c < cols_half; c += 32) {
@@ -470,46 +467,45 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             } else {
                 // Each block of 128 has its own scales: its products arrive in an accumulator of their own and
                 // are scaled and added here, in fp32 registers, 128 columns a thread at most.
-                uint64_t acc[4][16];  // pairs of fp32
+                uint64_t acc[2][32];  // pairs of fp32
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 2; ++c)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[c][i] = 0;
+                    for (int i = 0; i < 32; ++i) acc[c][i] = 0;
                 const int64_t src = static_cast<int64_t>(q.row0) + min(row, q.rows - 1);
                 const uint8_t* xs = p.x_scales + src * p.x_scale_row_bytes;
                 const int nb = min(col0, p.cols_dim - 1) >> 7;
                 const float* ws = p.w_scales + (static_cast<int64_t>(q.group) * ((p.cols_dim + 127) >> 7) + nb) * q.steps;
-                // A block's scales are loaded two blocks before they are used, and only then looked at: a
+                // A block's scales are loaded a block before they are used, and only then looked at: a
                 // multiplication next to the loads would wait for them.
-                uint32_t x0 = raw_scale(xs, 0, p.scales_ue8m0), x1 = raw_scale(xs, min(1, q.steps - 1), p.scales_ue8m0);
-                float w0 = ws[0], w1 = ws[min(1, q.steps - 1)];
+                uint32_t x_next = raw_scale(xs, 0, p.scales_ue8m0);
+                float w_next = ws[0];
 #pragma unroll 1
                 for (int s = 0; s < q.steps; ++s) {
-                    const float f = scale_value(x0, p.scales_ue8m0) * w0;
-                    const uint64_t scale = pack_f32x2(__float_as_uint(f), __float_as_uint(f));
-                    x0 = x1, w0 = w1;
-                    const int ahead = min(s + 2, q.steps - 1);
-                    x1 = raw_scale(xs, ahead, p.scales_ue8m0);
-                    w1 = ws[ahead];
-                    ok = warp_wait(&ctl->acc_full[buf], acc_phase, abort_flag, p.status);
+                    ok = warp_wait(&ctl.acc_full[buf], acc_phase, &ctl.abort_flag, p.status);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t at = lane_base + buf * kMaxTileCols + half * cols_half;
+                    uint32_t u[64];
+                    tc_ld64(at, u);
+                    const float f = scale_value(x_next, p.scales_ue8m0) * w_next;  // while the load is on its way
+                    const uint64_t scale = pack_f32x2(__float_as_uint(f), __float_as_uint(f));
+                    if (s + 1 < q.steps) {
+                        x_next = raw_scale(xs, s + 1, p.scales_ue8m0);
+                        w_next = ws[s + 1];
+                    }
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        if (c * 32 < cols_half) {
-                            uint32_t u[32];
-                            tc_ld32(at + c * 32, u);
-                            tc_wait_ld(u);
-                            if (c == 3 || (c + 1) * 32 >= cols_half) {  // all read: the accumulator is free
-                                tc_fence_before();
-                                __syncwarp();
-                                if (lane_id() == 0) bar_arrive<CG>(acc_empty0 + 8 * buf);
-                            }
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                fma_f32x2(acc[c][i], pack_f32x2(u[2 * i], u[2 * i + 1]), scale);
+                    for (int c = 0; c < 2; ++c) {
+                        tc_wait_ld(u);
+                        if (c == 1 || cols_half <= 64) {  // all read: the accumulator is free
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane_id() == 0) bar_arrive<CG>(acc_empty0 + 8 * buf);
                         }
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) fma_f32x2(acc[c][i], pack_f32x2(u[2 * i], u[2 * i + 1]), scale);
+                        if (cols_half <= 64) break;
+                        if (c == 0) tc_ld64(at + 64, u);
                     }
                     buf ^= 1;
                     acc_phase ^= buf == 0;
@@ -521,8 +517,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                             float v[32];
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
-                                v[2 * i] = __uint_as_float(static_cast<uint32_t>(acc[c][i]));
-                                v[2 * i + 1] = __uint_as_float(static_cast<uint32_t>(acc[c][i] >> 32));
+                                const uint64_t pair = acc[c / 2][c % 2 * 16 + i];
+                                v[2 * i] = __uint_as_float(static_cast<uint32_t>(pair));
+                                v[2 * i + 1] = __uint_as_float(static_cast<uint32_t>(pair >> 32));
                             }
                             store_bf16(out_row(p, out_at), col0 + c * 32, p.cols_dim, v, p.wide_stores != 0);
                         }
