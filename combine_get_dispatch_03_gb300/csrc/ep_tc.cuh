@@ -21,13 +21,15 @@ __device__ __forceinline__ uint64_t global_ns() {
 }
 
 __device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int32_t* abort_flag, int32_t* status) {
-    const uint64_t begin = global_ns();
+    uint64_t begin = 0;  // the clock is read only after polls that came to nothing: reading it takes long
     for (;;) {
 #pragma unroll 1
         for (int i = 0; i < 64; ++i)
             if (mbar_try_wait(bar, parity)) return true;
         if (*abort_flag) return false;
-        if (global_ns() - begin > kWaitLimitNs) {
+        const uint64_t now = global_ns();
+        if (begin == 0) begin = now;
+        if (now - begin > kWaitLimitNs) {
             *abort_flag = 1;
             report(status, EP_ERR_TIMEOUT);
             return false;
