@@ -33,6 +33,7 @@ constexpr int kRowBytes = 128;      // bytes of one operand row in a stage (the 
 constexpr int kBox = 128;           // output elements (rows or columns) of a tensor-map load: 16 KB
 constexpr int kRowBox = 32;         // the same for a group's last rows: a short group loads few
 constexpr int kColBox = 64;         // the same for narrow tiles
+constexpr int kTileOverhead = 32;   // columns that a tile's width-independent cost is worth
 constexpr int kMaxStages = 12;
 constexpr int kEpilogueWarps = 8;
 constexpr int kGemmThreads = (4 + kEpilogueWarps) * kWarpSize;  // warps 2 and 3 are idle: register splits go by four warps
@@ -127,13 +128,13 @@ __device__ __forceinline__ void build_table(const Table& t, const GemmParams& p,
     if (threadIdx.x == 0) {
         t.before[groups] = total;
         // Tile width: the one whose waves over the CTAs take the least time, a wave costing its columns plus
-        // what a tile costs at any width.
+        // what a tile costs at any width (its rows' loads, its turn).
         const int workers = gridDim.x / CG;
         int best = kMaxTileCols;
         int64_t best_cost = INT64_MAX;
         for (int cols = kMaxTileCols; cols >= kColBox * CG; cols >>= 1) {
             const int64_t tiles = static_cast<int64_t>(total) * ((p.cols_dim + cols - 1) / cols);
-            const int64_t cost = (tiles + workers - 1) / workers * (cols + 32);
+            const int64_t cost = (tiles + workers - 1) / workers * (cols + kTileOverhead);
             if (cost < best_cost) best_cost = cost, best = cols;
         }
         ctl.tile_cols = best;

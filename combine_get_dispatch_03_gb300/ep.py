@@ -556,28 +556,34 @@ def _rows(t, name, dtype, device, rows=None, width=None):
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the handle lives on {device}")
-    if t.dim() < 2:
-        raise ValueError(f"{name} must be [rows][width], got {tuple(t.shape)}")
-    n, inner = t.numel() // t.shape[-1] if t.shape[-1] else 0, t.shape[-1]
+    shape = t.shape
+    if len(shape) < 2:
+        raise ValueError(f"{name} must be [rows][width], got {tuple(shape)}")
+    inner, count = shape[-1], t.numel()
+    n = count // inner if inner else 0
     if (rows is not None and n != rows) or (width is not None and inner != width):
         raise ValueError(f"{name}: {n} rows of {inner}, expected {n if rows is None else rows} of "
                          f"{inner if width is None else width}")
-    step = None  # elements between rows; an axis of one entry has no say in it
-    span = 1
-    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
-        if size == 1:
-            continue
-        if step is None:
-            step = stride
-        elif stride != step * span:
-            raise ValueError(f"{name}: its rows are not evenly spaced")
-        span *= size
-    if n and inner > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name}: the elements of a row must be contiguous")
-    row_bytes = (inner if step is None else step) * t.element_size()
-    if step is None:  # one row: any stride will do
+    row_bytes = inner * dtype.itemsize
+    if n == 1:  # one row: any stride will do
+        if t.stride(-1) != 1 and inner > 1:
+            raise ValueError(f"{name}: the elements of a row must be contiguous")
         row_bytes = (row_bytes + 15) // 16 * 16
-    return (t.data_ptr() if t.numel() else _dummy(device).data_ptr()), n, inner, row_bytes
+    elif not t.is_contiguous():
+        if count and inner > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name}: the elements of a row must be contiguous")
+        step = None  # elements between rows; an axis of one entry has no say in it
+        span = 1
+        for size, stride in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
+            if size == 1:
+                continue
+            if step is None:
+                step = stride
+            elif stride != step * span:
+                raise ValueError(f"{name}: its rows are not evenly spaced")
+            span *= size
+        row_bytes = step * dtype.itemsize
+    return (t.data_ptr() if count else _dummy(device).data_ptr()), n, inner, row_bytes
 
 
 def _group_arrays(h, group_count, group_begin):
