@@ -27,6 +27,12 @@ namespace {
 
 enum GemmForm { kForward = 0, kTransposed = 1, kWeightGrad = 2, kFp8 = 3 };
 
+// Steps (128 bytes of the contraction) that one accumulator sums in tensor memory before its sums are added up in
+// fp32 registers; 0: all of them.  FP8: one block, for its scales.  Weight gradient: 512 rows -- the tensor cores cut
+// sums off instead of rounding them, and over 2048 rows in one accumulator that left 2.4e-6 of the
+// result against 64 bits; the other forms round to bf16, far above that.
+constexpr int segment_steps(int form) { return form == kFp8 ? 1 : form == kWeightGrad ? 8 : 0; }
+
 constexpr int kTileRows = 128;      // output rows per CTA
 constexpr int kMaxTileCols = 256;
 constexpr int kRowBytes = 128;      // bytes of one operand row in a stage (the swizzle's span)
@@ -251,11 +257,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const uint32_t stage_bytes = a_bytes + cols_here * kRowBytes;
     const int num_stages = min(kMaxStages, static_cast<int>((kMaxSmem - 1024u - table_end) / stage_bytes));
     const int worker = blockIdx.x / CG, workers = gridDim.x / CG;
+    constexpr int kSegment = segment_steps(FORM);
 
-    // The FP8 form holds 128 sums a thread in its eight epilogue warps: registers move there from the
+    // Forms with segments hold 128 sums a thread in their eight epilogue warps: registers move there from the
     // others (72 + 2 * 216 = 3 * 168, what the block was launched with).
     if (warp < 4) {
-    if constexpr (FORM == kFp8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if constexpr (kSegment != 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0) {
         if (elect_one()) {
         // ------------------------------------------------------------- loads
@@ -356,9 +363,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const uint32_t idesc = mma_desc(FORM == kFp8 ? 0 : 1, a_mn, b_mn, kTileRows * CG, ctl.tile_cols);
             for (int tile = worker; ok && tile < ctl.tiles; tile += workers) {
                 const Tile q = decode<FORM, CG>(t, p, ctl, tile);
-                if (FORM != kFp8) ok = wait_phase(&ctl.acc_empty[buf], acc_phase ^ 1, &ctl.abort_flag, p.status);
                 for (int s = 0; s < q.steps && ok; ++s) {
-                    if (FORM == kFp8) {
+                    const int in_segment = kSegment ? s % kSegment : s;
+                    if (in_segment == 0) {
                         ok = wait_phase(&ctl.acc_empty[buf], acc_phase ^ 1, &ctl.abort_flag, p.status);
                         if (!ok) break;
                     }
@@ -373,19 +380,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         tc_mma<CG, FORM == kFp8>(d, da + i * (a_mn ? 128 : 2), db + i * (b_mn ? 128 : 2), idesc,
-                                                 (FORM == kFp8 ? 0 : s) | i);
+                                                 in_segment | i);
                     tc_commit<CG>(&ctl.empty[stage]);
-                    if (FORM == kFp8) {
+                    if (s == q.steps - 1 || (kSegment && in_segment == kSegment - 1)) {
                         tc_commit<CG>(&ctl.acc_full[buf]);
                         buf ^= 1;
                         acc_phase ^= buf == 0;
                     }
                     if (++stage == static_cast<uint32_t>(num_stages)) stage = 0, phase ^= 1;
-                }
-                if (FORM != kFp8 && ok) {
-                    tc_commit<CG>(&ctl.acc_full[buf]);
-                    buf ^= 1;
-                    acc_phase ^= buf == 0;
                 }
             }
             if (!ok) {
@@ -423,7 +425,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     } else {
         // ------------------------------------------------- accumulators out
-        if constexpr (FORM == kFp8) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        if constexpr (kSegment != 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int w = warp - 4;
         const int quarter = warp & 3;               // the 32 lanes of tensor memory that this warp may read
         const int half = w >> 2;                    // which half of the tile's columns
@@ -439,7 +441,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const int col0 = q.n0 + half * cols_half;
             const bool row_ok = row < (FORM == kWeightGrad ? p.rows_dim : q.rows);
             const int64_t out_at = FORM == kWeightGrad ? static_cast<int64_t>(q.group) * p.rows_dim + row : static_cast<int64_t>(q.row0) + row;
-            if constexpr (FORM != kFp8) {
+            if constexpr (kSegment == 0) {
                 ok = warp_wait(&ctl.acc_full[buf], acc_phase, &ctl.abort_flag, p.status);
                 if (!ok) break;
                 tc_fence_after();
@@ -455,46 +457,51 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     }
                     float v[32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = FORM == kWeightGrad && q.steps == 0 ? 0.0f : __uint_as_float(u[i]);
-                    if (row_ok && col0 + c < p.cols_dim) {
-                        if (FORM == kWeightGrad && p.out_fp32)
-                            store_fp32(out_row(p, out_at), col0 + c, p.cols_dim, v, p.accumulate != 0, p.wide_stores != 0);
-                        else
-                            store_bf16(out_row(p, out_at), col0 + c, p.cols_dim, v, p.wide_stores != 0);
-                    }
+                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+                    if (row_ok && col0 + c < p.cols_dim)
+                        store_bf16(out_row(p, out_at), col0 + c, p.cols_dim, v, p.wide_stores != 0);
                 }
                 buf ^= 1;
                 acc_phase ^= buf == 0;
             } else {
-                // Each block of 128 has its own scales: its products arrive in an accumulator of their own and
-                // are scaled and added here, in fp32 registers, 128 columns a thread at most.
+                // The sums of a segment arrive in an accumulator of their own and are added up here, 128 columns a
+                // thread at most; in FP8 a segment is a block of 128 with its own scales.
                 uint64_t acc[2][32];  // pairs of fp32
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) acc[c][i] = 0;
-                const int64_t src = static_cast<int64_t>(q.row0) + min(row, q.rows - 1);
-                const uint8_t* xs = p.x_scales + src * p.x_scale_row_bytes;
-                const int nb = min(col0, p.cols_dim - 1) >> 7;
-                const float* ws = p.w_scales + (static_cast<int64_t>(q.group) * ((p.cols_dim + 127) >> 7) + nb) * q.steps;
+                const int segments = (q.steps + kSegment - 1) / kSegment;
                 // A block's scales are loaded a block before they are used, and only then looked at: a
                 // multiplication next to the loads would wait for them.
-                uint32_t x_next = raw_scale(xs, 0, p.scales_ue8m0);
-                float w_next = ws[0];
+                const uint8_t* xs = nullptr;
+                const float* ws = nullptr;
+                uint32_t x_next = 0;
+                float w_next = 0.0f;
+                if constexpr (FORM == kFp8) {
+                    xs = p.x_scales + (static_cast<int64_t>(q.row0) + min(row, q.rows - 1)) * p.x_scale_row_bytes;
+                    const int nb = min(col0, p.cols_dim - 1) >> 7;
+                    ws = p.w_scales + (static_cast<int64_t>(q.group) * ((p.cols_dim + 127) >> 7) + nb) * q.steps;
+                    x_next = raw_scale(xs, 0, p.scales_ue8m0);
+                    w_next = ws[0];
+                }
 #pragma unroll 1
-                for (int s = 0; s < q.steps; ++s) {
+                for (int s = 0; s < segments; ++s) {
                     ok = warp_wait(&ctl.acc_full[buf], acc_phase, &ctl.abort_flag, p.status);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t at = lane_base + buf * kMaxTileCols + half * cols_half;
                     uint32_t u[64];
                     tc_ld64(at, u);
-                    const float f = scale_value(x_next, p.scales_ue8m0) * w_next;  // while the load is on its way
-                    const uint64_t scale = pack_f32x2(__float_as_uint(f), __float_as_uint(f));
-                    if (s + 1 < q.steps) {
-                        x_next = raw_scale(xs, s + 1, p.scales_ue8m0);
-                        w_next = ws[s + 1];
+                    float f = 1.0f;
+                    if constexpr (FORM == kFp8) {  // while the load is on its way
+                        f = scale_value(x_next, p.scales_ue8m0) * w_next;
+                        if (s + 1 < segments) {
+                            x_next = raw_scale(xs, s + 1, p.scales_ue8m0);
+                            w_next = ws[s + 1];
+                        }
                     }
+                    const uint64_t scale = pack_f32x2(__float_as_uint(f), __float_as_uint(f));
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         tc_wait_ld(u);
@@ -522,7 +529,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                                 v[2 * i] = __uint_as_float(static_cast<uint32_t>(pair));
                                 v[2 * i + 1] = __uint_as_float(static_cast<uint32_t>(pair >> 32));
                             }
-                            store_bf16(out_row(p, out_at), col0 + c * 32, p.cols_dim, v, p.wide_stores != 0);
+                            if (FORM == kWeightGrad && p.out_fp32)
+                                store_fp32(out_row(p, out_at), col0 + c * 32, p.cols_dim, v, p.accumulate != 0, p.wide_stores != 0);
+                            else
+                                store_bf16(out_row(p, out_at), col0 + c * 32, p.cols_dim, v, p.wide_stores != 0);
                         }
                 }
             }
