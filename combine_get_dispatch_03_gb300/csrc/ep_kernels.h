@@ -19,6 +19,8 @@ struct LaunchPlan {
     int ll_combine_blocks_small_k = 0;  // the variant with every top-k slot in one batch
     int bulk_stages[3] = {0, 0, 0};      // bulk-copy dispatch: stages per CTA (0 = not usable)
     unsigned bulk_smem[3] = {0, 0, 0};   // its dynamic shared memory
+    int swiglu_blocks[3] = {0, 0, 0};    // gated activation: bf16, FP8 cast, gradient
+    int reduce_blocks = 0;               // expert rows back into receive rows
     int gemm_pairs = 0;                  // grouped products: pairs of CTAs resident on the GPU at once
     int bulk_resident[3] = {1, 1, 1};    // its CTAs resident on the GPU at once
 };

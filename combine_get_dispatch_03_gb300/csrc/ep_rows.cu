@@ -370,8 +370,12 @@ ep_status check_rows(int64_t num_rows) {
 
 }  // namespace
 
-cudaError_t plan_rows() {
-    cudaError_t err = cudaFuncSetAttribute(layout_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+cudaError_t plan_rows(LaunchPlan* plan) {
+    int per_sm = 0;
+    cudaError_t err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, rows_reduce_kernel, kRowThreads, 0);
+    plan->reduce_blocks = plan->num_sms * (per_sm > 0 ? per_sm : 1);
+    if (err == cudaSuccess)
+        err = cudaFuncSetAttribute(layout_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            (1 + kRowWarps) * kMaxExperts * static_cast<int>(sizeof(int32_t)));
     if (err == cudaSuccess)
         err = cudaFuncSetAttribute(rows_gather_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGatherSmem);
@@ -486,7 +490,7 @@ ep_status ep_expert_reduce(ep_handle* h, const void* y, int64_t y_row_bytes, con
     p.topk = c.num_topk;
     p.status = h->status;
     const int64_t wanted = (static_cast<int64_t>(p.cap) * p.ranks + kRowWarps - 1) / kRowWarps;
-    const int64_t most = static_cast<int64_t>(h->plan.num_sms) * (2048 / kRowThreads);
+    const int64_t most = h->plan.reduce_blocks;  // resident at once: warps stride over the rows
     DeviceGuard guard(h->device);
     const cudaError_t err = launch_kernel(rows_reduce_kernel, dim3(static_cast<unsigned>(wanted < most ? wanted : most)),
                                           dim3(kRowThreads), 0, stream, 1, p);

@@ -6,8 +6,8 @@
 //   gradient   dgate = dv * p * up * sig * (1 + gate * (1 - sig));  dup = dv * p * gate * sig;
 //              dp = sum over the row of dv * gate * sig * up
 // All in fp32, rounded once.  exp and the reciprocal are the hardware's approximations (2 ulp each for the
-// |gate| that leaves a value bf16 can tell from 0): with the correctly rounded ones the forward pass was bound by
-// its instructions and not by memory.
+// |gate| that leaves a value bf16 can tell from 0), five instructions a value: the kernels are near the bound of
+// their instructions, not only of memory.
 //
 // A warp owns a row: 32 lanes of 8 columns, so that a scale's 128 columns are 16 lanes and their maximum four
 // shuffles.  Only rows of a group are touched; warps stride over them through the group table.
@@ -40,11 +40,13 @@ struct SwigluParams {
 
 enum SwigluForm { kToBf16 = 0, kToFp8 = 1, kGradient = 2 };
 
-// rcp.approx keeps the subnormal results that __fdividef turns into 0: gates down to -88.7 leave a sigmoid.
+// 1 / (1 + exp(-g)).  The reciprocal is taken of a quarter of the sum, which the flushing instruction leaves a normal
+// result of up to exp(-g) = 2^128: gates down to -88.7 keep a (subnormal) sigmoid, below that it is 0.
 __device__ __forceinline__ float sigmoid(float g) {
-    float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-g)));
-    return r;
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(e, 0.25f, 0.25f)));
+    return r * 0.25f;
 }
 
 template <int FORM>
@@ -149,14 +151,24 @@ __global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluParams p) 
     }
 }
 
+size_t table_bytes(int groups) { return 2 * sizeof(int32_t) * static_cast<size_t>(groups); }
+
+template <int FORM>
+cudaError_t plan_form(LaunchPlan* plan, int groups) {
+    int per_sm = 0;
+    const cudaError_t err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, swiglu_kernel<FORM>, kThreads, table_bytes(groups));
+    plan->swiglu_blocks[FORM] = plan->num_sms * (per_sm > 0 ? per_sm : 1);
+    return err;
+}
+
 template <int FORM>
 ep_status launch(const ep_handle* h, const SwigluParams& p, cudaStream_t stream) {
     DeviceGuard guard(h->device);
-    // no more warps than rows, and no more CTAs than fill the SMs' threads once
+    // no more warps than rows, and no more CTAs than are resident at once: warps stride over the rows
     const int64_t wanted = (p.groups.num_rows + kThreads / kWarpSize - 1) / (kThreads / kWarpSize);
-    const int64_t most = static_cast<int64_t>(h->plan.num_sms) * (2048 / kThreads);
+    const int64_t most = h->plan.swiglu_blocks[FORM];
     const cudaError_t err = launch_kernel(swiglu_kernel<FORM>, dim3(static_cast<unsigned>(wanted < most ? wanted : most)),
-                                          dim3(kThreads), 2 * sizeof(int32_t) * p.groups.groups, stream, 1, p);
+                                          dim3(kThreads), table_bytes(p.groups.groups), stream, 1, p);
     if (err != cudaSuccess) return cuda_fail(err, "swiglu launch");
     return EP_OK;
 }
@@ -184,6 +196,14 @@ ep_status check(const ep_handle* h, int64_t num_rows, int32_t width, const int32
 }
 
 }  // namespace
+
+cudaError_t plan_swiglu(LaunchPlan* plan, int groups) {
+    cudaError_t err = plan_form<kToBf16>(plan, groups);
+    if (err == cudaSuccess) err = plan_form<kToFp8>(plan, groups);
+    if (err == cudaSuccess) err = plan_form<kGradient>(plan, groups);
+    return err;
+}
+
 }  // namespace ep
 
 using namespace ep;
