@@ -79,7 +79,7 @@ struct Control {
     uint64_t drained;
     uint32_t tmem;
     int32_t abort_flag;
-    int32_t warp_sums[kGemmThreads / kWarpSize];
+    int64_t warp_sums[kGemmThreads / kWarpSize];
     int32_t tiles, col_tiles, tile_cols;  // output tiles in all, tiles across, columns of one
 };
 static_assert(sizeof(Control) <= kControlBytes, "control block");
@@ -122,17 +122,21 @@ __device__ __forceinline__ void build_table(const Table& t, const GemmParams& p,
     const int per = (groups + kGemmThreads - 1) / kGemmThreads;
     const int first = threadIdx.x * per;
     const int last = min(first + per, groups);
-    int sum = 0, total = 0;
+    int64_t sum = 0, row_tiles = 0;
     for (int g = first; g < last; ++g) {
         const Group q = load_group(p.groups, g, p.status);
         t.count[g] = q.count;
         t.begin[g] = q.begin;
-        t.before[g] = sum;
-        sum += ((FORM == kWeightGrad ? p.rows_dim : q.count) + kRows - 1) / kRows;
+        t.before[g] = static_cast<int32_t>(sum);
+        sum += (static_cast<int64_t>(FORM == kWeightGrad ? p.rows_dim : q.count) + kRows - 1) / kRows;
     }
-    const int base = block_prefix<kGemmThreads>(sum, ctl.warp_sums, &total);
-    for (int g = first; g < last; ++g) t.before[g] += base;
+    const int64_t base = block_prefix<kGemmThreads>(sum, ctl.warp_sums, &row_tiles);
+    for (int g = first; g < last; ++g) t.before[g] += static_cast<int32_t>(base);
     if (threadIdx.x == 0) {
+        // more row tiles than rows that do not overlap can fill: nothing is computed
+        const bool overlap = FORM != kWeightGrad && row_tiles > p.groups.num_rows / kRows + groups;
+        if (overlap) report(p.status, EP_ERR_CAPACITY);
+        const int total = overlap ? 0 : static_cast<int>(row_tiles);
         t.before[groups] = total;
         // Tile width: the one whose waves over the CTAs take the least time, a wave costing its columns plus
         // what a tile costs at any width (its rows' loads, its turn).

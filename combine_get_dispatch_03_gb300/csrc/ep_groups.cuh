@@ -31,18 +31,19 @@ __device__ __forceinline__ Group load_group(const Groups& s, int g, int32_t* sta
 }
 
 // Exclusive prefix sum of one value per thread over a block of THREADS threads; `sums` has THREADS / 32
-// words of shared memory.  Returns this thread's prefix; *total gets the block's sum.
+// words of shared memory.  Returns this thread's prefix; *total gets the block's sum.  In 64 bits: groups that
+// overlap can hold more rows together than there are, and the sum is what shows it.
 template <int THREADS>
-__device__ __forceinline__ int block_prefix(int v, int32_t* sums, int* total) {
-    int scan = v;
+__device__ __forceinline__ int64_t block_prefix(int64_t v, int64_t* sums, int64_t* total) {
+    int64_t scan = v;
 #pragma unroll
     for (int o = 1; o < kWarpSize; o <<= 1) {
-        const int u = __shfl_up_sync(kFullMask, scan, o);
+        const int64_t u = __shfl_up_sync(kFullMask, scan, o);
         if (lane_id() >= o) scan += u;
     }
     if (lane_id() == kWarpSize - 1) sums[threadIdx.x / kWarpSize] = scan;
     __syncthreads();
-    int base = scan - v, all = 0;
+    int64_t base = scan - v, all = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / kWarpSize; ++w) {
         if (w < static_cast<int>(threadIdx.x / kWarpSize)) base += sums[w];

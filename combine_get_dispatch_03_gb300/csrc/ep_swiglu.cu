@@ -128,23 +128,28 @@ __device__ __forceinline__ void swiglu_row(const SwigluParams& p, int64_t row) {
 template <int FORM>
 __global__ void __launch_bounds__(kThreads) swiglu_kernel(const SwigluParams p) {
     extern __shared__ int32_t table[];
-    __shared__ int32_t sums[kThreads / kWarpSize];
+    __shared__ int64_t sums[kThreads / kWarpSize];
     const int groups = p.groups.groups;
     int32_t* before = table;              // [groups] rows before each group
     int32_t* begin = table + groups;      // [groups]
     pdl_enter();
     const int per = (groups + kThreads - 1) / kThreads;
     const int first = threadIdx.x * per, last = min(first + per, groups);
-    int sum = 0, total = 0;
+    int64_t sum = 0, rows = 0;
     for (int g = first; g < last; ++g) {
         const Group q = load_group(p.groups, g, p.status);
-        before[g] = sum;
+        before[g] = static_cast<int32_t>(sum);
         begin[g] = q.begin;
         sum += q.count;
     }
-    const int base = block_prefix<kThreads>(sum, sums, &total);
-    for (int g = first; g < last; ++g) before[g] += base;
+    const int64_t base = block_prefix<kThreads>(sum, sums, &rows);
+    if (rows > p.groups.num_rows) {  // overlapping groups
+        report(p.status, EP_ERR_CAPACITY);
+        return;
+    }
+    for (int g = first; g < last; ++g) before[g] += static_cast<int32_t>(base);
     __syncthreads();
+    const int total = static_cast<int>(rows);
     const int warps = gridDim.x * (kThreads / kWarpSize);
     for (int i = blockIdx.x * (kThreads / kWarpSize) + threadIdx.x / kWarpSize; i < total; i += warps) {
         const int g = find_group(before, groups, i);

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import math
 import os
 
 import torch
@@ -560,7 +561,7 @@ def _rows(t, name, dtype, device, rows=None, width=None):
     if len(shape) < 2:
         raise ValueError(f"{name} must be [rows][width], got {tuple(shape)}")
     inner, count = shape[-1], t.numel()
-    n = count // inner if inner else 0
+    n = count // inner if inner else math.prod(shape[:-1])
     if (rows is not None and n != rows) or (width is not None and inner != width):
         raise ValueError(f"{name}: {n} rows of {inner}, expected {n if rows is None else rows} of "
                          f"{inner if width is None else width}")
@@ -586,10 +587,18 @@ def _rows(t, name, dtype, device, rows=None, width=None):
     return (t.data_ptr() if count else _dummy(device).data_ptr()), n, inner, row_bytes
 
 
+def _out(shape, dtype, h, stream):
+    """An output that the call allocates: on the call's stream, so that its memory is not handed out while it is in use."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=h.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=h.device)
+
+
 def _group_arrays(h, group_count, group_begin):
     E = (h.cfg.num_experts,)
     if group_count is not None and group_count.dim() == 2:  # packed_recv_count [R][EL]
-        group_count = group_count.reshape(-1)
+        group_count = group_count.view(-1)
     return (_ptr(group_count, "group_count", torch.int32, E, h.device),
             _ptr(group_begin, "group_begin", torch.int32, E, h.device))
 
@@ -606,7 +615,7 @@ def ep_grouped_gemm(h: Handle, x: torch.Tensor, w: torch.Tensor, group_count, gr
     n, k = (w.shape[2], w.shape[1]) if w_transposed else (w.shape[1], w.shape[2])
     xp, rows, _, xs = _rows(x, "x", torch.bfloat16, d, None, k)
     if out is None:
-        out = _empty(x.shape[:-1] + (n,), torch.bfloat16, d)
+        out = _out(x.shape[:-1] + (n,), torch.bfloat16, h, stream)
     op, _, _, os_ = _rows(out, "out", torch.bfloat16, d, rows, n)
     cnt, beg = _group_arrays(h, group_count, group_begin)
     _raise(lib().ep_grouped_gemm(h.ptr, rows, n, k, cnt, beg, xp, xs,
@@ -624,7 +633,7 @@ def ep_grouped_gemm_wgrad(h: Handle, dy: torch.Tensor, x: torch.Tensor, group_co
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = _empty((h.cfg.num_experts, n, k), out_dtype, d)
+        out = _out((h.cfg.num_experts, n, k), out_dtype, h, stream)
     if out.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("the weight gradient is float32 or bfloat16")
     cnt, beg = _group_arrays(h, group_count, group_begin)
@@ -656,7 +665,7 @@ def ep_grouped_gemm_fp8(h: Handle, x: torch.Tensor, x_scales: torch.Tensor, w: t
         x_scales = x_scales[..., :G]
     sp, _, _, ss = _rows(x_scales, "x_scales", x_scales.dtype, d, rows, G)
     if out is None:
-        out = _empty(x.shape[:-1] + (n,), torch.bfloat16, d)
+        out = _out(x.shape[:-1] + (n,), torch.bfloat16, h, stream)
     op, _, _, os_ = _rows(out, "out", torch.bfloat16, d, rows, n)
     cnt, beg = _group_arrays(h, group_count, group_begin)
     _raise(lib().ep_grouped_gemm_fp8(h.ptr, rows, n, k, cnt, beg, xp, xs, sp, ss, int(ue8m0),
@@ -676,9 +685,9 @@ def ep_swiglu(h: Handle, x: torch.Tensor, group_count, group_begin=None, row_wei
         raise ValueError(f"x must hold gate and up of one width, got rows of {wide}")
     dtype = torch.float8_e4m3fn if cast_to_fp8 else torch.bfloat16
     if out is None:
-        out = _empty(x.shape[:-1] + (width,), dtype, d)
+        out = _out(x.shape[:-1] + (width,), dtype, h, stream)
     if cast_to_fp8 and out_scales is None:
-        out_scales = _empty(x.shape[:-1] + (width // 128,), torch.float32, d)
+        out_scales = _out(x.shape[:-1] + (width // 128,), torch.float32, h, stream)
     op, _, _, os_ = _rows(out, "out", dtype, d, rows, width)
     cnt, beg = _group_arrays(h, group_count, group_begin)
     _raise(lib().ep_swiglu(h.ptr, rows, width, cnt, beg, xp, xs, _ptr(row_weights, "row_weights", torch.float32, (rows,), d),
@@ -698,9 +707,9 @@ def ep_swiglu_grad(h: Handle, dy: torch.Tensor, x: torch.Tensor, group_count, gr
         raise ValueError(f"x must hold gate and up of one width, got rows of {wide}")
     yp, _, _, ys = _rows(dy, "dy", torch.bfloat16, d, rows, width)
     if dx is None:
-        dx = _empty(x.shape, torch.bfloat16, d)
+        dx = _out(x.shape, torch.bfloat16, h, stream)
     if row_weights is not None and d_row_weights is None:
-        d_row_weights = _empty((rows,), torch.float32, d)
+        d_row_weights = _out((rows,), torch.float32, h, stream)
     gp, _, _, gs = _rows(dx, "dx", torch.bfloat16, d, rows, wide)
     cnt, beg = _group_arrays(h, group_count, group_begin)
     _raise(lib().ep_swiglu_grad(h.ptr, rows, width, cnt, beg, yp, ys, xp, xs,
@@ -717,11 +726,11 @@ def ep_expert_layout(h: Handle, recv_topk_idx: torch.Tensor, num_rows: int, num_
     c, d = h.cfg, h.device
     R, K, cap, E = c.num_ranks, c.num_topk, c.recv_capacity, c.num_experts
     if group_count is None:
-        group_count = _empty((E,), torch.int32, d)
+        group_count = _out((E,), torch.int32, h, stream)
     if group_begin is None:
-        group_begin = _empty((E,), torch.int32, d)
+        group_begin = _out((E,), torch.int32, h, stream)
     if slot_row is None:
-        slot_row = _empty((R, cap, K), torch.int32, d)
+        slot_row = _out((R, cap, K), torch.int32, h, stream)
     _raise(lib().ep_expert_layout(
         h.ptr, _ptr(recv_topk_idx, "recv_topk_idx", torch.int64, (R, cap, K), d),
         _ptr(num_recv, "num_recv", torch.int32, (R,), d), num_rows,
@@ -738,11 +747,11 @@ def ep_expert_gather(h: Handle, x: torch.Tensor, slot_row: torch.Tensor, num_row
     fp8 = x.dtype == torch.float8_e4m3fn
     dtype = torch.float8_e4m3fn if fp8 else torch.bfloat16
     if out is None:
-        out = _empty((num_rows, H), dtype, d)
+        out = _out((num_rows, H), dtype, h, stream)
     if fp8 and out_scales is None:
-        out_scales = _empty((num_rows, H // 128), torch.float32, d)
+        out_scales = _out((num_rows, H // 128), torch.float32, h, stream)
     if topk_weights is not None and row_weights is None:
-        row_weights = _empty((num_rows,), torch.float32, d)
+        row_weights = _out((num_rows,), torch.float32, h, stream)
     _raise(lib().ep_expert_gather(
         h.ptr, _ptr(x, "x", dtype, (R, cap, H), d), EP_FP8_E4M3 if fp8 else EP_BF16,
         _ptr(x_scales, "x_scales", torch.float32, (R, cap, H // 128), d),
@@ -761,9 +770,9 @@ def ep_expert_reduce(h: Handle, y: torch.Tensor, slot_row: torch.Tensor, num_rec
     R, K, cap, H = c.num_ranks, c.num_topk, c.recv_capacity, c.hidden
     yp, rows, _, ys = _rows(y, "y", torch.bfloat16, d, None, H)
     if out is None:
-        out = _empty((R, cap, H), torch.bfloat16, d)
+        out = _out((R, cap, H), torch.bfloat16, h, stream)
     if row_weights is not None and out_topk_weights is None:
-        out_topk_weights = _empty((R, cap, K), torch.float32, d)
+        out_topk_weights = _out((R, cap, K), torch.float32, h, stream)
     _raise(lib().ep_expert_reduce(
         h.ptr, yp, ys, _ptr(slot_row, "slot_row", torch.int32, (R, cap, K), d),
         _ptr(row_weights, "row_weights", torch.float32, (rows,), d), _ptr(num_recv, "num_recv", torch.int32, (R,), d),

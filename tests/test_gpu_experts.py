@@ -579,3 +579,159 @@ def test_expert_gather_and_reduce(R, EL, K, cap, alignment, mask, H, fp8):
     assert (back.t.view(torch.uint8)[~wrote] == back.fill).all()
     assert torch.equal(back_w.t[wrote], torch.where(slot_d >= 0, rw[slot_d.long().clamp_min(0)], 0.0)[wrote])
     assert (back_w.t.view(torch.uint8).view(R, cap, -1)[~wrote] == back.fill).all()
+
+
+# --------------------------------------------------------------------------------------------- the layer they make up
+
+def layer_reference(x, idx, w, w_up, w_down, dy):
+    """Output and gradients of the layer in 64 bits, by differentiating the plain formula."""
+    leaves = [v.detach().double().requires_grad_() for v in (x, w, w_up, w_down)]
+    xd, wd, ud, dd = leaves
+    R, T, H = x.shape
+    flat, out = xd.view(R * T, H), torch.zeros((R * T, H), dtype=torch.float64, device=DEV)
+    for e in range(w_up.shape[0]):
+        tok, slot = torch.nonzero(idx.view(R * T, -1) == e, as_tuple=True)
+        a = flat[tok] @ ud[e].t()
+        gate, up = a.chunk(2, 1)
+        v = gate / (1 + torch.exp(-gate)) * up * wd.view(R * T, -1)[tok, slot][:, None]
+        out = out.index_add(0, tok, v @ dd[e].t())
+    out = out.view(R, T, H)
+    grads = torch.autograd.grad((out * dy.double()).sum(), leaves)
+    return out.detach(), grads
+
+
+def norm_error(got, want):
+    return float((got.double() - want).norm() / want.norm())
+
+
+def test_moe_layer_trains_and_serves():
+    """examples/moe_layer.py against 64 bits.  Each result passes at most eight roundings to bf16 (2^-8 of a value each,
+    and a rounded gate or up value moves the activation by at most about twice that): 16 * 2^-8 in norm.  FP8 decode:
+    three casts to e4m3 (2^-4 each at worst), 3 * 2^-4."""
+    from examples import moe_layer as M
+    R, T, H, E, K, I = 4, 37, 512, 12, 3, 256
+    g = gen(41)
+    x, dy = randn(g, (R, T, H)), randn(g, (R, T, H))
+    w, idx = torch.softmax(torch.randn((R, T, E), generator=g, device=DEV), -1).topk(K)
+    w, idx = w.contiguous(), idx.contiguous()
+    idx[1, 5, 2] = -1  # a masked slot
+    w_up, w_down = randn(g, (E, 2 * I, H), H ** -0.5), randn(g, (E, H, I), I ** -0.5)
+    h = handle(E, R, H, T, K, R * T, 16)
+    y, saved = M.forward(h, x, idx, w, w_up, w_down)
+    got = M.backward(h, dy, saved, w_up, w_down)
+    h.check()
+    want_y, want = layer_reference(x, idx, w, w_up, w_down, dy)
+    assert norm_error(y, want_y) < 16 * 2.0 ** -8
+    for name, a, b in zip(("x", "topk_weights", "w_up", "w_down"), got, want):
+        assert norm_error(a, b) < 16 * 2.0 ** -8, name
+    yd = M.decode(h, x, idx, w, M.quantize(w_up), M.quantize(w_down))
+    h.check()
+    assert norm_error(yd, want_y) < 3 * 2.0 ** -4
+
+
+def test_graph_replays_follow_new_inputs():
+    """Products, activation and expert order captured once; replays read the counts, rows and weights that are there then."""
+    E, rows, k, width = 4, 300, 256, 128
+    g = gen(6)
+    h = handle(E)
+    x, w1, w2 = randn(g, (rows, k)), randn(g, (E, 2 * width, k), 0.1), randn(g, (E, k, width), 0.1)
+    c, b = i32([10, 0, 200, 5]), i32([0, 10, 10, 210])
+
+    def step():
+        a = ep.ep_grouped_gemm(h, x, w1, c, b)
+        v = ep.ep_swiglu(h, a, c, b)["out"]
+        y = ep.ep_grouped_gemm(h, v, w2, c, b)
+        return y, ep.ep_grouped_gemm_wgrad(h, y, v, c, b)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, dw = step()
+    for counts in ([10, 0, 200, 5], [0, 90, 1, 64], [0, 0, 0, 0], [300, 0, 0, 0]):
+        c.copy_(i32(counts))
+        b.copy_(i32(packed(counts)[0]))
+        x.copy_(randn(g, (rows, k)))
+        graph.replay()
+        want_y, want_dw = step()
+        h.check()
+        n = sum(counts)
+        assert torch.equal(y[:n], want_y[:n]) and torch.equal(dw, want_dw)
+
+
+def test_overlapping_groups_are_reported():
+    h = handle(64)
+    x = torch.zeros((256, 64), dtype=torch.bfloat16, device=DEV)
+    w = torch.zeros((64, 64, 64), dtype=torch.bfloat16, device=DEV)
+    c, b = i32([256] * 64), i32([0] * 64)
+    out = torch.full((256, 64), 3.0, dtype=torch.bfloat16, device=DEV)
+    ep.ep_grouped_gemm(h, x, w, c, b, out=out)
+    assert h.status() == 2 and (out == 3).all()
+    act = torch.full((256, 32), 3.0, dtype=torch.bfloat16, device=DEV)
+    ep.ep_swiglu(h, x, c, b, out=act)
+    assert h.status() == 2 and (act == 3).all()
+
+
+# --------------------------------------------------------------------------------------------- refusals
+
+def refused(code, words, f, *a, **kw):
+    with pytest.raises(ep.EPError) as e:
+        f(*a, **kw)
+    assert e.value.status == code and words in str(e.value), str(e.value)
+
+
+def test_refusals():
+    h = handle(4, 2, 512, 8, 2, 16)
+    low = handle(4, 2, 512, 8, 2, 0)
+    c, b = i32([1, 0, 0, 0]), i32([0, 0, 0, 0])
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device=DEV)  # noqa: E731
+    f8 = lambda *s: torch.zeros(s, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)  # noqa: E731
+    f32 = lambda *s: torch.zeros(s, device=DEV)  # noqa: E731
+    g = ep.ep_grouped_gemm
+    refused(1, "multiples of 8", g, h, bf(8, 60), bf(4, 64, 60), c, b)
+    refused(1, "multiples of 8", g, h, bf(8, 64), bf(4, 12, 64), c, b)
+    refused(1, "multiple of num_experts", g, h, bf(9, 64), bf(4, 64, 64), c)
+    refused(1, "group_count", g, h, bf(8, 64), bf(4, 64, 64), None, b)
+    refused(1, "16-byte aligned", g, h, bf(8 * 64 + 4)[4:].view(8, 64), bf(4, 64, 64), c, b)
+    refused(1, "multiples of 16", g, h, bf(8, 68)[:, :64], bf(4, 64, 64), c, b)
+    refused(1, "expected_rows", g, h, bf(8, 64), bf(4, 64, 64), c, b, expected_rows=-1)
+    for bad in (bf(8, 72), f32(8, 64), torch.zeros((8, 64), dtype=torch.bfloat16)):
+        with pytest.raises((TypeError, ValueError)):
+            g(h, bad, bf(4, 64, 64), c, b)
+    with pytest.raises(ValueError):
+        g(h, bf(8, 64), bf(3, 64, 64), c, b)      # weights of three experts
+    with pytest.raises(ValueError):
+        g(h, bf(2, 4, 3, 64)[:, :, :2], bf(4, 64, 64), c, b)  # rows not evenly spaced
+    with pytest.raises(ValueError):
+        g(h, bf(64, 8).t(), bf(4, 64, 64), c, b)  # rows not contiguous inside
+    with pytest.raises(TypeError):
+        g(h, bf(8, 64), bf(4, 64, 64), c.long(), b)
+    wg = ep.ep_grouped_gemm_wgrad
+    refused(1, "accumulate needs", wg, h, bf(8, 64), bf(8, 64), c, b, out=bf(4, 64, 64), accumulate=True)
+    with pytest.raises(ValueError):
+        wg(h, bf(8, 64), bf(8, 64), c, b, accumulate=True)
+    with pytest.raises(TypeError):
+        wg(h, bf(8, 64), bf(8, 64), c, b, out=torch.zeros((4, 64, 64), dtype=torch.float16, device=DEV))
+    q = ep.ep_grouped_gemm_fp8
+    refused(5, "k % 128", q, h, f8(8, 64), f32(8, 0), f8(4, 64, 64), f32(4, 1, 0), c, b)
+    with pytest.raises(ValueError):
+        q(h, f8(8, 256), f32(8, 1), f8(4, 64, 256), f32(4, 1, 2), c, b)
+    with pytest.raises(TypeError):
+        q(h, f8(8, 256), bf(8, 2), f8(4, 64, 256), f32(4, 1, 2), c, b)
+    s = ep.ep_swiglu
+    refused(1, "multiple of 8", s, h, bf(8, 24), c, b)
+    refused(5, "width % 128", s, h, bf(8, 128), c, b, cast_to_fp8=True, out=f8(8, 64), out_scales=f32(8, 0))
+    refused(1, "go with cast_to_fp8", s, h, bf(8, 256), c, b, round_scale=True)
+    with pytest.raises(ValueError):
+        s(h, bf(8, 256), c, b, row_weights=f32(7))
+    idx, n = torch.zeros((2, 16, 2), dtype=torch.int64, device=DEV), i32([1, 1])
+    refused(8, "no normal dispatch", ep.ep_expert_layout, h, idx, 64)
+    refused(1, "normal mode disabled", ep.ep_expert_layout, low, idx[:, :0].contiguous(), 64, num_recv=n)
+    slot = torch.full((2, 16, 2), -1, dtype=torch.int32, device=DEV)
+    refused(1, "go together", ep.ep_expert_gather, h, bf(2, 16, 512), slot, 64, num_recv=n, row_weights=f32(64))
+    refused(1, "FP8 payload", ep.ep_expert_gather, h, f8(2, 16, 512), slot, 64, num_recv=n)
+    refused(1, "go together", ep.ep_expert_reduce, h, bf(64, 512), slot, num_recv=n, row_weights=None,
+            out_topk_weights=f32(2, 16, 2))
+    with pytest.raises(ValueError):
+        ep.ep_expert_reduce(h, bf(64, 256), slot, num_recv=n)
+    h.check()
