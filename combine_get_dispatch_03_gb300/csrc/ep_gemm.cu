@@ -370,12 +370,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 const Tile q = decode<FORM, CG>(t, p, ctl, tile);
                 for (int s = 0; s < q.steps && ok; ++s) {
                     const int in_segment = kSegment ? s % kSegment : s;
+                    // operands first: they are there, and with short segments the accumulator is what is waited for
+                    ok = wait_phase(&ctl.full[stage], phase, &ctl.abort_flag, p.status);
+                    if (!ok) break;
                     if (in_segment == 0) {
                         ok = wait_phase(&ctl.acc_empty[buf], acc_phase ^ 1, &ctl.abort_flag, p.status);
                         if (!ok) break;
                     }
-                    ok = wait_phase(&ctl.full[stage], phase, &ctl.abort_flag, p.status);
-                    if (!ok) break;
                     if (FORM == kWeightGrad && q.rows - s * 64 < 64) fence_written<CG>();
                     tc_fence_after();
                     const uint32_t a = smem_u32(stages) + stage * stage_bytes;
