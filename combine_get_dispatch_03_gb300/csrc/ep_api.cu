@@ -172,11 +172,11 @@ ep_status ep_handle_create(const ep_config* cfg, ep_handle** out) {
     const size_t scan_words = ep::layout_scan_scratch_words(cfg->num_ranks, cfg->num_experts, cfg->num_max_tokens);
     const size_t sizes[] = {1, R * R, R * R * C, R * R * C, R, R * cap, R * T * R, R * T * K, R * E, R,
                             R * NN * C, R * NN, 2, scan_words,
-                            cap ? static_cast<size_t>(ep::layout_chunks(*cfg)) * E : 0};
+                            cap ? static_cast<size_t>(ep::layout_chunks(*cfg)) * E : 0, R};
     int32_t** slots[] = {&h->status,   &h->rank_prefix,  &h->channel_prefix, &h->recv_channel_prefix,
                          &h->num_recv, &h->recv_src_idx, &h->send_head,      &h->ll_slot,
                          &h->ll_cnt,   &h->rank_mask,    &h->rdma_channel_prefix, &h->recv_rdma_rank_prefix,
-                         &h->claims,   &h->layout_scratch, &h->expert_counts};
+                         &h->claims,   &h->layout_scratch, &h->expert_counts, &h->layout_tickets};
     size_t total = 0;
     for (size_t s : sizes) total += align_up(s * sizeof(int32_t), 256);
     err = cudaMalloc(&h->dmem, total);

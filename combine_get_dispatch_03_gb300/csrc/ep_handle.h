@@ -28,6 +28,7 @@ struct ep_handle {
     int32_t* claims = nullptr;                 // [2]: the combine's next token and finished warps
     int32_t* layout_scratch = nullptr;         // tile states of the one-pass layout + record scan
     int32_t* expert_counts = nullptr;          // [R][layout_chunks][EL]: the expert layout's counts per chunk of slots
+    int32_t* layout_tickets = nullptr;         // [R]: CTAs of a rank that the expert layout has counted
     int normal_tokens = -1;                  // T of the current dispatch record, -1 = none
     bool prepared = false;                   // record built by ep_notify_dispatch, not yet used
     int ll_tokens = -1;                      // T of the last LL dispatch, -1 = none

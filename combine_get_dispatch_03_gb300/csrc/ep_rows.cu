@@ -8,8 +8,8 @@
 //   reduce   out[r][row] = sum over k of y[slot_row[r][row][k]]    fp32, in slot order
 // The gather's gradient is the reduce and the other way round.
 //
-// The layout is a stable counting sort of cap * K slots per rank in chunks of 2048: count, scan over a
-// rank's chunks (a warp per expert), place.  The data kernels move each row once: the gather reads a
+// The layout is a stable counting sort of cap * K slots per rank in chunks of 2048: count, with the scan over a
+// rank's chunks done by its last CTA, then place.  The data kernels move each row once: the gather reads a
 // received row into shared memory with one bulk copy and writes it with one bulk copy per slot, so that it reads
 // every row once however many experts want it; the reduce holds a row's columns in registers.
 #include "ep_groups.cuh"
@@ -45,15 +45,19 @@ __device__ __forceinline__ int expert_of(const int64_t* idx, int64_t at, int EL,
     return static_cast<int>(e);
 }
 
-// counts[r][chunk][j] = slots of the chunk that chose local expert j.
+// counts[r][chunk][j] = slots of the chunk that chose local expert j; the CTA of a rank that counts last turns the
+// rank's counts into the rows before each chunk, a warp per expert, and writes group_count.  tickets [ranks] is zero
+// before and after (a launch for the scan alone took 5 us of the layout's 27).
 __global__ void __launch_bounds__(kRowThreads)
     layout_count_kernel(const int64_t* idx, const int32_t* num_recv, int cap, int K, int EL, int32_t* counts,
-                        int32_t* status) {
+                        uint32_t* tickets, int32_t* group_count, int32_t* status) {
     extern __shared__ int32_t hist[];
+    __shared__ bool last_of_rank;
     pdl_enter();
-    const int r = blockIdx.y, chunk = blockIdx.x;
+    const int r = blockIdx.y, chunk = blockIdx.x, chunks = gridDim.x;
     const int n = filled_slots(num_recv, r, cap, K);
-    if (chunk * kLayoutChunk >= n) return;
+    const int used = (n + kLayoutChunk - 1) / kLayoutChunk;
+    if (chunk >= max(used, 1)) return;  // an empty rank's first CTA still writes its counts of 0
     for (int j = threadIdx.x; j < EL; j += kRowThreads) hist[j] = 0;
     __syncthreads();
     const int64_t base = static_cast<int64_t>(r) * cap * K;
@@ -63,34 +67,35 @@ __global__ void __launch_bounds__(kRowThreads)
         if (e >= 0) atomicAdd(&hist[e], 1);
     }
     __syncthreads();
-    int32_t* out = counts + (static_cast<int64_t>(r) * gridDim.x + chunk) * EL;
-    for (int j = threadIdx.x; j < EL; j += kRowThreads) out[j] = hist[j];
-}
-
-// One warp per expert: its counts become the rows before each chunk, group_count the total.
-__global__ void __launch_bounds__(kRowThreads)
-    layout_scan_chunks_kernel(const int32_t* num_recv, int cap, int K, int EL, int experts, int chunks, int32_t* counts,
-                              int32_t* group_count) {
-    pdl_enter();
-    const int e = blockIdx.x * kRowWarps + threadIdx.x / kWarpSize;
-    if (e >= experts) return;
-    const int r = e / EL, j = e % EL;
-    const int used = (filled_slots(num_recv, r, cap, K) + kLayoutChunk - 1) / kLayoutChunk;
-    int total = 0;
-    for (int c0 = 0; c0 < used; c0 += kWarpSize) {
-        const int c = c0 + lane_id();
-        int32_t* at = counts + (static_cast<int64_t>(r) * chunks + c) * EL + j;
-        const int v = c < used ? *at : 0;
-        int scan = v;
-#pragma unroll
-        for (int o = 1; o < kWarpSize; o <<= 1) {
-            const int u = __shfl_up_sync(kFullMask, scan, o);
-            if (lane_id() >= o) scan += u;
-        }
-        if (c < used) *at = total + scan - v;
-        total += __shfl_sync(kFullMask, scan, kWarpSize - 1);
+    int32_t* const mine = counts + static_cast<int64_t>(r) * chunks * EL;
+    for (int j = threadIdx.x; j < EL; j += kRowThreads) mine[static_cast<int64_t>(chunk) * EL + j] = hist[j];
+    // publish this CTA's counts, then take a ticket; the last one sees them all
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        last_of_rank = atomicAdd(&tickets[r], 1u) == static_cast<uint32_t>(max(used, 1)) - 1u;
+        if (last_of_rank) tickets[r] = 0;
     }
-    if (lane_id() == 0) group_count[e] = total;
+    __syncthreads();
+    if (!last_of_rank) return;
+    __threadfence();
+    for (int j = threadIdx.x / kWarpSize; j < EL; j += kRowWarps) {
+        int total = 0;
+        for (int c0 = 0; c0 < used; c0 += kWarpSize) {
+            const int c = c0 + lane_id();
+            int32_t* at = mine + static_cast<int64_t>(c) * EL + j;
+            const int v = c < used ? __ldcg(at) : 0;
+            int scan = v;
+#pragma unroll
+            for (int o = 1; o < kWarpSize; o <<= 1) {
+                const int u = __shfl_up_sync(kFullMask, scan, o);
+                if (lane_id() >= o) scan += u;
+            }
+            if (c < used) *at = total + scan - v;
+            total += __shfl_sync(kFullMask, scan, kWarpSize - 1);
+        }
+        if (lane_id() == 0) group_count[r * EL + j] = total;
+    }
 }
 
 // Begins of the experts (each rounded up to the alignment), and every slot's row.
@@ -411,10 +416,8 @@ ep_status ep_expert_layout(ep_handle* h, const int64_t* recv_topk_idx, const int
     const int chunks = static_cast<int>(layout_chunks(c));
     DeviceGuard guard(h->device);
     cudaError_t err = launch_kernel(layout_count_kernel, dim3(chunks, R), dim3(kRowThreads), EL * sizeof(int32_t), stream, 1,
-                                    recv_topk_idx, recv, cap, K, EL, h->expert_counts, h->status);
-    if (err == cudaSuccess)
-        err = launch_kernel(layout_scan_chunks_kernel, dim3((E + kRowWarps - 1) / kRowWarps), dim3(kRowThreads), 0, stream, 1,
-                            recv, cap, K, EL, E, chunks, h->expert_counts, group_count);
+                                    recv_topk_idx, recv, cap, K, EL, h->expert_counts,
+                                    reinterpret_cast<uint32_t*>(h->layout_tickets), group_count, h->status);
     if (err == cudaSuccess)
         err = launch_kernel(layout_place_kernel, dim3(chunks, R), dim3(kRowThreads), (1 + kRowWarps) * EL * sizeof(int32_t),
                             stream, 1, recv_topk_idx, recv, cap, K, EL, E, c.expert_alignment, num_rows, h->expert_counts,
