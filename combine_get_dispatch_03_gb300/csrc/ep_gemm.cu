@@ -371,13 +371,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 for (int s = 0; s < q.steps && ok; ++s) {
                     const int in_segment = kSegment ? s % kSegment : s;
                     // operands first: they are there, and with short segments the accumulator is what is waited for
-                    ok = wait_phase(&ctl.full[stage], phase, &ctl.abort_flag, p.status);
+                    if (FORM == kWeightGrad && CG == 2 && q.rows - s * 64 < 64)  // zeroed rows, maybe the peer's
+                        ok = wait_phase<true>(&ctl.full[stage], phase, &ctl.abort_flag, p.status);
+                    else
+                        ok = wait_phase(&ctl.full[stage], phase, &ctl.abort_flag, p.status);
                     if (!ok) break;
                     if (in_segment == 0) {
                         ok = wait_phase(&ctl.acc_empty[buf], acc_phase ^ 1, &ctl.abort_flag, p.status);
                         if (!ok) break;
                     }
-                    if (FORM == kWeightGrad && q.rows - s * 64 < 64) fence_written<CG>();
                     tc_fence_after();
                     const uint32_t a = smem_u32(stages) + stage * stage_bytes;
                     const uint64_t da = smem_desc(a, a_mn ? 8192 : 16);

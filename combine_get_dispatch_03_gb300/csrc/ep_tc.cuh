@@ -20,12 +20,30 @@ __device__ __forceinline__ uint64_t global_ns() {
     return t;
 }
 
-__device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int32_t* abort_flag, int32_t* status) {
+// One poll.  kCluster: acquires at cluster scope, the other side of bar_arrive_written().
+template <bool kCluster>
+__device__ __forceinline__ bool poll_phase(uint64_t* bar, uint32_t parity) {
+    if constexpr (!kCluster) return mbar_try_wait(bar, parity);
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
+template <bool kCluster = false>
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int32_t* abort_flag,
+                                           int32_t* status) {
+    if (poll_phase<kCluster>(bar, parity)) return true;
     uint64_t begin = 0;  // the clock is read only after polls that came to nothing: reading it takes long
     for (;;) {
 #pragma unroll 1
         for (int i = 0; i < 64; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
+            if (poll_phase<kCluster>(bar, parity)) return true;
         if (*abort_flag) return false;
         const uint64_t now = global_ns();
         if (begin == 0) begin = now;
@@ -35,12 +53,6 @@ __device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, volati
             return false;
         }
     }
-}
-
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int32_t* abort_flag,
-                                           int32_t* status) {
-    if (mbar_try_wait(bar, parity)) return true;
-    return wait_long(bar, parity, abort_flag, status);
 }
 
 // One lane of a converged warp.  Code that it guards is known to run in a single thread: products and loads
@@ -95,12 +107,6 @@ __device__ __forceinline__ void bar_arrive_written(uint32_t bar) {
         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
     else
         asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// The other side of bar_arrive_written(), after the wait.
-template <int CG>
-__device__ __forceinline__ void fence_written() {
-    if constexpr (CG == 2) asm volatile("fence.acq_rel.cluster;\n\tfence.proxy.async;" ::: "memory");
 }
 
 template <int CG>
