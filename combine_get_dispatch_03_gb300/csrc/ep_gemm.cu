@@ -43,7 +43,7 @@ constexpr int kColBox = 64;         // the same for narrow tiles
 constexpr int kTileOverhead = 32;   // columns that a tile's width-independent cost is worth
 constexpr int kMaxStages = 12;
 constexpr int kEpilogueWarps = 8;
-constexpr int kGemmThreads = (4 + kEpilogueWarps) * kWarpSize;  // warps 2 and 3 are idle: register splits go by four warps
+constexpr int kGemmThreads = (4 + kEpilogueWarps) * kWarpSize;  // of warps 0 to 3 not all have work: registers are split by four warps
 constexpr int kControlBytes = 512;  // static shared memory
 constexpr int kMaxSmem = 232448 - kControlBytes;
 
@@ -217,6 +217,317 @@ __device__ __forceinline__ uint8_t* out_row(const GemmParams& p, int64_t row) {
     return static_cast<uint8_t*>(p.out) + row * p.out_row_bytes;
 }
 
+// What a CTA's roles share.
+struct Roles {
+    const Maps& maps;
+    const GemmParams& p;
+    const Table& t;
+    Control& ctl;
+    uint8_t* stages;
+    uint32_t tmem, rank, stage_bytes;  // rank: of the CTA in its pair
+    int cols_here;                     // columns of the weight operand that this CTA loads
+    int num_stages, worker, workers;
+};
+
+constexpr uint32_t kABytes = kTileRows * kRowBytes;
+
+// One thread: the loads.
+template <int FORM, int CG>
+__device__ __forceinline__ void load_operands(const Roles& x) {
+    const GemmParams& p = x.p;
+    const Table& t = x.t;
+    Control& ctl = x.ctl;
+    uint32_t stage = 0, phase = 0;
+    uint32_t tail_phase = 0, tail_last = 0;  // per stage: uses of tail_full, mod 2; whether its last use was one
+    bool ok = true;
+    const uint32_t full0 = CG == 1 ? smem_u32(ctl.full) : cluster_addr(ctl.full, 0);
+    uint32_t used = 0;
+    for (int tile = x.worker; ok && tile < ctl.tiles; tile += x.workers) {
+        const Tile q = decode<FORM, CG>(t, p, ctl, tile);
+        const int my_m0 = q.m0 + static_cast<int>(x.rank) * kTileRows;
+        const int rows_here = min(kTileRows, q.rows - my_m0);
+        const int small_boxes = rows_here > kTileRows / 2 ? 0 : (max(0, rows_here) + kRowBox - 1) / kRowBox;
+        const uint32_t row_bytes = rows_here > kTileRows / 2 ? kABytes : small_boxes * (kRowBox * kRowBytes);
+        const uint32_t bytes = FORM == kWeightGrad ? x.stage_bytes : x.cols_here * kRowBytes + row_bytes;
+        for (int s = 0; s < q.steps; ++s) {
+            ok = wait_phase(&ctl.empty[stage], phase ^ 1, &ctl.abort_flag, p.status);
+            if (!ok) break;
+            uint8_t* a = x.stages + stage * x.stage_bytes;
+            uint8_t* b = a + kABytes;
+            uint32_t bar = full0 + 8 * stage;
+            const int cb = static_cast<int>(x.rank) * x.cols_here;
+            if constexpr (FORM == kWeightGrad) {
+                const bool tail = (s + 1) * 64 > q.rows;
+                if (tail) {
+                    bar = smem_u32(&ctl.tail_full[stage]);
+                    mbar_arrive_expect_tx(&ctl.tail_full[stage], x.stage_bytes);
+                    tail_phase ^= 1u << stage;
+                    tail_last |= 1u << stage;
+                } else {
+                    bar_arrive_expect_tx<CG>(bar, x.stage_bytes);
+                    tail_last &= ~(1u << stage);
+                }
+                const int r = q.row0 + s * 64;
+                if (p.a_chunked) {
+                    tma_load_3d<CG>(a, &x.maps.a, 0, r, my_m0 / 64, bar);
+                } else {
+                    tma_load_2d<CG>(a, &x.maps.a_small, my_m0, r, bar);
+                    tma_load_2d<CG>(a + 8192, &x.maps.a_small, my_m0 + 64, r, bar);
+                }
+                if (p.b_chunked && x.cols_here >= kBox) {
+                    for (int c = 0; c < x.cols_here; c += kBox)
+                        tma_load_3d<CG>(b + c * kRowBytes, &x.maps.b, 0, r, (q.n0 + cb + c) / 64, bar);
+                } else {
+                    for (int c = 0; c < x.cols_here; c += kColBox)
+                        tma_load_2d<CG>(b + c * kRowBytes, &x.maps.b_small, q.n0 + cb + c, r, bar);
+                }
+            } else {
+                bar_arrive_expect_tx<CG>(bar, bytes);
+                const int k0 = s * (FORM == kFp8 ? 128 : 64);
+                if (small_boxes == 0) {
+                    if (rows_here > 0) tma_load_2d<CG>(a, &x.maps.a, k0, q.row0 + my_m0, bar);
+                } else {
+                    for (int c = 0; c < small_boxes; ++c)
+                        tma_load_2d<CG>(a + c * (kRowBox * kRowBytes), &x.maps.a_small, k0, q.row0 + my_m0 + c * kRowBox, bar);
+                }
+                if (FORM == kTransposed) {
+                    if (p.b_chunked && x.cols_here >= kBox) {
+                        for (int c = 0; c < x.cols_here; c += kBox)
+                            tma_load_4d<CG>(b + c * kRowBytes, &x.maps.b, 0, k0, (q.n0 + cb + c) / 64, q.group, bar);
+                    } else {
+                        for (int c = 0; c < x.cols_here; c += kColBox)
+                            tma_load_3d<CG>(b + c * kRowBytes, &x.maps.b_small, q.n0 + cb + c, k0, q.group, bar);
+                    }
+                } else if (x.cols_here >= kBox) {
+                    for (int c = 0; c < x.cols_here; c += kBox)
+                        tma_load_3d<CG>(b + c * kRowBytes, &x.maps.b, k0, q.n0 + cb + c, q.group, bar);
+                } else {
+                    tma_load_3d<CG>(b, &x.maps.b_small, k0, q.n0 + cb, q.group, bar);
+                }
+            }
+            ++used;
+            if (++stage == static_cast<uint32_t>(x.num_stages)) stage = 0, phase ^= 1;
+        }
+    }
+    // The copies in flight land before the memory goes away: at once where all went well, within a limit where
+    // some warp gave up.  With a pair they all arrive at the leader, but for the ends of groups, and neither CTA
+    // leaves before the other.
+    for (int i = 0; i < x.num_stages && used > 0; ++i, --used) {
+        if (stage == 0) phase ^= 1;
+        stage = (stage == 0 ? x.num_stages : stage) - 1;
+        const bool tail = (tail_last >> stage) & 1;
+        if (x.rank != 0 && !tail) continue;
+        uint64_t* bar = tail ? &ctl.tail_full[stage] : &ctl.full[stage];
+        const uint32_t parity = tail ? ((tail_phase >> stage) & 1) ^ 1 : phase;
+        for (int k = 0; k < (1 << 12) && !mbar_try_wait(bar, parity); ++k) {
+        }
+    }
+}
+
+// One thread of the pair: the products.
+template <int FORM, int CG>
+__device__ __forceinline__ void multiply(const Roles& x) {
+    constexpr int kSegment = segment_steps(FORM);
+    const GemmParams& p = x.p;
+    const Table& t = x.t;
+    Control& ctl = x.ctl;
+    uint32_t stage = 0, phase = 0, acc_phase = 0;
+    int buf = 0;
+    bool ok = true;
+    constexpr bool a_mn = FORM == kWeightGrad;
+    constexpr bool b_mn = FORM == kWeightGrad || FORM == kTransposed;
+    const uint32_t idesc = mma_desc(FORM == kFp8 ? 0 : 1, a_mn, b_mn, kTileRows * CG, ctl.tile_cols);
+    for (int tile = x.worker; ok && tile < ctl.tiles; tile += x.workers) {
+        const Tile q = decode<FORM, CG>(t, p, ctl, tile);
+        for (int s = 0; s < q.steps && ok; ++s) {
+            const int in_segment = kSegment ? s % kSegment : s;
+            // operands first: they are there, and with short segments the accumulator is what is waited for
+            if (FORM == kWeightGrad && CG == 2 && q.rows - s * 64 < 64)  // zeroed rows, maybe the peer's
+                ok = wait_phase<true>(&ctl.full[stage], phase, &ctl.abort_flag, p.status);
+            else
+                ok = wait_phase(&ctl.full[stage], phase, &ctl.abort_flag, p.status);
+            if (!ok) break;
+            if (in_segment == 0) {
+                ok = wait_phase(&ctl.acc_empty[buf], acc_phase ^ 1, &ctl.abort_flag, p.status);
+                if (!ok) break;
+            }
+            tc_fence_after();
+            const uint32_t a = smem_u32(x.stages) + stage * x.stage_bytes;
+            const uint64_t da = smem_desc(a, a_mn ? 8192 : 16);
+            const uint64_t db = smem_desc(a + kABytes, b_mn ? 8192 : 16);
+            const uint32_t d = x.tmem + buf * kMaxTileCols;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                tc_mma<CG, FORM == kFp8>(d, da + i * (a_mn ? 128 : 2), db + i * (b_mn ? 128 : 2), idesc,
+                                         in_segment | i);
+            tc_commit<CG>(&ctl.empty[stage]);
+            if (s == q.steps - 1 || (kSegment && in_segment == kSegment - 1)) {
+                tc_commit<CG>(&ctl.acc_full[buf]);
+                buf ^= 1;
+                acc_phase ^= buf == 0;
+            }
+            if (++stage == static_cast<uint32_t>(x.num_stages)) stage = 0, phase ^= 1;
+        }
+    }
+    if (!ok) {
+        // Given up: the products already issued still write tensor memory.
+        tc_commit<CG>(&ctl.drained);
+        for (int k = 0; k < (1 << 12) && !mbar_try_wait(&ctl.drained, 0); ++k) {
+        }
+    }
+}
+
+// One warp, weight gradient: the ends of groups.
+template <int FORM, int CG>
+__device__ __forceinline__ void zero_tails(const Roles& x) {
+    const GemmParams& p = x.p;
+    const Table& t = x.t;
+    Control& ctl = x.ctl;
+    // The rows of a group's last, partial block past its end belong to others: zero them in both operands.
+    uint32_t stage = 0, tail_phase = 0;  // tail_phase, per stage: uses of tail_full, mod 2
+    bool ok = true;
+    for (int tile = x.worker; ok && tile < ctl.tiles; tile += x.workers) {
+        const Tile q = decode<FORM, CG>(t, p, ctl, tile);
+        const int whole = q.rows / 64, valid = q.rows % 64;
+        stage = (stage + whole) % x.num_stages;
+        if (valid == 0) continue;
+        ok = warp_wait(&ctl.tail_full[stage], (tail_phase >> stage) & 1, &ctl.abort_flag, p.status);
+        tail_phase ^= 1u << stage;
+        uint8_t* a = x.stages + stage * x.stage_bytes;
+        const int chunks = (kTileRows + x.cols_here) / 64;
+        const int pieces = (64 - valid) * 8;
+        for (int c = 0; c < chunks; ++c) {
+            uint4* z = reinterpret_cast<uint4*>(a + c * 8192 + valid * 128);
+            for (int i = lane_id(); i < pieces; i += kWarpSize) z[i] = make_uint4(0, 0, 0, 0);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane_id() == 0)
+            bar_arrive_written<CG>(CG == 1 ? smem_u32(&ctl.full[stage]) : cluster_addr(&ctl.full[stage], 0));
+        stage = (stage + 1) % x.num_stages;
+    }
+}
+
+// Eight warps: accumulators to the output.
+template <int FORM, int CG>
+__device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
+    constexpr int kSegment = segment_steps(FORM);
+    const GemmParams& p = x.p;
+    const Table& t = x.t;
+    Control& ctl = x.ctl;
+    const int w = warp - 4;
+    const int quarter = warp & 3;               // the 32 lanes of tensor memory that this warp may read
+    const int half = w >> 2;                    // which half of the tile's columns
+    const uint32_t lane_base = x.tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const int cols_half = ctl.tile_cols / 2;
+    const uint32_t acc_empty0 = CG == 1 ? smem_u32(ctl.acc_empty) : cluster_addr(ctl.acc_empty, 0);
+    int buf = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    for (int tile = x.worker; ok && tile < ctl.tiles; tile += x.workers) {
+        const Tile q = decode<FORM, CG>(t, p, ctl, tile);
+        const int row = q.m0 + static_cast<int>(x.rank) * kTileRows + quarter * 32 + lane_id();  // in the group
+        const int col0 = q.n0 + half * cols_half;
+        const bool row_ok = row < (FORM == kWeightGrad ? p.rows_dim : q.rows);
+        const int64_t out_at = (FORM == kWeightGrad ? static_cast<int64_t>(q.group) * p.rows_dim : q.row0) + static_cast<int64_t>(row);
+        if constexpr (kSegment == 0) {
+            ok = warp_wait(&ctl.acc_full[buf], acc_phase, &ctl.abort_flag, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            for (int c = 0; c < cols_half; c += 32) {
+                uint32_t u[32];
+                __syncwarp();
+                tc_ld32(lane_base + buf * kMaxTileCols + half * cols_half + c, u);
+                tc_wait_ld(u);
+                if (c + 32 >= cols_half) {  // read out: the accumulator is free before the last stores
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane_id() == 0) bar_arrive<CG>(acc_empty0 + 8 * buf);
+                }
+                float v[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+                if (row_ok && col0 + c < p.cols_dim)
+                    store_bf16(out_row(p, out_at), col0 + c, p.cols_dim, v, p.wide_stores != 0);
+            }
+            buf ^= 1;
+            acc_phase ^= buf == 0;
+        } else {
+            // The sums of a segment arrive in an accumulator of their own and are added up here, 128 columns a
+            // thread at most; in FP8 a segment is a block of 128 with its own scales.
+            uint64_t acc[2][32];  // pairs of fp32
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) acc[c][i] = 0;
+            const int segments = (q.steps + kSegment - 1) / kSegment;
+            // A block's scales are loaded a block before they are used, and only then looked at: a
+            // multiplication next to the loads would wait for them.
+            const uint8_t* xs = nullptr;
+            const float* ws = nullptr;
+            uint32_t x_next = 0;
+            float w_next = 0.0f;
+            if constexpr (FORM == kFp8) {
+                xs = p.x_scales + (static_cast<int64_t>(q.row0) + min(row, q.rows - 1)) * p.x_scale_row_bytes;
+                const int nb = min(col0, p.cols_dim - 1) >> 7;
+                ws = p.w_scales + (static_cast<int64_t>(q.group) * ((p.cols_dim + 127) >> 7) + nb) * q.steps;
+                x_next = raw_scale(xs, 0, p.scales_ue8m0);
+                w_next = ws[0];
+            }
+#pragma unroll 1
+            for (int s = 0; s < segments; ++s) {
+                ok = warp_wait(&ctl.acc_full[buf], acc_phase, &ctl.abort_flag, p.status);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t at = lane_base + buf * kMaxTileCols + half * cols_half;
+                uint32_t u[64];
+                tc_ld64(at, u);
+                float f = 1.0f;
+                if constexpr (FORM == kFp8) {  // while the load is on its way
+                    f = scale_value(x_next, p.scales_ue8m0) * w_next;
+                    if (s + 1 < segments) {
+                        x_next = raw_scale(xs, s + 1, p.scales_ue8m0);
+                        w_next = ws[s + 1];
+                    }
+                }
+                const uint64_t scale = pack_f32x2(__float_as_uint(f), __float_as_uint(f));
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    tc_wait_ld(u);
+                    if (c == 1 || cols_half <= 64) {  // all read: the accumulator is free
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane_id() == 0) bar_arrive<CG>(acc_empty0 + 8 * buf);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) fma_f32x2(acc[c][i], pack_f32x2(u[2 * i], u[2 * i + 1]), scale);
+                    if (cols_half <= 64) break;
+                    if (c == 0) tc_ld64(at + 64, u);
+                }
+                buf ^= 1;
+                acc_phase ^= buf == 0;
+            }
+            if (ok && row_ok) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (c * 32 < cols_half && col0 + c * 32 < p.cols_dim) {
+                        float v[32];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const uint64_t pair = acc[c / 2][c % 2 * 16 + i];
+                            v[2 * i] = __uint_as_float(static_cast<uint32_t>(pair));
+                            v[2 * i + 1] = __uint_as_float(static_cast<uint32_t>(pair >> 32));
+                        }
+                        if (FORM == kWeightGrad && p.out_fp32)
+                            store_fp32(out_row(p, out_at), col0 + c * 32, p.cols_dim, v, p.accumulate != 0, p.wide_stores != 0);
+                        else
+                            store_bf16(out_row(p, out_at), col0 + c * 32, p.cols_dim, v, p.wide_stores != 0);
+                    }
+            }
+        }
+    }
+}
+
 template <int FORM, int CG>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     grouped_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
@@ -256,302 +567,33 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     else __syncthreads();
     tc_fence_after();
 
-    const uint32_t tmem = ctl.tmem;
-    const int cols_here = ctl.tile_cols / CG;  // columns of the weight operand that this CTA loads
-    const uint32_t a_bytes = kTileRows * kRowBytes;
-    const uint32_t stage_bytes = a_bytes + cols_here * kRowBytes;
-    const int num_stages = min(kMaxStages, static_cast<int>((kMaxSmem - 1024u - table_end) / stage_bytes));
-    const int worker = blockIdx.x / CG, workers = gridDim.x / CG;
-    constexpr int kSegment = segment_steps(FORM);
-
+    const int cols_here = ctl.tile_cols / CG;
+    const uint32_t stage_bytes = kABytes + cols_here * kRowBytes;
+    const Roles x = {maps, p, t, ctl, stages, ctl.tmem, rank, stage_bytes, cols_here,
+                     min(kMaxStages, static_cast<int>((kMaxSmem - 1024u - table_end) / stage_bytes)),
+                     static_cast<int>(blockIdx.x / CG), static_cast<int>(gridDim.x / CG)};
     // Forms with segments hold 128 sums a thread in their eight epilogue warps: registers move there from the
     // others (72 + 2 * 216 = 3 * 168, what the block was launched with).
+    constexpr bool kSums = segment_steps(FORM) != 0;
     if (warp < 4) {
-    if constexpr (kSegment != 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 0) {
-        if (elect_one()) {
-        // ------------------------------------------------------------- loads
-        uint32_t stage = 0, phase = 0;
-        uint32_t tail_phase = 0, tail_last = 0;  // per stage: uses of tail_full, mod 2; whether its last use was one
-        bool ok = true;
-        const uint32_t full0 = CG == 1 ? smem_u32(ctl.full) : cluster_addr(ctl.full, 0);
-        uint32_t used = 0;
-        for (int tile = worker; ok && tile < ctl.tiles; tile += workers) {
-            const Tile q = decode<FORM, CG>(t, p, ctl, tile);
-            const int my_m0 = q.m0 + static_cast<int>(rank) * kTileRows;
-            const int rows_here = min(kTileRows, q.rows - my_m0);
-            const int small_boxes = rows_here > kTileRows / 2 ? 0 : (max(0, rows_here) + kRowBox - 1) / kRowBox;
-            const uint32_t bytes = FORM == kWeightGrad ? stage_bytes
-                                                       : cols_here * kRowBytes + (rows_here > kTileRows / 2 ? a_bytes : small_boxes * (kRowBox * kRowBytes));
-            for (int s = 0; s < q.steps; ++s) {
-                ok = wait_phase(&ctl.empty[stage], phase ^ 1, &ctl.abort_flag, p.status);
-                if (!ok) break;
-                uint8_t* a = stages + stage * stage_bytes;
-                uint8_t* b = a + a_bytes;
-                uint32_t bar = full0 + 8 * stage;
-                const int cb = static_cast<int>(rank) * cols_here;
-                if constexpr (FORM == kWeightGrad) {
-                    const bool tail = (s + 1) * 64 > q.rows;
-                    if (tail) {
-                        bar = smem_u32(&ctl.tail_full[stage]);
-                        mbar_arrive_expect_tx(&ctl.tail_full[stage], stage_bytes);
-                        tail_phase ^= 1u << stage;
-                        tail_last |= 1u << stage;
-                    } else {
-                        bar_arrive_expect_tx<CG>(bar, stage_bytes);
-                        tail_last &= ~(1u << stage);
-                    }
-                    const int r = q.row0 + s * 64;
-                    if (p.a_chunked) {
-                        tma_load_3d<CG>(a, &maps.a, 0, r, my_m0 / 64, bar);
-                    } else {
-                        tma_load_2d<CG>(a, &maps.a_small, my_m0, r, bar);
-                        tma_load_2d<CG>(a + 8192, &maps.a_small, my_m0 + 64, r, bar);
-                    }
-                    if (p.b_chunked && cols_here >= kBox) {
-                        for (int c = 0; c < cols_here; c += kBox)
-                            tma_load_3d<CG>(b + c * kRowBytes, &maps.b, 0, r, (q.n0 + cb + c) / 64, bar);
-                    } else {
-                        for (int c = 0; c < cols_here; c += kColBox)
-                            tma_load_2d<CG>(b + c * kRowBytes, &maps.b_small, q.n0 + cb + c, r, bar);
-                    }
-                } else {
-                    bar_arrive_expect_tx<CG>(bar, bytes);
-                    const int x = s * (FORM == kFp8 ? 128 : 64);
-                    if (small_boxes == 0) {
-                        if (rows_here > 0) tma_load_2d<CG>(a, &maps.a, x, q.row0 + my_m0, bar);
-                    } else {
-                        for (int c = 0; c < small_boxes; ++c)
-                            tma_load_2d<CG>(a + c * (kRowBox * kRowBytes), &maps.a_small, x, q.row0 + my_m0 + c * kRowBox, bar);
-                    }
-                    if (FORM == kTransposed) {
-                        if (p.b_chunked && cols_here >= kBox) {
-                            for (int c = 0; c < cols_here; c += kBox)
-                                tma_load_4d<CG>(b + c * kRowBytes, &maps.b, 0, x, (q.n0 + cb + c) / 64, q.group, bar);
-                        } else {
-                            for (int c = 0; c < cols_here; c += kColBox)
-                                tma_load_3d<CG>(b + c * kRowBytes, &maps.b_small, q.n0 + cb + c, x, q.group, bar);
-                        }
-                    } else if (cols_here >= kBox) {
-                        for (int c = 0; c < cols_here; c += kBox)
-                            tma_load_3d<CG>(b + c * kRowBytes, &maps.b, x, q.n0 + cb + c, q.group, bar);
-                    } else {
-                        tma_load_3d<CG>(b, &maps.b_small, x, q.n0 + cb, q.group, bar);
-                    }
-                }
-                ++used;
-                if (++stage == static_cast<uint32_t>(num_stages)) stage = 0, phase ^= 1;
-            }
+        if constexpr (kSums) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 0) {
+            if (elect_one()) load_operands<FORM, CG>(x);
+        } else if (warp == 1) {
+            if (rank == 0 && elect_one()) multiply<FORM, CG>(x);
+        } else if (FORM == kWeightGrad && warp == 2) {
+            zero_tails<FORM, CG>(x);
         }
-        if (!ok) {
-            // Given up: wait (again with a limit) for the copies in flight before the memory goes away.
-            // (With a pair, both CTAs' copies arrive at the leader, and neither leaves before the other.)
-            for (int i = 0; i < num_stages && used > 0; ++i, --used) {
-                if (stage == 0) phase ^= 1;
-                stage = (stage == 0 ? num_stages : stage) - 1;
-                const bool tail = (tail_last >> stage) & 1;
-                uint64_t* bar = tail ? &ctl.tail_full[stage] : &ctl.full[stage];
-                const uint32_t parity = tail ? ((tail_phase >> stage) & 1) ^ 1 : phase;
-                for (int k = 0; k < (1 << 12) && !mbar_try_wait(bar, parity); ++k) {
-                }
-            }
-        }
-        }
-    } else if (warp == 1) {
-        // ---------------------------------------------------------- products
-        if (rank == 0 && elect_one()) {
-            uint32_t stage = 0, phase = 0, acc_phase = 0;
-            int buf = 0;
-            bool ok = true;
-            constexpr bool a_mn = FORM == kWeightGrad;
-            constexpr bool b_mn = FORM == kWeightGrad || FORM == kTransposed;
-            const uint32_t idesc = mma_desc(FORM == kFp8 ? 0 : 1, a_mn, b_mn, kTileRows * CG, ctl.tile_cols);
-            for (int tile = worker; ok && tile < ctl.tiles; tile += workers) {
-                const Tile q = decode<FORM, CG>(t, p, ctl, tile);
-                for (int s = 0; s < q.steps && ok; ++s) {
-                    const int in_segment = kSegment ? s % kSegment : s;
-                    // operands first: they are there, and with short segments the accumulator is what is waited for
-                    if (FORM == kWeightGrad && CG == 2 && q.rows - s * 64 < 64)  // zeroed rows, maybe the peer's
-                        ok = wait_phase<true>(&ctl.full[stage], phase, &ctl.abort_flag, p.status);
-                    else
-                        ok = wait_phase(&ctl.full[stage], phase, &ctl.abort_flag, p.status);
-                    if (!ok) break;
-                    if (in_segment == 0) {
-                        ok = wait_phase(&ctl.acc_empty[buf], acc_phase ^ 1, &ctl.abort_flag, p.status);
-                        if (!ok) break;
-                    }
-                    tc_fence_after();
-                    const uint32_t a = smem_u32(stages) + stage * stage_bytes;
-                    const uint64_t da = smem_desc(a, a_mn ? 8192 : 16);
-                    const uint64_t db = smem_desc(a + a_bytes, b_mn ? 8192 : 16);
-                    const uint32_t d = tmem + buf * kMaxTileCols;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        tc_mma<CG, FORM == kFp8>(d, da + i * (a_mn ? 128 : 2), db + i * (b_mn ? 128 : 2), idesc,
-                                                 in_segment | i);
-                    tc_commit<CG>(&ctl.empty[stage]);
-                    if (s == q.steps - 1 || (kSegment && in_segment == kSegment - 1)) {
-                        tc_commit<CG>(&ctl.acc_full[buf]);
-                        buf ^= 1;
-                        acc_phase ^= buf == 0;
-                    }
-                    if (++stage == static_cast<uint32_t>(num_stages)) stage = 0, phase ^= 1;
-                }
-            }
-            if (!ok) {
-                // Given up: the products already issued still write tensor memory.
-                tc_commit<CG>(&ctl.drained);
-                for (int k = 0; k < (1 << 12) && !mbar_try_wait(&ctl.drained, 0); ++k) {
-                }
-            }
-        }
-    } else if (FORM == kWeightGrad && warp == 2) {
-        // ------------------------------------------------- ends of groups
-        // The rows of a group's last, partial block past its end belong to others: zero them in both operands.
-        uint32_t stage = 0, tail_phase = 0;  // tail_phase, per stage: uses of tail_full, mod 2
-        bool ok = true;
-        for (int tile = worker; ok && tile < ctl.tiles; tile += workers) {
-            const Tile q = decode<FORM, CG>(t, p, ctl, tile);
-            const int whole = q.rows / 64, valid = q.rows % 64;
-            stage = (stage + whole) % num_stages;
-            if (valid == 0) continue;
-            ok = warp_wait(&ctl.tail_full[stage], (tail_phase >> stage) & 1, &ctl.abort_flag, p.status);
-            tail_phase ^= 1u << stage;
-            uint8_t* a = stages + stage * stage_bytes;
-            const int chunks = (kTileRows + cols_here) / 64;
-            const int pieces = (64 - valid) * 8;
-            for (int c = 0; c < chunks; ++c) {
-                uint4* z = reinterpret_cast<uint4*>(a + c * 8192 + valid * 128);
-                for (int i = lane_id(); i < pieces; i += kWarpSize) z[i] = make_uint4(0, 0, 0, 0);
-            }
-            fence_async_smem();
-            __syncwarp();
-            if (lane_id() == 0)
-                bar_arrive_written<CG>(CG == 1 ? smem_u32(&ctl.full[stage]) : cluster_addr(&ctl.full[stage], 0));
-            stage = (stage + 1) % num_stages;
-        }
-    }
     } else {
-        // ------------------------------------------------- accumulators out
-        if constexpr (kSegment != 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        const int w = warp - 4;
-        const int quarter = warp & 3;               // the 32 lanes of tensor memory that this warp may read
-        const int half = w >> 2;                    // which half of the tile's columns
-        const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-        const int cols_half = ctl.tile_cols / 2;
-        const uint32_t acc_empty0 = CG == 1 ? smem_u32(ctl.acc_empty) : cluster_addr(ctl.acc_empty, 0);
-        int buf = 0;
-        uint32_t acc_phase = 0;
-        bool ok = true;
-        for (int tile = worker; ok && tile < ctl.tiles; tile += workers) {
-            const Tile q = decode<FORM, CG>(t, p, ctl, tile);
-            const int row = q.m0 + static_cast<int>(rank) * kTileRows + quarter * 32 + lane_id();  // in the group
-            const int col0 = q.n0 + half * cols_half;
-            const bool row_ok = row < (FORM == kWeightGrad ? p.rows_dim : q.rows);
-            const int64_t out_at = FORM == kWeightGrad ? static_cast<int64_t>(q.group) * p.rows_dim + row : static_cast<int64_t>(q.row0) + row;
-            if constexpr (kSegment == 0) {
-                ok = warp_wait(&ctl.acc_full[buf], acc_phase, &ctl.abort_flag, p.status);
-                if (!ok) break;
-                tc_fence_after();
-                for (int c = 0; c < cols_half; c += 32) {
-                    uint32_t u[32];
-                    __syncwarp();
-                    tc_ld32(lane_base + buf * kMaxTileCols + half * cols_half + c, u);
-                    tc_wait_ld(u);
-                    if (c + 32 >= cols_half) {  // read out: the accumulator is free before the last stores
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane_id() == 0) bar_arrive<CG>(acc_empty0 + 8 * buf);
-                    }
-                    float v[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
-                    if (row_ok && col0 + c < p.cols_dim)
-                        store_bf16(out_row(p, out_at), col0 + c, p.cols_dim, v, p.wide_stores != 0);
-                }
-                buf ^= 1;
-                acc_phase ^= buf == 0;
-            } else {
-                // The sums of a segment arrive in an accumulator of their own and are added up here, 128 columns a
-                // thread at most; in FP8 a segment is a block of 128 with its own scales.
-                uint64_t acc[2][32];  // pairs of fp32
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) acc[c][i] = 0;
-                const int segments = (q.steps + kSegment - 1) / kSegment;
-                // A block's scales are loaded a block before they are used, and only then looked at: a
-                // multiplication next to the loads would wait for them.
-                const uint8_t* xs = nullptr;
-                const float* ws = nullptr;
-                uint32_t x_next = 0;
-                float w_next = 0.0f;
-                if constexpr (FORM == kFp8) {
-                    xs = p.x_scales + (static_cast<int64_t>(q.row0) + min(row, q.rows - 1)) * p.x_scale_row_bytes;
-                    const int nb = min(col0, p.cols_dim - 1) >> 7;
-                    ws = p.w_scales + (static_cast<int64_t>(q.group) * ((p.cols_dim + 127) >> 7) + nb) * q.steps;
-                    x_next = raw_scale(xs, 0, p.scales_ue8m0);
-                    w_next = ws[0];
-                }
-#pragma unroll 1
-                for (int s = 0; s < segments; ++s) {
-                    ok = warp_wait(&ctl.acc_full[buf], acc_phase, &ctl.abort_flag, p.status);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t at = lane_base + buf * kMaxTileCols + half * cols_half;
-                    uint32_t u[64];
-                    tc_ld64(at, u);
-                    float f = 1.0f;
-                    if constexpr (FORM == kFp8) {  // while the load is on its way
-                        f = scale_value(x_next, p.scales_ue8m0) * w_next;
-                        if (s + 1 < segments) {
-                            x_next = raw_scale(xs, s + 1, p.scales_ue8m0);
-                            w_next = ws[s + 1];
-                        }
-                    }
-                    const uint64_t scale = pack_f32x2(__float_as_uint(f), __float_as_uint(f));
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        tc_wait_ld(u);
-                        if (c == 1 || cols_half <= 64) {  // all read: the accumulator is free
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane_id() == 0) bar_arrive<CG>(acc_empty0 + 8 * buf);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) fma_f32x2(acc[c][i], pack_f32x2(u[2 * i], u[2 * i + 1]), scale);
-                        if (cols_half <= 64) break;
-                        if (c == 0) tc_ld64(at + 64, u);
-                    }
-                    buf ^= 1;
-                    acc_phase ^= buf == 0;
-                }
-                if (ok && row_ok) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if (c * 32 < cols_half && col0 + c * 32 < p.cols_dim) {
-                            float v[32];
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const uint64_t pair = acc[c / 2][c % 2 * 16 + i];
-                                v[2 * i] = __uint_as_float(static_cast<uint32_t>(pair));
-                                v[2 * i + 1] = __uint_as_float(static_cast<uint32_t>(pair >> 32));
-                            }
-                            if (FORM == kWeightGrad && p.out_fp32)
-                                store_fp32(out_row(p, out_at), col0 + c * 32, p.cols_dim, v, p.accumulate != 0, p.wide_stores != 0);
-                            else
-                                store_bf16(out_row(p, out_at), col0 + c * 32, p.cols_dim, v, p.wide_stores != 0);
-                        }
-                }
-            }
-        }
+        if constexpr (kSums) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        store_tiles<FORM, CG>(x, warp);
     }
     __syncwarp();
     tc_fence_before();
     if constexpr (CG == 2) cluster_barrier();
     else __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc<CG>(tmem, 512);
+    if (warp == 1) tmem_dealloc<CG>(x.tmem, 512);
 }
 
 // ---------------------------------------------------------------------------
