@@ -595,6 +595,11 @@ def _out(shape, dtype, h, stream):
         return torch.empty(shape, dtype=dtype, device=h.device)
 
 
+def _like(x, rows, width):
+    """The shape of an output with x's leading axes and rows of `width`."""
+    return (rows, width) if x.dim() == 2 else x.shape[:-1] + (width,)
+
+
 def _group_arrays(h, group_count, group_begin):
     E = (h.cfg.num_experts,)
     if group_count is not None and group_count.dim() == 2:  # packed_recv_count [R][EL]
@@ -615,7 +620,7 @@ def ep_grouped_gemm(h: Handle, x: torch.Tensor, w: torch.Tensor, group_count, gr
     n, k = (w.shape[2], w.shape[1]) if w_transposed else (w.shape[1], w.shape[2])
     xp, rows, _, xs = _rows(x, "x", torch.bfloat16, d, None, k)
     if out is None:
-        out = _out(x.shape[:-1] + (n,), torch.bfloat16, h, stream)
+        out = _out(_like(x, rows, n), torch.bfloat16, h, stream)
     op, _, _, os_ = _rows(out, "out", torch.bfloat16, d, rows, n)
     cnt, beg = _group_arrays(h, group_count, group_begin)
     _raise(lib().ep_grouped_gemm(h.ptr, rows, n, k, cnt, beg, xp, xs,
@@ -665,7 +670,7 @@ def ep_grouped_gemm_fp8(h: Handle, x: torch.Tensor, x_scales: torch.Tensor, w: t
         x_scales = x_scales[..., :G]
     sp, _, _, ss = _rows(x_scales, "x_scales", x_scales.dtype, d, rows, G)
     if out is None:
-        out = _out(x.shape[:-1] + (n,), torch.bfloat16, h, stream)
+        out = _out(_like(x, rows, n), torch.bfloat16, h, stream)
     op, _, _, os_ = _rows(out, "out", torch.bfloat16, d, rows, n)
     cnt, beg = _group_arrays(h, group_count, group_begin)
     _raise(lib().ep_grouped_gemm_fp8(h.ptr, rows, n, k, cnt, beg, xp, xs, sp, ss, int(ue8m0),
@@ -685,14 +690,14 @@ def ep_swiglu(h: Handle, x: torch.Tensor, group_count, group_begin=None, row_wei
         raise ValueError(f"x must hold gate and up of one width, got rows of {wide}")
     dtype = torch.float8_e4m3fn if cast_to_fp8 else torch.bfloat16
     if out is None:
-        out = _out(x.shape[:-1] + (width,), dtype, h, stream)
+        out = _out(_like(x, rows, width), dtype, h, stream)
     if cast_to_fp8 and out_scales is None:
-        out_scales = _out(x.shape[:-1] + (width // 128,), torch.float32, h, stream)
+        out_scales = _out(_like(x, rows, width // 128), torch.float32, h, stream)
     op, _, _, os_ = _rows(out, "out", dtype, d, rows, width)
     cnt, beg = _group_arrays(h, group_count, group_begin)
     _raise(lib().ep_swiglu(h.ptr, rows, width, cnt, beg, xp, xs, _ptr(row_weights, "row_weights", torch.float32, (rows,), d),
                            int(bool(cast_to_fp8)), int(bool(round_scale)), op, os_,
-                           _ptr(out_scales, "out_scales", torch.float32, tuple(x.shape[:-1]) + (width // 128,), d),
+                           _ptr(out_scales, "out_scales", torch.float32, _like(x, rows, width // 128), d),
                            _stream(stream, d)))
     return dict(out=out, out_scales=out_scales)
 
