@@ -41,6 +41,7 @@ constexpr int kBox = 128;           // output elements (rows or columns) of a te
 constexpr int kRowBox = 32;         // the same for a group's last rows: a short group loads few
 constexpr int kColBox = 64;         // the same for narrow tiles
 constexpr int kTileOverhead = 32;   // columns that a tile's width-independent cost is worth
+constexpr int kPairRowsFp8 = 1024;  // rows of a group from which the FP8 form runs on pairs of CTAs
 constexpr int kMaxStages = 12;
 constexpr int kEpilogueWarps = 8;
 constexpr int kGemmThreads = (4 + kEpilogueWarps) * kWarpSize;  // of warps 0 to 3 not all have work: registers are split by four warps
@@ -61,7 +62,7 @@ struct GemmParams {
     int32_t out_fp32;       // weight grad
     int32_t accumulate;     // weight grad
     int32_t wide_stores;    // output rows are 32-byte aligned
-    int32_t a_chunked, b_chunked;  // operands read across: kBox columns in one load (else kColBox)
+    int32_t a_chunked, b_chunked;  // operands read across: columns up to which loads of kBox reach (then kColBox)
     int32_t* status;
 };
 
@@ -85,7 +86,7 @@ struct Control {
 static_assert(sizeof(Control) <= kControlBytes, "control block");
 
 struct Tile {
-    int group, row0, rows, m0, n0, steps;  // rows: valid rows of the group; m0: tile's first row in the group
+    int group, row0, rows, m0, n0, cols, steps;  // rows: valid rows of the group; m0: tile's first row in the group
 };
 
 // The group table in shared memory.
@@ -106,6 +107,9 @@ __device__ __forceinline__ Tile decode(const Table& t, const GemmParams& p, cons
     r.rows = t.count[lo];
     // row tiles turn fastest: CTAs side by side share a weight tile
     r.n0 = in / row_tiles * ctl.tile_cols;
+    // the last tile across is no wider than it has to be
+    r.cols = ctl.tile_cols;
+    while (r.cols > kColBox * CG && 2 * (p.cols_dim - r.n0) <= r.cols) r.cols >>= 1;
     r.m0 = in % row_tiles * (kTileRows * CG);
     if constexpr (FORM == kWeightGrad) r.steps = (r.rows + 63) >> 6;
     else if constexpr (FORM == kFp8) r.steps = (p.contraction + 127) >> 7;
@@ -225,7 +229,6 @@ struct Roles {
     Control& ctl;
     uint8_t* stages;
     uint32_t tmem, rank, stage_bytes;  // rank: of the CTA in its pair
-    int cols_here;                     // columns of the weight operand that this CTA loads
     int num_stages, worker, workers;
 };
 
@@ -247,39 +250,43 @@ __device__ __forceinline__ void load_operands(const Roles& x) {
         const int my_m0 = q.m0 + static_cast<int>(x.rank) * kTileRows;
         const int rows_here = min(kTileRows, q.rows - my_m0);
         const int small_boxes = rows_here > kTileRows / 2 ? 0 : (max(0, rows_here) + kRowBox - 1) / kRowBox;
-        const uint32_t row_bytes = rows_here > kTileRows / 2 ? kABytes : small_boxes * (kRowBox * kRowBytes);
-        const uint32_t bytes = FORM == kWeightGrad ? x.stage_bytes : x.cols_here * kRowBytes + row_bytes;
+        const uint32_t row_bytes = FORM == kWeightGrad || rows_here > kTileRows / 2 ? kABytes : small_boxes * (kRowBox * kRowBytes);
+        const int cols = q.cols / CG;                     // columns that this CTA loads
+        const int cb = static_cast<int>(x.rank) * cols;
+        const uint32_t bytes = row_bytes + cols * kRowBytes;
         for (int s = 0; s < q.steps; ++s) {
             ok = wait_phase(&ctl.empty[stage], phase ^ 1, &ctl.abort_flag, p.status);
             if (!ok) break;
             uint8_t* a = x.stages + stage * x.stage_bytes;
             uint8_t* b = a + kABytes;
             uint32_t bar = full0 + 8 * stage;
-            const int cb = static_cast<int>(x.rank) * x.cols_here;
             if constexpr (FORM == kWeightGrad) {
                 const bool tail = (s + 1) * 64 > q.rows;
                 if (tail) {
                     bar = smem_u32(&ctl.tail_full[stage]);
-                    mbar_arrive_expect_tx(&ctl.tail_full[stage], x.stage_bytes);
+                    mbar_arrive_expect_tx(&ctl.tail_full[stage], bytes);
                     tail_phase ^= 1u << stage;
                     tail_last |= 1u << stage;
                 } else {
-                    bar_arrive_expect_tx<CG>(bar, x.stage_bytes);
+                    bar_arrive_expect_tx<CG>(bar, bytes);
                     tail_last &= ~(1u << stage);
                 }
                 const int r = q.row0 + s * 64;
-                if (p.a_chunked) {
+                if (my_m0 + kBox <= p.a_chunked) {
                     tma_load_3d<CG>(a, &x.maps.a, 0, r, my_m0 / 64, bar);
                 } else {
                     tma_load_2d<CG>(a, &x.maps.a_small, my_m0, r, bar);
                     tma_load_2d<CG>(a + 8192, &x.maps.a_small, my_m0 + 64, r, bar);
                 }
-                if (p.b_chunked && x.cols_here >= kBox) {
-                    for (int c = 0; c < x.cols_here; c += kBox)
-                        tma_load_3d<CG>(b + c * kRowBytes, &x.maps.b, 0, r, (q.n0 + cb + c) / 64, bar);
-                } else {
-                    for (int c = 0; c < x.cols_here; c += kColBox)
-                        tma_load_2d<CG>(b + c * kRowBytes, &x.maps.b_small, q.n0 + cb + c, r, bar);
+                for (int c = 0; c < cols;) {
+                    const int at = q.n0 + cb + c;
+                    if (c + kBox <= cols && at + kBox <= p.b_chunked) {
+                        tma_load_3d<CG>(b + c * kRowBytes, &x.maps.b, 0, r, at / 64, bar);
+                        c += kBox;
+                    } else {
+                        tma_load_2d<CG>(b + c * kRowBytes, &x.maps.b_small, at, r, bar);
+                        c += kColBox;
+                    }
                 }
             } else {
                 bar_arrive_expect_tx<CG>(bar, bytes);
@@ -290,19 +297,21 @@ __device__ __forceinline__ void load_operands(const Roles& x) {
                     for (int c = 0; c < small_boxes; ++c)
                         tma_load_2d<CG>(a + c * (kRowBox * kRowBytes), &x.maps.a_small, k0, q.row0 + my_m0 + c * kRowBox, bar);
                 }
-                if (FORM == kTransposed) {
-                    if (p.b_chunked && x.cols_here >= kBox) {
-                        for (int c = 0; c < x.cols_here; c += kBox)
-                            tma_load_4d<CG>(b + c * kRowBytes, &x.maps.b, 0, k0, (q.n0 + cb + c) / 64, q.group, bar);
+                for (int c = 0; c < cols;) {
+                    const int at = q.n0 + cb + c;
+                    if (FORM == kTransposed && c + kBox <= cols && at + kBox <= p.b_chunked) {
+                        tma_load_4d<CG>(b + c * kRowBytes, &x.maps.b, 0, k0, at / 64, q.group, bar);
+                        c += kBox;
+                    } else if (FORM == kTransposed) {
+                        tma_load_3d<CG>(b + c * kRowBytes, &x.maps.b_small, at, k0, q.group, bar);
+                        c += kColBox;
+                    } else if (c + kBox <= cols) {
+                        tma_load_3d<CG>(b + c * kRowBytes, &x.maps.b, k0, at, q.group, bar);
+                        c += kBox;
                     } else {
-                        for (int c = 0; c < x.cols_here; c += kColBox)
-                            tma_load_3d<CG>(b + c * kRowBytes, &x.maps.b_small, q.n0 + cb + c, k0, q.group, bar);
+                        tma_load_3d<CG>(b + c * kRowBytes, &x.maps.b_small, k0, at, q.group, bar);
+                        c += kColBox;
                     }
-                } else if (x.cols_here >= kBox) {
-                    for (int c = 0; c < x.cols_here; c += kBox)
-                        tma_load_3d<CG>(b + c * kRowBytes, &x.maps.b, k0, q.n0 + cb + c, q.group, bar);
-                } else {
-                    tma_load_3d<CG>(b, &x.maps.b_small, k0, q.n0 + cb, q.group, bar);
                 }
             }
             ++used;
@@ -336,9 +345,9 @@ __device__ __forceinline__ void multiply(const Roles& x) {
     bool ok = true;
     constexpr bool a_mn = FORM == kWeightGrad;
     constexpr bool b_mn = FORM == kWeightGrad || FORM == kTransposed;
-    const uint32_t idesc = mma_desc(FORM == kFp8 ? 0 : 1, a_mn, b_mn, kTileRows * CG, ctl.tile_cols);
     for (int tile = x.worker; ok && tile < ctl.tiles; tile += x.workers) {
         const Tile q = decode<FORM, CG>(t, p, ctl, tile);
+        const uint32_t idesc = mma_desc(FORM == kFp8 ? 0 : 1, a_mn, b_mn, kTileRows * CG, q.cols);
         for (int s = 0; s < q.steps && ok; ++s) {
             const int in_segment = kSegment ? s % kSegment : s;
             // operands first: they are there, and with short segments the accumulator is what is waited for
@@ -394,7 +403,7 @@ __device__ __forceinline__ void zero_tails(const Roles& x) {
         ok = warp_wait(&ctl.tail_full[stage], (tail_phase >> stage) & 1, &ctl.abort_flag, p.status);
         tail_phase ^= 1u << stage;
         uint8_t* a = x.stages + stage * x.stage_bytes;
-        const int chunks = (kTileRows + x.cols_here) / 64;
+        const int chunks = (kTileRows + q.cols / CG) / 64;
         const int pieces = (64 - valid) * 8;
         for (int c = 0; c < chunks; ++c) {
             uint4* z = reinterpret_cast<uint4*>(a + c * 8192 + valid * 128);
@@ -419,13 +428,13 @@ __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
     const int quarter = warp & 3;               // the 32 lanes of tensor memory that this warp may read
     const int half = w >> 2;                    // which half of the tile's columns
     const uint32_t lane_base = x.tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const int cols_half = ctl.tile_cols / 2;
     const uint32_t acc_empty0 = CG == 1 ? smem_u32(ctl.acc_empty) : cluster_addr(ctl.acc_empty, 0);
     int buf = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
     for (int tile = x.worker; ok && tile < ctl.tiles; tile += x.workers) {
         const Tile q = decode<FORM, CG>(t, p, ctl, tile);
+        const int cols_half = q.cols / 2;
         const int row = q.m0 + static_cast<int>(x.rank) * kTileRows + quarter * 32 + lane_id();  // in the group
         const int col0 = q.n0 + half * cols_half;
         const bool row_ok = row < (FORM == kWeightGrad ? p.rows_dim : q.rows);
@@ -567,9 +576,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     else __syncthreads();
     tc_fence_after();
 
-    const int cols_here = ctl.tile_cols / CG;
-    const uint32_t stage_bytes = kABytes + cols_here * kRowBytes;
-    const Roles x = {maps, p, t, ctl, stages, ctl.tmem, rank, stage_bytes, cols_here,
+    const uint32_t stage_bytes = kABytes + ctl.tile_cols / CG * kRowBytes;
+    const Roles x = {maps, p, t, ctl, stages, ctl.tmem, rank, stage_bytes,
                      min(kMaxStages, static_cast<int>((kMaxSmem - 1024u - table_end) / stage_bytes)),
                      static_cast<int>(blockIdx.x / CG), static_cast<int>(gridDim.x / CG)};
     // Forms with segments hold 128 sums a thread in their eight epilogue warps: registers move there from the
@@ -642,8 +650,11 @@ Operand row_operand(const void* base, bool fp8, uint64_t inner, uint64_t rows, u
     return {base, fp8, 2, {inner, rows, 1, 1}, {row_bytes, 0, 0}, {fp8 ? 128u : 64u, box_rows, 1, 1}};
 }
 
-// The same rows read across, 64 columns by 64 rows; `chunks` of 64 columns in one load. More than one needs inner % 64
-// == 0: a chunk is an index of its own there, and a last, partial one would reach into the next row.
+// The same rows read across, 64 columns by 64 rows; `chunks` of 64 columns in one load.  With more than one, a chunk
+// is an index of its own and the map ends at the last whole one (chunked_columns): a partial one would reach into
+// the next row, and past the last row's end.
+int chunked_columns(int inner) { return inner >= kBox ? inner / 64 * 64 : 0; }
+
 Operand across_operand(const void* base, uint64_t inner, uint64_t rows, uint64_t row_bytes, uint32_t chunks) {
     if (chunks == 1) return row_operand(base, false, inner, rows, row_bytes, 64);
     return {base, false, 3, {64, rows, inner / 64, 1}, {row_bytes, 128, 0}, {64, 64, chunks, 1}};
@@ -663,7 +674,7 @@ Operand weight_across_operand(const void* base, uint64_t inner, uint64_t rows, u
 
 template <int FORM>
 ep_status launch(const ep_handle* h, const Operand& a, const Operand& a_small, const Operand& b, const Operand& b_small,
-                 const GemmParams& p, int64_t tile_rows, cudaStream_t stream) {
+                 const GemmParams& p, int64_t rows_each, cudaStream_t stream) {
     Maps m;
     ep_status st = encode(&m.a, a);
     if (st == EP_OK) st = encode(&m.a_small, a_small);
@@ -672,9 +683,13 @@ ep_status launch(const ep_handle* h, const Operand& a, const Operand& a_small, c
     if (st != EP_OK) return st;
     DeviceGuard guard(h->device);
     // A pair of CTAs computes 256 rows: each loads half of the weight tile, so that a row of products takes a
-    // third less shared-memory fill.  Where the rows of a group would leave one of the two idle, single CTAs.
+    // third less shared-memory fill.  Where the rows of a group would leave one of the two idle, single CTAs; in
+    // FP8, where a block's sums wait for both CTAs of a pair, single CTAs up to 1024 rows.  Measured at 32 experts,
+    // 4096 x 4096, single against pair: bf16 185 and 185 us at 128 rows an expert, 222 and 203 at 200, 1361 and
+    // 1241 at 2048; FP8 106 and 125 at 128, 363 and 388 at 700, 567 and 557 at 1024, 1105 and 1034 at 2048.
+    const int64_t pair_rows = FORM == kFp8 ? kPairRowsFp8 : kTileRows + 1;
     const cudaError_t err =
-        tile_rows > kTileRows && h->plan.gemm_pairs > 0
+        rows_each >= pair_rows && h->plan.gemm_pairs > 0
             ? launch_kernel(grouped_gemm_kernel<FORM, 2>, dim3(2 * h->plan.gemm_pairs), dim3(kGemmThreads), kMaxSmem, stream,
                             2, m, p)
             : launch_kernel(grouped_gemm_kernel<FORM, 1>, dim3(h->plan.num_sms), dim3(kGemmThreads), kMaxSmem, stream, 1,
@@ -777,7 +792,7 @@ ep_status ep_grouped_gemm(ep_handle* h, int64_t num_rows, int32_t n, int32_t k, 
     if (!w_transposed)
         return launch<kForward>(h, a, a_small, weight_operand(w, false, k, n, groups, kBox),
                                 weight_operand(w, false, k, n, groups, kColBox), p, rows_each, stream);
-    p.b_chunked = n % 64 == 0;
+    p.b_chunked = chunked_columns(n);
     return launch<kTransposed>(h, a, a_small, weight_across_operand(w, n, k, groups, p.b_chunked ? kBox / 64 : 1),
                                weight_across_operand(w, n, k, groups, 1), p, rows_each, stream);
 }
@@ -812,8 +827,8 @@ ep_status ep_grouped_gemm_wgrad(ep_handle* h, int64_t num_rows, int32_t n, int32
     p.accumulate = accumulate != 0;
     p.out_row_bytes = static_cast<int64_t>(k) * (p.out_fp32 ? 4 : 2);
     p.wide_stores = rows_aligned32(dw, p.out_row_bytes);
-    p.a_chunked = n % 64 == 0;
-    p.b_chunked = k % 64 == 0;
+    p.a_chunked = chunked_columns(n);
+    p.b_chunked = chunked_columns(k);
     return launch<kWeightGrad>(h, across_operand(dy, n, num_rows, dy_row_bytes, p.a_chunked ? kBox / 64 : 1),
                                across_operand(dy, n, num_rows, dy_row_bytes, 1),
                                across_operand(x, k, num_rows, x_row_bytes, p.b_chunked ? kBox / 64 : 1),
