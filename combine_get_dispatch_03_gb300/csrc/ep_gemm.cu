@@ -4,14 +4,29 @@
 // weights.  Four forms share one persistent kernel:
 //   forward       out[r][j] = sum_c x[r][c] * w[e][j][c]          bf16, both operands contraction-major
 //   transposed    out[r][j] = sum_c x[r][c] * w[e][c][j]          bf16, the weights read across (gradient of the rows)
-//   weight grad   dw[e][j][c] = sum_r dy[r][j] * x[r][c]          bf16, both operands read across, contraction over a group's rows
-//   fp8           out[r][j] = sum_b sx[r][b] * sw[e][j/128][b] * sum_{c in block b} x[r][c] * w[e][j][c]    e4m3, blocks of 128
+//   weight grad   dw[e][j][c] = sum_r dy[r][j] * x[r][c]          bf16, both operands read across, over a group's rows
+//   fp8           out[r][j] = sum_b sx[r][b] * sw[e][j/128][b] * sum_{c in b} x[r][c] * w[e][j][c]    e4m3, blocks b of 128
 //
 // Work is cut into output tiles of 128 rows (256 for a pair of CTAs) by 64, 128 or 256 columns, taken
-// in turn by the CTAs of one resident wave.  In a CTA one warp loads operand tiles with tensor maps into a
-// ring of shared-memory stages (128 bytes of the contraction a stage), one warp issues tcgen05.mma from
-// them into tensor memory, and the remaining warps read the fp32 accumulators back, round and store.  Two
+// in turn by the CTAs of one resident wave.  In a CTA one thread loads operand tiles with tensor maps into a
+// ring of shared-memory stages (128 bytes of the contraction a stage), one thread issues tcgen05.mma from
+// them into tensor memory, and eight warps read the fp32 accumulators back, round and store.  Two
 // accumulators of 256 columns let the next tile's products run under this tile's stores.
+//
+// What bounds it, measured on a GB300 (1946.7 TFLOP/s bf16, 6787 GB/s copied):
+//   - many rows an expert, bf16: the tensor cores, at the clock that the power limit leaves.  8 experts of 2048 rows,
+//     4096 x 7168: 526 to 542 us, 1770 to 1830 TFLOP/s, 512 to 516 cycles a stage where a stage's products take
+//     512; the gradient of the rows 510 to 524 us, of the weights 550 to 573 us (its 0.94 GB of fp32 results
+//     and the ends of groups cost the rest).
+//   - few rows an expert: memory, the weights.  32 experts of 64 rows, 4096 x 7168 bf16: 286 us, 6.7 TB/s.
+//   - FP8: a block's sums go from tensor memory through registers, 32768 FMAs a stage and CTA at 128 a cycle; with the
+//     way there and back between the products' thread and the eight warps a stage takes about 800 cycles for
+//     512 of products.  The same 8 experts: 374 to 384 us, 2500 to 2570 TFLOP/s; 64 experts of 128 rows read from
+//     messages: 334 us, 6.0 TB/s.
+//
+// Two loads of 16 KB a stage (one an operand) rather than smaller ones: a load costs the issuing thread about
+// 95 cycles.  64 columns of an accumulator a read in the FP8 form: 292 cycles for 128 columns and their FMAs in eight
+// warps, 335 with 32 a read.
 //
 // The group table (tiles before each expert, counts, begins) is built in shared memory by each CTA from the
 // device arrays, so that no count has to reach the host.
@@ -44,7 +59,7 @@ constexpr int kTileOverhead = 32;   // columns that a tile's width-independent c
 constexpr int kPairRowsFp8 = 1024;  // rows of a group from which the FP8 form runs on pairs of CTAs
 constexpr int kMaxStages = 12;
 constexpr int kEpilogueWarps = 8;
-constexpr int kGemmThreads = (4 + kEpilogueWarps) * kWarpSize;  // of warps 0 to 3 not all have work: registers are split by four warps
+constexpr int kGemmThreads = (4 + kEpilogueWarps) * kWarpSize;  // warps 0 to 3 for loads and products: registers go by four warps
 constexpr int kControlBytes = 512;  // static shared memory
 constexpr int kMaxSmem = 232448 - kControlBytes;
 
