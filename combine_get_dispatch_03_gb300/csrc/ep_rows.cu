@@ -153,10 +153,10 @@ __global__ void __launch_bounds__(kRowThreads)
         __syncthreads();
         const int32_t* before = before_chunk + (static_cast<int64_t>(r) * gridDim.x + chunk) * EL;
         for (int j = threadIdx.x; j < EL; j += kRowThreads) {
-            int at = place[j] + before[j];
+            uint32_t at = static_cast<uint32_t>(place[j]) + before[j];
             for (int w = 1; w <= kRowWarps; ++w) {
                 const int c = place[w * EL + j];
-                place[w * EL + j] = at;
+                place[w * EL + j] = static_cast<int32_t>(at);
                 at += c;
             }
         }
@@ -169,11 +169,10 @@ __global__ void __launch_bounds__(kRowThreads)
         const unsigned same = __match_any_sync(kFullMask, e);
         int row = -1;
         if (e >= 0) {
-            row = mine[e] + __popc(same & lanemask_lt());
-            if (row >= num_rows) {
-                report(status, EP_ERR_CAPACITY);
-                row = -1;
-            }
+            // unsigned: a begin past the rows there are, cut to 2^31 - 1, plus the rows before this one
+            const uint32_t at = static_cast<uint32_t>(mine[e]) + __popc(same & lanemask_lt());
+            if (at < num_rows) row = static_cast<int>(at);
+            else report(status, EP_ERR_CAPACITY);
         }
         __syncwarp();
         if (e >= 0 && (same & lanemask_lt()) == 0) mine[e] += __popc(same);

@@ -412,7 +412,9 @@ ep_status ep_ll_dispatch_noalloc(int32_t num_ranks, int32_t num_tokens, int32_t 
  * int32 [E] in device memory; groups may be empty, and rows outside every
  * group are neither used nor written.  A group that passes num_rows (or
  * num_rows / E without group_begin), or with a negative begin or count, sets
- * EP_ERR_CAPACITY; the rows that do not fit are left out.
+ * EP_ERR_CAPACITY; the rows that do not fit are left out.  Groups must not
+ * overlap where a call writes their rows: if together they hold more rows than
+ * there are, EP_ERR_CAPACITY is set and nothing is written.
  * Row operands and outputs have row strides in bytes: multiples of 16, base
  * 16-byte aligned.  n and k are multiples of 8.  Sums are fp32, rounded once.
  * NaN and infinities in a row reach that row's outputs only (a weight

@@ -524,6 +524,16 @@ def test_expert_layout(R, EL, K, cap, alignment, mask):
         assert torch.equal(few["slot_row"].cpu(), torch.where(slot < rows // 2, slot, -1))
 
 
+def test_expert_layout_with_begins_past_every_row():
+    """An alignment that pushes later experts' begins past 2^31: their slots have no row and the capacity is reported."""
+    h = handle(4, 1, 64, 8, 1, 8, 2 ** 30)
+    idx = torch.tensor([0, 1, 2, 3, 3, 2, 1, 0], dtype=torch.int64, device=DEV).view(1, 8, 1)
+    lay = ep.ep_expert_layout(h, idx, 64, num_recv=i32([8]))
+    assert h.status() == 2
+    assert lay["group_count"].tolist() == [2, 2, 2, 2]
+    assert lay["slot_row"].view(-1).tolist() == [0, -1, -1, -1, -1, -1, -1, 1]
+
+
 def test_expert_layout_reports_bad_experts():
     h = handle(4, 2, 64, 8, 2, 8)
     idx = torch.zeros((2, 8, 2), dtype=torch.int64, device=DEV)
