@@ -78,6 +78,8 @@ struct GemmParams {
     int32_t accumulate;     // weight grad
     int32_t wide_stores;    // output rows are 32-byte aligned
     int32_t a_chunked, b_chunked;  // operands read across: columns up to which loads of kBox reach (then kColBox)
+    const uint8_t* a_words;        // rows that no tensor map can describe (not 16 bytes apart), or NULL
+    int64_t a_row_bytes;
     int32_t* status;
 };
 
@@ -249,8 +251,8 @@ struct Roles {
 
 constexpr uint32_t kABytes = kTileRows * kRowBytes;
 
-// One thread: the loads.
-template <int FORM, int CG>
+// One thread: the loads.  kWords: copy_rows() has the row operand.
+template <int FORM, int CG, bool kWords>
 __device__ __forceinline__ void load_operands(const Roles& x) {
     const GemmParams& p = x.p;
     const Table& t = x.t;
@@ -265,7 +267,9 @@ __device__ __forceinline__ void load_operands(const Roles& x) {
         const int my_m0 = q.m0 + static_cast<int>(x.rank) * kTileRows;
         const int rows_here = min(kTileRows, q.rows - my_m0);
         const int small_boxes = rows_here > kTileRows / 2 ? 0 : (max(0, rows_here) + kRowBox - 1) / kRowBox;
-        const uint32_t row_bytes = FORM == kWeightGrad || rows_here > kTileRows / 2 ? kABytes : small_boxes * (kRowBox * kRowBytes);
+        uint32_t row_bytes = rows_here > kTileRows / 2 ? kABytes : small_boxes * (kRowBox * kRowBytes);
+        if (FORM == kWeightGrad) row_bytes = kABytes;
+        else if (kWords) row_bytes = 0;
         const int cols = q.cols / CG;                     // columns that this CTA loads
         const int cb = static_cast<int>(x.rank) * cols;
         const uint32_t bytes = row_bytes + cols * kRowBytes;
@@ -307,8 +311,8 @@ __device__ __forceinline__ void load_operands(const Roles& x) {
                 bar_arrive_expect_tx<CG>(bar, bytes);
                 const int k0 = s * (FORM == kFp8 ? 128 : 64);
                 if (small_boxes == 0) {
-                    if (rows_here > 0) tma_load_2d<CG>(a, &x.maps.a, k0, q.row0 + my_m0, bar);
-                } else {
+                    if (!kWords && rows_here > 0) tma_load_2d<CG>(a, &x.maps.a, k0, q.row0 + my_m0, bar);
+                } else if (!kWords) {
                     for (int c = 0; c < small_boxes; ++c)
                         tma_load_2d<CG>(a + c * (kRowBox * kRowBytes), &x.maps.a_small, k0, q.row0 + my_m0 + c * kRowBox, bar);
                 }
@@ -397,6 +401,46 @@ __device__ __forceinline__ void multiply(const Roles& x) {
         // Given up: the products already issued still write tensor memory.
         tc_commit<CG>(&ctl.drained);
         for (int k = 0; k < (1 << 12) && !mbar_try_wait(&ctl.drained, 0); ++k) {
+        }
+    }
+}
+
+// Two warps: row operands whose rows are not 16 bytes apart (messages of some hidden sizes), in words of four bytes,
+// into the place and order in which a tensor-map load puts them.  A warp copies a row's 128 bytes at a time, several
+// rows in flight.
+template <int FORM>
+__device__ __forceinline__ void copy_rows(const Roles& x, int warp) {
+    const GemmParams& p = x.p;
+    const Table& t = x.t;
+    Control& ctl = x.ctl;
+    constexpr int kInFlight = FORM == kFp8 ? 8 : 16;  // its registers are fewer
+    const int row_bytes = p.contraction * (FORM == kFp8 ? 1 : 2);
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;
+    for (int tile = x.worker; ok && tile < ctl.tiles; tile += x.workers) {
+        const Tile q = decode<FORM, 1>(t, p, ctl, tile);
+        const int rows = min(kTileRows, q.rows - q.m0);
+        for (int s = 0; s < q.steps; ++s) {
+            ok = warp_wait(&ctl.empty[stage], phase ^ 1, &ctl.abort_flag, p.status);
+            if (!ok) break;
+            uint8_t* a = x.stages + stage * x.stage_bytes;
+            const int at = s * kRowBytes + lane_id() * 4;
+            const uint8_t* from = p.a_words + (static_cast<int64_t>(q.row0) + q.m0) * p.a_row_bytes + at;
+            for (int r0 = (warp - 2) * kInFlight; r0 < rows; r0 += 2 * kInFlight) {
+                uint32_t v[kInFlight];
+#pragma unroll
+                for (int i = 0; i < kInFlight; ++i)
+                    v[i] = r0 + i < rows && at < row_bytes ? *reinterpret_cast<const uint32_t*>(from + (r0 + i) * p.a_row_bytes) : 0;
+#pragma unroll
+                for (int i = 0; i < kInFlight; ++i) {
+                    const int r = r0 + i;  // the 16-byte pieces of a row lie exclusive-or'd with its number
+                    *reinterpret_cast<uint32_t*>(a + r * kRowBytes + (((lane_id() >> 2) ^ (r & 7)) << 4) + (lane_id() & 3) * 4) = v[i];
+                }
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane_id() == 0) bar_arrive<1>(smem_u32(&ctl.full[stage]));
+            if (++stage == static_cast<uint32_t>(x.num_stages)) stage = 0, phase ^= 1;
         }
     }
 }
@@ -552,7 +596,9 @@ __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
     }
 }
 
-template <int FORM, int CG>
+// kWords (single CTAs only): rows in words of four bytes, by two more warps.  A kernel of its own: its code in the
+// others took registers from the FP8 form's sums (334 to 414 us on messages of 64 experts).
+template <int FORM, int CG, bool kWords = false>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     grouped_gemm_kernel(const __grid_constant__ Maps maps, const GemmParams p) {
     extern __shared__ uint8_t raw[];
@@ -569,7 +615,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const uint32_t rank = CG == 1 ? 0 : cluster_rank();
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
-            mbar_init(&ctl.full[i], CG);
+            mbar_init(&ctl.full[i], CG + (kWords ? 2 : 0));
             mbar_init(&ctl.empty[i], 1);
             mbar_init(&ctl.tail_full[i], 1);
         }
@@ -601,11 +647,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (warp < 4) {
         if constexpr (kSums) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 0) {
-            if (elect_one()) load_operands<FORM, CG>(x);
+            if (elect_one()) load_operands<FORM, CG, kWords>(x);
         } else if (warp == 1) {
             if (rank == 0 && elect_one()) multiply<FORM, CG>(x);
         } else if (FORM == kWeightGrad && warp == 2) {
             zero_tails<FORM, CG>(x);
+        } else if (kWords) {
+            copy_rows<FORM>(x, warp);
         }
     } else {
         if constexpr (kSums) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
@@ -691,10 +739,14 @@ template <int FORM>
 ep_status launch(const ep_handle* h, const Operand& a, const Operand& a_small, const Operand& b, const Operand& b_small,
                  const GemmParams& p, int64_t rows_each, cudaStream_t stream) {
     Maps m;
-    ep_status st = encode(&m.a, a);
-    if (st == EP_OK) st = encode(&m.a_small, a_small);
-    if (st == EP_OK) st = encode(&m.b, b);
+    ep_status st = encode(&m.b, b);
     if (st == EP_OK) st = encode(&m.b_small, b_small);
+    if (p.a_words) {
+        m.a = m.a_small = m.b;  // not used
+    } else {
+        if (st == EP_OK) st = encode(&m.a, a);
+        if (st == EP_OK) st = encode(&m.a_small, a_small);
+    }
     if (st != EP_OK) return st;
     DeviceGuard guard(h->device);
     // A pair of CTAs computes 256 rows: each loads half of the weight tile, so that a row of products takes a
@@ -703,12 +755,15 @@ ep_status launch(const ep_handle* h, const Operand& a, const Operand& a_small, c
     // 4096 x 4096, single against pair: bf16 185 and 185 us at 128 rows an expert, 222 and 203 at 200, 1361 and
     // 1241 at 2048; FP8 106 and 125 at 128, 363 and 388 at 700, 567 and 557 at 1024, 1105 and 1034 at 2048.
     const int64_t pair_rows = FORM == kFp8 ? kPairRowsFp8 : kTileRows + 1;
-    const cudaError_t err =
-        rows_each >= pair_rows && h->plan.gemm_pairs > 0
-            ? launch_kernel(grouped_gemm_kernel<FORM, 2>, dim3(2 * h->plan.gemm_pairs), dim3(kGemmThreads), kMaxSmem, stream,
-                            2, m, p)
-            : launch_kernel(grouped_gemm_kernel<FORM, 1>, dim3(h->plan.num_sms), dim3(kGemmThreads), kMaxSmem, stream, 1,
-                            m, p);
+    cudaError_t err;
+    if (FORM != kWeightGrad && p.a_words)
+        err = launch_kernel(grouped_gemm_kernel<FORM, 1, FORM != kWeightGrad>, dim3(h->plan.num_sms), dim3(kGemmThreads),
+                            kMaxSmem, stream, 1, m, p);
+    else if (rows_each >= pair_rows && h->plan.gemm_pairs > 0)
+        err = launch_kernel(grouped_gemm_kernel<FORM, 2>, dim3(2 * h->plan.gemm_pairs), dim3(kGemmThreads), kMaxSmem, stream,
+                            2, m, p);
+    else
+        err = launch_kernel(grouped_gemm_kernel<FORM, 1>, dim3(h->plan.num_sms), dim3(kGemmThreads), kMaxSmem, stream, 1, m, p);
     if (err != cudaSuccess) return cuda_fail(err, "grouped product launch");
     return EP_OK;
 }
@@ -738,6 +793,23 @@ bool rows_aligned32(const void* p, int64_t row_bytes) {
     return (reinterpret_cast<uintptr_t>(p) & 31u) == 0 && row_bytes % 32 == 0;
 }
 
+// The operands of a product of rows; fills the rows' and the output's part of the parameters.
+ep_status check_rows(const void* x, int64_t x_row_bytes, int64_t x_least, const void* w, void* out, int64_t out_row_bytes,
+                     int32_t n, GemmParams* p) {
+    EP_CHECK_ARG(x && w && out && aligned4(x) && aligned16(w) && aligned16(out),
+                 "x must be a 4-byte, w and out 16-byte aligned device pointers");
+    EP_CHECK_ARG(x_row_bytes >= x_least && x_row_bytes % 4 == 0 && x_row_bytes < (INT64_C(1) << 40) &&
+                     row_stride_ok(out_row_bytes, 2 * static_cast<int64_t>(n)),
+                 "row strides must hold a row, in multiples of 4 (x %lld bytes) and 16 (out %lld)",
+                 static_cast<long long>(x_row_bytes), static_cast<long long>(out_row_bytes));
+    if (!aligned16(x) || x_row_bytes % 16 != 0) p->a_words = static_cast<const uint8_t*>(x);
+    p->a_row_bytes = x_row_bytes;
+    p->out = out;
+    p->out_row_bytes = out_row_bytes;
+    p->wide_stores = rows_aligned32(out, out_row_bytes);
+    return EP_OK;
+}
+
 }  // namespace
 
 template <int FORM>
@@ -745,6 +817,9 @@ cudaError_t plan_form(LaunchPlan* plan) {
     cudaError_t err = cudaFuncSetAttribute(grouped_gemm_kernel<FORM, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (err == cudaSuccess)
         err = cudaFuncSetAttribute(grouped_gemm_kernel<FORM, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (err == cudaSuccess && FORM != kWeightGrad)
+        err = cudaFuncSetAttribute(grouped_gemm_kernel<FORM, 1, FORM != kWeightGrad>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   kMaxSmem);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(plan->num_sms / 2 * 2);
@@ -789,17 +864,10 @@ ep_status ep_grouped_gemm(ep_handle* h, int64_t num_rows, int32_t n, int32_t k, 
     if (st != EP_OK) return st;
     EP_CHECK_ARG(expected_rows >= 0, "expected_rows %lld < 0", static_cast<long long>(expected_rows));
     if (num_rows == 0) return EP_OK;
-    EP_CHECK_ARG(x && w && out && aligned16(x) && aligned16(w) && aligned16(out),
-                 "x, w and out must be 16-byte aligned device pointers");
-    EP_CHECK_ARG(row_stride_ok(x_row_bytes, 2 * static_cast<int64_t>(k)) &&
-                     row_stride_ok(out_row_bytes, 2 * static_cast<int64_t>(n)),
-                 "row strides must be multiples of 16 that hold a row (x %lld, out %lld bytes)",
-                 static_cast<long long>(x_row_bytes), static_cast<long long>(out_row_bytes));
+    const ep_status rows = check_rows(x, x_row_bytes, 2 * static_cast<int64_t>(k), w, out, out_row_bytes, n, &p);
+    if (rows != EP_OK) return rows;
     p.cols_dim = n;
     p.contraction = k;
-    p.out = out;
-    p.out_row_bytes = out_row_bytes;
-    p.wide_stores = rows_aligned32(out, out_row_bytes);
     const int64_t rows_each = expected_rows ? expected_rows : num_rows / p.groups.groups;
     const int groups = p.groups.groups;
     const Operand a = row_operand(x, false, k, num_rows, x_row_bytes, kBox);
@@ -861,11 +929,8 @@ ep_status ep_grouped_gemm_fp8(ep_handle* h, int64_t num_rows, int32_t n, int32_t
     if (k % kFp8Group != 0) return fail(EP_ERR_UNSUPPORTED, "FP8 products need k %% 128 == 0 (k %d)", k);
     EP_CHECK_ARG(expected_rows >= 0, "expected_rows %lld < 0", static_cast<long long>(expected_rows));
     if (num_rows == 0) return EP_OK;
-    EP_CHECK_ARG(x && w && out && aligned16(x) && aligned16(w) && aligned16(out),
-                 "x, w and out must be 16-byte aligned device pointers");
-    EP_CHECK_ARG(row_stride_ok(x_row_bytes, k) && row_stride_ok(out_row_bytes, 2 * static_cast<int64_t>(n)),
-                 "row strides must be multiples of 16 that hold a row (x %lld, out %lld bytes)",
-                 static_cast<long long>(x_row_bytes), static_cast<long long>(out_row_bytes));
+    const ep_status rows = check_rows(x, x_row_bytes, k, w, out, out_row_bytes, n, &p);
+    if (rows != EP_OK) return rows;
     const int64_t scale_row = static_cast<int64_t>(k / kFp8Group) * (scales_ue8m0 ? 1 : 4);
     EP_CHECK_ARG(x_scales && w_scales && aligned4(w_scales) && x_scale_row_bytes >= scale_row &&
                      (scales_ue8m0 || (aligned4(x_scales) && x_scale_row_bytes % 4 == 0)),
@@ -873,9 +938,6 @@ ep_status ep_grouped_gemm_fp8(ep_handle* h, int64_t num_rows, int32_t n, int32_t
                  static_cast<long long>(x_scale_row_bytes));
     p.cols_dim = n;
     p.contraction = k;
-    p.out = out;
-    p.out_row_bytes = out_row_bytes;
-    p.wide_stores = rows_aligned32(out, out_row_bytes);
     p.x_scales = static_cast<const uint8_t*>(x_scales);
     p.x_scale_row_bytes = x_scale_row_bytes;
     p.scales_ue8m0 = scales_ue8m0 != 0;

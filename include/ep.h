@@ -416,7 +416,8 @@ ep_status ep_ll_dispatch_noalloc(int32_t num_ranks, int32_t num_tokens, int32_t 
  * overlap where a call writes their rows: if together they hold more rows than
  * there are, EP_ERR_CAPACITY is set and nothing is written.
  * Row operands and outputs have row strides in bytes: multiples of 16, base
- * 16-byte aligned.  n and k are multiples of 8.  Sums are fp32, rounded once.
+ * 16-byte aligned; the x of ep_grouped_gemm() and ep_grouped_gemm_fp8() may do
+ * with 4, at a lower speed.  n and k are multiples of 8.  Sums are fp32, rounded once.
  * NaN and infinities in a row reach that row's outputs only (a weight
  * gradient: its expert's). */
 

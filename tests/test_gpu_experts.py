@@ -227,6 +227,52 @@ def test_low_latency_messages_in_place(fmt):
         assert (out[r, j, c:] == 7.0).all()
 
 
+@pytest.mark.parametrize("counts", COUNTS, ids=lambda c: f"{len(c)}g{sum(c)}")
+@pytest.mark.parametrize("expected", [1, 100000], ids=["few", "many"])
+@pytest.mark.parametrize("n,k,pad,offset", [(72, 136, 2, 0), (520, 1032, 8, 2), (264, 72, 6, 6)])
+def test_rows_four_bytes_apart(counts, expected, n, k, pad, offset):
+    """Rows that are not 16 bytes apart, or do not begin at 16 bytes: the bits of the aligned call, both orientations."""
+    begin, rows = packed(counts, gap=1)
+    g = gen(k + pad)
+    flat = randn(g, (rows * (k + pad) + offset,))
+    x = flat[offset:].view(rows, k + pad)[:, :k]
+    h = handle(len(counts))
+    c, b = i32(counts), i32(begin)
+    for transposed in (False, True):
+        w = randn(g, (len(counts), k, n) if transposed else (len(counts), n, k), 0.1)
+        want, out = (torch.full((rows, n), 3.0, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        ep.ep_grouped_gemm(h, x.contiguous(), w, c, b, w_transposed=transposed, out=want, expected_rows=expected)
+        ep.ep_grouped_gemm(h, x, w, c, b, w_transposed=transposed, out=out, expected_rows=expected)
+        assert torch.equal(out, want)
+    h.check()
+
+
+@pytest.mark.parametrize("k", [128, 384, 2944])
+@pytest.mark.parametrize("ue8m0", [False, True])
+def test_fp8_messages_of_any_hidden_size(k, ue8m0):
+    """Message buffers whose size is no multiple of 16 bytes, read in place."""
+    R, EL, rows, n, G = 2, 3, 140, 136, k // 128
+    g = gen(k)
+    msgs = torch.zeros((R, EL, rows, 16 + k + 4 * G), dtype=torch.uint8, device=DEV)
+    msgs[..., 16:16 + k] = codes(g, (R, EL, rows, k)).view(torch.uint8)
+    if ue8m0:
+        msgs[..., 16 + k:16 + k + G] = torch.randint(117, 130, (R, EL, rows, G), generator=g, device=DEV).to(torch.uint8)
+    else:
+        msgs[..., 16 + k:] = (torch.rand((R, EL, rows, G), generator=g, device=DEV) + 0.1).view(torch.uint8)
+    px, scales, _ = ep.ll_views(msgs, k, True)
+    counts = [140, 0, 1, 129, 33, 64]
+    w, ws = codes(g, (6, n, k)), torch.rand((6, 2, G), generator=g, device=DEV) * 0.01
+    s = scales if ue8m0 else scales.view(torch.float32)
+    h = handle(6, R)
+    out = ep.ep_grouped_gemm_fp8(h, px, s, w, ws, i32(counts))
+    h.check()
+    for e, c in enumerate(counts):
+        r, j = divmod(e, EL)
+        xs = torch.exp2(scales[r, j, :c, :G].double() - 127) if ue8m0 else s[r, j, :c]
+        want, magnitude = fp8_reference(px[r, j, :c], xs, w[e], ws[e])
+        close(out[r, j, :c], want, magnitude, k)
+
+
 def test_strides_streams_and_repeats():
     """Strided rows in and out, a side stream, an SM cap: the same bits as the plain call, call after call."""
     counts = [3, 200, 0, 61]
@@ -702,8 +748,11 @@ def test_refusals():
     refused(1, "multiples of 8", g, h, bf(8, 64), bf(4, 12, 64), c, b)
     refused(1, "multiple of num_experts", g, h, bf(9, 64), bf(4, 64, 64), c)
     refused(1, "group_count", g, h, bf(8, 64), bf(4, 64, 64), None, b)
-    refused(1, "16-byte aligned", g, h, bf(8 * 64 + 4)[4:].view(8, 64), bf(4, 64, 64), c, b)
-    refused(1, "multiples of 16", g, h, bf(8, 68)[:, :64], bf(4, 64, 64), c, b)
+    refused(1, "4-byte", g, h, bf(8 * 64 + 1)[1:].view(8, 64), bf(4, 64, 64), c, b)
+    refused(1, "multiples of 4", g, h, bf(8, 65)[:, :64], bf(4, 64, 64), c, b)
+    refused(1, "16-byte aligned", g, h, bf(8, 64), bf(4 * 64 * 64 + 4)[4:].view(4, 64, 64), c, b)
+    refused(1, "multiples of 4", g, h, bf(8, 64), bf(4, 64, 64), c, b, out=bf(8, 68)[:, :64])
+    refused(1, "multiples of 16", ep.ep_grouped_gemm_wgrad, h, bf(8, 68)[:, :64], bf(8, 64), c, b)
     refused(1, "expected_rows", g, h, bf(8, 64), bf(4, 64, 64), c, b, expected_rows=-1)
     for bad in (bf(8, 72), f32(8, 64), torch.zeros((8, 64), dtype=torch.bfloat16)):
         with pytest.raises((TypeError, ValueError)):
