@@ -55,7 +55,10 @@ constexpr int kRowBytes = 128;      // bytes of one operand row in a stage (the 
 constexpr int kBox = 128;           // output elements (rows or columns) of a tensor-map load: 16 KB
 constexpr int kRowBox = 32;         // the same for a group's last rows: a short group loads few
 constexpr int kColBox = 64;         // the same for narrow tiles
-constexpr int kTileOverhead = 32;   // columns that a tile's width-independent cost is worth
+// Columns that a tile's width-independent cost is worth.  A single CTA's: 32 (64 and 128: decode steps 2 to 8 % slower).
+// A pair's: 256, the loads of its rows, since a pair's tiles of 128 columns wait for their operands (weight gradient of
+// 8 experts, 560 x 2448, 83592 rows: 401 us with 32, 257 with 128, 246 with 256).
+constexpr int tile_overhead(int ctas) { return ctas == 2 ? 256 : 32; }
 constexpr int kPairRowsFp8 = 1024;  // rows of a group from which the FP8 form runs on pairs of CTAs
 constexpr int kMaxStages = 12;
 constexpr int kEpilogueWarps = 8;
@@ -166,7 +169,7 @@ __device__ __forceinline__ void build_table(const Table& t, const GemmParams& p,
         int64_t best_cost = INT64_MAX;
         for (int cols = kMaxTileCols; cols >= kColBox * CG; cols >>= 1) {
             const int64_t tiles = static_cast<int64_t>(total) * ((p.cols_dim + cols - 1) / cols);
-            const int64_t cost = (tiles + workers - 1) / workers * (cols + kTileOverhead);
+            const int64_t cost = (tiles + workers - 1) / workers * (cols + tile_overhead(CG));
             if (cost < best_cost) best_cost = cost, best = cols;
         }
         ctl.tile_cols = best;
