@@ -55,15 +55,15 @@ constexpr int kRowBytes = 128;      // bytes of one operand row in a stage (the 
 constexpr int kBox = 128;           // output elements (rows or columns) of a tensor-map load: 16 KB
 constexpr int kRowBox = 32;         // the same for a group's last rows: a short group loads few
 constexpr int kColBox = 64;         // the same for narrow tiles
-// Columns that a tile's width-independent cost is worth.  A single CTA's: 32 (64 and 128: decode steps 2 to 8 % slower).
-// A pair's: 256, the loads of its rows, since a pair's tiles of 128 columns wait for their operands (weight gradient of
-// 8 experts, 560 x 2448, 83592 rows: 401 us with 32, 257 with 128, 246 with 256).
-constexpr int tile_overhead(int ctas) { return ctas == 2 ? 256 : 32; }
 constexpr int kPairRowsFp8 = 1024;  // rows of a group from which the FP8 form runs on pairs of CTAs
 constexpr int kMaxStages = 12;
 constexpr int kEpilogueWarps = 8;
 constexpr int kGemmThreads = (4 + kEpilogueWarps) * kWarpSize;  // warps 0 to 3 for loads and products: registers go by four warps
-constexpr int kControlBytes = 512;  // static shared memory
+constexpr int kControlBytes = 640;  // static shared memory
+constexpr uint32_t kOutBox = 32 * kRowBytes;  // a warp's results on their way out: 32 rows of 128 bytes
+// Of them a warp: in FP8 one for each 64 columns, since there a tile's stores hold up the next one's sums (2048 rows an
+// expert, 7168 x 2048: 1740 us with one, 1682 with two).
+constexpr int out_boxes(int form) { return form == kFp8 ? 2 : 1; }
 constexpr int kMaxSmem = 232448 - kControlBytes;
 
 struct GemmParams {
@@ -80,16 +80,35 @@ struct GemmParams {
     int32_t out_fp32;       // weight grad
     int32_t accumulate;     // weight grad
     int32_t wide_stores;    // output rows are 32-byte aligned
+    int32_t tile_overhead;  // columns that a tile's width-independent cost is worth
+    int32_t staged;         // whole blocks of 32 rows go out through shared memory
     int32_t a_chunked, b_chunked;  // operands read across: columns up to which loads of kBox reach (then kColBox)
     const uint8_t* a_words;        // rows that no tensor map can describe (not 16 bytes apart), or NULL
     int64_t a_row_bytes;
     int32_t* status;
 };
 
-// Tensor maps of the two operands: loads of kBox output elements, and smaller ones.
+// Tensor maps of the two operands: loads of kBox output elements, and smaller ones; and of the results, 32 rows by
+// 128 bytes.
 struct Maps {
-    CUtensorMap a, a_small, b, b_small;
+    CUtensorMap a, a_small, b, b_small, out;
 };
+
+// Where a warp's 32 rows of a tile go: the output row of the first (weight grad: in the group), how many of them exist,
+// the first column.
+struct alignas(16) Place {
+    int row, col, group;
+    short rows, cols;
+};
+static_assert(sizeof(Place) == 16 && alignof(Place) == 16, "read as one vector");
+
+// Read where it is used (a plain read could be made early and kept in registers).
+__device__ __forceinline__ Place read_place(const Place* from) {
+    int4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(smem_u32(from)) : "memory");
+    return {v.x, v.y, v.z, static_cast<short>(v.w & 0xffff), static_cast<short>(v.w >> 16)};
+}
 
 struct Control {
     uint64_t full[kMaxStages];
@@ -102,6 +121,7 @@ struct Control {
     int32_t abort_flag;
     int64_t warp_sums[kGemmThreads / kWarpSize];
     int32_t tiles, col_tiles, tile_cols;  // output tiles in all, tiles across, columns of one
+    Place at[kEpilogueWarps];             // forms with segments: of the tile that a warp is adding up
 };
 static_assert(sizeof(Control) <= kControlBytes, "control block");
 
@@ -163,13 +183,13 @@ __device__ __forceinline__ void build_table(const Table& t, const GemmParams& p,
         const int total = overlap ? 0 : static_cast<int>(row_tiles);
         t.before[groups] = total;
         // Tile width: the one whose waves over the CTAs take the least time, a wave costing its columns plus
-        // what a tile costs at any width (its rows' loads, its turn).
+        // what a tile costs at any width.
         const int workers = gridDim.x / CG;
         int best = kMaxTileCols;
         int64_t best_cost = INT64_MAX;
         for (int cols = kMaxTileCols; cols >= kColBox * CG; cols >>= 1) {
             const int64_t tiles = static_cast<int64_t>(total) * ((p.cols_dim + cols - 1) / cols);
-            const int64_t cost = (tiles + workers - 1) / workers * (cols + tile_overhead(CG));
+            const int64_t cost = (tiles + workers - 1) / workers * (cols + p.tile_overhead);
             if (cost < best_cost) best_cost = cost, best = cols;
         }
         ctl.tile_cols = best;
@@ -237,10 +257,6 @@ __device__ __forceinline__ void store_fp32(uint8_t* row, int col, int cols, cons
     }
 }
 
-__device__ __forceinline__ uint8_t* out_row(const GemmParams& p, int64_t row) {
-    return static_cast<uint8_t*>(p.out) + row * p.out_row_bytes;
-}
-
 // What a CTA's roles share.
 struct Roles {
     const Maps& maps;
@@ -248,6 +264,7 @@ struct Roles {
     const Table& t;
     Control& ctl;
     uint8_t* stages;
+    uint8_t* boxes;
     uint32_t tmem, rank, stage_bytes;  // rank: of the CTA in its pair
     int num_stages, worker, workers;
 };
@@ -479,6 +496,57 @@ __device__ __forceinline__ void zero_tails(const Roles& x) {
     }
 }
 
+// 32 columns of a lane's row, rounded to bf16, into the first or second half of its warp's box of 32 rows by 64
+// columns; 16-byte pieces lie exclusive-or'd with the row's number.
+__device__ __forceinline__ void box_columns(uint32_t box, int second, const float (&v)[32]) {
+    const uint32_t row = box + lane_id() * kRowBytes;
+    const uint32_t turn = lane_id() & 7;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = pack_bf16(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
+        st_shared_v4(row + (((second * 4 + j) ^ turn) << 4), w);
+    }
+}
+
+// 32 columns of a warp's rows, from column `c` of its part of the tile.  Staged: whole blocks of 32 rows go through the
+// warp's boxes in shared memory, 64 columns at a time (the map leaves out what lies past the last column).  The ends of
+// groups and tiles of 64 columns go by stores of each lane.
+template <int FORM>
+__device__ __forceinline__ void put_columns(const Roles& x, uint32_t box, const Place& at, int c, const float (&v)[32]) {
+    const GemmParams& p = x.p;
+    const int col = at.col + c;
+    if (FORM != kWeightGrad && p.staged && at.cols >= 64 && at.rows == 32) {
+        constexpr int kBoxes = out_boxes(FORM);
+        const int second = (c >> 5) & 1;
+        const int first_col = col - 32 * second;
+        box += (c >> 6 & (kBoxes - 1)) * kOutBox;
+        if (first_col < p.cols_dim) {
+            if (!second) {  // the last copy out of this box has read it: boxes take turns
+                if (lane_id() == 0) bulk_wait_read<kBoxes - 1>();
+                __syncwarp();
+            }
+            box_columns(box, second, v);
+        }
+        if (!second) return;
+        fence_async_smem();
+        __syncwarp();
+        if (lane_id() == 0) {
+            if (first_col < p.cols_dim) tma_store_2d(&x.maps.out, box, first_col, at.row);
+            bulk_commit();                                   // empty past the last column: a turn all the same
+            if (kBoxes == 2 && at.cols == 64) bulk_commit();  // the second box's
+        }
+    } else if (lane_id() < at.rows && col < p.cols_dim) {
+        const int64_t row = (FORM == kWeightGrad ? static_cast<int64_t>(at.group) * p.rows_dim : 0) + at.row + lane_id();
+        uint8_t* out = static_cast<uint8_t*>(p.out) + row * p.out_row_bytes;
+        if (FORM == kWeightGrad && p.out_fp32)
+            store_fp32(out, col, p.cols_dim, v, p.accumulate != 0, p.wide_stores != 0);
+        else
+            store_bf16(out, col, p.cols_dim, v, p.wide_stores != 0);
+    }
+}
+
 // Eight warps: accumulators to the output.
 template <int FORM, int CG>
 __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
@@ -491,16 +559,17 @@ __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
     const int half = w >> 2;                    // which half of the tile's columns
     const uint32_t lane_base = x.tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t acc_empty0 = CG == 1 ? smem_u32(ctl.acc_empty) : cluster_addr(ctl.acc_empty, 0);
+    const uint32_t box = smem_u32(x.boxes) + w * (out_boxes(FORM) * kOutBox);
     int buf = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
     for (int tile = x.worker; ok && tile < ctl.tiles; tile += x.workers) {
         const Tile q = decode<FORM, CG>(t, p, ctl, tile);
         const int cols_half = q.cols / 2;
-        const int row = q.m0 + static_cast<int>(x.rank) * kTileRows + quarter * 32 + lane_id();  // in the group
-        const int col0 = q.n0 + half * cols_half;
-        const bool row_ok = row < (FORM == kWeightGrad ? p.rows_dim : q.rows);
-        const int64_t out_at = (FORM == kWeightGrad ? static_cast<int64_t>(q.group) * p.rows_dim : q.row0) + static_cast<int64_t>(row);
+        const int in_group = q.m0 + static_cast<int>(x.rank) * kTileRows + quarter * 32;
+        const int rows = min(32, max(0, (FORM == kWeightGrad ? p.rows_dim : q.rows) - in_group));
+        const Place at = {(FORM == kWeightGrad ? 0 : q.row0) + in_group, q.n0 + half * cols_half, q.group,
+                          static_cast<short>(rows), static_cast<short>(cols_half)};
         if constexpr (kSegment == 0) {
             ok = warp_wait(&ctl.acc_full[buf], acc_phase, &ctl.abort_flag, p.status);
             if (!ok) break;
@@ -518,19 +587,20 @@ __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
                 float v[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
-                if (row_ok && col0 + c < p.cols_dim)
-                    store_bf16(out_row(p, out_at), col0 + c, p.cols_dim, v, p.wide_stores != 0);
+                put_columns<FORM>(x, box, at, c, v);
             }
             buf ^= 1;
             acc_phase ^= buf == 0;
         } else {
             // The sums of a segment arrive in an accumulator of their own and are added up here, 128 columns a
-            // thread at most; in FP8 a segment is a block of 128 with its own scales.
+            // thread at most; in FP8 a segment is a block of 128 with its own scales.  Meanwhile the tile's place
+            // lies in shared memory: there are no registers for it.
             uint64_t acc[2][32];  // pairs of fp32
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) acc[c][i] = 0;
+            if (lane_id() == 0) ctl.at[w] = at;
             const int segments = (q.steps + kSegment - 1) / kSegment;
             // A block's scales are loaded a block before they are used, and only then looked at: a
             // multiplication next to the loads would wait for them.
@@ -539,26 +609,27 @@ __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
             uint32_t x_next = 0;
             float w_next = 0.0f;
             if constexpr (FORM == kFp8) {
-                xs = p.x_scales + (static_cast<int64_t>(q.row0) + min(row, q.rows - 1)) * p.x_scale_row_bytes;
-                const int nb = min(col0, p.cols_dim - 1) >> 7;
+                xs = p.x_scales + (static_cast<int64_t>(q.row0) + min(in_group + lane_id(), q.rows - 1)) * p.x_scale_row_bytes;
+                const int nb = min(at.col, p.cols_dim - 1) >> 7;
                 ws = p.w_scales + (static_cast<int64_t>(q.group) * ((p.cols_dim + 127) >> 7) + nb) * q.steps;
                 x_next = raw_scale(xs, 0, p.scales_ue8m0);
                 w_next = ws[0];
             }
 #pragma unroll 1
-            for (int s = 0; s < segments; ++s) {
+            for (int left = segments; left > 0; --left) {
                 ok = warp_wait(&ctl.acc_full[buf], acc_phase, &ctl.abort_flag, p.status);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t at = lane_base + buf * kMaxTileCols + half * cols_half;
+                const uint32_t from = lane_base + buf * kMaxTileCols + half * cols_half;
                 uint32_t u[64];
-                tc_ld64(at, u);
+                tc_ld64(from, u);
                 float f = 1.0f;
                 if constexpr (FORM == kFp8) {  // while the load is on its way
                     f = scale_value(x_next, p.scales_ue8m0) * w_next;
-                    if (s + 1 < segments) {
-                        x_next = raw_scale(xs, s + 1, p.scales_ue8m0);
-                        w_next = ws[s + 1];
+                    if (left > 1) {
+                        xs += p.scales_ue8m0 ? 1 : 4;
+                        x_next = raw_scale(xs, 0, p.scales_ue8m0);
+                        w_next = *++ws;
                     }
                 }
                 const uint64_t scale = pack_f32x2(__float_as_uint(f), __float_as_uint(f));
@@ -573,30 +644,31 @@ __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) fma_f32x2(acc[c][i], pack_f32x2(u[2 * i], u[2 * i + 1]), scale);
                     if (cols_half <= 64) break;
-                    if (c == 0) tc_ld64(at + 64, u);
+                    if (c == 0) tc_ld64(from + 64, u);
                 }
                 buf ^= 1;
                 acc_phase ^= buf == 0;
             }
-            if (ok && row_ok) {
+            __syncwarp();
+            if (!ok) break;
+            const Place to = read_place(&ctl.at[w]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (c * 32 < cols_half && col0 + c * 32 < p.cols_dim) {
-                        float v[32];
+            for (int c = 0; c < 4; ++c) {
+                if (32 * c >= to.cols) break;
+                float v[32];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const uint64_t pair = acc[c / 2][c % 2 * 16 + i];
-                            v[2 * i] = __uint_as_float(static_cast<uint32_t>(pair));
-                            v[2 * i + 1] = __uint_as_float(static_cast<uint32_t>(pair >> 32));
-                        }
-                        if (FORM == kWeightGrad && p.out_fp32)
-                            store_fp32(out_row(p, out_at), col0 + c * 32, p.cols_dim, v, p.accumulate != 0, p.wide_stores != 0);
-                        else
-                            store_bf16(out_row(p, out_at), col0 + c * 32, p.cols_dim, v, p.wide_stores != 0);
-                    }
+                for (int i = 0; i < 16; ++i) {
+                    const uint64_t pair = acc[c / 2][c % 2 * 16 + i];
+                    v[2 * i] = __uint_as_float(static_cast<uint32_t>(pair));
+                    v[2 * i + 1] = __uint_as_float(static_cast<uint32_t>(pair >> 32));
+                }
+                put_columns<FORM>(x, box, to, 32 * c, v);
             }
+            __syncwarp();  // the place has been read
         }
     }
+    if (lane_id() == 0) bulk_wait_all();
+    __syncwarp();
 }
 
 // kWords (single CTAs only): rows in words of four bytes, by two more warps.  A kernel of its own: its code in the
@@ -612,7 +684,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     t.count = t.before + p.groups.groups + 1;
     t.begin = t.count + p.groups.groups;
     const uint32_t table_end = (4u * (3u * p.groups.groups + 1u) + 1023u) & ~1023u;
-    uint8_t* const stages = smem + table_end;
+    uint8_t* const boxes = smem + table_end;
+    const uint32_t out_bytes = p.staged ? kEpilogueWarps * out_boxes(FORM) * kOutBox : 0;
+    uint8_t* const stages = boxes + out_bytes;
 
     const int warp = threadIdx.x / kWarpSize;
     const uint32_t rank = CG == 1 ? 0 : cluster_rank();
@@ -641,8 +715,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     tc_fence_after();
 
     const uint32_t stage_bytes = kABytes + ctl.tile_cols / CG * kRowBytes;
-    const Roles x = {maps, p, t, ctl, stages, ctl.tmem, rank, stage_bytes,
-                     min(kMaxStages, static_cast<int>((kMaxSmem - 1024u - table_end) / stage_bytes)),
+    const Roles x = {maps, p, t, ctl, stages, boxes, ctl.tmem, rank, stage_bytes,
+                     min(kMaxStages, static_cast<int>((kMaxSmem - 1024u - table_end - out_bytes) / stage_bytes)),
                      static_cast<int>(blockIdx.x / CG), static_cast<int>(gridDim.x / CG)};
     // Forms with segments hold 128 sums a thread in their eight epilogue warps: registers move there from the
     // others (72 + 2 * 216 = 3 * 168, what the block was launched with).
@@ -738,12 +812,34 @@ Operand weight_across_operand(const void* base, uint64_t inner, uint64_t rows, u
     return {base, false, 4, {64, rows, inner / 64, groups}, {row, 128, row * rows}, {64, 64, chunks, 1}};
 }
 
+// Whether results go out through shared memory (whole blocks of 32 rows): tensor-map stores of 4 KB take a warp less time
+// than its lanes' stores of 32 bytes, or of 16 where rows are not 32 bytes aligned, but cost operand stages.  In bf16 the
+// stores run under the next tile's products and only short tiles wait for them; in FP8 its sums always do.  Measured
+// without and with, 64 experts of 1024 rows, bf16, k 256, 512, 1024, 2048: 172 and 138 us, 224 and 215, 356 and 366, 658 and
+// 674 for n = 4096; 320 and 163, 295 and 254, 408 and 387, 702 and 700 for n = 4104.  FP8, k 512, 2048, 7168, n = 4096:
+// 32 experts of 2048 rows (pairs) 258 and 213, 553 and 495, 1519 and 1475; 64 of 700 (single CTAs) 183 and 153, 412 and 387,
+// 1143 and 1156; 64 of 128 52 and 45, 114 and 114, 329 and 342 (k 4096: 202 and 207, 727 and 707 of 700).
+bool staged_pays(bool fp8, bool pairs, const GemmParams& p, int64_t rows_each) {
+    if (!fp8) return !p.wide_stores || p.contraction <= 512;
+    return pairs || p.contraction <= (rows_each > 2 * kTileRows ? 4096 : 2048);
+}
+
 template <int FORM>
 ep_status launch(const ep_handle* h, const Operand& a, const Operand& a_small, const Operand& b, const Operand& b_small,
-                 const GemmParams& p, int64_t rows_each, cudaStream_t stream) {
+                 GemmParams p, int64_t rows_each, cudaStream_t stream) {
     Maps m;
+    const bool pairs = !p.a_words && rows_each >= (FORM == kFp8 ? kPairRowsFp8 : kTileRows + 1) && h->plan.gemm_pairs > 0;
+    // A single CTA's: 32 (64 and 128: decode steps 2 to 8 % slower).  A pair's: 256, the loads of its rows, since a pair's
+    // tiles of 128 columns wait for their operands (weight gradient of 8 experts, 560 x 2448, 83592 rows: 401 us with 32,
+    // 257 with 128, 246 with 256).
+    p.tile_overhead = pairs ? 2 * kTileRows : 32;
+    p.staged = FORM != kWeightGrad && rows_each >= kRowBox && staged_pays(FORM == kFp8, pairs, p, rows_each);
     ep_status st = encode(&m.b, b);
     if (st == EP_OK) st = encode(&m.b_small, b_small);
+    m.out = m.b;  // not used
+    if (st == EP_OK && p.staged)
+        st = encode(&m.out, {p.out, false, 2, {static_cast<uint64_t>(p.cols_dim), static_cast<uint64_t>(p.groups.num_rows), 1, 1},
+                             {static_cast<uint64_t>(p.out_row_bytes), 0, 0}, {64, 32, 1, 1}});
     if (p.a_words) {
         m.a = m.a_small = m.b;  // not used
     } else {
@@ -757,12 +853,11 @@ ep_status launch(const ep_handle* h, const Operand& a, const Operand& a_small, c
     // FP8, where a block's sums wait for both CTAs of a pair, single CTAs up to 1024 rows.  Measured at 32 experts,
     // 4096 x 4096, single against pair: bf16 185 and 185 us at 128 rows an expert, 222 and 203 at 200, 1361 and
     // 1241 at 2048; FP8 106 and 125 at 128, 363 and 388 at 700, 567 and 557 at 1024, 1105 and 1034 at 2048.
-    const int64_t pair_rows = FORM == kFp8 ? kPairRowsFp8 : kTileRows + 1;
     cudaError_t err;
     if (FORM != kWeightGrad && p.a_words)
         err = launch_kernel(grouped_gemm_kernel<FORM, 1, FORM != kWeightGrad>, dim3(h->plan.num_sms), dim3(kGemmThreads),
                             kMaxSmem, stream, 1, m, p);
-    else if (rows_each >= pair_rows && h->plan.gemm_pairs > 0)
+    else if (pairs)
         err = launch_kernel(grouped_gemm_kernel<FORM, 2>, dim3(2 * h->plan.gemm_pairs), dim3(kGemmThreads), kMaxSmem, stream,
                             2, m, p);
     else

@@ -247,6 +247,49 @@ def test_rows_four_bytes_apart(counts, expected, n, k, pad, offset):
     h.check()
 
 
+@pytest.mark.parametrize("expected", [40, 300, 100000])  # single CTAs, pairs in bf16, pairs in both
+@pytest.mark.parametrize("n,pad", [(8, 0), (72, 8), (136, 24), (264, 0), (200, 56)])
+@pytest.mark.parametrize("form", ["forward", "transposed", "fp8"])
+def test_many_tiles_a_cta(expected, n, pad, form):
+    """Whole and ragged blocks of rows in turn, several tiles a CTA, rows of the result apart: against 64 bits, nothing
+    written beside the result, and the bits of the call that expects few rows."""
+    counts, k = [33, 0, 64, 30011, 31, 1, 1300], 256
+    E = len(counts)
+    begin, rows = packed(counts, gap=2)
+    g = gen(n + expected)
+    h = handle(E)
+    c, b = i32(counts), i32(begin)
+    if form == "fp8":
+        x, w = codes(g, (rows, k)), codes(g, (E, n, k))
+        xs = torch.rand((rows, k // 128), generator=g, device=DEV) + 0.01
+        ws = torch.rand((E, -(-n // 128), k // 128), generator=g, device=DEV) * 0.01
+    else:
+        x, w = randn(g, (rows, k)), randn(g, (E, k, n) if form == "transposed" else (E, n, k), 0.1)
+
+    def run(expect):
+        out = Guarded((rows, n + pad), torch.bfloat16)
+        if form == "fp8":
+            ep.ep_grouped_gemm_fp8(h, x, xs, w, ws, c, b, out=out.t[:, :n], expected_rows=expect)
+        else:
+            ep.ep_grouped_gemm(h, x, w, c, b, w_transposed=form == "transposed", out=out.t[:, :n], expected_rows=expect)
+        h.check()
+        out.check()
+        assert (out.t[:, n:].contiguous().view(torch.uint8) == out.fill).all()
+        return out
+    out = run(expected)
+    used = torch.zeros(rows, dtype=torch.bool, device=DEV)
+    for e, (at, m) in enumerate(zip(begin, counts)):
+        used[at:at + m] = True
+        if form == "fp8":
+            want, magnitude = fp8_reference(x[at:at + m], xs[at:at + m], w[e], ws[e])
+        else:
+            we, xe = w[e].double() if form == "transposed" else w[e].double().t(), x[at:at + m].double()
+            want, magnitude = xe @ we, xe.abs() @ we.abs()
+        close(out.t[at:at + m, :n], want, magnitude, k)
+    assert (out.t[~used].view(torch.uint8) == out.fill).all(), "a row outside every group was written"
+    assert torch.equal(run(1).t.view(torch.int16), out.t.view(torch.int16))
+
+
 @pytest.mark.parametrize("k", [128, 384, 2944])
 @pytest.mark.parametrize("ue8m0", [False, True])
 def test_fp8_messages_of_any_hidden_size(k, ue8m0):
