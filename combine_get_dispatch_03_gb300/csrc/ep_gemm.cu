@@ -829,10 +829,15 @@ ep_status launch(const ep_handle* h, const Operand& a, const Operand& a_small, c
                  GemmParams p, int64_t rows_each, cudaStream_t stream) {
     Maps m;
     const bool pairs = !p.a_words && rows_each >= (FORM == kFp8 ? kPairRowsFp8 : kTileRows + 1) && h->plan.gemm_pairs > 0;
-    // A single CTA's: 32 (64 and 128: decode steps 2 to 8 % slower).  A pair's: 256, the loads of its rows, since a pair's
-    // tiles of 128 columns wait for their operands (weight gradient of 8 experts, 560 x 2448, 83592 rows: 401 us with 32,
-    // 257 with 128, 246 with 256).
-    p.tile_overhead = pairs ? 2 * kTileRows : 32;
+    // A tile's stages wait for their operands, and a tile is worth the rows that a CTA loads beside its columns: a pair's
+    // 128 beside half of the columns (weight gradient of 8 experts, 560 x 2448, 83592 rows: 401 us with 32 columns'
+    // worth, 257 with 128, 246 with 256), a single CTA's as many as a group's tiles have, at least one load's (FP8, 64
+    // experts, 1560 x 7168, against always 32: 256 rows an expert 311 and 233 us, 512 550 and 396, 100 163 and 147; always
+    // 128: decode steps up to 8 % slower).
+    const int64_t row_tiles = (rows_each + kTileRows - 1) / kTileRows;
+    p.tile_overhead = pairs                 ? 2 * kTileRows
+                      : FORM == kWeightGrad ? kTileRows
+                                            : static_cast<int32_t>(rows_each < kRowBox ? kRowBox : rows_each / row_tiles);
     p.staged = FORM != kWeightGrad && rows_each >= kRowBox && staged_pays(FORM == kFp8, pairs, p, rows_each);
     ep_status st = encode(&m.b, b);
     if (st == EP_OK) st = encode(&m.b_small, b_small);
