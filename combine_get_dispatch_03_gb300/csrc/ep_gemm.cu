@@ -78,18 +78,18 @@ struct GemmParams {
     const float* w_scales;
     int32_t scales_ue8m0;
     int32_t out_fp32;       // weight grad
-    int32_t accumulate;     // weight grad
+    int32_t accumulate;     // weight grad: then staged
     int32_t wide_stores;    // output rows are 32-byte aligned
     int32_t tile_overhead;  // columns that a tile's width-independent cost is worth
-    int32_t staged;         // whole blocks of 32 rows go out through shared memory
+    int32_t staged;         // blocks of 32 rows go out through shared memory
     int32_t a_chunked, b_chunked;  // operands read across: columns up to which loads of kBox reach (then kColBox)
     const uint8_t* a_words;        // rows that no tensor map can describe (not 16 bytes apart), or NULL
     int64_t a_row_bytes;
     int32_t* status;
 };
 
-// Tensor maps of the two operands: loads of kBox output elements, and smaller ones; and of the results, 32 rows by
-// 128 bytes.
+// Tensor maps of the two operands: loads of kBox output elements, and smaller ones; and of the results, boxes of 32
+// rows by 128 bytes.
 struct Maps {
     CUtensorMap a, a_small, b, b_small, out;
 };
@@ -230,21 +230,16 @@ __device__ __forceinline__ void store_bf16(uint8_t* row, int col, int cols, cons
     }
 }
 
-// The same in fp32, optionally added to what is there.
-__device__ __forceinline__ void store_fp32(uint8_t* row, int col, int cols, const float (&v)[32], bool accumulate, bool wide) {
+// The same in fp32.
+__device__ __forceinline__ void store_fp32(uint8_t* row, int col, int cols, const float (&v)[32], bool wide) {
     float* p = reinterpret_cast<float*>(row) + col;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if (col + 8 * i + 8 > cols) break;
         float4 q[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < 2; ++j)
             q[j] = make_float4(v[8 * i + 4 * j], v[8 * i + 4 * j + 1], v[8 * i + 4 * j + 2], v[8 * i + 4 * j + 3]);
-            if (accumulate) {
-                const float4 o = *reinterpret_cast<const float4*>(p + 8 * i + 4 * j);
-                q[j] = make_float4(q[j].x + o.x, q[j].y + o.y, q[j].z + o.z, q[j].w + o.w);
-            }
-        }
         if (wide) {
             const uint32_t w[8] = {__float_as_uint(q[0].x), __float_as_uint(q[0].y), __float_as_uint(q[0].z),
                                    __float_as_uint(q[0].w), __float_as_uint(q[1].x), __float_as_uint(q[1].y),
@@ -510,14 +505,38 @@ __device__ __forceinline__ void box_columns(uint32_t box, int second, const floa
     }
 }
 
+// 32 fp32 columns of a lane's row into its warp's box of 32 rows by 32 columns.
+__device__ __forceinline__ void box_columns_fp32(uint32_t box, const float (&v)[32]) {
+    const uint32_t row = box + lane_id() * kRowBytes;
+    const uint32_t turn = lane_id() & 7;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t w[4] = {__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),
+                               __float_as_uint(v[4 * j + 3])};
+        st_shared_v4(row + ((j ^ turn) << 4), w);
+    }
+}
+
 // 32 columns of a warp's rows, from column `c` of its part of the tile.  Staged: whole blocks of 32 rows go through the
-// warp's boxes in shared memory, 64 columns at a time (the map leaves out what lies past the last column).  The ends of
-// groups and tiles of 64 columns go by stores of each lane.
+// warp's boxes in shared memory, 128 bytes of columns at a time (the map leaves out what lies past the last column, and
+// in the weight gradient past the last row).  The ends of groups and tiles of 64 columns go by stores of each lane.
 template <int FORM>
 __device__ __forceinline__ void put_columns(const Roles& x, uint32_t box, const Place& at, int c, const float (&v)[32]) {
     const GemmParams& p = x.p;
     const int col = at.col + c;
-    if (FORM != kWeightGrad && p.staged && at.cols >= 64 && at.rows == 32) {
+    if (FORM == kWeightGrad && p.staged) {
+        if (at.rows == 0 || col >= p.cols_dim) return;
+        if (lane_id() == 0) bulk_wait_read<0>();
+        __syncwarp();
+        box_columns_fp32(box, v);
+        fence_async_smem();
+        __syncwarp();
+        if (lane_id() == 0) {
+            if (p.accumulate) tma_add_3d(&x.maps.out, box, col, at.row, at.group);
+            else tma_store_3d(&x.maps.out, box, col, at.row, at.group);
+            bulk_commit();
+        }
+    } else if (FORM != kWeightGrad && p.staged && at.cols >= 64 && at.rows == 32) {
         constexpr int kBoxes = out_boxes(FORM);
         const int second = (c >> 5) & 1;
         const int first_col = col - 32 * second;
@@ -541,7 +560,7 @@ __device__ __forceinline__ void put_columns(const Roles& x, uint32_t box, const 
         const int64_t row = (FORM == kWeightGrad ? static_cast<int64_t>(at.group) * p.rows_dim : 0) + at.row + lane_id();
         uint8_t* out = static_cast<uint8_t*>(p.out) + row * p.out_row_bytes;
         if (FORM == kWeightGrad && p.out_fp32)
-            store_fp32(out, col, p.cols_dim, v, p.accumulate != 0, p.wide_stores != 0);
+            store_fp32(out, col, p.cols_dim, v, p.wide_stores != 0);
         else
             store_bf16(out, col, p.cols_dim, v, p.wide_stores != 0);
     }
@@ -565,6 +584,7 @@ __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
     bool ok = true;
     for (int tile = x.worker; ok && tile < ctl.tiles; tile += x.workers) {
         const Tile q = decode<FORM, CG>(t, p, ctl, tile);
+        if (FORM == kWeightGrad && p.accumulate && q.steps == 0) continue;  // nothing to add
         const int cols_half = q.cols / 2;
         const int in_group = q.m0 + static_cast<int>(x.rank) * kTileRows + quarter * 32;
         const int rows = min(32, max(0, (FORM == kWeightGrad ? p.rows_dim : q.rows) - in_group));
@@ -761,9 +781,11 @@ PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
     return fn;
 }
 
+enum class Element { kBf16, kFp8, kFp32 };
+
 struct Operand {
     const void* base;
-    bool fp8;
+    Element element;
     int dims;
     uint64_t size[4];
     uint64_t stride[3];  // bytes
@@ -777,7 +799,10 @@ ep_status encode(CUtensorMap* map, const Operand& o) {
     cuuint32_t box[4], step[4] = {1, 1, 1, 1};
     for (int i = 0; i < 4; ++i) size[i] = o.size[i], box[i] = o.box[i];
     for (int i = 0; i < 3; ++i) stride[i] = o.stride[i];
-    const CUresult rc = fn(map, o.fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, o.dims,
+    const CUtensorMapDataType type = o.element == Element::kFp8    ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : o.element == Element::kFp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                                                   : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUresult rc = fn(map, type, o.dims,
                            const_cast<void*>(o.base), size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -787,7 +812,7 @@ ep_status encode(CUtensorMap* map, const Operand& o) {
 
 // Rows [rows][inner] with a row stride.
 Operand row_operand(const void* base, bool fp8, uint64_t inner, uint64_t rows, uint64_t row_bytes, uint32_t box_rows) {
-    return {base, fp8, 2, {inner, rows, 1, 1}, {row_bytes, 0, 0}, {fp8 ? 128u : 64u, box_rows, 1, 1}};
+    return {base, fp8 ? Element::kFp8 : Element::kBf16, 2, {inner, rows, 1, 1}, {row_bytes, 0, 0}, {fp8 ? 128u : 64u, box_rows, 1, 1}};
 }
 
 // The same rows read across, 64 columns by 64 rows; `chunks` of 64 columns in one load.  With more than one, a chunk
@@ -797,30 +822,41 @@ int chunked_columns(int inner) { return inner >= kBox ? inner / 64 * 64 : 0; }
 
 Operand across_operand(const void* base, uint64_t inner, uint64_t rows, uint64_t row_bytes, uint32_t chunks) {
     if (chunks == 1) return row_operand(base, false, inner, rows, row_bytes, 64);
-    return {base, false, 3, {64, rows, inner / 64, 1}, {row_bytes, 128, 0}, {64, 64, chunks, 1}};
+    return {base, Element::kBf16, 3, {64, rows, inner / 64, 1}, {row_bytes, 128, 0}, {64, 64, chunks, 1}};
 }
 
 // Weights [groups][rows][inner], contiguous.
 Operand weight_operand(const void* base, bool fp8, uint64_t inner, uint64_t rows, uint64_t groups, uint32_t box_rows) {
     const uint64_t row = inner * (fp8 ? 1 : 2);
-    return {base, fp8, 3, {inner, rows, groups, 1}, {row, row * rows, 0}, {fp8 ? 128u : 64u, box_rows, 1, 1}};
+    return {base, fp8 ? Element::kFp8 : Element::kBf16, 3, {inner, rows, groups, 1}, {row, row * rows, 0}, {fp8 ? 128u : 64u, box_rows, 1, 1}};
 }
 
 Operand weight_across_operand(const void* base, uint64_t inner, uint64_t rows, uint64_t groups, uint32_t chunks) {
     if (chunks == 1) return weight_operand(base, false, inner, rows, groups, 64);
     const uint64_t row = inner * 2;
-    return {base, false, 4, {64, rows, inner / 64, groups}, {row, 128, row * rows}, {64, 64, chunks, 1}};
+    return {base, Element::kBf16, 4, {64, rows, inner / 64, groups}, {row, 128, row * rows}, {64, 64, chunks, 1}};
 }
 
-// Whether results go out through shared memory (whole blocks of 32 rows): tensor-map stores of 4 KB take a warp less time
-// than its lanes' stores of 32 bytes, or of 16 where rows are not 32 bytes aligned, but cost operand stages.  In bf16 the
-// stores run under the next tile's products and only short tiles wait for them; in FP8 its sums always do.  Measured
-// without and with, 64 experts of 1024 rows, bf16, k 256, 512, 1024, 2048: 172 and 138 us, 224 and 215, 356 and 366, 658 and
-// 674 for n = 4096; 320 and 163, 295 and 254, 408 and 387, 702 and 700 for n = 4104.  FP8, k 512, 2048, 7168, n = 4096:
-// 32 experts of 2048 rows (pairs) 258 and 213, 553 and 495, 1519 and 1475; 64 of 700 (single CTAs) 183 and 153, 412 and 387,
-// 1143 and 1156; 64 of 128 52 and 45, 114 and 114, 329 and 342 (k 4096: 202 and 207, 727 and 707 of 700).
-bool staged_pays(bool fp8, bool pairs, const GemmParams& p, int64_t rows_each) {
-    if (!fp8) return !p.wide_stores || p.contraction <= 512;
+// Whether results go out through shared memory: tensor-map stores of 4 KB take a warp less time than its lanes' stores of
+// 32 bytes, or of 16 where rows are not 32 bytes aligned, but cost operand stages.
+//   - bf16: the lanes' stores run under the next tile's products and only short tiles wait for them.  Without and with, 64
+//     experts of 1024 rows, k 256, 512, 1024, 2048: 172 and 138 us, 224 and 215, 356 and 366, 658 and 674 for n = 4096;
+//     320 and 163, 295 and 254, 408 and 387, 702 and 700 for n = 4104.
+//   - FP8: its sums always wait for them.  k 512, 2048, 7168, n = 4096: 32 experts of 2048 rows (pairs) 258 and 213, 553 and
+//     495, 1519 and 1475; 64 of 700 (single CTAs) 183 and 153, 412 and 387, 1143 and 1156; 64 of 128 52 and 45, 114 and 114,
+//     329 and 342 (k 4096: 202 and 207, 727 and 707 of 700).
+//   - Weight gradient: up to one accumulator's rows.  32 experts, 2048 x 2048, 16, 256, 512, 1024 rows: 134 and 89 us, 134 and
+//     111, 152 and 136, 204 and 200; of 2048 rows, 2048 x 7168, 1150 and 1210.  Rows of the gradient that are not 128 bytes
+//     aligned: always (16 experts of 2048 rows, 1680 x 3480, 300 and 283).  Added to what is there: always, since the
+//     lanes would wait for it to arrive (the copy adds in the L2 cache, each element once): 16 rows 316 and 215, 2048 rows
+//     498 and 368.
+template <int FORM>
+bool staged_pays(bool pairs, const GemmParams& p, int64_t rows_each) {
+    if (FORM == kWeightGrad)
+        return p.out_fp32 && (p.accumulate || p.out_row_bytes % 128 != 0 ||
+                              p.groups.num_rows <= static_cast<int64_t>(p.groups.groups) * (segment_steps(FORM) * 64));
+    if (rows_each < kRowBox) return false;  // no whole block
+    if (FORM != kFp8) return !p.wide_stores || p.contraction <= 512;
     return pairs || p.contraction <= (rows_each > 2 * kTileRows ? 4096 : 2048);
 }
 
@@ -838,13 +874,19 @@ ep_status launch(const ep_handle* h, const Operand& a, const Operand& a_small, c
     p.tile_overhead = pairs                 ? 2 * kTileRows
                       : FORM == kWeightGrad ? kTileRows
                                             : static_cast<int32_t>(rows_each < kRowBox ? kRowBox : rows_each / row_tiles);
-    p.staged = FORM != kWeightGrad && rows_each >= kRowBox && staged_pays(FORM == kFp8, pairs, p, rows_each);
+    p.staged = staged_pays<FORM>(pairs, p, rows_each);
     ep_status st = encode(&m.b, b);
     if (st == EP_OK) st = encode(&m.b_small, b_small);
     m.out = m.b;  // not used
-    if (st == EP_OK && p.staged)
-        st = encode(&m.out, {p.out, false, 2, {static_cast<uint64_t>(p.cols_dim), static_cast<uint64_t>(p.groups.num_rows), 1, 1},
-                             {static_cast<uint64_t>(p.out_row_bytes), 0, 0}, {64, 32, 1, 1}});
+    if (st == EP_OK && p.staged) {
+        const uint64_t cols = p.cols_dim, row = p.out_row_bytes;
+        if (FORM == kWeightGrad)
+            st = encode(&m.out, {p.out, Element::kFp32, 3, {cols, static_cast<uint64_t>(p.rows_dim), static_cast<uint64_t>(p.groups.groups), 1},
+                                 {row, row * p.rows_dim, 0}, {32, 32, 1, 1}});
+        else
+            st = encode(&m.out, {p.out, Element::kBf16, 2, {cols, static_cast<uint64_t>(p.groups.num_rows), 1, 1},
+                                 {row, 0, 0}, {64, 32, 1, 1}});
+    }
     if (p.a_words) {
         m.a = m.a_small = m.b;  // not used
     } else {

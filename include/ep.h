@@ -436,7 +436,8 @@ ep_status ep_grouped_gemm(ep_handle* h, int64_t num_rows, int32_t n, int32_t k, 
 /* Gradient of the weights of a grouped product, for every expert e:
  *   dw[e][j][c] = sum over e's rows r of dy[r][j] * x[r][c]      dw [E][n][k], contiguous
  * dy rows of n, x rows of k bf16; dw fp32 or bf16 (dw_dtype).  An expert
- * without rows gets zeros.  accumulate != 0 (fp32 only): adds to what dw holds. */
+ * without rows gets zeros.  accumulate != 0 (fp32 only): adds to what dw holds, each
+ * element once; an expert without rows leaves its own as it is. */
 ep_status ep_grouped_gemm_wgrad(ep_handle* h, int64_t num_rows, int32_t n, int32_t k, const int32_t* group_count,
                                 const int32_t* group_begin, const void* dy, int64_t dy_row_bytes, const void* x,
                                 int64_t x_row_bytes, void* dw, ep_dtype dw_dtype, int32_t accumulate,

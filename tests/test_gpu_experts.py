@@ -123,6 +123,43 @@ def test_weight_gradient_accumulates():
     assert torch.equal(more, start + once)
 
 
+@pytest.mark.parametrize("n,k", [(8, 8), (72, 136), (264, 1032)])
+@pytest.mark.parametrize("counts", [[1], [5, 0, 1, 0], [128, 127, 129, 31], [900, 1100], [2000, 0, 1]], ids=lambda c: f"{len(c)}g{sum(c)}")
+def test_weight_gradient_added_and_of_many_rows(counts, n, k):
+    """Few and many rows an expert, written and added: the same sums, nothing beside them."""
+    E = len(counts)
+    begin, rows = packed(counts)
+    g = gen(n + k)
+    x, dy = randn(g, (rows, k)), randn(g, (rows, n))
+    once, more = Guarded((E, n, k), torch.float32), Guarded((E, n, k), torch.float32)
+    start = torch.randn((E, n, k), generator=g, device=DEV)
+    more.t.copy_(start)
+    h = handle(E)
+    for out, accumulate in ((once, False), (more, True), (more, True)):
+        ep.ep_grouped_gemm_wgrad(h, dy, x, i32(counts), i32(begin), out=out.t, accumulate=accumulate)
+        h.check()
+        out.check()
+    for e, (b, c) in enumerate(zip(begin, counts)):
+        ye, xe = dy[b:b + c].double(), x[b:b + c].double()
+        close(once.t[e], ye.t() @ xe, ye.abs().t() @ xe.abs(), c, 2.0 ** -24)
+    assert torch.equal(more.t, start + once.t + once.t)
+
+
+def test_weight_gradient_added_to_special_values():
+    g = gen(9)
+    x, dy = randn(g, (50, 64)), randn(g, (50, 32))
+    h = handle(2)
+    c, b = i32([50, 0]), i32([0, 50])
+    once = ep.ep_grouped_gemm_wgrad(h, dy, x, c, b)
+    start = torch.zeros((2, 32, 64), device=DEV)
+    start[:, 0, 0], start[:, 5, 3], start[:, 31, 63], start[:, 1, :] = float("inf"), float("nan"), float("-inf"), 3e38
+    more = start.clone()
+    ep.ep_grouped_gemm_wgrad(h, dy, x, c, b, out=more, accumulate=True)
+    h.check()
+    assert torch.equal(more.isnan(), (start + once).isnan())
+    assert torch.equal(more.nan_to_num(nan=0.5), (start + once).nan_to_num(nan=0.5))
+
+
 def test_products_are_each_others_gradients():
     """sum(dy * forward(x)) changes with x and w as the two gradients say (differences along a direction)."""
     counts = [40, 0, 133, 7]
