@@ -558,10 +558,14 @@ def _rows(t, name, dtype, device, rows=None, width=None):
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the handle lives on {device}")
     shape = t.shape
-    if len(shape) < 2:
+    if len(shape) == 2:
+        n, inner = shape
+        count = n * inner
+    elif len(shape) < 2:
         raise ValueError(f"{name} must be [rows][width], got {tuple(shape)}")
-    inner, count = shape[-1], t.numel()
-    n = count // inner if inner else math.prod(shape[:-1])
+    else:
+        inner, count = shape[-1], t.numel()
+        n = count // inner if inner else math.prod(shape[:-1])
     if (rows is not None and n != rows) or (width is not None and inner != width):
         raise ValueError(f"{name}: {n} rows of {inner}, expected {n if rows is None else rows} of "
                          f"{inner if width is None else width}")
@@ -590,9 +594,20 @@ def _rows(t, name, dtype, device, rows=None, width=None):
 def _out(shape, dtype, h, stream):
     """An output that the call allocates: on the call's stream, so that its memory is not handed out while it is in use."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=h.device)
+        return torch.empty(*shape, dtype=dtype, device=h.device)  # sizes one by one: a tuple takes a microsecond longer
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=h.device)
+        return torch.empty(*shape, dtype=dtype, device=h.device)
+
+
+def _out_rows(out, name, x, rows, width, dtype, h, stream):
+    """(out, address, row stride in bytes) of the rows that a call writes: checked, or allocated with x's leading axes."""
+    if out is not None:
+        p, _, _, row_bytes = _rows(out, name, dtype, h.device, rows, width)
+        return out, p, row_bytes
+    out = _out(_like(x, rows, width), dtype, h, stream)
+    row_bytes = width * dtype.itemsize
+    return (out, out.data_ptr() if rows and width else _dummy(h.device).data_ptr(),
+            row_bytes if rows != 1 else (row_bytes + 15) // 16 * 16)
 
 
 def _like(x, rows, width):
@@ -617,14 +632,13 @@ def ep_grouped_gemm(h: Handle, x: torch.Tensor, w: torch.Tensor, group_count, gr
     d = h.device
     if w.dim() != 3:
         raise ValueError(f"w must be [E][n][k], got {tuple(w.shape)}")
-    n, k = (w.shape[2], w.shape[1]) if w_transposed else (w.shape[1], w.shape[2])
+    _, a, b = w.shape
+    n, k = (b, a) if w_transposed else (a, b)
     xp, rows, _, xs = _rows(x, "x", torch.bfloat16, d, None, k)
-    if out is None:
-        out = _out(_like(x, rows, n), torch.bfloat16, h, stream)
-    op, _, _, os_ = _rows(out, "out", torch.bfloat16, d, rows, n)
+    out, op, os_ = _out_rows(out, "out", x, rows, n, torch.bfloat16, h, stream)
     cnt, beg = _group_arrays(h, group_count, group_begin)
     _raise(lib().ep_grouped_gemm(h.ptr, rows, n, k, cnt, beg, xp, xs,
-                                 _ptr(w, "w", torch.bfloat16, (h.cfg.num_experts,) + tuple(w.shape[1:]), d),
+                                 _ptr(w, "w", torch.bfloat16, (h.cfg.num_experts, a, b), d),
                                  int(bool(w_transposed)), op, os_, expected_rows, _stream(stream, d)))
     return out
 
@@ -669,9 +683,7 @@ def ep_grouped_gemm_fp8(h: Handle, x: torch.Tensor, x_scales: torch.Tensor, w: t
             raise ValueError(f"x_scales must hold {G} exponent bytes per row, got {tuple(x_scales.shape)}")
         x_scales = x_scales[..., :G]
     sp, _, _, ss = _rows(x_scales, "x_scales", x_scales.dtype, d, rows, G)
-    if out is None:
-        out = _out(_like(x, rows, n), torch.bfloat16, h, stream)
-    op, _, _, os_ = _rows(out, "out", torch.bfloat16, d, rows, n)
+    out, op, os_ = _out_rows(out, "out", x, rows, n, torch.bfloat16, h, stream)
     cnt, beg = _group_arrays(h, group_count, group_begin)
     _raise(lib().ep_grouped_gemm_fp8(h.ptr, rows, n, k, cnt, beg, xp, xs, sp, ss, int(ue8m0),
                                      _ptr(w, "w", torch.float8_e4m3fn, (h.cfg.num_experts, n, k), d),
@@ -689,14 +701,13 @@ def ep_swiglu(h: Handle, x: torch.Tensor, group_count, group_begin=None, row_wei
     if wide != 2 * width:
         raise ValueError(f"x must hold gate and up of one width, got rows of {wide}")
     dtype = torch.float8_e4m3fn if cast_to_fp8 else torch.bfloat16
-    if out is None:
-        out = _out(_like(x, rows, width), dtype, h, stream)
+    out, op, os_ = _out_rows(out, "out", x, rows, width, dtype, h, stream)
     if cast_to_fp8 and out_scales is None:
         out_scales = _out(_like(x, rows, width // 128), torch.float32, h, stream)
-    op, _, _, os_ = _rows(out, "out", dtype, d, rows, width)
     cnt, beg = _group_arrays(h, group_count, group_begin)
     _raise(lib().ep_swiglu(h.ptr, rows, width, cnt, beg, xp, xs, _ptr(row_weights, "row_weights", torch.float32, (rows,), d),
                            int(bool(cast_to_fp8)), int(bool(round_scale)), op, os_,
+                           None if out_scales is None else
                            _ptr(out_scales, "out_scales", torch.float32, _like(x, rows, width // 128), d),
                            _stream(stream, d)))
     return dict(out=out, out_scales=out_scales)
@@ -711,11 +722,9 @@ def ep_swiglu_grad(h: Handle, dy: torch.Tensor, x: torch.Tensor, group_count, gr
     if wide != 2 * width:
         raise ValueError(f"x must hold gate and up of one width, got rows of {wide}")
     yp, _, _, ys = _rows(dy, "dy", torch.bfloat16, d, rows, width)
-    if dx is None:
-        dx = _out(x.shape, torch.bfloat16, h, stream)
+    dx, gp, gs = _out_rows(dx, "dx", x, rows, wide, torch.bfloat16, h, stream)
     if row_weights is not None and d_row_weights is None:
         d_row_weights = _out((rows,), torch.float32, h, stream)
-    gp, _, _, gs = _rows(dx, "dx", torch.bfloat16, d, rows, wide)
     cnt, beg = _group_arrays(h, group_count, group_begin)
     _raise(lib().ep_swiglu_grad(h.ptr, rows, width, cnt, beg, yp, ys, xp, xs,
                                 _ptr(row_weights, "row_weights", torch.float32, (rows,), d), gp, gs,
