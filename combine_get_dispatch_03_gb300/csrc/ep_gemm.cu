@@ -517,14 +517,14 @@ __device__ __forceinline__ void box_columns_fp32(uint32_t box, const float (&v)[
     }
 }
 
-// 32 columns of a warp's rows, from column `c` of its part of the tile.  Staged: whole blocks of 32 rows go through the
-// warp's boxes in shared memory, 128 bytes of columns at a time (the map leaves out what lies past the last column, and
-// in the weight gradient past the last row).  The ends of groups and tiles of 64 columns go by stores of each lane.
-template <int FORM>
+// 32 columns of a warp's rows, from column `c` of its part of the tile.  kStaged: through the warp's boxes in shared
+// memory, 128 bytes of columns at a time (the map leaves out what lies past the last column, and in the weight gradient
+// past the last row).  Otherwise by stores of each lane.
+template <int FORM, bool kStaged>
 __device__ __forceinline__ void put_columns(const Roles& x, uint32_t box, const Place& at, int c, const float (&v)[32]) {
     const GemmParams& p = x.p;
     const int col = at.col + c;
-    if (FORM == kWeightGrad && p.staged) {
+    if constexpr (FORM == kWeightGrad && kStaged) {
         if (at.rows == 0 || col >= p.cols_dim) return;
         if (lane_id() == 0) bulk_wait_read<0>();
         __syncwarp();
@@ -536,7 +536,7 @@ __device__ __forceinline__ void put_columns(const Roles& x, uint32_t box, const 
             else tma_store_3d(&x.maps.out, box, col, at.row, at.group);
             bulk_commit();
         }
-    } else if (FORM != kWeightGrad && p.staged && at.cols >= 64 && at.rows == 32) {
+    } else if constexpr (kStaged) {
         constexpr int kBoxes = out_boxes(FORM);
         const int second = (c >> 5) & 1;
         const int first_col = col - 32 * second;
@@ -563,6 +563,30 @@ __device__ __forceinline__ void put_columns(const Roles& x, uint32_t box, const 
             store_fp32(out, col, p.cols_dim, v, p.wide_stores != 0);
         else
             store_bf16(out, col, p.cols_dim, v, p.wide_stores != 0);
+    }
+}
+
+// Whether a warp's part of a tile leaves through its boxes: not the ends of groups, nor tiles of 64 columns.  Asked once a
+// tile (64 experts of 2048 rows, 7168 x 2048 in FP8: 1692 us asked for every 32 columns, 1679 so).
+template <int FORM>
+__device__ __forceinline__ bool in_boxes(const GemmParams& p, const Place& at) {
+    return p.staged && (FORM == kWeightGrad || (at.cols >= 64 && at.rows == 32));
+}
+
+// A warp's sums, 128 columns a lane at most, to their place.
+template <int FORM, bool kStaged>
+__device__ __forceinline__ void put_sums(const Roles& x, uint32_t box, const Place& at, const uint64_t (&acc)[2][32]) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        if (32 * c >= at.cols) break;
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const uint64_t pair = acc[c / 2][c % 2 * 16 + i];
+            v[2 * i] = __uint_as_float(static_cast<uint32_t>(pair));
+            v[2 * i + 1] = __uint_as_float(static_cast<uint32_t>(pair >> 32));
+        }
+        put_columns<FORM, kStaged>(x, box, at, 32 * c, v);
     }
 }
 
@@ -594,6 +618,7 @@ __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
             ok = warp_wait(&ctl.acc_full[buf], acc_phase, &ctl.abort_flag, p.status);
             if (!ok) break;
             tc_fence_after();
+            const bool staged = in_boxes<FORM>(p, at);
             for (int c = 0; c < cols_half; c += 32) {
                 uint32_t u[32];
                 __syncwarp();
@@ -607,7 +632,8 @@ __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
                 float v[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
-                put_columns<FORM>(x, box, at, c, v);
+                if (staged) put_columns<FORM, true>(x, box, at, c, v);
+                else put_columns<FORM, false>(x, box, at, c, v);
             }
             buf ^= 1;
             acc_phase ^= buf == 0;
@@ -672,18 +698,8 @@ __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
             __syncwarp();
             if (!ok) break;
             const Place to = read_place(&ctl.at[w]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if (32 * c >= to.cols) break;
-                float v[32];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const uint64_t pair = acc[c / 2][c % 2 * 16 + i];
-                    v[2 * i] = __uint_as_float(static_cast<uint32_t>(pair));
-                    v[2 * i + 1] = __uint_as_float(static_cast<uint32_t>(pair >> 32));
-                }
-                put_columns<FORM>(x, box, to, 32 * c, v);
-            }
+            if (in_boxes<FORM>(p, to)) put_sums<FORM, true>(x, box, to, acc);
+            else put_sums<FORM, false>(x, box, to, acc);
             __syncwarp();  // the place has been read
         }
     }
