@@ -649,7 +649,9 @@ __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
             if (lane_id() == 0) ctl.at[w] = at;
             const int segments = (q.steps + kSegment - 1) / kSegment;
             // A block's scales are loaded a block before they are used, and only then looked at: a
-            // multiplication next to the loads would wait for them.
+            // multiplication next to the loads would wait for them.  All of it comes before the wait for the block's
+            // products, and without a branch (the last block loads its own scales again): 8 experts of 2048 rows,
+            // 4096 x 7168, 381 us with a branch after the wait, 369 without it, 362 so.
             const uint8_t* xs = nullptr;
             const float* ws = nullptr;
             uint32_t x_next = 0;
@@ -663,21 +665,21 @@ __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
             }
 #pragma unroll 1
             for (int left = segments; left > 0; --left) {
+                float f = 1.0f;
+                if constexpr (FORM == kFp8) {
+                    f = scale_value(x_next, p.scales_ue8m0) * w_next;
+                    const int on = left > 1;
+                    xs += p.scales_ue8m0 ? on : 4 * on;
+                    ws += on;
+                    x_next = raw_scale(xs, 0, p.scales_ue8m0);
+                    w_next = *ws;
+                }
                 ok = warp_wait(&ctl.acc_full[buf], acc_phase, &ctl.abort_flag, p.status);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t from = lane_base + buf * kMaxTileCols + half * cols_half;
                 uint32_t u[64];
                 tc_ld64(from, u);
-                float f = 1.0f;
-                if constexpr (FORM == kFp8) {  // while the load is on its way
-                    f = scale_value(x_next, p.scales_ue8m0) * w_next;
-                    if (left > 1) {
-                        xs += p.scales_ue8m0 ? 1 : 4;
-                        x_next = raw_scale(xs, 0, p.scales_ue8m0);
-                        w_next = *++ws;
-                    }
-                }
                 const uint64_t scale = pack_f32x2(__float_as_uint(f), __float_as_uint(f));
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
