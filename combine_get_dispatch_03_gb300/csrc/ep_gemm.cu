@@ -20,9 +20,11 @@
 //     and the ends of groups cost the rest).
 //   - few rows an expert: memory, the weights.  32 experts of 64 rows, 4096 x 7168 bf16: 286 us, 6.7 TB/s.
 //   - FP8: a block's sums go from tensor memory through registers, 32768 FMAs a stage and CTA at 128 a cycle; with the
-//     way there and back between the products' thread and the eight warps a stage takes about 800 cycles for
-//     512 of products.  The same 8 experts: 374 to 384 us, 2500 to 2570 TFLOP/s; 64 experts of 128 rows read from
-//     messages: 334 us, 6.0 TB/s.
+//     way there and back between the products' thread and the eight warps a stage takes about 770 cycles for
+//     512 of products.  The same 8 experts: 362 us, 2660 TFLOP/s; 64 experts of 128 rows read from messages: 334 us,
+//     6.0 TB/s.
+//   - short contractions and few rows: the results' way out (staged_pays()).  64 experts of 1024 rows, 4096 x 256 bf16:
+//     138 us, 5.1 TB/s; gradients of 32 experts of 16 rows, 2048 x 2048: 89 us, 6.0 TB/s.
 //
 // Two loads of 16 KB a stage (one an operand) rather than smaller ones: a load costs the issuing thread about
 // 95 cycles.  64 columns of an accumulator a read in the FP8 form: 292 cycles for 128 columns and their FMAs in eight
