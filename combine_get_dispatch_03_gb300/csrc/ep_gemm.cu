@@ -880,11 +880,36 @@ bool staged_pays(bool pairs, const GemmParams& p, int64_t rows_each) {
     return pairs || p.contraction <= (rows_each > 2 * kTileRows ? 4096 : 2048);
 }
 
+// Whether the weight gradient runs on pairs of CTAs: its tiles are known here, and it is the side whose waves take less.
+// A stage takes 2 cycles a column of products or 3 for two rows of operands that a CTA loads, whichever is longer.
+// Measured, pairs against single CTAs where the model prefers these, 1500 and 256 rows an expert: 64 experts of 344 x 4096
+// 311 and 293 us, 101 and 87; 8 of 560 x 2448 49.0 and 45.2, 20.0 and 17.8; where it prefers pairs: 8 of 2048 x 2048 76 and
+// 89, 31 and 32; 16 of 392 x 2048 54 and 59, 21 and 22.
+bool wgrad_on_pairs(const ep_handle* h, const GemmParams& p) {
+    if (p.rows_dim <= kTileRows) return false;  // one of the two would idle
+    int64_t best[2];
+    for (int ctas = 1; ctas <= 2; ++ctas) {
+        const int64_t workers = ctas == 2 ? h->plan.gemm_pairs : h->plan.num_sms;
+        if (workers == 0) return false;
+        best[ctas - 1] = INT64_MAX;
+        for (int cols = kMaxTileCols; cols >= kColBox * ctas; cols >>= 1) {
+            const int64_t rows = kTileRows * ctas;
+            const int64_t tiles = p.groups.groups * ((p.rows_dim + rows - 1) / rows) * ((p.cols_dim + cols - 1) / cols);
+            const int64_t stage = 4 * cols > 3 * (kTileRows + cols / ctas) ? 4 * cols : 3 * (kTileRows + cols / ctas);
+            const int64_t cost = (tiles + workers - 1) / workers * stage;
+            if (cost < best[ctas - 1]) best[ctas - 1] = cost;
+        }
+    }
+    return best[1] <= best[0];
+}
+
 template <int FORM>
 ep_status launch(const ep_handle* h, const Operand& a, const Operand& a_small, const Operand& b, const Operand& b_small,
                  GemmParams p, int64_t rows_each, cudaStream_t stream) {
     Maps m;
-    const bool pairs = !p.a_words && rows_each >= (FORM == kFp8 ? kPairRowsFp8 : kTileRows + 1) && h->plan.gemm_pairs > 0;
+    const bool pairs = FORM == kWeightGrad ? wgrad_on_pairs(h, p)
+                                           : !p.a_words && rows_each >= (FORM == kFp8 ? kPairRowsFp8 : kTileRows + 1) &&
+                                                 h->plan.gemm_pairs > 0;
     // A tile's stages wait for their operands, and a tile is worth the rows that a CTA loads beside its columns: a pair's
     // 128 beside half of the columns (weight gradient of 8 experts, 560 x 2448, 83592 rows: 401 us with 32 columns'
     // worth, 257 with 128, 246 with 256), a single CTA's as many as a group's tiles have, at least one load's (FP8, 64
