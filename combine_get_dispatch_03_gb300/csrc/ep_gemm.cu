@@ -884,9 +884,11 @@ bool staged_pays(bool pairs, const GemmParams& p, int64_t rows_each) {
 // A stage takes 2 cycles a column of products or 3 for two rows of operands that a CTA loads, whichever is longer.
 // Measured, pairs against single CTAs where the model prefers these, 1500 and 256 rows an expert: 64 experts of 344 x 4096
 // 311 and 293 us, 101 and 87; 8 of 560 x 2448 49.0 and 45.2, 20.0 and 17.8; where it prefers pairs: 8 of 2048 x 2048 76 and
-// 89, 31 and 32; 16 of 392 x 2048 54 and 59, 21 and 22.
+// 89, 31 and 32; 16 of 392 x 2048 54 and 59, 21 and 22.  Groups of more than 1536 rows always on pairs: their operands no
+// longer wait in the L2 cache for the next tile (8 experts of 10449 rows, 560 x 2448: 250 and 305).
 bool wgrad_on_pairs(const ep_handle* h, const GemmParams& p) {
     if (p.rows_dim <= kTileRows) return false;  // one of the two would idle
+    if (p.groups.num_rows > INT64_C(1536) * p.groups.groups) return h->plan.gemm_pairs > 0;
     int64_t best[2];
     for (int ctas = 1; ctas <= 2; ++ctas) {
         const int64_t workers = ctas == 2 ? h->plan.gemm_pairs : h->plan.num_sms;
