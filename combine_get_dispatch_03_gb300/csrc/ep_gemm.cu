@@ -61,7 +61,7 @@ constexpr int kPairRowsFp8 = 1024;  // rows of a group from which the FP8 form r
 constexpr int kMaxStages = 12;
 constexpr int kEpilogueWarps = 8;
 constexpr int kGemmThreads = (4 + kEpilogueWarps) * kWarpSize;  // warps 0 to 3 for loads and products: registers go by four warps
-constexpr int kControlBytes = 640;  // static shared memory
+constexpr int kControlBytes = 704;  // static shared memory
 constexpr uint32_t kOutBox = 32 * kRowBytes;  // a warp's results on their way out: 32 rows of 128 bytes
 // Of them a warp: in FP8 one for each 64 columns, since there a tile's stores hold up the next one's sums (2048 rows an
 // expert, 7168 x 2048: 1740 us with one, 1682 with two).
@@ -122,6 +122,7 @@ struct Control {
     uint32_t tmem;
     int32_t abort_flag;
     int64_t warp_sums[kGemmThreads / kWarpSize];
+    int64_t warp_rows[kGemmThreads / kWarpSize];
     int32_t tiles, col_tiles, tile_cols;  // output tiles in all, tiles across, columns of one
     Place at[kEpilogueWarps];             // forms with segments: of the tile that a warp is adding up
 };
@@ -160,7 +161,7 @@ __device__ __forceinline__ Tile decode(const Table& t, const GemmParams& p, cons
 }
 
 // Fills the table: clamps every group to the rows that exist (the first group that does not fit sets
-// EP_ERR_CAPACITY), and sums the row tiles.  All threads of the CTA.
+// EP_ERR_CAPACITY), and sums the row tiles and, where rows are written, the rows.  All threads of the CTA.
 template <int FORM, int CG>
 __device__ __forceinline__ void build_table(const Table& t, const GemmParams& p, Control& ctl) {
     constexpr int kRows = kTileRows * CG;
@@ -168,19 +169,31 @@ __device__ __forceinline__ void build_table(const Table& t, const GemmParams& p,
     const int per = (groups + kGemmThreads - 1) / kGemmThreads;
     const int first = threadIdx.x * per;
     const int last = min(first + per, groups);
-    int64_t sum = 0, row_tiles = 0;
+    int64_t sum = 0, row_tiles = 0, rows = 0;
     for (int g = first; g < last; ++g) {
         const Group q = load_group(p.groups, g, p.status);
+        rows += q.count;
         t.count[g] = q.count;
         t.begin[g] = q.begin;
         t.before[g] = static_cast<int32_t>(sum);
         sum += (static_cast<int64_t>(FORM == kWeightGrad ? p.rows_dim : q.count) + kRows - 1) / kRows;
     }
+    if constexpr (FORM != kWeightGrad) {
+#pragma unroll
+        for (int o = kWarpSize / 2; o > 0; o >>= 1) rows += __shfl_xor_sync(kFullMask, rows, o);
+        if (lane_id() == 0) ctl.warp_rows[threadIdx.x / kWarpSize] = rows;  // read after the prefix's barrier
+    }
     const int64_t base = block_prefix<kGemmThreads>(sum, ctl.warp_sums, &row_tiles);
     for (int g = first; g < last; ++g) t.before[g] += static_cast<int32_t>(base);
     if (threadIdx.x == 0) {
-        // more row tiles than rows that do not overlap can fill: nothing is computed
-        const bool overlap = FORM != kWeightGrad && row_tiles > p.groups.num_rows / kRows + groups;
+        // Groups that together hold more rows than there are overlap: nothing is computed.  The rows decide, not the
+        // tiles: eight groups of the same 100 rows have no more tiles than eight groups of 100 rows apart.
+        bool overlap = false;
+        if constexpr (FORM != kWeightGrad) {
+            rows = 0;
+            for (int w = 0; w < kGemmThreads / kWarpSize; ++w) rows += ctl.warp_rows[w];
+            overlap = rows > p.groups.num_rows;
+        }
         if (overlap) report(p.status, EP_ERR_CAPACITY);
         const int total = overlap ? 0 : static_cast<int>(row_tiles);
         t.before[groups] = total;
