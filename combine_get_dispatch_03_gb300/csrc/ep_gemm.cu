@@ -835,10 +835,18 @@ ep_status encode(CUtensorMap* map, const Operand& o) {
     const CUtensorMapDataType type = o.element == Element::kFp8    ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                      : o.element == Element::kFp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    const CUresult rc = fn(map, type, o.dims,
-                           const_cast<void*>(o.base), size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    CUresult rc = CUDA_SUCCESS;
+    for (int attempt = 0; attempt < 2; ++attempt) {
+        rc = fn(map, type, o.dims, const_cast<void*>(o.base), size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (rc != CUDA_ERROR_INVALID_CONTEXT) break;
+        // A thread that has not used its device yet has no context, and the encoder, unlike the runtime's calls, makes
+        // none current.
+        int device = 0;
+        cudaError_t err = cudaGetDevice(&device);
+        if (err == cudaSuccess) err = cudaSetDevice(device);
+        if (err != cudaSuccess) return cuda_fail(err, "making the device's context current");
+    }
     if (rc != CUDA_SUCCESS) return fail(EP_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(rc));
     return EP_OK;
 }
@@ -921,6 +929,7 @@ bool wgrad_on_pairs(const ep_handle* h, const GemmParams& p) {
 template <int FORM>
 ep_status launch(const ep_handle* h, const Operand& a, const Operand& a_small, const Operand& b, const Operand& b_small,
                  GemmParams p, int64_t rows_each, cudaStream_t stream) {
+    DeviceGuard guard(h->device);
     Maps m;
     const bool pairs = FORM == kWeightGrad ? wgrad_on_pairs(h, p)
                                            : !p.a_words && rows_each >= (FORM == kFp8 ? kPairRowsFp8 : kTileRows + 1) &&
@@ -954,7 +963,6 @@ ep_status launch(const ep_handle* h, const Operand& a, const Operand& a_small, c
         if (st == EP_OK) st = encode(&m.a_small, a_small);
     }
     if (st != EP_OK) return st;
-    DeviceGuard guard(h->device);
     // A pair of CTAs computes 256 rows: each loads half of the weight tile, so that a row of products takes a
     // third less shared-memory fill.  Where the rows of a group would leave one of the two idle, single CTAs; in
     // FP8, where a block's sums wait for both CTAs of a pair, single CTAs up to 1024 rows.  Measured at 32 experts,

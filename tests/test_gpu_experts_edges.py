@@ -1,11 +1,13 @@
 """The expert operators at their edges: groups that overlap, waits that run out, calls from new threads, values at the
 ends of the formats, and the paths that only some sizes take."""
+import threading
+
 import pytest
 import torch
 
 from combine_get_dispatch_03_gb300 import ep
 from _parity import Guarded
-from test_gpu_experts import DEV, handle, i32
+from test_gpu_experts import DEV, gen, handle, i32, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +44,38 @@ def test_more_rows_than_there_are_write_nothing(counts, begin, rows, expected, f
     run(i32([rows] + [0] * (E - 1)))  # every row there is, once
     h.check()
     assert (out.t == 0).all()
+
+
+@pytest.mark.parametrize("form", ["forward", "transposed", "weight_grad", "fp8"])
+def test_first_cuda_call_of_a_thread(form):
+    """A product as the first CUDA call that a host thread makes: no context is current in it yet."""
+    g = gen(2)
+    h, c, b = handle(2), i32([30, 34]), i32([0, 30])
+    x, w = randn(g, (64, 128)), randn(g, (2, 128, 128))
+    ones, codes = torch.ones((64, 1), device=DEV), x.to(torch.float8_e4m3fn)
+    wcodes, wones = w.to(torch.float8_e4m3fn), torch.ones((2, 1, 1), device=DEV)
+    outs = [torch.zeros((2, 128, 128) if form == "weight_grad" else (64, 128), device=DEV,
+                        dtype=torch.float32 if form == "weight_grad" else torch.bfloat16) for _ in range(2)]
+
+    def call(out):
+        if form == "weight_grad":
+            ep.ep_grouped_gemm_wgrad(h, x, x, c, b, out=out)
+        elif form == "fp8":
+            ep.ep_grouped_gemm_fp8(h, codes, ones, wcodes, wones, c, b, out=out)
+        else:
+            ep.ep_grouped_gemm(h, x, w, c, b, w_transposed=form == "transposed", out=out)
+    errors = []
+
+    def run():
+        try:
+            call(outs[0])
+        except Exception as e:  # noqa: BLE001 -- shown by the thread that started this one
+            errors.append(e)
+    torch.cuda.synchronize()
+    thread = threading.Thread(target=run)
+    thread.start()
+    thread.join()
+    assert not errors, errors
+    call(outs[1])
+    h.check()
+    assert bool(outs[1].any()) and torch.equal(outs[0], outs[1])
