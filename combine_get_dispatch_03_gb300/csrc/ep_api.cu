@@ -599,4 +599,12 @@ ep_status ep_selftest_bounded_wait(ep_handle* h, uint32_t max_iterations, int32_
     return EP_OK;
 }
 
+ep_status ep_selftest_wait_limit(ep_handle* h, int64_t limit_ns) {
+    EP_TRACE();
+    if (h == nullptr) return fail(EP_ERR_INVALID_ARG, "handle is NULL");
+    EP_CHECK_ARG(limit_ns >= 0, "limit_ns %lld < 0", static_cast<long long>(limit_ns));
+    h->wait_limit_ns = limit_ns ? static_cast<uint64_t>(limit_ns) : kWaitLimitNs;
+    return EP_OK;
+}
+
 }  // extern "C"

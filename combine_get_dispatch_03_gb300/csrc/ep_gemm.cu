@@ -88,6 +88,7 @@ struct GemmParams {
     const uint8_t* a_words;        // rows that no tensor map can describe (not 16 bytes apart), or NULL
     int64_t a_row_bytes;
     int32_t* status;
+    uint64_t wait_limit_ns;
 };
 
 // Tensor maps of the two operands: loads of kBox output elements, and smaller ones; and of the results, boxes of 32
@@ -118,7 +119,7 @@ struct Control {
     uint64_t acc_full[2];
     uint64_t acc_empty[2];
     uint64_t tail_full[kMaxStages];  // weight grad: instead of full, for a group's last, partial block of rows
-    uint64_t drained;
+    uint64_t drained;  // every product has been computed
     uint32_t tmem;
     int32_t abort_flag;
     int64_t warp_sums[kGemmThreads / kWarpSize];
@@ -273,6 +274,7 @@ struct Roles {
     const GemmParams& p;
     const Table& t;
     Control& ctl;
+    Waits waits;
     uint8_t* stages;
     uint8_t* boxes;
     uint32_t tmem, rank, stage_bytes;  // rank: of the CTA in its pair
@@ -304,7 +306,7 @@ __device__ __forceinline__ void load_operands(const Roles& x) {
         const int cb = static_cast<int>(x.rank) * cols;
         const uint32_t bytes = row_bytes + cols * kRowBytes;
         for (int s = 0; s < q.steps; ++s) {
-            ok = wait_phase(&ctl.empty[stage], phase ^ 1, &ctl.abort_flag, p.status);
+            ok = wait_phase(&ctl.empty[stage], phase ^ 1, x.waits);
             if (!ok) break;
             uint8_t* a = x.stages + stage * x.stage_bytes;
             uint8_t* b = a + kABytes;
@@ -367,18 +369,23 @@ __device__ __forceinline__ void load_operands(const Roles& x) {
             if (++stage == static_cast<uint32_t>(x.num_stages)) stage = 0, phase ^= 1;
         }
     }
-    // The copies in flight land before the memory goes away: at once where all went well, within a limit where
-    // some warp gave up.  With a pair they all arrive at the leader, but for the ends of groups, and neither CTA
-    // leaves before the other.
+    // Copies and products in flight end before the memory goes away.  Where all went well the products have read every
+    // copy when the last stages are free again, and their arrivals (a pair's at both CTAs) have landed.  Where
+    // some warp gave up, each within a limit: the copies that completed a stage, then the products; what a pair has in
+    // flight beside that, see the kernel's end.
     for (int i = 0; i < x.num_stages && used > 0; ++i, --used) {
         if (stage == 0) phase ^= 1;
         stage = (stage == 0 ? x.num_stages : stage) - 1;
+        if (ok) ok = wait_phase(&ctl.empty[stage], phase, x.waits);
+        if (ok) continue;
         const bool tail = (tail_last >> stage) & 1;
         if (x.rank != 0 && !tail) continue;
         uint64_t* bar = tail ? &ctl.tail_full[stage] : &ctl.full[stage];
         const uint32_t parity = tail ? ((tail_phase >> stage) & 1) ^ 1 : phase;
         for (int k = 0; k < (1 << 12) && !mbar_try_wait(bar, parity); ++k) {
         }
+    }
+    for (int k = 0; k < (1 << 12) && !mbar_try_wait(&ctl.drained, 0); ++k) {
     }
 }
 
@@ -401,12 +408,12 @@ __device__ __forceinline__ void multiply(const Roles& x) {
             const int in_segment = kSegment ? s % kSegment : s;
             // operands first: they are there, and with short segments the accumulator is what is waited for
             if (FORM == kWeightGrad && CG == 2 && q.rows - s * 64 < 64)  // zeroed rows, maybe the peer's
-                ok = wait_phase<true>(&ctl.full[stage], phase, &ctl.abort_flag, p.status);
+                ok = wait_phase<true>(&ctl.full[stage], phase, x.waits);
             else
-                ok = wait_phase(&ctl.full[stage], phase, &ctl.abort_flag, p.status);
+                ok = wait_phase(&ctl.full[stage], phase, x.waits);
             if (!ok) break;
             if (in_segment == 0) {
-                ok = wait_phase(&ctl.acc_empty[buf], acc_phase ^ 1, &ctl.abort_flag, p.status);
+                ok = wait_phase(&ctl.acc_empty[buf], acc_phase ^ 1, x.waits);
                 if (!ok) break;
             }
             tc_fence_after();
@@ -427,12 +434,9 @@ __device__ __forceinline__ void multiply(const Roles& x) {
             if (++stage == static_cast<uint32_t>(x.num_stages)) stage = 0, phase ^= 1;
         }
     }
-    if (!ok) {
-        // Given up: the products already issued still write tensor memory.
-        tc_commit<CG>(&ctl.drained);
-        for (int k = 0; k < (1 << 12) && !mbar_try_wait(&ctl.drained, 0); ++k) {
-        }
-    }
+    // The products already issued still write tensor memory, also where another warp gave up on them: load_operands()
+    // waits for this.
+    tc_commit<CG>(&ctl.drained);
 }
 
 // Two warps: row operands whose rows are not 16 bytes apart (messages of some hidden sizes), in words of four bytes,
@@ -451,7 +455,7 @@ __device__ __forceinline__ void copy_rows(const Roles& x, int warp) {
         const Tile q = decode<FORM, 1>(t, p, ctl, tile);
         const int rows = min(kTileRows, q.rows - q.m0);
         for (int s = 0; s < q.steps; ++s) {
-            ok = warp_wait(&ctl.empty[stage], phase ^ 1, &ctl.abort_flag, p.status);
+            ok = warp_wait(&ctl.empty[stage], phase ^ 1, x.waits);
             if (!ok) break;
             uint8_t* a = x.stages + stage * x.stage_bytes;
             const int at = s * kRowBytes + lane_id() * 4;
@@ -489,7 +493,7 @@ __device__ __forceinline__ void zero_tails(const Roles& x) {
         const int whole = q.rows / 64, valid = q.rows % 64;
         stage = (stage + whole) % x.num_stages;
         if (valid == 0) continue;
-        ok = warp_wait(&ctl.tail_full[stage], (tail_phase >> stage) & 1, &ctl.abort_flag, p.status);
+        ok = warp_wait(&ctl.tail_full[stage], (tail_phase >> stage) & 1, x.waits);
         tail_phase ^= 1u << stage;
         uint8_t* a = x.stages + stage * x.stage_bytes;
         const int chunks = (kTileRows + q.cols / CG) / 64;
@@ -630,7 +634,7 @@ __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
         const Place at = {(FORM == kWeightGrad ? 0 : q.row0) + in_group, q.n0 + half * cols_half, q.group,
                           static_cast<short>(rows), static_cast<short>(cols_half)};
         if constexpr (kSegment == 0) {
-            ok = warp_wait(&ctl.acc_full[buf], acc_phase, &ctl.abort_flag, p.status);
+            ok = warp_wait(&ctl.acc_full[buf], acc_phase, x.waits);
             if (!ok) break;
             tc_fence_after();
             const bool staged = in_boxes<FORM>(p, at);
@@ -689,7 +693,7 @@ __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
                     x_next = raw_scale(xs, 0, p.scales_ue8m0);
                     w_next = *ws;
                 }
-                ok = warp_wait(&ctl.acc_full[buf], acc_phase, &ctl.abort_flag, p.status);
+                ok = warp_wait(&ctl.acc_full[buf], acc_phase, x.waits);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t from = lane_base + buf * kMaxTileCols + half * cols_half;
@@ -768,7 +772,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     tc_fence_after();
 
     const uint32_t stage_bytes = kABytes + ctl.tile_cols / CG * kRowBytes;
-    const Roles x = {maps, p, t, ctl, stages, boxes, ctl.tmem, rank, stage_bytes,
+    const Roles x = {maps, p, t, ctl, {&ctl.abort_flag, p.status, p.wait_limit_ns}, stages, boxes, ctl.tmem, rank, stage_bytes,
                      min(kMaxStages, static_cast<int>((kMaxSmem - 1024u - table_end - out_bytes) / stage_bytes)),
                      static_cast<int>(blockIdx.x / CG), static_cast<int>(gridDim.x / CG)};
     // Forms with segments hold 128 sums a thread in their eight epilogue warps: registers move there from the
@@ -791,8 +795,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     __syncwarp();
     tc_fence_before();
-    if constexpr (CG == 2) cluster_barrier();
-    else __syncthreads();
+    if constexpr (CG == 2) {
+        cluster_barrier();
+        // Given up (both CTAs have the flag): a stage that only one of the two has loaded completes no barrier, so its copy
+        // is given a hundred times what a copy takes, instead of being waited for.
+        if (x.waits.abort_flag[0]) {
+            if (threadIdx.x == 0)
+                for (const uint64_t begin = global_ns(); global_ns() - begin < 1000000;) __nanosleep(1000);
+            __syncwarp();
+            cluster_barrier();
+        }
+    } else {
+        __syncthreads();
+    }
     tc_fence_after();
     if (warp == 1) tmem_dealloc<CG>(x.tmem, 512);
 }
@@ -997,6 +1012,7 @@ ep_status check_groups(const ep_handle* h, int64_t num_rows, int32_t n, int32_t 
                     static_cast<long long>(wide));
     p->groups = {group_count, group_begin, num_rows, static_cast<int32_t>(num_rows / groups), groups};
     p->status = h->status;
+    p->wait_limit_ns = h->wait_limit_ns;
     return EP_OK;
 }
 

@@ -7,6 +7,10 @@
 
 #include "ep_kernels.h"
 
+namespace ep {
+constexpr uint64_t kWaitLimitNs = 4000000000ull;
+}
+
 struct ep_handle {
     ep_config cfg;
     int device = -1;
@@ -32,6 +36,7 @@ struct ep_handle {
     int normal_tokens = -1;                  // T of the current dispatch record, -1 = none
     bool prepared = false;                   // record built by ep_notify_dispatch, not yet used
     int ll_tokens = -1;                      // T of the last LL dispatch, -1 = none
+    uint64_t wait_limit_ns = ep::kWaitLimitNs;  // of a wait inside the grouped products
 };
 
 namespace ep {

@@ -9,10 +9,14 @@ namespace ep {
 
 // ---------------------------------------------------------------------------
 // Waits.  Every wait on an mbarrier ends: when the phase completes, when another
-// warp of the CTA gave up, or after four seconds, which sets the CTA's abort
-// flag and EP_ERR_TIMEOUT.  The caller then leaves its loop.
+// warp of the CTA or of its pair gave up, or after the handle's limit, which sets the
+// abort flag of every CTA of the cluster and EP_ERR_TIMEOUT.  The caller then leaves its loop.
 // ---------------------------------------------------------------------------
-constexpr uint64_t kWaitLimitNs = 4000000000ull;
+struct Waits {
+    volatile int32_t* abort_flag;  // in the CTA's shared memory, at the same place in its peer's
+    int32_t* status;
+    uint64_t limit_ns;
+};
 
 __device__ __forceinline__ uint64_t global_ns() {
     uint64_t t;
@@ -35,21 +39,47 @@ __device__ __forceinline__ bool poll_phase(uint64_t* bar, uint32_t parity) {
     return done != 0;
 }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t n;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+    return n;
+}
+
+// Address in the cluster's shared window of `p` (this CTA's shared memory) as it lies in CTA `rank`.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+
+__device__ __forceinline__ void give_up(const Waits& w) {
+    *w.abort_flag = 1;
+    if (cluster_size() == 2)  // neither CTA of a pair leaves before the other: its flag is there
+        asm volatile("st.shared::cluster.u32 [%0], 1;"
+                     ::"r"(cluster_addr(const_cast<int32_t*>(w.abort_flag), cluster_rank() ^ 1)) : "memory");
+    report(w.status, EP_ERR_TIMEOUT);
+}
+
+// A poll that comes to nothing takes about 3.8 us: the abort flag and the clock are looked at every 0.24 ms.
 template <bool kCluster = false>
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int32_t* abort_flag,
-                                           int32_t* status) {
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, const Waits& w) {
     if (poll_phase<kCluster>(bar, parity)) return true;
     uint64_t begin = 0;  // the clock is read only after polls that came to nothing: reading it takes long
     for (;;) {
 #pragma unroll 1
         for (int i = 0; i < 64; ++i)
             if (poll_phase<kCluster>(bar, parity)) return true;
-        if (*abort_flag) return false;
+        if (*w.abort_flag) return false;
         const uint64_t now = global_ns();
         if (begin == 0) begin = now;
-        if (now - begin > kWaitLimitNs) {
-            *abort_flag = 1;
-            report(status, EP_ERR_TIMEOUT);
+        if (now - begin > w.limit_ns) {
+            give_up(w);
             return false;
         }
     }
@@ -64,29 +94,15 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // The same for a whole warp: every lane gets the same answer.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int32_t* abort_flag,
-                                          int32_t* status) {
-    return __all_sync(kFullMask, wait_phase(bar, parity, abort_flag, status));
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const Waits& w) {
+    return __all_sync(kFullMask, wait_phase(bar, parity, w));
 }
 
 // ---------------------------------------------------------------------------
 // Clusters of CG CTAs (1 or 2).
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// Address in the cluster's shared window of `p` (this CTA's shared memory) as it lies in CTA `rank`.
-__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
-    uint32_t a;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-    return a;
 }
 
 // Arrivals at a barrier of this CTA (CG == 1) or, by its address in the cluster's shared window, of any CTA

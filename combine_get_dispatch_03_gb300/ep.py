@@ -55,7 +55,7 @@ EXPORTS = ("ep_handle_create", "ep_handle_destroy", "ep_handle_status", "ep_hand
            "ep_query_mask_buffer", "ep_clean_mask_buffer", "ep_selftest_bounded_wait", "ep_ll_combine_strided",
            "ep_expected_topk", "ep_theoretical_num_sms", "ep_layout_notify", "ep_grouped_gemm",
            "ep_grouped_gemm_wgrad", "ep_grouped_gemm_fp8", "ep_swiglu", "ep_swiglu_grad",
-           "ep_expert_layout", "ep_expert_gather", "ep_expert_reduce")
+           "ep_expert_layout", "ep_expert_gather", "ep_expert_reduce", "ep_selftest_wait_limit")
 
 
 def library_path() -> str:
@@ -103,6 +103,7 @@ def lib():
         L.ep_selftest_bounded_wait.argtypes = [P, ctypes.c_uint32, I32, P]
         L.ep_ll_dispatch_noalloc.argtypes = [I32, I32, I32, I32, I32, I32, P, P, I32, I32, I32, P, P, P, P, P, P,
                                              P]
+        L.ep_selftest_wait_limit.argtypes = [P, I64]
         L.ep_grouped_gemm.argtypes = [P, I64, I32, I32, P, P, P, I64, P, I32, P, I64, I64, P]
         L.ep_grouped_gemm_wgrad.argtypes = [P, I64, I32, I32, P, P, P, I64, P, I64, P, S, I32, P]
         L.ep_grouped_gemm_fp8.argtypes = [P, I64, I32, I32, P, P, P, I64, P, I64, I32, P, P, P, I64, I64, P]
@@ -117,7 +118,7 @@ def lib():
                      "ep_query_mask_buffer", "ep_clean_mask_buffer", "ep_selftest_bounded_wait",
                      "ep_ll_combine_strided", "ep_layout_notify", "ep_grouped_gemm", "ep_grouped_gemm_wgrad",
                      "ep_grouped_gemm_fp8", "ep_swiglu", "ep_swiglu_grad", "ep_expert_layout", "ep_expert_gather",
-                     "ep_expert_reduce"):
+                     "ep_expert_reduce", "ep_selftest_wait_limit"):
             getattr(L, name).restype = S
         _lib = L
     return _lib
@@ -287,6 +288,10 @@ def ep_clean_mask_buffer(h: Handle, stream=None):
 
 def ep_selftest_bounded_wait(h: Handle, max_iterations: int, rank: int, stream=None):
     _raise(lib().ep_selftest_bounded_wait(h.ptr, max_iterations, rank, _stream(stream, h.device)))
+
+
+def ep_selftest_wait_limit(h: Handle, limit_ns: int = 0):
+    _raise(lib().ep_selftest_wait_limit(h.ptr, limit_ns))
 
 
 def ep_handle_create(cfg: Config, device=None) -> Handle:

@@ -357,6 +357,15 @@ ep_status ep_clean_mask_buffer(ep_handle* h, ep_stream_t stream);
  * or traps; read the outcome with ep_handle_status() / ep_query_mask_buffer(). */
 ep_status ep_selftest_bounded_wait(ep_handle* h, uint32_t max_iterations, int32_t rank, ep_stream_t stream);
 
+/* Self-test of the waits inside the grouped products: sets how long one may
+ * last (limit_ns >= 1; 0: four seconds again) in the products that are called
+ * on the handle from now on.  A wait that lasts longer -- the limit is looked at
+ * every quarter of a millisecond -- records EP_ERR_TIMEOUT; the product's other
+ * waits end with it, what it has in flight is waited for, and the
+ * kernel returns with its output incomplete.  A limit of some
+ * microseconds makes this happen wherever a product's contraction takes longer. */
+ep_status ep_selftest_wait_limit(ep_handle* h, int64_t limit_ns);
+
 /* ------------------------------------- low-latency dispatch, no allocation */
 
 /* Capacity of the fixed count scratch of ep_ll_dispatch_noalloc(): int32

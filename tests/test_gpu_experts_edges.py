@@ -79,3 +79,56 @@ def test_first_cuda_call_of_a_thread(form):
     call(outs[1])
     h.check()
     assert bool(outs[1].any()) and torch.equal(outs[0], outs[1])
+
+
+# Waits that run out.  Contractions of 2^18 take a tile longer than the half millisecond in which a limit of a microsecond
+# is noticed (a stage of 64 is at least 512 cycles of products: 4096 stages, 1 ms), and one CTA, or one pair, has several
+# tiles: the eight warps that wait for a tile's sums give up first, the products run into accumulators that nobody empties, the
+# loads into stages that nobody frees.  Nothing is broken for it: every wait would be met later.
+
+def after_a_timeout(h, ctas):
+    """The handle and the GPU's tensor memory are as usable as before."""
+    g = gen(ctas)
+    counts = [150, 0, 31, 300]
+    x, w = randn(g, (sum(counts), 200)), randn(g, (4, 264, 200), 0.1)
+    c, b = i32(counts), i32([0, 150, 150, 181])
+    fresh = handle(4, max_sms=ctas)
+    for limit in (0, 1000):  # waits this short are met before the limit is looked at
+        ep.ep_selftest_wait_limit(h, limit)
+        for expected in (1, 100000):
+            got = ep.ep_grouped_gemm(h, x, w, c, b, expected_rows=expected)
+            assert torch.equal(got, ep.ep_grouped_gemm(fresh, x, w, c, b, expected_rows=expected))
+        dw = ep.ep_grouped_gemm_wgrad(h, got, x, c, b)
+        assert torch.equal(dw, ep.ep_grouped_gemm_wgrad(fresh, got, x, c, b))
+    h.check()
+    fresh.check()
+
+
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("ctas", [1, 2], ids=["single", "pair"])
+def test_wait_that_runs_out(ctas, transposed):
+    E, n, k = 4, 256, 1 << 18
+    h = handle(E, max_sms=ctas)
+    x = torch.ones((E, k), dtype=torch.bfloat16, device=DEV)
+    w = torch.ones((E, k, n) if transposed else (E, n, k), dtype=torch.bfloat16, device=DEV)
+    c, b = i32([1] * E), i32(list(range(E)))
+    out = Guarded((E, n), torch.bfloat16)
+
+    def run():
+        ep.ep_grouped_gemm(h, x, w, c, b, w_transposed=transposed, out=out.t, expected_rows=1 if ctas == 1 else 100000)
+    ep.ep_selftest_wait_limit(h, 1000)
+    run()
+    assert h.status() == 3
+    out.check()
+    ep.ep_selftest_wait_limit(h)
+    run()
+    h.check()
+    out.check()
+    assert (out.t == k).all()
+    after_a_timeout(h, ctas)
+
+
+def test_wait_limit_is_checked():
+    with pytest.raises(ep.EPError) as e:
+        ep.ep_selftest_wait_limit(handle(1), -1)
+    assert e.value.status == 1 and "limit_ns" in str(e.value)
