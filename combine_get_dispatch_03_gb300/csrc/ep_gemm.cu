@@ -494,6 +494,7 @@ __device__ __forceinline__ void zero_tails(const Roles& x) {
         stage = (stage + whole) % x.num_stages;
         if (valid == 0) continue;
         ok = warp_wait(&ctl.tail_full[stage], (tail_phase >> stage) & 1, x.waits);
+        if (!ok) break;  // a copy may still be on its way there
         tail_phase ^= 1u << stage;
         uint8_t* a = x.stages + stage * x.stage_bytes;
         const int chunks = (kTileRows + q.cols / CG) / 64;

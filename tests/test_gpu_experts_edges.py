@@ -128,6 +128,28 @@ def test_wait_that_runs_out(ctas, transposed):
     after_a_timeout(h, ctas)
 
 
+@pytest.mark.parametrize("ctas", [1, 2], ids=["single", "pair"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_wait_for_the_end_of_a_group_that_runs_out(ctas, dtype):
+    """Weight gradient of groups of 2^18 + 10 rows: the warp that zeroes what follows a group's end waits for its last block
+    of rows from the start.  Giving up, it leaves that block alone and does not release it."""
+    E, n, k, m = 4, 256, 256, (1 << 18) + 10
+    h = handle(E, max_sms=ctas)
+    x = torch.ones((E * m, k), dtype=torch.bfloat16, device=DEV)
+    c, b = i32([m] * E), i32([m * e for e in range(E)])
+    out = Guarded((E, n, k), dtype)
+    ep.ep_selftest_wait_limit(h, 1000)
+    ep.ep_grouped_gemm_wgrad(h, x, x, c, b, out=out.t)
+    assert h.status() == 3
+    out.check()
+    ep.ep_selftest_wait_limit(h)
+    ep.ep_grouped_gemm_wgrad(h, x, x, c, b, out=out.t)
+    h.check()
+    out.check()
+    assert (out.t == torch.tensor(m, dtype=torch.float32).to(dtype).item()).all()
+    after_a_timeout(h, ctas)
+
+
 def test_wait_limit_is_checked():
     with pytest.raises(ep.EPError) as e:
         ep.ep_selftest_wait_limit(handle(1), -1)
