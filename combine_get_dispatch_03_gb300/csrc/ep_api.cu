@@ -20,9 +20,6 @@
 namespace ep {
 cudaError_t plan_dispatch_combine(LaunchPlan* plan, int hidden);
 cudaError_t plan_ll(LaunchPlan* plan, int num_experts);
-cudaError_t plan_gemm(LaunchPlan* plan);
-cudaError_t plan_rows(LaunchPlan* plan);
-cudaError_t plan_swiglu(LaunchPlan* plan, int groups);
 }  // namespace ep
 
 using namespace ep;
@@ -158,9 +155,6 @@ ep_status ep_handle_create(const ep_config* cfg, ep_handle** out) {
     }
     if (err == cudaSuccess) err = ep::plan_dispatch_combine(&h->plan, cfg->hidden);
     if (err == cudaSuccess) err = ep::plan_ll(&h->plan, cfg->num_experts);
-    if (err == cudaSuccess) err = ep::plan_gemm(&h->plan);
-    if (err == cudaSuccess) err = ep::plan_rows(&h->plan);
-    if (err == cudaSuccess) err = ep::plan_swiglu(&h->plan, cfg->num_experts);
     if (err != cudaSuccess) {
         delete h;
         return cuda_fail(err, "planning launches");

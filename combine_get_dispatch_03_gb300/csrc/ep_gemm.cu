@@ -943,9 +943,47 @@ bool wgrad_on_pairs(const ep_handle* h, const GemmParams& p) {
 }
 
 template <int FORM>
-ep_status launch(const ep_handle* h, const Operand& a, const Operand& a_small, const Operand& b, const Operand& b_small,
+cudaError_t plan_form(LaunchPlan* plan) {
+    cudaError_t err = cudaFuncSetAttribute(grouped_gemm_kernel<FORM, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (err == cudaSuccess)
+        err = cudaFuncSetAttribute(grouped_gemm_kernel<FORM, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (err == cudaSuccess && FORM != kWeightGrad)
+        err = cudaFuncSetAttribute(grouped_gemm_kernel<FORM, 1, FORM != kWeightGrad>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   kMaxSmem);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(plan->num_sms / 2 * 2);
+    cfg.blockDim = dim3(kGemmThreads);
+    cfg.dynamicSmemBytes = kMaxSmem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int pairs = 0;
+    if (plan->num_sms >= 2) err = cudaOccupancyMaxActiveClusters(&pairs, grouped_gemm_kernel<FORM, 2>, &cfg);
+    if (err != cudaSuccess) return err;
+    if (pairs < plan->gemm_pairs) plan->gemm_pairs = pairs;
+    return cudaSuccess;
+}
+
+// The pairs of CTAs that are resident at once.
+cudaError_t plan_gemm(LaunchPlan* plan) {
+    plan->gemm_pairs = plan->num_sms / 2;
+    cudaError_t err = plan_form<kForward>(plan);
+    if (err == cudaSuccess) err = plan_form<kTransposed>(plan);
+    if (err == cudaSuccess) err = plan_form<kWeightGrad>(plan);
+    if (err == cudaSuccess) err = plan_form<kFp8>(plan);
+    return err;
+}
+
+template <int FORM>
+ep_status launch(ep_handle* h, const Operand& a, const Operand& a_small, const Operand& b, const Operand& b_small,
                  GemmParams p, int64_t rows_each, cudaStream_t stream) {
     DeviceGuard guard(h->device);
+    const ep_status planned = plan_once(&h->plan.gemm_ready, [h] { return plan_gemm(&h->plan); });
+    if (planned != EP_OK) return planned;
     Maps m;
     const bool pairs = FORM == kWeightGrad ? wgrad_on_pairs(h, p)
                                            : !p.a_words && rows_each >= (FORM == kFp8 ? kPairRowsFp8 : kTileRows + 1) &&
@@ -1041,43 +1079,6 @@ ep_status check_rows(const void* x, int64_t x_row_bytes, int64_t x_least, const 
 }
 
 }  // namespace
-
-template <int FORM>
-cudaError_t plan_form(LaunchPlan* plan) {
-    cudaError_t err = cudaFuncSetAttribute(grouped_gemm_kernel<FORM, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-    if (err == cudaSuccess)
-        err = cudaFuncSetAttribute(grouped_gemm_kernel<FORM, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-    if (err == cudaSuccess && FORM != kWeightGrad)
-        err = cudaFuncSetAttribute(grouped_gemm_kernel<FORM, 1, FORM != kWeightGrad>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   kMaxSmem);
-    if (err != cudaSuccess) return err;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(plan->num_sms / 2 * 2);
-    cfg.blockDim = dim3(kGemmThreads);
-    cfg.dynamicSmemBytes = kMaxSmem;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    int pairs = 0;
-    if (plan->num_sms >= 2) err = cudaOccupancyMaxActiveClusters(&pairs, grouped_gemm_kernel<FORM, 2>, &cfg);
-    if (err != cudaSuccess) return err;
-    if (pairs < plan->gemm_pairs) plan->gemm_pairs = pairs;
-    return cudaSuccess;
-}
-
-// The pairs of CTAs that are resident at once.
-cudaError_t plan_gemm(LaunchPlan* plan) {
-    plan->gemm_pairs = plan->num_sms / 2;
-    cudaError_t err = plan_form<kForward>(plan);
-    if (err == cudaSuccess) err = plan_form<kTransposed>(plan);
-    if (err == cudaSuccess) err = plan_form<kWeightGrad>(plan);
-    if (err == cudaSuccess) err = plan_form<kFp8>(plan);
-    return err;
-}
-
 }  // namespace ep
 
 using namespace ep;

@@ -22,6 +22,9 @@ struct LaunchPlan {
     int swiglu_blocks[3] = {0, 0, 0};    // gated activation: bf16, FP8 cast, gradient
     int reduce_blocks = 0;               // expert rows back into receive rows
     int gemm_pairs = 0;                  // grouped products: pairs of CTAs resident on the GPU at once
+    bool gemm_ready = false;             // the experts' parts are made by the first call that needs them (plan_once)
+    bool rows_ready = false;
+    bool swiglu_ready = false;
     int bulk_resident[3] = {1, 1, 1};    // its CTAs resident on the GPU at once
 };
 

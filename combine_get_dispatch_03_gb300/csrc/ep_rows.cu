@@ -378,8 +378,6 @@ ep_status check_rows(int64_t num_rows) {
     return EP_OK;
 }
 
-}  // namespace
-
 cudaError_t plan_rows(LaunchPlan* plan) {
     int per_sm = 0;
     cudaError_t err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, rows_reduce_kernel, kRowThreads, 0);
@@ -392,6 +390,11 @@ cudaError_t plan_rows(LaunchPlan* plan) {
     return err;
 }
 
+ep_status planned(ep_handle* h) {
+    return plan_once(&h->plan.rows_ready, [h] { return plan_rows(&h->plan); });
+}
+
+}  // namespace
 }  // namespace ep
 
 using namespace ep;
@@ -412,6 +415,8 @@ ep_status ep_expert_layout(ep_handle* h, const int64_t* recv_topk_idx, const int
     const int R = c.num_ranks, E = c.num_experts, EL = E / R, cap = static_cast<int>(c.recv_capacity), K = c.num_topk;
     const int chunks = static_cast<int>(layout_chunks(c));
     DeviceGuard guard(h->device);
+    st = planned(h);
+    if (st != EP_OK) return st;
     cudaError_t err = launch_kernel(layout_count_kernel, dim3(chunks, R), dim3(kRowThreads), EL * sizeof(int32_t), stream, 1,
                                     recv_topk_idx, recv, cap, K, EL, h->expert_counts,
                                     reinterpret_cast<uint32_t*>(h->layout_tickets), group_count, h->status);
@@ -465,6 +470,8 @@ ep_status ep_expert_gather(ep_handle* h, const void* x, ep_dtype x_dtype, const 
     const int64_t runs = (units + p.stages - 1) / p.stages;
     const int64_t most = static_cast<int64_t>(h->plan.num_sms) * kGatherPerSm * (h->plan.sm_limited ? 1 : kGatherWaves);
     DeviceGuard guard(h->device);
+    st = planned(h);
+    if (st != EP_OK) return st;
     const cudaError_t err = launch_kernel(rows_gather_kernel, dim3(static_cast<unsigned>(runs < most ? runs : most)),
                                           dim3(kWarpSize), static_cast<size_t>(p.stages) * p.piece_bytes, stream, 1, p);
     if (err != cudaSuccess) return cuda_fail(err, "expert gather launch");
@@ -499,8 +506,10 @@ ep_status ep_expert_reduce(ep_handle* h, const void* y, int64_t y_row_bytes, con
     p.topk = c.num_topk;
     p.status = h->status;
     const int64_t wanted = (static_cast<int64_t>(p.cap) * p.ranks + kRowWarps - 1) / kRowWarps;
-    const int64_t most = h->plan.reduce_blocks;  // resident at once: warps stride over the rows
     DeviceGuard guard(h->device);
+    st = planned(h);
+    if (st != EP_OK) return st;
+    const int64_t most = h->plan.reduce_blocks;  // resident at once: warps stride over the rows
     const cudaError_t err = launch_kernel(rows_reduce_kernel, dim3(static_cast<unsigned>(wanted < most ? wanted : most)),
                                           dim3(kRowThreads), 0, stream, 1, p);
     if (err != cudaSuccess) return cuda_fail(err, "expert reduce launch");

@@ -170,9 +170,18 @@ cudaError_t plan_form(LaunchPlan* plan, int groups) {
     return err;
 }
 
+cudaError_t plan_swiglu(LaunchPlan* plan, int groups) {
+    cudaError_t err = plan_form<kToBf16>(plan, groups);
+    if (err == cudaSuccess) err = plan_form<kToFp8>(plan, groups);
+    if (err == cudaSuccess) err = plan_form<kGradient>(plan, groups);
+    return err;
+}
+
 template <int FORM>
-ep_status launch(const ep_handle* h, const SwigluParams& p, cudaStream_t stream) {
+ep_status launch(ep_handle* h, const SwigluParams& p, cudaStream_t stream) {
     DeviceGuard guard(h->device);
+    const ep_status planned = plan_once(&h->plan.swiglu_ready, [h] { return plan_swiglu(&h->plan, h->cfg.num_experts); });
+    if (planned != EP_OK) return planned;
     // no more warps than rows; past kWaves waves, warps stride over the rows
     const int64_t wanted = (p.groups.num_rows + kThreads / kWarpSize - 1) / (kThreads / kWarpSize);
     const int64_t most = h->plan.swiglu_blocks[FORM];
@@ -205,14 +214,6 @@ ep_status check(const ep_handle* h, int64_t num_rows, int32_t width, const int32
 }
 
 }  // namespace
-
-cudaError_t plan_swiglu(LaunchPlan* plan, int groups) {
-    cudaError_t err = plan_form<kToBf16>(plan, groups);
-    if (err == cudaSuccess) err = plan_form<kToFp8>(plan, groups);
-    if (err == cudaSuccess) err = plan_form<kGradient>(plan, groups);
-    return err;
-}
-
 }  // namespace ep
 
 using namespace ep;

@@ -428,7 +428,10 @@ ep_status ep_ll_dispatch_noalloc(int32_t num_ranks, int32_t num_tokens, int32_t 
  * 16-byte aligned; the x of ep_grouped_gemm() and ep_grouped_gemm_fp8() may do
  * with 4, at a lower speed.  n and k are multiples of 8.  Sums are fp32, rounded once.
  * NaN and infinities in a row reach that row's outputs only (a weight
- * gradient: its expert's). */
+ * gradient: its expert's).
+ * A handle's first call of an expert operator plans its launches (about 10
+ * microseconds; a process's first also loads the kernels, half a millisecond). It may
+ * be under stream capture. */
 
 /* Grouped product, bf16: for every row r of expert e
  *   w_transposed == 0:  out[r][j] = sum_c x[r][c] * w[e][j][c]   w [E][n][k]

@@ -1,5 +1,8 @@
 """The expert operators at their edges: groups that overlap, waits that run out, calls from new threads, values at the
 ends of the formats, and the paths that only some sizes take."""
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -154,3 +157,65 @@ def test_wait_limit_is_checked():
     with pytest.raises(ep.EPError) as e:
         ep.ep_selftest_wait_limit(handle(1), -1)
     assert e.value.status == 1 and "limit_ns" in str(e.value)
+
+
+FIRST_HANDLE = """
+import time, torch
+from combine_get_dispatch_03_gb300 import ep
+x, w = (torch.ones(s, dtype=torch.bfloat16, device="cuda") for s in ((64, 256), (2, 256, 256)))
+c, b = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([30, 34], [0, 30]))
+out = torch.empty((64, 256), dtype=torch.bfloat16, device="cuda")
+ep.lib()
+torch.cuda.synchronize()
+at = [time.perf_counter()]
+h = ep.Handle(ep.Config(1, 8, 256, 2, 1))
+torch.cuda.synchronize()
+at.append(time.perf_counter())
+ep.ep_grouped_gemm(h, x, w, c, b, out=out)
+at.append(time.perf_counter())
+h.check()
+assert bool((out == 256).all())
+print((at[2] - at[1]) / (at[1] - at[0]))
+"""
+
+FIRST_CALLS_CAPTURED = """
+import torch
+from combine_get_dispatch_03_gb300 import ep
+x, w = (torch.ones(s, dtype=torch.bfloat16, device="cuda") for s in ((64, 256), (2, 256, 256)))
+c, b = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([30, 34], [0, 30]))
+idx = torch.zeros((1, 64, 1), dtype=torch.int64, device="cuda")
+n = torch.tensor([64], dtype=torch.int32, device="cuda")
+h = ep.Handle(ep.Config(1, 64, 256, 2, 1, recv_capacity=64))
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    lay = ep.ep_expert_layout(h, idx, 64, num_recv=n)
+    g = ep.ep_expert_gather(h, x.view(1, 64, 256), lay["slot_row"], 64, num_recv=n)["out"]
+    y = ep.ep_grouped_gemm(h, g, w, c, b)
+    s = ep.ep_swiglu(h, y, c, b)["out"]
+    r = ep.ep_expert_reduce(h, y, lay["slot_row"], num_recv=n)["out"]
+graph.replay()
+torch.cuda.synchronize()
+h.check()
+assert bool((y == 256).all()) and bool((s == 65536).all()) and torch.equal(r.view(64, 256), y)
+"""
+
+
+def child(code):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(ep.__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300,
+                       env=dict(os.environ, PYTHONPATH=root))
+    assert r.returncode == 0, r.stderr[-2000:]
+    return r.stdout
+
+
+def test_a_handle_loads_no_expert_kernels():
+    """A process's first handle and its first product: the product's kernels are loaded by the second (0.55 ms beside
+    1.5 ms of the handle), not, as once, by the first (0.06 beside 2.3)."""
+    ratios = []
+    while len(ratios) < 3 and not any(r > 0.1 for r in ratios):
+        ratios.append(float(child(FIRST_HANDLE)))
+    assert ratios[-1] > 0.1, ratios
+
+
+def test_first_calls_of_a_handle_may_be_captured():
+    child(FIRST_CALLS_CAPTURED)
