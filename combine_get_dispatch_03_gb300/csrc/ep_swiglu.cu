@@ -5,15 +5,15 @@
 //   forward    v = gate * sig * up * p, to bf16, or to e4m3 codes and one scale per 128 columns
 //   gradient   dgate = dv * p * up * sig * (1 + gate * (1 - sig));  dup = dv * p * gate * sig;
 //              dp = sum over the row of dv * gate * sig * up
-// All in fp32, rounded once.  exp and the reciprocal are the hardware's approximations (2 ulp each for the
-// |gate| that leaves a value bf16 can tell from 0), five instructions a value: the kernels are near the bound of
-// their instructions, not only of memory.
+// All in fp32, rounded once.  2^x and the reciprocal are the hardware's approximations, and a value is good to 2^-20 at
+// every gate above -87 (sigmoid2).  Below -88.7 exp(-gate) passes fp32 and the sigmoid is 0, as in the formula in 32 bits; in
+// 64 bits a gate of -90 would leave 7e-38 * up.  The kernels are near the bound of their instructions, not only of memory.
 //
 // A warp owns a row: 32 lanes of 8 columns, so that a scale's 128 columns are 16 lanes and their maximum four
 // shuffles.  Only rows of a group are touched; warps stride over them through the group table.
 //
-// Measured on a GB300 (6787 GB/s copied): the cast of 131072 rows of 2048 214 us, 6.3 TB/s, 72 % of the issue
-// slots; the gradient of 32672 rows of 1024 50.3 us, 6.6 TB/s; 128 rows of 1024 3.0 us, a launch.
+// Measured on a GB300 (6787 GB/s copied): the cast of 131072 rows of 2048 217 us, 6.2 TB/s, 72 % of the issue
+// slots before the correction; the gradient of 32672 rows of 1024 50.3 us, 6.6 TB/s; 128 rows of 1024 3.0 us, a launch.
 #include "ep_groups.cuh"
 #include "ep_handle.h"
 #include "ep_trace.h"
@@ -44,13 +44,26 @@ struct SwigluParams {
 
 enum SwigluForm { kToBf16 = 0, kToFp8 = 1, kGradient = 2 };
 
-// 1 / (1 + exp(-g)).  The reciprocal is taken of a quarter of the sum, which the flushing instruction leaves a normal
-// result of up to exp(-g) = 2^128: gates down to -88.7 keep a (subnormal) sigmoid, below that it is 0.
-__device__ __forceinline__ float sigmoid(float g) {
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(e, 0.25f, 0.25f)));
-    return r * 0.25f;
+// 1 / (1 + exp(-g)) of a bf16 gate.  exp(-g) = 2^(-g * hi) * exp(-g * lo) with log2(e) = hi + lo / ln(2): hi has 15
+// significant bits and g 8, so that the product which goes into the exponent is exact, and lo is small enough for
+// 1 - g * lo (second order: 1e-7 at g = -90; past 128 the first factor is 0).  One product with log2(e) rounded to 24 bits
+// was off by 5e-7 at |gate| = 16 and 4e-6 at 80.  The reciprocal is taken of a quarter of the sum, which the flushing
+// instruction leaves a normal result of up to exp(-g) = 2^128: gates down to -88.7 keep a (subnormal) sigmoid, below
+// that it is 0, as exp(-g) is infinite in 32 bits.
+// Two gates at a time: the cast of 131072 rows of 2048 takes 214.6 us without the correction, 222.6 with it one by one, 216.6 packed
+// (with the products that follow).
+__device__ __forceinline__ float2 sigmoid2(float2 g) {
+    constexpr float kHi = 1.44268798828125f, kLo = 4.8884951521e-6f;
+    const float2 quarter = make_float2(0.25f, 0.25f);
+    const float2 t = __fmul2_rn(g, make_float2(-kHi, -kHi));
+    float2 e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+    e = __ffma2_rn(e, __fmul2_rn(make_float2(fminf(g.x, 128.0f), fminf(g.y, 128.0f)), make_float2(-kLo, -kLo)), e);
+    e = __ffma2_rn(e, quarter, quarter);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
+    return __fmul2_rn(r, quarter);
 }
 
 template <int FORM>
@@ -84,17 +97,23 @@ __device__ __forceinline__ void swiglu_row(const SwigluParams& p, int64_t row) {
             float g[8], u[8];
             unpack8(g4[i], g);
             unpack8(u4[i], u);
+            float sig[8], act[8];  // act = g * sig
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                const float2 two = make_float2(g[j], g[j + 1]);
+                const float2 s = sigmoid2(two), a = __fmul2_rn(two, s);
+                sig[j] = s.x, sig[j + 1] = s.y;
+                act[j] = a.x, act[j + 1] = a.y;
+            }
             if constexpr (FORM == kGradient) {
                 float d[8], dg[8], du[8];
                 unpack8(d4[i], d);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float sig = sigmoid(g[j]);
-                    const float act = g[j] * sig;
                     const float dv = d[j] * weight;
-                    dg[j] = dv * u[j] * (sig * (1.0f + g[j] * (1.0f - sig)));
-                    du[j] = dv * act;
-                    dp += d[j] * act * u[j];
+                    dg[j] = dv * u[j] * (sig[j] * (1.0f + g[j] * (1.0f - sig[j])));
+                    du[j] = dv * act[j];
+                    dp += d[j] * act[j] * u[j];
                 }
                 if (in[i]) {
                     st_stream_v4(reinterpret_cast<int4*>(out + 2 * col[i]), pack8_bf16(dg));
@@ -103,7 +122,11 @@ __device__ __forceinline__ void swiglu_row(const SwigluParams& p, int64_t row) {
             } else {
                 float v[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = g[j] * sigmoid(g[j]) * u[j] * weight;
+                for (int j = 0; j < 8; j += 2) {
+                    const float2 a = __fmul2_rn(make_float2(act[j], act[j + 1]), make_float2(u[j], u[j + 1]));
+                    const float2 two = __fmul2_rn(a, make_float2(weight, weight));
+                    v[j] = two.x, v[j + 1] = two.y;
+                }
                 if constexpr (FORM == kToBf16) {
                     if (in[i]) st_stream_v4(reinterpret_cast<int4*>(out + 2 * col[i]), pack8_bf16(v));
                 } else {

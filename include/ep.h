@@ -473,7 +473,8 @@ ep_status ep_grouped_gemm_fp8(ep_handle* h, int64_t num_rows, int32_t n, int32_t
 /* Gated activation between an expert's two products.  A row of x holds
  * [gate: width][up: width] bf16; for every row r of every expert
  *   v[r][j] = gate * sigmoid(gate) * up * row_weights[r]      (row_weights fp32 [num_rows], NULL = 1)
- * in fp32, then cast_to_fp8 == 0: out = bf16 rows of width; cast_to_fp8 != 0
+ * in fp32 (a gate below -88.7, whose exp(-gate) passes fp32, has a sigmoid of
+ * 0), then cast_to_fp8 == 0: out = bf16 rows of width; cast_to_fp8 != 0
  * (width a multiple of 128): out = rows of width e4m3 codes and out_scales
  * (fp32 [num_rows][width/128]) by the dispatch's rule (amax = max(max|v|,
  * 1e-4), scale = amax/448; round_scale != 0: the next power of two). */

@@ -219,3 +219,69 @@ def test_a_handle_loads_no_expert_kernels():
 
 def test_first_calls_of_a_handle_may_be_captured():
     child(FIRST_CALLS_CAPTURED)
+
+
+# One value of the activation in fp32: ex2 and rcp are good to 2^-22 and 2^-23, the second order that sigmoid() leaves out is
+# 9e-8 at the largest gate, and there are five roundings of 2^-24: 7.5e-7 in all, below 2^-20.
+VALUE = 2.0 ** -20
+
+
+@pytest.mark.parametrize("lo,hi,p", [(-86.0, -64.0, 2.0 ** 120), (-64.0, -16.0, 2.0 ** 120), (-16.0, -0.01, 2.0 ** 20),
+                                     (0.01, 16.0, 1.0), (16.0, 86.0, 1.0)])
+def test_fp32_results_of_the_activation(lo, hi, p):
+    """The cast's scales and the routing weights' gradients, a gate to a row, so that nothing cancels: against 64 bits."""
+    rows, width = 64, 128
+    g = gen(7)
+    gate = torch.linspace(lo, hi, rows, device=DEV).to(torch.bfloat16)[:, None].expand(rows, width)
+    up = (torch.rand((rows, width), generator=g, device=DEV) + 0.5).to(torch.bfloat16)
+    x = torch.cat([gate, up], 1).contiguous()
+    weight = torch.full((rows,), p, device=DEV)  # keeps the largest value above the scale's floor of 1e-4
+    dy = torch.ones((rows, width), dtype=torch.bfloat16, device=DEV)
+    h, c, b = handle(1), i32([rows]), i32([0])
+    got = ep.ep_swiglu(h, x, c, b, row_weights=weight, cast_to_fp8=True)["out_scales"].double().view(-1)
+    grad = ep.ep_swiglu_grad(h, dy, x, c, b, row_weights=weight)["d_row_weights"].double()
+    h.check()
+    gd = gate.double()
+    act = gd / (1 + torch.exp(-gd)) * up.double()
+    scale = act.abs().amax(1) * p / 448
+    assert (scale * 448 > 1e-4).all()
+    err = (got - scale).abs() / scale
+    assert float(err.max()) <= VALUE + 2.0 ** -23, float(err.max())
+    # sums of 128 terms: eight in a lane, five times two lanes
+    err = (grad - act.sum(1)).abs() / act.sum(1).abs()
+    assert float(err.max()) <= VALUE + 13 * 2.0 ** -24, float(err.max())
+
+
+@pytest.mark.parametrize("weighted", [False, True])
+def test_gradient_of_the_activation_at_large_gates(weighted):
+    """Gates whose sigmoid is 0, 1 or as small as 2^-124, and infinite ones: the formula in 64 bits."""
+    g = gen(11)
+    gates = torch.tensor([-3e38, -1e4, -200.0, -100.0, -86.0, -60.0, -30.0, -16.0, 16.0, 30.0, 60.0, 88.0, 90.0, 200.0, 1e4, 3e38],
+                         device=DEV)
+    rows, width = 8, 16
+    x = torch.cat([gates.expand(rows, width), torch.randn((rows, width), generator=g, device=DEV)], 1).to(torch.bfloat16)
+    dy = (torch.rand((rows, width), generator=g, device=DEV) * 0.5 + 0.25).to(torch.bfloat16)
+    weight = torch.rand(rows, generator=g, device=DEV) * 0.5 + 0.25 if weighted else None
+    h, c, b = handle(1), i32([rows]), i32([0])
+    dx = ep.ep_swiglu_grad(h, dy, x, c, b, row_weights=weight)["dx"].double()
+    h.check()
+    gate, up, d = x[:, :width].double(), x[:, width:].double(), dy.double()
+    p = weight.double()[:, None] if weighted else 1.0
+    sig = torch.where(gate < -88.7, 0.0, 1 / (1 + torch.exp(-gate)))  # 0 where exp(-gate) is infinite in 32 bits
+    want = torch.cat([d * p * up * (sig + gate * sig * (1 - sig)), d * p * gate * sig], 1)
+    # 1 + gate * (1 - sig): sig is off by 2^-21 of itself, so past 16 the sum by 2^-21 * |gate| at most where sig is near 1
+    extra = torch.cat([(d * p * up).abs() * sig * (2.0 ** -21 * (1 + gate.clamp(-88, 88).abs())), torch.zeros_like(d)], 1)
+    assert ((dx - want).abs() <= (2.0 ** -8 + VALUE * 2) * want.abs() + extra + 1e-40).all()
+    for bad, slope in ((float("inf"), None), (float("-inf"), None), (float("nan"), None)):
+        x2 = x.clone()
+        x2[2, 5] = bad
+        dx2 = ep.ep_swiglu_grad(h, dy, x2, c, b, row_weights=weight)["dx"].double()
+        keep = torch.ones((rows, 2 * width), dtype=torch.bool, device=DEV)
+        keep[2, 5] = keep[2, width + 5] = False
+        assert torch.equal(dx2[keep], dx[keep])  # a column reaches its own two gradients only
+        both = dx2[2, [5, width + 5]]
+        if bad == float("inf"):  # sigmoid 1: inf * (1 - 1) has no value, and d up is infinite
+            assert both[0].isnan() and both[1].isinf()
+        else:
+            assert both.isnan().all()
+    h.check()
