@@ -135,8 +135,10 @@ __device__ __forceinline__ void swiglu_row(const SwigluParams& p, int64_t row) {
                     for (int o = 1; o < kFp8Group / kLaneCols; o <<= 1)
                         amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, o));
                     const Fp8Scale s = fp8_scale(amax, p.round_scale != 0);
+                    // of an infinite scale 0 (as 448 / amax is), where the power of two has none
+                    const float mult = isinf(s.scale) ? 0.0f : s.mult;
                     if (in[i]) {
-                        st_stream_v2(reinterpret_cast<int2*>(out + col[i]), cast8_e4m3(v, s.mult));
+                        st_stream_v2(reinterpret_cast<int2*>(out + col[i]), cast8_e4m3(v, mult));
                         if (lane_id() % (kFp8Group / kLaneCols) == 0)
                             p.out_scales[row * (p.width / kFp8Group) + col[i] / kFp8Group] = s.scale;
                     }

@@ -477,7 +477,9 @@ ep_status ep_grouped_gemm_fp8(ep_handle* h, int64_t num_rows, int32_t n, int32_t
  * 0), then cast_to_fp8 == 0: out = bf16 rows of width; cast_to_fp8 != 0
  * (width a multiple of 128): out = rows of width e4m3 codes and out_scales
  * (fp32 [num_rows][width/128]) by the dispatch's rule (amax = max(max|v|,
- * 1e-4), scale = amax/448; round_scale != 0: the next power of two). */
+ * 1e-4), scale = amax/448; round_scale != 0: the next power of two).  The maximum
+ * leaves NaN out, so that a NaN takes its own code only; an infinite value
+ * makes its 128 columns' scale infinite, its own code NaN and the others 0. */
 ep_status ep_swiglu(ep_handle* h, int64_t num_rows, int32_t width, const int32_t* group_count,
                     const int32_t* group_begin, const void* x, int64_t x_row_bytes, const float* row_weights,
                     int32_t cast_to_fp8, int32_t round_scale, void* out, int64_t out_row_bytes, float* out_scales,

@@ -285,3 +285,41 @@ def test_gradient_of_the_activation_at_large_gates(weighted):
         else:
             assert both.isnan().all()
     h.check()
+
+
+@pytest.mark.parametrize("round_scale", [False, True])
+def test_cast_of_nan_and_infinity(round_scale):
+    """NaN takes its own code and leaves the scale to the others; an infinity takes the scale of its 128 columns."""
+    rows, width = 4, 384
+    g = gen(21)
+    x = randn(g, (rows, 2 * width))
+    h, c, b = handle(1), i32([rows]), i32([0])
+
+    def cast(x):
+        r = ep.ep_swiglu(h, x, c, b, cast_to_fp8=True, round_scale=round_scale)
+        return r["out"].view(torch.uint8).clone(), r["out_scales"]
+    zeroed, special = x.clone(), x.clone()
+    for row, col in ((0, 5), (0, 127), (2, 200)):
+        zeroed[row, width + col] = 0
+        special[row, width + col] = float("nan")
+    codes, scales = cast(zeroed)
+    got, got_scales = cast(special)
+    assert torch.equal(got_scales, scales)
+    for row, col in ((0, 5), (0, 127), (2, 200)):
+        assert int(got[row, col]) & 0x7f == 0x7f
+        got[row, col] = codes[row, col]
+    assert torch.equal(got, codes)
+    codes, scales = cast(x)
+    special = x.clone()
+    special[1, 130], special[1, width + 130] = 1.0, float("inf")
+    special[3, 383], special[3, width + 383] = 1.0, float("-inf")
+    got, got_scales = cast(special)
+    h.check()
+    for row, first, col in ((1, 128, 130), (3, 256, 383)):
+        assert got_scales[row, first // 128] == float("inf")
+        assert int(got[row, col]) & 0x7f == 0x7f
+        got[row, col] = 0
+        assert ((got[row, first:first + 128] & 0x7f) == 0).all()
+        got[row, first:first + 128] = codes[row, first:first + 128]
+        got_scales[row, first // 128] = scales[row, first // 128]
+    assert torch.equal(got, codes) and torch.equal(got_scales, scales)
