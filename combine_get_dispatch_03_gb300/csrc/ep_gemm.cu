@@ -45,11 +45,12 @@ namespace {
 enum GemmForm { kForward = 0, kTransposed = 1, kWeightGrad = 2, kFp8 = 3 };
 
 // Steps (128 bytes of the contraction) that one accumulator sums in tensor memory before its sums are added up in
-// fp32 registers; 0: all of them.  FP8: one block, for its scales.  Weight gradient: 768 rows -- the tensor cores cut
+// fp32 registers; 0: all of them.  FP8: one block, for its scales.  Weight gradient: 512 rows -- the tensor cores cut
 // sums off instead of rounding them, and 2048 rows in one accumulator left 1.9e-6 of the result against 64 bits, 768
-// leave 7e-7 (512: 4.6e-7), for 1189 us instead of 1171 (1271) at 65536 rows, 32 experts of 2048 x 7168.  The other
+// 6.7e-7, 640 5.8e-7, 512 4.7e-7 (the same sums of products in fp32 by a library: 3.9e-7), for 1113 (768), 1164 and 1179 us
+// at 65536 rows, 32 experts of 2048 x 7168, and 1125 us where they leave through shared memory (staged_pays()).  The other
 // forms round to bf16, far above that.
-constexpr int segment_steps(int form) { return form == kFp8 ? 1 : form == kWeightGrad ? 12 : 0; }
+constexpr int segment_steps(int form) { return form == kFp8 ? 1 : form == kWeightGrad ? 8 : 0; }
 
 constexpr int kTileRows = 128;      // output rows per CTA
 constexpr int kMaxTileCols = 256;
@@ -79,8 +80,8 @@ struct GemmParams {
     int64_t x_scale_row_bytes;
     const float* w_scales;
     int32_t scales_ue8m0;
-    int32_t out_fp32;       // weight grad
-    int32_t accumulate;     // weight grad: then staged
+    int32_t out_fp32;       // weight grad: then staged
+    int32_t accumulate;     // weight grad
     int32_t wide_stores;    // output rows are 32-byte aligned
     int32_t tile_overhead;  // columns that a tile's width-independent cost is worth
     int32_t staged;         // blocks of 32 rows go out through shared memory
@@ -242,28 +243,6 @@ __device__ __forceinline__ void store_bf16(uint8_t* row, int col, int cols, cons
                 if (col + 16 * i + 8 * j + 8 <= cols)
                     *reinterpret_cast<uint4*>(p + 32 * i + 16 * j) =
                         make_uint4(w[8 * i + 4 * j], w[8 * i + 4 * j + 1], w[8 * i + 4 * j + 2], w[8 * i + 4 * j + 3]);
-        }
-    }
-}
-
-// The same in fp32.
-__device__ __forceinline__ void store_fp32(uint8_t* row, int col, int cols, const float (&v)[32], bool wide) {
-    float* p = reinterpret_cast<float*>(row) + col;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (col + 8 * i + 8 > cols) break;
-        float4 q[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            q[j] = make_float4(v[8 * i + 4 * j], v[8 * i + 4 * j + 1], v[8 * i + 4 * j + 2], v[8 * i + 4 * j + 3]);
-        if (wide) {
-            const uint32_t w[8] = {__float_as_uint(q[0].x), __float_as_uint(q[0].y), __float_as_uint(q[0].z),
-                                   __float_as_uint(q[0].w), __float_as_uint(q[1].x), __float_as_uint(q[1].y),
-                                   __float_as_uint(q[1].z), __float_as_uint(q[1].w)};
-            st_global_v8(p + 8 * i, w);
-        } else {
-            *reinterpret_cast<float4*>(p + 8 * i) = q[0];
-            *reinterpret_cast<float4*>(p + 8 * i + 4) = q[1];
         }
     }
 }
@@ -579,10 +558,7 @@ __device__ __forceinline__ void put_columns(const Roles& x, uint32_t box, const 
     } else if (lane_id() < at.rows && col < p.cols_dim) {
         const int64_t row = (FORM == kWeightGrad ? static_cast<int64_t>(at.group) * p.rows_dim : 0) + at.row + lane_id();
         uint8_t* out = static_cast<uint8_t*>(p.out) + row * p.out_row_bytes;
-        if (FORM == kWeightGrad && p.out_fp32)
-            store_fp32(out, col, p.cols_dim, v, p.wide_stores != 0);
-        else
-            store_bf16(out, col, p.cols_dim, v, p.wide_stores != 0);
+        store_bf16(out, col, p.cols_dim, v, p.wide_stores != 0);
     }
 }
 
@@ -902,16 +878,13 @@ Operand weight_across_operand(const void* base, uint64_t inner, uint64_t rows, u
 //   - FP8: its sums always wait for them.  k 512, 2048, 7168, n = 4096: 32 experts of 2048 rows (pairs) 258 and 213, 553 and
 //     495, 1519 and 1475; 64 of 700 (single CTAs) 183 and 153, 412 and 387, 1143 and 1156; 64 of 128 52 and 45, 114 and 114,
 //     329 and 342 (k 4096: 202 and 207, 727 and 707 of 700).
-//   - Weight gradient: up to one accumulator's rows.  32 experts, 2048 x 2048, 16, 256, 512, 1024 rows: 134 and 89 us, 134 and
-//     111, 152 and 136, 204 and 200; of 2048 rows, 2048 x 7168, 1150 and 1210.  Rows of the gradient that are not 128 bytes
-//     aligned: always (16 experts of 2048 rows, 1680 x 3480, 300 and 283).  Added to what is there: always, since the
-//     lanes would wait for it to arrive (the copy adds in the L2 cache, each element once): 16 rows 316 and 215, 2048 rows
-//     498 and 368.
+//   - Weight gradient in fp32: always.  Without and with, 32 experts, 2048 x 2048, 16, 512, 1024, 1536, 2048 rows: 134 and 89
+//     us, 136 and 135, 200 and 197, 284 and 265, 351 and 330; of 2048 rows, 2048 x 7168, 1179 and 1125; 16 experts of 2048
+//     rows, 1680 x 3480, 300 and 283.  Added to what is there the lanes would wait for it to arrive (the copy adds in the L2
+//     cache, each element once): 16 rows 316 and 215, 2048 rows 498 and 368.
 template <int FORM>
 bool staged_pays(bool pairs, const GemmParams& p, int64_t rows_each) {
-    if (FORM == kWeightGrad)
-        return p.out_fp32 && (p.accumulate || p.out_row_bytes % 128 != 0 ||
-                              p.groups.num_rows <= static_cast<int64_t>(p.groups.groups) * (segment_steps(FORM) * 64));
+    if (FORM == kWeightGrad) return p.out_fp32;
     if (rows_each < kRowBox) return false;  // no whole block
     if (FORM != kFp8) return !p.wide_stores || p.contraction <= 512;
     return pairs || p.contraction <= (rows_each > 2 * kTileRows ? 4096 : 2048);
