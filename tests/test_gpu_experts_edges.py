@@ -10,7 +10,7 @@ import torch
 
 from combine_get_dispatch_03_gb300 import ep
 from _parity import Guarded
-from test_gpu_experts import DEV, gen, handle, i32, randn
+from test_gpu_experts import DEV, gen, handle, i32, packed, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -342,3 +342,87 @@ def test_weight_gradient_is_as_good_as_sums_in_fp32(rows, n, k):
         at = slice(begin[e], begin[e] + counts[e])
         want = dy[at].double().t() @ x[at].double()
         assert float((dw[e].double() - want).norm() / want.norm()) < 5.3e-7
+
+
+def gradient_close(got, want, magnitude, rows, dtype):
+    """Errors of test_weight_gradient_is_as_good_as_sums_in_fp32's kind, element by element: 512 rows are 32 sums that are each
+    cut off by at most 2^-23 of the sum of magnitudes before them, and their fp32 sums round likewise; then dtype's rounding."""
+    steps = min(rows, 512) / 16 + rows / 512 + 2
+    tol = steps * 2.0 ** -23 * magnitude + (2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -23) * want.abs() + 1e-37
+    assert ((got.double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("counts,n,k,offset", [
+    ([900, 1100], 264, 1024, 0),         # pairs; rows of 128 bytes
+    ([900, 1100], 264, 1024, 16),        # a base that 16 bytes divide, not 32
+    ([900, 1100], 264, 1032, 16),
+    ([90, 1, 0, 70] * 16, 344, 4096, 0),  # single CTAs where pairs would do, several tiles each
+    ([1600, 0, 1500], 200, 72, 0),       # more than 1536 rows in a group of three
+], ids=["pairs", "offset", "odd", "single", "long"])
+def test_weight_gradient_of_many_tiles(counts, n, k, offset, dtype):
+    E = len(counts)
+    begin, rows = packed(counts, gap=1)
+    g = gen(n + k)
+    x, dy = randn(g, (rows, k)), randn(g, (rows, n))
+    for b, c in zip(begin, counts):
+        x[b - 1], dy[b - 1] = float("nan"), float("inf")
+    size = torch.empty((), dtype=dtype).element_size()
+    raw = Guarded((E * n * k * size + offset,), torch.uint8)
+    out = raw.t[offset:].view(dtype).view(E, n, k)
+    h = handle(E)
+    ep.ep_grouped_gemm_wgrad(h, dy, x, i32(counts), i32(begin), out=out)
+    h.check()
+    raw.check()
+    assert (raw.t[:offset] == raw.fill).all()
+    for e, (b, c) in enumerate(zip(begin, counts)):
+        ye, xe = dy[b:b + c].double(), x[b:b + c].double()
+        gradient_close(out[e], ye.t() @ xe, ye.abs().t() @ xe.abs(), c, dtype)
+
+
+@pytest.mark.parametrize("n", [64, 264])
+@pytest.mark.parametrize("counts,begin,rows", [([4, 100], [0, 4], 60), ([4, 5], [0, 70], 64), ([4, -3], [0, 4], 64),
+                                               ([4, 5], [-1, 4], 64), ([40, 60], [0, 30], 100)])
+def test_weight_gradient_of_groups_that_do_not_fit(counts, begin, rows, n):
+    """The rows that exist are summed, and the rest is reported; groups may share rows, since none is written."""
+    g = gen(n)
+    x, dy = randn(g, (rows, 72)), randn(g, (rows, n))
+    h = handle(2)
+    dw = ep.ep_grouped_gemm_wgrad(h, dy, x, i32(counts), i32(begin))
+    good = [max(0, min(c, rows - b)) if b >= 0 and c >= 0 else 0 for c, b in zip(counts, begin)]
+    assert h.status() == (0 if good == counts else 2)
+    for e, (b, c) in enumerate(zip(begin, good)):
+        ye, xe = dy[max(b, 0):max(b, 0) + c].double(), x[max(b, 0):max(b, 0) + c].double()
+        gradient_close(dw[e], ye.t() @ xe, ye.abs().t() @ xe.abs(), c, torch.float32)
+
+
+def test_weight_gradient_added_to_subnormals():
+    """The additions in the L2 cache keep subnormals: what dw holds of them, and sums that become one."""
+    h, c, b = handle(2), i32([30, 34]), i32([0, 30])
+    x, dy = torch.zeros((64, 64), dtype=torch.bfloat16, device=DEV), torch.zeros((64, 64), dtype=torch.bfloat16, device=DEV)
+    dw = torch.full((2, 64, 64), 1e-40, device=DEV)
+    start = dw.clone()
+    ep.ep_grouped_gemm_wgrad(h, dy, x, c, b, out=dw, accumulate=True)
+    assert torch.equal(dw, start)
+    x[[0, 30]], dy[[0, 30]] = 2.0 ** -27, -(2.0 ** -99)
+    dw.fill_(2.0 ** -126 * 1.5)
+    ep.ep_grouped_gemm_wgrad(h, dy, x, c, b, out=dw, accumulate=True)
+    h.check()
+    assert (dw == 2.0 ** -127).all()  # 1.5 * 2^-126 - 2^-126
+    ep.ep_grouped_gemm_wgrad(h, dy, x, c, b, out=dw, accumulate=True)
+    h.check()
+    assert (dw == -(2.0 ** -127)).all()
+
+
+def test_message_rows_without_expected_rows():
+    """A message buffer's capacity stands in for the rows that are expected: the bits do not depend on it."""
+    E, cap, n, k = 6, 700, 136, 256
+    g = gen(3)
+    x, w = randn(g, (2, 3, cap, k)), randn(g, (E, n, k), 0.1)
+    c = i32([1, 0, 130, 3, 64, 2])
+    h = handle(E, 2)
+    outs = [torch.zeros((2, 3, cap, n), dtype=torch.bfloat16, device=DEV) for _ in range(3)]
+    for out, expected in zip(outs, (0, 1, 33)):
+        ep.ep_grouped_gemm(h, x, w, c, out=out, expected_rows=expected)
+    h.check()
+    assert bool(outs[0].any()) and torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
