@@ -14,17 +14,18 @@
 // accumulators of 256 columns let the next tile's products run under this tile's stores.
 //
 // What bounds it, measured on a GB300 (1946.7 TFLOP/s bf16, 6787 GB/s copied):
-//   - many rows an expert, bf16: the tensor cores, at the clock that the power limit leaves.  8 experts of 2048 rows,
-//     4096 x 7168: 526 to 542 us, 1770 to 1830 TFLOP/s, 512 to 516 cycles a stage where a stage's products take
-//     512; the gradient of the rows 510 to 524 us, of the weights 550 to 573 us (its 0.94 GB of fp32 results
-//     and the ends of groups cost the rest).
-//   - few rows an expert: memory, the weights.  32 experts of 64 rows, 4096 x 7168 bf16: 286 us, 6.7 TB/s.
+//   - many rows an expert, bf16: the tensor cores, at the clock that the power limit leaves, so that times go by the card
+//     and by how long it has been busy.  8 experts of 2048 rows, 4096 x 7168: 521 to 549 us, 1750 to 1850 TFLOP/s, 512
+//     to 516 cycles a stage where a stage's products take 512; the gradient of the rows 510 to 572 us, of the weights
+//     557 to 639 us (its 0.94 GB of fp32 results and the ends of groups cost the rest; 573 to 591 in bf16).
+//   - few rows an expert: memory, the weights.  32 experts of 64 rows, 4096 x 7168 bf16: 286 to 309 us, 6.2 to 6.7 TB/s.
 //   - FP8: a block's sums go from tensor memory through registers, 32768 FMAs a stage and CTA at 128 a cycle; with the
 //     way there and back between the products' thread and the eight warps a stage takes about 770 cycles for
-//     512 of products.  The same 8 experts: 362 us, 2660 TFLOP/s; 64 experts of 128 rows read from messages: 334 us,
-//     6.0 TB/s.
+//     512 of products.  The same 8 experts: 340 to 362 us, 2660 to 2820 TFLOP/s; 64 experts of 128 rows read from
+//     messages: 308 to 334 us, 6.0 to 6.5 TB/s (375 to 385 where half of the experts have more than 128).
 //   - short contractions and few rows: the results' way out (staged_pays()).  64 experts of 1024 rows, 4096 x 256 bf16:
-//     138 us, 5.1 TB/s; gradients of 32 experts of 16 rows, 2048 x 2048: 89 us, 6.0 TB/s.
+//     128 to 138 us, 5.1 to 5.5 TB/s; gradients of 32 experts of 16 rows, 2048 x 2048: 89 us, 6.0 TB/s.
+//   - rows four bytes apart: the two warps that copy them, a round trip to memory for every 8 or 16 rows (copy_rows()).
 //
 // Two loads of 16 KB a stage (one an operand) rather than smaller ones: a load costs the issuing thread about
 // 95 cycles.  64 columns of an accumulator a read in the FP8 form: 292 cycles for 128 columns and their FMAs in eight
@@ -420,7 +421,8 @@ __device__ __forceinline__ void multiply(const Roles& x) {
 
 // Two warps: row operands whose rows are not 16 bytes apart (messages of some hidden sizes), in words of four bytes,
 // into the place and order in which a tensor-map load puts them.  A warp copies a row's 128 bytes at a time, several
-// rows in flight.
+// rows in flight, and waits for them: FP8, 32 experts, n 2048, rows of 2944 bytes 53, 284 and 1500 us at 16, 128 and 1024
+// rows an expert, where loads by tensor maps of rows of 3584 take 43, 50 and 200.
 template <int FORM>
 __device__ __forceinline__ void copy_rows(const Roles& x, int warp) {
     const GemmParams& p = x.p;
@@ -880,8 +882,8 @@ Operand weight_across_operand(const void* base, uint64_t inner, uint64_t rows, u
 //     329 and 342 (k 4096: 202 and 207, 727 and 707 of 700).
 //   - Weight gradient in fp32: always.  Without and with, 32 experts, 2048 x 2048, 16, 512, 1024, 1536, 2048 rows: 134 and 89
 //     us, 136 and 135, 200 and 197, 284 and 265, 351 and 330; of 2048 rows, 2048 x 7168, 1179 and 1125; 16 experts of 2048
-//     rows, 1680 x 3480, 300 and 283.  Added to what is there the lanes would wait for it to arrive (the copy adds in the L2
-//     cache, each element once): 16 rows 316 and 215, 2048 rows 498 and 368.
+//     rows, 1680 x 3480, 300 and 283 (768 rows an accumulator).  Added to what is there the lanes would wait for it to
+//     arrive (the copy adds in the L2 cache, each element once): 16 rows 316 and 215, 2048 rows 498 and 368 (768).
 template <int FORM>
 bool staged_pays(bool pairs, const GemmParams& p, int64_t rows_each) {
     if (FORM == kWeightGrad) return p.out_fp32;

@@ -13,9 +13,10 @@
 // received row into shared memory with one bulk copy and writes it with one bulk copy per slot, so that it reads
 // every row once however many experts want it; the reduce holds a row's columns in registers.
 //
-// Measured on a GB300 (6787 GB/s copied): 86 thousand received rows of 14336 bytes into 131072 expert rows, layout
-// 22 us, gather 454 us, 6.9 TB/s; the reduce of 16288 rows of 4096 bytes into 13.5 thousand 22 us, 5.6 TB/s
-// (a row or two a warp: latency).
+// Measured on a GB300 (6787 GB/s copied): 89 thousand received rows of 14336 bytes into 131072 expert rows, layout
+// 13 us in a CUDA graph and 22 in calls, gather 454 to 459 us, 6.9 TB/s; of 7392 bytes (FP8 with scales) 521 us, 3.1 TB/s, the
+// scales' small stores before each row's; the reduce of as many bf16 rows 541 us, 5.8 TB/s, and of 16288 rows of 4096
+// bytes into 13.5 thousand 22 to 28 us, 4.4 to 5.6 TB/s (a row or two a warp: latency).
 #include "ep_groups.cuh"
 #include "ep_handle.h"
 #include "ep_trace.h"
@@ -312,7 +313,7 @@ struct ReduceParams {
 __global__ void __launch_bounds__(kRowThreads) rows_reduce_kernel(const ReduceParams p) {
     pdl_enter();
     // Loads in flight per lane: four column blocks of one row.  Two rows at once took registers from a third CTA per SM
-    // and were slower (16288 rows of 4096 bytes: 23.9 against 22.0 us).
+    // and were slower (16288 rows of 4096 bytes: 23.9 against 22.0 us on one card).
     constexpr int kCols = 4;
     const Received q = received_rows(p.num_recv, p.ranks, p.cap);
     const int warps = gridDim.x * kRowWarps;

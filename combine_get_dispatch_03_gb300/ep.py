@@ -633,7 +633,8 @@ def ep_grouped_gemm(h: Handle, x: torch.Tensor, w: torch.Tensor, group_count, gr
     """Grouped product: each expert's rows times its bf16 weights w [E][n][k] (or, transposed, [E][k][n]).
 
     x is [rows][k] or a view with evenly spaced rows, such as the packed_recv_x of a bf16 message buffer; out has
-    x's leading axes.  Rows outside every group are left as they are."""
+    x's leading axes.  Rows outside every group are left as they are.  expected_rows (0: rows / E) guides the choice of
+    tiles: with a message buffer, whose rows / E is its capacity, give the rows that an expert is expected to hold."""
     d = h.device
     if w.dim() != 3:
         raise ValueError(f"w must be [E][n][k], got {tuple(w.shape)}")
@@ -673,7 +674,8 @@ def ep_grouped_gemm_fp8(h: Handle, x: torch.Tensor, x_scales: torch.Tensor, w: t
     """Grouped product in FP8 e4m3: x rows with one scale per 128 channels, w [E][n][k] with one per 128 x 128.
 
     x_scales is float32 [rows][k/128], or uint8 with the UE8M0 exponent bytes in its first k/128 columns; the views
-    that ll_views() gives of a message buffer are read in place (for fp32 scales: scales.view(torch.float32))."""
+    that ll_views() gives of a message buffer are read in place (for fp32 scales: scales.view(torch.float32)).
+    expected_rows as in ep_grouped_gemm()."""
     d = h.device
     if w.dim() != 3:
         raise ValueError(f"w must be [E][n][k], got {tuple(w.shape)}")

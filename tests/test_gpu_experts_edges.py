@@ -131,6 +131,25 @@ def test_wait_that_runs_out(ctas, transposed):
     after_a_timeout(h, ctas)
 
 
+def test_wait_that_runs_out_beside_copied_rows():
+    """The same where two warps copy rows that lie four bytes apart."""
+    E, n, k = 4, 256, 1 << 18
+    h = handle(E, max_sms=1)
+    x = torch.ones((E, k + 2), dtype=torch.bfloat16, device=DEV)[:, :k]
+    w = torch.ones((E, n, k), dtype=torch.bfloat16, device=DEV)
+    c, b = i32([1] * E), i32(list(range(E)))
+    out = Guarded((E, n), torch.bfloat16)
+    ep.ep_selftest_wait_limit(h, 1000)
+    ep.ep_grouped_gemm(h, x, w, c, b, out=out.t)
+    assert h.status() == 3
+    out.check()
+    ep.ep_selftest_wait_limit(h)
+    ep.ep_grouped_gemm(h, x, w, c, b, out=out.t)
+    h.check()
+    assert (out.t == k).all()
+    after_a_timeout(h, 1)
+
+
 @pytest.mark.parametrize("ctas", [1, 2], ids=["single", "pair"])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_wait_for_the_end_of_a_group_that_runs_out(ctas, dtype):
