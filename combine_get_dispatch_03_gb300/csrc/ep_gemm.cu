@@ -1,11 +1,15 @@
 // ep_gemm.cu -- matrix products grouped by expert, with ragged groups (sm_103a tensor cores).
 //
 // Rows of all experts lie in one array; expert e has rows [begin[e], begin[e] + count[e]) and its own
-// weights.  Four forms share one persistent kernel:
+// weights.  Six forms share one persistent kernel:
 //   forward       out[r][j] = sum_c x[r][c] * w[e][j][c]          bf16, both operands contraction-major
 //   transposed    out[r][j] = sum_c x[r][c] * w[e][c][j]          bf16, the weights read across (gradient of the rows)
 //   weight grad   dw[e][j][c] = sum_r dy[r][j] * x[r][c]          bf16, both operands read across, over a group's rows
 //   fp8           out[r][j] = sum_b sx[r][b] * sw[e][j/128][b] * sum_{c in b} x[r][c] * w[e][j][c]    e4m3, blocks b of 128
+// and the forward form with an epilogue (finish_columns()), v = x w^T + bias:
+//   activated     out[r][j] = act(v[r][j]) * row_weights[r] + residual[r][j]
+//   gated         out[r][j] = act(v[r][j]) * v[r][width + j] * row_weights[r] + residual[r][j]
+// A gated tile's columns are half gate, half up: both accumulators of an output lie in the same lane of tensor memory.
 //
 // Work is cut into output tiles of 128 rows (256 for a pair of CTAs) by 64, 128 or 256 columns, taken
 // in turn by the CTAs of one resident wave.  In a CTA one thread loads operand tiles with tensor maps into a
@@ -35,15 +39,58 @@
 // device arrays, so that no count has to reach the host.
 #include <cudaTypedefs.h>
 
+#include "ep_act.cuh"
 #include "ep_groups.cuh"
 #include "ep_handle.h"
+#include "ep_maps.h"
 #include "ep_tc.cuh"
 #include "ep_trace.h"
 
 namespace ep {
+
+// The driver's tensor-map encoder, looked up once (the library does not link against libcuda).
+static PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }();
+    return fn;
+}
+
+ep_status encode(CUtensorMap* map, const Operand& o) {
+    const PFN_cuTensorMapEncodeTiled_v12000 fn = map_encoder();
+    if (fn == nullptr) return fail(EP_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
+    cuuint64_t size[4], stride[3];
+    cuuint32_t box[4], step[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 4; ++i) size[i] = o.size[i], box[i] = o.box[i];
+    for (int i = 0; i < 3; ++i) stride[i] = o.stride[i];
+    const CUtensorMapDataType type = o.element == Element::kFp8    ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : o.element == Element::kFp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                                                   : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    CUresult rc = CUDA_SUCCESS;
+    for (int attempt = 0; attempt < 2; ++attempt) {
+        rc = fn(map, type, o.dims, const_cast<void*>(o.base), size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (rc != CUDA_ERROR_INVALID_CONTEXT) break;
+        // A thread that has not used its device yet has no context, and the encoder, unlike the runtime's calls, makes
+        // none current.
+        int device = 0;
+        cudaError_t err = cudaGetDevice(&device);
+        if (err == cudaSuccess) err = cudaSetDevice(device);
+        if (err != cudaSuccess) return cuda_fail(err, "making the device's context current");
+    }
+    if (rc != CUDA_SUCCESS) return fail(EP_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(rc));
+    return EP_OK;
+}
+
 namespace {
 
-enum GemmForm { kForward = 0, kTransposed = 1, kWeightGrad = 2, kFp8 = 3 };
+enum GemmForm { kForward = 0, kTransposed = 1, kWeightGrad = 2, kFp8 = 3, kActivated = 4, kGated = 5 };
+constexpr bool has_epilogue(int form) { return form == kActivated || form == kGated; }
 
 // Steps (128 bytes of the contraction) that one accumulator sums in tensor memory before its sums are added up in
 // fp32 registers; 0: all of them.  FP8: one block, for its scales.  Weight gradient: 512 rows -- the tensor cores cut
@@ -91,6 +138,15 @@ struct GemmParams {
     int64_t a_row_bytes;
     int32_t* status;
     uint64_t wait_limit_ns;
+    // the epilogue of the forms that have one; each may be NULL
+    const float* bias;          // [groups][n]
+    const float* row_weights;   // [num_rows]
+    const uint8_t* residual;    // bf16 rows like the output's
+    int64_t residual_row_bytes;
+    uint8_t* pre;               // v in bf16, rows of n
+    int64_t pre_row_bytes;
+    int32_t pre_wide;           // its rows are 32-byte aligned
+    int32_t act;
 };
 
 // Tensor maps of the two operands: loads of kBox output elements, and smaller ones; and of the results, boxes of 32
@@ -142,6 +198,12 @@ struct Table {
     int32_t* begin;   // [groups]
 };
 
+// Output columns of a tile of `cols` columns of products, and the fewest columns of products.
+template <int FORM>
+__device__ __forceinline__ int out_cols(int cols) { return FORM == kGated ? cols / 2 : cols; }
+template <int FORM, int CG>
+constexpr int min_cols() { return kColBox * (FORM == kGated ? 2 : CG); }
+
 template <int FORM, int CG>
 __device__ __forceinline__ Tile decode(const Table& t, const GemmParams& p, const Control& ctl, int tile) {
     Tile r;
@@ -152,10 +214,10 @@ __device__ __forceinline__ Tile decode(const Table& t, const GemmParams& p, cons
     r.row0 = t.begin[lo];
     r.rows = t.count[lo];
     // row tiles turn fastest: CTAs side by side share a weight tile
-    r.n0 = in / row_tiles * ctl.tile_cols;
+    r.n0 = in / row_tiles * out_cols<FORM>(ctl.tile_cols);
     // the last tile across is no wider than it has to be
     r.cols = ctl.tile_cols;
-    while (r.cols > kColBox * CG && 2 * (p.cols_dim - r.n0) <= r.cols) r.cols >>= 1;
+    while (r.cols > min_cols<FORM, CG>() && 2 * (p.cols_dim - r.n0) <= out_cols<FORM>(r.cols)) r.cols >>= 1;
     r.m0 = in % row_tiles * (kTileRows * CG);
     if constexpr (FORM == kWeightGrad) r.steps = (r.rows + 63) >> 6;
     else if constexpr (FORM == kFp8) r.steps = (p.contraction + 127) >> 7;
@@ -205,13 +267,14 @@ __device__ __forceinline__ void build_table(const Table& t, const GemmParams& p,
         const int workers = gridDim.x / CG;
         int best = kMaxTileCols;
         int64_t best_cost = INT64_MAX;
-        for (int cols = kMaxTileCols; cols >= kColBox * CG; cols >>= 1) {
-            const int64_t tiles = static_cast<int64_t>(total) * ((p.cols_dim + cols - 1) / cols);
+        for (int cols = kMaxTileCols; cols >= min_cols<FORM, CG>(); cols >>= 1) {
+            const int across = out_cols<FORM>(cols);
+            const int64_t tiles = static_cast<int64_t>(total) * ((p.cols_dim + across - 1) / across);
             const int64_t cost = (tiles + workers - 1) / workers * (cols + p.tile_overhead);
             if (cost < best_cost) best_cost = cost, best = cols;
         }
         ctl.tile_cols = best;
-        ctl.col_tiles = (p.cols_dim + best - 1) / best;
+        ctl.col_tiles = (p.cols_dim + out_cols<FORM>(best) - 1) / out_cols<FORM>(best);
         ctl.tiles = total * ctl.col_tiles;
     }
 }
@@ -244,6 +307,24 @@ __device__ __forceinline__ void store_bf16(uint8_t* row, int col, int cols, cons
                 if (col + 16 * i + 8 * j + 8 <= cols)
                     *reinterpret_cast<uint4*>(p + 32 * i + 16 * j) =
                         make_uint4(w[8 * i + 4 * j], w[8 * i + 4 * j + 1], w[8 * i + 4 * j + 2], w[8 * i + 4 * j + 3]);
+        }
+    }
+}
+
+// 32 fp32 columns of one output row, at once; columns at or past `cols` (a multiple of 8) are left out.
+__device__ __forceinline__ void store_fp32(uint8_t* row, int col, int cols, const float (&v)[32], bool wide) {
+    uint8_t* p = row + 4 * static_cast<int64_t>(col);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (col + 8 * i + 8 > cols) break;
+        const uint32_t q[8] = {__float_as_uint(v[8 * i]), __float_as_uint(v[8 * i + 1]), __float_as_uint(v[8 * i + 2]),
+                               __float_as_uint(v[8 * i + 3]), __float_as_uint(v[8 * i + 4]), __float_as_uint(v[8 * i + 5]),
+                               __float_as_uint(v[8 * i + 6]), __float_as_uint(v[8 * i + 7])};
+        if (wide) {
+            st_global_v8(p + 32 * i, q);
+        } else {
+            *reinterpret_cast<uint4*>(p + 32 * i) = make_uint4(q[0], q[1], q[2], q[3]);
+            *reinterpret_cast<uint4*>(p + 32 * i + 16) = make_uint4(q[4], q[5], q[6], q[7]);
         }
     }
 }
@@ -328,7 +409,16 @@ __device__ __forceinline__ void load_operands(const Roles& x) {
                     for (int c = 0; c < small_boxes; ++c)
                         tma_load_2d<CG>(a + c * (kRowBox * kRowBytes), &x.maps.a_small, k0, q.row0 + my_m0 + c * kRowBox, bar);
                 }
-                for (int c = 0; c < cols;) {
+                if constexpr (FORM == kGated) {
+                    // the tile's first half of columns are gates, the second their ups (of a pair: each CTA has one half)
+                    const int half = q.cols / 2;
+                    for (int c = 0; c < cols;) {
+                        const int at = q.n0 + (cb + c < half ? cb + c : p.cols_dim + cb + c - half);
+                        tma_load_3d<CG>(b + c * kRowBytes, half >= kBox ? &x.maps.b : &x.maps.b_small, k0, at, q.group, bar);
+                        c += half >= kBox ? kBox : kColBox;
+                    }
+                }
+                for (int c = 0; FORM != kGated && c < cols;) {
                     const int at = q.n0 + cb + c;
                     if (FORM == kTransposed && c + kBox <= cols && at + kBox <= p.b_chunked) {
                         tma_load_4d<CG>(b + c * kRowBytes, &x.maps.b, 0, k0, at / 64, q.group, bar);
@@ -560,7 +650,74 @@ __device__ __forceinline__ void put_columns(const Roles& x, uint32_t box, const 
     } else if (lane_id() < at.rows && col < p.cols_dim) {
         const int64_t row = (FORM == kWeightGrad ? static_cast<int64_t>(at.group) * p.rows_dim : 0) + at.row + lane_id();
         uint8_t* out = static_cast<uint8_t*>(p.out) + row * p.out_row_bytes;
-        store_bf16(out, col, p.cols_dim, v, p.wide_stores != 0);
+        if (FORM == kActivated && p.out_fp32) store_fp32(out, col, p.cols_dim, v, p.wide_stores != 0);
+        else store_bf16(out, col, p.cols_dim, v, p.wide_stores != 0);
+    }
+}
+
+// v += bias of 32 columns from `col`, in pieces of 8 that are there.  All lanes read the same words.
+__device__ __forceinline__ void add_bias(const float* bias, int col, int cols, float (&v)[32]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (col + 8 * i + 8 > cols) break;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[8 * i + j] += __ldg(bias + col + 8 * i + j);
+    }
+}
+
+// The epilogue of 32 output columns of a lane's row, from column `c` of its warp's part of the tile: v holds the sums
+// (gated: of the gates, and `up` of the ups) and gets what is written.
+template <int FORM>
+__device__ __forceinline__ void finish_columns(const GemmParams& p, const Place& at, int c, float (&v)[32], float (&up)[32]) {
+    const int col = at.col + c;
+    if (col >= p.cols_dim) return;
+    const int n = FORM == kGated ? 2 * p.cols_dim : p.cols_dim;
+    const int64_t row = static_cast<int64_t>(at.row) + lane_id();
+    const bool in = lane_id() < at.rows;
+    if (p.bias) {
+        const float* bias = p.bias + static_cast<int64_t>(at.group) * n;
+        add_bias(bias, col, p.cols_dim, v);
+        if (FORM == kGated) add_bias(bias + p.cols_dim, col, p.cols_dim, up);
+    }
+    if (p.pre && in) {
+        uint8_t* pre = p.pre + row * p.pre_row_bytes;
+        store_bf16(pre, col, p.cols_dim, v, p.pre_wide != 0);
+        if (FORM == kGated) store_bf16(pre + 2 * static_cast<int64_t>(p.cols_dim), col, p.cols_dim, up, p.pre_wide != 0);
+    }
+    switch (p.act) {  // the same for all: a loop each, not a choice for each value
+        case EP_ACT_RELU:
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = activate(EP_ACT_RELU, v[i]);
+            break;
+        case EP_ACT_SILU:
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = activate(EP_ACT_SILU, v[i]);
+            break;
+        case EP_ACT_GELU:
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = activate(EP_ACT_GELU, v[i]);
+            break;
+        default: break;
+    }
+    if (FORM == kGated) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= up[i];
+    }
+    if (p.row_weights) {
+        const float w = in ? p.row_weights[row] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= w;
+    }
+    if (p.residual && in) {
+        const int4* from = reinterpret_cast<const int4*>(p.residual + row * p.residual_row_bytes + 2 * static_cast<int64_t>(col));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (col + 8 * i + 8 > p.cols_dim) break;
+            float r[8];
+            unpack8(ld_stream_v4(from + i), r);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[8 * i + j] += r[j];
+        }
     }
 }
 
@@ -607,7 +764,7 @@ __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
     for (int tile = x.worker; ok && tile < ctl.tiles; tile += x.workers) {
         const Tile q = decode<FORM, CG>(t, p, ctl, tile);
         if (FORM == kWeightGrad && p.accumulate && q.steps == 0) continue;  // nothing to add
-        const int cols_half = q.cols / 2;
+        const int cols_half = out_cols<FORM>(q.cols) / 2;
         const int in_group = q.m0 + static_cast<int>(x.rank) * kTileRows + quarter * 32;
         const int rows = min(32, max(0, (FORM == kWeightGrad ? p.rows_dim : q.rows) - in_group));
         const Place at = {(FORM == kWeightGrad ? 0 : q.row0) + in_group, q.n0 + half * cols_half, q.group,
@@ -620,7 +777,16 @@ __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
             for (int c = 0; c < cols_half; c += 32) {
                 uint32_t u[32];
                 __syncwarp();
-                tc_ld32(lane_base + buf * kMaxTileCols + half * cols_half + c, u);
+                const uint32_t from = lane_base + buf * kMaxTileCols + half * cols_half + c;
+                tc_ld32(from, u);
+                float up[32];  // gated
+                if constexpr (FORM == kGated) {
+                    uint32_t u2[32];
+                    tc_ld32(from + q.cols / 2, u2);
+                    tc_wait_ld(u2);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) up[i] = __uint_as_float(u2[i]);
+                }
                 tc_wait_ld(u);
                 if (c + 32 >= cols_half) {  // read out: the accumulator is free before the last stores
                     tc_fence_before();
@@ -630,6 +796,7 @@ __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
                 float v[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+                if constexpr (has_epilogue(FORM)) finish_columns<FORM>(p, at, c, v, up);
                 if (staged) put_columns<FORM, true>(x, box, at, c, v);
                 else put_columns<FORM, false>(x, box, at, c, v);
             }
@@ -795,56 +962,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 // Host side
 // ---------------------------------------------------------------------------
 
-// The driver's tensor-map encoder, looked up once (the library does not link against libcuda).
-PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
-    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
-            found != cudaDriverEntryPointSuccess)
-            f = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    }();
-    return fn;
-}
-
-enum class Element { kBf16, kFp8, kFp32 };
-
-struct Operand {
-    const void* base;
-    Element element;
-    int dims;
-    uint64_t size[4];
-    uint64_t stride[3];  // bytes
-    uint32_t box[4];
-};
-
-ep_status encode(CUtensorMap* map, const Operand& o) {
-    const PFN_cuTensorMapEncodeTiled_v12000 fn = map_encoder();
-    if (fn == nullptr) return fail(EP_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
-    cuuint64_t size[4], stride[3];
-    cuuint32_t box[4], step[4] = {1, 1, 1, 1};
-    for (int i = 0; i < 4; ++i) size[i] = o.size[i], box[i] = o.box[i];
-    for (int i = 0; i < 3; ++i) stride[i] = o.stride[i];
-    const CUtensorMapDataType type = o.element == Element::kFp8    ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                     : o.element == Element::kFp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                                                   : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    CUresult rc = CUDA_SUCCESS;
-    for (int attempt = 0; attempt < 2; ++attempt) {
-        rc = fn(map, type, o.dims, const_cast<void*>(o.base), size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-        if (rc != CUDA_ERROR_INVALID_CONTEXT) break;
-        // A thread that has not used its device yet has no context, and the encoder, unlike the runtime's calls, makes
-        // none current.
-        int device = 0;
-        cudaError_t err = cudaGetDevice(&device);
-        if (err == cudaSuccess) err = cudaSetDevice(device);
-        if (err != cudaSuccess) return cuda_fail(err, "making the device's context current");
-    }
-    if (rc != CUDA_SUCCESS) return fail(EP_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(rc));
-    return EP_OK;
-}
-
 // Rows [rows][inner] with a row stride.
 Operand row_operand(const void* base, bool fp8, uint64_t inner, uint64_t rows, uint64_t row_bytes, uint32_t box_rows) {
     return {base, fp8 ? Element::kFp8 : Element::kBf16, 2, {inner, rows, 1, 1}, {row_bytes, 0, 0}, {fp8 ? 128u : 64u, box_rows, 1, 1}};
@@ -887,7 +1004,7 @@ Operand weight_across_operand(const void* base, uint64_t inner, uint64_t rows, u
 template <int FORM>
 bool staged_pays(bool pairs, const GemmParams& p, int64_t rows_each) {
     if (FORM == kWeightGrad) return p.out_fp32;
-    if (rows_each < kRowBox) return false;  // no whole block
+    if (rows_each < kRowBox || p.out_fp32) return false;  // no whole block; fp32 rows (activated form) go out by lanes
     if (FORM != kFp8) return !p.wide_stores || p.contraction <= 512;
     return pairs || p.contraction <= (rows_each > 2 * kTileRows ? 4096 : 2048);
 }
@@ -917,13 +1034,16 @@ bool wgrad_on_pairs(const ep_handle* h, const GemmParams& p) {
     return best[1] <= best[0];
 }
 
+// Forms that read rows in words of four bytes.
+constexpr bool has_words(int form) { return form != kWeightGrad && !has_epilogue(form); }
+
 template <int FORM>
 cudaError_t plan_form(LaunchPlan* plan) {
     cudaError_t err = cudaFuncSetAttribute(grouped_gemm_kernel<FORM, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (err == cudaSuccess)
         err = cudaFuncSetAttribute(grouped_gemm_kernel<FORM, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-    if (err == cudaSuccess && FORM != kWeightGrad)
-        err = cudaFuncSetAttribute(grouped_gemm_kernel<FORM, 1, FORM != kWeightGrad>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (err == cudaSuccess && has_words(FORM))
+        err = cudaFuncSetAttribute(grouped_gemm_kernel<FORM, 1, has_words(FORM)>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    kMaxSmem);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
@@ -939,7 +1059,8 @@ cudaError_t plan_form(LaunchPlan* plan) {
     int pairs = 0;
     if (plan->num_sms >= 2) err = cudaOccupancyMaxActiveClusters(&pairs, grouped_gemm_kernel<FORM, 2>, &cfg);
     if (err != cudaSuccess) return err;
-    if (pairs < plan->gemm_pairs) plan->gemm_pairs = pairs;
+    int* const least = has_epilogue(FORM) ? &plan->act_pairs : &plan->gemm_pairs;
+    if (pairs < *least) *least = pairs;
     return cudaSuccess;
 }
 
@@ -953,16 +1074,25 @@ cudaError_t plan_gemm(LaunchPlan* plan) {
     return err;
 }
 
+// The same for the forms with an epilogue, whose kernels the others' callers do not load.
+cudaError_t plan_act(LaunchPlan* plan) {
+    plan->act_pairs = plan->num_sms / 2;
+    const cudaError_t err = plan_form<kActivated>(plan);
+    return err == cudaSuccess ? plan_form<kGated>(plan) : err;
+}
+
 template <int FORM>
 ep_status launch(ep_handle* h, const Operand& a, const Operand& a_small, const Operand& b, const Operand& b_small,
                  GemmParams p, int64_t rows_each, cudaStream_t stream) {
     DeviceGuard guard(h->device);
-    const ep_status planned = plan_once(&h->plan.gemm_ready, [h] { return plan_gemm(&h->plan); });
+    const ep_status planned = has_epilogue(FORM) ? plan_once(&h->plan.act_ready, [h] { return plan_act(&h->plan); })
+                                                 : plan_once(&h->plan.gemm_ready, [h] { return plan_gemm(&h->plan); });
     if (planned != EP_OK) return planned;
+    const int most_pairs = has_epilogue(FORM) ? h->plan.act_pairs : h->plan.gemm_pairs;
     Maps m;
     const bool pairs = FORM == kWeightGrad ? wgrad_on_pairs(h, p)
                                            : !p.a_words && rows_each >= (FORM == kFp8 ? kPairRowsFp8 : kTileRows + 1) &&
-                                                 h->plan.gemm_pairs > 0;
+                                                 most_pairs > 0;
     // A tile's stages wait for their operands, and a tile is worth the rows that a CTA loads beside its columns: a pair's
     // 128 beside half of the columns (weight gradient of 8 experts, 560 x 2448, 83592 rows: 401 us with 32 columns'
     // worth, 257 with 128, 246 with 256), a single CTA's as many as a group's tiles have, at least one load's (FP8, 64
@@ -998,11 +1128,11 @@ ep_status launch(ep_handle* h, const Operand& a, const Operand& a_small, const O
     // 4096 x 4096, single against pair: bf16 185 and 185 us at 128 rows an expert, 222 and 203 at 200, 1361 and
     // 1241 at 2048; FP8 106 and 125 at 128, 363 and 388 at 700, 567 and 557 at 1024, 1105 and 1034 at 2048.
     cudaError_t err;
-    if (FORM != kWeightGrad && p.a_words)
-        err = launch_kernel(grouped_gemm_kernel<FORM, 1, FORM != kWeightGrad>, dim3(h->plan.num_sms), dim3(kGemmThreads),
+    if (has_words(FORM) && p.a_words)
+        err = launch_kernel(grouped_gemm_kernel<FORM, 1, has_words(FORM)>, dim3(h->plan.num_sms), dim3(kGemmThreads),
                             kMaxSmem, stream, 1, m, p);
     else if (pairs)
-        err = launch_kernel(grouped_gemm_kernel<FORM, 2>, dim3(2 * h->plan.gemm_pairs), dim3(kGemmThreads), kMaxSmem, stream,
+        err = launch_kernel(grouped_gemm_kernel<FORM, 2>, dim3(2 * most_pairs), dim3(kGemmThreads), kMaxSmem, stream,
                             2, m, p);
     else
         err = launch_kernel(grouped_gemm_kernel<FORM, 1>, dim3(h->plan.num_sms), dim3(kGemmThreads), kMaxSmem, stream, 1, m, p);
@@ -1084,6 +1214,51 @@ ep_status ep_grouped_gemm(ep_handle* h, int64_t num_rows, int32_t n, int32_t k, 
     p.b_chunked = chunked_columns(n);
     return launch<kTransposed>(h, a, a_small, weight_across_operand(w, n, k, groups, p.b_chunked ? kBox / 64 : 1),
                                weight_across_operand(w, n, k, groups, 1), p, rows_each, stream);
+}
+
+ep_status ep_grouped_gemm_act(ep_handle* h, int64_t num_rows, int32_t n, int32_t k, const int32_t* group_count,
+                              const int32_t* group_begin, const void* x, int64_t x_row_bytes, const void* w,
+                              const float* bias, int32_t act, int32_t gated, const float* row_weights, const void* residual,
+                              int64_t residual_row_bytes, void* pre, int64_t pre_row_bytes, void* out, ep_dtype out_dtype,
+                              int64_t out_row_bytes, int64_t expected_rows, ep_stream_t stream) {
+    EP_TRACE();
+    GemmParams p = {};
+    const ep_status st = check_groups(h, num_rows, n, k, group_count, group_begin, &p);
+    if (st != EP_OK) return st;
+    EP_CHECK_ARG(!gated || n % 16 == 0, "gated: n %d must be two widths of a multiple of 8", n);
+    EP_CHECK_ARG(act >= EP_ACT_NONE && act <= EP_ACT_GELU, "act %d is no activation", act);
+    EP_CHECK_ARG(out_dtype == EP_BF16 || (out_dtype == EP_FP32 && !gated), "out_dtype must be EP_BF16, or EP_FP32 where it is not gated");
+    EP_CHECK_ARG(expected_rows >= 0, "expected_rows %lld < 0", static_cast<long long>(expected_rows));
+    if (num_rows == 0) return EP_OK;
+    const int32_t width = gated ? n / 2 : n;
+    p.out_fp32 = out_dtype == EP_FP32;
+    const ep_status rows = check_rows(x, x_row_bytes, 2 * static_cast<int64_t>(k), w, out, out_row_bytes, p.out_fp32 ? 2 * width : width, &p);
+    if (rows != EP_OK) return rows;
+    EP_CHECK_ARG(p.a_words == nullptr, "x must be 16-byte aligned, its rows multiples of 16 bytes apart (%lld)", static_cast<long long>(x_row_bytes));
+    EP_CHECK_ARG(aligned4(bias) && aligned4(row_weights), "misaligned bias or row_weights");
+    EP_CHECK_ARG(!residual || (aligned16(residual) && row_stride_ok(residual_row_bytes, 2 * static_cast<int64_t>(width))),
+                 "residual must be 16-byte aligned with a row stride in multiples of 16 that holds a row (%lld bytes)",
+                 static_cast<long long>(residual_row_bytes));
+    EP_CHECK_ARG(!pre || (aligned16(pre) && row_stride_ok(pre_row_bytes, 2 * static_cast<int64_t>(n))),
+                 "pre must be 16-byte aligned with a row stride in multiples of 16 that holds a row (%lld bytes)",
+                 static_cast<long long>(pre_row_bytes));
+    p.cols_dim = width;
+    p.contraction = k;
+    p.bias = bias;
+    p.act = act;
+    p.row_weights = row_weights;
+    p.residual = static_cast<const uint8_t*>(residual);
+    p.residual_row_bytes = residual_row_bytes;
+    p.pre = static_cast<uint8_t*>(pre);
+    p.pre_row_bytes = pre_row_bytes;
+    p.pre_wide = pre && rows_aligned32(pre, pre_row_bytes) && (!gated || width % 16 == 0);
+    const int64_t rows_each = expected_rows ? expected_rows : num_rows / p.groups.groups;
+    const int groups = p.groups.groups;
+    const Operand a = row_operand(x, false, k, num_rows, x_row_bytes, kBox);
+    const Operand a_small = row_operand(x, false, k, num_rows, x_row_bytes, kRowBox);
+    const Operand b = weight_operand(w, false, k, n, groups, kBox), b_small = weight_operand(w, false, k, n, groups, kColBox);
+    return gated ? launch<kGated>(h, a, a_small, b, b_small, p, rows_each, stream)
+                 : launch<kActivated>(h, a, a_small, b, b_small, p, rows_each, stream);
 }
 
 ep_status ep_grouped_gemm_wgrad(ep_handle* h, int64_t num_rows, int32_t n, int32_t k, const int32_t* group_count,

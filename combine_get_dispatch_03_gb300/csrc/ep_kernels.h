@@ -22,6 +22,9 @@ struct LaunchPlan {
     int swiglu_blocks[3] = {0, 0, 0};    // gated activation: bf16, FP8 cast, gradient
     int reduce_blocks = 0;               // expert rows back into receive rows
     int gemm_pairs = 0;                  // grouped products: pairs of CTAs resident on the GPU at once
+    int act_pairs = 0;                   // the same of their forms with an epilogue
+    bool act_ready = false;
+    bool layer_ready = false;
     bool gemm_ready = false;             // the experts' parts are made by the first call that needs them (plan_once)
     bool rows_ready = false;
     bool swiglu_ready = false;

@@ -1,0 +1,591 @@
+// ep_router.cu -- the router in front of a dispatch: every token's experts and their weights, and its gradient (sm_103a).
+//
+//   forward    s = softmax(l) or sigmoid(l);  key = s + bias;  of G groups of E / G experts the L with the largest sums of
+//              their two largest keys stay;  the K largest keys in descending order, ties to the lowest expert;
+//              w = scale * s, or scale * s / sum of the chosen s
+//   gradient   dl from dw.  With normalised weights u = w / scale only the chosen logits have one:
+//                softmax  dl = scale * u * (dw - sum dw u)        sigmoid  dl = scale * u * (dw - sum dw u) * (1 - s)
+//              else  sigmoid  dl = scale * dw * s * (1 - s) of the chosen,  softmax  dl_e = p_e * (scale * dw_e - sum scale dw p)
+//
+// A warp owns a token; its lanes hold neighbouring experts.  A round of the selection is a maximum over the
+// warp of order-preserving 32-bit keys, a vote for the lowest lane that has it, and that lane's next largest.
+//
+// Which experts are chosen must not hang on the rounding of s.  Without bias and groups the keys are the logits
+// themselves.  Otherwise 32-bit keys decide unless two that are compared lie closer than their error (kSigmoidError); such
+// a token's keys are computed again in 64 bits (choose_exactly), a fraction of a percent of the tokens.
+#include "ep_groups.cuh"
+#include "ep_handle.h"
+#include "ep_trace.h"
+
+namespace ep {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / kWarpSize;
+constexpr int kMaxGroups = 32;
+// The error of a comparison of two keys, as a part of the token's largest score.  Sigmoid: 2^-22.3 a key from the
+// exponential, the reciprocal and two roundings.  Softmax: at most 28 roundings of 2^-24 more in its sum, which a bias feels.
+constexpr float kSigmoidError = 1e-6f, kSoftmaxError = 2e-6f;
+constexpr float kSumError = 2.4e-7f;  // 2^-22 of the key itself, from adding the bias or a second key
+
+struct RouterParams {
+    const void* logits;
+    const float* bias;
+    const uint8_t* token_mask;
+    int64_t* topk_idx;
+    float* topk_weights;
+    const int64_t* chosen;      // gradient: topk_idx
+    const float* d_weights;
+    void* d_logits;
+    int32_t* status;
+    int64_t tokens;
+    int32_t experts, topk, groups, kept, softmax, normalize, vector;
+    float scale;
+};
+
+// Order-preserving 32-bit key; 0 for what cannot be chosen (NaN, -inf).
+__device__ __forceinline__ uint32_t ordered(float v) {
+    if (!(v > -INFINITY)) return 0;
+    const uint32_t u = __float_as_uint(v + 0.0f);  // -0 as 0
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ float unordered(uint32_t k) {
+    if (k == 0) return -INFINITY;
+    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+__device__ __forceinline__ uint64_t ordered64(double v) {
+    if (!(v > -INFINITY)) return 0;
+    const uint64_t u = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
+    return u >> 63 ? ~u : u | (1ull << 63);
+}
+
+__device__ __forceinline__ double unordered64(uint64_t k) {
+    if (k == 0) return -INFINITY;
+    return __longlong_as_double(static_cast<long long>(k >> 63 ? k & ~(1ull << 63) : ~k));
+}
+
+// exp(v) to 2^-22: log2(e) in two parts, so that the exponent's rounding comes back as a factor.  Past e^88 and e^-104
+// (0) it stays there: keys that become equal so are looked at in 64 bits.
+__device__ __forceinline__ float exp_fast(float v) {
+    v = fminf(fmaxf(v, -104.0f), 88.0f);
+    constexpr float kHi = 1.44269502f, kLo = 1.92596303e-8f, kLn2 = 0.693147182f;
+    const float t = v * kHi;
+    const float rest = fmaf(v, kHi, -t) + v * kLo;
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    return fmaf(e, rest * kLn2, e);
+}
+
+// A logit: NaN counts as -inf (it cannot be chosen and has no weight), +inf as the largest finite value.
+template <typename T>
+__device__ __forceinline__ float logit(const void* p, int64_t at) {
+    float v;
+    if constexpr (sizeof(T) == 4) v = __ldg(static_cast<const float*>(p) + at);
+    else v = __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p) + at)) << 16);
+    return v != v ? -INFINITY : fminf(v, 3.402823466e38f);
+}
+
+// Experts [lane * V, lane * V + V) of a token; -inf past the last, for NaN, and the largest finite value for +inf.
+template <typename T, int V>
+__device__ __forceinline__ void load_row(const RouterParams& p, int64_t token, float (&l)[V]) {
+    const int first = lane_id() * V;
+    constexpr int kVec = 16 / sizeof(T);
+    if constexpr (V >= kVec) {
+        if (p.vector) {  // rows are 16-byte aligned: pieces of kVec experts are there or not
+            const int4* row = reinterpret_cast<const int4*>(static_cast<const uint8_t*>(p.logits) + (token * p.experts + first) * sizeof(T));
+#pragma unroll
+            for (int i = 0; i < V / kVec; ++i) {
+                int4 q = make_int4(0, 0, 0, 0);
+                const bool in = first + i * kVec < p.experts;
+                if (in) q = ld_stream_v4(row + i);
+                float f[kVec];
+                if constexpr (sizeof(T) == 4) {
+                    f[0] = __int_as_float(q.x), f[1] = __int_as_float(q.y), f[2] = __int_as_float(q.z), f[3] = __int_as_float(q.w);
+                } else {
+                    unpack8(q, f);
+                }
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) l[i * kVec + j] = !in || f[j] != f[j] ? -INFINITY : fminf(f[j], 3.402823466e38f);
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) l[v] = first + v < p.experts ? logit<T>(p.logits, token * p.experts + first + v) : -INFINITY;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = kWarpSize / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
+    return v;
+}
+
+// The largest logit (-inf without any) and the sum of exp(l - largest).
+template <int V>
+__device__ __forceinline__ void softmax_stats(const float (&l)[V], float* most, float* sum) {
+    float m = l[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) m = fmaxf(m, l[v]);
+    m = unordered(__reduce_max_sync(kFullMask, ordered(m)));
+    const float base = m > -INFINITY ? m : 0.0f;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int v = 0; v < V; ++v) s[v & 3] += l[v] > -INFINITY ? exp_fast(l[v] - base) : 0.0f;
+    *most = base;
+    *sum = warp_sum((s[0] + s[1]) + (s[2] + s[3]));
+}
+
+// The token's choice with keys in 64 bits.  Returns lane k's expert (-1: none) for k < topk.
+template <typename T, int V>
+__device__ __noinline__ int choose_exactly(const RouterParams& p, int64_t token) {
+    uint64_t key[V];
+    const int first = lane_id() * V;
+    double most = 0.0, sum = 1.0;
+    if (p.softmax) {
+        most = -INFINITY;
+        for (int v = 0; v < V && first + v < p.experts; ++v) most = fmax(most, static_cast<double>(logit<T>(p.logits, token * p.experts + first + v)));
+        for (int o = kWarpSize / 2; o > 0; o >>= 1) most = fmax(most, __shfl_xor_sync(kFullMask, most, o));
+        if (!(most > -INFINITY)) most = 0.0;
+        sum = 0.0;
+        for (int v = 0; v < V && first + v < p.experts; ++v) sum += exp(static_cast<double>(logit<T>(p.logits, token * p.experts + first + v)) - most);
+        for (int o = kWarpSize / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFullMask, sum, o);
+    }
+    for (int v = 0; v < V; ++v) {
+        key[v] = 0;
+        if (first + v >= p.experts) continue;
+        const double l = static_cast<double>(logit<T>(p.logits, token * p.experts + first + v));
+        if (!(l > -INFINITY)) continue;
+        const double s = p.softmax ? exp(l - most) / sum : 1.0 / (1.0 + exp(-l));
+        key[v] = ordered64(p.bias ? s + static_cast<double>(p.bias[first + v]) : s);
+    }
+    if (p.groups > 1) {
+        const int size = p.experts / p.groups;
+        uint64_t mine = 0;  // lane g: the score of group g
+        for (int g = 0; g < p.groups; ++g) {
+            uint64_t a = 0, b = 0;
+            for (int v = 0; v < V; ++v) {
+                if (first + v >= p.experts || (first + v) / size != g) continue;
+                if (key[v] > a) b = a, a = key[v];
+                else if (key[v] > b) b = key[v];
+            }
+            for (int o = kWarpSize / 2; o > 0; o >>= 1) {
+                const uint64_t c = __shfl_xor_sync(kFullMask, a, o), d = __shfl_xor_sync(kFullMask, b, o);
+                b = c > a ? (a > d ? a : d) : (b > c ? b : c);
+                a = c > a ? c : a;
+            }
+            const uint64_t score = size == 1 ? a : ordered64(unordered64(a) + unordered64(b));
+            if (lane_id() == g) mine = score;
+        }
+        int better = 0;
+        for (int g = 0; g < p.groups; ++g) {
+            const uint64_t other = __shfl_sync(kFullMask, mine, g);
+            better += other > mine || (other == mine && g < lane_id());
+        }
+        const unsigned stay = __ballot_sync(kFullMask, lane_id() < p.groups && better < p.kept);
+        for (int v = 0; v < V; ++v)
+            if (first + v < p.experts && !(stay >> ((first + v) / size) & 1)) key[v] = 0;
+    }
+    int chosen = -1;
+    for (int k = 0; k < p.topk; ++k) {
+        uint64_t best = 0;
+        int at = -1;
+        for (int v = 0; v < V; ++v)
+            if (key[v] > best) best = key[v], at = v;
+        uint64_t top = best;
+        for (int o = kWarpSize / 2; o > 0; o >>= 1) {
+            const uint64_t c = __shfl_xor_sync(kFullMask, top, o);
+            top = c > top ? c : top;
+        }
+        if (top == 0) break;
+        const int lane = __ffs(__ballot_sync(kFullMask, best == top)) - 1;
+        const int expert = __shfl_sync(kFullMask, first + at, lane);
+        if (lane_id() == k) chosen = expert;
+        if (lane_id() == lane) key[at] = 0;
+    }
+    return chosen;
+}
+
+// The score of the group of this lane's number (lane g < groups), from the warp's keys: two largest, added up.
+template <int V>
+__device__ __forceinline__ float group_score(const RouterParams& p, const uint32_t (&key)[V], uint32_t* scratch) {
+    const int size = p.experts / p.groups;
+    uint32_t a = 0, b = 0;
+    const int lanes = size / V;
+    if (lanes * V == size && (lanes & (lanes - 1)) == 0) {  // a group is a power of two of whole lanes
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            b = max(b, min(a, key[v]));
+            a = max(a, key[v]);
+        }
+        for (int o = 1; o < lanes; o <<= 1) {
+            const uint32_t c = __shfl_xor_sync(kFullMask, a, o), d = __shfl_xor_sync(kFullMask, b, o);
+            b = max(min(a, c), max(b, d));
+            a = max(a, c);
+        }
+        const int from = min(lane_id() * lanes, kWarpSize - 1);
+        a = __shfl_sync(kFullMask, a, from);
+        b = __shfl_sync(kFullMask, b, from);
+    } else {
+        __syncwarp();
+#pragma unroll
+        for (int v = 0; v < V; ++v) scratch[lane_id() * V + v] = key[v];
+        __syncwarp();
+        if (lane_id() < p.groups)
+            for (int i = 0; i < size; ++i) {
+                const uint32_t k = scratch[lane_id() * size + i];
+                b = max(b, min(a, k));
+                a = max(a, k);
+            }
+    }
+    return size == 1 ? unordered(a) : unordered(a) + unordered(b);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void route_token(const RouterParams& p, int64_t token, uint32_t* scratch) {
+    const int first = lane_id() * V;
+    const int64_t out = token * p.topk + lane_id();
+    if (p.token_mask && p.token_mask[token] == 0) {
+        if (lane_id() < p.topk) p.topk_idx[out] = -1, p.topk_weights[out] = 0.0f;
+        return;
+    }
+    float l[V];
+    load_row<T, V>(p, token, l);
+    const bool by_logit = p.bias == nullptr && p.groups == 1;  // the scores' order is the logits'
+    const bool whole_sum = p.softmax && !(p.normalize && by_logit);
+    float most = 0.0f, sum = 1.0f;
+    if (whole_sum) softmax_stats<V>(l, &most, &sum);
+    uint32_t key[V];
+    float largest = 1.0f;  // score
+    if (by_logit) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = ordered(l[v]);
+    } else {
+        const float inv = 1.0f / sum;
+        float top = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const bool in = l[v] > -INFINITY;
+            const float e = exp_fast(p.softmax ? l[v] - most : -l[v]);
+            float s = p.softmax ? e * inv : __frcp_rn(1.0f + e);
+            top = fmaxf(top, in ? s : 0.0f);
+            if (p.bias && in) s += __ldg(p.bias + first + v);
+            key[v] = in ? ordered(s) : 0;
+        }
+        largest = unordered(__reduce_max_sync(kFullMask, ordered(top)));
+    }
+    const float error = (p.softmax ? kSoftmaxError : kSigmoidError) * largest;
+    bool close = false;
+    if (p.groups > 1) {
+        const int size = p.experts / p.groups;
+        const float score = group_score<V>(p, key, scratch);
+        const uint32_t mine = score > -INFINITY ? ordered(score) : 1;
+        int better = 0;
+        for (int g = 0; g < p.groups; ++g) {
+            const uint32_t other = __shfl_sync(kFullMask, mine, g);
+            better += other > mine || (other == mine && g < lane_id());
+        }
+        const bool there = lane_id() < p.groups, in = there && better < p.kept;
+        const unsigned stay = __ballot_sync(kFullMask, in);
+        // the last that stays and the first that does not
+        const float last = unordered(__reduce_min_sync(kFullMask, in ? mine : 0xffffffffu));
+        const float next = unordered(__reduce_max_sync(kFullMask, there && !in ? mine : 0u));
+        close = last - next <= 2.0f * error + kSumError * (fabsf(last) + fabsf(next));  // false for infinite ones
+        if (size % V == 0) {
+            if (first < p.experts && !(stay >> (first / size) & 1))
+#pragma unroll
+                for (int v = 0; v < V; ++v) key[v] = 0;
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (first + v < p.experts && !(stay >> ((first + v) / size) & 1)) key[v] = 0;
+        }
+    }
+    int chosen = -1;
+    uint32_t chosen_key = 0, last_key = 0;
+#pragma unroll 1
+    for (int k = 0; k < p.topk; ++k) {
+        uint32_t best = key[0];
+#pragma unroll
+        for (int v = 1; v < V; ++v) best = max(best, key[v]);
+        const uint32_t top = __reduce_max_sync(kFullMask, best);
+        last_key = top;
+        if (top == 0) break;
+        const int lane = __ffs(__ballot_sync(kFullMask, best == top)) - 1;
+        int at = 0;
+        bool found = lane_id() != lane;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const bool hit = !found && key[v] == top;
+            if (hit) at = v, key[v] = 0;
+            found |= hit;
+        }
+        const int expert = __shfl_sync(kFullMask, first + at, lane);
+        if (lane_id() == k) chosen = expert, chosen_key = top;
+    }
+    if (!by_logit && !close) {
+        // Neighbours in the order, unless they tie because their inputs are the same.
+        float lc = 0.0f, bc = 0.0f;
+        if (chosen >= 0) {
+            lc = logit<T>(p.logits, token * p.experts + chosen);
+            if (p.bias) bc = p.bias[chosen];
+        }
+        const float mine = unordered(chosen_key), after = __shfl_down_sync(kFullMask, mine, 1);
+        const float l_after = __shfl_down_sync(kFullMask, lc, 1), b_after = __shfl_down_sync(kFullMask, bc, 1);
+        bool near = chosen >= 0 && lane_id() < p.topk - 1 && lane_id() < kWarpSize - 1 && after > -INFINITY &&
+                    mine - after <= error + kSumError * (fabsf(mine) + fabsf(after)) && !(lc == l_after && bc == b_after);
+        if (last_key != 0) {  // all K are there: who is left, next to the last
+            uint32_t best = key[0];
+#pragma unroll
+            for (int v = 1; v < V; ++v) best = max(best, key[v]);
+            const float last = unordered(last_key);
+            const uint32_t border = ordered(last - error - 2.0f * kSumError * fabsf(last));
+            if (__any_sync(kFullMask, best >= border)) {
+                const float l_last = __shfl_sync(kFullMask, lc, p.topk - 1), b_last = __shfl_sync(kFullMask, bc, p.topk - 1);
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (key[v] >= border && key[v] != 0)
+                        near |= !(l[v] == l_last && (p.bias == nullptr || p.bias[first + v] == b_last));
+            }
+        }
+        close = __any_sync(kFullMask, near);
+    }
+    if (close) chosen = choose_exactly<T, V>(p, token);
+
+    // lane k: the score of expert k
+    const bool mine = chosen >= 0;
+    float s = 0.0f;
+    const float lc = mine ? logit<T>(p.logits, token * p.experts + chosen) : -INFINITY;
+    if (p.softmax) {
+        float base = most;
+        if (p.normalize) base = unordered(__reduce_max_sync(kFullMask, ordered(lc)));  // the sum cancels
+        if (mine) s = expf(lc - base);
+        if (mine && !p.normalize) s /= sum;
+    } else if (mine) {
+        s = 1.0f / (1.0f + expf(-lc));
+    }
+    float w = s * p.scale;
+    if (p.normalize) {
+        const float total = warp_sum(s);
+        w = total > 0.0f ? s / total * p.scale : 0.0f;
+    }
+    if (lane_id() < p.topk) {
+        p.topk_idx[out] = chosen;
+        p.topk_weights[out] = w;
+    }
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads) router_kernel(const RouterParams p) {
+    extern __shared__ uint32_t scratch[];  // a warp's keys, where groups cut across lanes
+    pdl_enter();
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / kWarpSize; t < p.tokens; t += warps)
+        route_token<T, V>(p, t, scratch + threadIdx.x / kWarpSize * (kWarpSize * V));
+}
+
+template <typename T>
+__device__ __forceinline__ void store_logit(void* p, int64_t at, float v) {
+    if constexpr (sizeof(T) == 4) static_cast<float*>(p)[at] = v;
+    else static_cast<__nv_bfloat16*>(p)[at] = __float2bfloat16_rn(v);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_row(const RouterParams& p, int64_t token, const float (&d)[V]) {
+    const int first = lane_id() * V;
+    constexpr int kVec = 16 / sizeof(T);
+    if constexpr (V >= kVec) {
+        if (p.vector) {
+            int4* row = reinterpret_cast<int4*>(static_cast<uint8_t*>(p.d_logits) + (token * p.experts + first) * sizeof(T));
+#pragma unroll
+            for (int i = 0; i < V / kVec; ++i) {
+                if (first + i * kVec >= p.experts) break;
+                float f[kVec];
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) f[j] = d[i * kVec + j];
+                if constexpr (sizeof(T) == 4)
+                    st_stream_v4(row + i, make_int4(__float_as_int(f[0]), __float_as_int(f[1]), __float_as_int(f[2]), __float_as_int(f[3])));
+                else
+                    st_stream_v4(row + i, pack8_bf16(f));
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        if (first + v < p.experts) store_logit<T>(p.d_logits, token * p.experts + first + v, d[v]);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void route_gradient(const RouterParams& p, int64_t token) {
+    const int64_t in = token * p.topk + lane_id();
+    const int64_t raw = lane_id() < p.topk ? p.chosen[in] : -1;
+    if (raw < -1 || raw >= p.experts) report(p.status, EP_ERR_BAD_EXPERT);
+    const int chosen = raw >= 0 && raw < p.experts ? static_cast<int>(raw) : -1;
+    const bool mine = chosen >= 0;
+    const float lc = mine ? logit<T>(p.logits, token * p.experts + chosen) : -INFINITY;
+    const float dw = mine ? p.d_weights[in] * p.scale : 0.0f;
+    float d[V];
+    float own = 0.0f, base = 0.0f;  // the chosen logit's gradient in two parts: its slot's, and what every logit of the token gets
+    if (p.softmax && !p.normalize) {
+        load_row<T, V>(p, token, d);
+        float most, sum;
+        softmax_stats<V>(d, &most, &sum);
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+        const float u = mine && lc > -INFINITY ? expf(lc - most) * inv : 0.0f;
+        own = dw * u;
+        const float dot = warp_sum(own);
+        base = -u * dot;
+#pragma unroll
+        for (int v = 0; v < V; ++v) d[v] = d[v] > -INFINITY ? -(exp_fast(d[v] - most) * inv) * dot : 0.0f;
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) d[v] = 0.0f;
+        float s = 0.0f, rest = 1.0f;  // rest: 1 - s
+        if (p.softmax) {
+            const float top = unordered(__reduce_max_sync(kFullMask, ordered(lc)));
+            if (mine && lc > -INFINITY) s = expf(lc - top);
+        } else if (mine) {
+            const float e = expf(-fabsf(lc)), small = e / (1.0f + e), large = 1.0f / (1.0f + e);
+            s = lc >= 0.0f ? large : small;
+            rest = lc >= 0.0f ? small : large;
+        }
+        if (p.normalize) {
+            const float total = warp_sum(s);
+            const float u = total > 0.0f ? s / total : 0.0f;
+            own = u * (dw - warp_sum(dw * u)) * rest;
+        } else {
+            own = dw * s * rest;
+        }
+    }
+    store_row<T, V>(p, token, d);
+    // the chosen ones: the same expert twice gets both
+    const unsigned same = __match_any_sync(kFullMask, chosen);
+    float total = own;
+    if (__any_sync(kFullMask, mine && (same & (same - 1)))) {
+        total = 0.0f;
+        for (int k = 0; k < p.topk; ++k) {
+            const float other = __shfl_sync(kFullMask, own, k);
+            if (same >> k & 1) total += other;
+        }
+    }
+    __syncwarp();  // after the row's stores
+    if (mine) store_logit<T>(p.d_logits, token * p.experts + chosen, base + total);
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads) router_grad_kernel(const RouterParams p) {
+    pdl_enter();
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / kWarpSize; t < p.tokens; t += warps)
+        route_gradient<T, V>(p, t);
+}
+
+constexpr int kCtasPerSm = 4;  // that any variant can have resident
+constexpr int kWaves = 8;
+
+template <bool kGrad, typename T, int V>
+cudaError_t start(const ep_handle* h, const RouterParams& p, cudaStream_t stream) {
+    const int64_t wanted = (p.tokens + kWarps - 1) / kWarps;
+    const int64_t most = static_cast<int64_t>(h->plan.num_sms) * kCtasPerSm * (h->plan.sm_limited ? 1 : kWaves);
+    const dim3 grid(static_cast<unsigned>(wanted < most ? wanted : most));
+    if constexpr (kGrad) return launch_kernel(router_grad_kernel<T, V>, grid, dim3(kThreads), 0, stream, 1, p);
+    const int size = p.experts / p.groups, lanes = size / V;
+    const bool cut = p.groups > 1 && (lanes * V != size || (lanes & (lanes - 1)) != 0);
+    const size_t smem = cut ? sizeof(uint32_t) * kThreads * V : 0;
+    if (smem > 48 * 1024) {
+        const cudaError_t err = cudaFuncSetAttribute(router_kernel<T, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (err != cudaSuccess) return err;
+    }
+    return launch_kernel(router_kernel<T, V>, grid, dim3(kThreads), smem, stream, 1, p);
+}
+
+template <bool kGrad, typename T>
+cudaError_t start_type(const ep_handle* h, const RouterParams& p, cudaStream_t stream) {
+    if (p.experts <= 32) return start<kGrad, T, 1>(h, p, stream);
+    if (p.experts <= 128) return start<kGrad, T, 4>(h, p, stream);
+    if (p.experts <= 256) return start<kGrad, T, 8>(h, p, stream);
+    if (p.experts <= 512) return start<kGrad, T, 16>(h, p, stream);
+    return start<kGrad, T, 64>(h, p, stream);
+}
+
+template <bool kGrad>
+ep_status launch(const ep_handle* h, const RouterParams& p, ep_dtype dtype, cudaStream_t stream) {
+    if (p.tokens == 0) return EP_OK;
+    DeviceGuard guard(h->device);
+    const cudaError_t err = dtype == EP_FP32 ? start_type<kGrad, float>(h, p, stream) : start_type<kGrad, __nv_bfloat16>(h, p, stream);
+    if (err != cudaSuccess) return cuda_fail(err, "router launch");
+    return EP_OK;
+}
+
+ep_status check(const ep_handle* h, int64_t num_tokens, const void* logits, ep_dtype dtype, int32_t score, float scale, RouterParams* p) {
+    if (h == nullptr) return fail(EP_ERR_INVALID_ARG, "handle is NULL");
+    EP_CHECK_ARG(num_tokens >= 0 && num_tokens <= INT32_MAX, "num_tokens %lld outside [0, 2^31)", static_cast<long long>(num_tokens));
+    EP_CHECK_ARG(dtype == EP_FP32 || dtype == EP_BF16, "logits must be EP_FP32 or EP_BF16");
+    EP_CHECK_ARG(score == EP_SCORE_SOFTMAX || score == EP_SCORE_SIGMOID, "score must be EP_SCORE_SOFTMAX or EP_SCORE_SIGMOID");
+    EP_CHECK_ARG(scale == scale && scale - scale == 0.0f, "scale must be finite");
+    EP_CHECK_ARG(num_tokens == 0 || (logits && (reinterpret_cast<uintptr_t>(logits) & (dtype == EP_FP32 ? 3u : 1u)) == 0),
+                 "logits is NULL or misaligned");
+    p->logits = logits;
+    p->tokens = num_tokens;
+    p->experts = h->cfg.num_experts;
+    p->topk = h->cfg.num_topk;
+    p->softmax = score == EP_SCORE_SOFTMAX;
+    p->scale = scale;
+    p->groups = p->kept = 1;
+    p->status = h->status;
+    p->vector = aligned16(logits) && p->experts % (dtype == EP_FP32 ? 4 : 8) == 0;
+    return EP_OK;
+}
+
+}  // namespace
+}  // namespace ep
+
+using namespace ep;
+
+extern "C" {
+
+ep_status ep_router(ep_handle* h, int64_t num_tokens, const void* logits, ep_dtype logits_dtype, const float* bias,
+                    const uint8_t* token_mask, int32_t score, int32_t num_groups, int32_t kept_groups, int32_t normalize,
+                    float scale, int64_t* topk_idx, float* topk_weights, ep_stream_t stream) {
+    EP_TRACE();
+    RouterParams p = {};
+    const ep_status st = check(h, num_tokens, logits, logits_dtype, score, scale, &p);
+    if (st != EP_OK) return st;
+    EP_CHECK_ARG(num_groups >= 1 && num_groups <= kMaxGroups && p.experts % num_groups == 0,
+                 "num_groups %d must divide num_experts %d and be at most %d", num_groups, p.experts, kMaxGroups);
+    EP_CHECK_ARG(kept_groups >= 1 && kept_groups <= num_groups, "kept_groups %d outside [1, num_groups=%d]", kept_groups, num_groups);
+    EP_CHECK_ARG(num_tokens == 0 || (topk_idx && topk_weights && aligned8(topk_idx) && aligned4(topk_weights)),
+                 "topk_idx or topk_weights is NULL or misaligned");
+    EP_CHECK_ARG(aligned4(bias), "misaligned bias");
+    p.bias = bias;
+    p.token_mask = token_mask;
+    p.groups = kept_groups == num_groups ? 1 : num_groups;  // all stay
+    p.kept = kept_groups;
+    p.normalize = normalize != 0;
+    p.topk_idx = topk_idx;
+    p.topk_weights = topk_weights;
+    return launch<false>(h, p, logits_dtype, stream);
+}
+
+ep_status ep_router_grad(ep_handle* h, int64_t num_tokens, const void* logits, ep_dtype logits_dtype, const int64_t* topk_idx,
+                         const float* d_topk_weights, int32_t score, int32_t normalize, float scale, void* d_logits,
+                         ep_stream_t stream) {
+    EP_TRACE();
+    RouterParams p = {};
+    const ep_status st = check(h, num_tokens, logits, logits_dtype, score, scale, &p);
+    if (st != EP_OK) return st;
+    EP_CHECK_ARG(num_tokens == 0 || (topk_idx && d_topk_weights && aligned8(topk_idx) && aligned4(d_topk_weights)),
+                 "topk_idx or d_topk_weights is NULL or misaligned");
+    EP_CHECK_ARG(num_tokens == 0 || (d_logits && (reinterpret_cast<uintptr_t>(d_logits) & (logits_dtype == EP_FP32 ? 3u : 1u)) == 0),
+                 "d_logits is NULL or misaligned");
+    p.chosen = topk_idx;
+    p.d_weights = d_topk_weights;
+    p.normalize = normalize != 0;
+    p.d_logits = d_logits;
+    p.vector = p.vector && aligned16(d_logits);
+    return launch<true>(h, p, logits_dtype, stream);
+}
+
+}  // extern "C"

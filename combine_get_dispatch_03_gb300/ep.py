@@ -23,6 +23,8 @@ STATUS_NAMES = {0: "EP_OK", 1: "EP_ERR_INVALID_ARG", 2: "EP_ERR_CAPACITY", 3: "E
                 4: "EP_ERR_CUDA", 5: "EP_ERR_UNSUPPORTED", 6: "EP_ERR_INCONSISTENT",
                 7: "EP_ERR_BAD_EXPERT", 8: "EP_ERR_STATE"}
 EP_BF16, EP_FP8_E4M3, EP_FP32 = 0, 1, 2
+SCORES = {"softmax": 0, "sigmoid": 1}
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 EP_DISPATCH_FRESH, EP_DISPATCH_CACHED, EP_DISPATCH_PREPARED = 0, 1, 2
 FIELDS = {"rank_prefix_matrix": 0, "channel_prefix_matrix": 1, "recv_channel_prefix_matrix": 2,
           "recv_src_idx": 3, "send_head": 4, "num_recv": 5, "ll_slot_row": 6,
@@ -55,7 +57,9 @@ EXPORTS = ("ep_handle_create", "ep_handle_destroy", "ep_handle_status", "ep_hand
            "ep_query_mask_buffer", "ep_clean_mask_buffer", "ep_selftest_bounded_wait", "ep_ll_combine_strided",
            "ep_expected_topk", "ep_theoretical_num_sms", "ep_layout_notify", "ep_grouped_gemm",
            "ep_grouped_gemm_wgrad", "ep_grouped_gemm_fp8", "ep_swiglu", "ep_swiglu_grad",
-           "ep_expert_layout", "ep_expert_gather", "ep_expert_reduce", "ep_selftest_wait_limit")
+           "ep_expert_layout", "ep_expert_gather", "ep_expert_reduce", "ep_selftest_wait_limit",
+           "ep_grouped_gemm_act", "ep_act_grad", "ep_act_grad_workspace", "ep_router", "ep_router_grad", "ep_moe_layer",
+           "ep_moe_layer_workspace")
 
 
 def library_path() -> str:
@@ -112,13 +116,24 @@ def lib():
         L.ep_expert_layout.argtypes = [P, P, P, I64, P, P, P, P]
         L.ep_expert_gather.argtypes = [P, P, S, P, P, P, P, I64, P, P, P, P]
         L.ep_expert_reduce.argtypes = [P, P, I64, P, P, P, I64, P, P, P]
+        F = ctypes.c_float
+        L.ep_grouped_gemm_act.argtypes = [P, I64, I32, I32, P, P, P, I64, P, P, I32, I32, P, P, I64, P, I64, P, S, I64, I64, P]
+        L.ep_act_grad_workspace.argtypes = [P, I64, I32]
+        L.ep_act_grad_workspace.restype = I64
+        L.ep_act_grad.argtypes = [P, I64, I32, P, P, P, I64, P, I64, I32, I32, P, P, I64, P, P, P, I64, P]
+        L.ep_router.argtypes = [P, I64, P, S, P, P, I32, I32, I32, I32, F, P, P, P]
+        L.ep_router_grad.argtypes = [P, I64, P, S, P, P, I32, I32, F, P, P]
+        L.ep_moe_layer_workspace.argtypes = [P, I32, I32]
+        L.ep_moe_layer_workspace.restype = I64
+        L.ep_moe_layer.argtypes = [P, I32, I32, P, P, P, P, P, P, P, S, P, P, P, P, I64, P]
         for name in ("ep_handle_create", "ep_handle_status", "ep_handle_num_recv", "ep_handle_export",
                      "ep_get_dispatch_layout", "ep_dispatch", "ep_combine", "ep_ll_dispatch", "ep_ll_combine",
                      "ep_ll_dispatch_noalloc", "ep_notify_dispatch", "ep_update_mask_buffer",
                      "ep_query_mask_buffer", "ep_clean_mask_buffer", "ep_selftest_bounded_wait",
                      "ep_ll_combine_strided", "ep_layout_notify", "ep_grouped_gemm", "ep_grouped_gemm_wgrad",
                      "ep_grouped_gemm_fp8", "ep_swiglu", "ep_swiglu_grad", "ep_expert_layout", "ep_expert_gather",
-                     "ep_expert_reduce", "ep_selftest_wait_limit"):
+                     "ep_expert_reduce", "ep_selftest_wait_limit", "ep_grouped_gemm_act", "ep_act_grad", "ep_router",
+                     "ep_router_grad", "ep_moe_layer"):
             getattr(L, name).restype = S
         _lib = L
     return _lib
@@ -649,6 +664,79 @@ def ep_grouped_gemm(h: Handle, x: torch.Tensor, w: torch.Tensor, group_count, gr
     return out
 
 
+def _choice(value, choices, name):
+    if value not in choices:
+        raise ValueError(f"{name} must be one of {', '.join(choices)}, got {value!r}")
+    return choices[value]
+
+
+def ep_grouped_gemm_act(h: Handle, x: torch.Tensor, w: torch.Tensor, group_count, group_begin=None, bias=None, act: str = "none",
+                        gated: bool = False, row_weights=None, residual=None, keep_pre: bool = False, pre=None, out=None,
+                        out_dtype=torch.bfloat16, expected_rows: int = 0, stream=None):
+    """Grouped product with an epilogue: act(x w^T + bias) * row weight + residual, w [E][n][k] bf16, bias [E][n] fp32.
+
+    gated: the first n/2 columns' activation times the last n/2 (silu: ep_grouped_gemm and ep_swiglu in one).  act is
+    "none", "relu", "silu" or "gelu".  keep_pre (or a given pre) keeps x w^T + bias in bf16, which ep_act_grad() takes.
+    out is bf16, or float32 where it is not gated; the residual may be out itself.  A handle with one expert makes it a
+    dense product.  Returns dict(out, pre); rows outside every group are left as they are."""
+    d = h.device
+    if w.dim() != 3:
+        raise ValueError(f"w must be [E][n][k], got {tuple(w.shape)}")
+    E, n, k = w.shape
+    if gated and n % 2:
+        raise ValueError(f"gated weights must hold gate and up of one width, got {n} rows")
+    width = n // 2 if gated else n
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out is bfloat16 or float32")
+    xp, rows, _, xs = _rows(x, "x", torch.bfloat16, d, None, k)
+    out, op, os_ = _out_rows(out, "out", x, rows, width, out_dtype, h, stream)
+    pp, ps = None, 0
+    if pre is not None or keep_pre:
+        pre, pp, ps = _out_rows(pre, "pre", x, rows, n, torch.bfloat16, h, stream)
+    rp, rs = None, 0
+    if residual is not None:
+        rp, _, _, rs = _rows(residual, "residual", torch.bfloat16, d, rows, width)
+    cnt, beg = _group_arrays(h, group_count, group_begin)
+    _raise(lib().ep_grouped_gemm_act(
+        h.ptr, rows, n, k, cnt, beg, xp, xs, _ptr(w, "w", torch.bfloat16, (h.cfg.num_experts, n, k), d),
+        _ptr(bias, "bias", torch.float32, (h.cfg.num_experts, n), d), _choice(act, ACTS, "act"), int(bool(gated)),
+        _ptr(row_weights, "row_weights", torch.float32, (rows,), d), rp, rs, pp, ps, op,
+        EP_FP32 if out_dtype == torch.float32 else EP_BF16, os_, expected_rows, _stream(stream, d)))
+    return dict(out=out, pre=pre)
+
+
+def ep_act_grad(h: Handle, dy: torch.Tensor, pre, group_count, group_begin=None, act: str = "none", gated: bool = False,
+                row_weights=None, with_bias: bool = False, d_pre=None, d_row_weights=None, d_bias=None, stream=None):
+    """Gradient of ep_grouped_gemm_act's epilogue from dy and the kept pre: d_pre (of x w^T + bias), with row_weights
+    theirs, and with_bias (or a given d_bias) the bias's [E][n] fp32.
+
+    Without activation and gate pre may be None; d_pre is then dy's size (dy itself without row_weights)."""
+    d, E = h.device, h.cfg.num_experts
+    yp, rows, width, ys = _rows(dy, "dy", torch.bfloat16, d)
+    n = 2 * width if gated else width
+    pp, ps = None, 0
+    if pre is not None:
+        pp, _, _, ps = _rows(pre, "pre", torch.bfloat16, d, rows, n)
+    d_pre, gp, gs = _out_rows(d_pre, "d_pre", dy, rows, n, torch.bfloat16, h, stream)
+    if row_weights is not None and d_row_weights is None and pre is not None:
+        d_row_weights = _out((rows,), torch.float32, h, stream)
+    if with_bias and d_bias is None:
+        d_bias = _out((E, n), torch.float32, h, stream)
+    work, work_bytes = None, 0
+    if d_bias is not None:
+        work_bytes = lib().ep_act_grad_workspace(h.ptr, rows, n)
+        work = _out((max(16, work_bytes),), torch.uint8, h, stream)
+    cnt, beg = _group_arrays(h, group_count, group_begin)
+    _raise(lib().ep_act_grad(
+        h.ptr, rows, n, cnt, beg, yp, ys, pp, ps, _choice(act, ACTS, "act"), int(bool(gated)),
+        _ptr(row_weights, "row_weights", torch.float32, (rows,), d), gp, gs,
+        _ptr(d_row_weights, "d_row_weights", torch.float32, (rows,), d), _ptr(d_bias, "d_bias", torch.float32, (E, n), d),
+        None if work is None else work.data_ptr(), work_bytes, _stream(stream, d)))
+    return dict(d_pre=d_pre, d_row_weights=d_row_weights, d_bias=d_bias)
+
+
 def ep_grouped_gemm_wgrad(h: Handle, dy: torch.Tensor, x: torch.Tensor, group_count, group_begin=None, out=None,
                           out_dtype=torch.float32, accumulate: bool = False, stream=None):
     """Weight gradient of a grouped product: dw[e] = dy_e^T x_e, [E][n][k], fp32 (or bf16)."""
@@ -800,6 +888,89 @@ def ep_expert_reduce(h: Handle, y: torch.Tensor, slot_row: torch.Tensor, num_rec
         rows, _ptr(out, "out", torch.bfloat16, (R, cap, H), d),
         _ptr(out_topk_weights, "out_topk_weights", torch.float32, (R, cap, K), d), _stream(stream, d)))
     return dict(out=out, out_topk_weights=out_topk_weights)
+
+
+def _logits(h, logits):
+    """(tokens, address, type) of a router's logits [...][E]."""
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"logits: dtype {logits.dtype}, expected float32 or bfloat16")
+    if logits.dim() < 1 or logits.shape[-1] != h.cfg.num_experts:
+        raise ValueError(f"logits must be [...][E={h.cfg.num_experts}], got {tuple(logits.shape)}")
+    return (logits.numel() // h.cfg.num_experts, _ptr(logits, "logits", device=h.device),
+            EP_FP32 if logits.dtype == torch.float32 else EP_BF16)
+
+
+def ep_router(h: Handle, logits: torch.Tensor, bias=None, token_mask=None, score: str = "softmax", num_groups: int = 1,
+              kept_groups: int | None = None, normalize: bool = True, scale: float = 1.0, topk_idx=None, topk_weights=None,
+              stream=None):
+    """Every token's top-k experts and their weights from logits [...][E] (float32 or bfloat16): dict(topk_idx int64,
+    topk_weights float32), both [...][K].
+
+    score is "softmax" or "sigmoid"; bias (float32 [E]) is added for the selection only; kept_groups of num_groups groups
+    of experts stay; normalize divides by the chosen scores' sum.  token_mask (bool [...]) is False for tokens without experts."""
+    d, K = h.device, h.cfg.num_topk
+    tokens, lp, dtype = _logits(h, logits)
+    shape = tuple(logits.shape[:-1]) + (K,)
+    if topk_idx is None:
+        topk_idx = _out(shape, torch.int64, h, stream)
+    if topk_weights is None:
+        topk_weights = _out(shape, torch.float32, h, stream)
+    _raise(lib().ep_router(
+        h.ptr, tokens, lp, dtype, _ptr(bias, "bias", torch.float32, (h.cfg.num_experts,), d),
+        _ptr(token_mask, "token_mask", torch.bool, shape[:-1], d), _choice(score, SCORES, "score"), num_groups,
+        num_groups if kept_groups is None else kept_groups, int(bool(normalize)), scale,
+        _ptr(topk_idx, "topk_idx", torch.int64, shape, d), _ptr(topk_weights, "topk_weights", torch.float32, shape, d),
+        _stream(stream, d)))
+    return dict(topk_idx=topk_idx, topk_weights=topk_weights)
+
+
+def ep_router_grad(h: Handle, logits: torch.Tensor, topk_idx: torch.Tensor, d_topk_weights: torch.Tensor, score: str = "softmax",
+                   normalize: bool = True, scale: float = 1.0, d_logits=None, stream=None):
+    """Gradient of ep_router's weights: d_logits (logits' type and shape) from d_topk_weights [...][K] and its topk_idx."""
+    d, K = h.device, h.cfg.num_topk
+    tokens, lp, dtype = _logits(h, logits)
+    shape = tuple(logits.shape[:-1]) + (K,)
+    if d_logits is None:
+        d_logits = _out(tuple(logits.shape), logits.dtype, h, stream)
+    _raise(lib().ep_router_grad(
+        h.ptr, tokens, lp, dtype, _ptr(topk_idx, "topk_idx", torch.int64, shape, d),
+        _ptr(d_topk_weights, "d_topk_weights", torch.float32, shape, d), _choice(score, SCORES, "score"),
+        int(bool(normalize)), scale, _ptr(d_logits, "d_logits", logits.dtype, tuple(logits.shape), d), _stream(stream, d)))
+    return d_logits
+
+
+def ep_moe_layer(h: Handle, x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor, w_up: torch.Tensor,
+                 w_down: torch.Tensor, up_scales=None, down_scales=None, bias_0=None, bias_1=None, out=None, stream=None):
+    """A whole layer of experts for a few tokens (R * T <= 64): x [R][T][H] bf16 -> [R][T][H] bf16, in two kernels.
+
+    w_up [E][2I][H] and w_down [E][H][I] are bf16, or float8_e4m3fn with one float32 scale per 128 x 128 (up_scales,
+    down_scales), as ep_grouped_gemm_fp8() takes them; the tokens stay bf16 either way.  bias_0 and bias_1 (bf16, x's
+    shape: a residual stream, a shared expert's output) are added as in ep_combine()."""
+    c, d = h.cfg, h.device
+    R, K, H, E = c.num_ranks, c.num_topk, c.hidden, c.num_experts
+    if x.dim() != 3:
+        raise ValueError(f"x must be [R={R}][T][H={H}], got {tuple(x.shape)}")
+    T = x.shape[1]
+    if w_up.dim() != 3 or w_up.shape[1] % 2:
+        raise ValueError(f"w_up must be [E][2I][H], got {tuple(w_up.shape)}")
+    I = w_up.shape[1] // 2  # noqa: E741
+    if w_up.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise TypeError(f"w_up: dtype {w_up.dtype}, expected bfloat16 or float8_e4m3fn")
+    fp8 = w_up.dtype == torch.float8_e4m3fn
+    xp = _ptr(x, "x", torch.bfloat16, (R, T, H), d)
+    if out is None:
+        out = _out((R, T, H), torch.bfloat16, h, stream)
+    work_bytes = lib().ep_moe_layer_workspace(h.ptr, T, I)  # -1: more tokens than the layer takes, which the call reports
+    work = _out((max(16, work_bytes),), torch.uint8, h, stream)
+    _raise(lib().ep_moe_layer(
+        h.ptr, T, I, xp, _ptr(topk_idx, "topk_idx", torch.int64, (R, T, K), d),
+        _ptr(topk_weights, "topk_weights", torch.float32, (R, T, K), d), _ptr(w_up, "w_up", w_up.dtype, (E, 2 * I, H), d),
+        _ptr(up_scales, "up_scales", torch.float32, (E, 2 * I // 128, H // 128), d),
+        _ptr(w_down, "w_down", w_up.dtype, (E, H, I), d),
+        _ptr(down_scales, "down_scales", torch.float32, (E, H // 128, I // 128), d), EP_FP8_E4M3 if fp8 else EP_BF16,
+        _ptr(bias_0, "bias_0", torch.bfloat16, (R, T, H), d), _ptr(bias_1, "bias_1", torch.bfloat16, (R, T, H), d),
+        _ptr(out, "out", torch.bfloat16, (R, T, H), d), work.data_ptr(), work_bytes, _stream(stream, d)))
+    return out
 
 
 def recv_hook(stream=None):

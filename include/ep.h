@@ -67,6 +67,20 @@ typedef enum ep_dtype {
     EP_FP32 = 2      /* IEEE binary32                                       */
 } ep_dtype;
 
+/* Scores of the router. */
+typedef enum ep_score {
+    EP_SCORE_SOFTMAX = 0, /* over all experts                                   */
+    EP_SCORE_SIGMOID = 1
+} ep_score;
+
+/* Activations of products with an epilogue. */
+typedef enum ep_act {
+    EP_ACT_NONE = 0,
+    EP_ACT_RELU = 1,
+    EP_ACT_SILU = 2, /* v * sigmoid(v)                                          */
+    EP_ACT_GELU = 3  /* v * the normal distribution up to v (no tanh)           */
+} ep_act;
+
 /* Sizes fixed for the lifetime of a handle (the Buffer of [P1]/[P3]). */
 typedef struct ep_config {
     int32_t num_ranks;        /* R: 1..32                                                       */
@@ -452,6 +466,42 @@ ep_status ep_grouped_gemm(ep_handle* h, int64_t num_rows, int32_t n, int32_t k, 
                           int32_t w_transposed, void* out, int64_t out_row_bytes, int64_t expected_rows,
                           ep_stream_t stream);
 
+/* Grouped product with an epilogue, bf16: for every row r of expert e, with
+ *   v[r][j] = sum_c x[r][c] * w[e][j][c] + bias[e][j]             w [E][n][k], bias fp32 [E][n]
+ * in fp32,
+ *   gated == 0:  out[r][j] = act(v[r][j]) * row_weights[r] + residual[r][j]                      rows of width = n
+ *   gated != 0:  out[r][j] = act(v[r][j]) * v[r][width + j] * row_weights[r] + residual[r][j]    rows of width = n / 2
+ * rounded once to out_dtype (EP_BF16, or EP_FP32 where it is not gated).  bias, row_weights
+ * (fp32 [num_rows]), residual (bf16 rows of width; it may be out) and pre may be NULL; pre
+ * gets v (bf16 rows of n), which ep_act_grad() takes.  Gated: n a multiple
+ * of 16; with act EP_ACT_SILU and pre's rows this is ep_grouped_gemm() and ep_swiglu()
+ * without the rounding between them.  A handle with one expert makes it
+ * a dense product.  All row strides are multiples of 16 bytes, x's too.
+ * expected_rows as in ep_grouped_gemm(). */
+ep_status ep_grouped_gemm_act(ep_handle* h, int64_t num_rows, int32_t n, int32_t k, const int32_t* group_count,
+                              const int32_t* group_begin, const void* x, int64_t x_row_bytes, const void* w,
+                              const float* bias, int32_t act, int32_t gated, const float* row_weights,
+                              const void* residual, int64_t residual_row_bytes, void* pre, int64_t pre_row_bytes,
+                              void* out, ep_dtype out_dtype, int64_t out_row_bytes, int64_t expected_rows,
+                              ep_stream_t stream);
+
+/* Gradient of that epilogue, from dy (of out; bf16 rows of width) and pre (v, bf16 rows of n):
+ *   not gated:  d_pre = dy * w * act'(v)                                         d_w = sum_j dy * act(v)
+ *   gated:      d_pre = [dy * w * up * act'(gate) | dy * w * act(gate)]          d_w = sum_j dy * act(gate) * up
+ * with w = row_weights[r] (1 for NULL); d_pre bf16 rows of n (it may be pre); if not NULL,
+ * d_row_weights (fp32 [num_rows]) and d_bias (fp32 [E][n]): the sum over e's rows of d_pre before it is
+ * rounded, in an order that only the groups' sizes fix; 0 for an expert without rows.  d_pre may be NULL
+ * too; pre only with EP_ACT_NONE, not gated, without d_row_weights.  The residual's
+ * gradient is dy itself, x's and w's come from d_pre by ep_grouped_gemm() and ep_grouped_gemm_wgrad().
+ * d_bias needs a workspace of ep_act_grad_workspace() bytes (-1: bad arguments), whose content
+ * does not matter and which the call uses until it has run. */
+int64_t ep_act_grad_workspace(const ep_handle* h, int64_t num_rows, int32_t n);
+ep_status ep_act_grad(ep_handle* h, int64_t num_rows, int32_t n, const int32_t* group_count, const int32_t* group_begin,
+                      const void* dy, int64_t dy_row_bytes, const void* pre, int64_t pre_row_bytes, int32_t act,
+                      int32_t gated, const float* row_weights, void* d_pre, int64_t d_pre_row_bytes,
+                      float* d_row_weights, float* d_bias, void* workspace, int64_t workspace_bytes,
+                      ep_stream_t stream);
+
 /* Gradient of the weights of a grouped product, for every expert e:
  *   dw[e][j][c] = sum over e's rows r of dy[r][j] * x[r][c]      dw [E][n][k], contiguous
  * dy rows of n, x rows of k bf16; dw fp32 or bf16 (dw_dtype).  An expert
@@ -532,6 +582,51 @@ ep_status ep_expert_gather(ep_handle* h, const void* x, ep_dtype x_dtype, const 
 ep_status ep_expert_reduce(ep_handle* h, const void* y, int64_t y_row_bytes, const int32_t* slot_row,
                            const float* row_weights, const int32_t* num_recv, int64_t num_rows, void* out,
                            float* out_topk_weights, ep_stream_t stream);
+
+/* ------------------------------------------------------------ router and layer */
+
+/* The router in front of a dispatch.  For each of num_tokens tokens (R * T in all), from its logits l (fp32 or bf16
+ * [num_tokens][E]):
+ *   s = softmax(l) over the experts, or sigmoid(l);  key = s + bias        (bias fp32 [E], NULL = 0: it only selects)
+ *   num_groups > 1: of num_groups (<= 32) groups of neighbouring experts the kept_groups with the largest sums of
+ *     their two largest keys stay (of groups of one expert: its key); ties to the lower group
+ *   topk_idx:     the K largest keys that are left, in descending order, ties to the lower expert   int64 [num_tokens][K]
+ *   topk_weights: scale * s, normalize != 0: scale * s / (sum of the chosen s)                      fp32 [num_tokens][K]
+ * -- the topk_idx and topk_weights of ep_dispatch(), ep_ll_dispatch() and ep_moe_layer().  Keys are compared as 64-bit
+ * arithmetic gives them (without bias and groups, the logits themselves): rounding does not choose
+ * experts.  A logit of -inf or NaN, or a bias of -inf or NaN, keeps its expert from being chosen (the first two
+ * count nothing in the softmax); +inf counts as the largest finite value.  Slots that no expert is left for, and all slots of
+ * tokens whose token_mask (one byte each, NULL = all 1) is 0, get -1 and weight 0. */
+ep_status ep_router(ep_handle* h, int64_t num_tokens, const void* logits, ep_dtype logits_dtype, const float* bias,
+                    const uint8_t* token_mask, int32_t score, int32_t num_groups, int32_t kept_groups,
+                    int32_t normalize, float scale, int64_t* topk_idx, float* topk_weights, ep_stream_t stream);
+
+/* Its gradient: d_logits (the logits' type and shape; every element is written) from d_topk_weights (fp32
+ * [num_tokens][K]) and the topk_idx of the forward pass, with the same score, normalize and scale; slots of -1 count
+ * nothing, an expert that a token names twice counts twice.  An index outside [-1, E) sets EP_ERR_BAD_EXPERT and
+ * counts nothing.  d_logits may not be logits. */
+ep_status ep_router_grad(ep_handle* h, int64_t num_tokens, const void* logits, ep_dtype logits_dtype,
+                         const int64_t* topk_idx, const float* d_topk_weights, int32_t score, int32_t normalize,
+                         float scale, void* d_logits, ep_stream_t stream);
+
+/* A whole layer of experts for a few tokens, R * num_tokens <= 64: dispatch, both products with the gated
+ * activation, and combine, in two kernels that read the weights of the experts that are hit once:
+ *   out[t] = sum_k topk_weights[t][k] * w_down[e] (silu(g) * u) + bias_0[t] + bias_1[t],   e = topk_idx[t][k],
+ *   [g | u] = w_up[e] x[t]
+ * x, out and the biases (NULL = 0) bf16 [R][num_tokens][H]; topk_idx and topk_weights [R][num_tokens][K]
+ * as for ep_ll_dispatch(), slots of -1, from or to a masked rank left out, an expert named twice counted
+ * twice; an index outside [-1, E) sets EP_ERR_BAD_EXPERT and is left out.  w_up [E][2 * width][H] (gate rows,
+ * then up rows) and w_down [E][H][width] are bf16 (scales NULL), or e4m3 codes with fp32 scales per 128 x 128
+ * (w_up_scales [E][2 * width / 128][H / 128], w_down_scales [E][H / 128][width / 128]; H and width multiples
+ * of 128).  silu(g) * u is rounded to bf16; the tokens are not rounded to FP8.  With FP8 weights an
+ * infinite value makes its token's outputs NaN.  out may not be x.
+ * The order of the sums is fixed by the routing and the handle.  workspace: ep_moe_layer_workspace() bytes (-1: bad
+ * arguments) whose content does not matter, in use until the call has run. */
+int64_t ep_moe_layer_workspace(const ep_handle* h, int32_t num_tokens, int32_t width);
+ep_status ep_moe_layer(ep_handle* h, int32_t num_tokens, int32_t width, const void* x, const int64_t* topk_idx,
+                       const float* topk_weights, const void* w_up, const float* w_up_scales, const void* w_down,
+                       const float* w_down_scales, ep_dtype w_dtype, const void* bias_0, const void* bias_1, void* out,
+                       void* workspace, int64_t workspace_bytes, ep_stream_t stream);
 
 /* ------------------------------------------------------------ launch model
  * The SM-count model of [P1] (get_theoretical_num_sms, elastic.py), with the
