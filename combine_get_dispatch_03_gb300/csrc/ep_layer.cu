@@ -6,9 +6,9 @@
 // tensor cores' products (128 at a time) and the tokens their columns (16 to 64): every byte of weights goes from memory to
 // shared memory by tensor map and into tcgen05.mma once, and no product has empty rows of weights.
 //   up     a tile is 128 gate rows and the 128 up rows beside them, times ALL tokens' x: no gather, the columns of tokens
-//          that are not the expert's are not read back.  silu(gate) * up goes to a workspace row of (expert, token).
-//   down   a tile is 128 output channels of one expert, times its rows of the workspace; a CTA adds up the weighted
-//          results of the experts it works on in shared memory, [token][128 channels] in fp32.
+//          that are not the expert's are dropped.  silu(gate) * up goes to a workspace row of (expert, token).
+//   down   a tile is 256 output channels of one expert, times its rows of the workspace; a CTA adds up the weighted
+//          results of the experts it works on in shared memory, [token][256 channels] in fp32.
 //
 // The work of a kernel is one row of units (a tile's step of 128 bytes of the contraction) that the CTAs share evenly, so
 // that none waits for a last wave: 8 experts of 7168 x 2048 are 128 tiles of the first kernel on 152 SMs.  A tile that
@@ -18,8 +18,8 @@
 // fills its shared memory with weights, which do not hang on the first kernel, before it waits for it.
 //
 // FP8 weights: e4m3 with one scale per 128 x 128.  The tokens stay bf16: a block of 128 channels is scaled by a power of two
-// and split into two e4m3 values (split_e4m3()) whose products share an accumulator, so that nothing of bf16's eight bits is lost but
-// what lies 2^-17 below the block's largest value.  A block's sums are scaled and added up in fp32 registers.
+// and split into two e4m3 values (split_e4m3()), columns of their own in the products, so that nothing of bf16's eight bits is
+// lost but what lies 2^-17 below the block's largest value.  A block's sums are added, scaled and added up in fp32 registers.
 #include "ep_act.cuh"
 #include "ep_groups.cuh"
 #include "ep_handle.h"
@@ -31,17 +31,21 @@ namespace ep {
 namespace {
 
 constexpr int kMaxTokens = 64;
-constexpr int kTile = 128;                  // rows of weights
+constexpr int kTile = 128;                  // rows of weights of a product
+constexpr int kOps = 2;                     // products of a unit: gate and up, or two times 128 channels
+constexpr int kSwap = 4;                    // up: tokens whose gates and ups change hands at a time
 constexpr uint32_t kRow = 128;              // bytes of the contraction in a stage
 constexpr uint32_t kTileBytes = kTile * kRow;
-constexpr int kColStep = 16;                // tokens (columns of products) come in steps of this
+constexpr int col_step(bool fp8) { return fp8 ? 8 : 16; }  // tokens come in steps of 16 columns of products, FP8 two columns a token
 constexpr int kMaxStages = 8;
+constexpr int kLeastUnits = 4;
 constexpr int kSumWarps = 8;                // warps 4 to 11: accumulators to sums and out
-constexpr int kSplitWarps = 4;              // warps 12 to 15, FP8: x in two e4m3 parts
 constexpr int kScaleRing = 16;              // blocks whose token scales are kept: more than stages and accumulators
-constexpr int kBuffers = 2;                 // accumulators
 constexpr int kSmallTokens = 16;            // up to which both kernels fit an SM
-static_assert(kScaleRing > kMaxStages + kBuffers + 1, "a block's scales outlive it");
+constexpr int buffers(int tokens) { return tokens <= kSmallTokens ? 4 : 2; }  // accumulators
+constexpr int batch_pairs(int tokens) { return tokens <= kSmallTokens ? 4 : 8; }  // of tokens that a splitting warp has in hand, and as many on their way
+constexpr int kSplitWarps = 4;              // warps 12 to 15, FP8: the tokens' values in two e4m3 parts
+static_assert(kScaleRing > kMaxStages + 4 + 1, "a block's scales outlive it");
 constexpr int layer_threads(bool fp8) { return (4 + kSumWarps + (fp8 ? kSplitWarps : 0)) * kWarpSize; }
 
 struct LayerParams {
@@ -51,7 +55,7 @@ struct LayerParams {
     const uint8_t* tokens_x;   // up: x rows; down: the workspace's rows (bf16)
     const float* w_scales;     // FP8
     uint8_t* act;              // [rows][width] bf16
-    float* partial;            // of this kernel: up [CTA][2][token][gate, up][128], down [CTA][2][token][128]
+    float* partial;            // of this kernel: [CTA][2][token][gate, up or channels][128]
     int32_t* tickets;          // [CTAs], 0
     const uint8_t* bias_0;
     const uint8_t* bias_1;
@@ -59,10 +63,13 @@ struct LayerParams {
     int32_t* status;
     uint64_t wait_limit_ns;
     int32_t tokens, tokens_per_rank, topk, experts, local_experts, hidden, width;
-    int32_t cols;              // tokens, rounded up to kColStep
-    int32_t stages;
+    int32_t cols;              // tokens, rounded up to col_step()
+    uint32_t op_cols;          // columns of tensor memory for a product: cols, FP8 twice that
+    int32_t stages, ctas;
     uint32_t stage_bytes, tmem_columns;
 };
+
+__host__ __device__ inline int part_words(int ctas) { return (ctas + kWarpSize - 1) / kWarpSize; }
 
 struct LayerMaps {
     CUtensorMap w, x;
@@ -71,14 +78,14 @@ struct LayerMaps {
 struct LayerControl {
     uint64_t full[kMaxStages];
     uint64_t empty[kMaxStages];
-    uint64_t acc_full[kBuffers];
-    uint64_t acc_empty[kBuffers];
+    uint64_t acc_full[4];
+    uint64_t acc_empty[4];
     uint64_t drained;
     uint32_t tmem;
     int32_t abort_flag;
-    int32_t last_arrival;
+    int32_t last_arrival[2];
     int32_t hits;
-    int64_t sums[16];
+    int64_t sums[20];
 };
 
 // Which experts the tokens hit, in shared memory.
@@ -92,23 +99,25 @@ struct Routing {
 __device__ __forceinline__ int count_bits(uint64_t m) { return __popcll(static_cast<long long>(m)); }
 __device__ __forceinline__ int lowest_bit(uint64_t m) { return __ffsll(static_cast<long long>(m)) - 1; }
 
-// The expert of slot (token, k), -1 for none: as in the low-latency dispatch, a masked rank neither sends nor receives.
-__device__ __forceinline__ int slot_expert(const LayerParams& p, int slot) {
-    const int64_t e = p.topk_idx[slot];
+// The expert of a token's slot that names `e`, -1 for none: as in the low-latency dispatch, a masked rank neither sends nor receives.
+__device__ __forceinline__ int slot_expert(const LayerParams& p, uint32_t masked, int64_t e, int token) {
     if (e < 0 || e >= p.experts) return -1;
-    if (p.rank_mask[slot / p.topk / p.tokens_per_rank] || p.rank_mask[static_cast<int>(e) / p.local_experts]) return -1;
+    if (masked && ((masked >> (token / p.tokens_per_rank) | masked >> (static_cast<int>(e) / p.local_experts)) & 1)) return -1;
     return static_cast<int>(e);
 }
 
 template <int THREADS, bool kWeights>
 __device__ __forceinline__ void build_routing(const Routing& t, const LayerParams& p, LayerControl& ctl) {
+    const int slots = p.tokens * p.topk;
+    // a thread's first slot is on its way meanwhile, as the ranks' masks are
+    const int64_t raw0 = static_cast<int>(threadIdx.x) < slots ? p.topk_idx[threadIdx.x] : -1;
+    const uint32_t masked = __ballot_sync(kFullMask, lane_id() < p.experts / p.local_experts && p.rank_mask[lane_id()] != 0);
     for (int e = threadIdx.x; e < p.experts; e += THREADS) t.tokens[e] = 0;
     __syncthreads();
-    const int slots = p.tokens * p.topk;
     for (int s = threadIdx.x; s < slots; s += THREADS) {
-        const int64_t raw = p.topk_idx[s];
+        const int64_t raw = s == static_cast<int>(threadIdx.x) ? raw0 : p.topk_idx[s];
         if (raw < -1 || raw >= p.experts) report(p.status, EP_ERR_BAD_EXPERT);
-        const int e = slot_expert(p, s);
+        const int e = slot_expert(p, masked, raw, s / p.topk);
         if (e >= 0) atomicOr(reinterpret_cast<unsigned long long*>(&t.tokens[e]), 1ull << (s / p.topk));
     }
     __syncthreads();
@@ -129,9 +138,9 @@ __device__ __forceinline__ void build_routing(const Routing& t, const LayerParam
     if constexpr (kWeights) {
         // an expert that a token names twice counts with both weights
         for (int s = threadIdx.x; s < slots; s += THREADS) {
-            const int e = slot_expert(p, s);
-            if (e < 0) continue;
             const int token = s / p.topk;
+            const int e = slot_expert(p, masked, p.topk_idx[s], token);
+            if (e < 0) continue;
             bool before = false;
             float w = 0.0f;
             for (int q = token * p.topk; q < (token + 1) * p.topk; ++q) {
@@ -153,28 +162,52 @@ struct Shares {
     __device__ __forceinline__ int owner(int64_t unit) const { return static_cast<int>(((unit + 1) * ctas - 1) / units); }
 };
 
-// A unit: a tile and a step of its contraction.
-struct Unit {
-    int expert, col, step;  // col: first gate row (up) or output channel (down) of the tile
-    uint64_t tokens;
-};
-
+// A CTA's units [first, last): steps of `steps` of the contraction of tiles, by expert and then `across` (up), or
+// across and then by expert (down).
 template <bool kDown>
 struct Work {
     const Routing& t;
     Shares shares;
     int64_t first, last;
     int hits, across, steps;
+};
 
-    __device__ __forceinline__ Unit at(int64_t unit) const {
-        const int tile = static_cast<int>(unit / steps);
-        Unit u;
-        u.step = static_cast<int>(unit - static_cast<int64_t>(tile) * steps);
-        const int i = kDown ? tile % hits : tile / across;
-        u.expert = t.hit[i];
-        u.col = (kDown ? tile / hits : tile % across) * kTile;
-        u.tokens = t.tokens[u.expert];
-        return u;
+// A unit: a tile and a step of its contraction.  Moves on without divisions, which a thread alone waits for long.
+template <bool kDown>
+struct Unit {
+    const Work<kDown>& w;
+    int64_t at;
+    int step, hit, col;  // col: first gate row (up) or output channel (down) of the tile
+    int expert;
+    uint64_t tokens;
+
+    __device__ __forceinline__ Unit(const Work<kDown>& work, int64_t unit) : w(work), at(unit) {
+        if (!more()) return;
+        const int tile = static_cast<int>(unit / w.steps);
+        step = static_cast<int>(unit - static_cast<int64_t>(tile) * w.steps);
+        hit = kDown ? tile % w.hits : tile / w.across;
+        col = kDown ? tile / w.hits * (kOps * kTile) : tile % w.across * kTile;
+        look();
+    }
+    __device__ __forceinline__ bool more() const { return at < w.last; }
+    __device__ __forceinline__ void look() {
+        expert = w.t.hit[hit];
+        tokens = w.t.tokens[expert];
+    }
+    // n units on, at most a tile's
+    __device__ __forceinline__ void move(int n) {
+        at += n;
+        step += n;
+        while (step >= w.steps && more()) {
+            step -= w.steps;
+            if (kDown) {
+                if (++hit == w.hits) hit = 0, col += kOps * kTile;
+            } else {
+                col += kTile;
+                if (col >= w.across * kTile) col = 0, ++hit;
+            }
+            look();
+        }
     }
 };
 
@@ -188,37 +221,50 @@ struct LayerRoles {
     LayerControl& ctl;
     Waits waits;
     uint8_t* stages;
-    float* scales;   // FP8: [kScaleRing][kMaxTokens] of the tokens' blocks
-    float* sums;     // down: [tokens][128]
+    float* scales;   // FP8: [kScaleRing][kTokens] of the tokens' blocks
+    float* sums;     // down: [tokens][256]; up: [kSwap][gate, up][128]
+    uint32_t* parts;  // down: [tokens][part_words] a bit for each CTA whose part has something for the token
 };
 
-constexpr uint32_t a_bytes(bool down) { return down ? kTileBytes : 2 * kTileBytes; }
+constexpr uint32_t kABytes = kOps * kTileBytes;
 
-__device__ __forceinline__ int round_cols(int n) { return (n + kColStep - 1) / kColStep * kColStep; }
+template <bool kFp8>
+__device__ __forceinline__ int round_cols(int n) { return (n + col_step(kFp8) - 1) / col_step(kFp8) * col_step(kFp8); }
+
+// Tokens of a unit: up all, down the expert's; as columns of products.
+template <bool kDown>
+__device__ __forceinline__ int unit_tokens(const LayerParams& p, const Unit<kDown>& u) {
+    return kDown ? count_bits(u.tokens) : p.tokens;
+}
+
+template <bool kFp8, bool kDown>
+__device__ __forceinline__ int unit_cols(const LayerParams& p, const Unit<kDown>& u) {
+    return kDown ? round_cols<kFp8>(count_bits(u.tokens)) : p.cols;
+}
 
 // Weights of a unit into its stage.
 template <bool kFp8, bool kDown>
-__device__ __forceinline__ void load_weights(const LayerRoles<kDown>& x, const Unit& u, int stage) {
+__device__ __forceinline__ void load_weights(const LayerRoles<kDown>& x, const Unit<kDown>& u, int stage) {
     const int k0 = u.step * (kFp8 ? 128 : 64);
     uint8_t* a = x.stages + stage * x.p.stage_bytes;
     const uint32_t bar = smem_u32(&x.ctl.full[stage]);
     tma_load_3d<1>(a, &x.maps.w, k0, u.col, u.expert, bar);
-    if (!kDown) tma_load_3d<1>(a + kTileBytes, &x.maps.w, k0, x.p.width + u.col, u.expert, bar);
+    tma_load_3d<1>(a + kTileBytes, &x.maps.w, k0, (kDown ? kTile : x.p.width) + u.col, u.expert, bar);
 }
 
 // Bytes and copies of a unit's tokens, bf16.
 template <bool kDown>
-__device__ __forceinline__ uint32_t token_bytes(const LayerParams& p, const Unit& u) {
-    return (kDown ? round_cols(count_bits(u.tokens)) : p.cols) * kRow;
+__device__ __forceinline__ uint32_t token_bytes(const LayerParams& p, const Unit<kDown>& u) {
+    return unit_cols<false>(p, u) * kRow;
 }
 
 template <bool kDown>
-__device__ __forceinline__ void load_tokens(const LayerRoles<kDown>& x, const Unit& u, int stage) {
-    uint8_t* b = x.stages + stage * x.p.stage_bytes + a_bytes(kDown);
+__device__ __forceinline__ void load_tokens(const LayerRoles<kDown>& x, const Unit<kDown>& u, int stage) {
+    uint8_t* b = x.stages + stage * x.p.stage_bytes + kABytes;
     const uint32_t bar = smem_u32(&x.ctl.full[stage]);
     const int first = kDown ? x.t.begin[u.expert] : 0;
-    const int cols = kDown ? round_cols(count_bits(u.tokens)) : x.p.cols;
-    for (int c = 0; c < cols; c += kColStep) tma_load_2d<1>(b + c * kRow, &x.maps.x, u.step * 64, first + c, bar);
+    const int cols = unit_cols<false>(x.p, u);
+    for (int c = 0; c < cols; c += col_step(false)) tma_load_2d<1>(b + c * kRow, &x.maps.x, u.step * 64, first + c, bar);
 }
 
 // One thread: the loads.
@@ -227,31 +273,29 @@ __device__ __forceinline__ void layer_loads(const LayerRoles<kDown>& x) {
     const LayerParams& p = x.p;
     LayerControl& ctl = x.ctl;
     const Work<kDown>& w = x.work;
-    int64_t unit = w.first;
+    Unit<kDown> u(w, w.first);
     bool ok = true;
     int stage = 0, used = 0;
     uint32_t phase = 0;
     if constexpr (kDown) {
         // Weights for every stage, then the first kernel's results.
-        const int ahead = static_cast<int>(min(static_cast<int64_t>(p.stages), w.last - w.first));
-        for (int i = 0; i < ahead; ++i) {
-            const Unit u = w.at(unit + i);
-            bar_arrive_expect_tx<1>(smem_u32(&ctl.full[i]), a_bytes(kDown) + (kFp8 ? 0 : token_bytes<kDown>(p, u)));
-            load_weights<kFp8, kDown>(x, u, i);
+        Unit<kDown> v = u;
+        int ahead = 0;
+        for (; ahead < p.stages && u.more(); ++ahead, u.move(1)) {
+            bar_arrive_expect_tx<1>(smem_u32(&ctl.full[ahead]), kABytes + (kFp8 ? 0 : token_bytes<kDown>(p, u)));
+            load_weights<kFp8, kDown>(x, u, ahead);
         }
         asm volatile("griddepcontrol.wait;" ::: "memory");
         if constexpr (!kFp8)
-            for (int i = 0; i < ahead; ++i) load_tokens<kDown>(x, w.at(unit + i), i);
-        unit += ahead;
+            for (int i = 0; i < ahead; ++i, v.move(1)) load_tokens<kDown>(x, v, i);
         used = ahead;
         if (ahead == p.stages) phase = 1;
         else stage = ahead;
     }
-    for (; unit < w.last; ++unit) {
+    for (; u.more(); u.move(1)) {
         ok = wait_phase(&ctl.empty[stage], phase ^ 1, x.waits);
         if (!ok) break;
-        const Unit u = w.at(unit);
-        bar_arrive_expect_tx<1>(smem_u32(&ctl.full[stage]), a_bytes(kDown) + (kFp8 ? 0 : token_bytes<kDown>(p, u)));
+        bar_arrive_expect_tx<1>(smem_u32(&ctl.full[stage]), kABytes + (kFp8 ? 0 : token_bytes<kDown>(p, u)));
         load_weights<kFp8, kDown>(x, u, stage);
         if constexpr (!kFp8) load_tokens<kDown>(x, u, stage);
         ++used;
@@ -275,7 +319,7 @@ __device__ __forceinline__ void layer_loads(const LayerRoles<kDown>& x) {
 }
 
 // One thread: the products.
-template <bool kFp8, bool kDown>
+template <bool kFp8, int kTokens, bool kDown>
 __device__ __forceinline__ void layer_products(const LayerRoles<kDown>& x) {
     const LayerParams& p = x.p;
     LayerControl& ctl = x.ctl;
@@ -283,33 +327,28 @@ __device__ __forceinline__ void layer_products(const LayerRoles<kDown>& x) {
     int stage = 0, buf = 0;
     uint32_t phase = 0, acc_phase = 0;
     bool first = true;  // of an accumulator
-    for (int64_t unit = w.first; unit < w.last; ++unit) {
-        const Unit u = w.at(unit);
+    for (Unit<kDown> u(w, w.first); u.more(); u.move(1)) {
         if (!wait_phase(&ctl.full[stage], phase, x.waits)) break;
         if (first && !wait_phase(&ctl.acc_empty[buf], acc_phase ^ 1, x.waits)) break;
         tc_fence_after();
-        const uint32_t cols = kDown ? round_cols(count_bits(u.tokens)) : p.cols;
+        const uint32_t cols = (kFp8 ? 2 : 1) * unit_cols<kFp8>(p, u);  // FP8: both parts' columns
         const uint32_t idesc = mma_desc(kFp8 ? 0 : 1, false, false, kTile, cols);
         const uint32_t a = smem_u32(x.stages) + stage * p.stage_bytes;
-        const uint32_t d = ctl.tmem + buf * (kDown ? 1 : 2) * p.cols;
+        const uint32_t d = ctl.tmem + buf * kOps * p.op_cols;
+        const uint64_t db = smem_desc(a + kABytes, 16);
 #pragma unroll
-        for (int part = 0; part < (kFp8 ? 2 : 1); ++part) {
-            const uint64_t db = smem_desc(a + a_bytes(kDown) + part * p.cols * kRow, 16);
+        for (int op = 0; op < kOps; ++op) {
+            const uint64_t da = smem_desc(a + op * kTileBytes, 16);
 #pragma unroll
-            for (int op = 0; op < (kDown ? 1 : 2); ++op) {
-                const uint64_t da = smem_desc(a + op * kTileBytes, 16);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    tc_mma<1, kFp8>(d + op * p.cols, da + i * 2, db + i * 2, idesc, !first || part || i);
-            }
+            for (int i = 0; i < 4; ++i) tc_mma<1, kFp8>(d + op * p.op_cols, da + i * 2, db + i * 2, idesc, !first || i);
         }
         tc_commit<1>(&ctl.empty[stage]);
         first = false;
-        if (kFp8 || u.step == w.steps - 1 || unit == w.last - 1) {
+        if (kFp8 || u.step == w.steps - 1 || u.at == w.last - 1) {
             // this thread's own arrival passes on what it acquired with the stage: the tokens' scales
             bar_arrive<1>(smem_u32(&ctl.acc_full[buf]));
             tc_commit<1>(&ctl.acc_full[buf]);
-            if (++buf == kBuffers) buf = 0, acc_phase ^= 1;
+            if (++buf == buffers(kTokens)) buf = 0, acc_phase ^= 1;
             first = true;
         }
         if (++stage == p.stages) stage = 0, phase ^= 1;
@@ -334,331 +373,397 @@ __device__ __forceinline__ void split_e4m3(const float (&f)[8], float mult, uint
     *low = make_uint2(l[0], l[1]);
 }
 
-// Four warps, FP8: the tokens' blocks of a unit, split, into the place and order in which a tensor-map load would put
-// them.  Sixteen lanes have a token's 128 channels; the next unit's values are on their way meanwhile.
+// FP8: the tokens' blocks of a unit, split, into the place and order in which a tensor-map load would put them: a row
+// for each token's first part, then one for each second.  The warps take units in turn, so that each has several units' time
+// for a round trip to memory; half a warp has a token's 128 channels, and a batch's values are loaded before the one before it
+// is worked on.  No more warps than stages: one that waits for a stage's use has filled a stage after the use before the last,
+// so that the barrier's parity tells the two uses apart.
 template <int kTokens, bool kDown>
 __device__ __forceinline__ void layer_splits(const LayerRoles<kDown>& x, int warp) {
-    constexpr int kPer = kTokens / (2 * kSplitWarps);  // tokens of half a warp
+    constexpr int kBatchPairs = batch_pairs(kTokens);
+    constexpr int kBatch = 2 * kBatchPairs;  // tokens
     const LayerParams& p = x.p;
     LayerControl& ctl = x.ctl;
     const Work<kDown>& w = x.work;
     const int64_t row_bytes = 2 * static_cast<int64_t>(kDown ? p.width : p.hidden);
-    const int first_token = warp * 2 + (lane_id() >> 4), piece = lane_id() & 15;
-    int4 next[kPer];
-    auto fetch = [&](int64_t unit) {
-        const Unit u = w.at(unit);
-        const int count = kDown ? count_bits(u.tokens) : p.tokens;
-        const int64_t row0 = kDown ? x.t.begin[u.expert] : 0;
+    const int half = lane_id() >> 4, piece = lane_id() & 15;
+    const int warps = min(kSplitWarps, p.stages);
+    if (warp >= warps) return;
+    // what is loaded next: tokens [first, count) of a unit
+    Unit<kDown> next(w, w.first + warp);
+    int next_first = 0, next_count = 0;
+    const uint8_t* next_row = nullptr;
+    auto enter = [&] {
+        next_first = next_count = 0;
+        if (!next.more()) return;
+        next_count = unit_tokens(p, next);
+        next_row = p.tokens_x + (kDown ? x.t.begin[next.expert] : 0) * row_bytes + next.step * 256 + half * row_bytes + piece * 16;
+    };
+    int4 ahead[kBatchPairs];
+    auto fetch = [&] {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int t = first_token + i * 2 * kSplitWarps;
-            next[i] = make_int4(0, 0, 0, 0);
-            if (t < count) next[i] = __ldcg(reinterpret_cast<const int4*>(p.tokens_x + (row0 + t) * row_bytes + u.step * 256) + piece);
+        for (int i = 0; i < kBatchPairs; ++i) {
+            ahead[i] = make_int4(0, 0, 0, 0);
+            if (next_first + 2 * i + half < next_count)
+                ahead[i] = __ldcg(reinterpret_cast<const int4*>(next_row + (next_first + 2 * i) * row_bytes));
         }
     };
+    auto advance = [&] {
+        next_first += kBatch;
+        if (next_first >= next_count) next.move(warps), enter();
+        fetch();
+    };
     if (kDown) asm volatile("griddepcontrol.wait;" ::: "memory");
-    int stage = 0;
+    enter();
+    fetch();
+    int stage = warp;
     uint32_t phase = 0;
-    if (w.first < w.last) fetch(w.first);
-    for (int64_t unit = w.first; unit < w.last; ++unit) {
-        const int count = kDown ? count_bits(w.at(unit).tokens) : p.tokens;
+    for (int64_t unit = w.first + warp; unit < w.last; unit += warps) {
+        const int count = next_count;  // at least one
+        const uint32_t low_part = round_cols<true>(count) * kRow;
         if (!warp_wait(&ctl.empty[stage], phase ^ 1, x.waits)) break;
-        uint8_t* b = x.stages + stage * p.stage_bytes + a_bytes(kDown);
-        float* scales = x.scales + static_cast<int>((unit - w.first) % kScaleRing) * kMaxTokens;
+        uint8_t* b = x.stages + stage * p.stage_bytes + kABytes;
+        float* scales = x.scales + static_cast<int>((unit - w.first) % kScaleRing) * kTokens;
+        for (int first = 0; first < count; first += kBatch) {
+            int4 value[kBatchPairs];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int t = first_token + i * 2 * kSplitWarps;
-            if (t - (lane_id() >> 4) >= count) break;  // the whole warp
-            float f[8];
-            unpack8(next[i], f);
-            float most = absmax8(f);
+            for (int i = 0; i < kBatchPairs; ++i) value[i] = ahead[i];
+            advance();
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kFullMask, most, o));
-            // 2^(7 - exponent), at most 2^126; an infinite value has no scale and makes the token's sums NaN, as NaN does
-            const int exponent = static_cast<int>(__float_as_uint(most) >> 23);
-            const int up = min(134 - exponent, 126);
-            const float mult = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-            uint2 high, low;
-            split_e4m3(f, mult, &high, &low);
-            if (t < count) {
-                const uint32_t at = t * kRow + (((piece >> 1) ^ (t & 7)) << 4) + (piece & 1) * 8;
-                *reinterpret_cast<uint2*>(b + at) = high;
-                *reinterpret_cast<uint2*>(b + p.cols * kRow + at) = low;
-                if (piece == 0) scales[t] = exponent == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+            for (int i0 = 0; i0 < kBatchPairs; i0 += 2) {  // two at a time: there are registers for no more
+                if (first + 2 * i0 >= count) break;
+                float f[2][8], most[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    unpack8(value[i0 + i], f[i]);
+                    most[i] = absmax8(f[i]);
+                }
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) most[i] = fmaxf(most[i], __shfl_xor_sync(kFullMask, most[i], o));
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    // 2^(7 - exponent), at most 2^126; an infinite value has no scale and makes the token's sums NaN, as NaN does
+                    const int exponent = static_cast<int>(__float_as_uint(most[i]) >> 23);
+                    const int up = min(134 - exponent, 126);
+                    uint2 high, low;
+                    split_e4m3(f[i], __uint_as_float(static_cast<uint32_t>(127 + up) << 23), &high, &low);
+                    const int t = first + 2 * (i0 + i) + half;
+                    if (t < count) {
+                        const uint32_t at = t * kRow + (((piece >> 1) ^ (t & 7)) << 4) + (piece & 1) * 8;
+                        *reinterpret_cast<uint2*>(b + at) = high;
+                        *reinterpret_cast<uint2*>(b + low_part + at) = low;
+                        if (piece == 0) scales[t] = exponent == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+                    }
+                }
             }
         }
         fence_async_smem();
         __syncwarp();
         if (lane_id() == 0) bar_arrive<1>(smem_u32(&ctl.full[stage]));
-        if (unit + 1 < w.last) fetch(unit + 1);
-        if (++stage == p.stages) stage = 0, phase ^= 1;
+        stage += warps;  // at most once around
+        if (stage >= p.stages) stage -= p.stages, phase ^= 1;
     }
 }
 
-// One fp32 column of this warp's 32 lanes of tensor memory: starts the load.
-__device__ __forceinline__ void tc_ld1(uint32_t addr, uint32_t& v) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v) : "r"(addr));
+// 8 fp32 columns of this warp's 32 lanes of tensor memory: starts the load.
+__device__ __forceinline__ void tc_ld8(uint32_t addr, uint32_t (&v)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(addr));
 }
 
-template <int N>
-__device__ __forceinline__ void tc_wait_columns(uint32_t (&v)[N]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));  // no use before the wait
+// Waits for this thread's loads; no use of `v` is scheduled before it.
+__device__ __forceinline__ void tc_wait8(uint32_t (&v)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7])
+                 :: "memory");
 }
 
 __device__ __forceinline__ void sum_warps_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kSumWarps * kWarpSize) : "memory"); }
 
 // After the sum warps wrote a part of what `parts` CTAs add up: whether this CTA is the last to arrive, and may read all.
 template <bool kDown>
-__device__ __forceinline__ bool last_to_arrive(const LayerRoles<kDown>& x, int ticket, int parts) {
+__device__ __forceinline__ bool last_to_arrive(const LayerRoles<kDown>& x, int ticket, int parts, int& turn) {
     __threadfence();
     sum_warps_barrier();
     if (threadIdx.x == 4 * kWarpSize) {
         const bool last = atomicAdd(x.p.tickets + ticket, 1) == parts - 1;
         if (last) x.p.tickets[ticket] = 0;  // for the next call
-        x.ctl.last_arrival = last;
+        x.ctl.last_arrival[turn & 1] = last;
         __threadfence();
     }
     sum_warps_barrier();
-    const bool last = *const_cast<volatile int32_t*>(&x.ctl.last_arrival) != 0;
-    sum_warps_barrier();  // read before the next one is written
-    return last;
+    return *const_cast<volatile int32_t*>(&x.ctl.last_arrival[turn++ & 1]) != 0;  // the other word is written next
 }
 
-// The sums of a run of one tile's units that this CTA has, OPS values for each of a warp's tokens.  column(q): the
-// accumulator's column of its q-th token.
-template <bool kFp8, int OPS, int PER, bool kDown, typename Column>
-__device__ __forceinline__ void read_sums(const LayerRoles<kDown>& x, int64_t unit, int steps, int mine, uint32_t lanes, const Unit& u,
-                                          int& buf, uint32_t& acc_phase, bool& ok, Column column, float (&v)[OPS][PER]) {
+// The sums of a run of one tile's units that this CTA has, for all columns of a thread's row of one product.
+template <bool kFp8, int kTokens, bool kDown>
+__device__ __forceinline__ void read_sums(const LayerRoles<kDown>& x, int steps, int quarter, int op, const Unit<kDown>& u, int& buf,
+                                          uint32_t& acc_phase, bool& ok, float (&v)[kTokens]) {
     const LayerParams& p = x.p;
     LayerControl& ctl = x.ctl;
-    constexpr int kBatch = 4;
+    const int count = unit_tokens(p, u), cols = unit_cols<kFp8>(p, u);
 #pragma unroll
-    for (int o = 0; o < OPS; ++o)
-#pragma unroll
-        for (int q = 0; q < PER; ++q) v[o][q] = 0.0f;
-    const float* ws[OPS];
-    float w_next[OPS];
+    for (int t = 0; t < kTokens; ++t) v[t] = 0.0f;
+    const float* ws = nullptr;
+    float w_next = 0.0f;
     if constexpr (kFp8) {
-#pragma unroll
-        for (int o = 0; o < OPS; ++o) {
-            const int rows = (kDown ? p.hidden : 2 * p.width) / kFp8Group;
-            const int row = u.col / kFp8Group + o * (p.width / kFp8Group);
-            ws[o] = p.w_scales + (static_cast<int64_t>(u.expert) * rows + row) * x.work.steps + u.step;
-            w_next[o] = __ldg(ws[o]);
-        }
+        const int rows = (kDown ? p.hidden : 2 * p.width) / kFp8Group;
+        const int row = min(u.col / kFp8Group + op * (kDown ? 1 : p.width / kFp8Group), rows - 1);  // the last channels: no second half
+        ws = p.w_scales + (static_cast<int64_t>(u.expert) * rows + row) * x.work.steps + u.step;
+        w_next = __ldg(ws);
     }
     for (int s = 0; s < (kFp8 ? steps : 1); ++s) {
-        float ww[OPS];
-        if constexpr (kFp8) {
-#pragma unroll
-            for (int o = 0; o < OPS; ++o) {
-                ww[o] = w_next[o];
-                w_next[o] = __ldg(ws[o] + min(s + 1, steps - 1));
-            }
-        }
+        const float w = w_next;
+        if constexpr (kFp8) w_next = __ldg(ws + min(s + 1, steps - 1));
         if (ok) ok = warp_wait(&ctl.acc_full[buf], acc_phase, x.waits);
         if (!ok) return;
         tc_fence_after();
-        const uint32_t from = ctl.tmem + lanes + buf * OPS * p.cols;
-        const float* scales = x.scales + static_cast<int>((unit + s - x.work.first) % kScaleRing) * kMaxTokens;
+        const uint32_t from = ctl.tmem + (static_cast<uint32_t>(quarter * 32) << 16) + (buf * kOps + op) * p.op_cols;
+        const float4* scales = reinterpret_cast<const float4*>(x.scales + static_cast<int>((u.at + s - x.work.first) % kScaleRing) * kTokens);
 #pragma unroll
-        for (int q0 = 0; q0 < PER; q0 += kBatch) {
-            if (q0 >= mine) break;
-            uint32_t r[OPS * kBatch];
+        for (int c = 0; c < kTokens; c += 8) {
+            if (c >= count) break;
+            uint32_t r[8], low[8];
+            tc_ld8(from + c, r);
+            if constexpr (kFp8) {
+                tc_ld8(from + cols + c, low);
+                tc_wait8(low);
+            }
+            tc_wait8(r);
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
+            for (int i = 0; i < 8; i += 4) {
+                float4 f = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+                if constexpr (kFp8) f = scales[(c + i) / 4];
+                const float ff[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-                for (int o = 0; o < OPS; ++o) {
-                    r[o * kBatch + i] = 0;
-                    if (q0 + i < mine) tc_ld1(from + o * p.cols + column(q0 + i), r[o * kBatch + i]);
+                for (int j = 0; j < 4; ++j) {
+                    const float d = __uint_as_float(r[i + j]);
+                    if constexpr (kFp8) v[c + i + j] = fmaf(d + __uint_as_float(low[i + j]), ff[j] * w, v[c + i + j]);
+                    else v[c + i + j] = d;
                 }
             }
-            tc_wait_columns(r);
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-#pragma unroll
-                for (int o = 0; o < OPS; ++o) {
-                    const float d = __uint_as_float(r[o * kBatch + i]);
-                    if constexpr (!kFp8) v[o][q0 + i] = d;
-                    else if (q0 + i < mine) v[o][q0 + i] = fmaf(d, ww[o] * scales[column(q0 + i)], v[o][q0 + i]);
-                }
         }
         tc_fence_before();
         __syncwarp();
         if (lane_id() == 0) bar_arrive<1>(smem_u32(&ctl.acc_empty[buf]));
-        if (++buf == kBuffers) buf = 0, acc_phase ^= 1;
+        if (++buf == buffers(kTokens)) buf = 0, acc_phase ^= 1;
     }
 }
 
-// Eight warps of the first kernel: accumulators to silu(gate) * up.  A warp has 32 rows of the tile and every second
-// token of the expert.
+// The same bits, which the compiler does not take apart early: 64 predicates have no registers.
+__device__ __forceinline__ uint64_t unseen(uint64_t bits) {
+    asm volatile("" : "+l"(bits));
+    return bits;
+}
+
+// bf16, as the second product's operand is.
+__device__ __forceinline__ void put_act(const LayerParams& p, int64_t act_row, int col, float gate, float up) {
+    if (col < p.width)
+        *reinterpret_cast<__nv_bfloat16*>(p.act + 2 * (act_row * p.width + col)) = __float2bfloat16_rn(activate(EP_ACT_SILU, gate) * up);
+}
+
+// Eight warps of the first kernel: accumulators to silu(gate) * up.  Four have the tile's gates, four its ups, each 32 rows and
+// all tokens.
 template <bool kFp8, int kTokens>
 __device__ __forceinline__ void up_sums(const LayerRoles<false>& x, int warp) {
-    constexpr int kPer = kTokens / 2;
     const LayerParams& p = x.p;
     const Work<false>& w = x.work;
-    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    const int quarter = warp & 3, op = (warp - 4) >> 2;
     const int row = quarter * 32 + lane_id();
     int buf = 0;
     uint32_t acc_phase = 0;
+    int turn = 0;
     bool ok = true;
-    for (int64_t unit = w.first; unit < w.last;) {
-        const Unit u = w.at(unit);
-        const int steps = static_cast<int>(min(static_cast<int64_t>(w.steps - u.step), w.last - unit));
+    for (Unit<false> u(w, w.first); u.more();) {
+        const int steps = static_cast<int>(min(static_cast<int64_t>(w.steps - u.step), w.last - u.at));
+        float v[kTokens];
+        read_sums<kFp8, kTokens, false>(x, steps, quarter, op, u, buf, acc_phase, ok, v);
         const int count = count_bits(u.tokens);
-        const int mine = (count + 1 - half) / 2;
-        float v[2][kPer];
-        // the columns of this warp's tokens, six bits each in order of q
-        uint8_t tokens[kPer];
-        {
-            uint64_t m = half ? u.tokens & (u.tokens - 1) : u.tokens;
+        const int64_t first = x.t.begin[u.expert];
+        const int thread = threadIdx.x - 4 * kWarpSize;
+        if (steps == w.steps) {
+            // through shared memory, kSwap tokens at a time
+            for (int base = 0; base < count; base += kSwap) {
+                int q = -base;  // the token's number among the expert's, from base
+                const uint64_t has = unseen(u.tokens);
 #pragma unroll
-            for (int q = 0; q < kPer; ++q) {
-                tokens[q] = static_cast<uint8_t>(m ? lowest_bit(m) : 0);
-                m &= m - 1;
-                m &= m - 1;
-            }
-        }
-        read_sums<kFp8, 2, kPer, false>(x, unit, steps, mine, static_cast<uint32_t>(quarter * 32) << 16, u, buf, acc_phase, ok,
-                                        [&](int q) { return static_cast<int>(tokens[q]); }, v);
-        bool finish = true;
-        if (steps < w.steps) {
-            const int64_t tile0 = unit - u.step;
-            const int a = w.shares.owner(tile0), b = w.shares.owner(tile0 + w.steps - 1);
-            const int64_t each = static_cast<int64_t>(p.tokens) * 2 * kTile;
-            float* own = p.partial + (2 * static_cast<int64_t>(blockIdx.x) + (u.step == 0)) * each + row;
-#pragma unroll
-            for (int q = 0; q < kPer; ++q) {
-                if (q >= mine) break;
-                own[(half + 2 * q) * 2 * kTile] = v[0][q];
-                own[(half + 2 * q) * 2 * kTile + kTile] = v[1][q];
-            }
-            finish = last_to_arrive(x, a, b - a + 1);
-            if (finish) {
-#pragma unroll
-                for (int q = 0; q < kPer; ++q) v[0][q] = v[1][q] = 0.0f;
-                for (int c = a; c <= b; ++c) {
-                    const float* part = p.partial + (2 * static_cast<int64_t>(c) + (c == a)) * each + row;
-#pragma unroll
-                    for (int q = 0; q < kPer; ++q) {
-                        if (q >= mine) break;
-                        v[0][q] += __ldcg(part + (half + 2 * q) * 2 * kTile);
-                        v[1][q] += __ldcg(part + (half + 2 * q) * 2 * kTile + kTile);
+                for (int t = 0; t < kTokens; ++t)
+                    if (has >> t & 1) {
+                        if (q >= 0 && q < kSwap) x.sums[(q * kOps + op) * kTile + row] = v[t];
+                        ++q;
                     }
+                sum_warps_barrier();
+                for (int i = thread; i < min(kSwap, count - base) * kTile; i += kSumWarps * kWarpSize) {
+                    const float* from = x.sums + i / kTile * (kOps * kTile) + i % kTile;
+                    put_act(p, first + base + i / kTile, u.col + i % kTile, from[0], from[kTile]);
+                }
+                sum_warps_barrier();
+            }
+        } else {
+            const int64_t tile0 = u.at - u.step;
+            const int a = w.shares.owner(tile0), b = w.shares.owner(tile0 + w.steps - 1);
+            const int64_t each = static_cast<int64_t>(p.tokens) * kOps * kTile;
+            float* own = p.partial + (2 * static_cast<int64_t>(blockIdx.x) + (u.step == 0)) * each + op * kTile + row;
+            const uint64_t has = unseen(u.tokens);
+#pragma unroll
+            for (int t = 0; t < kTokens; ++t)
+                if (has >> t & 1) own[t * (kOps * kTile)] = v[t];
+            if (last_to_arrive(x, a, b - a + 1, turn)) {
+                // two tokens at a time, a thread one of a token's rows: the parts in the CTAs' order
+                uint64_t left = u.tokens;
+                if (thread >= kTile) left &= left - 1;
+                for (int q = thread / kTile; q < count; q += 2) {
+                    const float* part = p.partial + (lowest_bit(left) * kOps) * kTile + thread % kTile;
+                    float gate = __ldcg(part + (2 * static_cast<int64_t>(a) + 1) * each), up = __ldcg(part + (2 * static_cast<int64_t>(a) + 1) * each + kTile);
+#pragma unroll 8
+                    for (int c = a + 1; c <= b; ++c) {
+                        gate += __ldcg(part + 2 * static_cast<int64_t>(c) * each);
+                        up += __ldcg(part + 2 * static_cast<int64_t>(c) * each + kTile);
+                    }
+                    put_act(p, first + q, u.col + thread % kTile, gate, up);
+                    left &= left - 1;
+                    left &= left - 1;
                 }
             }
         }
-        if (finish && u.col + row < p.width) {
-            const int64_t first = x.t.begin[u.expert];
-#pragma unroll
-            for (int q = 0; q < kPer; ++q) {
-                if (q >= mine) break;
-                const float a = activate(EP_ACT_SILU, v[0][q]) * v[1][q];
-                // bf16, as the second product's operand is
-                *reinterpret_cast<__nv_bfloat16*>(p.act + 2 * ((first + half + 2 * q) * p.width + u.col + row)) = __float2bfloat16_rn(a);
-            }
-        }
-        unit += steps;
+        u.move(steps);
     }
 }
 
-// Output channel `row` of a tile for the tokens of one parity, from the sums.
-__device__ __forceinline__ void put_output(const LayerParams& p, int token, int channel, float sum) {
-    const int64_t at = 2 * (static_cast<int64_t>(token) * p.hidden + channel);
-    if (p.bias_0) sum += __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p.bias_0 + at));
-    if (p.bias_1) sum += __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p.bias_1 + at));
-    *reinterpret_cast<__nv_bfloat16*>(p.out + at) = __float2bfloat16_rn(sum);
+// The sum warps' 256 channels from `col` of all tokens, four channels a thread and four tokens at a time; sum(t, c): the sums of
+// token t's four channels from c.
+template <typename Sum>
+__device__ __forceinline__ void put_outputs(const LayerParams& p, int col, Sum sum) {
+    const int thread = threadIdx.x - 4 * kWarpSize, c = thread % 64 * 4;
+    if (col + c >= p.hidden) return;
+#pragma unroll 1
+    for (int t = thread / 64; t < p.tokens; t += 4) {
+        const int64_t at = 2 * (static_cast<int64_t>(t) * p.hidden + col + c);
+        const uint2 b0 = p.bias_0 ? *reinterpret_cast<const uint2*>(p.bias_0 + at) : make_uint2(0, 0);
+        const uint2 b1 = p.bias_1 ? *reinterpret_cast<const uint2*>(p.bias_1 + at) : make_uint2(0, 0);
+        float4 s = sum(t, c);
+        s.x += bf16_lo(b0.x) + bf16_lo(b1.x), s.y += bf16_hi(b0.x) + bf16_hi(b1.x);
+        s.z += bf16_lo(b0.y) + bf16_lo(b1.y), s.w += bf16_hi(b0.y) + bf16_hi(b1.y);
+        *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+    }
 }
 
-// Eight warps of the second kernel: accumulators to the tokens' weighted sums.  A warp has 32 channels of the tile and the
-// tokens of one parity, so that a sum belongs to one thread whatever the expert.
+// The tokens that a CTA's part of some channels can have something for: those of its experts there, all where these are many.
+__device__ __forceinline__ uint64_t part_tokens(const Work<true>& w, int cta, int64_t tile0, int64_t each_tile) {
+    const int64_t first = max(w.shares.begin(cta), tile0) - tile0, last = min(w.shares.begin(cta + 1), tile0 + each_tile) - 1 - tile0;
+    const int from = static_cast<int>(first / w.steps), to = static_cast<int>(last / w.steps);
+    if (to - from >= 32) return ~0ull;
+    uint64_t m = 0;
+    for (int i = from; i <= to; ++i) m |= w.t.tokens[w.t.hit[i]];
+    return m;
+}
+
+// Eight warps of the second kernel: accumulators to the tokens' weighted sums.  A thread has one of the tile's channels, so
+// that a sum belongs to one thread whatever the expert.
 template <bool kFp8, int kTokens>
 __device__ __forceinline__ void down_sums(const LayerRoles<true>& x, int warp) {
-    constexpr int kPer = kTokens / 2;
+    constexpr int kChannels = kOps * kTile;
     const LayerParams& p = x.p;
     const Work<true>& w = x.work;
-    const int quarter = warp & 3, half = (warp - 4) >> 2;
-    const int row = quarter * 32 + lane_id();
+    const int quarter = warp & 3, op = (warp - 4) >> 2;
+    const int mine = op * kTile + quarter * 32 + lane_id();
     if (w.hits == 0) {  // no token has an expert
         for (int j = blockIdx.x; j < w.across; j += gridDim.x)
-            for (int t = half; t < p.tokens; t += 2)
-                if (j * kTile + row < p.hidden) put_output(p, t, j * kTile + row, 0.0f);
+            put_outputs(p, j * kChannels, [](int, int) { return make_float4(0.0f, 0.0f, 0.0f, 0.0f); });
         return;
     }
-    float* const sums = x.sums + row;
-    for (int t = half; t < p.tokens; t += 2) sums[t * kTile] = 0.0f;
-    const int64_t each_tile = static_cast<int64_t>(w.hits) * w.steps;  // units of 128 channels
+    float* const sums = x.sums + mine;
+    for (int t = 0; t < p.tokens; ++t) sums[t * kChannels] = 0.0f;
+    const int64_t each_tile = static_cast<int64_t>(w.hits) * w.steps;  // units of kChannels
     int buf = 0;
     uint32_t acc_phase = 0;
+    int turn = 0;
     bool ok = true;
-    for (int64_t unit = w.first; unit < w.last;) {
-        const Unit u = w.at(unit);
-        const int steps = static_cast<int>(min(static_cast<int64_t>(w.steps - u.step), w.last - unit));
-        const uint64_t parity = u.tokens & (half ? 0xaaaaaaaaaaaaaaaaull : 0x5555555555555555ull);
-        const int mine = count_bits(parity);
-        uint8_t tokens[kPer], cols[kPer];
-        {
-            uint64_t m = parity;
-#pragma unroll
-            for (int q = 0; q < kPer; ++q) {
-                const int t = m ? lowest_bit(m) : 0;
-                tokens[q] = static_cast<uint8_t>(t);
-                cols[q] = static_cast<uint8_t>(count_bits(u.tokens & ((1ull << t) - 1)));
-                m &= m - 1;
-            }
-        }
-        float v[1][kPer];
-        read_sums<kFp8, 1, kPer, true>(x, unit, steps, mine, static_cast<uint32_t>(quarter * 32) << 16, u, buf, acc_phase, ok,
-                                       [&](int q) { return static_cast<int>(cols[q]); }, v);
+    int64_t tile0 = w.first / each_tile * each_tile;  // first unit of the channels that are being summed
+    for (Unit<true> u(w, w.first); u.more();) {
+        const int steps = static_cast<int>(min(static_cast<int64_t>(w.steps - u.step), w.last - u.at));
+        float v[kTokens];
+        read_sums<kFp8, kTokens, true>(x, steps, quarter, op, u, buf, acc_phase, ok, v);
         const float* weight = x.t.weight + x.t.begin[u.expert];
+        uint64_t left = u.tokens;
 #pragma unroll
-        for (int q = 0; q < kPer; ++q) {
-            if (q >= mine) break;
-            sums[tokens[q] * kTile] += weight[cols[q]] * v[0][q];
+        for (int q = 0; q < kTokens; ++q) {
+            if (left == 0) break;
+            sums[lowest_bit(left) * kChannels] += weight[q] * v[q];
+            left &= left - 1;
         }
-        unit += steps;
-        const int64_t tile0 = (unit - 1) / each_tile * each_tile;
-        if (unit < w.last && unit < tile0 + each_tile) continue;  // more of these channels
-        bool finish = true, summed = false;
-        const bool whole = tile0 >= w.first && unit == tile0 + each_tile;
-        int a = 0, b = 0;
-        const int64_t each = static_cast<int64_t>(p.tokens) * kTile;
-        if (!whole) {
-            a = w.shares.owner(tile0), b = w.shares.owner(tile0 + each_tile - 1);
-            float* own = p.partial + (2 * static_cast<int64_t>(blockIdx.x) + (tile0 >= w.first)) * each + row;
-            for (int t = half; t < p.tokens; t += 2) own[t * kTile] = sums[t * kTile];
-            finish = last_to_arrive(x, a, b - a + 1);
-            summed = finish;
-        }
-        if (finish && u.col + row < p.hidden) {
-            for (int t = half; t < p.tokens; t += 2) {
-                float s = summed ? 0.0f : sums[t * kTile];
-                if (summed) {
-#pragma unroll 4
-                    for (int c = a; c <= b; ++c) s += __ldcg(p.partial + (2 * static_cast<int64_t>(c) + (c == a)) * each + row + t * kTile);
+        const int col = u.col;
+        u.move(steps);
+        if (u.more() && u.at < tile0 + each_tile) continue;  // more of these channels
+        const bool whole = tile0 >= w.first && u.at == tile0 + each_tile;
+        if (whole) {
+            sum_warps_barrier();
+            put_outputs(p, col, [&](int t, int c) { return *reinterpret_cast<const float4*>(x.sums + t * kChannels + c); });
+            sum_warps_barrier();
+        } else {
+            const int a = w.shares.owner(tile0), b = w.shares.owner(tile0 + each_tile - 1);
+            const int64_t each = static_cast<int64_t>(p.tokens) * kChannels;
+            float* own = p.partial + (2 * static_cast<int64_t>(blockIdx.x) + (tile0 >= w.first)) * each + mine;
+            const uint64_t has = part_tokens(w, blockIdx.x, tile0, each_tile);
+            for (int t = 0; t < p.tokens; ++t)
+                if (has >> t & 1) own[t * kChannels] = sums[t * kChannels];
+            if (last_to_arrive(x, a, b - a + 1, turn)) {  // the same for all
+                // which parts a token is in, a warp 32 parts at a time
+                const int words = part_words(p.ctas);
+                for (int i = warp - 4; i <= (b - a) / kWarpSize; i += kSumWarps) {
+                    const int c = a + i * kWarpSize + lane_id();
+                    const uint64_t m = c <= b ? part_tokens(w, c, tile0, each_tile) : 0;
+                    for (int t = 0; t < p.tokens; ++t) {
+                        const uint32_t in = __ballot_sync(kFullMask, m >> t & 1);
+                        if (lane_id() == 0) x.parts[t * words + i] = in;
+                    }
                 }
-                put_output(p, t, u.col + row, s);
+                sum_warps_barrier();
+                put_outputs(p, col, [&](int t, int c) {
+                    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    for (int word = 0; word <= (b - a) / kWarpSize; ++word) {
+                        uint32_t in = x.parts[t * words + word];
+                        const int c0 = a + word * kWarpSize;
+                        while (in) {  // four parts on their way
+                            float4 v[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int cta = c0 + __ffs(in) - 1;
+                                v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                                if (in) v[k] = __ldcg(reinterpret_cast<const float4*>(p.partial + (2 * static_cast<int64_t>(cta) + (cta == a)) * each + t * kChannels + c));
+                                in &= in - 1;
+                            }
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) s.x += v[k].x, s.y += v[k].y, s.z += v[k].z, s.w += v[k].w;
+                        }
+                    }
+                    return s;
+                });
             }
         }
-        for (int t = half; t < p.tokens; t += 2) sums[t * kTile] = 0.0f;
+        for (int t = 0; t < p.tokens; ++t) sums[t * kChannels] = 0.0f;
+        tile0 += each_tile;
     }
 }
 
 // The dynamic shared memory of a kernel, after alignment to 1024: stages, then the rest.
 struct Layout {
-    uint32_t tokens, begin, hit, weight, scales, sums, bytes;
+    uint32_t tokens, parts, begin, hit, weight, scales, sums, bytes;
 };
 
 __host__ __device__ inline Layout layer_layout(const LayerParams& p, bool fp8, bool down) {
     Layout l;
     uint32_t at = p.stages * p.stage_bytes;
+    l.scales = at, at += fp8 ? 4u * kScaleRing * (p.tokens <= kSmallTokens ? kSmallTokens : kMaxTokens) : 0u;
+    l.sums = at, at += 4u * kTile * kOps * (down ? p.tokens : kSwap);
     l.tokens = at, at += 8u * p.experts;
+    l.parts = at, at += down ? 4u * part_words(p.ctas) * p.tokens : 0u;
     l.begin = at, at += 4u * p.experts;
-    l.sums = at, at += down ? 4u * p.tokens * kTile : 0u;
+
     l.weight = at, at += down ? 4u * p.tokens * p.topk : 0u;
-    l.scales = at, at += fp8 ? 4u * kScaleRing * kMaxTokens : 0u;
     const int most = p.tokens * p.topk < p.experts ? p.tokens * p.topk : p.experts;
     l.hit = at, at += 2u * most;
     l.bytes = at;
@@ -678,10 +783,10 @@ __global__ void __launch_bounds__(layer_threads(kFp8), kTokens <= kSmallTokens ?
     const int warp = threadIdx.x / kWarpSize;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
-            mbar_init(&ctl.full[i], kFp8 ? 1 + kSplitWarps : 1);
+            mbar_init(&ctl.full[i], kFp8 ? 2 : 1);
             mbar_init(&ctl.empty[i], 1);
         }
-        for (int i = 0; i < kBuffers; ++i) {
+        for (int i = 0; i < buffers(kTokens); ++i) {
             mbar_init(&ctl.acc_full[i], 2);
             mbar_init(&ctl.acc_empty[i], kSumWarps);
         }
@@ -702,18 +807,20 @@ __global__ void __launch_bounds__(layer_threads(kFp8), kTokens <= kSmallTokens ?
     tc_fence_after();
 
     const int steps = ((kDown ? p.width : p.hidden) * (kFp8 ? 1 : 2) + static_cast<int>(kRow) - 1) / static_cast<int>(kRow);
-    const int across = ((kDown ? p.hidden : p.width) + kTile - 1) / kTile;
+    const int across = kDown ? (p.hidden + kOps * kTile - 1) / (kOps * kTile) : (p.width + kTile - 1) / kTile;
     const int64_t units = static_cast<int64_t>(ctl.hits) * across * steps;
-    const Shares shares = {units, static_cast<int>(min(units, static_cast<int64_t>(gridDim.x)))};
+    // a CTA has kLeastUnits at least: a part costs its sum more than their loads
+    const Shares shares = {units, static_cast<int>(min((units + kLeastUnits - 1) / kLeastUnits, static_cast<int64_t>(gridDim.x)))};
     const bool works = static_cast<int>(blockIdx.x) < shares.ctas;
     const Work<kDown> work = {t, shares, works ? shares.begin(blockIdx.x) : 0, works ? shares.begin(blockIdx.x + 1) : 0,
                               ctl.hits, across, steps};
     const LayerRoles<kDown> x = {maps, p, t, work, ctl, {&ctl.abort_flag, p.status, p.wait_limit_ns}, smem,
-                                 reinterpret_cast<float*>(smem + l.scales), reinterpret_cast<float*>(smem + l.sums)};
+                                 reinterpret_cast<float*>(smem + l.scales), reinterpret_cast<float*>(smem + l.sums),
+                                 reinterpret_cast<uint32_t*>(smem + l.parts)};
     if (warp == 0) {
         if (elect_one()) layer_loads<kFp8, kDown>(x);
     } else if (warp == 1) {
-        if (elect_one()) layer_products<kFp8, kDown>(x);
+        if (elect_one()) layer_products<kFp8, kTokens, kDown>(x);
     } else if (warp >= 4 && warp < 4 + kSumWarps) {
         if constexpr (kDown) down_sums<kFp8, kTokens>(x, warp);
         else up_sums<kFp8, kTokens>(x, warp);
@@ -731,8 +838,9 @@ __global__ void __launch_bounds__(layer_threads(kFp8), kTokens <= kSmallTokens ?
 // Host side
 // ---------------------------------------------------------------------------
 
-constexpr int64_t kSmallSmem[2] = {119 * 1024, 104 * 1024};  // up, down: together on an SM
-constexpr int64_t kLargeSmem = 224 * 1024;
+constexpr int kMostSmem = 226 * 1024;   // dynamic, of one kernel
+constexpr int kBothSmem = 224 * 1024;   // of the two together, for an SM that holds a CTA of each
+constexpr int kUpStages = 3;            // of the first kernel, then; the second takes what is left
 
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 
@@ -745,8 +853,8 @@ Workspace workspace_of(const ep_handle* h, int64_t tokens, int32_t width) {
     const int64_t ctas = h->plan.num_sms;
     Workspace w;
     w.up_partial = align256(rows * width * 2);
-    w.down_partial = w.up_partial + align256(ctas * 2 * tokens * 2 * kTile * 4);
-    w.bytes = w.down_partial + align256(ctas * 2 * tokens * kTile * 4);
+    w.down_partial = w.up_partial + align256(ctas * 2 * tokens * kOps * kTile * 4);
+    w.bytes = w.down_partial + align256(ctas * 2 * tokens * kOps * kTile * 4);
     return w;
 }
 
@@ -759,7 +867,7 @@ cudaError_t plan_kernels(int smem) {
 }
 
 cudaError_t plan_layer() {
-    constexpr int kSmem = 226 * 1024;
+    constexpr int kSmem = kMostSmem;
     cudaError_t err = plan_kernels<false, kSmallTokens>(kSmem);
     if (err == cudaSuccess) err = plan_kernels<false, kMaxTokens>(kSmem);
     if (err == cudaSuccess) err = plan_kernels<true, kSmallTokens>(kSmem);
@@ -767,26 +875,34 @@ cudaError_t plan_layer() {
     return err;
 }
 
-// Stages and tensor memory of a kernel.
-ep_status size_kernel(LayerParams* p, bool fp8, bool down, uint32_t* smem) {
-    p->cols = (p->tokens + kColStep - 1) / kColStep * kColStep;
-    p->stage_bytes = (down ? kTileBytes : 2 * kTileBytes) + (fp8 ? 2 : 1) * p->cols * kRow;
+// Tensor memory and stages of a kernel that may have `room` bytes of shared memory and `most` stages; the bytes it takes.
+int size_kernel(LayerParams* p, bool fp8, bool down, int room, int most) {
+    p->cols = (p->tokens + col_step(fp8) - 1) / col_step(fp8) * col_step(fp8);
+    p->op_cols = (fp8 ? 2 : 1) * p->cols;
+    p->stage_bytes = kABytes + p->op_cols * kRow;
     p->tmem_columns = 32;
-    while (p->tmem_columns < static_cast<uint32_t>(kBuffers * (down ? 1 : 2) * p->cols)) p->tmem_columns *= 2;
-    const int64_t room = p->tokens <= kSmallTokens ? kSmallSmem[down] : kLargeSmem;
+    while (p->tmem_columns < buffers(p->tokens) * kOps * p->op_cols) p->tmem_columns *= 2;
     p->stages = 0;
-    const int64_t rest = layer_layout(*p, fp8, down).bytes + 1024;
-    // with very many experts the table takes more: then the kernels no longer fit an SM together
-    int64_t stages = (room - rest) / p->stage_bytes;
-    if (stages < 2) stages = 2;
-    p->stages = static_cast<int32_t>(stages < kMaxStages ? stages : kMaxStages);
-    *smem = layer_layout(*p, fp8, down).bytes + 1024;
-    if (*smem > 226 * 1024) return fail(EP_ERR_UNSUPPORTED, "the layer's tables need too much shared memory");
+    const int stages = (room - static_cast<int>(layer_layout(*p, fp8, down).bytes) - 1024) / static_cast<int>(p->stage_bytes);
+    p->stages = stages < most ? stages : most;
+    return static_cast<int>(layer_layout(*p, fp8, down).bytes) + 1024;
+}
+
+// Both kernels' sizes: together on an SM if they fit with two stages each, else each for itself.
+ep_status size_kernels(LayerParams* up, LayerParams* down, bool fp8, int* up_smem, int* down_smem) {
+    if (up->tokens <= kSmallTokens) {
+        *up_smem = size_kernel(up, fp8, false, kMostSmem, kUpStages);
+        *down_smem = size_kernel(down, fp8, true, kBothSmem - *up_smem, kMaxStages);
+        if (up->stages >= 2 && down->stages >= 2) return EP_OK;
+    }
+    *up_smem = size_kernel(up, fp8, false, kMostSmem, kMaxStages);
+    *down_smem = size_kernel(down, fp8, true, kMostSmem, kMaxStages);
+    if (up->stages < 2 || down->stages < 2) return fail(EP_ERR_UNSUPPORTED, "the layer's tables need too much shared memory");
     return EP_OK;
 }
 
 template <bool kFp8, int kTokens, bool kDown>
-cudaError_t start(const ep_handle* h, const LayerMaps& m, const LayerParams& p, uint32_t smem, cudaStream_t stream) {
+cudaError_t start(const ep_handle* h, const LayerMaps& m, const LayerParams& p, int smem, cudaStream_t stream) {
     return launch_kernel(layer_kernel<kFp8, kTokens, kDown>, dim3(h->plan.num_sms), dim3(layer_threads(kFp8)), smem, stream, 1, m, p);
 }
 
@@ -809,9 +925,8 @@ ep_status run(ep_handle* h, LayerParams p, const void* x, const void* w_up, cons
     down.partial = reinterpret_cast<float*>(workspace + ws.down_partial);
     up.tickets = h->layer_tickets;
     down.tickets = h->layer_tickets + h->plan.num_sms;
-    uint32_t up_smem = 0, down_smem = 0;
-    ep_status st = size_kernel(&up, kFp8, false, &up_smem);
-    if (st == EP_OK) st = size_kernel(&down, kFp8, true, &down_smem);
+    int up_smem = 0, down_smem = 0;
+    ep_status st = size_kernels(&up, &down, kFp8, &up_smem, &down_smem);
     LayerMaps mu, md;
     if (st == EP_OK) st = encode(&mu.w, {w_up, element, 3, {H, 2 * I, E, 1}, {H * esize, H * esize * 2 * I, 0}, {inner, kTile, 1, 1}});
     if (st == EP_OK) st = encode(&md.w, {w_down, element, 3, {I, H, E, 1}, {I * esize, I * esize * H, 0}, {inner, kTile, 1, 1}});
@@ -819,8 +934,8 @@ ep_status run(ep_handle* h, LayerParams p, const void* x, const void* w_up, cons
         mu.x = mu.w, md.x = md.w;  // not used
     } else {
         const uint64_t act_rows = static_cast<uint64_t>(p.tokens) * (p.topk < p.experts ? p.topk : p.experts);
-        if (st == EP_OK) st = encode(&mu.x, {x, Element::kBf16, 2, {H, static_cast<uint64_t>(p.tokens), 1, 1}, {2 * H, 0, 0}, {64, kColStep, 1, 1}});
-        if (st == EP_OK) st = encode(&md.x, {workspace, Element::kBf16, 2, {I, act_rows, 1, 1}, {2 * I, 0, 0}, {64, kColStep, 1, 1}});
+        if (st == EP_OK) st = encode(&mu.x, {x, Element::kBf16, 2, {H, static_cast<uint64_t>(p.tokens), 1, 1}, {2 * H, 0, 0}, {64, static_cast<uint32_t>(col_step(false)), 1, 1}});
+        if (st == EP_OK) st = encode(&md.x, {workspace, Element::kBf16, 2, {I, act_rows, 1, 1}, {2 * I, 0, 0}, {64, static_cast<uint32_t>(col_step(false)), 1, 1}});
     }
     if (st != EP_OK) return st;
     const bool small = p.tokens <= kSmallTokens;
@@ -865,7 +980,7 @@ ep_status ep_moe_layer(ep_handle* h, int32_t num_tokens, int32_t width, const vo
     EP_CHECK_ARG(x && w_up && w_down && out && aligned16(x) && aligned16(w_up) && aligned16(w_down) && aligned16(out),
                  "x, w_up, w_down and out must be 16-byte aligned device pointers");
     EP_CHECK_ARG(topk_idx && topk_weights && aligned8(topk_idx) && aligned4(topk_weights), "topk_idx or topk_weights is NULL or misaligned");
-    EP_CHECK_ARG((reinterpret_cast<uintptr_t>(bias_0) & 1u) == 0 && (reinterpret_cast<uintptr_t>(bias_1) & 1u) == 0, "misaligned bias");
+    EP_CHECK_ARG(aligned16(bias_0) && aligned16(bias_1), "bias_0 and bias_1 must be 16-byte aligned");
     const int64_t need = workspace_of(h, tokens, width).bytes;
     EP_CHECK_ARG(workspace && aligned16(workspace) && workspace_bytes >= need,
                  "the layer needs a 16-byte aligned workspace of %lld bytes (ep_moe_layer_workspace), got %lld",
@@ -886,6 +1001,7 @@ ep_status ep_moe_layer(ep_handle* h, int32_t num_tokens, int32_t width, const vo
     p.local_experts = c.num_experts / c.num_ranks;
     p.hidden = c.hidden;
     p.width = width;
+    p.ctas = h->plan.num_sms;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     return fp8 ? run<true>(h, p, x, w_up, w_up_scales, w_down, w_down_scales, ws, stream)
                : run<false>(h, p, x, w_up, nullptr, w_down, nullptr, ws, stream);
