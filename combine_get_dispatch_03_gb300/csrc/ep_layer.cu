@@ -41,12 +41,14 @@ constexpr int kMaxStages = 8;
 constexpr int kLeastUnits = 4;
 constexpr int kSumWarps = 8;                // warps 4 to 11: accumulators to sums and out
 constexpr int kScaleRing = 16;              // blocks whose token scales are kept: more than stages and accumulators
-constexpr int kSmallTokens = 16;            // up to which both kernels fit an SM
+constexpr int kSmallTokens = 8;             // up to which both kernels fit an SM
 constexpr int buffers(int tokens) { return tokens <= kSmallTokens ? 4 : 2; }  // accumulators
-constexpr int batch_pairs(int tokens) { return tokens <= kSmallTokens ? 4 : 8; }  // of tokens that a splitting warp has in hand, and as many on their way
-constexpr int kSplitWarps = 4;              // warps 12 to 15, FP8: the tokens' values in two e4m3 parts
+constexpr int kBatchPairs = 4;              // of tokens that a splitting warp has in hand, and as many on their way
+// Warps 12 on, FP8: the tokens' values in two e4m3 parts, so many warps for a unit.
+constexpr int split_group(int tokens) { return tokens <= kSmallTokens ? 1 : 2; }
+constexpr int split_warps(int tokens) { return 4 * split_group(tokens); }
 static_assert(kScaleRing > kMaxStages + 4 + 1, "a block's scales outlive it");
-constexpr int layer_threads(bool fp8) { return (4 + kSumWarps + (fp8 ? kSplitWarps : 0)) * kWarpSize; }
+constexpr int layer_threads(bool fp8, int tokens) { return (4 + kSumWarps + (fp8 ? split_warps(tokens) : 0)) * kWarpSize; }
 
 struct LayerParams {
     const int64_t* topk_idx;
@@ -65,7 +67,7 @@ struct LayerParams {
     int32_t tokens, tokens_per_rank, topk, experts, local_experts, hidden, width;
     int32_t cols;              // tokens, rounded up to col_step()
     uint32_t op_cols;          // columns of tensor memory for a product: cols, FP8 twice that
-    int32_t stages, ctas;
+    int32_t stages, ctas, small;  // small: the variant of up to kSmallTokens
     uint32_t stage_bytes, tmem_columns;
 };
 
@@ -363,38 +365,40 @@ __device__ __forceinline__ void split_e4m3(const float (&f)[8], float mult, uint
     uint32_t h[2] = {0, 0}, l[2] = {0, 0};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float a = f[2 * i] * mult, b = f[2 * i + 1] * mult;
-        const __nv_fp8x2_storage_t code = e4m3x2(a, b);
-        const float2 back = __half22float2(static_cast<__half2>(__nv_cvt_fp8x2_to_halfraw2(code, __NV_E4M3)));
+        const __half2 v = __floats2half2_rn(f[2 * i] * mult, f[2 * i + 1] * mult);  // eight bits of eleven, to 2^-25
+        const __nv_fp8x2_storage_t code = __nv_cvt_halfraw2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+        const __half2 rest = __hsub2(v, static_cast<__half2>(__nv_cvt_fp8x2_to_halfraw2(code, __NV_E4M3)));  // exact
         h[i / 2] |= static_cast<uint32_t>(code) << (i % 2 * 16);
-        l[i / 2] |= static_cast<uint32_t>(e4m3x2(a - back.x, b - back.y)) << (i % 2 * 16);
+        l[i / 2] |= static_cast<uint32_t>(__nv_cvt_halfraw2_to_fp8x2(rest, __NV_SATFINITE, __NV_E4M3)) << (i % 2 * 16);
     }
     *high = make_uint2(h[0], h[1]);
     *low = make_uint2(l[0], l[1]);
 }
 
 // FP8: the tokens' blocks of a unit, split, into the place and order in which a tensor-map load would put them: a row
-// for each token's first part, then one for each second.  The warps take units in turn, so that each has several units' time
+// for each token's first part, then one for each second.  Groups of warps take units in turn, so that each has several units' time
 // for a round trip to memory; half a warp has a token's 128 channels, and a batch's values are loaded before the one before it
-// is worked on.  No more warps than stages: one that waits for a stage's use has filled a stage after the use before the last,
+// is worked on.  No more groups than stages: one that waits for a stage's use has filled a stage after the use before the last,
 // so that the barrier's parity tells the two uses apart.
 template <int kTokens, bool kDown>
 __device__ __forceinline__ void layer_splits(const LayerRoles<kDown>& x, int warp) {
-    constexpr int kBatchPairs = batch_pairs(kTokens);
+    constexpr int kGroup = split_group(kTokens);
     constexpr int kBatch = 2 * kBatchPairs;  // tokens
     const LayerParams& p = x.p;
     LayerControl& ctl = x.ctl;
     const Work<kDown>& w = x.work;
     const int64_t row_bytes = 2 * static_cast<int64_t>(kDown ? p.width : p.hidden);
     const int half = lane_id() >> 4, piece = lane_id() & 15;
-    const int warps = min(kSplitWarps, p.stages);
-    if (warp >= warps) return;
+    const int groups = min(split_warps(kTokens) / kGroup, p.stages), group = warp / kGroup;
+    const int begin = warp % kGroup * kBatch;  // of a unit's tokens
+    if (group >= groups) return;
     // what is loaded next: tokens [first, count) of a unit
-    Unit<kDown> next(w, w.first + warp);
+    Unit<kDown> next(w, w.first + group);
     int next_first = 0, next_count = 0;
     const uint8_t* next_row = nullptr;
     auto enter = [&] {
-        next_first = next_count = 0;
+        next_first = begin;
+        next_count = 0;
         if (!next.more()) return;
         next_count = unit_tokens(p, next);
         next_row = p.tokens_x + (kDown ? x.t.begin[next.expert] : 0) * row_bytes + next.step * 256 + half * row_bytes + piece * 16;
@@ -409,22 +413,23 @@ __device__ __forceinline__ void layer_splits(const LayerRoles<kDown>& x, int war
         }
     };
     auto advance = [&] {
-        next_first += kBatch;
-        if (next_first >= next_count) next.move(warps), enter();
+        next_first += kBatch * kGroup;
+        if (next_first >= next_count) next.move(groups), enter();
         fetch();
     };
     if (kDown) asm volatile("griddepcontrol.wait;" ::: "memory");
     enter();
     fetch();
-    int stage = warp;
+    int stage = group;
     uint32_t phase = 0;
-    for (int64_t unit = w.first + warp; unit < w.last; unit += warps) {
+    for (int64_t unit = w.first + group; unit < w.last; unit += groups) {
         const int count = next_count;  // at least one
         const uint32_t low_part = round_cols<true>(count) * kRow;
         if (!warp_wait(&ctl.empty[stage], phase ^ 1, x.waits)) break;
         uint8_t* b = x.stages + stage * p.stage_bytes + kABytes;
         float* scales = x.scales + static_cast<int>((unit - w.first) % kScaleRing) * kTokens;
-        for (int first = 0; first < count; first += kBatch) {
+        if (begin >= count) advance();  // none for this warp
+        for (int first = begin; first < count; first += kBatch * kGroup) {
             int4 value[kBatchPairs];
 #pragma unroll
             for (int i = 0; i < kBatchPairs; ++i) value[i] = ahead[i];
@@ -462,7 +467,7 @@ __device__ __forceinline__ void layer_splits(const LayerRoles<kDown>& x, int war
         fence_async_smem();
         __syncwarp();
         if (lane_id() == 0) bar_arrive<1>(smem_u32(&ctl.full[stage]));
-        stage += warps;  // at most once around
+        stage += groups;  // at most once around
         if (stage >= p.stages) stage -= p.stages, phase ^= 1;
     }
 }
@@ -757,7 +762,7 @@ struct Layout {
 __host__ __device__ inline Layout layer_layout(const LayerParams& p, bool fp8, bool down) {
     Layout l;
     uint32_t at = p.stages * p.stage_bytes;
-    l.scales = at, at += fp8 ? 4u * kScaleRing * (p.tokens <= kSmallTokens ? kSmallTokens : kMaxTokens) : 0u;
+    l.scales = at, at += fp8 ? 4u * kScaleRing * (p.small ? kSmallTokens : kMaxTokens) : 0u;
     l.sums = at, at += 4u * kTile * kOps * (down ? p.tokens : kSwap);
     l.tokens = at, at += 8u * p.experts;
     l.parts = at, at += down ? 4u * part_words(p.ctas) * p.tokens : 0u;
@@ -771,9 +776,9 @@ __host__ __device__ inline Layout layer_layout(const LayerParams& p, bool fp8, b
 }
 
 template <bool kFp8, int kTokens, bool kDown>
-__global__ void __launch_bounds__(layer_threads(kFp8), kTokens <= kSmallTokens ? 2 : 1)
+__global__ void __launch_bounds__(layer_threads(kFp8, kTokens), kTokens <= kSmallTokens ? 2 : 1)
     layer_kernel(const __grid_constant__ LayerMaps maps, const LayerParams p) {
-    constexpr int kThreads = layer_threads(kFp8);
+    constexpr int kThreads = layer_threads(kFp8, kTokens);
     extern __shared__ uint8_t raw[];
     __shared__ LayerControl ctl;
     uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -783,7 +788,7 @@ __global__ void __launch_bounds__(layer_threads(kFp8), kTokens <= kSmallTokens ?
     const int warp = threadIdx.x / kWarpSize;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
-            mbar_init(&ctl.full[i], kFp8 ? 2 : 1);
+            mbar_init(&ctl.full[i], kFp8 ? 1 + split_group(kTokens) : 1);
             mbar_init(&ctl.empty[i], 1);
         }
         for (int i = 0; i < buffers(kTokens); ++i) {
@@ -817,14 +822,24 @@ __global__ void __launch_bounds__(layer_threads(kFp8), kTokens <= kSmallTokens ?
     const LayerRoles<kDown> x = {maps, p, t, work, ctl, {&ctl.abort_flag, p.status, p.wait_limit_ns}, smem,
                                  reinterpret_cast<float*>(smem + l.scales), reinterpret_cast<float*>(smem + l.sums),
                                  reinterpret_cast<uint32_t*>(smem + l.parts)};
-    if (warp == 0) {
-        if (elect_one()) layer_loads<kFp8, kDown>(x);
-    } else if (warp == 1) {
-        if (elect_one()) layer_products<kFp8, kTokens, kDown>(x);
-    } else if (warp >= 4 && warp < 4 + kSumWarps) {
+    // FP8: registers move from the loads' and products' warps to the others: of 640 threads of 96 (61440) 128 * 40 + 256 * 136 +
+    // 256 * 80, of 512 of 64 (32768, so that two CTAs fit an SM) 128 * 40 + 256 * 72 + 128 * 72.
+    constexpr bool kMany = kTokens > kSmallTokens;
+    if (warp < 4) {
+        if constexpr (kFp8) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == 0) {
+            if (elect_one()) layer_loads<kFp8, kDown>(x);
+        } else if (warp == 1) {
+            if (elect_one()) layer_products<kFp8, kTokens, kDown>(x);
+        }
+    } else if (warp < 4 + kSumWarps) {
+        if constexpr (kFp8 && kMany) asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
+        else if constexpr (kFp8) asm volatile("setmaxnreg.inc.sync.aligned.u32 72;");
         if constexpr (kDown) down_sums<kFp8, kTokens>(x, warp);
         else up_sums<kFp8, kTokens>(x, warp);
-    } else if (kFp8 && warp >= 4 + kSumWarps) {
+    } else if constexpr (kFp8) {
+        if constexpr (kMany) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 72;");
         layer_splits<kTokens, kDown>(x, warp - 4 - kSumWarps);
     }
     __syncwarp();
@@ -881,16 +896,26 @@ int size_kernel(LayerParams* p, bool fp8, bool down, int room, int most) {
     p->op_cols = (fp8 ? 2 : 1) * p->cols;
     p->stage_bytes = kABytes + p->op_cols * kRow;
     p->tmem_columns = 32;
-    while (p->tmem_columns < buffers(p->tokens) * kOps * p->op_cols) p->tmem_columns *= 2;
+    while (p->tmem_columns < buffers(p->small ? kSmallTokens : kMaxTokens) * kOps * p->op_cols) p->tmem_columns *= 2;
     p->stages = 0;
     const int stages = (room - static_cast<int>(layer_layout(*p, fp8, down).bytes) - 1024) / static_cast<int>(p->stage_bytes);
     p->stages = stages < most ? stages : most;
     return static_cast<int>(layer_layout(*p, fp8, down).bytes) + 1024;
 }
 
+// Whether the two kernels shall fit an SM together.  Alone each has more stages, and the second starts when the first ends:
+// one bf16 token through 8 of 32 experts of 7168 x 2048 121 us together and 119 alone, 8 tokens through 28 of them 315 and 308, but 8
+// experts of 1024 x 512 18.3 and 20.9, 4 tokens of 2048 x 1024 51 and 59; FP8 81 and 85, 184 and 185, 20.8 and 21.6, 38 and 44.
+bool both_on_an_sm(const LayerParams& p, bool fp8) {
+    if (p.tokens > kSmallTokens) return false;
+    const int64_t hits = p.tokens * p.topk < p.experts ? p.tokens * p.topk : p.experts;
+    return fp8 || 6 * hits * p.hidden * p.width < (INT64_C(1) << 29);
+}
+
 // Both kernels' sizes: together on an SM if they fit with two stages each, else each for itself.
-ep_status size_kernels(LayerParams* up, LayerParams* down, bool fp8, int* up_smem, int* down_smem) {
-    if (up->tokens <= kSmallTokens) {
+ep_status size_kernels(LayerParams* up, LayerParams* down, bool fp8, bool small, int* up_smem, int* down_smem) {
+    up->small = down->small = small;
+    if (small) {
         *up_smem = size_kernel(up, fp8, false, kMostSmem, kUpStages);
         *down_smem = size_kernel(down, fp8, true, kBothSmem - *up_smem, kMaxStages);
         if (up->stages >= 2 && down->stages >= 2) return EP_OK;
@@ -903,7 +928,7 @@ ep_status size_kernels(LayerParams* up, LayerParams* down, bool fp8, int* up_sme
 
 template <bool kFp8, int kTokens, bool kDown>
 cudaError_t start(const ep_handle* h, const LayerMaps& m, const LayerParams& p, int smem, cudaStream_t stream) {
-    return launch_kernel(layer_kernel<kFp8, kTokens, kDown>, dim3(h->plan.num_sms), dim3(layer_threads(kFp8)), smem, stream, 1, m, p);
+    return launch_kernel(layer_kernel<kFp8, kTokens, kDown>, dim3(h->plan.num_sms), dim3(layer_threads(kFp8, kTokens)), smem, stream, 1, m, p);
 }
 
 template <bool kFp8>
@@ -926,7 +951,8 @@ ep_status run(ep_handle* h, LayerParams p, const void* x, const void* w_up, cons
     up.tickets = h->layer_tickets;
     down.tickets = h->layer_tickets + h->plan.num_sms;
     int up_smem = 0, down_smem = 0;
-    ep_status st = size_kernels(&up, &down, kFp8, &up_smem, &down_smem);
+    const bool small = both_on_an_sm(p, kFp8);
+    ep_status st = size_kernels(&up, &down, kFp8, small, &up_smem, &down_smem);
     LayerMaps mu, md;
     if (st == EP_OK) st = encode(&mu.w, {w_up, element, 3, {H, 2 * I, E, 1}, {H * esize, H * esize * 2 * I, 0}, {inner, kTile, 1, 1}});
     if (st == EP_OK) st = encode(&md.w, {w_down, element, 3, {I, H, E, 1}, {I * esize, I * esize * H, 0}, {inner, kTile, 1, 1}});
@@ -938,7 +964,6 @@ ep_status run(ep_handle* h, LayerParams p, const void* x, const void* w_up, cons
         if (st == EP_OK) st = encode(&md.x, {workspace, Element::kBf16, 2, {I, act_rows, 1, 1}, {2 * I, 0, 0}, {64, static_cast<uint32_t>(col_step(false)), 1, 1}});
     }
     if (st != EP_OK) return st;
-    const bool small = p.tokens <= kSmallTokens;
     cudaError_t err = small ? start<kFp8, kSmallTokens, false>(h, mu, up, up_smem, stream) : start<kFp8, kMaxTokens, false>(h, mu, up, up_smem, stream);
     if (err == cudaSuccess)
         err = small ? start<kFp8, kSmallTokens, true>(h, md, down, down_smem, stream) : start<kFp8, kMaxTokens, true>(h, md, down, down_smem, stream);
