@@ -5,8 +5,9 @@
 // With up to 64 tokens the weights of the experts that they hit are all there is to read, so the weights are the rows of the
 // tensor cores' products (128 at a time) and the tokens their columns (16 to 64): every byte of weights goes from memory to
 // shared memory by tensor map and into tcgen05.mma once, and no product has empty rows of weights.
-//   up     a tile is 128 gate rows and the 128 up rows beside them, times ALL tokens' x: no gather, the columns of tokens
-//          that are not the expert's are dropped.  silu(gate) * up goes to a workspace row of (expert, token).
+//   up     a tile is 128 gate rows and the 128 up rows beside them, times x: in bf16 that of ALL tokens (no gather, the columns
+//          of tokens that are not the expert's are dropped), in FP8 that of the expert's.  silu(gate) * up goes to a workspace
+//          row of (expert, token).
 //   down   a tile is 256 output channels of one expert, times its rows of the workspace; a CTA adds up the weighted
 //          results of the experts it works on in shared memory, [token][256 channels] in fp32.
 //
@@ -96,6 +97,7 @@ struct Routing {
     int32_t* begin;     // [experts] first workspace row of a hit expert
     uint16_t* hit;      // hit experts in ascending order
     float* weight;      // down: [rows] the weight of a row's (expert, token)
+    uint8_t* token;     // up, FP8: [rows] the token
 };
 
 __device__ __forceinline__ int count_bits(uint64_t m) { return __popcll(static_cast<long long>(m)); }
@@ -108,7 +110,7 @@ __device__ __forceinline__ int slot_expert(const LayerParams& p, uint32_t masked
     return static_cast<int>(e);
 }
 
-template <int THREADS, bool kWeights>
+template <int THREADS, bool kWeights, bool kTokenOf>
 __device__ __forceinline__ void build_routing(const Routing& t, const LayerParams& p, LayerControl& ctl) {
     const int slots = p.tokens * p.topk;
     // a thread's first slot is on its way meanwhile, as the ranks' masks are
@@ -137,6 +139,14 @@ __device__ __forceinline__ void build_routing(const Routing& t, const LayerParam
     }
     if (threadIdx.x == 0) ctl.hits = static_cast<int>(all >> 32);
     __syncthreads();
+    if constexpr (kTokenOf) {
+        for (int s = threadIdx.x; s < slots; s += THREADS) {
+            const int token = s / p.topk;
+            const int e = slot_expert(p, masked, s == static_cast<int>(threadIdx.x) ? raw0 : p.topk_idx[s], token);
+            if (e >= 0) t.token[t.begin[e] + count_bits(t.tokens[e] & ((1ull << token) - 1))] = static_cast<uint8_t>(token);
+        }
+        __syncthreads();
+    }
     if constexpr (kWeights) {
         // an expert that a token names twice counts with both weights
         for (int s = threadIdx.x; s < slots; s += THREADS) {
@@ -233,15 +243,15 @@ constexpr uint32_t kABytes = kOps * kTileBytes;
 template <bool kFp8>
 __device__ __forceinline__ int round_cols(int n) { return (n + col_step(kFp8) - 1) / col_step(kFp8) * col_step(kFp8); }
 
-// Tokens of a unit: up all, down the expert's; as columns of products.
-template <bool kDown>
+// Tokens of a unit: the expert's, in the first kernel's bf16 form all; as columns of products.
+template <bool kFp8, bool kDown>
 __device__ __forceinline__ int unit_tokens(const LayerParams& p, const Unit<kDown>& u) {
-    return kDown ? count_bits(u.tokens) : p.tokens;
+    return kFp8 || kDown ? count_bits(u.tokens) : p.tokens;
 }
 
 template <bool kFp8, bool kDown>
 __device__ __forceinline__ int unit_cols(const LayerParams& p, const Unit<kDown>& u) {
-    return kDown ? round_cols<kFp8>(count_bits(u.tokens)) : p.cols;
+    return kFp8 || kDown ? round_cols<kFp8>(count_bits(u.tokens)) : p.cols;
 }
 
 // Weights of a unit into its stage.
@@ -395,21 +405,26 @@ __device__ __forceinline__ void layer_splits(const LayerRoles<kDown>& x, int war
     // what is loaded next: tokens [first, count) of a unit
     Unit<kDown> next(w, w.first + group);
     int next_first = 0, next_count = 0;
-    const uint8_t* next_row = nullptr;
+    int next_begin = 0;
+    const uint8_t* next_at = nullptr;
     auto enter = [&] {
         next_first = begin;
         next_count = 0;
         if (!next.more()) return;
-        next_count = unit_tokens(p, next);
-        next_row = p.tokens_x + (kDown ? x.t.begin[next.expert] : 0) * row_bytes + next.step * 256 + half * row_bytes + piece * 16;
+        next_count = count_bits(next.tokens);
+        next_begin = x.t.begin[next.expert];
+        next_at = p.tokens_x + next.step * 256 + piece * 16;
     };
     int4 ahead[kBatchPairs];
     auto fetch = [&] {
 #pragma unroll
         for (int i = 0; i < kBatchPairs; ++i) {
             ahead[i] = make_int4(0, 0, 0, 0);
-            if (next_first + 2 * i + half < next_count)
-                ahead[i] = __ldcg(reinterpret_cast<const int4*>(next_row + (next_first + 2 * i) * row_bytes));
+            const int q = next_first + 2 * i + half;
+            if (q < next_count) {
+                const int row = next_begin + q;
+                ahead[i] = __ldcg(reinterpret_cast<const int4*>(next_at + (kDown ? row : x.t.token[row]) * row_bytes));
+            }
         }
     };
     auto advance = [&] {
@@ -509,7 +524,7 @@ __device__ __forceinline__ void read_sums(const LayerRoles<kDown>& x, int steps,
                                           uint32_t& acc_phase, bool& ok, float (&v)[kTokens]) {
     const LayerParams& p = x.p;
     LayerControl& ctl = x.ctl;
-    const int count = unit_tokens(p, u), cols = unit_cols<kFp8>(p, u);
+    const int count = unit_tokens<kFp8>(p, u), cols = unit_cols<kFp8>(p, u);
 #pragma unroll
     for (int t = 0; t < kTokens; ++t) v[t] = 0.0f;
     const float* ws = nullptr;
@@ -587,13 +602,14 @@ __device__ __forceinline__ void up_sums(const LayerRoles<false>& x, int warp) {
         float v[kTokens];
         read_sums<kFp8, kTokens, false>(x, steps, quarter, op, u, buf, acc_phase, ok, v);
         const int count = count_bits(u.tokens);
+        const uint64_t columns = kFp8 ? ~0ull >> (64 - count) : u.tokens;  // of the expert's tokens, in order
         const int64_t first = x.t.begin[u.expert];
         const int thread = threadIdx.x - 4 * kWarpSize;
         if (steps == w.steps) {
             // through shared memory, kSwap tokens at a time
             for (int base = 0; base < count; base += kSwap) {
                 int q = -base;  // the token's number among the expert's, from base
-                const uint64_t has = unseen(u.tokens);
+                const uint64_t has = unseen(columns);
 #pragma unroll
                 for (int t = 0; t < kTokens; ++t)
                     if (has >> t & 1) {
@@ -612,13 +628,13 @@ __device__ __forceinline__ void up_sums(const LayerRoles<false>& x, int warp) {
             const int a = w.shares.owner(tile0), b = w.shares.owner(tile0 + w.steps - 1);
             const int64_t each = static_cast<int64_t>(p.tokens) * kOps * kTile;
             float* own = p.partial + (2 * static_cast<int64_t>(blockIdx.x) + (u.step == 0)) * each + op * kTile + row;
-            const uint64_t has = unseen(u.tokens);
+            const uint64_t has = unseen(columns);
 #pragma unroll
             for (int t = 0; t < kTokens; ++t)
                 if (has >> t & 1) own[t * (kOps * kTile)] = v[t];
             if (last_to_arrive(x, a, b - a + 1, turn)) {
                 // two tokens at a time, a thread one of a token's rows: the parts in the CTAs' order
-                uint64_t left = u.tokens;
+                uint64_t left = columns;
                 if (thread >= kTile) left &= left - 1;
                 for (int q = thread / kTile; q < count; q += 2) {
                     const float* part = p.partial + (lowest_bit(left) * kOps) * kTile + thread % kTile;
@@ -756,7 +772,7 @@ __device__ __forceinline__ void down_sums(const LayerRoles<true>& x, int warp) {
 
 // The dynamic shared memory of a kernel, after alignment to 1024: stages, then the rest.
 struct Layout {
-    uint32_t tokens, parts, begin, hit, weight, scales, sums, bytes;
+    uint32_t tokens, parts, begin, hit, weight, token, scales, sums, bytes;
 };
 
 __host__ __device__ inline Layout layer_layout(const LayerParams& p, bool fp8, bool down) {
@@ -771,6 +787,7 @@ __host__ __device__ inline Layout layer_layout(const LayerParams& p, bool fp8, b
     l.weight = at, at += down ? 4u * p.tokens * p.topk : 0u;
     const int most = p.tokens * p.topk < p.experts ? p.tokens * p.topk : p.experts;
     l.hit = at, at += 2u * most;
+    l.token = at, at += fp8 && !down ? p.tokens * p.topk : 0u;
     l.bytes = at;
     return l;
 }
@@ -784,7 +801,7 @@ __global__ void __launch_bounds__(layer_threads(kFp8, kTokens), kTokens <= kSmal
     uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     const Layout l = layer_layout(p, kFp8, kDown);
     const Routing t = {reinterpret_cast<uint64_t*>(smem + l.tokens), reinterpret_cast<int32_t*>(smem + l.begin),
-                       reinterpret_cast<uint16_t*>(smem + l.hit), reinterpret_cast<float*>(smem + l.weight)};
+                       reinterpret_cast<uint16_t*>(smem + l.hit), reinterpret_cast<float*>(smem + l.weight), smem + l.token};
     const int warp = threadIdx.x / kWarpSize;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
@@ -806,7 +823,7 @@ __global__ void __launch_bounds__(layer_threads(kFp8, kTokens), kTokens <= kSmal
     // there, the routing and the weights among it; only the first kernel's results are waited for, where they are read.
     if constexpr (kDown) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     else pdl_enter();
-    build_routing<kThreads, kDown>(t, p, ctl);
+    build_routing<kThreads, kDown, kFp8 && !kDown>(t, p, ctl);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
