@@ -1,7 +1,7 @@
 // ep_gemm.cu -- matrix products grouped by expert, with ragged groups (sm_103a tensor cores).
 //
 // Rows of all experts lie in one array; expert e has rows [begin[e], begin[e] + count[e]) and its own
-// weights.  Six forms share one persistent kernel:
+// weights.  Its kernels are of one template:
 //   forward       out[r][j] = sum_c x[r][c] * w[e][j][c]          bf16, both operands contraction-major
 //   transposed    out[r][j] = sum_c x[r][c] * w[e][c][j]          bf16, the weights read across (gradient of the rows)
 //   weight grad   dw[e][j][c] = sum_r dy[r][j] * x[r][c]          bf16, both operands read across, over a group's rows
@@ -89,16 +89,17 @@ ep_status encode(CUtensorMap* map, const Operand& o) {
 
 namespace {
 
-enum GemmForm { kForward = 0, kTransposed = 1, kWeightGrad = 2, kFp8 = 3, kActivated = 4, kGated = 5 };
-constexpr bool has_epilogue(int form) { return form == kActivated || form == kGated; }
+enum GemmForm { kForward = 0, kTransposed = 1, kWeightGrad = 2, kFp8 = 3, kActivated = 4, kGated = 5, kActivatedFp32 = 6 };
+constexpr bool has_epilogue(int form) { return form >= kActivated; }
 
 // Steps (128 bytes of the contraction) that one accumulator sums in tensor memory before its sums are added up in
 // fp32 registers; 0: all of them.  FP8: one block, for its scales.  Weight gradient: 512 rows -- the tensor cores cut
 // sums off instead of rounding them, and 2048 rows in one accumulator left 1.9e-6 of the result against 64 bits, 768
 // 6.7e-7, 640 5.8e-7, 512 4.7e-7 (the same sums of products in fp32 by a library: 3.9e-7), for 1113 (768), 1164 and 1179 us
-// at 65536 rows, 32 experts of 2048 x 7168, and 1125 us where they leave through shared memory (staged_pays()).  The other
-// forms round to bf16, far above that.
-constexpr int segment_steps(int form) { return form == kFp8 ? 1 : form == kWeightGrad ? 8 : 0; }
+// at 65536 rows, 32 experts of 2048 x 7168, and 1125 us where they leave through shared memory (staged_pays()).  The
+// activated form's fp32 output (a router's logits) is summed like it: over 7168 in one accumulator it was off by 7.9e-6.  The
+// other forms round to bf16, far above that.
+constexpr int segment_steps(int form) { return form == kFp8 ? 1 : form == kWeightGrad || form == kActivatedFp32 ? 8 : 0; }
 
 constexpr int kTileRows = 128;      // output rows per CTA
 constexpr int kMaxTileCols = 256;
@@ -150,9 +151,9 @@ struct GemmParams {
 };
 
 // Tensor maps of the two operands: loads of kBox output elements, and smaller ones; and of the results, boxes of 32
-// rows by 128 bytes.
+// rows by 128 bytes, as of the residual.
 struct Maps {
-    CUtensorMap a, a_small, b, b_small, out;
+    CUtensorMap a, a_small, b, b_small, out, residual;
 };
 
 // Where a warp's 32 rows of a tile go: the output row of the first (weight grad: in the group), how many of them exist,
@@ -176,7 +177,7 @@ struct Control {
     uint64_t empty[kMaxStages];
     uint64_t acc_full[2];
     uint64_t acc_empty[2];
-    uint64_t tail_full[kMaxStages];  // weight grad: instead of full, for a group's last, partial block of rows
+    uint64_t tail_full[kMaxStages];  // weight grad: instead of full, for a group's last, partial block of rows; epilogue: a warp's residual
     uint64_t drained;  // every product has been computed
     uint32_t tmem;
     int32_t abort_flag;
@@ -338,6 +339,7 @@ struct Roles {
     Waits waits;
     uint8_t* stages;
     uint8_t* boxes;
+    uint8_t* residuals;  // a box for each warp
     uint32_t tmem, rank, stage_bytes;  // rank: of the CTA in its pair
     int num_stages, worker, workers;
 };
@@ -650,34 +652,83 @@ __device__ __forceinline__ void put_columns(const Roles& x, uint32_t box, const 
     } else if (lane_id() < at.rows && col < p.cols_dim) {
         const int64_t row = (FORM == kWeightGrad ? static_cast<int64_t>(at.group) * p.rows_dim : 0) + at.row + lane_id();
         uint8_t* out = static_cast<uint8_t*>(p.out) + row * p.out_row_bytes;
-        if (FORM == kActivated && p.out_fp32) store_fp32(out, col, p.cols_dim, v, p.wide_stores != 0);
+        if (FORM == kActivatedFp32) store_fp32(out, col, p.cols_dim, v, p.wide_stores != 0);
         else store_bf16(out, col, p.cols_dim, v, p.wide_stores != 0);
     }
 }
 
-// v += bias of 32 columns from `col`, in pieces of 8 that are there.  All lanes read the same words.
-__device__ __forceinline__ void add_bias(const float* bias, int col, int cols, float (&v)[32]) {
+// A warp's box of the residual: 32 rows by 64 columns.  By tensor map, not by the lanes: of 227 KB of shared memory the L1
+// cache keeps nothing, and loads of 32 rows at once wait for its few lines (8187 rows, 7168 x 2048: 245 us, 123 without a
+// residual).  One box, since two leave four stages of a pair's operands instead of six (161 us).
+constexpr uint32_t kResidualBytes = kEpilogueWarps * kOutBox;
+
+// What a warp asks for of its part of a tile before the tile's sums are there: the bias, lane l columns 4 l to 4 l + 3, and
+// the residual.
+template <int FORM>
+struct Ahead {
+    float4 bias, up_bias;
+    uint8_t* box;
+    uint64_t* arrived;
+    uint32_t phase;
+    bool asked;
+
+    __device__ __forceinline__ Ahead(const Roles& x, int w)
+        : box(x.residuals + w * kOutBox), arrived(&x.ctl.tail_full[w]), phase(0), asked(false) {}
+    __device__ __forceinline__ void load_bias(const GemmParams& p, const Place& at) {
+        bias = up_bias = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (p.bias == nullptr || 4 * lane_id() >= at.cols || at.col + 4 * lane_id() >= p.cols_dim) return;
+        const float* from = p.bias + static_cast<int64_t>(at.group) * (FORM == kGated ? 2 : 1) * p.cols_dim + at.col + 4 * lane_id();
+        bias = __ldg(reinterpret_cast<const float4*>(from));
+        if (FORM == kGated) up_bias = __ldg(reinterpret_cast<const float4*>(from + p.cols_dim));
+    }
+    // 64 columns from column c of the warp's part, after the warp has read what is there.
+    __device__ __forceinline__ void ask_residual(const Roles& x, const Place& at, int c) {
+        asked = x.p.residual != nullptr && at.rows > 0 && c < at.cols && at.col + c < x.p.cols_dim;
+        if (!asked) return;
+        __syncwarp();
+        if (lane_id() == 0) {
+            mbar_arrive_expect_tx(arrived, kOutBox);
+            tma_load_2d<1>(box, &x.maps.residual, at.col + c, at.row, smem_u32(arrived));
+        }
+    }
+    __device__ __forceinline__ bool wait_residual(const Waits& waits) {
+        if (!asked) return true;
+        if (!warp_wait(arrived, phase, waits)) return false;
+        asked = false;
+        phase ^= 1;
+        return true;
+    }
+    // Of a wait that was given up: the copy ends before the memory goes away.
+    __device__ __forceinline__ void leave() {
+        for (int k = 0; asked && k < (1 << 8) && !mbar_try_wait(arrived, phase); ++k) {
+        }
+    }
+};
+
+// v += 32 columns of the bias from column `c` of the warp's part, which the lanes hold.
+__device__ __forceinline__ void add_bias(const float4& bias, int c, float (&v)[32]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (col + 8 * i + 8 > cols) break;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[8 * i + j] += __ldg(bias + col + 8 * i + j);
+    for (int i = 0; i < 8; ++i) {
+        const int from = c / 4 + i;
+        v[4 * i] += __shfl_sync(kFullMask, bias.x, from);
+        v[4 * i + 1] += __shfl_sync(kFullMask, bias.y, from);
+        v[4 * i + 2] += __shfl_sync(kFullMask, bias.z, from);
+        v[4 * i + 3] += __shfl_sync(kFullMask, bias.w, from);
     }
 }
 
 // The epilogue of 32 output columns of a lane's row, from column `c` of its warp's part of the tile: v holds the sums
-// (gated: of the gates, and `up` of the ups) and gets what is written.
+// (gated: of the gates, and `up` of the ups) and gets what is written.  False: the wait for the residual was given up.
 template <int FORM>
-__device__ __forceinline__ void finish_columns(const GemmParams& p, const Place& at, int c, float (&v)[32], float (&up)[32]) {
+__device__ __forceinline__ bool finish_columns(const Roles& x, const Place& at, int c, Ahead<FORM>& ahead, float (&v)[32], float (&up)[32]) {
+    const GemmParams& p = x.p;
     const int col = at.col + c;
-    if (col >= p.cols_dim) return;
-    const int n = FORM == kGated ? 2 * p.cols_dim : p.cols_dim;
+    if (col >= p.cols_dim) return true;
     const int64_t row = static_cast<int64_t>(at.row) + lane_id();
     const bool in = lane_id() < at.rows;
     if (p.bias) {
-        const float* bias = p.bias + static_cast<int64_t>(at.group) * n;
-        add_bias(bias, col, p.cols_dim, v);
-        if (FORM == kGated) add_bias(bias + p.cols_dim, col, p.cols_dim, up);
+        add_bias(ahead.bias, c, v);
+        if (FORM == kGated) add_bias(ahead.up_bias, c, up);
     }
     if (p.pre && in) {
         uint8_t* pre = p.pre + row * p.pre_row_bytes;
@@ -708,17 +759,19 @@ __device__ __forceinline__ void finish_columns(const GemmParams& p, const Place&
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] *= w;
     }
-    if (p.residual && in) {
-        const int4* from = reinterpret_cast<const int4*>(p.residual + row * p.residual_row_bytes + 2 * static_cast<int64_t>(col));
+    if (p.residual) {
+        if (!ahead.wait_residual(x.waits)) return false;
+        const uint8_t* from = ahead.box + lane_id() * kRowBytes;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (col + 8 * i + 8 > p.cols_dim) break;
+        for (int i = 0; i < 4; ++i) {  // 16-byte pieces lie exclusive-or'd with the row's number
             float r[8];
-            unpack8(ld_stream_v4(from + i), r);
+            unpack8(*reinterpret_cast<const int4*>(from + ((((c >> 5 & 1) * 4 + i) ^ (lane_id() & 7)) << 4)), r);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[8 * i + j] += r[j];
         }
+        if (c & 32) ahead.ask_residual(x, at, c + 32);
     }
+    return true;
 }
 
 // Whether a warp's part of a tile leaves through its boxes: not the ends of groups, nor tiles of 64 columns.  Asked once a
@@ -745,6 +798,25 @@ __device__ __forceinline__ void put_sums(const Roles& x, uint32_t box, const Pla
     }
 }
 
+// The same after their epilogue, by stores of each lane.
+template <int FORM>
+__device__ __forceinline__ bool put_finished(const Roles& x, const Place& at, Ahead<FORM>& ahead, const uint64_t (&acc)[2][32]) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        if (32 * c >= at.cols) break;
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const uint64_t pair = acc[c / 2][c % 2 * 16 + i];
+            v[2 * i] = __uint_as_float(static_cast<uint32_t>(pair));
+            v[2 * i + 1] = __uint_as_float(static_cast<uint32_t>(pair >> 32));
+        }
+        if (!finish_columns<FORM>(x, at, 32 * c, ahead, v, v)) return false;
+        put_columns<FORM, false>(x, 0, at, 32 * c, v);
+    }
+    return true;
+}
+
 // Eight warps: accumulators to the output.
 template <int FORM, int CG>
 __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
@@ -761,6 +833,7 @@ __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
     int buf = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
+    Ahead<FORM> ahead(x, w);
     for (int tile = x.worker; ok && tile < ctl.tiles; tile += x.workers) {
         const Tile q = decode<FORM, CG>(t, p, ctl, tile);
         if (FORM == kWeightGrad && p.accumulate && q.steps == 0) continue;  // nothing to add
@@ -769,6 +842,10 @@ __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
         const int rows = min(32, max(0, (FORM == kWeightGrad ? p.rows_dim : q.rows) - in_group));
         const Place at = {(FORM == kWeightGrad ? 0 : q.row0) + in_group, q.n0 + half * cols_half, q.group,
                           static_cast<short>(rows), static_cast<short>(cols_half)};
+        if constexpr (has_epilogue(FORM)) {
+            ahead.load_bias(p, at);
+            ahead.ask_residual(x, at, 0);
+        }
         if constexpr (kSegment == 0) {
             ok = warp_wait(&ctl.acc_full[buf], acc_phase, x.waits);
             if (!ok) break;
@@ -796,7 +873,10 @@ __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
                 float v[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
-                if constexpr (has_epilogue(FORM)) finish_columns<FORM>(p, at, c, v, up);
+                if constexpr (has_epilogue(FORM)) {
+                    ok = ok && finish_columns<FORM>(x, at, c, ahead, v, up);
+                    if (!ok) continue;  // the accumulator is freed all the same
+                }
                 if (staged) put_columns<FORM, true>(x, box, at, c, v);
                 else put_columns<FORM, false>(x, box, at, c, v);
             }
@@ -865,11 +945,15 @@ __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
             __syncwarp();
             if (!ok) break;
             const Place to = read_place(&ctl.at[w]);
-            if (in_boxes<FORM>(p, to)) put_sums<FORM, true>(x, box, to, acc);
+            if constexpr (has_epilogue(FORM)) {
+                ok = put_finished<FORM>(x, to, ahead, acc);
+                if (!ok) break;
+            } else if (in_boxes<FORM>(p, to)) put_sums<FORM, true>(x, box, to, acc);
             else put_sums<FORM, false>(x, box, to, acc);
             __syncwarp();  // the place has been read
         }
     }
+    if constexpr (has_epilogue(FORM)) ahead.leave();
     if (lane_id() == 0) bulk_wait_all();
     __syncwarp();
 }
@@ -888,7 +972,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     t.begin = t.count + p.groups.groups;
     const uint32_t table_end = (4u * (3u * p.groups.groups + 1u) + 1023u) & ~1023u;
     uint8_t* const boxes = smem + table_end;
-    const uint32_t out_bytes = p.staged ? kEpilogueWarps * out_boxes(FORM) * kOutBox : 0;
+    uint32_t out_bytes = p.staged ? kEpilogueWarps * out_boxes(FORM) * kOutBox : 0;
+    uint8_t* const residuals = boxes + out_bytes;
+    if (has_epilogue(FORM) && p.residual) out_bytes += kResidualBytes;
     uint8_t* const stages = boxes + out_bytes;
 
     const int warp = threadIdx.x / kWarpSize;
@@ -918,7 +1004,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     tc_fence_after();
 
     const uint32_t stage_bytes = kABytes + ctl.tile_cols / CG * kRowBytes;
-    const Roles x = {maps, p, t, ctl, {&ctl.abort_flag, p.status, p.wait_limit_ns}, stages, boxes, ctl.tmem, rank, stage_bytes,
+    const Roles x = {maps, p, t, ctl, {&ctl.abort_flag, p.status, p.wait_limit_ns}, stages, boxes, residuals, ctl.tmem, rank, stage_bytes,
                      min(kMaxStages, static_cast<int>((kMaxSmem - 1024u - table_end - out_bytes) / stage_bytes)),
                      static_cast<int>(blockIdx.x / CG), static_cast<int>(gridDim.x / CG)};
     // Forms with segments hold 128 sums a thread in their eight epilogue warps: registers move there from the
@@ -1077,7 +1163,8 @@ cudaError_t plan_gemm(LaunchPlan* plan) {
 // The same for the forms with an epilogue, whose kernels the others' callers do not load.
 cudaError_t plan_act(LaunchPlan* plan) {
     plan->act_pairs = plan->num_sms / 2;
-    const cudaError_t err = plan_form<kActivated>(plan);
+    cudaError_t err = plan_form<kActivated>(plan);
+    if (err == cudaSuccess) err = plan_form<kActivatedFp32>(plan);
     return err == cudaSuccess ? plan_form<kGated>(plan) : err;
 }
 
@@ -1115,6 +1202,10 @@ ep_status launch(ep_handle* h, const Operand& a, const Operand& a_small, const O
             st = encode(&m.out, {p.out, Element::kBf16, 2, {cols, static_cast<uint64_t>(p.groups.num_rows), 1, 1},
                                  {row, 0, 0}, {64, 32, 1, 1}});
     }
+    m.residual = m.b;  // not used
+    if (st == EP_OK && p.residual)
+        st = encode(&m.residual, {p.residual, Element::kBf16, 2, {static_cast<uint64_t>(p.cols_dim), static_cast<uint64_t>(p.groups.num_rows), 1, 1},
+                                  {static_cast<uint64_t>(p.residual_row_bytes), 0, 0}, {64, 32, 1, 1}});
     if (p.a_words) {
         m.a = m.a_small = m.b;  // not used
     } else {
@@ -1235,7 +1326,7 @@ ep_status ep_grouped_gemm_act(ep_handle* h, int64_t num_rows, int32_t n, int32_t
     const ep_status rows = check_rows(x, x_row_bytes, 2 * static_cast<int64_t>(k), w, out, out_row_bytes, p.out_fp32 ? 2 * width : width, &p);
     if (rows != EP_OK) return rows;
     EP_CHECK_ARG(p.a_words == nullptr, "x must be 16-byte aligned, its rows multiples of 16 bytes apart (%lld)", static_cast<long long>(x_row_bytes));
-    EP_CHECK_ARG(aligned4(bias) && aligned4(row_weights), "misaligned bias or row_weights");
+    EP_CHECK_ARG(aligned16(bias) && aligned4(row_weights), "bias must be 16-byte aligned, row_weights 4-byte aligned");
     EP_CHECK_ARG(!residual || (aligned16(residual) && row_stride_ok(residual_row_bytes, 2 * static_cast<int64_t>(width))),
                  "residual must be 16-byte aligned with a row stride in multiples of 16 that holds a row (%lld bytes)",
                  static_cast<long long>(residual_row_bytes));
@@ -1257,6 +1348,7 @@ ep_status ep_grouped_gemm_act(ep_handle* h, int64_t num_rows, int32_t n, int32_t
     const Operand a = row_operand(x, false, k, num_rows, x_row_bytes, kBox);
     const Operand a_small = row_operand(x, false, k, num_rows, x_row_bytes, kRowBox);
     const Operand b = weight_operand(w, false, k, n, groups, kBox), b_small = weight_operand(w, false, k, n, groups, kColBox);
+    if (p.out_fp32) return launch<kActivatedFp32>(h, a, a_small, b, b_small, p, rows_each, stream);
     return gated ? launch<kGated>(h, a, a_small, b, b_small, p, rows_each, stream)
                  : launch<kActivated>(h, a, a_small, b, b_small, p, rows_each, stream);
 }
