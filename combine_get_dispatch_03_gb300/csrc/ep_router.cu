@@ -7,12 +7,15 @@
 //                softmax  dl = scale * u * (dw - sum dw u)        sigmoid  dl = scale * u * (dw - sum dw u) * (1 - s)
 //              else  sigmoid  dl = scale * dw * s * (1 - s) of the chosen,  softmax  dl_e = p_e * (scale * dw_e - sum scale dw p)
 //
-// A warp owns a token; its lanes hold neighbouring experts.  A round of the selection is a maximum over the
-// warp of order-preserving 32-bit keys, a vote for the lowest lane that has it, and that lane's next largest.
+// A warp owns a token; its lanes hold neighbouring experts.  The K-th largest of the lanes' largest keys is a bound that at
+// least K keys reach, few more do, and no chosen key lies below: those that reach it are given a lane each, which counts
+// the ones before it.  Where more than 32 reach it (ties), the keys are taken one by one (choose_in_turn).
 //
-// Which experts are chosen must not hang on the rounding of s.  Without bias and groups the keys are the logits
-// themselves.  Otherwise 32-bit keys decide unless two that are compared lie closer than their error (kSigmoidError); such
-// a token's keys are computed again in 64 bits (choose_exactly), a fraction of a percent of the tokens.
+// Which experts are chosen must not hang on the rounding of s.  Without bias the keys are the logits themselves; groups
+// are compared by their scores.  32-bit scores decide unless two that are compared lie closer than their error
+// (kSigmoidError): such a token's keys are computed again in 64 bits, those that reached the bound (sigmoid) or all of them
+// (choose_exactly), a fraction of a percent of the tokens.
+#include "ep_act.cuh"
 #include "ep_groups.cuh"
 #include "ep_handle.h"
 #include "ep_trace.h"
@@ -43,18 +46,7 @@ struct RouterParams {
     float scale;
 };
 
-// Order-preserving 32-bit key; 0 for what cannot be chosen (NaN, -inf).
-__device__ __forceinline__ uint32_t ordered(float v) {
-    if (!(v > -INFINITY)) return 0;
-    const uint32_t u = __float_as_uint(v + 0.0f);  // -0 as 0
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-
-__device__ __forceinline__ float unordered(uint32_t k) {
-    if (k == 0) return -INFINITY;
-    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
-}
-
+// Order-preserving 64-bit key; 0 for what cannot be chosen (NaN, -inf).
 __device__ __forceinline__ uint64_t ordered64(double v) {
     if (!(v > -INFINITY)) return 0;
     const uint64_t u = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
@@ -66,16 +58,13 @@ __device__ __forceinline__ double unordered64(uint64_t k) {
     return __longlong_as_double(static_cast<long long>(k >> 63 ? k & ~(1ull << 63) : ~k));
 }
 
-// exp(v) to 2^-22: log2(e) in two parts, so that the exponent's rounding comes back as a factor.  Past e^88 and e^-104
-// (0) it stays there: keys that become equal so are looked at in 64 bits.
-__device__ __forceinline__ float exp_fast(float v) {
-    v = fminf(fmaxf(v, -104.0f), 88.0f);
-    constexpr float kHi = 1.44269502f, kLo = 1.92596303e-8f, kLn2 = 0.693147182f;
-    const float t = v * kHi;
-    const float rest = fmaf(v, kHi, -t) + v * kLo;
-    float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
-    return fmaf(e, rest * kLn2, e);
+// exp(v) to 2^-22.  Past e^88 and e^-104 (0) it stays there: keys that become equal so are looked at in 64 bits.
+__device__ __forceinline__ float exp_fast(float v) { return exp_fp32(fminf(fmaxf(v, -104.0f), 88.0f)); }
+
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
 
 // A logit: NaN counts as -inf (it cannot be chosen and has no weight), +inf as the largest finite value.
@@ -107,7 +96,7 @@ __device__ __forceinline__ void load_row(const RouterParams& p, int64_t token, f
                     unpack8(q, f);
                 }
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) l[i * kVec + j] = !in || f[j] != f[j] ? -INFINITY : fminf(f[j], 3.402823466e38f);
+                for (int j = 0; j < kVec; ++j) l[i * kVec + j] = in ? fminf(fmaxf(f[j], -INFINITY), 3.402823466e38f) : -INFINITY;  // fmaxf drops NaN
             }
             return;
         }
@@ -128,7 +117,7 @@ __device__ __forceinline__ void softmax_stats(const float (&l)[V], float* most, 
     float m = l[0];
 #pragma unroll
     for (int v = 1; v < V; ++v) m = fmaxf(m, l[v]);
-    m = unordered(__reduce_max_sync(kFullMask, ordered(m)));
+    m = warp_max(m);
     const float base = m > -INFINITY ? m : 0.0f;
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -137,46 +126,73 @@ __device__ __forceinline__ void softmax_stats(const float (&l)[V], float* most, 
     *sum = warp_sum((s[0] + s[1]) + (s[2] + s[3]));
 }
 
-// The token's choice with keys in 64 bits.  Returns lane k's expert (-1: none) for k < topk.
+__device__ __forceinline__ uint64_t warp_max64(uint64_t v) {
+    const uint32_t high = __reduce_max_sync(kFullMask, static_cast<uint32_t>(v >> 32));
+    const uint32_t low = __reduce_max_sync(kFullMask, v >> 32 == high ? static_cast<uint32_t>(v) : 0u);
+    return static_cast<uint64_t>(high) << 32 | low;
+}
+
+// a >= b: the two largest of four.
+__device__ __forceinline__ void join_two(uint64_t& a, uint64_t& b, uint64_t c, uint64_t d) {
+    b = c > a ? (a > d ? a : d) : (b > c ? b : c);
+    a = c > a ? c : a;
+}
+
+// The token's choice with keys in 64 bits.  Returns lane k's expert (-1: none) for k < topk.  The lanes' experts are worked
+// on side by side: FP64 instructions are slow, and each alone waits for the one before.
 template <typename T, int V>
 __device__ __noinline__ int choose_exactly(const RouterParams& p, int64_t token) {
     uint64_t key[V];
     const int first = lane_id() * V;
-    double most = 0.0, sum = 1.0;
+    double most = 0.0, inv_sum = 1.0;
     if (p.softmax) {
-        most = -INFINITY;
-        for (int v = 0; v < V && first + v < p.experts; ++v) most = fmax(most, static_cast<double>(logit<T>(p.logits, token * p.experts + first + v)));
-        for (int o = kWarpSize / 2; o > 0; o >>= 1) most = fmax(most, __shfl_xor_sync(kFullMask, most, o));
-        if (!(most > -INFINITY)) most = 0.0;
-        sum = 0.0;
-        for (int v = 0; v < V && first + v < p.experts; ++v) sum += exp(static_cast<double>(logit<T>(p.logits, token * p.experts + first + v)) - most);
+        float top = -INFINITY;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (first + v < p.experts) top = fmaxf(top, logit<T>(p.logits, token * p.experts + first + v));
+        top = warp_max(top);
+        most = top > -INFINITY ? top : 0.0;
+        double sum = 0.0;
+#pragma unroll 8
+        for (int v = 0; v < V; ++v) {
+            const float l = first + v < p.experts ? logit<T>(p.logits, token * p.experts + first + v) : -INFINITY;
+            sum += exp(static_cast<double>(l) - most);
+        }
         for (int o = kWarpSize / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFullMask, sum, o);
+        inv_sum = sum > 0.0 ? sum : 1.0;
     }
+#pragma unroll 8
     for (int v = 0; v < V; ++v) {
-        key[v] = 0;
-        if (first + v >= p.experts) continue;
-        const double l = static_cast<double>(logit<T>(p.logits, token * p.experts + first + v));
-        if (!(l > -INFINITY)) continue;
-        const double s = p.softmax ? exp(l - most) / sum : 1.0 / (1.0 + exp(-l));
-        key[v] = ordered64(p.bias ? s + static_cast<double>(p.bias[first + v]) : s);
+        const float l = first + v < p.experts ? logit<T>(p.logits, token * p.experts + first + v) : -INFINITY;
+        const double e = exp(p.softmax ? static_cast<double>(l) - most : -static_cast<double>(l));
+        double s = p.softmax ? e / inv_sum : 1.0 / (1.0 + e);
+        if (p.bias && first + v < p.experts) s += static_cast<double>(p.bias[first + v]);
+        key[v] = l > -INFINITY ? ordered64(s) : 0;
     }
     if (p.groups > 1) {
-        const int size = p.experts / p.groups;
+        const int size = p.experts / p.groups, lanes = size / V;
         uint64_t mine = 0;  // lane g: the score of group g
-        for (int g = 0; g < p.groups; ++g) {
+        if (lanes * V == size && (lanes & (lanes - 1)) == 0) {  // a group is a power of two of whole lanes
             uint64_t a = 0, b = 0;
-            for (int v = 0; v < V; ++v) {
-                if (first + v >= p.experts || (first + v) / size != g) continue;
-                if (key[v] > a) b = a, a = key[v];
-                else if (key[v] > b) b = key[v];
-            }
-            for (int o = kWarpSize / 2; o > 0; o >>= 1) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) join_two(a, b, key[v], 0);
+            for (int o = 1; o < lanes; o <<= 1) {
                 const uint64_t c = __shfl_xor_sync(kFullMask, a, o), d = __shfl_xor_sync(kFullMask, b, o);
-                b = c > a ? (a > d ? a : d) : (b > c ? b : c);
-                a = c > a ? c : a;
+                join_two(a, b, c, d);
             }
             const uint64_t score = size == 1 ? a : ordered64(unordered64(a) + unordered64(b));
-            if (lane_id() == g) mine = score;
+            mine = __shfl_sync(kFullMask, score, min(lane_id() * lanes, kWarpSize - 1));
+        } else {
+            for (int g = 0; g < p.groups; ++g) {
+                uint64_t a = 0, b = 0;
+                for (int v = 0; v < V; ++v)
+                    if (first + v < p.experts && (first + v) / size == g) join_two(a, b, key[v], 0);
+                for (int o = kWarpSize / 2; o > 0; o >>= 1) {
+                    const uint64_t c = __shfl_xor_sync(kFullMask, a, o), d = __shfl_xor_sync(kFullMask, b, o);
+                    join_two(a, b, c, d);
+                }
+                if (lane_id() == g) mine = size == 1 ? a : ordered64(unordered64(a) + unordered64(b));
+            }
         }
         int better = 0;
         for (int g = 0; g < p.groups; ++g) {
@@ -184,45 +200,46 @@ __device__ __noinline__ int choose_exactly(const RouterParams& p, int64_t token)
             better += other > mine || (other == mine && g < lane_id());
         }
         const unsigned stay = __ballot_sync(kFullMask, lane_id() < p.groups && better < p.kept);
+#pragma unroll
         for (int v = 0; v < V; ++v)
             if (first + v < p.experts && !(stay >> ((first + v) / size) & 1)) key[v] = 0;
     }
     int chosen = -1;
+#pragma unroll 1
     for (int k = 0; k < p.topk; ++k) {
         uint64_t best = 0;
-        int at = -1;
+        int at = 0;
+#pragma unroll
         for (int v = 0; v < V; ++v)
             if (key[v] > best) best = key[v], at = v;
-        uint64_t top = best;
-        for (int o = kWarpSize / 2; o > 0; o >>= 1) {
-            const uint64_t c = __shfl_xor_sync(kFullMask, top, o);
-            top = c > top ? c : top;
-        }
+        const uint64_t top = warp_max64(best);
         if (top == 0) break;
         const int lane = __ffs(__ballot_sync(kFullMask, best == top)) - 1;
         const int expert = __shfl_sync(kFullMask, first + at, lane);
         if (lane_id() == k) chosen = expert;
-        if (lane_id() == lane) key[at] = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (lane_id() == lane && v == at) key[v] = 0;
     }
     return chosen;
 }
 
 // The score of the group of this lane's number (lane g < groups), from the warp's keys: two largest, added up.
 template <int V>
-__device__ __forceinline__ float group_score(const RouterParams& p, const uint32_t (&key)[V], uint32_t* scratch) {
+__device__ __forceinline__ float group_score(const RouterParams& p, const float (&key)[V], float* scratch) {
     const int size = p.experts / p.groups;
-    uint32_t a = 0, b = 0;
+    float a = -INFINITY, b = -INFINITY;
     const int lanes = size / V;
     if (lanes * V == size && (lanes & (lanes - 1)) == 0) {  // a group is a power of two of whole lanes
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            b = max(b, min(a, key[v]));
-            a = max(a, key[v]);
+            b = fmaxf(b, fminf(a, key[v]));
+            a = fmaxf(a, key[v]);
         }
         for (int o = 1; o < lanes; o <<= 1) {
-            const uint32_t c = __shfl_xor_sync(kFullMask, a, o), d = __shfl_xor_sync(kFullMask, b, o);
-            b = max(min(a, c), max(b, d));
-            a = max(a, c);
+            const float c = __shfl_xor_sync(kFullMask, a, o), d = __shfl_xor_sync(kFullMask, b, o);
+            b = fmaxf(fminf(a, c), fmaxf(b, d));
+            a = fmaxf(a, c);
         }
         const int from = min(lane_id() * lanes, kWarpSize - 1);
         a = __shfl_sync(kFullMask, a, from);
@@ -234,135 +251,234 @@ __device__ __forceinline__ float group_score(const RouterParams& p, const uint32
         __syncwarp();
         if (lane_id() < p.groups)
             for (int i = 0; i < size; ++i) {
-                const uint32_t k = scratch[lane_id() * size + i];
-                b = max(b, min(a, k));
-                a = max(a, k);
+                const float k = scratch[lane_id() * size + i];
+                b = fmaxf(b, fminf(a, k));
+                a = fmaxf(a, k);
             }
     }
-    return size == 1 ? unordered(a) : unordered(a) + unordered(b);
+    return size == 1 ? a : a + b;
 }
 
+// How far apart two keys must lie for 32 bits to tell them; `error` is that of their scores.
+__device__ __forceinline__ float key_error(float error, float a, float b) { return error + kSumError * (fabsf(a) + fabsf(b)); }
+
+struct Chosen {
+    int expert;  // lane k's, -1: none
+    bool close;  // 32 bits may have it wrong
+};
+
+// The K largest keys one by one, each the maximum of the lanes' largest, the lowest lane's and expert's of equal ones.
 template <typename T, int V>
-__device__ __forceinline__ void route_token(const RouterParams& p, int64_t token, uint32_t* scratch) {
+__device__ __noinline__ Chosen choose_in_turn(const RouterParams& p, int64_t token, float (&key)[V], float error, bool scored) {
     const int first = lane_id() * V;
-    const int64_t out = token * p.topk + lane_id();
-    if (p.token_mask && p.token_mask[token] == 0) {
-        if (lane_id() < p.topk) p.topk_idx[out] = -1, p.topk_weights[out] = 0.0f;
-        return;
-    }
-    float l[V];
-    load_row<T, V>(p, token, l);
-    const bool by_logit = p.bias == nullptr && p.groups == 1;  // the scores' order is the logits'
-    const bool whole_sum = p.softmax && !(p.normalize && by_logit);
-    float most = 0.0f, sum = 1.0f;
-    if (whole_sum) softmax_stats<V>(l, &most, &sum);
-    uint32_t key[V];
-    float largest = 1.0f;  // score
-    if (by_logit) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) key[v] = ordered(l[v]);
-    } else {
-        const float inv = 1.0f / sum;
-        float top = 0.0f;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const bool in = l[v] > -INFINITY;
-            const float e = exp_fast(p.softmax ? l[v] - most : -l[v]);
-            float s = p.softmax ? e * inv : __frcp_rn(1.0f + e);
-            top = fmaxf(top, in ? s : 0.0f);
-            if (p.bias && in) s += __ldg(p.bias + first + v);
-            key[v] = in ? ordered(s) : 0;
-        }
-        largest = unordered(__reduce_max_sync(kFullMask, ordered(top)));
-    }
-    const float error = (p.softmax ? kSoftmaxError : kSigmoidError) * largest;
-    bool close = false;
-    if (p.groups > 1) {
-        const int size = p.experts / p.groups;
-        const float score = group_score<V>(p, key, scratch);
-        const uint32_t mine = score > -INFINITY ? ordered(score) : 1;
-        int better = 0;
-        for (int g = 0; g < p.groups; ++g) {
-            const uint32_t other = __shfl_sync(kFullMask, mine, g);
-            better += other > mine || (other == mine && g < lane_id());
-        }
-        const bool there = lane_id() < p.groups, in = there && better < p.kept;
-        const unsigned stay = __ballot_sync(kFullMask, in);
-        // the last that stays and the first that does not
-        const float last = unordered(__reduce_min_sync(kFullMask, in ? mine : 0xffffffffu));
-        const float next = unordered(__reduce_max_sync(kFullMask, there && !in ? mine : 0u));
-        close = last - next <= 2.0f * error + kSumError * (fabsf(last) + fabsf(next));  // false for infinite ones
-        if (size % V == 0) {
-            if (first < p.experts && !(stay >> (first / size) & 1))
-#pragma unroll
-                for (int v = 0; v < V; ++v) key[v] = 0;
-        } else {
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (first + v < p.experts && !(stay >> ((first + v) / size) & 1)) key[v] = 0;
-        }
-    }
-    int chosen = -1;
-    uint32_t chosen_key = 0, last_key = 0;
+    Chosen r = {-1, false};
+    float chosen_key = -INFINITY, last = -INFINITY;
 #pragma unroll 1
     for (int k = 0; k < p.topk; ++k) {
-        uint32_t best = key[0];
-#pragma unroll
-        for (int v = 1; v < V; ++v) best = max(best, key[v]);
-        const uint32_t top = __reduce_max_sync(kFullMask, best);
-        last_key = top;
-        if (top == 0) break;
-        const int lane = __ffs(__ballot_sync(kFullMask, best == top)) - 1;
+        float best = key[0];
         int at = 0;
-        bool found = lane_id() != lane;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const bool hit = !found && key[v] == top;
-            if (hit) at = v, key[v] = 0;
-            found |= hit;
-        }
+        for (int v = 1; v < V; ++v)
+            if (key[v] > best) best = key[v], at = v;
+        const float top = warp_max(best);
+        last = top;
+        if (!(top > -INFINITY)) break;
+        const int lane = __ffs(__ballot_sync(kFullMask, best == top)) - 1;
         const int expert = __shfl_sync(kFullMask, first + at, lane);
-        if (lane_id() == k) chosen = expert, chosen_key = top;
+        if (lane_id() == k) r.expert = expert, chosen_key = top;
+        if (lane_id() == lane) key[at] = -INFINITY;
     }
-    if (!by_logit && !close) {
-        // Neighbours in the order, unless they tie because their inputs are the same.
-        float lc = 0.0f, bc = 0.0f;
-        if (chosen >= 0) {
-            lc = logit<T>(p.logits, token * p.experts + chosen);
-            if (p.bias) bc = p.bias[chosen];
+    if (!scored) return r;
+    // Neighbours in the order, and who is left next to the last: too close, unless they tie because their inputs are the same.
+    float lc = 0.0f, bc = 0.0f;
+    if (r.expert >= 0) {
+        lc = logit<T>(p.logits, token * p.experts + r.expert);
+        if (p.bias) bc = p.bias[r.expert];
+    }
+    const float after = __shfl_down_sync(kFullMask, chosen_key, 1);
+    const float l_after = __shfl_down_sync(kFullMask, lc, 1), b_after = __shfl_down_sync(kFullMask, bc, 1);
+    bool near = r.expert >= 0 && lane_id() < p.topk - 1 && lane_id() < kWarpSize - 1 && after > -INFINITY &&
+                chosen_key - after <= key_error(error, chosen_key, after) && !(lc == l_after && bc == b_after);
+    if (last > -INFINITY) {  // all K are there
+        const float l_last = __shfl_sync(kFullMask, lc, p.topk - 1), b_last = __shfl_sync(kFullMask, bc, p.topk - 1);
+        for (int v = 0; v < V; ++v)
+            if (key[v] > -INFINITY && last - key[v] <= key_error(error, last, key[v]))
+                near |= !(logit<T>(p.logits, token * p.experts + first + v) == l_last && (p.bias == nullptr || p.bias[first + v] == b_last));
+    }
+    r.close = __any_sync(kFullMask, near);
+    return r;
+}
+
+// What a warp knows of the keys that reach the bound: of each its key, expert and logit, in order of experts, and the keys in
+// descending order.
+struct Reach {
+    float2 key_expert[kWarpSize];
+    float logit[kWarpSize];
+    float2 sorted[kWarpSize];  // key, which (as bits)
+};
+
+// The scored tokens' keys, s + bias, of the groups that stay; *error: of a score.  Whether 32 bits may have the groups wrong.
+template <int V>
+__device__ __forceinline__ bool make_keys(const RouterParams& p, const float (&l)[V], float most, float sum, float* scratch,
+                                          float (&key)[V], float* error) {
+    const int first = lane_id() * V;
+    const float inv = 1.0f / sum;
+    float top = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const bool in = l[v] > -INFINITY;
+        const float e = exp_fast(p.softmax ? l[v] - most : -l[v]);
+        const float s = p.softmax ? e * inv : reciprocal(1.0f + e);
+        top = fmaxf(top, in ? s : 0.0f);
+        // NaN (a bias) as -inf
+        key[v] = in ? fmaxf(p.bias ? s + __ldg(p.bias + first + v) : s, -INFINITY) : -INFINITY;
+    }
+    *error = (p.softmax ? kSoftmaxError : kSigmoidError) * warp_max(top);
+    if (p.groups == 1) return false;
+    const int size = p.experts / p.groups;
+    const float score = group_score<V>(p, key, scratch);
+    int better = 0;
+    for (int g = 0; g < p.groups; ++g) {
+        const float other = __shfl_sync(kFullMask, score, g);
+        better += other > score || (other == score && g < lane_id());
+    }
+    const bool there = lane_id() < p.groups, in = there && better < p.kept;
+    const unsigned stay = __ballot_sync(kFullMask, in);
+    // the last that stays and the first that does not
+    const float last = -warp_max(in ? -score : -INFINITY), next = warp_max(there && !in ? score : -INFINITY);
+    if (size % V == 0) {
+        if (first < p.experts && !(stay >> (first / size) & 1))
+#pragma unroll
+            for (int v = 0; v < V; ++v) key[v] = -INFINITY;
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (first + v < p.experts && !(stay >> ((first + v) / size) & 1)) key[v] = -INFINITY;
+    }
+    return next > -INFINITY && last - next <= key_error(2.0f * *error, last, next);
+}
+
+// kScored: with bias or groups; otherwise the scores' order is the logits'.
+template <typename T, int V, bool kScored>
+__device__ __forceinline__ void route_token(const RouterParams& p, int64_t token, const float (&l)[V], float* scratch, Reach& reach) {
+    const int first = lane_id() * V;
+    const int64_t out = token * p.topk;
+    if (p.token_mask && p.token_mask[token] == 0) {
+        if (lane_id() < p.topk) p.topk_idx[out + lane_id()] = -1, p.topk_weights[out + lane_id()] = 0.0f;
+        return;
+    }
+    float most = 0.0f, sum = 1.0f;
+    if (p.softmax && (kScored || !p.normalize)) softmax_stats<V>(l, &most, &sum);
+    float key[V];
+    float error = 0.0f;
+    bool close = false;
+    if constexpr (kScored) {
+        close = make_keys<V>(p, l, most, sum, scratch, key, &error);
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = l[v];
+    }
+    // the K-th largest of the lanes' largest keys: at least K keys reach it
+    float mine = key[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) mine = fmaxf(mine, key[v]);
+    float bound;
+    int reached = 0;
+    do {
+        bound = warp_max(mine);
+        const bool is = mine == bound;
+        reached += __popc(__ballot_sync(kFullMask, is));
+        mine = is ? -INFINITY : mine;
+    } while (reached < p.topk && bound > -INFINITY);
+    // who reaches it, with the room that 32 bits need
+    if (kScored) bound -= 2.0f * key_error(error, bound, bound);
+    bound = fmaxf(bound, -3.402823466e38f);
+    int count = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) count += key[v] >= bound;
+    int at = count;
+#pragma unroll
+    for (int o = 1; o < kWarpSize; o <<= 1) {
+        const int other = __shfl_up_sync(kFullMask, at, o);
+        if (lane_id() >= o) at += other;
+    }
+    const int all = __shfl_sync(kFullMask, at, kWarpSize - 1);
+    at -= count;
+    int expert = -1, rank = kWarpSize;
+    float lc = -INFINITY;
+    if (!close && all <= kWarpSize) {
+        __syncwarp();  // the last token's have been read
+        if (count)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (key[v] >= bound) {
+                    reach.key_expert[at] = make_float2(key[v], __int_as_float(first + v));
+                    if (kScored) reach.logit[at] = l[v];
+                    ++at;
+                }
+        __syncwarp();
+        const bool there = lane_id() < all;
+        float k = -INFINITY;
+        if (there) {
+            const float2 c = reach.key_expert[lane_id()];
+            k = c.x, expert = __float_as_int(c.y);
+            lc = kScored ? reach.logit[lane_id()] : k;
         }
-        const float mine = unordered(chosen_key), after = __shfl_down_sync(kFullMask, mine, 1);
-        const float l_after = __shfl_down_sync(kFullMask, lc, 1), b_after = __shfl_down_sync(kFullMask, bc, 1);
-        bool near = chosen >= 0 && lane_id() < p.topk - 1 && lane_id() < kWarpSize - 1 && after > -INFINITY &&
-                    mine - after <= error + kSumError * (fabsf(mine) + fabsf(after)) && !(lc == l_after && bc == b_after);
-        if (last_key != 0) {  // all K are there: who is left, next to the last
-            uint32_t best = key[0];
-#pragma unroll
-            for (int v = 1; v < V; ++v) best = max(best, key[v]);
-            const float last = unordered(last_key);
-            const uint32_t border = ordered(last - error - 2.0f * kSumError * fabsf(last));
-            if (__any_sync(kFullMask, best >= border)) {
-                const float l_last = __shfl_sync(kFullMask, lc, p.topk - 1), b_last = __shfl_sync(kFullMask, bc, p.topk - 1);
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (key[v] >= border && key[v] != 0)
-                        near |= !(l[v] == l_last && (p.bias == nullptr || p.bias[first + v] == b_last));
+        int before = 0;
+        for (int j = 0; j < all; ++j) {  // in order of experts
+            const float other = reach.key_expert[j].x;
+            before += other > k || (other == k && j < lane_id());
+        }
+        if (there) rank = before;
+        if constexpr (kScored) {
+            // Neighbours in the order of which one at least is chosen: too close, unless they tie because their inputs are the same.
+            if (there) reach.sorted[rank] = make_float2(k, __int_as_float(lane_id()));
+            __syncwarp();
+            bool near = false;
+            if (rank < p.topk && rank + 1 < all) {
+                const float2 next = reach.sorted[rank + 1];
+                near = k - next.x <= key_error(error, k, next.x);
+                if (near) {
+                    const int j = __float_as_int(next.y), e = __float_as_int(reach.key_expert[j].y);
+                    near = reach.logit[j] != lc || (p.bias && p.bias[e] != p.bias[expert]);
+                }
+            }
+            if (__any_sync(kFullMask, near)) {
+                if (p.softmax) {
+                    close = true;
+                } else {
+                    const double exact = there ? 1.0 / (1.0 + exp(-static_cast<double>(lc))) + (p.bias ? static_cast<double>(p.bias[expert]) : 0.0) : 0.0;
+                    before = 0;
+                    for (int j = 0; j < all; ++j) {
+                        const double other = __shfl_sync(kFullMask, exact, j);
+                        before += other > exact || (other == exact && j < lane_id());
+                    }
+                    if (there) rank = before;
+                }
             }
         }
-        close = __any_sync(kFullMask, near);
     }
-    if (close) chosen = choose_exactly<T, V>(p, token);
+    if (close || all > kWarpSize) {
+        if (!close) {
+            float copy[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) copy[v] = key[v];
+            const Chosen r = choose_in_turn<T, V>(p, token, copy, error, kScored);
+            expert = r.expert;
+            close = r.close;
+        }
+        if (close) expert = choose_exactly<T, V>(p, token);
+        rank = lane_id();
+        lc = expert >= 0 ? logit<T>(p.logits, token * p.experts + expert) : -INFINITY;
+    }
 
-    // lane k: the score of expert k
-    const bool mine = chosen >= 0;
+    const bool chosen = expert >= 0 && rank < p.topk;
     float s = 0.0f;
-    const float lc = mine ? logit<T>(p.logits, token * p.experts + chosen) : -INFINITY;
     if (p.softmax) {
         float base = most;
-        if (p.normalize) base = unordered(__reduce_max_sync(kFullMask, ordered(lc)));  // the sum cancels
-        if (mine) s = expf(lc - base);
-        if (mine && !p.normalize) s /= sum;
-    } else if (mine) {
+        if (p.normalize) base = warp_max(chosen ? lc : -INFINITY);  // the sum cancels
+        if (chosen) s = expf(lc - base);
+        if (chosen && !p.normalize) s /= sum;
+    } else if (chosen) {
         s = 1.0f / (1.0f + expf(-lc));
     }
     float w = s * p.scale;
@@ -370,19 +486,32 @@ __device__ __forceinline__ void route_token(const RouterParams& p, int64_t token
         const float total = warp_sum(s);
         w = total > 0.0f ? s / total * p.scale : 0.0f;
     }
-    if (lane_id() < p.topk) {
-        p.topk_idx[out] = chosen;
-        p.topk_weights[out] = w;
+    if (chosen) {
+        p.topk_idx[out + rank] = expert;
+        p.topk_weights[out + rank] = w;
     }
+    const int found = __popc(__ballot_sync(kFullMask, chosen));
+    if (lane_id() >= found && lane_id() < p.topk) p.topk_idx[out + lane_id()] = -1, p.topk_weights[out + lane_id()] = 0.0f;
 }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) router_kernel(const RouterParams p) {
-    extern __shared__ uint32_t scratch[];  // a warp's keys, where groups cut across lanes
+template <typename T, int V, bool kScored>
+__global__ void __launch_bounds__(kThreads, V <= 8 ? 4 : V <= 16 ? 2 : 1) router_kernel(const RouterParams p) {
+    extern __shared__ float scratch[];  // a warp's keys, where groups cut across lanes
+    __shared__ Reach reach[kWarps];
     pdl_enter();
     const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / kWarpSize; t < p.tokens; t += warps)
-        route_token<T, V>(p, t, scratch + threadIdx.x / kWarpSize * (kWarpSize * V));
+    int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / kWarpSize;
+    if (t >= p.tokens) return;
+    // the next token's logits are on their way while one is worked on
+    float next[V];
+    load_row<T, V>(p, t, next);
+    for (; t < p.tokens; t += warps) {
+        float l[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) l[v] = next[v];
+        if (t + warps < p.tokens) load_row<T, V>(p, t + warps, next);
+        route_token<T, V, kScored>(p, t, l, scratch + threadIdx.x / kWarpSize * (kWarpSize * V), reach[threadIdx.x / kWarpSize]);
+    }
 }
 
 template <typename T>
@@ -444,7 +573,7 @@ __device__ __forceinline__ void route_gradient(const RouterParams& p, int64_t to
         for (int v = 0; v < V; ++v) d[v] = 0.0f;
         float s = 0.0f, rest = 1.0f;  // rest: 1 - s
         if (p.softmax) {
-            const float top = unordered(__reduce_max_sync(kFullMask, ordered(lc)));
+            const float top = warp_max(lc);
             if (mine && lc > -INFINITY) s = expf(lc - top);
         } else if (mine) {
             const float e = expf(-fabsf(lc)), small = e / (1.0f + e), large = 1.0f / (1.0f + e);
@@ -482,23 +611,26 @@ __global__ void __launch_bounds__(kThreads) router_grad_kernel(const RouterParam
         route_gradient<T, V>(p, t);
 }
 
+constexpr int ctas_per_sm(int per_lane) { return per_lane <= 8 ? 4 : per_lane <= 16 ? 2 : 1; }  // of the forward pass: one resident wave
 constexpr int kCtasPerSm = 4;  // that any variant can have resident
 constexpr int kWaves = 8;
 
 template <bool kGrad, typename T, int V>
 cudaError_t start(const ep_handle* h, const RouterParams& p, cudaStream_t stream) {
     const int64_t wanted = (p.tokens + kWarps - 1) / kWarps;
-    const int64_t most = static_cast<int64_t>(h->plan.num_sms) * kCtasPerSm * (h->plan.sm_limited ? 1 : kWaves);
+    const int64_t most = static_cast<int64_t>(h->plan.num_sms) * (kGrad ? kCtasPerSm * (h->plan.sm_limited ? 1 : kWaves) : ctas_per_sm(V));
     const dim3 grid(static_cast<unsigned>(wanted < most ? wanted : most));
     if constexpr (kGrad) return launch_kernel(router_grad_kernel<T, V>, grid, dim3(kThreads), 0, stream, 1, p);
+    if (p.bias == nullptr && p.groups == 1)
+        return launch_kernel(router_kernel<T, V, false>, grid, dim3(kThreads), 0, stream, 1, p);
     const int size = p.experts / p.groups, lanes = size / V;
     const bool cut = p.groups > 1 && (lanes * V != size || (lanes & (lanes - 1)) != 0);
-    const size_t smem = cut ? sizeof(uint32_t) * kThreads * V : 0;
-    if (smem > 48 * 1024) {
-        const cudaError_t err = cudaFuncSetAttribute(router_kernel<T, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const size_t smem = cut ? sizeof(float) * kThreads * V : 0;
+    if (smem > 40 * 1024) {
+        const cudaError_t err = cudaFuncSetAttribute(router_kernel<T, V, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (err != cudaSuccess) return err;
     }
-    return launch_kernel(router_kernel<T, V>, grid, dim3(kThreads), smem, stream, 1, p);
+    return launch_kernel(router_kernel<T, V, true>, grid, dim3(kThreads), smem, stream, 1, p);
 }
 
 template <bool kGrad, typename T>
