@@ -5,10 +5,12 @@
 //   gated       d gate = dy * w * up * act'(gate),  d up = dy * w * act(gate)     d w = sum of dy * act(gate) * up
 // with the row's weight w (1 without), and d bias[e] = the sum of the unrounded d v over the rows of expert e.
 //
-// A CTA takes kChunkRows rows of one group, a warp kWarpRows of them, 256 columns at a time: a lane's sums over its rows
-// stay in registers, its rows' sums over columns in a word of shared memory each.  The warps' column sums are added up
-// through shared memory and go out as one row of partial sums a chunk; a second kernel adds up the chunks of each
-// group in their order.  No atomics: the same input gives the same sums.
+// A CTA takes chunk_rows() rows of one group.  A warp has 256 columns of them, all of its rows, or where there are fewer than
+// 2048 columns every second, third... row: a lane's column sums stay in registers, and what the warps have of the same
+// columns is added up through shared memory once a chunk, as are the rows' sums.  (With rows for each warp and the columns in
+// turn, two barriers for every 256 columns: 69 us for 32672 rows of 1024 gates and ups.)  The column sums go out as one row
+// of partial sums a chunk; a second kernel adds up the chunks of each group in their order.  No atomics: the same
+// input gives the same sums.
 #include "ep_act.cuh"
 #include "ep_groups.cuh"
 #include "ep_handle.h"
@@ -19,10 +21,13 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / kWarpSize;
-constexpr int kWarpRows = 4;
-constexpr int kChunkRows = kWarps * kWarpRows;
+constexpr int kMostChunkRows = 64;
 constexpr int kLaneCols = 8;
 constexpr int kWarpCols = kWarpSize * kLaneCols;
+
+// Rows of a chunk: fewer where there are few rows, so that every SM has some.  By the rows alone: the sums' order is
+// the same whatever the handle may use of the GPU.
+__host__ __device__ inline int chunk_rows(int64_t num_rows) { return num_rows >= 100000 ? kMostChunkRows : num_rows >= 32000 ? 32 : num_rows >= 12000 ? 16 : 8; }
 
 struct ActGradParams {
     Groups groups;
@@ -41,9 +46,11 @@ struct ActGradParams {
 };
 
 // The table of chunks before each group, in shared memory; returns how many there are, -1 where groups overlap.
+template <int THREADS>
 __device__ __forceinline__ int build_chunks(const Groups& groups, int32_t* before, int32_t* begin, int32_t* count,
                                             int64_t* sums, int32_t* status) {
-    const int per = (groups.groups + kThreads - 1) / kThreads;
+    const int each = chunk_rows(groups.num_rows);
+    const int per = (groups.groups + THREADS - 1) / THREADS;
     const int first = threadIdx.x * per, last = min(first + per, groups.groups);
     int64_t chunks = 0, rows = 0, all_chunks = 0, all_rows = 0;
     for (int g = first; g < last; ++g) {
@@ -51,12 +58,12 @@ __device__ __forceinline__ int build_chunks(const Groups& groups, int32_t* befor
         before[g] = static_cast<int32_t>(chunks);
         begin[g] = q.begin;
         count[g] = q.count;
-        chunks += (q.count + kChunkRows - 1) / kChunkRows;
+        chunks += (q.count + each - 1) / each;
         rows += q.count;
     }
-    block_prefix<kThreads>(rows, sums, &all_rows);
+    block_prefix<THREADS>(rows, sums, &all_rows);
     __syncthreads();
-    const int64_t base = block_prefix<kThreads>(chunks, sums, &all_chunks);
+    const int64_t base = block_prefix<THREADS>(chunks, sums, &all_chunks);
     for (int g = first; g < last; ++g) before[g] += static_cast<int32_t>(base);
     __syncthreads();
     if (all_rows > groups.num_rows) {
@@ -67,136 +74,168 @@ __device__ __forceinline__ int build_chunks(const Groups& groups, int32_t* befor
 }
 
 template <int ACT, bool kGated>
-__global__ void __launch_bounds__(kThreads) act_grad_kernel(const ActGradParams p) {
+__global__ void __launch_bounds__(kThreads, 3) act_grad_kernel(const ActGradParams p) {
     constexpr int kParts = kGated ? 2 : 1;
+    constexpr int kRows = kGated ? 2 : 4;  // in flight
     extern __shared__ int32_t table[];
     __shared__ int64_t sums[kWarps];
-    __shared__ float row_sums[kChunkRows][kWarpSize];
+    __shared__ float row_sums[kMostChunkRows][kWarps];
     __shared__ float4 col_sums[kWarps][kParts * kWarpSize * 2];
     const int groups = p.groups.groups;
     int32_t* before = table;
     int32_t* begin = before + groups;
     int32_t* count = begin + groups;
     pdl_enter();
-    const int chunks = build_chunks(p.groups, before, begin, count, sums, p.status);
+    const int chunks = build_chunks<kThreads>(p.groups, before, begin, count, sums, p.status);
     const int warp = threadIdx.x / kWarpSize;
-    const int n = kParts * p.width;
+    const int n = kParts * p.width, each = chunk_rows(p.groups.num_rows);
     const int64_t half = 2 * static_cast<int64_t>(p.width);  // bytes from gate to up
+    const int blocks = (p.width + kWarpCols - 1) / kWarpCols;  // of columns
+    const int across = min(blocks, kWarps), turns = kWarps / across;  // warps side by side, and sharing rows
+    const int mine = warp / across, block0 = warp % across;
     for (int chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x) {
         const int g = find_group(before, groups, chunk);
-        const int in_group = (chunk - before[g]) * kChunkRows + warp * kWarpRows;
-        const int rows = min(kWarpRows, count[g] - in_group);
+        const int in_group = (chunk - before[g]) * each;
+        const int rows = min(each, count[g] - in_group);
         const int64_t row0 = static_cast<int64_t>(begin[g]) + in_group;
-#pragma unroll
-        for (int r = 0; r < kWarpRows; ++r) row_sums[warp * kWarpRows + r][lane_id()] = 0.0f;
-        for (int c0 = 0; c0 < p.width; c0 += kWarpCols) {
-            const int col = c0 + lane_id() * kLaneCols;
+        for (int block = block0; mine < turns && block < blocks; block += across) {
+            const int col = block * kWarpCols + lane_id() * kLaneCols;
             const bool in = col < p.width;
-            float acc[kParts][kLaneCols];
+            float2 acc[kParts][kLaneCols / 2];
 #pragma unroll
             for (int i = 0; i < kParts; ++i)
 #pragma unroll
-                for (int j = 0; j < kLaneCols; ++j) acc[i][j] = 0.0f;
-#pragma unroll 2
-            for (int r = 0; r < rows; ++r) {
-                if (!in) break;
-                const int64_t row = row0 + r;
-                const int4 d4 = ld_stream_v4(reinterpret_cast<const int4*>(p.dy + row * p.dy_row_bytes + 2 * col));
-                int4 v4 = make_int4(0, 0, 0, 0), u4 = v4;
-                if (p.pre) {
-                    const uint8_t* pre = p.pre + row * p.pre_row_bytes + 2 * col;
-                    v4 = ld_stream_v4(reinterpret_cast<const int4*>(pre));
-                    if (kGated) u4 = ld_stream_v4(reinterpret_cast<const int4*>(pre + half));
-                }
-                const float w = p.row_weights ? __ldg(p.row_weights + row) : 1.0f;
-                float d[8], v[8], u[8], dv[8], du[8];
-                unpack8(d4, d);
-                unpack8(v4, v);
-                if (kGated) unpack8(u4, u);
-                float dot = 0.0f;
+                for (int j = 0; j < kLaneCols / 2; ++j) acc[i][j] = both(0.0f);
+            for (int r0 = mine; r0 < rows; r0 += kRows * turns) {
+                int4 d4[kRows], v4[kRows], u4[kRows];
+                float w[kRows];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float2 a = activate_with_slope(ACT, v[j]);
-                    const float dw = d[j] * w;
-                    dv[j] = kGated ? dw * u[j] * a.y : dw * a.y;
-                    dot += kGated ? d[j] * a.x * u[j] : d[j] * a.x;
-                    acc[0][j] += dv[j];
-                    if (kGated) du[j] = dw * a.x, acc[kParts - 1][j] += du[j];
+                for (int i = 0; i < kRows; ++i) {
+                    const int64_t row = row0 + r0 + i * turns;
+                    d4[i] = v4[i] = u4[i] = make_int4(0, 0, 0, 0);
+                    w[i] = 1.0f;
+                    if (r0 + i * turns < rows && in) {
+                        d4[i] = ld_stream_v4(reinterpret_cast<const int4*>(p.dy + row * p.dy_row_bytes + 2 * col));
+                        if (p.pre) {
+                            const uint8_t* pre = p.pre + row * p.pre_row_bytes + 2 * col;
+                            v4[i] = ld_stream_v4(reinterpret_cast<const int4*>(pre));
+                            if (kGated) u4[i] = ld_stream_v4(reinterpret_cast<const int4*>(pre + half));
+                        }
+                        if (p.row_weights) w[i] = __ldg(p.row_weights + row);
+                    }
                 }
-                if (p.d_pre) {
-                    uint8_t* out = p.d_pre + row * p.d_pre_row_bytes + 2 * col;
-                    st_stream_v4(reinterpret_cast<int4*>(out), pack8_bf16(dv));
-                    if (kGated) st_stream_v4(reinterpret_cast<int4*>(out + half), pack8_bf16(du));
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) {
+                    const int r = r0 + i * turns;
+                    if (r >= rows) break;
+                    float d[8], v[8], u[8], dv[8], du[8];
+                    unpack8(d4[i], d);
+                    unpack8(v4[i], v);
+                    if (kGated) unpack8(u4[i], u);
+                    float2 dot = both(0.0f);
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2) {
+                        float2 slope;
+                        const float2 a = activate_with_slope(ACT, make_float2(v[j], v[j + 1]), &slope);
+                        const float2 dd = make_float2(d[j], d[j + 1]), dw = __fmul2_rn(dd, both(w[i]));
+                        float2 one = __fmul2_rn(dw, slope), value = a;
+                        if (kGated) {
+                            const float2 uu = make_float2(u[j], u[j + 1]), two = __fmul2_rn(dw, a);
+                            one = __fmul2_rn(one, uu);
+                            value = __fmul2_rn(a, uu);
+                            du[j] = two.x, du[j + 1] = two.y;
+                            acc[kParts - 1][j / 2] = __fadd2_rn(acc[kParts - 1][j / 2], two);
+                        }
+                        dot = __ffma2_rn(dd, value, dot);
+                        dv[j] = one.x, dv[j + 1] = one.y;
+                        acc[0][j / 2] = __fadd2_rn(acc[0][j / 2], one);
+                    }
+                    if (p.d_pre && in) {
+                        uint8_t* out = p.d_pre + (row0 + r) * p.d_pre_row_bytes + 2 * col;
+                        st_stream_v4(reinterpret_cast<int4*>(out), pack8_bf16(dv));
+                        if (kGated) st_stream_v4(reinterpret_cast<int4*>(out + half), pack8_bf16(du));
+                    }
+                    if (p.d_row_weights) {
+                        float s = dot.x + dot.y;
+#pragma unroll
+                        for (int o = kWarpSize / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kFullMask, s, o);
+                        if (lane_id() == 0) row_sums[r][block0] = block == block0 ? s : row_sums[r][block0] + s;
+                    }
                 }
-                row_sums[warp * kWarpRows + r][lane_id()] += dot;
             }
             if (p.partial) {
 #pragma unroll
                 for (int i = 0; i < kParts; ++i) {
-                    col_sums[warp][(i * 2 + 0) * kWarpSize + lane_id()] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-                    col_sums[warp][(i * 2 + 1) * kWarpSize + lane_id()] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
-                }
-                __syncthreads();
-                // thread: four columns of a part
-                for (int i = threadIdx.x; i < kParts * 2 * kWarpSize; i += kThreads) {
-                    float4 s = col_sums[0][i];
-#pragma unroll
-                    for (int w = 1; w < kWarps; ++w) {
-                        const float4 t = col_sums[w][i];
-                        s.x += t.x, s.y += t.y, s.z += t.z, s.w += t.w;
+                    const float4 low = make_float4(acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y);
+                    const float4 high = make_float4(acc[i][2].x, acc[i][2].y, acc[i][3].x, acc[i][3].y);
+                    if (turns > 1) {
+                        col_sums[warp][i * 2 * kWarpSize + 2 * lane_id()] = low;
+                        col_sums[warp][i * 2 * kWarpSize + 2 * lane_id() + 1] = high;
+                    } else if (in) {
+                        float4* to = reinterpret_cast<float4*>(p.partial + static_cast<int64_t>(chunk) * n + static_cast<int64_t>(i) * p.width + col);
+                        to[0] = low, to[1] = high;
                     }
-                    const int part = i / (2 * kWarpSize), quad = i / kWarpSize % 2, c = c0 + (i % kWarpSize) * kLaneCols + 4 * quad;
-                    if (c < p.width)
-                        *reinterpret_cast<float4*>(p.partial + static_cast<int64_t>(chunk) * n + static_cast<int64_t>(part) * p.width + c) = s;
                 }
-                __syncthreads();
             }
         }
-        if (p.d_row_weights) {
-            __syncwarp();
-#pragma unroll
-            for (int r = 0; r < kWarpRows; ++r) {
-                float s = row_sums[warp * kWarpRows + r][lane_id()];
-#pragma unroll
-                for (int o = kWarpSize / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kFullMask, s, o);
-                if (lane_id() == 0 && r < rows) p.d_row_weights[row0 + r] = s;
+        if ((p.partial && turns > 1) || p.d_row_weights) {
+            __syncthreads();
+            if (p.partial && turns > 1)
+                for (int i = threadIdx.x; i < kParts * across * 2 * kWarpSize; i += kThreads) {  // four columns of a part
+                    const int part = i / (across * 2 * kWarpSize), quad = i % (across * 2 * kWarpSize), w = quad / (2 * kWarpSize);
+                    float4 s = col_sums[w][part * 2 * kWarpSize + quad % (2 * kWarpSize)];
+                    for (int k = 1; k < turns; ++k) {
+                        const float4 t = col_sums[k * across + w][part * 2 * kWarpSize + quad % (2 * kWarpSize)];
+                        s.x += t.x, s.y += t.y, s.z += t.z, s.w += t.w;
+                    }
+                    if (4 * quad < p.width)
+                        *reinterpret_cast<float4*>(p.partial + static_cast<int64_t>(chunk) * n + static_cast<int64_t>(part) * p.width + 4 * quad) = s;
+                }
+            if (p.d_row_weights && static_cast<int>(threadIdx.x) < rows) {
+                float s = row_sums[threadIdx.x][0];
+                for (int k = 1; k < across; ++k) s += row_sums[threadIdx.x][k];
+                p.d_row_weights[row0 + threadIdx.x] = s;
             }
+            __syncthreads();
         }
     }
 }
 
-// d bias: the chunks' rows of partial sums, added up for each group.  A CTA has 128 columns of one group, a warp every
-// kWarps-th chunk of it.
-__global__ void __launch_bounds__(kThreads) bias_sum_kernel(const ActGradParams p, int n) {
+// d bias: the chunks' rows of partial sums, added up for each group.  A CTA has 128 columns of one group, a warp
+// every kSumWarps-th chunk of it: many warps where few CTAs have something to do (1 group of 32672 rows, 512 columns: 24 us for
+// eight warps, 11 for 32; 32 groups of 1021 rows, 2048 columns: 7 and 19).
+template <int kSumThreads>
+__global__ void __launch_bounds__(kSumThreads) bias_sum_kernel(const ActGradParams p, int n) {
+    constexpr int kSumWarps = kSumThreads / kWarpSize;
     extern __shared__ int32_t table[];
-    __shared__ int64_t sums[kWarps];
-    __shared__ float4 col_sums[kWarps][kWarpSize];
+    __shared__ int64_t sums[kSumWarps];
+    __shared__ float4 col_sums[kSumWarps][kWarpSize];
     const int groups = p.groups.groups;
     int32_t* before = table;
     int32_t* begin = before + groups;
     int32_t* count = begin + groups;
     pdl_enter();
-    if (build_chunks(p.groups, before, begin, count, sums, p.status) < 0) return;
-    const int warp = threadIdx.x / kWarpSize;
+    if (build_chunks<kSumThreads>(p.groups, before, begin, count, sums, p.status) < 0) return;
+    const int warp = threadIdx.x / kWarpSize, each = chunk_rows(p.groups.num_rows);
     const int blocks = (n + 4 * kWarpSize - 1) / (4 * kWarpSize);
     for (int64_t item = blockIdx.x; item < static_cast<int64_t>(groups) * blocks; item += gridDim.x) {
         const int g = static_cast<int>(item / blocks);
         const int col = static_cast<int>(item % blocks) * 4 * kWarpSize + 4 * lane_id();
-        const int chunks = (count[g] + kChunkRows - 1) / kChunkRows;
+        const int chunks = (count[g] + each - 1) / each;
         const float* from = p.partial + static_cast<int64_t>(before[g]) * n + col;
         float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (col < n) {
 #pragma unroll 4
-            for (int c = warp; c < chunks; c += kWarps) {
+            for (int c = warp; c < chunks; c += kSumWarps) {
                 const float4 t = *reinterpret_cast<const float4*>(from + static_cast<int64_t>(c) * n);
                 s.x += t.x, s.y += t.y, s.z += t.z, s.w += t.w;
             }
         }
         col_sums[warp][lane_id()] = s;
         __syncthreads();
+        const int used = min(chunks, kSumWarps);
         if (warp == 0 && col < n) {
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) {
+            for (int w = 1; w < used; ++w) {
                 const float4 t = col_sums[w][lane_id()];
                 s.x += t.x, s.y += t.y, s.z += t.z, s.w += t.w;
             }
@@ -208,7 +247,7 @@ __global__ void __launch_bounds__(kThreads) bias_sum_kernel(const ActGradParams 
 
 size_t table_bytes(int groups) { return 3 * sizeof(int32_t) * static_cast<size_t>(groups); }
 
-int64_t most_chunks(int64_t num_rows, int groups) { return num_rows / kChunkRows + groups; }
+int64_t most_chunks(int64_t num_rows, int groups) { return num_rows / chunk_rows(num_rows) + groups; }
 
 template <int ACT, bool kGated>
 cudaError_t start(const ep_handle* h, const ActGradParams& p, cudaStream_t stream) {
@@ -291,8 +330,10 @@ ep_status ep_act_grad(ep_handle* h, int64_t num_rows, int32_t n, const int32_t* 
     if (err == cudaSuccess && d_bias) {
         const int64_t wanted = static_cast<int64_t>(h->cfg.num_experts) * ((n + 4 * kWarpSize - 1) / (4 * kWarpSize));
         const int64_t most = static_cast<int64_t>(h->plan.num_sms) * (h->plan.sm_limited ? 4 : 16);
-        err = launch_kernel(bias_sum_kernel, dim3(static_cast<unsigned>(wanted < most ? wanted : most)), dim3(kThreads),
-                            table_bytes(h->cfg.num_experts), stream, 1, p, n);
+        const dim3 grid(static_cast<unsigned>(wanted < most ? wanted : most));
+        const size_t table = table_bytes(h->cfg.num_experts);
+        err = wanted >= 256 ? launch_kernel(bias_sum_kernel<256>, grid, dim3(256), table, stream, 1, p, n)
+                            : launch_kernel(bias_sum_kernel<1024>, grid, dim3(1024), table, stream, 1, p, n);
     }
     if (err != cudaSuccess) return cuda_fail(err, "activation gradient launch");
     return EP_OK;

@@ -717,6 +717,15 @@ __device__ __forceinline__ void add_bias(const float4& bias, int c, float (&v)[3
     }
 }
 
+template <int ACT>
+__device__ __forceinline__ void activate_columns(float (&v)[32]) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+        const float2 a = activate(ACT, make_float2(v[i], v[i + 1]));
+        v[i] = a.x, v[i + 1] = a.y;
+    }
+}
+
 // The epilogue of 32 output columns of a lane's row, from column `c` of its warp's part of the tile: v holds the sums
 // (gated: of the gates, and `up` of the ups) and gets what is written.  False: the wait for the residual was given up.
 template <int FORM>
@@ -736,18 +745,9 @@ __device__ __forceinline__ bool finish_columns(const Roles& x, const Place& at, 
         if (FORM == kGated) store_bf16(pre + 2 * static_cast<int64_t>(p.cols_dim), col, p.cols_dim, up, p.pre_wide != 0);
     }
     switch (p.act) {  // the same for all: a loop each, not a choice for each value
-        case EP_ACT_RELU:
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = activate(EP_ACT_RELU, v[i]);
-            break;
-        case EP_ACT_SILU:
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = activate(EP_ACT_SILU, v[i]);
-            break;
-        case EP_ACT_GELU:
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = activate(EP_ACT_GELU, v[i]);
-            break;
+        case EP_ACT_RELU: activate_columns<EP_ACT_RELU>(v); break;
+        case EP_ACT_SILU: activate_columns<EP_ACT_SILU>(v); break;
+        case EP_ACT_GELU: activate_columns<EP_ACT_GELU>(v); break;
         default: break;
     }
     if (FORM == kGated) {
@@ -1123,6 +1123,14 @@ bool wgrad_on_pairs(const ep_handle* h, const GemmParams& p) {
 // Forms that read rows in words of four bytes.
 constexpr bool has_words(int form) { return form != kWeightGrad && !has_epilogue(form); }
 
+// Whether a product with an epilogue has a tile for every pair of CTAs.  With fewer, as for a router's few columns, single
+// CTAs take twice as many narrower ones.
+template <int FORM>
+bool fills_pairs(const GemmParams& p, int64_t rows_each, int pairs) {
+    constexpr int64_t kRows = 2 * kTileRows, kCols = FORM == kGated ? kColBox : 2 * kColBox;
+    return p.groups.groups * ((rows_each + kRows - 1) / kRows) * ((p.cols_dim + kCols - 1) / kCols) >= pairs;
+}
+
 template <int FORM>
 cudaError_t plan_form(LaunchPlan* plan) {
     cudaError_t err = cudaFuncSetAttribute(grouped_gemm_kernel<FORM, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
@@ -1179,7 +1187,7 @@ ep_status launch(ep_handle* h, const Operand& a, const Operand& a_small, const O
     Maps m;
     const bool pairs = FORM == kWeightGrad ? wgrad_on_pairs(h, p)
                                            : !p.a_words && rows_each >= (FORM == kFp8 ? kPairRowsFp8 : kTileRows + 1) &&
-                                                 most_pairs > 0;
+                                                 most_pairs > 0 && (!has_epilogue(FORM) || fills_pairs<FORM>(p, rows_each, most_pairs));
     // A tile's stages wait for their operands, and a tile is worth the rows that a CTA loads beside its columns: a pair's
     // 128 beside half of the columns (weight gradient of 8 experts, 560 x 2448, 83592 rows: 401 us with 32 columns'
     // worth, 257 with 128, 246 with 256), a single CTA's as many as a group's tiles have, at least one load's (FP8, 64

@@ -582,7 +582,7 @@ __device__ __forceinline__ uint64_t unseen(uint64_t bits) {
 // bf16, as the second product's operand is.
 __device__ __forceinline__ void put_act(const LayerParams& p, int64_t act_row, int col, float gate, float up) {
     if (col < p.width)
-        *reinterpret_cast<__nv_bfloat16*>(p.act + 2 * (act_row * p.width + col)) = __float2bfloat16_rn(activate(EP_ACT_SILU, gate) * up);
+        *reinterpret_cast<__nv_bfloat16*>(p.act + 2 * (act_row * p.width + col)) = __float2bfloat16_rn(activate(EP_ACT_SILU, both(gate)).x * up);
 }
 
 // Eight warps of the first kernel: accumulators to silu(gate) * up.  Four have the tile's gates, four its ups, each 32 rows and

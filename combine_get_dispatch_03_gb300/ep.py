@@ -223,6 +223,7 @@ class Handle:
             _raise(lib().ep_handle_create(ctypes.byref(cfg.c()), ctypes.byref(self._ptr)))
         self.normal_tokens = None
         self.ll_tokens = None
+        self._scratch = {}  # raw stream -> workspace of the calls on it
 
     @property
     def ptr(self):
@@ -619,6 +620,24 @@ def _out(shape, dtype, h, stream):
         return torch.empty(*shape, dtype=dtype, device=h.device)
 
 
+_capturing = torch.cuda.is_current_stream_capturing
+
+
+def _scratch(h, nbytes, stream):
+    """The address of a workspace of nbytes for a call, and what keeps it alive until the call is enqueued.
+
+    The handle keeps one for each stream that was current in a call, for calls on one stream run in their order.  A captured
+    call gets its own from the graph's memory, a call with a stream of its own from that stream's."""
+    if stream is not None or _capturing():
+        t = _out((max(16, nbytes),), torch.uint8, h, stream)
+        return t.data_ptr(), t
+    key = _stream(None, h.device)
+    t = h._scratch.get(key)
+    if t is None or t.numel() < nbytes:
+        t = h._scratch[key] = torch.empty(max(16, nbytes), dtype=torch.uint8, device=h.device)
+    return t.data_ptr(), t
+
+
 def _out_rows(out, name, x, rows, width, dtype, h, stream):
     """(out, address, row stride in bytes) of the rows that a call writes: checked, or allocated with x's leading axes."""
     if out is not None:
@@ -724,16 +743,17 @@ def ep_act_grad(h: Handle, dy: torch.Tensor, pre, group_count, group_begin=None,
         d_row_weights = _out((rows,), torch.float32, h, stream)
     if with_bias and d_bias is None:
         d_bias = _out((E, n), torch.float32, h, stream)
-    work, work_bytes = None, 0
+    work, work_bytes, keep = None, 0, None
     if d_bias is not None:
         work_bytes = lib().ep_act_grad_workspace(h.ptr, rows, n)
-        work = _out((max(16, work_bytes),), torch.uint8, h, stream)
+        work, keep = _scratch(h, work_bytes, stream)
     cnt, beg = _group_arrays(h, group_count, group_begin)
     _raise(lib().ep_act_grad(
         h.ptr, rows, n, cnt, beg, yp, ys, pp, ps, _choice(act, ACTS, "act"), int(bool(gated)),
         _ptr(row_weights, "row_weights", torch.float32, (rows,), d), gp, gs,
         _ptr(d_row_weights, "d_row_weights", torch.float32, (rows,), d), _ptr(d_bias, "d_bias", torch.float32, (E, n), d),
-        None if work is None else work.data_ptr(), work_bytes, _stream(stream, d)))
+        work, work_bytes, _stream(stream, d)))
+    del keep
     return dict(d_pre=d_pre, d_row_weights=d_row_weights, d_bias=d_bias)
 
 
@@ -910,17 +930,21 @@ def ep_router(h: Handle, logits: torch.Tensor, bias=None, token_mask=None, score
     of experts stay; normalize divides by the chosen scores' sum.  token_mask (bool [...]) is False for tokens without experts."""
     d, K = h.device, h.cfg.num_topk
     tokens, lp, dtype = _logits(h, logits)
-    shape = tuple(logits.shape[:-1]) + (K,)
+    shape = (*logits.shape[:-1], K)
     if topk_idx is None:
         topk_idx = _out(shape, torch.int64, h, stream)
+        ip = topk_idx.data_ptr() if tokens else _dummy(d).data_ptr()
+    else:
+        ip = _ptr(topk_idx, "topk_idx", torch.int64, shape, d)
     if topk_weights is None:
         topk_weights = _out(shape, torch.float32, h, stream)
+        wp = topk_weights.data_ptr() if tokens else _dummy(d).data_ptr()
+    else:
+        wp = _ptr(topk_weights, "topk_weights", torch.float32, shape, d)
     _raise(lib().ep_router(
         h.ptr, tokens, lp, dtype, _ptr(bias, "bias", torch.float32, (h.cfg.num_experts,), d),
         _ptr(token_mask, "token_mask", torch.bool, shape[:-1], d), _choice(score, SCORES, "score"), num_groups,
-        num_groups if kept_groups is None else kept_groups, int(bool(normalize)), scale,
-        _ptr(topk_idx, "topk_idx", torch.int64, shape, d), _ptr(topk_weights, "topk_weights", torch.float32, shape, d),
-        _stream(stream, d)))
+        num_groups if kept_groups is None else kept_groups, int(bool(normalize)), scale, ip, wp, _stream(stream, d)))
     return dict(topk_idx=topk_idx, topk_weights=topk_weights)
 
 
@@ -960,8 +984,11 @@ def ep_moe_layer(h: Handle, x: torch.Tensor, topk_idx: torch.Tensor, topk_weight
     xp = _ptr(x, "x", torch.bfloat16, (R, T, H), d)
     if out is None:
         out = _out((R, T, H), torch.bfloat16, h, stream)
+        op = out.data_ptr() if T else _dummy(d).data_ptr()
+    else:
+        op = _ptr(out, "out", torch.bfloat16, (R, T, H), d)
     work_bytes = lib().ep_moe_layer_workspace(h.ptr, T, I)  # -1: more tokens than the layer takes, which the call reports
-    work = _out((max(16, work_bytes),), torch.uint8, h, stream)
+    work, keep = _scratch(h, work_bytes, stream)
     _raise(lib().ep_moe_layer(
         h.ptr, T, I, xp, _ptr(topk_idx, "topk_idx", torch.int64, (R, T, K), d),
         _ptr(topk_weights, "topk_weights", torch.float32, (R, T, K), d), _ptr(w_up, "w_up", w_up.dtype, (E, 2 * I, H), d),
@@ -969,7 +996,8 @@ def ep_moe_layer(h: Handle, x: torch.Tensor, topk_idx: torch.Tensor, topk_weight
         _ptr(w_down, "w_down", w_up.dtype, (E, H, I), d),
         _ptr(down_scales, "down_scales", torch.float32, (E, H // 128, I // 128), d), EP_FP8_E4M3 if fp8 else EP_BF16,
         _ptr(bias_0, "bias_0", torch.bfloat16, (R, T, H), d), _ptr(bias_1, "bias_1", torch.bfloat16, (R, T, H), d),
-        _ptr(out, "out", torch.bfloat16, (R, T, H), d), work.data_ptr(), work_bytes, _stream(stream, d)))
+        op, work, work_bytes, _stream(stream, d)))
+    del keep
     return out
 
 
