@@ -167,12 +167,12 @@ ep_status ep_handle_create(const ep_config* cfg, ep_handle** out) {
     const size_t sizes[] = {1, R * R, R * R * C, R * R * C, R, R * cap, R * T * R, R * T * K, R * E, R,
                             R * NN * C, R * NN, 2, scan_words,
                             cap ? static_cast<size_t>(ep::layout_chunks(*cfg)) * E : 0, R,
-                            2 * static_cast<size_t>(h->plan.num_sms)};
+                            2 * static_cast<size_t>(h->plan.num_sms), 8 * static_cast<size_t>(h->plan.num_sms)};
     int32_t** slots[] = {&h->status,   &h->rank_prefix,  &h->channel_prefix, &h->recv_channel_prefix,
                          &h->num_recv, &h->recv_src_idx, &h->send_head,      &h->ll_slot,
                          &h->ll_cnt,   &h->rank_mask,    &h->rdma_channel_prefix, &h->recv_rdma_rank_prefix,
                          &h->claims,   &h->layout_scratch, &h->expert_counts, &h->layout_tickets,
-                         &h->layer_tickets};
+                         &h->layer_tickets, &h->part_tickets};
     size_t total = 0;
     for (size_t s : sizes) total += align_up(s * sizeof(int32_t), 256);
     err = cudaMalloc(&h->dmem, total);

@@ -112,6 +112,9 @@ constexpr int kMaxStages = 12;
 constexpr int kEpilogueWarps = 8;
 constexpr int kGemmThreads = (4 + kEpilogueWarps) * kWarpSize;  // warps 0 to 3 for loads and products: registers go by four warps
 constexpr int kControlBytes = 704;  // static shared memory
+constexpr int kLeastPartSteps = 8;
+constexpr int kMostParts = 8;
+constexpr int kPartFloats = 128 * kWarpSize;  // a warp's sums of a part: 128 columns at most
 constexpr uint32_t kOutBox = 32 * kRowBytes;  // a warp's results on their way out: 32 rows of 128 bytes
 // Of them a warp: in FP8 one for each 64 columns, since there a tile's stores hold up the next one's sums (2048 rows an
 // expert, 7168 x 2048: 1740 us with one, 1682 with two).
@@ -148,6 +151,8 @@ struct GemmParams {
     int64_t pre_row_bytes;
     int32_t pre_wide;           // its rows are 32-byte aligned
     int32_t act;
+    float* parts;               // where parts of a contraction meet: [tile][part][warp][column][lane], or NULL: it is not cut
+    int32_t* tickets;           // [tile][warp], 0
 };
 
 // Tensor maps of the two operands: loads of kBox output elements, and smaller ones; and of the results, boxes of 32
@@ -183,13 +188,15 @@ struct Control {
     int32_t abort_flag;
     int64_t warp_sums[kGemmThreads / kWarpSize];
     int64_t warp_rows[kGemmThreads / kWarpSize];
-    int32_t tiles, col_tiles, tile_cols;  // output tiles in all, tiles across, columns of one
+    int32_t tiles, col_tiles, tile_cols;  // output tiles in all (parts of them), tiles across, columns of one
+    int32_t parts, part_steps;            // of a tile's contraction, and steps of one
     Place at[kEpilogueWarps];             // forms with segments: of the tile that a warp is adding up
 };
 static_assert(sizeof(Control) <= kControlBytes, "control block");
 
 struct Tile {
     int group, row0, rows, m0, n0, cols, steps;  // rows: valid rows of the group; m0: tile's first row in the group
+    int step0, tile;                             // parts: the first step, the tile
 };
 
 // The group table in shared memory.
@@ -208,6 +215,12 @@ constexpr int min_cols() { return kColBox * (FORM == kGated ? 2 : CG); }
 template <int FORM, int CG>
 __device__ __forceinline__ Tile decode(const Table& t, const GemmParams& p, const Control& ctl, int tile) {
     Tile r;
+    int part = 0;
+    if constexpr (has_epilogue(FORM)) {
+        part = tile % ctl.parts;
+        tile /= ctl.parts;
+    }
+    r.tile = tile;
     const int lo = find_group(t.before, p.groups.groups, tile / ctl.col_tiles);
     const int in = tile - t.before[lo] * ctl.col_tiles;
     const int row_tiles = t.before[lo + 1] - t.before[lo];
@@ -223,6 +236,11 @@ __device__ __forceinline__ Tile decode(const Table& t, const GemmParams& p, cons
     if constexpr (FORM == kWeightGrad) r.steps = (r.rows + 63) >> 6;
     else if constexpr (FORM == kFp8) r.steps = (p.contraction + 127) >> 7;
     else r.steps = (p.contraction + 63) >> 6;
+    r.step0 = 0;
+    if constexpr (has_epilogue(FORM)) {
+        r.step0 = part * ctl.part_steps;
+        r.steps = min(ctl.part_steps, r.steps - r.step0);
+    }
     return r;
 }
 
@@ -268,15 +286,35 @@ __device__ __forceinline__ void build_table(const Table& t, const GemmParams& p,
         const int workers = gridDim.x / CG;
         int best = kMaxTileCols;
         int64_t best_cost = INT64_MAX;
+        const int steps = (p.contraction + 63) >> 6;  // forms with an epilogue
+        ctl.parts = 1;
+        ctl.part_steps = steps;
         for (int cols = kMaxTileCols; cols >= min_cols<FORM, CG>(); cols >>= 1) {
             const int across = out_cols<FORM>(cols);
-            const int64_t tiles = static_cast<int64_t>(total) * ((p.cols_dim + across - 1) / across);
-            const int64_t cost = (tiles + workers - 1) / workers * (cols + p.tile_overhead);
-            if (cost < best_cost) best_cost = cost, best = cols;
+            if constexpr (has_epilogue(FORM)) {
+                // (in 32 bits: there are fewer than 2^30 tiles, and one thread divides while all wait)
+                const uint32_t tiles = static_cast<uint32_t>(total) * ((p.cols_dim + across - 1) / across);
+                const uint32_t each = cols + p.tile_overhead, waves = (tiles + workers - 1) / workers;
+                int64_t cost = static_cast<int64_t>(waves) * each * steps;
+                if (cost < best_cost) best_cost = cost, best = cols, ctl.parts = 1, ctl.part_steps = steps;
+                // With few tiles, parts of the contraction, one wave of them: what they cost to meet is worth about 1500 and 250
+                // a part (steps of a column).
+                if (p.parts == nullptr || tiles == 0) continue;
+                const int most = min(min(workers / static_cast<int>(tiles), steps / kLeastPartSteps), kMostParts);
+                for (int parts = 2; parts <= most; ++parts) {
+                    const int part_steps = (steps + parts - 1) / parts;
+                    cost = static_cast<int64_t>(part_steps) * each + 1500 + 250 * parts;
+                    if (cost < best_cost) best_cost = cost, best = cols, ctl.part_steps = part_steps, ctl.parts = (steps + part_steps - 1) / part_steps;
+                }
+            } else {
+                const int64_t tiles = static_cast<int64_t>(total) * ((p.cols_dim + across - 1) / across);
+                const int64_t cost = (tiles + workers - 1) / workers * (cols + p.tile_overhead);
+                if (cost < best_cost) best_cost = cost, best = cols;
+            }
         }
         ctl.tile_cols = best;
         ctl.col_tiles = (p.cols_dim + out_cols<FORM>(best) - 1) / out_cols<FORM>(best);
-        ctl.tiles = total * ctl.col_tiles;
+        ctl.tiles = total * ctl.col_tiles * ctl.parts;
     }
 }
 
@@ -404,7 +442,7 @@ __device__ __forceinline__ void load_operands(const Roles& x) {
                 }
             } else {
                 bar_arrive_expect_tx<CG>(bar, bytes);
-                const int k0 = s * (FORM == kFp8 ? 128 : 64);
+                const int k0 = (q.step0 + s) * (FORM == kFp8 ? 128 : 64);
                 if (small_boxes == 0) {
                     if (!kWords && rows_here > 0) tma_load_2d<CG>(a, &x.maps.a, k0, q.row0 + my_m0, bar);
                 } else if (!kWords) {
@@ -717,6 +755,39 @@ __device__ __forceinline__ void add_bias(const float4& bias, int c, float (&v)[3
     }
 }
 
+// After a warp's sums of a part of a tile are written: whether they are the last of the tile's, and all may be read.  Each
+// warp of a CTA meets its like in the others, so that the CTA does not wait.
+__device__ __forceinline__ bool last_part(const GemmParams& p, int meeting, int parts) {
+    __threadfence();
+    __syncwarp();
+    int before = 0;
+    if (lane_id() == 0) {
+        before = atomicAdd(p.tickets + meeting, 1);
+        if (before == parts - 1) p.tickets[meeting] = 0;  // for the next call
+        __threadfence();
+    }
+    return __shfl_sync(kFullMask, before, 0) == parts - 1;
+}
+
+// 32 columns from c of a warp's sums, the parts in their order, two on their way at a time.
+__device__ __forceinline__ void sum_parts(const GemmParams& p, int meeting, int parts, int c, float (&v)[32]) {
+    const float* from = p.parts + static_cast<int64_t>(meeting) * parts * kPartFloats + c * kWarpSize + lane_id();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __ldcg(from + i * kWarpSize);
+    for (int k = 1; k < parts; k += 2) {
+        float one[32], two[32];
+        from += kPartFloats;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) one[i] = __ldcg(from + i * kWarpSize);
+        const bool more = k + 1 < parts;
+        if (more) from += kPartFloats;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) two[i] = more ? __ldcg(from + i * kWarpSize) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = v[i] + one[i] + two[i];
+    }
+}
+
 template <int ACT>
 __device__ __forceinline__ void activate_columns(float (&v)[32]) {
 #pragma unroll
@@ -798,18 +869,22 @@ __device__ __forceinline__ void put_sums(const Roles& x, uint32_t box, const Pla
     }
 }
 
-// The same after their epilogue, by stores of each lane.
+// The same after their epilogue, by stores of each lane; meeting >= 0: of a tile's parts, from there.
 template <int FORM>
-__device__ __forceinline__ bool put_finished(const Roles& x, const Place& at, Ahead<FORM>& ahead, const uint64_t (&acc)[2][32]) {
+__device__ __forceinline__ bool put_finished(const Roles& x, const Place& at, Ahead<FORM>& ahead, const uint64_t (&acc)[2][32], int meeting) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         if (32 * c >= at.cols) break;
         float v[32];
+        if (meeting >= 0) {
+            sum_parts(x.p, meeting, x.ctl.parts, 32 * c, v);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const uint64_t pair = acc[c / 2][c % 2 * 16 + i];
-            v[2 * i] = __uint_as_float(static_cast<uint32_t>(pair));
-            v[2 * i + 1] = __uint_as_float(static_cast<uint32_t>(pair >> 32));
+            for (int i = 0; i < 16; ++i) {
+                const uint64_t pair = acc[c / 2][c % 2 * 16 + i];
+                v[2 * i] = __uint_as_float(static_cast<uint32_t>(pair));
+                v[2 * i + 1] = __uint_as_float(static_cast<uint32_t>(pair >> 32));
+            }
         }
         if (!finish_columns<FORM>(x, at, 32 * c, ahead, v, v)) return false;
         put_columns<FORM, false>(x, 0, at, 32 * c, v);
@@ -834,8 +909,15 @@ __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
     uint32_t acc_phase = 0;
     bool ok = true;
     Ahead<FORM> ahead(x, w);
-    for (int tile = x.worker; ok && tile < ctl.tiles; tile += x.workers) {
+    const bool cut = has_epilogue(FORM) && ctl.parts > 1;  // then the tickets are taken also after a wait was given up
+    for (int tile = x.worker; (ok || cut) && tile < ctl.tiles; tile += x.workers) {
         const Tile q = decode<FORM, CG>(t, p, ctl, tile);
+        const int meeting = (q.tile * CG + static_cast<int>(x.rank)) * kEpilogueWarps + w;  // of a tile's parts
+        float* const part = cut ? p.parts + (static_cast<int64_t>(meeting) * ctl.parts + (tile - q.tile * ctl.parts)) * kPartFloats + lane_id() : nullptr;
+        if (!ok) {
+            last_part(p, meeting, ctl.parts);
+            continue;
+        }
         if (FORM == kWeightGrad && p.accumulate && q.steps == 0) continue;  // nothing to add
         const int cols_half = out_cols<FORM>(q.cols) / 2;
         const int in_group = q.m0 + static_cast<int>(x.rank) * kTileRows + quarter * 32;
@@ -844,35 +926,61 @@ __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
                           static_cast<short>(rows), static_cast<short>(cols_half)};
         if constexpr (has_epilogue(FORM)) {
             ahead.load_bias(p, at);
-            ahead.ask_residual(x, at, 0);
+            if (!cut) ahead.ask_residual(x, at, 0);
         }
         if constexpr (kSegment == 0) {
             ok = warp_wait(&ctl.acc_full[buf], acc_phase, x.waits);
-            if (!ok) break;
+            if (!ok) {
+                if (!cut) break;
+                last_part(p, meeting, ctl.parts);
+                continue;
+            }
             tc_fence_after();
             const bool staged = in_boxes<FORM>(p, at);
-            for (int c = 0; c < cols_half; c += 32) {
-                uint32_t u[32];
-                __syncwarp();
-                const uint32_t from = lane_base + buf * kMaxTileCols + half * cols_half + c;
-                tc_ld32(from, u);
-                float up[32];  // gated
-                if constexpr (FORM == kGated) {
-                    uint32_t u2[32];
-                    tc_ld32(from + q.cols / 2, u2);
-                    tc_wait_ld(u2);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) up[i] = __uint_as_float(u2[i]);
-                }
-                tc_wait_ld(u);
-                if (c + 32 >= cols_half) {  // read out: the accumulator is free before the last stores
-                    tc_fence_before();
+            bool mine = true;  // this warp's to finish
+            if (cut) {
+                for (int c = 0; c < (FORM == kGated ? 2 : 1) * cols_half; c += 32) {
+                    uint32_t u[32];
                     __syncwarp();
-                    if (lane_id() == 0) bar_arrive<CG>(acc_empty0 + 8 * buf);
-                }
-                float v[32];
+                    const int at_up = FORM == kGated && c >= cols_half ? q.cols / 2 - cols_half : 0;
+                    tc_ld32(lane_base + buf * kMaxTileCols + half * cols_half + c + at_up, u);
+                    tc_wait_ld(u);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+                    for (int i = 0; i < 32; ++i) part[(c + i) * kWarpSize] = __uint_as_float(u[i]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane_id() == 0) bar_arrive<CG>(acc_empty0 + 8 * buf);
+                mine = last_part(p, meeting, ctl.parts);
+                if constexpr (has_epilogue(FORM))
+                    if (mine) ahead.ask_residual(x, at, 0);
+            }
+            for (int c = 0; mine && c < cols_half; c += 32) {
+                float v[32], up[32];  // up: gated
+                if (cut) {
+                    sum_parts(p, meeting, ctl.parts, c, v);
+                    if (FORM == kGated) sum_parts(p, meeting, ctl.parts, cols_half + c, up);
+                } else {
+                    uint32_t u[32];
+                    __syncwarp();
+                    const uint32_t from = lane_base + buf * kMaxTileCols + half * cols_half + c;
+                    tc_ld32(from, u);
+                    if constexpr (FORM == kGated) {
+                        uint32_t u2[32];
+                        tc_ld32(from + q.cols / 2, u2);
+                        tc_wait_ld(u2);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) up[i] = __uint_as_float(u2[i]);
+                    }
+                    tc_wait_ld(u);
+                    if (c + 32 >= cols_half) {  // read out: the accumulator is free before the last stores
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane_id() == 0) bar_arrive<CG>(acc_empty0 + 8 * buf);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+                }
                 if constexpr (has_epilogue(FORM)) {
                     ok = ok && finish_columns<FORM>(x, at, c, ahead, v, up);
                     if (!ok) continue;  // the accumulator is freed all the same
@@ -943,11 +1051,28 @@ __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
                 acc_phase ^= buf == 0;
             }
             __syncwarp();
-            if (!ok) break;
+            if (!ok) {
+                if (!cut) break;
+                last_part(p, meeting, ctl.parts);
+                continue;
+            }
+            if (cut) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (32 * c >= cols_half) break;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const uint64_t two = acc[c / 2][c % 2 * 16 + i];
+                        part[(32 * c + 2 * i) * kWarpSize] = __uint_as_float(static_cast<uint32_t>(two));
+                        part[(32 * c + 2 * i + 1) * kWarpSize] = __uint_as_float(static_cast<uint32_t>(two >> 32));
+                    }
+                }
+                if (!last_part(p, meeting, ctl.parts)) continue;
+                if constexpr (has_epilogue(FORM)) ahead.ask_residual(x, at, 0);
+            }
             const Place to = read_place(&ctl.at[w]);
             if constexpr (has_epilogue(FORM)) {
-                ok = put_finished<FORM>(x, to, ahead, acc);
-                if (!ok) break;
+                ok = put_finished<FORM>(x, to, ahead, acc, cut ? meeting : -1);
             } else if (in_boxes<FORM>(p, to)) put_sums<FORM, true>(x, box, to, acc);
             else put_sums<FORM, false>(x, box, to, acc);
             __syncwarp();  // the place has been read
@@ -1187,7 +1312,7 @@ ep_status launch(ep_handle* h, const Operand& a, const Operand& a_small, const O
     Maps m;
     const bool pairs = FORM == kWeightGrad ? wgrad_on_pairs(h, p)
                                            : !p.a_words && rows_each >= (FORM == kFp8 ? kPairRowsFp8 : kTileRows + 1) &&
-                                                 most_pairs > 0 && (!has_epilogue(FORM) || fills_pairs<FORM>(p, rows_each, most_pairs));
+                                                 most_pairs > 0 && (!has_epilogue(FORM) || (!p.parts && fills_pairs<FORM>(p, rows_each, most_pairs)));
     // A tile's stages wait for their operands, and a tile is worth the rows that a CTA loads beside its columns: a pair's
     // 128 beside half of the columns (weight gradient of 8 experts, 560 x 2448, 83592 rows: 401 us with 32 columns'
     // worth, 257 with 128, 246 with 256), a single CTA's as many as a group's tiles have, at least one load's (FP8, 64
@@ -1259,6 +1384,9 @@ ep_status check_groups(const ep_handle* h, int64_t num_rows, int32_t n, int32_t 
     return EP_OK;
 }
 
+// Of the parts of one wave of tiles.
+int64_t parts_bytes(const ep_handle* h) { return static_cast<int64_t>(h->plan.num_sms) * kEpilogueWarps * kPartFloats * sizeof(float); }
+
 bool row_stride_ok(int64_t bytes, int64_t least) { return bytes >= least && bytes % 16 == 0 && bytes < (INT64_C(1) << 40); }
 
 bool rows_aligned32(const void* p, int64_t row_bytes) {
@@ -1315,11 +1443,21 @@ ep_status ep_grouped_gemm(ep_handle* h, int64_t num_rows, int32_t n, int32_t k, 
                                weight_across_operand(w, n, k, groups, 1), p, rows_each, stream);
 }
 
+int64_t ep_grouped_gemm_act_workspace(const ep_handle* h, int64_t num_rows, int32_t n, int32_t k, int32_t gated, int64_t expected_rows) {
+    if (h == nullptr || num_rows <= 0 || n <= 0 || k < 2 * kLeastPartSteps * 64) return 0;
+    // wide tiles leave half of the CTAs without one, or more
+    const int64_t rows_each = expected_rows > 0 ? expected_rows : num_rows / h->cfg.num_experts;
+    const int32_t width = gated ? n / 2 : n, cols = gated ? kMaxTileCols / 2 : kMaxTileCols;
+    const int64_t tiles = h->cfg.num_experts * ((rows_each + kTileRows - 1) / kTileRows) * ((width + cols - 1) / cols);
+    return 2 * tiles <= h->plan.num_sms ? parts_bytes(h) : 0;
+}
+
 ep_status ep_grouped_gemm_act(ep_handle* h, int64_t num_rows, int32_t n, int32_t k, const int32_t* group_count,
                               const int32_t* group_begin, const void* x, int64_t x_row_bytes, const void* w,
                               const float* bias, int32_t act, int32_t gated, const float* row_weights, const void* residual,
                               int64_t residual_row_bytes, void* pre, int64_t pre_row_bytes, void* out, ep_dtype out_dtype,
-                              int64_t out_row_bytes, int64_t expected_rows, ep_stream_t stream) {
+                              int64_t out_row_bytes, int64_t expected_rows, void* workspace, int64_t workspace_bytes,
+                              ep_stream_t stream) {
     EP_TRACE();
     GemmParams p = {};
     const ep_status st = check_groups(h, num_rows, n, k, group_count, group_begin, &p);
@@ -1350,6 +1488,11 @@ ep_status ep_grouped_gemm_act(ep_handle* h, int64_t num_rows, int32_t n, int32_t
     p.residual_row_bytes = residual_row_bytes;
     p.pre = static_cast<uint8_t*>(pre);
     p.pre_row_bytes = pre_row_bytes;
+    const int64_t need = parts_bytes(h);
+    EP_CHECK_ARG(!workspace || (aligned16(workspace) && workspace_bytes >= need),
+                 "workspace must be 16-byte aligned and hold %lld bytes, got %lld", static_cast<long long>(need), static_cast<long long>(workspace_bytes));
+    if (ep_grouped_gemm_act_workspace(h, num_rows, n, k, gated, expected_rows) > 0) p.parts = static_cast<float*>(workspace);
+    p.tickets = h->part_tickets;
     p.pre_wide = pre && rows_aligned32(pre, pre_row_bytes) && (!gated || width % 16 == 0);
     const int64_t rows_each = expected_rows ? expected_rows : num_rows / p.groups.groups;
     const int groups = p.groups.groups;

@@ -34,6 +34,7 @@ struct ep_handle {
     int32_t* expert_counts = nullptr;          // [R][layout_chunks][EL]: the expert layout's counts per chunk of slots
     int32_t* layout_tickets = nullptr;         // [R]: CTAs of a rank that the expert layout has counted
     int32_t* layer_tickets = nullptr;          // [2][CTAs]: arrivals at what several CTAs of the layer's kernels add up
+    int32_t* part_tickets = nullptr;           // [CTAs][8]: the same of the products' parts
     int normal_tokens = -1;                  // T of the current dispatch record, -1 = none
     bool prepared = false;                   // record built by ep_notify_dispatch, not yet used
     int ll_tokens = -1;                      // T of the last LL dispatch, -1 = none

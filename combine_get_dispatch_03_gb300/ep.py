@@ -58,8 +58,8 @@ EXPORTS = ("ep_handle_create", "ep_handle_destroy", "ep_handle_status", "ep_hand
            "ep_expected_topk", "ep_theoretical_num_sms", "ep_layout_notify", "ep_grouped_gemm",
            "ep_grouped_gemm_wgrad", "ep_grouped_gemm_fp8", "ep_swiglu", "ep_swiglu_grad",
            "ep_expert_layout", "ep_expert_gather", "ep_expert_reduce", "ep_selftest_wait_limit",
-           "ep_grouped_gemm_act", "ep_act_grad", "ep_act_grad_workspace", "ep_router", "ep_router_grad", "ep_moe_layer",
-           "ep_moe_layer_workspace")
+           "ep_grouped_gemm_act", "ep_grouped_gemm_act_workspace", "ep_act_grad", "ep_act_grad_workspace", "ep_router",
+           "ep_router_grad", "ep_moe_layer", "ep_moe_layer_workspace")
 
 
 def library_path() -> str:
@@ -117,7 +117,9 @@ def lib():
         L.ep_expert_gather.argtypes = [P, P, S, P, P, P, P, I64, P, P, P, P]
         L.ep_expert_reduce.argtypes = [P, P, I64, P, P, P, I64, P, P, P]
         F = ctypes.c_float
-        L.ep_grouped_gemm_act.argtypes = [P, I64, I32, I32, P, P, P, I64, P, P, I32, I32, P, P, I64, P, I64, P, S, I64, I64, P]
+        L.ep_grouped_gemm_act.argtypes = [P, I64, I32, I32, P, P, P, I64, P, P, I32, I32, P, P, I64, P, I64, P, S, I64, I64, P, I64, P]
+        L.ep_grouped_gemm_act_workspace.argtypes = [P, I64, I32, I32, I32, I64]
+        L.ep_grouped_gemm_act_workspace.restype = I64
         L.ep_act_grad_workspace.argtypes = [P, I64, I32]
         L.ep_act_grad_workspace.restype = I64
         L.ep_act_grad.argtypes = [P, I64, I32, P, P, P, I64, P, I64, I32, I32, P, P, I64, P, P, P, I64, P]
@@ -718,11 +720,16 @@ def ep_grouped_gemm_act(h: Handle, x: torch.Tensor, w: torch.Tensor, group_count
     if residual is not None:
         rp, _, _, rs = _rows(residual, "residual", torch.bfloat16, d, rows, width)
     cnt, beg = _group_arrays(h, group_count, group_begin)
+    work, keep = None, None
+    work_bytes = lib().ep_grouped_gemm_act_workspace(h.ptr, rows, n, k, int(bool(gated)), expected_rows) if k >= 1024 else 0
+    if work_bytes:
+        work, keep = _scratch(h, work_bytes, stream)
     _raise(lib().ep_grouped_gemm_act(
         h.ptr, rows, n, k, cnt, beg, xp, xs, _ptr(w, "w", torch.bfloat16, (h.cfg.num_experts, n, k), d),
         _ptr(bias, "bias", torch.float32, (h.cfg.num_experts, n), d), _choice(act, ACTS, "act"), int(bool(gated)),
         _ptr(row_weights, "row_weights", torch.float32, (rows,), d), rp, rs, pp, ps, op,
-        EP_FP32 if out_dtype == torch.float32 else EP_BF16, os_, expected_rows, _stream(stream, d)))
+        EP_FP32 if out_dtype == torch.float32 else EP_BF16, os_, expected_rows, work, work_bytes, _stream(stream, d)))
+    del keep
     return dict(out=out, pre=pre)
 
 

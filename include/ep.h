@@ -476,14 +476,18 @@ ep_status ep_grouped_gemm(ep_handle* h, int64_t num_rows, int32_t n, int32_t k, 
  * gets v (bf16 rows of n), which ep_act_grad() takes.  Gated: n a multiple
  * of 16; with act EP_ACT_SILU and pre's rows this is ep_grouped_gemm() and ep_swiglu()
  * without the rounding between them.  A handle with one expert makes it
- * a dense product.  All row strides are multiples of 16 bytes, x's too.
- * expected_rows as in ep_grouped_gemm(). */
+ * a dense product.  All row strides are multiples of 16 bytes, x's too; bias is 16-byte aligned.
+ * expected_rows as in ep_grouped_gemm().  Where the product has few tiles and a long contraction, CTAs that would idle can take
+ * parts of it, if the call is given a workspace (NULL: it does without) of ep_grouped_gemm_act_workspace() bytes (0: it would not
+ * help), whose content does not matter and which the call uses until it has run.  The sums of the parts are added in a fixed order. */
+int64_t ep_grouped_gemm_act_workspace(const ep_handle* h, int64_t num_rows, int32_t n, int32_t k, int32_t gated,
+                                      int64_t expected_rows);
 ep_status ep_grouped_gemm_act(ep_handle* h, int64_t num_rows, int32_t n, int32_t k, const int32_t* group_count,
                               const int32_t* group_begin, const void* x, int64_t x_row_bytes, const void* w,
                               const float* bias, int32_t act, int32_t gated, const float* row_weights,
                               const void* residual, int64_t residual_row_bytes, void* pre, int64_t pre_row_bytes,
                               void* out, ep_dtype out_dtype, int64_t out_row_bytes, int64_t expected_rows,
-                              ep_stream_t stream);
+                              void* workspace, int64_t workspace_bytes, ep_stream_t stream);
 
 /* Gradient of that epilogue, from dy (of out; bf16 rows of width) and pre (v, bf16 rows of n):
  *   not gated:  d_pre = dy * w * act'(v)                                         d_w = sum_j dy * act(v)

@@ -122,6 +122,52 @@ def test_many_tiles_a_cta(gated, n, k, expected):
     check_forward([33, 0, 64, 9011, 31, 1, 1300], n, k, "gelu", gated, True, True, True, True, torch.bfloat16, expected, max_sms=20)
 
 
+@pytest.mark.parametrize("counts", [[1], [16], [130], [300, 0, 5]], ids=lambda c: f"{len(c)}g{sum(c)}")
+@pytest.mark.parametrize("n,k", [(16, 1024), (272, 2056), (1008, 1544), (256, 7168)])
+@pytest.mark.parametrize("form", ["bf16", "gated", "fp32"])
+@pytest.mark.parametrize("max_sms", [0, 5])
+def test_contraction_in_parts(counts, n, k, form, max_sms):
+    """Few tiles and a long contraction: parts of it meet in a workspace."""
+    check_forward(counts, n, k, "silu" if form == "gated" else "gelu", form == "gated", True, True, True, form != "fp32",
+                  torch.float32 if form == "fp32" else torch.bfloat16, 0, pad=8, gap=0, max_sms=max_sms)
+
+
+def test_contraction_in_parts_repeats_and_is_optional():
+    """The same bits call after call, captured and on a side stream; without a workspace it is not cut."""
+    g = gen(40)
+    rows, n, k = 70, 264, 4104
+    x, w, res = randn(g, (rows, k)), randn(g, (1, n, k), k ** -0.5), randn(g, (rows, n))
+    h, c = handle(1), i32([rows])
+    want = ep.ep_grouped_gemm_act(h, x, w, c, residual=res, act="gelu")["out"]
+    for _ in range(20):
+        assert torch.equal(ep.ep_grouped_gemm_act(h, x, w, c, residual=res, act="gelu")["out"], want)
+    place = res.clone()
+    ep.ep_grouped_gemm_act(h, x, w, c, residual=place, act="gelu", out=place)
+    assert torch.equal(place, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = [ep.ep_grouped_gemm_act(h, x, w, c, residual=res, act="gelu")["out"] for _ in range(3)]
+    for _ in range(3):
+        graph.replay()
+        assert all(torch.equal(o, want) for o in outs)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    again = ep.ep_grouped_gemm_act(h, x, w, c, residual=res, act="gelu", stream=side)["out"]
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(again, want)
+    L, st = ep.lib(), torch.cuda.current_stream().cuda_stream
+    need = L.ep_grouped_gemm_act_workspace(h.ptr, rows, n, k, 0, 0)
+    assert need > 0 and L.ep_grouped_gemm_act_workspace(h.ptr, 100000, 4096, k, 0, 0) == 0
+    whole, ws = torch.empty_like(want), torch.empty(need, dtype=torch.uint8, device=DEV)
+    args = [h.ptr, rows, n, k, c.data_ptr(), None, x.data_ptr(), 2 * k, w.data_ptr(), None, 3, 0, None, res.data_ptr(), 2 * n, None, 0,
+            whole.data_ptr(), 0, 2 * n, 0]
+    assert L.ep_grouped_gemm_act(*args, ws.data_ptr(), need - 1, st) == 1 and b"workspace" in L.ep_last_error()
+    assert L.ep_grouped_gemm_act(*args, None, 0, st) == 0
+    h.check()
+    # both are sums of the same products, each off by (k / 16 + 8) 2^-22 of unit magnitudes at most, and rounded
+    assert ((whole.double() - want.double()).abs() <= 2 * 1.13 * (k / 16 + 8) * 2.0 ** -22 * 16 + 2.0 ** -7 * want.double().abs()).all()
+
+
 def test_dense_product_in_place_and_side_stream():
     """One expert is a dense product; the residual may be the output itself."""
     g = gen(1)

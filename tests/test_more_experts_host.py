@@ -7,7 +7,7 @@ from combine_get_dispatch_03_gb300 import ep
 
 def test_calls_without_a_handle_are_refused():
     L = ep.lib()
-    for rc in (L.ep_grouped_gemm_act(None, 0, 8, 8, None, None, None, 16, None, None, 0, 0, None, None, 0, None, 0, None, 0, 16, 0, None),
+    for rc in (L.ep_grouped_gemm_act(None, 0, 8, 8, None, None, None, 16, None, None, 0, 0, None, None, 0, None, 0, None, 0, 16, 0, None, 0, None),
                L.ep_act_grad(None, 0, 8, None, None, None, 16, None, 16, 0, 0, None, None, 0, None, None, None, 0, None),
                L.ep_router(None, 0, None, 2, None, None, 0, 1, 1, 1, 1.0, None, None, None),
                L.ep_router_grad(None, 0, None, 2, None, None, 0, 1, 1.0, None, None),
