@@ -1,13 +1,16 @@
 """A mixture-of-experts layer on the dispatch / combine handle: training in bf16 and low-latency serving in FP8.
 
-    python examples/moe_layer.py          # one training step and one decode step on random weights
+    python examples/moe_layer.py          # one training step and decode steps on random weights
+
+The routing is that of the logits x gate^T: a product kept in fp32 -> router.
 
 Training (normal mode): layout and record -> dispatch -> expert order -> gather -> up product -> gated activation with
 the routing weights -> down product -> reduce -> combine; the backward pass is the same path with every step's gradient
 (a combine's gradient is a cached dispatch, a gather's a reduce, and the other way round).
 
 Serving (low-latency mode): FP8 dispatch -> up product straight from the message buffer -> gated activation with the
-FP8 cast -> down product -> combine with the routing weights.
+FP8 cast -> down product -> combine with the routing weights.  For at most 64 tokens in all the layer is one call of two
+kernels, and the tokens are not rounded to FP8.
 """
 from __future__ import annotations
 
@@ -81,6 +84,20 @@ def decode(h: ep.Handle, x, topk_idx, topk_weights, up, down):
     return ep.ep_ll_combine(h, y, topk_idx, topk_weights)
 
 
+def route(h: ep.Handle, one: ep.Handle, x, gate):
+    """Logits x gate^T (gate [E][H] bf16; `one` is a handle of one expert, for dense products) and their top-k experts."""
+    rows = x.view(1, -1, h.cfg.hidden)
+    count = torch.full((1,), rows.shape[1], dtype=torch.int32, device=h.device)
+    logits = ep.ep_grouped_gemm_act(one, rows, gate[None], count, out_dtype=torch.float32)["out"].view(*x.shape[:2], -1)
+    r = ep.ep_router(h, logits)
+    return r["topk_idx"], r["topk_weights"]
+
+
+def decode_few(h: ep.Handle, x, topk_idx, topk_weights, up, down):
+    """The same step for R * T <= 64 tokens in one call; `up` and `down` are quantize()d weights."""
+    return ep.ep_moe_layer(h, x, topk_idx, topk_weights, up[0], down[0], up_scales=up[1], down_scales=down[1])
+
+
 def main():
     R, T, H, E, K, I = 8, 256, 1024, 32, 4, 512
     dev = torch.device("cuda", torch.cuda.current_device())
@@ -90,20 +107,21 @@ def main():
         return (torch.randn(shape, generator=g, device=dev) * std).to(torch.bfloat16)
 
     x, dy = randn(R, T, H), randn(R, T, H)
-    topk_weights, topk_idx = torch.softmax(torch.randn((R, T, E), generator=g, device=dev), -1).topk(K)
-    topk_idx, topk_weights = topk_idx.contiguous(), topk_weights.contiguous()
-    w_up, w_down = randn(E, 2 * I, H, std=H ** -0.5), randn(E, H, I, std=I ** -0.5)
+    w_up, w_down, gate = randn(E, 2 * I, H, std=H ** -0.5), randn(E, H, I, std=I ** -0.5), randn(E, H, std=H ** -0.5)
     h = ep.Handle(ep.Config(num_ranks=R, num_max_tokens=T, hidden=H, num_experts=E, num_topk=K, recv_capacity=R * T))
+    one = ep.Handle(ep.Config(num_ranks=1, num_max_tokens=R * T, hidden=H, num_experts=1, num_topk=1))
+    topk_idx, topk_weights = route(h, one, x, gate)
     y, saved = forward(h, x, topk_idx, topk_weights, w_up, w_down)
     grads = backward(h, dy, saved, w_up, w_down)
     h.check()
     print("training: output", tuple(y.shape), "gradients", [tuple(v.shape) for v in grads])
     t = 8
-    yd = decode(h, x[:, :t].contiguous(), topk_idx[:, :t].contiguous(), topk_weights[:, :t].contiguous(),
-                quantize(w_up), quantize(w_down))
-    h.check()
-    off = (yd.float() - y[:, :t].float()).norm() / y[:, :t].float().norm()
-    print(f"decode: output {tuple(yd.shape)}, {float(off):.3f} from the bf16 layer (FP8 weights and activations)")
+    step = [v[:, :t].contiguous() for v in (x, topk_idx, topk_weights)] + [quantize(w_up), quantize(w_down)]
+    for name, run in (("FP8 weights and activations", decode), ("FP8 weights, two kernels", decode_few)):
+        yd = run(h, *step)
+        h.check()
+        off = (yd.float() - y[:, :t].float()).norm() / y[:, :t].float().norm()
+        print(f"decode: output {tuple(yd.shape)}, {float(off):.3f} from the bf16 layer ({name})")
 
 
 if __name__ == "__main__":

@@ -371,8 +371,8 @@ ep_status ep_clean_mask_buffer(ep_handle* h, ep_stream_t stream);
  * or traps; read the outcome with ep_handle_status() / ep_query_mask_buffer(). */
 ep_status ep_selftest_bounded_wait(ep_handle* h, uint32_t max_iterations, int32_t rank, ep_stream_t stream);
 
-/* Self-test of the waits inside the grouped products: sets how long one may
- * last (limit_ns >= 1; 0: four seconds again) in the products that are called
+/* Self-test of the waits inside the grouped products and ep_moe_layer(): sets how long one may
+ * last (limit_ns >= 1; 0: four seconds again) in those that are called
  * on the handle from now on.  A wait that lasts longer -- the limit is looked at
  * every quarter of a millisecond -- records EP_ERR_TIMEOUT; the product's other
  * waits end with it, what it has in flight is waited for, and the
@@ -623,7 +623,7 @@ ep_status ep_router_grad(ep_handle* h, int64_t num_tokens, const void* logits, e
  * then up rows) and w_down [E][H][width] are bf16 (scales NULL), or e4m3 codes with fp32 scales per 128 x 128
  * (w_up_scales [E][2 * width / 128][H / 128], w_down_scales [E][H / 128][width / 128]; H and width multiples
  * of 128).  silu(g) * u is rounded to bf16; the tokens are not rounded to FP8.  With FP8 weights an
- * infinite value makes its token's outputs NaN.  out may not be x.
+ * infinite value makes its token's outputs NaN.  out may be a bias, not x.
  * The order of the sums is fixed by the routing and the handle.  workspace: ep_moe_layer_workspace() bytes (-1: bad
  * arguments) whose content does not matter, in use until the call has run. */
 int64_t ep_moe_layer_workspace(const ep_handle* h, int32_t num_tokens, int32_t width);

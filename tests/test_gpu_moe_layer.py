@@ -106,6 +106,8 @@ SHAPES = [  # R, T, E, K, H, I
     (1, 64, 2, 1, 128, 256),
     (1, 2, 3, 3, 3968, 2176),
     (16, 1, 2048, 32, 128, 128),
+    (2, 32, 2048, 32, 128, 128),
+    (1, 9, 16, 3, 640, 128),
 ]
 
 
@@ -156,13 +158,18 @@ def test_slots_left_out_and_named_twice(fp8):
     tw[0, 0] = float("nan")              # of slots without an expert: not read
     out = run(h, x, idx, tw, w, bias_0=b)
     h.check()
-    tw[0, 0] = 0
-    within(out, *reference(x, idx, tw, w, [b]))
+    again = tw.clone()
+    again[0, 0] = 0
+    within(out, *reference(x, idx, again, w, [b]))
     assert torch.equal(out[0, 0], b[0, 0])
+    place = b.clone()                    # a bias may be the output
+    ep.ep_moe_layer(h, x, idx, tw, w[0], w[2], up_scales=w[1], down_scales=w[3], bias_0=place, out=place)
+    assert torch.equal(place, out)
     none = run(h, x, torch.full_like(idx, -1), tw, w, bias_1=b)
     h.check()
     assert torch.equal(none, b)
     assert (run(h, x, torch.full_like(idx, -1), tw, w) == 0).all()
+    tw = again
     everyone = torch.full_like(idx, -1)
     everyone[..., 2] = 7                 # one expert for all tokens
     within(run(h, x, everyone, tw, w), *reference(x, everyone, tw, w))

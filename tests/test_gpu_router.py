@@ -105,6 +105,34 @@ def test_groups(E, K, groups, kept, score, dtype, biased):
     check(handle(E, K), logits, bias=bias, score=score, num_groups=groups, kept_groups=kept)
 
 
+@pytest.mark.parametrize("E,K", [(1, 32), (3, 8), (31, 32), (40, 32)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("biased", [False, True])
+def test_more_slots_than_experts_and_most_slots(E, K, score, normalize, biased):
+    g = gen(E)
+    bias = torch.randn(E, generator=g, device=DEV) * 0.05 if biased else None
+    logits = torch.randn((37, E), generator=g, device=DEV)
+    idx, _ = check(handle(E, K), logits, bias=bias, score=score, normalize=normalize)
+    assert (idx[:, E:] == -1).all()
+    dw = torch.randn((37, K), generator=g, device=DEV)
+    dl = ep.ep_router_grad(handle(E, K), logits, idx, dw, score=score, normalize=normalize)
+    want, mag = grad_reference(logits, idx, dw, score, normalize, 1.0)
+    assert ((dl.double() - want).abs() <= GRAD_EPS * mag + 2.0 ** -24 * want.abs() + 1e-37).all()
+
+
+@pytest.mark.parametrize("biased,groups", [(False, 1), (True, 1), (False, 4), (True, 4)])
+def test_equal_logits(biased, groups):
+    """More keys reach the bound than a warp has lanes."""
+    bias = torch.zeros(256, device=DEV) if biased else None
+    for score in ("softmax", "sigmoid"):
+        same = torch.full((70, 256), 0.25, device=DEV)
+        idx, _ = check(handle(256, 8), same, bias=bias, score=score, num_groups=groups, kept_groups=max(1, groups // 2))
+        assert torch.equal(idx, torch.arange(8, device=DEV).expand(70, 8))
+        same[:, 200] = 0.5
+        check(handle(256, 8), same, bias=bias, score=score, num_groups=groups, kept_groups=max(1, groups // 2))
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("kw", [{}, dict(zero_bias=True), dict(num_groups=8, kept_groups=3), dict(num_groups=8, kept_groups=3, zero_bias=True)],
                          ids=["plain", "bias", "groups", "both"])
