@@ -13,8 +13,8 @@
 //
 // Which experts are chosen must not hang on the rounding of s.  Without bias the keys are the logits themselves; groups
 // are compared by their scores.  32-bit scores decide unless two that are compared lie closer than their error
-// (kSigmoidError): such a token's keys are computed again in 64 bits, those that reached the bound (sigmoid) or all of them
-// (choose_exactly), a fraction of a percent of the tokens.
+// (kSigmoidError): such a token's keys are computed again in 64 bits, those that reached the bound, or all of them (choose_exactly) where a bias
+// stands beside a softmax: a fraction of a percent of the tokens.
 #include "ep_act.cuh"
 #include "ep_groups.cuh"
 #include "ep_handle.h"
@@ -224,9 +224,10 @@ __device__ __noinline__ int choose_exactly(const RouterParams& p, int64_t token)
     return chosen;
 }
 
-// The score of the group of this lane's number (lane g < groups), from the warp's keys: two largest, added up.
+// The score of the group of this lane's number (lane g < groups), from the warp's keys: two largest, added up.  *second: the
+// smaller.
 template <int V>
-__device__ __forceinline__ float group_score(const RouterParams& p, const float (&key)[V], float* scratch) {
+__device__ __forceinline__ float group_score(const RouterParams& p, const float (&key)[V], float* scratch, float* second) {
     const int size = p.experts / p.groups;
     float a = -INFINITY, b = -INFINITY;
     const int lanes = size / V;
@@ -256,7 +257,19 @@ __device__ __forceinline__ float group_score(const RouterParams& p, const float 
                 a = fmaxf(a, k);
             }
     }
+    *second = size == 1 ? a : b;
     return size == 1 ? a : a + b;
+}
+
+// Whether a key's order in 64 bits hangs on its own logit alone: not on a softmax's sum, which a bias is added beside.
+__device__ __forceinline__ bool alone(const RouterParams& p) { return !p.softmax || p.bias == nullptr; }
+
+// A key in 64 bits, then; of a softmax times its sum.  One copy of it: code that few tokens run is fetched from memory when
+// they do.
+__device__ __noinline__ double key64(const RouterParams& p, float l, int expert, float most) {
+    const double e = exp(p.softmax ? static_cast<double>(l) - most : -static_cast<double>(l));
+    if (p.softmax) return e;
+    return 1.0 / (1.0 + e) + (p.bias ? static_cast<double>(p.bias[expert]) : 0.0);
 }
 
 // How far apart two keys must lie for 32 bits to tell them; `error` is that of their scores.
@@ -319,7 +332,7 @@ struct Reach {
 // The scored tokens' keys, s + bias, of the groups that stay; *error: of a score.  Whether 32 bits may have the groups wrong.
 template <int V>
 __device__ __forceinline__ bool make_keys(const RouterParams& p, const float (&l)[V], float most, float sum, float* scratch,
-                                          float (&key)[V], float* error) {
+                                          Reach& reach, float (&key)[V], float* error) {
     const int first = lane_id() * V;
     const float inv = 1.0f / sum;
     float top = 0.0f;
@@ -335,16 +348,59 @@ __device__ __forceinline__ bool make_keys(const RouterParams& p, const float (&l
     *error = (p.softmax ? kSoftmaxError : kSigmoidError) * warp_max(top);
     if (p.groups == 1) return false;
     const int size = p.experts / p.groups;
-    const float score = group_score<V>(p, key, scratch);
+    float second;
+    const float score = group_score<V>(p, key, scratch, &second);
     int better = 0;
     for (int g = 0; g < p.groups; ++g) {
         const float other = __shfl_sync(kFullMask, score, g);
         better += other > score || (other == score && g < lane_id());
     }
     const bool there = lane_id() < p.groups, in = there && better < p.kept;
-    const unsigned stay = __ballot_sync(kFullMask, in);
+    unsigned stay = __ballot_sync(kFullMask, in);
     // the last that stays and the first that does not
     const float last = -warp_max(in ? -score : -INFINITY), next = warp_max(there && !in ? score : -INFINITY);
+    const float apart = key_error(2.0f * *error, last, next);
+    bool close = next > -INFINITY && last - next <= apart;
+    if (close && alone(p) && size % V == 0) {
+        // Groups around the border compete again, by what their largest members are worth in 64 bits, a lane each.
+        const bool rival = there && score >= next - apart && score <= last + apart;
+        const unsigned rivals = __ballot_sync(kFullMask, rival), above = __ballot_sync(kFullMask, there && score > last + apart);
+        const int mine = first < p.experts ? first / size : 0;
+        const float least = __shfl_sync(kFullMask, second - 2.0f * key_error(*error, second, second), mine);
+        int all = 0;
+        __syncwarp();
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const bool member = first < p.experts && (rivals >> mine & 1) && key[v] > -INFINITY && key[v] >= least;
+            const unsigned members = __ballot_sync(kFullMask, member);
+            const int at = all + __popc(members & lanemask_lt());
+            if (member && at < kWarpSize) reach.key_expert[at] = make_float2(l[v], __int_as_float(first + v));
+            all += __popc(members);
+        }
+        __syncwarp();
+        if (all <= kWarpSize) {
+            const float2 c = lane_id() < all ? reach.key_expert[lane_id()] : make_float2(0.0f, 0.0f);
+            const int expert = __float_as_int(c.y);
+            const uint64_t exact = lane_id() < all ? ordered64(key64(p, c.x, expert, most)) : 0;
+            uint64_t sum = 0;  // lane g: the score of rival g
+            for (unsigned left = rivals; left; left &= left - 1) {
+                const int g = __ffs(left) - 1;
+                uint64_t k = lane_id() < all && expert / size == g ? exact : 0;
+                const uint64_t a = warp_max64(k);
+                if (lane_id() == __ffs(__ballot_sync(kFullMask, k == a)) - 1) k = 0;
+                const uint64_t b = warp_max64(k);
+                if (lane_id() == g) sum = size == 1 ? a : ordered64(unordered64(a) + unordered64(b));
+            }
+            int ahead = 0;
+            for (unsigned left = rivals; left; left &= left - 1) {
+                const int g = __ffs(left) - 1;
+                const uint64_t other = __shfl_sync(kFullMask, sum, g);
+                ahead += other > sum || (other == sum && g < lane_id());
+            }
+            stay = above | __ballot_sync(kFullMask, rival && ahead < p.kept - __popc(above));
+            close = false;
+        }
+    }
     if (size % V == 0) {
         if (first < p.experts && !(stay >> (first / size) & 1))
 #pragma unroll
@@ -354,7 +410,7 @@ __device__ __forceinline__ bool make_keys(const RouterParams& p, const float (&l
         for (int v = 0; v < V; ++v)
             if (first + v < p.experts && !(stay >> ((first + v) / size) & 1)) key[v] = -INFINITY;
     }
-    return next > -INFINITY && last - next <= key_error(2.0f * *error, last, next);
+    return close;
 }
 
 // kScored: with bias or groups; otherwise the scores' order is the logits'.
@@ -372,7 +428,7 @@ __device__ __forceinline__ void route_token(const RouterParams& p, int64_t token
     float error = 0.0f;
     bool close = false;
     if constexpr (kScored) {
-        close = make_keys<V>(p, l, most, sum, scratch, key, &error);
+        close = make_keys<V>(p, l, most, sum, scratch, reach, key, &error);
     } else {
 #pragma unroll
         for (int v = 0; v < V; ++v) key[v] = l[v];
@@ -443,10 +499,10 @@ __device__ __forceinline__ void route_token(const RouterParams& p, int64_t token
                 }
             }
             if (__any_sync(kFullMask, near)) {
-                if (p.softmax) {
+                if (!alone(p)) {
                     close = true;
                 } else {
-                    const double exact = there ? 1.0 / (1.0 + exp(-static_cast<double>(lc))) + (p.bias ? static_cast<double>(p.bias[expert]) : 0.0) : 0.0;
+                    const double exact = there ? key64(p, lc, expert, most) : 0.0;
                     before = 0;
                     for (int j = 0; j < all; ++j) {
                         const double other = __shfl_sync(kFullMask, exact, j);
