@@ -76,6 +76,12 @@ __device__ __forceinline__ float logit(const void* p, int64_t at) {
     return v != v ? -INFINITY : fminf(v, 3.402823466e38f);
 }
 
+// An expert's bias: -inf for NaN; of finite size, 2^100 at most, so that sums of two keys and their errors stay finite.
+__device__ __forceinline__ float bias_of(const RouterParams& p, int expert) {
+    const float b = __ldg(p.bias + expert);
+    return b > -INFINITY ? fminf(fmaxf(b, -0x1p100f), 0x1p100f) : -INFINITY;
+}
+
 // Experts [lane * V, lane * V + V) of a token; -inf past the last, for NaN, and the largest finite value for +inf.
 template <typename T, int V>
 __device__ __forceinline__ void load_row(const RouterParams& p, int64_t token, float (&l)[V]) {
@@ -166,7 +172,7 @@ __device__ __noinline__ int choose_exactly(const RouterParams& p, int64_t token)
         const float l = first + v < p.experts ? logit<T>(p.logits, token * p.experts + first + v) : -INFINITY;
         const double e = exp(p.softmax ? static_cast<double>(l) - most : -static_cast<double>(l));
         double s = p.softmax ? e / inv_sum : 1.0 / (1.0 + e);
-        if (p.bias && first + v < p.experts) s += static_cast<double>(p.bias[first + v]);
+        if (p.bias && first + v < p.experts) s += static_cast<double>(bias_of(p, first + v));
         key[v] = l > -INFINITY ? ordered64(s) : 0;
     }
     if (p.groups > 1) {
@@ -269,7 +275,7 @@ __device__ __forceinline__ bool alone(const RouterParams& p) { return !p.softmax
 __device__ __noinline__ double key64(const RouterParams& p, float l, int expert, float most) {
     const double e = exp(p.softmax ? static_cast<double>(l) - most : -static_cast<double>(l));
     if (p.softmax) return e;
-    return 1.0 / (1.0 + e) + (p.bias ? static_cast<double>(p.bias[expert]) : 0.0);
+    return 1.0 / (1.0 + e) + (p.bias ? static_cast<double>(bias_of(p, expert)) : 0.0);
 }
 
 // How far apart two keys must lie for 32 bits to tell them; `error` is that of their scores.
@@ -342,8 +348,7 @@ __device__ __forceinline__ bool make_keys(const RouterParams& p, const float (&l
         const float e = exp_fast(p.softmax ? l[v] - most : -l[v]);
         const float s = p.softmax ? e * inv : reciprocal(1.0f + e);
         top = fmaxf(top, in ? s : 0.0f);
-        // NaN (a bias) as -inf
-        key[v] = in ? fmaxf(p.bias ? s + __ldg(p.bias + first + v) : s, -INFINITY) : -INFINITY;
+        key[v] = in ? (p.bias ? s + bias_of(p, first + v) : s) : -INFINITY;
     }
     *error = (p.softmax ? kSoftmaxError : kSigmoidError) * warp_max(top);
     if (p.groups == 1) return false;

@@ -599,7 +599,7 @@ ep_status ep_expert_reduce(ep_handle* h, const void* y, int64_t y_row_bytes, con
  * -- the topk_idx and topk_weights of ep_dispatch(), ep_ll_dispatch() and ep_moe_layer().  Keys are compared as 64-bit
  * arithmetic gives them (without bias and groups, the logits themselves): rounding does not choose
  * experts.  A logit of -inf or NaN, or a bias of -inf or NaN, keeps its expert from being chosen (the first two
- * count nothing in the softmax); +inf counts as the largest finite value.  Slots that no expert is left for, and all slots of
+ * count nothing in the softmax); +inf counts as the largest finite value, and biases beyond 2^100 and -2^100 as these.  Slots that no expert is left for, and all slots of
  * tokens whose token_mask (one byte each, NULL = all 1) is 0, get -1 and weight 0. */
 ep_status ep_router(ep_handle* h, int64_t num_tokens, const void* logits, ep_dtype logits_dtype, const float* bias,
                     const uint8_t* token_mask, int32_t score, int32_t num_groups, int32_t kept_groups,

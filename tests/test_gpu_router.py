@@ -189,6 +189,33 @@ def test_special_logits(score, biased, groups, normalize):
     check(handle(E, 8), logits, bias=bias, score=score, num_groups=groups, kept_groups=max(1, groups // 2), normalize=normalize)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,kept", [(32, 1, 1), (32, 4, 2), (64, 8, 3), (48, 16, 5), (160, 8, 3), (256, 8, 4)])
+def test_extreme_biases(score, E, groups, kept):
+    """Biases that force experts in or to the end: infinite ones, the type's largest and lowest values, and large ones.  Beyond
+    2^100 they count as that, so that the sums of two that compare groups stay finite."""
+    g = gen(21 + E)
+    logits = torch.randn((70, E), generator=g, device=DEV)
+    values = torch.tensor([float("inf"), float("-inf"), float("nan"), 3.4e38, -3.4e38, 1e35, -1e35, 2.0 ** 90, -2.0 ** 90, 0.0, 0.1],
+                          device=DEV)
+    h = handle(E, 8)
+    for case in range(6):
+        bias = values[torch.randint(0, len(values), (E,), generator=g, device=DEV)]
+        if case == 1:
+            bias = torch.where(torch.arange(E, device=DEV) % 3 == 0, 0.0, torch.finfo(torch.float32).min)
+        if case == 2:
+            bias = torch.full((E,), float("inf"), device=DEV)
+        if case == 3:
+            bias = torch.where(torch.arange(E, device=DEV) % 8 < 2, float("inf"), 0.0)
+        counts = torch.where(bias.isinf() & (bias < 0), bias, bias.clamp(-2.0 ** 100, 2.0 ** 100))
+        kw = dict(score=score, num_groups=groups, kept_groups=kept)
+        out = ep.ep_router(h, logits, bias=bias, **kw)
+        want_idx, want_w = reference(logits, 8, bias=counts, **kw)
+        assert torch.equal(out["topk_idx"], want_idx), case
+        assert ((out["topk_weights"].double() - want_w).abs() <= WEIGHT_EPS * want_w.abs() + 1e-37).all()
+    h.check()
+
+
 def test_token_mask_shapes_streams_and_caps():
     g = gen(5)
     R, T, E, K = 4, 9, 64, 6
