@@ -1488,10 +1488,10 @@ ep_status ep_grouped_gemm_act(ep_handle* h, int64_t num_rows, int32_t n, int32_t
     p.residual_row_bytes = residual_row_bytes;
     p.pre = static_cast<uint8_t*>(pre);
     p.pre_row_bytes = pre_row_bytes;
-    const int64_t need = parts_bytes(h);
-    EP_CHECK_ARG(!workspace || (aligned16(workspace) && workspace_bytes >= need),
+    const int64_t need = ep_grouped_gemm_act_workspace(h, num_rows, n, k, gated, expected_rows);
+    EP_CHECK_ARG(!workspace || need == 0 || (aligned16(workspace) && workspace_bytes >= need),
                  "workspace must be 16-byte aligned and hold %lld bytes, got %lld", static_cast<long long>(need), static_cast<long long>(workspace_bytes));
-    if (ep_grouped_gemm_act_workspace(h, num_rows, n, k, gated, expected_rows) > 0) p.parts = static_cast<float*>(workspace);
+    if (need > 0) p.parts = static_cast<float*>(workspace);
     p.tickets = h->part_tickets;
     p.pre_wide = pre && rows_aligned32(pre, pre_row_bytes) && (!gated || width % 16 == 0);
     const int64_t rows_each = expected_rows ? expected_rows : num_rows / p.groups.groups;

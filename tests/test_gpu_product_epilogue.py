@@ -164,6 +164,14 @@ def test_contraction_in_parts_repeats_and_is_optional():
     assert L.ep_grouped_gemm_act(*args, ws.data_ptr(), need - 1, st) == 1 and b"workspace" in L.ep_last_error()
     assert L.ep_grouped_gemm_act(*args, None, 0, st) == 0
     h.check()
+    # where none is needed, what is given is not looked at
+    short = [*args]
+    short[3], short[7] = 512, 2 * k
+    assert L.ep_grouped_gemm_act_workspace(h.ptr, rows, n, 512, 0, 0) == 0
+    w_short, out_short = w[:, :, :512].contiguous(), torch.empty_like(want)
+    short[8], short[17] = w_short.data_ptr(), out_short.data_ptr()
+    assert L.ep_grouped_gemm_act(*short, ws.data_ptr(), 1, st) == 0
+    h.check()
     # both are sums of the same products, each off by (k / 16 + 8) 2^-22 of unit magnitudes at most, and rounded
     assert ((whole.double() - want.double()).abs() <= 2 * 1.13 * (k / 16 + 8) * 2.0 ** -22 * 16 + 2.0 ** -7 * want.double().abs()).all()
 
