@@ -222,6 +222,14 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// One more arrival at a ticket; returns those before it.  What this thread knew of before is there for whoever arrives later: also
+// what others wrote ahead of a barrier that they shared with it, so that they need no fence of their own.
+__device__ __forceinline__ int32_t arrive_at(int32_t* ticket) {
+    int32_t before;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(ticket) : "memory");
+    return before;
+}
+
 // Acquire load / release store of one word in global memory, at GPU scope: the flags through
 // which CTAs of one launch publish results to one another.
 __device__ __forceinline__ uint32_t ld_acquire_u32(const uint32_t* p) {

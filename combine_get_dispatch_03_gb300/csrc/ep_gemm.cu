@@ -217,8 +217,10 @@ __device__ __forceinline__ Tile decode(const Table& t, const GemmParams& p, cons
     Tile r;
     int part = 0;
     if constexpr (has_epilogue(FORM)) {
-        part = tile % ctl.parts;
-        tile /= ctl.parts;
+        if (ctl.parts > 1) {
+            part = static_cast<uint32_t>(tile) % ctl.parts;
+            tile = static_cast<uint32_t>(tile) / ctl.parts;
+        }
     }
     r.tile = tile;
     const int lo = find_group(t.before, p.groups.groups, tile / ctl.col_tiles);
@@ -269,7 +271,7 @@ __device__ __forceinline__ void build_table(const Table& t, const GemmParams& p,
     }
     const int64_t base = block_prefix<kGemmThreads>(sum, ctl.warp_sums, &row_tiles);
     for (int g = first; g < last; ++g) t.before[g] += static_cast<int32_t>(base);
-    if (threadIdx.x == 0) {
+    if (threadIdx.x < kWarpSize) {
         // Groups that together hold more rows than there are overlap: nothing is computed.  The rows decide, not the
         // tiles: eight groups of the same 100 rows have no more tiles than eight groups of 100 rows apart.
         bool overlap = false;
@@ -278,43 +280,41 @@ __device__ __forceinline__ void build_table(const Table& t, const GemmParams& p,
             for (int w = 0; w < kGemmThreads / kWarpSize; ++w) rows += ctl.warp_rows[w];
             overlap = rows > p.groups.num_rows;
         }
-        if (overlap) report(p.status, EP_ERR_CAPACITY);
         const int total = overlap ? 0 : static_cast<int>(row_tiles);
-        t.before[groups] = total;
         // Tile width: the one whose waves over the CTAs take the least time, a wave costing its columns plus
-        // what a tile costs at any width.
-        const int workers = gridDim.x / CG;
-        int best = kMaxTileCols;
-        int64_t best_cost = INT64_MAX;
-        const int steps = (p.contraction + 63) >> 6;  // forms with an epilogue
-        ctl.parts = 1;
-        ctl.part_steps = steps;
-        for (int cols = kMaxTileCols; cols >= min_cols<FORM, CG>(); cols >>= 1) {
-            const int across = out_cols<FORM>(cols);
-            if constexpr (has_epilogue(FORM)) {
-                // (in 32 bits: there are fewer than 2^30 tiles, and one thread divides while all wait)
-                const uint32_t tiles = static_cast<uint32_t>(total) * ((p.cols_dim + across - 1) / across);
-                const uint32_t each = cols + p.tile_overhead, waves = (tiles + workers - 1) / workers;
-                int64_t cost = static_cast<int64_t>(waves) * each * steps;
-                if (cost < best_cost) best_cost = cost, best = cols, ctl.parts = 1, ctl.part_steps = steps;
-                // With few tiles, parts of the contraction, one wave of them: what they cost to meet is worth about 1500 and 250
-                // a part (steps of a column).
-                if (p.parts == nullptr || tiles == 0) continue;
-                const int most = min(min(workers / static_cast<int>(tiles), steps / kLeastPartSteps), kMostParts);
-                for (int parts = 2; parts <= most; ++parts) {
-                    const int part_steps = (steps + parts - 1) / parts;
-                    cost = static_cast<int64_t>(part_steps) * each + 1500 + 250 * parts;
-                    if (cost < best_cost) best_cost = cost, best = cols, ctl.part_steps = part_steps, ctl.parts = (steps + part_steps - 1) / part_steps;
-                }
-            } else {
-                const int64_t tiles = static_cast<int64_t>(total) * ((p.cols_dim + across - 1) / across);
-                const int64_t cost = (tiles + workers - 1) / workers * (cols + p.tile_overhead);
-                if (cost < best_cost) best_cost = cost, best = cols;
+        // what a tile costs at any width.  With an epilogue, few tiles and a workspace also parts of the contraction, one
+        // wave of them: what they cost to meet is worth about 1500 and 250 a part (steps of a column).  A lane has a width and a
+        // number of parts: one thread took 4 us over all of them (16 rows, 1024 x 7168: 16.8 us a call), while all waited.
+        // (In 32 bits: there are fewer than 2^30 tiles.)
+        static_assert(kWarpSize / kMostParts >= 4, "a lane for each");
+        const int step = lane_id() / kMostParts, cols = kMaxTileCols >> step, parts = lane_id() % kMostParts + 1;
+        const int shift = 8 - step - (FORM == kGated);  // of the columns of an output tile
+        const uint32_t workers = gridDim.x / CG, steps = (p.contraction + 63) >> 6;
+        const uint32_t across = static_cast<uint32_t>(p.cols_dim + (1 << shift) - 1) >> shift, tiles = total * across;
+        uint32_t part_steps = steps;
+        uint64_t cost = UINT64_MAX;
+        if (cols >= min_cols<FORM, CG>()) {
+            const uint32_t each = cols + p.tile_overhead;
+            if (parts == 1) {
+                cost = static_cast<uint64_t>((tiles + workers - 1) / workers) * each * (has_epilogue(FORM) ? steps : 1);
+            } else if (has_epilogue(FORM) && p.parts && tiles != 0 && tiles <= workers && parts * tiles <= workers && static_cast<uint32_t>(parts) * kLeastPartSteps <= steps) {
+                part_steps = (steps + parts - 1) / parts;
+                cost = static_cast<uint64_t>(part_steps) * each + 1500 + 250 * parts;
             }
         }
-        ctl.tile_cols = best;
-        ctl.col_tiles = (p.cols_dim + out_cols<FORM>(best) - 1) / out_cols<FORM>(best);
-        ctl.tiles = total * ctl.col_tiles * ctl.parts;
+        // the first of the cheapest
+        const uint32_t high = static_cast<uint32_t>(cost >> 32), least = __reduce_min_sync(kFullMask, high);
+        const uint32_t low = high == least ? static_cast<uint32_t>(cost) : UINT32_MAX;
+        const uint32_t least_low = __reduce_min_sync(kFullMask, low);  // by all lanes
+        if (lane_id() == __ffs(__ballot_sync(kFullMask, high == least && low == least_low)) - 1) {
+            if (overlap) report(p.status, EP_ERR_CAPACITY);
+            t.before[groups] = total;
+            ctl.tile_cols = cols;
+            ctl.col_tiles = across;
+            ctl.part_steps = part_steps;
+            ctl.parts = parts == 1 ? 1 : (steps + part_steps - 1) / part_steps;
+            ctl.tiles = tiles * ctl.parts;
+        }
     }
 }
 
@@ -758,14 +758,13 @@ __device__ __forceinline__ void add_bias(const float4& bias, int c, float (&v)[3
 // After a warp's sums of a part of a tile are written: whether they are the last of the tile's, and all may be read.  Each
 // warp of a CTA meets its like in the others, so that the CTA does not wait.
 __device__ __forceinline__ bool last_part(const GemmParams& p, int meeting, int parts) {
-    __threadfence();
     __syncwarp();
     int before = 0;
     if (lane_id() == 0) {
-        before = atomicAdd(p.tickets + meeting, 1);
+        before = arrive_at(p.tickets + meeting);
         if (before == parts - 1) p.tickets[meeting] = 0;  // for the next call
-        __threadfence();
     }
+    __syncwarp();
     return __shfl_sync(kFullMask, before, 0) == parts - 1;
 }
 

@@ -506,13 +506,11 @@ __device__ __forceinline__ void sum_warps_barrier() { asm volatile("bar.sync 1, 
 // After the sum warps wrote a part of what `parts` CTAs add up: whether this CTA is the last to arrive, and may read all.
 template <bool kDown>
 __device__ __forceinline__ bool last_to_arrive(const LayerRoles<kDown>& x, int ticket, int parts, int& turn) {
-    __threadfence();
     sum_warps_barrier();
     if (threadIdx.x == 4 * kWarpSize) {
-        const bool last = atomicAdd(x.p.tickets + ticket, 1) == parts - 1;
+        const bool last = arrive_at(x.p.tickets + ticket) == parts - 1;
         if (last) x.p.tickets[ticket] = 0;  // for the next call
         x.ctl.last_arrival[turn & 1] = last;
-        __threadfence();
     }
     sum_warps_barrier();
     return *const_cast<volatile int32_t*>(&x.ctl.last_arrival[turn++ & 1]) != 0;  // the other word is written next
