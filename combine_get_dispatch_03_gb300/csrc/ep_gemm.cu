@@ -406,77 +406,95 @@ __device__ __forceinline__ void load_operands(const Roles& x) {
         const int cols = q.cols / CG;                     // columns that this CTA loads
         const int cb = static_cast<int>(x.rank) * cols;
         const uint32_t bytes = row_bytes + cols * kRowBytes;
-        for (int s = 0; s < q.steps; ++s) {
-            ok = wait_phase(&ctl.empty[stage], phase ^ 1, x.waits);
-            if (!ok) break;
-            uint8_t* a = x.stages + stage * x.stage_bytes;
-            uint8_t* b = a + kABytes;
-            uint32_t bar = full0 + 8 * stage;
-            if constexpr (FORM == kWeightGrad) {
-                const bool tail = (s + 1) * 64 > q.rows;
-                if (tail) {
-                    bar = smem_u32(&ctl.tail_full[stage]);
-                    mbar_arrive_expect_tx(&ctl.tail_full[stage], bytes);
-                    tail_phase ^= 1u << stage;
-                    tail_last |= 1u << stage;
+        if constexpr (!kWords && FORM != kWeightGrad && FORM != kTransposed) {
+            // Every step of the tile loads the same: one or two boxes of rows, one or two of columns, found once.
+            const int half = FORM == kGated ? q.cols / 2 : cols;  // gated: the first half of columns are gates, the second their ups
+            const int box = half >= kBox ? kBox : kColBox;
+            const bool two_rows = small_boxes == 2, two_cols = cols > box;
+            auto column = [&](int c) { return q.n0 + (FORM != kGated || c < half ? c : p.cols_dim + c - half); };
+            const int at0 = column(cb), at1 = column(cb + box), row = q.row0 + my_m0;
+            const CUtensorMap* const rows_map = small_boxes ? &x.maps.a_small : &x.maps.a;
+            const CUtensorMap* const cols_map = box == kBox ? &x.maps.b : &x.maps.b_small;
+            constexpr int kStep = FORM == kFp8 ? 128 : 64;
+            int k0 = q.step0 * kStep;
+            for (int s = 0; s < q.steps; ++s, k0 += kStep) {
+                ok = wait_phase(&ctl.empty[stage], phase ^ 1, x.waits);
+                if (!ok) break;
+                uint8_t* a = x.stages + stage * x.stage_bytes;
+                uint8_t* b = a + kABytes;
+                const uint32_t bar = full0 + 8 * stage;
+                bar_arrive_expect_tx<CG>(bar, bytes);
+                if (rows_here > 0) tma_load_2d<CG>(a, rows_map, k0, row, bar);
+                if (two_rows) tma_load_2d<CG>(a + kRowBox * kRowBytes, rows_map, k0, row + kRowBox, bar);
+                tma_load_3d<CG>(b, cols_map, k0, at0, q.group, bar);
+                if (two_cols) tma_load_3d<CG>(b + box * kRowBytes, cols_map, k0, at1, q.group, bar);
+                ++used;
+                if (++stage == static_cast<uint32_t>(x.num_stages)) stage = 0, phase ^= 1;
+            }
+        } else {
+            for (int s = 0; s < q.steps; ++s) {
+                ok = wait_phase(&ctl.empty[stage], phase ^ 1, x.waits);
+                if (!ok) break;
+                uint8_t* a = x.stages + stage * x.stage_bytes;
+                uint8_t* b = a + kABytes;
+                uint32_t bar = full0 + 8 * stage;
+                if constexpr (FORM == kWeightGrad) {
+                    const bool tail = (s + 1) * 64 > q.rows;
+                    if (tail) {
+                        bar = smem_u32(&ctl.tail_full[stage]);
+                        mbar_arrive_expect_tx(&ctl.tail_full[stage], bytes);
+                        tail_phase ^= 1u << stage;
+                        tail_last |= 1u << stage;
+                    } else {
+                        bar_arrive_expect_tx<CG>(bar, bytes);
+                        tail_last &= ~(1u << stage);
+                    }
+                    const int r = q.row0 + s * 64;
+                    if (my_m0 + kBox <= p.a_chunked) {
+                        tma_load_3d<CG>(a, &x.maps.a, 0, r, my_m0 / 64, bar);
+                    } else {
+                        tma_load_2d<CG>(a, &x.maps.a_small, my_m0, r, bar);
+                        tma_load_2d<CG>(a + 8192, &x.maps.a_small, my_m0 + 64, r, bar);
+                    }
+                    for (int c = 0; c < cols;) {
+                        const int at = q.n0 + cb + c;
+                        if (c + kBox <= cols && at + kBox <= p.b_chunked) {
+                            tma_load_3d<CG>(b + c * kRowBytes, &x.maps.b, 0, r, at / 64, bar);
+                            c += kBox;
+                        } else {
+                            tma_load_2d<CG>(b + c * kRowBytes, &x.maps.b_small, at, r, bar);
+                            c += kColBox;
+                        }
+                    }
                 } else {
                     bar_arrive_expect_tx<CG>(bar, bytes);
-                    tail_last &= ~(1u << stage);
-                }
-                const int r = q.row0 + s * 64;
-                if (my_m0 + kBox <= p.a_chunked) {
-                    tma_load_3d<CG>(a, &x.maps.a, 0, r, my_m0 / 64, bar);
-                } else {
-                    tma_load_2d<CG>(a, &x.maps.a_small, my_m0, r, bar);
-                    tma_load_2d<CG>(a + 8192, &x.maps.a_small, my_m0 + 64, r, bar);
-                }
-                for (int c = 0; c < cols;) {
-                    const int at = q.n0 + cb + c;
-                    if (c + kBox <= cols && at + kBox <= p.b_chunked) {
-                        tma_load_3d<CG>(b + c * kRowBytes, &x.maps.b, 0, r, at / 64, bar);
-                        c += kBox;
-                    } else {
-                        tma_load_2d<CG>(b + c * kRowBytes, &x.maps.b_small, at, r, bar);
-                        c += kColBox;
+                    const int k0 = (q.step0 + s) * (FORM == kFp8 ? 128 : 64);
+                    if (small_boxes == 0) {
+                        if (!kWords && rows_here > 0) tma_load_2d<CG>(a, &x.maps.a, k0, q.row0 + my_m0, bar);
+                    } else if (!kWords) {
+                        for (int c = 0; c < small_boxes; ++c)
+                            tma_load_2d<CG>(a + c * (kRowBox * kRowBytes), &x.maps.a_small, k0, q.row0 + my_m0 + c * kRowBox, bar);
                     }
-                }
-            } else {
-                bar_arrive_expect_tx<CG>(bar, bytes);
-                const int k0 = (q.step0 + s) * (FORM == kFp8 ? 128 : 64);
-                if (small_boxes == 0) {
-                    if (!kWords && rows_here > 0) tma_load_2d<CG>(a, &x.maps.a, k0, q.row0 + my_m0, bar);
-                } else if (!kWords) {
-                    for (int c = 0; c < small_boxes; ++c)
-                        tma_load_2d<CG>(a + c * (kRowBox * kRowBytes), &x.maps.a_small, k0, q.row0 + my_m0 + c * kRowBox, bar);
-                }
-                if constexpr (FORM == kGated) {
-                    // the tile's first half of columns are gates, the second their ups (of a pair: each CTA has one half)
-                    const int half = q.cols / 2;
                     for (int c = 0; c < cols;) {
-                        const int at = q.n0 + (cb + c < half ? cb + c : p.cols_dim + cb + c - half);
-                        tma_load_3d<CG>(b + c * kRowBytes, half >= kBox ? &x.maps.b : &x.maps.b_small, k0, at, q.group, bar);
-                        c += half >= kBox ? kBox : kColBox;
+                        const int at = q.n0 + cb + c;
+                        if (FORM == kTransposed && c + kBox <= cols && at + kBox <= p.b_chunked) {
+                            tma_load_4d<CG>(b + c * kRowBytes, &x.maps.b, 0, k0, at / 64, q.group, bar);
+                            c += kBox;
+                        } else if (FORM == kTransposed) {
+                            tma_load_3d<CG>(b + c * kRowBytes, &x.maps.b_small, at, k0, q.group, bar);
+                            c += kColBox;
+                        } else if (c + kBox <= cols) {
+                            tma_load_3d<CG>(b + c * kRowBytes, &x.maps.b, k0, at, q.group, bar);
+                            c += kBox;
+                        } else {
+                            tma_load_3d<CG>(b + c * kRowBytes, &x.maps.b_small, k0, at, q.group, bar);
+                            c += kColBox;
+                        }
                     }
                 }
-                for (int c = 0; FORM != kGated && c < cols;) {
-                    const int at = q.n0 + cb + c;
-                    if (FORM == kTransposed && c + kBox <= cols && at + kBox <= p.b_chunked) {
-                        tma_load_4d<CG>(b + c * kRowBytes, &x.maps.b, 0, k0, at / 64, q.group, bar);
-                        c += kBox;
-                    } else if (FORM == kTransposed) {
-                        tma_load_3d<CG>(b + c * kRowBytes, &x.maps.b_small, at, k0, q.group, bar);
-                        c += kColBox;
-                    } else if (c + kBox <= cols) {
-                        tma_load_3d<CG>(b + c * kRowBytes, &x.maps.b, k0, at, q.group, bar);
-                        c += kBox;
-                    } else {
-                        tma_load_3d<CG>(b + c * kRowBytes, &x.maps.b_small, k0, at, q.group, bar);
-                        c += kColBox;
-                    }
-                }
+                ++used;
+                if (++stage == static_cast<uint32_t>(x.num_stages)) stage = 0, phase ^= 1;
             }
-            ++used;
-            if (++stage == static_cast<uint32_t>(x.num_stages)) stage = 0, phase ^= 1;
         }
     }
     // Copies and products in flight end before the memory goes away.  Where all went well the products have read every
@@ -514,34 +532,36 @@ __device__ __forceinline__ void multiply(const Roles& x) {
     for (int tile = x.worker; ok && tile < ctl.tiles; tile += x.workers) {
         const Tile q = decode<FORM, CG>(t, p, ctl, tile);
         const uint32_t idesc = mma_desc(FORM == kFp8 ? 0 : 1, a_mn, b_mn, kTileRows * CG, q.cols);
-        for (int s = 0; s < q.steps && ok; ++s) {
-            const int in_segment = kSegment ? s % kSegment : s;
-            // operands first: they are there, and with short segments the accumulator is what is waited for
-            if (FORM == kWeightGrad && CG == 2 && q.rows - s * 64 < 64)  // zeroed rows, maybe the peer's
-                ok = wait_phase<true>(&ctl.full[stage], phase, x.waits);
-            else
-                ok = wait_phase(&ctl.full[stage], phase, x.waits);
-            if (!ok) break;
-            if (in_segment == 0) {
-                ok = wait_phase(&ctl.acc_empty[buf], acc_phase ^ 1, x.waits);
-                if (!ok) break;
-            }
-            tc_fence_after();
-            const uint32_t a = smem_u32(x.stages) + stage * x.stage_bytes;
-            const uint64_t da = smem_desc(a, a_mn ? 8192 : 16);
-            const uint64_t db = smem_desc(a + kABytes, b_mn ? 8192 : 16);
+        for (int s = 0; ok && s < q.steps;) {
+            const int end = kSegment ? min(q.steps, s + kSegment) : q.steps;  // of an accumulator
             const uint32_t d = x.tmem + buf * kMaxTileCols;
+            bool first = true;
+            for (; s < end; ++s) {
+                // operands first: they are there, and with short segments the accumulator is what is waited for
+                if (FORM == kWeightGrad && CG == 2 && q.rows - s * 64 < 64)  // zeroed rows, maybe the peer's
+                    ok = wait_phase<true>(&ctl.full[stage], phase, x.waits);
+                else
+                    ok = wait_phase(&ctl.full[stage], phase, x.waits);
+                if (!ok) break;
+                if (first) {
+                    ok = wait_phase(&ctl.acc_empty[buf], acc_phase ^ 1, x.waits);
+                    if (!ok) break;
+                }
+                tc_fence_after();
+                const uint32_t a = smem_u32(x.stages) + stage * x.stage_bytes;
+                const uint64_t da = smem_desc(a, a_mn ? 8192 : 16);
+                const uint64_t db = smem_desc(a + kABytes, b_mn ? 8192 : 16);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                tc_mma<CG, FORM == kFp8>(d, da + i * (a_mn ? 128 : 2), db + i * (b_mn ? 128 : 2), idesc,
-                                         in_segment | i);
-            tc_commit<CG>(&ctl.empty[stage]);
-            if (s == q.steps - 1 || (kSegment && in_segment == kSegment - 1)) {
-                tc_commit<CG>(&ctl.acc_full[buf]);
-                buf ^= 1;
-                acc_phase ^= buf == 0;
+                for (int i = 0; i < 4; ++i)
+                    tc_mma<CG, FORM == kFp8>(d, da + i * (a_mn ? 128 : 2), db + i * (b_mn ? 128 : 2), idesc, !first || i);
+                tc_commit<CG>(&ctl.empty[stage]);
+                first = false;
+                if (++stage == static_cast<uint32_t>(x.num_stages)) stage = 0, phase ^= 1;
             }
-            if (++stage == static_cast<uint32_t>(x.num_stages)) stage = 0, phase ^= 1;
+            if (!ok) break;
+            tc_commit<CG>(&ctl.acc_full[buf]);
+            buf ^= 1;
+            acc_phase ^= buf == 0;
         }
     }
     // The products already issued still write tensor memory, also where another warp gave up on them: load_operands()
