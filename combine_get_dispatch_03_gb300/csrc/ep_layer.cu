@@ -15,12 +15,17 @@
 // that none waits for a last wave: 8 experts of 7168 x 2048 are 128 tiles of the first kernel on 152 SMs.  A tile that
 // crosses CTAs leaves partial sums in the workspace; the last CTA to arrive (a ticket) adds them up in the CTAs' order.
 //
-// The second kernel is launched beside the first (programmatic dependent launch; for up to 16 tokens both fit an SM) and
-// fills its shared memory with weights, which do not hang on the first kernel, before it waits for it.
+// The second kernel is launched beside the first (programmatic dependent launch; for up to 8 tokens both may fit an SM,
+// both_on_an_sm()) and fills its shared memory with weights, which do not hang on the first kernel, before it waits for it.
 //
 // FP8 weights: e4m3 with one scale per 128 x 128.  The tokens stay bf16: a block of 128 channels is scaled by a power of two
 // and split into two e4m3 values (split_e4m3()), columns of their own in the products, so that nothing of bf16's eight bits is
 // lost but what lies 2^-17 below the block's largest value.  A block's sums are added, scaled and added up in fp32 registers.
+//
+// What bounds it (6754 GB/s copied; experts of 7168 x 2048): bf16, memory: 1 token of 8 experts 117 us, 6.0 TB/s, 8 tokens of 23 309,
+// 6.6, 64 of 32 457, 6.2.  FP8, with half of the bytes, the two kernels' start and end (1 token 79 us, 4.5 TB/s; 8 of 23 180, 5.6),
+// then the splitting and the adding up of blocks (64 tokens of 32 experts 343, 4.1).  Small experts, 1024 x 512: 17 to 20 us for one
+// token, launches and the sums of parts.
 #include "ep_act.cuh"
 #include "ep_groups.cuh"
 #include "ep_handle.h"
@@ -919,7 +924,7 @@ int size_kernel(LayerParams* p, bool fp8, bool down, int room, int most) {
 }
 
 // Whether the two kernels shall fit an SM together.  Alone each has more stages, and the second starts when the first ends:
-// one bf16 token through 8 of 32 experts of 7168 x 2048 121 us together and 119 alone, 8 tokens through 28 of them 315 and 308, but 8
+// one bf16 token through 8 of 32 experts of 7168 x 2048 121 us together and 119 alone, 8 tokens through 23 of them 315 and 308, but 8
 // experts of 1024 x 512 18.3 and 20.9, 4 tokens of 2048 x 1024 51 and 59; FP8 81 and 85, 184 and 185, 20.8 and 21.6, 38 and 44.
 bool both_on_an_sm(const LayerParams& p, bool fp8) {
     if (p.tokens > kSmallTokens) return false;
