@@ -203,6 +203,14 @@ struct Tile {
     int step0, tile;                             // parts: the first step, the tile
 };
 
+// Steps of a stage.  A step's commit takes its 380 cycles whether one product lies before it or four, so that the narrowest tiles of
+// single CTAs have two steps a stage and a commit (16 rows, 1024 x 7168: 26.5 to 20.9 us).  Tiles of 128 columns do not: three
+// stages of 64 KB instead of six of 32 keep too little on its way (4096 rows, 256 x 7168: 24.9 to 27.1).
+template <int FORM, int CG, bool kWords>
+__device__ __forceinline__ bool deep_stages(int tile_cols) {
+    return CG == 1 && !kWords && (FORM == kForward || has_epilogue(FORM)) && tile_cols <= kColBox;
+}
+
 // The group table in shared memory.
 struct Table {
     int32_t* before;  // [groups + 1] row tiles before each group
@@ -287,8 +295,10 @@ __device__ __forceinline__ void build_table(const Table& t, const GemmParams& p,
         const int total = overlap ? 0 : static_cast<int>(row_tiles);
         // Tile width: the one whose waves over the CTAs take the least time, a wave costing its columns plus
         // what a tile costs at any width.  With an epilogue, few tiles and a workspace also parts of the contraction, one
-        // wave of them: what they cost to meet is worth about 1500 and 250 a part (steps of a column).  A lane has a width and a
-        // number of parts: one thread took 4 us over all of them (16 rows, 1024 x 7168: 16.8 us a call), while all waited.
+        // wave of them.  A step of a column is worth 1.65 cycles (64 columns of few rows take 270 a step, 128 380, 256 650);
+        // the parts' way out took 16 cycles a column, their way back to the last CTA 10 to 15 a column and part (4096 rows, 256 x
+        // 7168: 25 us with two parts of 128 columns, 28 with four of 256).  A lane has a width and a number of parts: one thread
+        // took 4 us over all of them while the others waited (16 rows, 1024 x 7168: 16.8 us a call, 13.0 by lanes).
         // (In 32 bits: there are fewer than 2^30 tiles.)
         static_assert(kWarpSize / kMostParts >= 4, "a lane for each");
         const int step = lane_id() / kMostParts, cols = kMaxTileCols >> step, parts = lane_id() % kMostParts + 1;
@@ -298,12 +308,12 @@ __device__ __forceinline__ void build_table(const Table& t, const GemmParams& p,
         uint32_t part_steps = steps;
         uint64_t cost = UINT64_MAX;
         if (cols >= min_cols<FORM, CG>()) {
-            const uint32_t each = cols + p.tile_overhead;
+            const uint32_t each = cols + (has_epilogue(FORM) ? max(p.tile_overhead, 100) : p.tile_overhead);
             if (parts == 1) {
                 cost = static_cast<uint64_t>((tiles + workers - 1) / workers) * each * (has_epilogue(FORM) ? steps : 1);
             } else if (has_epilogue(FORM) && p.parts && tiles != 0 && tiles <= workers && parts * tiles <= workers && static_cast<uint32_t>(parts) * kLeastPartSteps <= steps) {
                 part_steps = (steps + parts - 1) / parts;
-                cost = static_cast<uint64_t>(part_steps) * each + 1500 + 250 * parts;
+                cost = static_cast<uint64_t>(part_steps) * each + 1000 + cols * (8 + 6 * parts);
             }
         }
         // the first of the cheapest
@@ -384,6 +394,7 @@ struct Roles {
     uint8_t* residuals;  // a box for each warp
     uint32_t tmem, rank, stage_bytes;  // rank: of the CTA in its pair
     int num_stages, worker, workers;
+    bool deep;  // deep_stages()
 };
 
 constexpr uint32_t kABytes = kTileRows * kRowBytes;
@@ -420,18 +431,26 @@ __device__ __forceinline__ void load_operands(const Roles& x) {
             const CUtensorMap* const rows_map = small_boxes ? &x.maps.a_small : &x.maps.a;
             const CUtensorMap* const cols_map = box == kBox ? &x.maps.b : &x.maps.b_small;
             constexpr int kStep = FORM == kFp8 ? 128 : 64;
+            const bool deep = CG == 1 && x.deep;
+            const uint32_t step_bytes = kABytes + q.cols / CG * kRowBytes;
             int k0 = q.step0 * kStep;
-            for (int s = 0; s < q.steps; ++s, k0 += kStep) {
-                ok = wait_phase(&ctl.empty[stage], phase ^ 1, x.waits);
-                if (!ok) break;
-                uint8_t* a = x.stages + stage * x.stage_bytes;
+            auto load = [&](uint8_t* a, uint32_t bar) {
                 uint8_t* b = a + kABytes;
-                const uint32_t bar = full0 + 8 * stage;
-                bar_arrive_expect_tx<CG>(bar, bytes);
                 if (rows_here > 0) tma_load_2d<CG>(a, rows_map, k0, row, bar);
                 if (two_rows) tma_load_2d<CG>(a + kRowBox * kRowBytes, rows_map, k0, row + kRowBox, bar);
                 tma_load_3d<CG>(b, cols_map, k0, at0, q.group, bar);
                 if (two_cols) tma_load_3d<CG>(b + box * kRowBytes, cols_map, k0, at1, q.group, bar);
+                k0 += kStep;
+            };
+            for (int s = 0; s < q.steps; ++s) {
+                ok = wait_phase(&ctl.empty[stage], phase ^ 1, x.waits);
+                if (!ok) break;
+                uint8_t* a = x.stages + stage * x.stage_bytes;
+                const uint32_t bar = full0 + 8 * stage;
+                const bool second = deep && s + 1 < q.steps;
+                bar_arrive_expect_tx<CG>(bar, second ? 2 * bytes : bytes);
+                load(a, bar);
+                if (second) load(a + step_bytes, bar), ++s;
                 ++used;
                 if (++stage == static_cast<uint32_t>(x.num_stages)) stage = 0, phase ^= 1;
             }
@@ -522,9 +541,12 @@ __device__ __forceinline__ void load_operands(const Roles& x) {
 }
 
 // One thread of the pair: the products.
-template <int FORM, int CG>
+template <int FORM, int CG, bool kWords>
 __device__ __forceinline__ void multiply(const Roles& x) {
     constexpr int kSegment = segment_steps(FORM);
+    constexpr bool kDeep = CG == 1 && !kWords && (FORM == kForward || has_epilogue(FORM));
+    static_assert(kSegment % 2 == 0 || !kDeep, "whole stages a segment");
+    const bool deep = kDeep && x.deep;
     const GemmParams& p = x.p;
     const Table& t = x.t;
     Control& ctl = x.ctl;
@@ -536,6 +558,7 @@ __device__ __forceinline__ void multiply(const Roles& x) {
     for (int tile = x.worker; ok && tile < ctl.tiles; tile += x.workers) {
         const Tile q = decode<FORM, CG>(t, p, ctl, tile);
         const uint32_t idesc = mma_desc(FORM == kFp8 ? 0 : 1, a_mn, b_mn, kTileRows * CG, q.cols);
+        const uint32_t step_bytes = kABytes + q.cols / CG * kRowBytes;
         for (int s = 0; ok && s < q.steps;) {
             const int end = kSegment ? min(q.steps, s + kSegment) : q.steps;  // of an accumulator
             const uint32_t d = x.tmem + buf * kMaxTileCols;
@@ -553,13 +576,17 @@ __device__ __forceinline__ void multiply(const Roles& x) {
                 }
                 tc_fence_after();
                 const uint32_t a = smem_u32(x.stages) + stage * x.stage_bytes;
-                const uint64_t da = smem_desc(a, a_mn ? 8192 : 16);
-                const uint64_t db = smem_desc(a + kABytes, b_mn ? 8192 : 16);
+                auto step = [&](uint32_t a) {
+                    const uint64_t da = smem_desc(a, a_mn ? 8192 : 16);
+                    const uint64_t db = smem_desc(a + kABytes, b_mn ? 8192 : 16);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    tc_mma<CG, FORM == kFp8>(d, da + i * (a_mn ? 128 : 2), db + i * (b_mn ? 128 : 2), idesc, !first || i);
+                    for (int i = 0; i < 4; ++i)
+                        tc_mma<CG, FORM == kFp8>(d, da + i * (a_mn ? 128 : 2), db + i * (b_mn ? 128 : 2), idesc, !first || i);
+                    first = false;
+                };
+                step(a);
+                if (deep && s + 1 < end) step(a + step_bytes), ++s;
                 tc_commit<CG>(&ctl.empty[stage]);
-                first = false;
                 if (++stage == static_cast<uint32_t>(x.num_stages)) stage = 0, phase ^= 1;
             }
             if (!ok) break;
@@ -1151,10 +1178,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     else __syncthreads();
     tc_fence_after();
 
-    const uint32_t stage_bytes = kABytes + ctl.tile_cols / CG * kRowBytes;
+    const bool deep = deep_stages<FORM, CG, kWords>(ctl.tile_cols);
+    const uint32_t stage_bytes = (deep ? 2 : 1) * (kABytes + ctl.tile_cols / CG * kRowBytes);
     const Roles x = {maps, p, t, ctl, {&ctl.abort_flag, p.status, p.wait_limit_ns}, stages, boxes, residuals, ctl.tmem, rank, stage_bytes,
                      min(kMaxStages, static_cast<int>((kMaxSmem - 1024u - table_end - out_bytes) / stage_bytes)),
-                     static_cast<int>(blockIdx.x / CG), static_cast<int>(gridDim.x / CG)};
+                     static_cast<int>(blockIdx.x / CG), static_cast<int>(gridDim.x / CG), deep};
     // Forms with segments hold 128 sums a thread in their eight epilogue warps: registers move there from the
     // others (72 + 2 * 216 = 3 * 168, what the block was launched with).
     constexpr bool kSums = segment_steps(FORM) != 0;
@@ -1163,7 +1191,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (warp == 0) {
             if (elect_one()) load_operands<FORM, CG, kWords>(x);
         } else if (warp == 1) {
-            if (rank == 0 && elect_one()) multiply<FORM, CG>(x);
+            if (rank == 0 && elect_one()) multiply<FORM, CG, kWords>(x);
         } else if (FORM == kWeightGrad && warp == 2) {
             zero_tails<FORM, CG>(x);
         } else if (kWords) {
