@@ -29,8 +29,8 @@
 //     messages: 308 to 334 us, 6.0 to 6.5 TB/s (375 to 385 where half of the experts have more than 128).
 //   - short contractions and few rows: the results' way out (staged_pays()).  64 experts of 1024 rows, 4096 x 256 bf16:
 //     128 to 138 us, 5.1 to 5.5 TB/s; gradients of 32 experts of 16 rows, 2048 x 2048: 89 us, 6.0 TB/s.
-//   - few tiles: a launch, the table of groups (2000 cycles), and about 380 cycles a step, whatever the tile's width: 16 rows, 1024 x
-//     7168 26.5 us; with an epilogue and a workspace in eight parts 11.7.
+//   - few tiles: a launch, the table of groups (2000 cycles), and 250 to 400 cycles a step however little it computes
+//     (deep_stages()): 16 rows, 1024 x 7168 19.3 us; with an epilogue and a workspace in eight parts 10.8.
 //   - an epilogue: 8187 rows, 7168 x 2048 121 us without anything (120 without the form), 125 with a bias, 144 with a residual (117 MB
 //     more), 149 with gelu, 146 with silu, 139 gated: where a tile's contraction is short, its eight warps do not keep up.
 //   - rows four bytes apart: the two warps that copy them, a round trip to memory for every 8 or 16 rows (copy_rows()).
@@ -204,7 +204,7 @@ struct Tile {
 };
 
 // Steps of a stage.  A step's commit takes its 380 cycles whether one product lies before it or four, so that the narrowest tiles of
-// single CTAs have two steps a stage and a commit (16 rows, 1024 x 7168: 26.5 to 20.9 us).  Tiles of 128 columns do not: three
+// single CTAs have two steps a stage and a commit (16 rows, 1024 x 7168: 26.5 to 19.3 us).  Tiles of 128 columns do not: three
 // stages of 64 KB instead of six of 32 keep too little on its way (4096 rows, 256 x 7168: 24.9 to 27.1).
 template <int FORM, int CG, bool kWords>
 __device__ __forceinline__ bool deep_stages(int tile_cols) {

@@ -17,7 +17,7 @@
 // groups.  Beside a softmax a bias feels the sum of all exponentials: there the whole token is computed again (choose_exactly),
 // a percent of the tokens.
 //
-// Instructions bound it, not memory (an ncu capture: 1.3 thousand a token with bias and groups): 32768 tokens of 256 fp32 logits, K 8,
+// Instructions bound it, not memory (an ncu capture: 1245 a token with bias and groups, 657 without): 32768 tokens of 256 fp32 logits, K 8,
 // whose bytes take 5.4 us, take 24 us with sigmoid, 26 with softmax, 38 with a bias, 46 to 49 with 8 groups, 68 with softmax and
 // bias; 4096 tokens 6 to 10 us; a decode step of 32 tokens 2.  K rounds of a maximum over the warp took 42 us without bias and 90
 // with bias and groups.  Groups that begin inside a lane's experts (160 experts in 8) go through shared memory, 70 to 90 us.
