@@ -30,7 +30,7 @@
 //   - short contractions and few rows: the results' way out (staged_pays()).  64 experts of 1024 rows, 4096 x 256 bf16:
 //     128 to 138 us, 5.1 to 5.5 TB/s; gradients of 32 experts of 16 rows, 2048 x 2048: 89 us, 6.0 TB/s.
 //   - few tiles: a launch, the table of groups (2000 cycles), and 250 to 400 cycles a step however little it computes
-//     (deep_stages()): 16 rows, 1024 x 7168 19.3 us; with an epilogue and a workspace in eight parts 10.8.
+//     (deep_stages()): 16 rows, 1024 x 7168 19.3 us; with an epilogue and a workspace in eight parts 10.2.
 //   - an epilogue: 8187 rows, 7168 x 2048 121 us without anything (120 without the form), 125 with a bias, 144 with a residual (117 MB
 //     more), 149 with gelu, 146 with silu, 139 gated: where a tile's contraction is short, its eight warps do not keep up.
 //   - rows four bytes apart: the two warps that copy them, a round trip to memory for every 8 or 16 rows (copy_rows()).
@@ -964,28 +964,39 @@ __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
         const Tile q = decode<FORM, CG>(t, p, ctl, tile);
         const int meeting = (q.tile * CG + static_cast<int>(x.rank)) * kEpilogueWarps + w;  // of a tile's parts
         float* const part = cut ? p.parts + (static_cast<int64_t>(meeting) * ctl.parts + (tile - q.tile * ctl.parts)) * kPartFloats + lane_id() : nullptr;
-        if (!ok) {
-            last_part(p, meeting, ctl.parts);
-            continue;
-        }
         if (FORM == kWeightGrad && p.accumulate && q.steps == 0) continue;  // nothing to add
         const int cols_half = out_cols<FORM>(q.cols) / 2;
         const int in_group = q.m0 + static_cast<int>(x.rank) * kTileRows + quarter * 32;
         const int rows = min(32, max(0, (FORM == kWeightGrad ? p.rows_dim : q.rows) - in_group));
         const Place at = {(FORM == kWeightGrad ? 0 : q.row0) + in_group, q.n0 + half * cols_half, q.group,
                           static_cast<short>(rows), static_cast<short>(cols_half)};
+        // Whether this warp has nothing of the tile, in any of its parts: with up to 32 rows three of four warps, which then neither
+        // write nor meet (16 rows, 1024 x 7168: 10.8 to 10.2 us, gated 15.4 to 14.2; without parts no change).
+        const bool nothing = has_epilogue(FORM) && (rows == 0 || at.col >= p.cols_dim);
+        if (!ok) {
+            if (!nothing) last_part(p, meeting, ctl.parts);
+            continue;
+        }
         if constexpr (has_epilogue(FORM)) {
-            ahead.load_bias(p, at);
+            if (!nothing) ahead.load_bias(p, at);
             if (!cut) ahead.ask_residual(x, at, 0);
         }
         if constexpr (kSegment == 0) {
             ok = warp_wait(&ctl.acc_full[buf], acc_phase, x.waits);
             if (!ok) {
                 if (!cut) break;
-                last_part(p, meeting, ctl.parts);
+                if (!nothing) last_part(p, meeting, ctl.parts);
                 continue;
             }
             tc_fence_after();
+            if (nothing) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane_id() == 0) bar_arrive<CG>(acc_empty0 + 8 * buf);
+                buf ^= 1;
+                acc_phase ^= buf == 0;
+                continue;
+            }
             const bool staged = in_boxes<FORM>(p, at);
             bool mine = true;  // this warp's to finish
             if (cut) {
@@ -1103,9 +1114,10 @@ __device__ __forceinline__ void store_tiles(const Roles& x, int warp) {
             __syncwarp();
             if (!ok) {
                 if (!cut) break;
-                last_part(p, meeting, ctl.parts);
+                if (!nothing) last_part(p, meeting, ctl.parts);
                 continue;
             }
+            if (nothing) continue;
             if (cut) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
