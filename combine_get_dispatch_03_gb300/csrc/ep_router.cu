@@ -498,18 +498,19 @@ __device__ __forceinline__ void route_token(const RouterParams& p, int64_t token
         }
         if (there) rank = before;
         if constexpr (kScored) {
-            // Neighbours in the order of which one at least is chosen: too close, unless they tie because their inputs are the same.
+            // Neighbours in the order of which one at least is chosen: too close, unless they tie because their inputs are the
+            // same.  Then the next one is looked at: where equal inputs lie on both sides of the last place, it is what
+            // may belong before them.
             if (there) reach.sorted[rank] = make_float2(k, __int_as_float(lane_id()));
             __syncwarp();
             bool near = false;
-            if (rank < p.topk && rank + 1 < all) {
-                const float2 next = reach.sorted[rank + 1];
-                near = k - next.x <= key_error(error, k, next.x);
-                if (near) {
-                    const int j = __float_as_int(next.y), e = __float_as_int(reach.key_expert[j].y);
-                    near = reach.logit[j] != lc || (p.bias && p.bias[e] != p.bias[expert]);
-                }
+            for (int r = rank < p.topk ? rank + 1 : all; r < all && !near; ++r) {
+                const float2 next = reach.sorted[r];
+                if (k - next.x > key_error(error, k, next.x)) break;
+                const int j = __float_as_int(next.y), e = __float_as_int(reach.key_expert[j].y);
+                near = reach.logit[j] != lc || (p.bias && p.bias[e] != p.bias[expert]);
             }
+            __syncwarp();
             if (__any_sync(kFullMask, near)) {
                 if (!alone(p)) {
                     close = true;
