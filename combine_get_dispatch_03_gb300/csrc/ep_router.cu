@@ -36,7 +36,7 @@ constexpr int kMaxGroups = 32;
 // The error of a comparison of two keys, as a part of the token's largest score.  Sigmoid: 2^-22.3 a key from the
 // exponential, the reciprocal and two roundings.  Softmax: at most 28 roundings of 2^-24 more in its sum, which a bias feels.
 constexpr float kSigmoidError = 1e-6f, kSoftmaxError = 2e-6f;
-constexpr float kSumError = 2.4e-7f;  // 2^-22 of the key itself, from adding the bias or a second key
+constexpr float kSumError = 2.4e-7f;  // 2^-22 of the keys themselves, from adding the bias or a second key
 
 struct RouterParams {
     const void* logits;
@@ -238,9 +238,9 @@ __device__ __noinline__ int choose_exactly(const RouterParams& p, int64_t token)
 }
 
 // The score of the group of this lane's number (lane g < groups), from the warp's keys: two largest, added up.  *second: the
-// smaller.
+// smaller; *magnitude: their sizes added up, by which their roundings and the sum's go (the sum itself may be of two that cancel).
 template <int V>
-__device__ __forceinline__ float group_score(const RouterParams& p, const float (&key)[V], float* scratch, float* second) {
+__device__ __forceinline__ float group_score(const RouterParams& p, const float (&key)[V], float* scratch, float* second, float* magnitude) {
     const int size = p.experts / p.groups;
     float a = -INFINITY, b = -INFINITY;
     const int lanes = size / V;
@@ -271,6 +271,7 @@ __device__ __forceinline__ float group_score(const RouterParams& p, const float 
             }
     }
     *second = size == 1 ? a : b;
+    *magnitude = size == 1 ? fabsf(a) : fabsf(a) + fabsf(b);
     return size == 1 ? a : a + b;
 }
 
@@ -360,8 +361,8 @@ __device__ __forceinline__ bool make_keys(const RouterParams& p, const float (&l
     *error = (p.softmax ? kSoftmaxError : kSigmoidError) * warp_max(top);
     if (p.groups == 1) return false;
     const int size = p.experts / p.groups;
-    float second;
-    const float score = group_score<V>(p, key, scratch, &second);
+    float second, magnitude;
+    const float score = group_score<V>(p, key, scratch, &second, &magnitude);
     int better = 0;
     for (int g = 0; g < p.groups; ++g) {
         const float other = __shfl_sync(kFullMask, score, g);
@@ -369,14 +370,15 @@ __device__ __forceinline__ bool make_keys(const RouterParams& p, const float (&l
     }
     const bool there = lane_id() < p.groups, in = there && better < p.kept;
     unsigned stay = __ballot_sync(kFullMask, in);
-    // the last that stays and the first that does not
-    const float last = -warp_max(in ? -score : -INFINITY), next = warp_max(there && !in ? score : -INFINITY);
-    const float apart = key_error(2.0f * *error, last, next);
-    bool close = next > -INFINITY && last - next <= apart;
+    // A score lies in [low, high] in 64 bits: the least that one that stays can have, the most of one that does not.
+    const float own = score > -INFINITY ? *error + kSumError * magnitude : 0.0f;
+    const float low = score - own, high = score + own;
+    const float last = -warp_max(in ? -low : -INFINITY), next = warp_max(there && !in ? high : -INFINITY);
+    bool close = next > -INFINITY && last <= next;
     if (close && alone(p) && size % V == 0) {
         // Groups around the border compete again, by what their largest members are worth in 64 bits, a lane each.
-        const bool rival = there && score >= next - apart && score <= last + apart;
-        const unsigned rivals = __ballot_sync(kFullMask, rival), above = __ballot_sync(kFullMask, there && score > last + apart);
+        const bool rival = there && low <= next && high >= last;
+        const unsigned rivals = __ballot_sync(kFullMask, rival), above = __ballot_sync(kFullMask, in && !rival);
         const int mine = first < p.experts ? first / size : 0;
         const float least = __shfl_sync(kFullMask, second - 2.0f * key_error(*error, second, second), mine);
         int all = 0;

@@ -1,4 +1,4 @@
-"""The router where 32 bits tell keys apart no more: equal inputs at the last place that is chosen."""
+"""The router where 32 bits tell keys apart no more: equal inputs at the last place that is chosen, biases that cancel."""
 import pytest
 import torch
 
@@ -64,3 +64,23 @@ def test_saturated_scores_by_hand():
     assert idx.tolist() == [[20]]
     idx, _ = check(handle(32, 2), logits, bias=torch.zeros(32, device=DEV), score="sigmoid")
     assert idx.tolist() == [[20, 3]]
+
+
+@pytest.mark.parametrize("E,groups,kept", [(64, 8, 4), (256, 8, 4), (160, 8, 3), (96, 32, 9), (32, 16, 8), (512, 4, 1)])
+@pytest.mark.parametrize("size", [16.0, 64.0, 1000.0])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_biases_that_cancel_in_a_group(E, groups, kept, size, score):
+    """A group's two largest keys with large biases of opposite sign: each is rounded at its own size, and their sum is small.
+
+    Scores of neighbouring groups lie about 1e-5 apart; 64 bits round a key of 1000 by 1e-13."""
+    g = gen(E + int(size))
+    each = E // groups
+    bias = torch.full((groups, each), -4.0 * size, device=DEV)
+    first = torch.rand((groups, each), generator=g, device=DEV).argsort(1)
+    bias.scatter_(1, first[:, :1], size)
+    bias.scatter_(1, first[:, 1:2], -size)
+    logits = torch.randn((2000, 1), generator=g, device=DEV) + torch.randn((2000, E), generator=g, device=DEV) * 1e-4
+    check(handle(E, 2), logits, bias=bias.view(-1), score=score, num_groups=groups, kept_groups=kept)
+    # beside a group of small biases, whose sum 32 bits have right
+    bias[0] = torch.randn(each, generator=g, device=DEV) * 0.01
+    check(handle(E, 2), logits, bias=bias.view(-1), score=score, num_groups=groups, kept_groups=kept)
