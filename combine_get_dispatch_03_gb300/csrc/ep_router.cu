@@ -289,6 +289,9 @@ __device__ __noinline__ double key64(const RouterParams& p, float l, int expert,
 // How far apart two keys must lie for 32 bits to tell them; `error` is that of their scores.
 __device__ __forceinline__ float key_error(float error, float a, float b) { return error + kSumError * (fabsf(a) + fabsf(b)); }
 
+// sigmoid(l) * exp(-top) for l <= top < 0; 0 where sigmoid(l) is 0 in 64 bits too.
+__device__ __forceinline__ float low_sigmoid(float l, float top) { return l < -709.78f ? 0.0f : expf(l - top) / (1.0f + expf(l)); }
+
 struct Chosen {
     int expert;  // lane k's, -1: none
     bool close;  // 32 bits may have it wrong
@@ -549,8 +552,10 @@ __device__ __forceinline__ void route_token(const RouterParams& p, int64_t token
         if (p.normalize) base = warp_max(chosen ? lc : -INFINITY);  // the sum cancels
         if (chosen) s = expf(lc - base);
         if (chosen && !p.normalize) s /= sum;
-    } else if (chosen) {
-        s = 1.0f / (1.0f + expf(-lc));
+    } else {
+        // normalised, the largest score cancels: without it none is lost where all lie below what fp32 holds
+        const float top = p.normalize ? warp_max(chosen ? lc : -INFINITY) : 0.0f;
+        if (chosen) s = top < 0.0f ? low_sigmoid(lc, top) : 1.0f / (1.0f + expf(-lc));
     }
     float w = s * p.scale;
     if (p.normalize) {
@@ -643,12 +648,12 @@ __device__ __forceinline__ void route_gradient(const RouterParams& p, int64_t to
 #pragma unroll
         for (int v = 0; v < V; ++v) d[v] = 0.0f;
         float s = 0.0f, rest = 1.0f;  // rest: 1 - s
+        const float top = p.softmax || p.normalize ? warp_max(lc) : 0.0f;
         if (p.softmax) {
-            const float top = warp_max(lc);
             if (mine && lc > -INFINITY) s = expf(lc - top);
         } else if (mine) {
             const float e = expf(-fabsf(lc)), small = e / (1.0f + e), large = 1.0f / (1.0f + e);
-            s = lc >= 0.0f ? large : small;
+            s = top < 0.0f ? low_sigmoid(lc, top) : lc >= 0.0f ? large : small;
             rest = lc >= 0.0f ? small : large;
         }
         if (p.normalize) {

@@ -596,6 +596,7 @@ ep_status ep_expert_reduce(ep_handle* h, const void* y, int64_t y_row_bytes, con
  *     their two largest keys stay (of groups of one expert: its key); ties to the lower group
  *   topk_idx:     the K largest keys that are left, in descending order, ties to the lower expert   int64 [num_tokens][K]
  *   topk_weights: scale * s, normalize != 0: scale * s / (sum of the chosen s)                      fp32 [num_tokens][K]
+ *     (a normalised weight is right where the scores themselves pass fp32's range too; sigmoids below e^-709.78 are 0, as in 64 bits)
  * -- the topk_idx and topk_weights of ep_dispatch(), ep_ll_dispatch() and ep_moe_layer().  Keys are compared as 64-bit
  * arithmetic gives them (without bias and groups, the logits themselves): rounding does not choose
  * experts.  A logit of -inf or NaN, or a bias of -inf or NaN, keeps its expert from being chosen (the first two

@@ -1,7 +1,9 @@
-"""The router where 32 bits tell keys apart no more: equal inputs at the last place that is chosen, biases that cancel."""
+"""The router where 32 bits tell keys apart no more: equal inputs at the last place that is chosen, biases that cancel, scores
+below the least fp32 number."""
 import pytest
 import torch
 
+from combine_get_dispatch_03_gb300 import ep
 from test_gpu_experts import DEV, gen
 from test_gpu_router import check, handle
 
@@ -84,3 +86,69 @@ def test_biases_that_cancel_in_a_group(E, groups, kept, size, score):
     # beside a group of small biases, whose sum 32 bits have right
     bias[0] = torch.randn(each, generator=g, device=DEV) * 0.01
     check(handle(E, 2), logits, bias=bias.view(-1), score=score, num_groups=groups, kept_groups=kept)
+
+
+def far_logits(g, tokens, E):
+    """Logits of -80 to -200, of -600 to -700, of both, and beside an ordinary one."""
+    l = -80 - 120 * torch.rand((tokens, E), generator=g, device=DEV)
+    l[1::4] = -600 - 100 * torch.rand((l[1::4].shape[0], E), generator=g, device=DEV)
+    l[2::4, ::2] = -600 - 100 * torch.rand(l[2::4, ::2].shape, generator=g, device=DEV)
+    l[3::4, 0] = torch.randn(l[3::4, 0].shape, generator=g, device=DEV)
+    l[0, :3] = torch.tensor([-90.0, -91.0, -89.0])
+    return l
+
+
+def far_weights(l, idx):
+    """Normalised sigmoids in 64 bits from their logarithms, so that nothing underflows."""
+    c = torch.nn.functional.logsigmoid(l.double().gather(1, idx))
+    return torch.softmax(c, 1)
+
+
+@pytest.mark.parametrize("E,K", [(3, 2), (32, 8), (160, 6), (256, 32)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("groups", [1, 2])
+def test_normalised_sigmoids_of_low_logits(E, K, dtype, groups):
+    """Scores below the least fp32 number have weights all the same: s / sum, from which the largest score cancels.
+
+    A weight's argument l - max is rounded by 2^-18 at most (it is below 128 wherever the weight is above 1e-37), exp and the
+    quotient by 2^-22, the sum of 32 by 31 * 2^-24: 2^-17 together.  A gradient is scale * u * (dw - sum dw u) * (1 - s): two
+    such factors, 2^-15.5 of the magnitudes, and one rounding to its type."""
+    if E % groups or K > E // groups:
+        groups = 1
+    g = gen(E + K)
+    h = handle(E, K)
+    l = far_logits(g, 401, E).to(dtype)
+    if groups > 1:
+        l[:, E // 2:] = -704.0  # the first half stays
+    r = ep.ep_router(h, l, score="sigmoid", scale=2.5, num_groups=groups, kept_groups=max(1, groups // 2))
+    h.check()
+    idx, w = r["topk_idx"], r["topk_weights"].double()
+    want_idx = torch.sort(l.double()[:, :E // groups], dim=1, descending=True, stable=True).indices[:, :K]
+    assert torch.equal(idx, want_idx)
+    want = 2.5 * far_weights(l, idx)
+    assert ((w - want).abs() <= 2.0 ** -17 * want + 1e-37).all()
+    assert ((w.sum(1) - 2.5).abs() <= 2.5 * 2.0 ** -17).all()
+    dw = torch.randn((401, K), generator=g, device=DEV)
+    dl = ep.ep_router_grad(h, l, idx, dw, score="sigmoid", scale=2.5).double()
+    u, rest = want / 2.5, torch.sigmoid(-l.double().gather(1, idx))
+    d = 2.5 * u * (dw.double() - (dw.double() * u).sum(1, keepdim=True)) * rest
+    mag = 2.5 * u * (dw.double().abs() + (dw.double().abs() * u).sum(1, keepdim=True)) * rest
+    want = torch.zeros_like(dl).scatter_(1, idx, d)
+    mag = torch.zeros_like(dl).scatter_(1, idx, mag)
+    assert ((dl - want).abs() <= 2.0 ** -15.5 * mag + torch.finfo(dtype).eps / 2 * want.abs() + 1e-37).all()
+
+
+def test_sigmoids_that_64_bits_do_not_hold():
+    """Below -709.78 a score is 0 in 64 bits too: no weight, and no gradient."""
+    h = handle(16, 4)
+    l = torch.full((4, 16), -800.0, device=DEV)
+    l[1, 5] = -700.0
+    l[2] = torch.finfo(torch.float32).min
+    l[3, 2], l[3, 7] = 1.0, 2.0
+    idx, w = check(h, l[[0, 2, 3]].contiguous(), score="sigmoid")
+    assert (w[:2] == 0).all()
+    r = ep.ep_router(h, l, score="sigmoid")
+    assert r["topk_idx"][1].tolist() == [5, 0, 1, 2] and r["topk_weights"][1].tolist() == [1.0, 0.0, 0.0, 0.0]
+    dl = ep.ep_router_grad(h, l, r["topk_idx"], torch.ones((4, 4), device=DEV), score="sigmoid")
+    assert (dl[:3] == 0).all()
+    h.check()
