@@ -34,7 +34,7 @@ struct ActGradParams {
     int32_t width;
     const uint8_t* dy;
     int64_t dy_row_bytes;
-    const uint8_t* pre;       // NULL: not needed
+    const uint8_t* pre;       // NULL: not needed; it may be d_pre
     int64_t pre_row_bytes;
     const float* row_weights;
     uint8_t* d_pre;           // NULL: not wanted
@@ -118,8 +118,8 @@ __global__ void __launch_bounds__(kThreads, 3) act_grad_kernel(const ActGradPara
                         d4[i] = ld_stream_v4(reinterpret_cast<const int4*>(p.dy + row * p.dy_row_bytes + 2 * col));
                         if (p.pre) {
                             const uint8_t* pre = p.pre + row * p.pre_row_bytes + 2 * col;
-                            v4[i] = ld_stream_v4(reinterpret_cast<const int4*>(pre));
-                            if (kGated) u4[i] = ld_stream_v4(reinterpret_cast<const int4*>(pre + half));
+                            v4[i] = ld_stream_written_v4(reinterpret_cast<const int4*>(pre));
+                            if (kGated) u4[i] = ld_stream_written_v4(reinterpret_cast<const int4*>(pre + half));
                         }
                         if (p.row_weights) w[i] = __ldg(p.row_weights + row);
                     }

@@ -39,6 +39,16 @@ __device__ __forceinline__ int4 ld_stream_v4(const int4* p) {
     return v;
 }
 
+// The same of data that the kernel may write after it has read it (an output in its input's memory).
+__device__ __forceinline__ int4 ld_stream_written_v4(const int4* p) {
+    int4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.s32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
 // 16-byte store that is not kept in L1.
 __device__ __forceinline__ void st_stream_v4(int4* p, const int4& v) {
     asm volatile("st.global.L1::no_allocate.v4.s32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(v.x), "r"(v.y),
