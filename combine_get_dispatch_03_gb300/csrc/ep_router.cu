@@ -101,7 +101,7 @@ __device__ __forceinline__ void load_row(const RouterParams& p, int64_t token, f
             for (int i = 0; i < V / kVec; ++i) {
                 int4 q = make_int4(0, 0, 0, 0);
                 const bool in = first + i * kVec < p.experts;
-                if (in) q = ld_stream_v4(row + i);
+                if (in) q = ld_stream_ordered_v4(row + i);
                 float f[kVec];
                 if constexpr (sizeof(T) == 4) {
                     f[0] = __int_as_float(q.x), f[1] = __int_as_float(q.y), f[2] = __int_as_float(q.z), f[3] = __int_as_float(q.w);
