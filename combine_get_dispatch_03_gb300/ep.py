@@ -13,6 +13,7 @@ import ctypes
 import dataclasses
 import math
 import os
+import threading
 
 import torch
 
@@ -225,7 +226,7 @@ class Handle:
             _raise(lib().ep_handle_create(ctypes.byref(cfg.c()), ctypes.byref(self._ptr)))
         self.normal_tokens = None
         self.ll_tokens = None
-        self._scratch = {}  # raw stream -> workspace of the calls on it
+        self._scratch = {}  # (raw stream, host thread) -> workspace of the calls on it
 
     @property
     def ptr(self):
@@ -628,12 +629,14 @@ _capturing = torch.cuda.is_current_stream_capturing
 def _scratch(h, nbytes, stream):
     """The address of a workspace of nbytes for a call, and what keeps it alive until the call is enqueued.
 
-    The handle keeps one for each stream that was current in a call, for calls on one stream run in their order.  A captured
-    call gets its own from the graph's memory, a call with a stream of its own from that stream's."""
+    The handle keeps one for each stream that was current in a call, for calls on one stream run in their order, and for each
+    host thread: a call enqueues more than one kernel, and another thread's can come between them.  A captured
+    call gets its own from the graph's memory, a call with a stream of its own from that stream's.  That keeps workspaces apart; calls
+    on one handle must not overlap on the GPU all the same (include/ep.h): its counters are shared."""
     if stream is not None or _capturing():
         t = _out((max(16, nbytes),), torch.uint8, h, stream)
         return t.data_ptr(), t
-    key = _stream(None, h.device)
+    key = _stream(None, h.device), threading.get_ident()
     t = h._scratch.get(key)
     if t is None or t.numel() < nbytes:
         t = h._scratch[key] = torch.empty(max(16, nbytes), dtype=torch.uint8, device=h.device)

@@ -27,7 +27,9 @@
  *    legacy default stream) and returns after enqueueing its kernels.
  *    Calls on one handle must not overlap on the GPU -- issue them on one
  *    stream, or order them with events: the handle holds the dispatch record,
- *    the status word and the counters its kernels share.
+ *    the status word and the counters its kernels share.  That holds for
+ *    captured calls too (two graphs of one handle are not replayed side by
+ *    side), and whatever workspaces the calls are given.
  *  - Argument errors found on the host are returned at once and nothing is
  *    enqueued.  Errors found by the kernels (an expert id out of range,
  *    counts that disagree with is_token_in_rank, a receive buffer that is
