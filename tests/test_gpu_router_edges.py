@@ -152,3 +152,18 @@ def test_sigmoids_that_64_bits_do_not_hold():
     dl = ep.ep_router_grad(h, l, r["topk_idx"], torch.ones((4, 4), device=DEV), score="sigmoid")
     assert (dl[:3] == 0).all()
     h.check()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_one_normalised_expert_has_no_gradient(score, dtype):
+    """With one expert a token and normalised weights the weight is the scale, whatever the logits are: the gradient is 0, not what
+    rounding leaves of a difference."""
+    g = gen(31)
+    h = handle(40, 1)
+    logits = (torch.randn((300, 40), generator=g, device=DEV) * 3).to(dtype)
+    r = ep.ep_router(h, logits, score=score, scale=2.5)
+    assert (r["topk_weights"] == 2.5).all()
+    dl = ep.ep_router_grad(h, logits, r["topk_idx"], torch.randn((300, 1), generator=g, device=DEV), score=score, scale=2.5)
+    assert (dl == 0).all()
+    h.check()
