@@ -25,8 +25,11 @@ constexpr int kMostChunkRows = 64;
 constexpr int kLaneCols = 8;
 constexpr int kWarpCols = kWarpSize * kLaneCols;
 
-// Rows of a chunk: fewer where there are few rows, so that every SM has some.  By the rows alone: the sums' order is
-// the same whatever the handle may use of the GPU.
+// Rows of a chunk: fewer where there are few rows, so that every SM has some; more of many, whose partial sums cost less then.  By the rows
+// alone: the sums' order is the same whatever the handle may use of the GPU.  us at 8, 16, 32, 64 rows a chunk, 32 groups, gated
+// 2 x 1024 columns, all sums: 4096 rows 15.9, 16.6, 18.8, 25.2; 8192 24.6, 24.2, 26.3, 33.7; 16384 43.6, 40.3, 42.0, 46.0; 24576 59, 56, 53,
+// 51; 31968 74, 68, 69, 80; 48000 107, 96, 95, 95; 65536 145, 126, 122, 129; 98304 223, 187, 175, 178; 131072 293, 253, 229, 227.  Not gated, 264
+// columns: 4096 rows 11.7, 11.3, 14.2, 17.1; 11968 20, 16, 15, 21; 16384 25, 19, 19, 21; 48000 56, 43, 37, 35; 98304 104, 76, 68, 65.
 __host__ __device__ inline int chunk_rows(int64_t num_rows) { return num_rows >= 100000 ? kMostChunkRows : num_rows >= 32000 ? 32 : num_rows >= 12000 ? 16 : 8; }
 
 struct ActGradParams {

@@ -17,11 +17,17 @@
 // groups.  Beside a softmax a bias feels the sum of all exponentials: there the whole token is computed again (choose_exactly),
 // a percent of the tokens.
 //
-// Instructions bound it, not memory (an ncu capture: 1245 a token with bias and groups, 657 without): 32768 tokens of 256 fp32 logits, K 8,
-// whose bytes take 5.4 us, take 24 us with sigmoid, 26 with softmax, 38 with a bias, 46 to 49 with 8 groups, 68 with softmax and
-// bias; 4096 tokens 6 to 10 us; a decode step of 32 tokens 2.  K rounds of a maximum over the warp took 42 us without bias and 90
-// with bias and groups.  Groups that begin inside a lane's experts (160 experts in 8) go through shared memory, 70 to 90 us.
-// The gradient writes every logit once and is bound by memory: 13.6 us of a floor of 10.4 (normalised softmax).
+// Instructions bound it, not memory (an ncu capture: 1249 a token with bias and groups, 618 and 657 without): 32768 tokens of 256 fp32
+// logits, K 8, whose bytes take 5.4 us, take 24 us with sigmoid, 26 with softmax, 36 with a bias, 46 to 49 with 8 groups, 70 with
+// softmax and bias (bf16 the same: 24, 25, with 8 groups 47); 4096 tokens 6 to 10 us, with softmax and bias 25; a decode step of 32
+// tokens 2.  K rounds of a maximum over the warp took 42 us without bias and 90 with bias and groups.  Groups that begin inside a
+// lane's experts (160 experts in 8) go through shared memory, 70 to 90 us.
+//
+// The gradient writes every logit, and reads them all only for a softmax that is not normalised: 18.7 us, bf16 17.5, where the
+// bytes take 10.4 and 5.4.  The other forms read the chosen logits: normalised softmax 13.7 us, bf16 10.0, sigmoid 14.3 and 10.7, not
+// normalised 13.6 and 8.3, where the bytes (33.5 MB written in fp32, 8.4 in sectors of 32 bytes of the chosen, 3.1 of indices
+// and weights) take 6.7 and 4.2.  Not memory bounds them but a token's two loads, its indices and then their logits, with
+// nothing of the warp's next token on its way.
 #include "ep_act.cuh"
 #include "ep_groups.cuh"
 #include "ep_handle.h"
@@ -709,6 +715,9 @@ cudaError_t start(const ep_handle* h, const RouterParams& p, cudaStream_t stream
     return launch_kernel(router_kernel<T, V, true>, grid, dim3(kThreads), smem, stream, 1, p);
 }
 
+// Experts a lane: the fewest that hold all, so that few lanes are empty.  16384 tokens, sigmoid, without and with a bias: 264 experts
+// at 16 a lane 19.6 and 30 us, at 64 108 and 303; 512 19.5 and 33, 72 and 238; 520 to 1024 (at 64) 58 to 67 and 117 to 149, 2048 75
+// and 203.  At 32 a lane none is built.
 template <bool kGrad, typename T>
 cudaError_t start_type(const ep_handle* h, const RouterParams& p, cudaStream_t stream) {
     if (p.experts <= 32) return start<kGrad, T, 1>(h, p, stream);
