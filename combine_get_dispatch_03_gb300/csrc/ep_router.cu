@@ -42,6 +42,7 @@ constexpr int kMaxGroups = 32;
 // The error of a comparison of two keys, as a part of the token's largest score.  Sigmoid: 2^-22.3 a key from the
 // exponential, the reciprocal and two roundings.  Softmax: at most 28 roundings of 2^-24 more in its sum, which a bias feels.
 constexpr float kSigmoidError = 1e-6f, kSoftmaxError = 2e-6f;
+constexpr float kFlushError = 2.4e-38f;  // 2^-125: sigmoids below 2^-126 are flushed to 0
 constexpr float kSumError = 2.4e-7f;  // 2^-22 of the keys themselves, from adding the bias or a second key
 
 struct RouterParams {
@@ -367,7 +368,7 @@ __device__ __forceinline__ bool make_keys(const RouterParams& p, const float (&l
         top = fmaxf(top, in ? s : 0.0f);
         key[v] = in ? (p.bias ? s + bias_of(p, first + v) : s) : -INFINITY;
     }
-    *error = (p.softmax ? kSoftmaxError : kSigmoidError) * warp_max(top);
+    *error = fmaf(p.softmax ? kSoftmaxError : kSigmoidError, warp_max(top), kFlushError);
     if (p.groups == 1) return false;
     const int size = p.experts / p.groups;
     float second, magnitude;

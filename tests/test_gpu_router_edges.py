@@ -167,3 +167,14 @@ def test_one_normalised_expert_has_no_gradient(score, dtype):
     dl = ep.ep_router_grad(h, logits, r["topk_idx"], torch.randn((300, 1), generator=g, device=DEV), score=score, scale=2.5)
     assert (dl == 0).all()
     h.check()
+
+
+@pytest.mark.parametrize("E,groups,kept", [(16, 4, 1), (64, 8, 3), (256, 8, 4), (160, 8, 3)])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_scores_next_to_the_least_number(E, groups, kept, biased, dtype):
+    """Sigmoids around 2^-126 (a logit of -87.3), of which 32 bits keep some and flush others to 0: a group of two that are flushed
+    can be worth more than one with a single score that is not."""
+    g = gen(E)
+    logits = (torch.randn((4000, E), generator=g, device=DEV) * 1.5 - 88).to(dtype)
+    check(handle(E, 4), logits, bias=torch.zeros(E, device=DEV) if biased else None, score="sigmoid", num_groups=groups, kept_groups=kept)
